@@ -8,13 +8,16 @@ The names mirror the C ABI: :func:`fl_attn_fwd`, :func:`fl_attn_tile_shape`,
 :func:`fl_attn_status_string`, :func:`fl_attn_last_error`,
 :func:`fl_attn_version`, :func:`fl_attn_decode_workspace_size`,
 :func:`fl_attn_decode`, :func:`fl_attn_decode_static`, :func:`fl_attn_bwd`,
-:func:`fl_attn_diff_bwd`.  Tensors are torch tensors on the current CUDA device
+:func:`fl_attn_diff_bwd`, and for rotary positions and serving steps
+:func:`fl_rope`, :func:`fl_kv_plan`, :func:`fl_kv_append`, :func:`fl_attn_chunk`.
+Tensors are torch tensors on the current CUDA device
 (PyTorch provides device memory and streams; nothing else).
 """
 from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "_build", "libflattn.so")
@@ -50,6 +53,18 @@ FL_MASK_DOC = 4
 FL_INJECT_NONE = 0
 FL_INJECT_DROP_KV_LOAD = 1
 FL_DEVERR_TIMEOUT = 0x1
+FL_DEVERR_PAGES = 0x2
+FL_DEVERR_LENGTHS = 0x4
+# fl_rope_layout
+FL_ROPE_HALF = 0
+FL_ROPE_INTERLEAVED = 1
+# fl_rope_scaling
+FL_ROPE_SCALE_NONE = 0
+FL_ROPE_SCALE_LINEAR = 1
+FL_ROPE_SCALE_BASE = 2
+FL_ROPE_SCALE_BANDS = 3
+FL_ROPE_SCALE_RAMP = 4
+FL_ROPE_MAX_PAIRS = 128
 
 MODS = {"none": FL_MOD_NONE, "vanilla": FL_MOD_NONE, "alibi": FL_MOD_ALIBI,
         "softcap": FL_MOD_SOFTCAP, "expr": FL_MOD_EXPR}
@@ -57,6 +72,9 @@ MASKS = {"none": FL_MASK_NONE, "causal": FL_MASK_CAUSAL, "window": FL_MASK_WINDO
          "prefix": FL_MASK_PREFIX, "doc": FL_MASK_DOC}
 KINDS = {"standard": FL_KIND_STANDARD, "diff": FL_KIND_DIFF, "evo_row": FL_KIND_EVO_ROW,
          "evo_col": FL_KIND_EVO_COL}
+ROPE_LAYOUTS = {"half": FL_ROPE_HALF, "interleaved": FL_ROPE_INTERLEAVED}
+ROPE_SCALINGS = {"none": FL_ROPE_SCALE_NONE, "linear": FL_ROPE_SCALE_LINEAR, "base": FL_ROPE_SCALE_BASE,
+                 "bands": FL_ROPE_SCALE_BANDS, "ramp": FL_ROPE_SCALE_RAMP}
 
 
 class FlTensor(ctypes.Structure):
@@ -80,6 +98,40 @@ class FlDecodeDesc(ctypes.Structure):
     _fields_ = [
         ("score_mod", ctypes.c_int32), ("softcap", ctypes.c_float), ("causal", ctypes.c_int32),
         ("scale", ctypes.c_float), ("kv_lens", ctypes.c_void_p), ("max_kv_len", ctypes.c_int32),
+        ("block_table", ctypes.c_void_p), ("block_table_stride", ctypes.c_int32),
+        ("error_word", ctypes.c_void_p), ("wait_timeout_us", ctypes.c_uint32),
+    ]
+
+
+class FlRopeConfig(ctypes.Structure):
+    _fields_ = [
+        ("rot_dim", ctypes.c_int32), ("layout", ctypes.c_int32), ("scaling", ctypes.c_int32),
+        ("base", ctypes.c_double), ("factor", ctypes.c_double), ("context", ctypes.c_double),
+        ("low", ctypes.c_double), ("high", ctypes.c_double), ("magnitude", ctypes.c_double),
+    ]
+
+
+class FlRopeTable(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int32), ("layout", ctypes.c_int32), ("magnitude", ctypes.c_float),
+                ("valid", ctypes.c_uint32), ("turns", ctypes.c_uint64 * FL_ROPE_MAX_PAIRS)]
+
+
+class FlKvPlanDesc(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int32), ("page_size", ctypes.c_int32), ("max_tokens", ctypes.c_int32),
+        ("n_free", ctypes.c_int32), ("block_table_stride", ctypes.c_int32),
+        ("q_lens", ctypes.c_void_p), ("kv_lens", ctypes.c_void_p), ("free_pages", ctypes.c_void_p),
+        ("free_head", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
+        ("kv_lens_out", ctypes.c_void_p), ("cu_q", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+        ("slots", ctypes.c_void_p), ("free_head_out", ctypes.c_void_p), ("error_word", ctypes.c_void_p),
+    ]
+
+
+class FlChunkDesc(ctypes.Structure):
+    _fields_ = [
+        ("score_mod", ctypes.c_int32), ("softcap", ctypes.c_float), ("causal", ctypes.c_int32),
+        ("window", ctypes.c_int32), ("scale", ctypes.c_float), ("batch", ctypes.c_int32),
+        ("cu_q", ctypes.c_void_p), ("kv_lens", ctypes.c_void_p), ("max_kv_len", ctypes.c_int32),
         ("block_table", ctypes.c_void_p), ("block_table_stride", ctypes.c_int32),
         ("error_word", ctypes.c_void_p), ("wait_timeout_us", ctypes.c_uint32),
     ]
@@ -143,6 +195,22 @@ def load_library(path: str = LIB_PATH):
     lib.fl_attn_decode.argtypes = [P(FlTensor), P(FlTensor), P(FlTensor), P(FlTensor), P(FlTensor),
                                    P(FlDecodeDesc), ctypes.c_void_p, ctypes.c_size_t,
                                    ctypes.c_void_p]
+    # the rotary and serving-step entry points take their tensors (and the
+    # rotary desc) as packed bytes: see _pack
+    B = ctypes.c_char_p
+    lib.fl_rope_make_table.restype = ctypes.c_int
+    lib.fl_rope_make_table.argtypes = [P(FlRopeConfig), P(FlRopeTable)]
+    lib.fl_rope.restype = ctypes.c_int
+    lib.fl_rope.argtypes = [B] * 5 + [ctypes.c_void_p]
+    lib.fl_kv_plan.restype = ctypes.c_int
+    lib.fl_kv_plan.argtypes = [P(FlKvPlanDesc), ctypes.c_void_p]
+    lib.fl_kv_append.restype = ctypes.c_int
+    lib.fl_kv_append.argtypes = [B] * 6 + [ctypes.c_void_p, B, ctypes.c_void_p]
+    lib.fl_attn_chunk_workspace_size.restype = ctypes.c_int
+    lib.fl_attn_chunk_workspace_size.argtypes = [B, B, P(FlChunkDesc), P(ctypes.c_size_t)]
+    lib.fl_attn_chunk.restype = ctypes.c_int
+    lib.fl_attn_chunk.argtypes = [B] * 5 + [P(FlChunkDesc), ctypes.c_void_p, ctypes.c_size_t,
+                                            ctypes.c_void_p]
     _lib = lib
     return lib
 
@@ -405,3 +473,198 @@ def fl_attn_decode_static(q, k_cache, v_cache, out, lse, desc: FlDecodeDesc, str
     if st != FL_OK:
         raise FlAttnError(st, fl_attn_last_error())
 
+
+# ---------------------------------------------------------------------------
+# Rotary positions and serving steps.  These calls are a few microseconds of
+# GPU work, so their marshalling is kept short: a tensor travels as the packed
+# bytes of its fl_tensor (one struct.pack; a ctypes structure filled field by
+# field takes three times as long).
+
+_PACK = {n: struct.Struct(f"<Qii{n}q{8 * (5 - n)}x{n}q{8 * (5 - n)}x") for n in range(1, 6)}
+_CODES: dict = {}
+
+
+def _pack(t, device: int):
+    """A torch tensor (or None) of CUDA device `device` -> the bytes of its fl_tensor."""
+    if t is None:
+        return None
+    if t.get_device() != device:
+        raise ValueError(f"tensor on {t.device}: the current device is cuda:{device}")
+    if not _CODES:
+        import torch
+        _CODES.update({torch.bfloat16: FL_BF16, torch.float32: FL_F32})
+    code = _CODES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {t.dtype}")
+    shape = t.shape
+    if not 1 <= len(shape) <= 5:
+        raise ValueError(f"tensors have 1 to 5 dimensions, got {len(shape)}")
+    return _PACK[len(shape)].pack(t.data_ptr(), code, len(shape), *shape, *t.stride())
+
+
+def _device() -> int:
+    import torch
+    return torch.cuda.current_device()
+
+
+def _stream_of(stream) -> int:
+    if stream is None:
+        import torch
+        return torch.cuda.current_stream().cuda_stream
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
+
+
+def _check(st: int) -> None:
+    if st != FL_OK:
+        raise FlAttnError(st, fl_attn_last_error())
+
+
+def _index(t, name: str, shape, dtype="int32", device=None) -> int:
+    """The address of a contiguous integer tensor of the given shape (None entries: any size)."""
+    import torch
+    if t.dtype != getattr(torch, dtype):
+        raise TypeError(f"{name} must be {dtype}, is {t.dtype}")
+    if t.dim() != len(shape) or any(s is not None and s != n for s, n in zip(shape, t.shape)):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, has {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if device is not None and t.get_device() != device:
+        raise ValueError(f"{name} on {t.device}: the current device is cuda:{device}")
+    return t.data_ptr()
+
+
+def make_rope_table(rot_dim: int, *, base=10000.0, layout="half", scaling="none", factor=1.0,
+                    context=8192, low=0.0, high=0.0, magnitude=0.0) -> FlRopeTable:
+    """The frequencies of a model's rotary positions (see include/fl_attn.h);
+    made once per model and passed to :func:`fl_rope` and :func:`fl_kv_append`."""
+    c = FlRopeConfig()
+    c.rot_dim = int(rot_dim)
+    c.layout = ROPE_LAYOUTS[layout] if isinstance(layout, str) else int(layout)
+    c.scaling = ROPE_SCALINGS[scaling] if isinstance(scaling, str) else int(scaling)
+    c.base, c.factor, c.context = float(base), float(factor), float(context)
+    c.low, c.high, c.magnitude = float(low), float(high), float(magnitude)
+    table = FlRopeTable()
+    _check(load_library().fl_rope_make_table(ctypes.byref(c), ctypes.byref(table)))
+    return table
+
+
+_ROPE_DESC = struct.Struct("<QQqii")
+
+
+def fl_rope(q, k, q_out, k_out, table: FlRopeTable, positions=None, offset=0, backward=False,
+            stream=None) -> None:
+    """Enqueue rotary positions of q and (unless None) k into q_out and k_out,
+    which may be q and k themselves (see include/fl_attn.h).  Tensors are
+    [B, S, H, D] with positions (int32) [B, S] or [S], or [T, H, D] with
+    positions [T]; without positions, row s of a sequence is at s + offset.
+    ``backward`` maps the gradients of the outputs to those of the inputs."""
+    lib = load_library()
+    dev = _device()
+    at = rows = 0
+    if positions is not None:
+        if positions.dim() == 2:
+            at, rows = _index(positions, "positions", q.shape[:2], device=dev), q.shape[1]
+        else:
+            at = _index(positions, "positions", q.shape[-3:-2], device=dev)
+    desc = _ROPE_DESC.pack(ctypes.addressof(table), at, rows, int(offset), 1 if backward else 0)
+    _check(lib.fl_rope(_pack(q, dev), _pack(k, dev), _pack(q_out, dev), _pack(k_out, dev), desc,
+                       _stream_of(stream)))
+
+
+def make_kv_plan_desc(q_lens, kv_lens, free_pages, free_head, block_table, kv_lens_out, cu_q, positions,
+                      slots, free_head_out, *, page_size: int, error_word=None) -> FlKvPlanDesc:
+    """Build an fl_kv_plan_desc from contiguous device torch tensors, all int32
+    but slots (int64); slots and positions set the number of tokens a step may
+    have, slots may be None.  A serving loop keeps it: every step reads and
+    writes the same buffers."""
+    B = q_lens.shape[0]
+    dev = q_lens.get_device()
+    d = FlKvPlanDesc()
+    d.batch, d.page_size, d.max_tokens = B, int(page_size), positions.shape[0]
+    d.q_lens = _index(q_lens, "q_lens", (B,), device=dev)
+    d.kv_lens = _index(kv_lens, "kv_lens", (B,), device=dev)
+    d.n_free = free_pages.shape[0] if free_pages is not None else 0
+    d.free_pages = _index(free_pages, "free_pages", (None,), device=dev) if d.n_free else None
+    d.free_head = _index(free_head, "free_head", (1,), device=dev)
+    d.block_table = _index(block_table, "block_table", (B, None), device=dev)
+    d.block_table_stride = block_table.shape[1]
+    d.kv_lens_out = _index(kv_lens_out, "kv_lens_out", (B,), device=dev)
+    d.cu_q = _index(cu_q, "cu_q", (B + 1,), device=dev)
+    d.positions = _index(positions, "positions", (None,), device=dev)
+    d.slots = _index(slots, "slots", positions.shape, "int64", device=dev) if slots is not None else None
+    d.free_head_out = _index(free_head_out, "free_head_out", (1,), device=dev)
+    d.error_word = error_word.data_ptr() if error_word is not None else None
+    d._keep = (q_lens, kv_lens, free_pages, free_head, block_table, kv_lens_out, cu_q, positions, slots,
+               free_head_out, error_word)
+    return d
+
+
+def fl_kv_plan(desc: FlKvPlanDesc, stream=None) -> None:
+    """Enqueue a serving step's book-keeping (see include/fl_attn.h)."""
+    _check(load_library().fl_kv_plan(ctypes.byref(desc), _stream_of(stream)))
+
+
+def fl_kv_append(q, k, v, q_out, k_cache, v_cache, slots, *, rope: FlRopeTable | None = None,
+                 positions=None, stream=None) -> None:
+    """Enqueue the write of new keys and values [T, Hk, D] to their slots
+    (int64 [T]) of a paged cache, with the rotary positions of q (into q_out)
+    and k where ``rope`` is given (then positions, int32 [T], too); q and q_out
+    may both be None (see include/fl_attn.h)."""
+    lib = load_library()
+    dev = _device()
+    desc = None
+    if rope is not None:
+        if positions is None:
+            raise ValueError("rope needs positions")
+        desc = _ROPE_DESC.pack(ctypes.addressof(rope), _index(positions, "positions", k.shape[:1], device=dev),
+                               0, 0, 0)
+    _check(lib.fl_kv_append(_pack(q, dev), _pack(k, dev), _pack(v, dev), _pack(q_out, dev),
+                            _pack(k_cache, dev), _pack(v_cache, dev),
+                            _index(slots, "slots", k.shape[:1], "int64", device=dev), desc,
+                            _stream_of(stream)))
+
+
+def make_chunk_desc(cu_q, kv_lens, block_table, max_kv_len: int, *, score_mod="none", softcap=20.0,
+                    causal=True, window=0, scale=0.0, error_word=None, wait_timeout_us=0) -> FlChunkDesc:
+    """Build an fl_chunk_desc; cu_q [B + 1], kv_lens [B] and block_table
+    [B, pages] (None: contiguous cache) are contiguous device int32 torch tensors."""
+    B = kv_lens.shape[0]
+    dev = kv_lens.get_device()
+    d = FlChunkDesc()
+    d.score_mod = MODS[score_mod] if isinstance(score_mod, str) else int(score_mod)
+    d.softcap = float(softcap)
+    d.causal = 1 if causal else 0
+    d.window = int(window)
+    d.scale = float(scale)
+    d.batch = B
+    d.cu_q = _index(cu_q, "cu_q", (B + 1,), device=dev)
+    d.kv_lens = _index(kv_lens, "kv_lens", (B,), device=dev)
+    d.max_kv_len = int(max_kv_len)
+    if block_table is not None:
+        d.block_table = _index(block_table, "block_table", (B, None), device=dev)
+        d.block_table_stride = block_table.shape[1]
+    d.error_word = error_word.data_ptr() if error_word is not None else None
+    d.wait_timeout_us = int(wait_timeout_us)
+    d._keep = (cu_q, kv_lens, block_table, error_word)
+    return d
+
+
+def fl_attn_chunk_workspace_size(q, k_cache, desc: FlChunkDesc) -> int:
+    """Bytes of workspace fl_attn_chunk needs for these shapes."""
+    dev = _device()
+    n = ctypes.c_size_t()
+    _check(load_library().fl_attn_chunk_workspace_size(_pack(q, dev), _pack(k_cache, dev),
+                                                       ctypes.byref(desc), ctypes.byref(n)))
+    return n.value
+
+
+def fl_attn_chunk(q, k_cache, v_cache, out, lse, desc: FlChunkDesc, workspace, stream=None) -> None:
+    """Enqueue attention of ragged chunks of new tokens over the cache that
+    holds them (see include/fl_attn.h); q and out are [T, Hq, D], lse [Hq, T]
+    or None, workspace a device torch tensor of at least
+    fl_attn_chunk_workspace_size bytes."""
+    lib = load_library()
+    dev = _device()
+    _check(lib.fl_attn_chunk(_pack(q, dev), _pack(k_cache, dev), _pack(v_cache, dev), _pack(out, dev),
+                             _pack(lse, dev), ctypes.byref(desc), workspace.data_ptr(),
+                             workspace.numel() * workspace.element_size(), _stream_of(stream)))

@@ -18,7 +18,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libflattn.so")
 SOURCES = ["api.cu", "fwd_standard.cu", "fwd_diff.cu", "fwd_evo.cu", "fwd_decode.cu", "score_expr.cu",
-           "bwd_standard.cu", "bwd_diff.cu"]
+           "bwd_standard.cu", "bwd_diff.cu", "rope.cu", "kv_plan.cu", "fwd_chunk.cu"]
 # Sources of the standard kernel, embedded in the library for the runtime
 # compilation of score_mod expressions (score_expr.cu).
 JIT_SOURCES = ["fwd_standard.cu", "bwd_standard.cu", "common.cuh", "ptx.cuh", "softmax_tile.cuh",

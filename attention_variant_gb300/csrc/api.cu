@@ -964,6 +964,191 @@ fl_status diff_bwd_plan(const fl_tensor *q, const fl_tensor *k, const fl_tensor 
     return FL_OK;
 }
 
+// ------------------------------------------------------------------ rotary positions
+
+constexpr uint32_t kRopeTableValid = 0x726f7065u;
+
+// q, k, q_out, k_out of the rotary entry points: [B, S, H, D], or [T, H, D]
+// as one batch.
+fl_status check_rows(const fl_tensor *t, const char *name, int dtype, View &v)
+{
+    fl_status s;
+    if (!t)
+        return fail(FL_ERR_INVALID_ARG, "%s is NULL", name);
+    if (t->ndim == 4)
+        return check_tensor(t, name, 4, dtype, v);
+    if ((s = check_tensor(t, name, 3, dtype, v)) != FL_OK) return s;
+    for (int d = 3; d > 0; --d) {
+        v.size[d] = v.size[d - 1];
+        v.stride[d] = v.stride[d - 1];
+    }
+    v.size[0] = 1;
+    v.stride[0] = 0;
+    v.ndim = 4;
+    return FL_OK;
+}
+
+fl_status check_rope(const fl_rope_desc *d, int64_t D)
+{
+    if (!d || !d->table)
+        return fail(FL_ERR_INVALID_ARG, "desc or its table is NULL");
+    const fl_rope_table &t = *d->table;
+    if (t.valid != kRopeTableValid || t.rot_dim < 2 || t.rot_dim > 2 * FL_ROPE_MAX_PAIRS || t.rot_dim % 2 ||
+        (t.layout != FL_ROPE_HALF && t.layout != FL_ROPE_INTERLEAVED))
+        return fail(FL_ERR_INVALID_ARG, "the table was not made by fl_rope_make_table");
+    if (t.rot_dim > D)
+        return fail(FL_ERR_INVALID_ARG, "rot_dim %d exceeds the head dimension %lld", t.rot_dim, (long long)D);
+    if (reinterpret_cast<uintptr_t>(d->positions) % 4)
+        return fail(FL_ERR_ALIGNMENT, "positions is not 4-byte aligned");
+    if (d->positions_stride < 0)
+        return fail(FL_ERR_INVALID_ARG, "positions_stride must not be negative");
+    return FL_OK;
+}
+
+void set_rope(fl::RopeParams &p, const fl_rope_desc *d, int64_t D)
+{
+    p.div_seq = fl::make_fastdiv(1);
+    p.div_tile_page = fl::make_fastdiv(1);
+    if (d) {
+        const fl_rope_table &t = *d->table;
+        p.rot = t.rot_dim;
+        p.pairs = t.rot_dim / 2;
+        p.magnitude = t.magnitude;
+        p.positions = d->positions;
+        p.positions_stride = d->positions_stride;
+        p.offset = d->offset;
+        p.backward = d->backward ? 1 : 0;
+        std::memcpy(p.turns, t.turns, sizeof p.turns);
+    }
+    p.pass = int(D) - p.rot;
+}
+
+void add_stream(fl::RopeParams &p, const View &src, const View &dst, bool rotate, bool to_cache)
+{
+    fl::RopeStream &st = p.st[p.n_streams++];
+    st.src = src.ptr;
+    st.dst = dst.ptr;
+    st.s_b = src.stride[0];
+    st.s_s = src.stride[1];
+    st.s_h = src.stride[2];
+    st.d_b = dst.stride[0];
+    st.d_s = dst.stride[1];
+    st.d_h = dst.stride[2];
+    st.heads = int(src.size[2]);
+    st.rotate = rotate ? 1 : 0;
+    st.to_cache = to_cache ? 1 : 0;
+    p.heads += st.heads;
+}
+
+// The widest vector (in elements) that divides the rotated halves and the
+// copied rest, and to which every address of every tensor is aligned.
+int rope_vec(const fl::RopeParams &p, int elt, bool interleaved)
+{
+    for (int v = 16 / elt; v > 1; v /= 2) {
+        // a unit is V pairs: V elements of each half, or 2 V neighbours
+        bool fits = p.pairs % v == 0 && p.pass % v == 0;
+        if (interleaved)
+            fits = fits && p.rot % (2 * v) == 0;
+        else
+            fits = fits && p.rot % v == 0;
+        for (int i = 0; fits && i < p.n_streams; ++i) {
+            const fl::RopeStream &st = p.st[i];
+            for (int64_t s : {st.s_b, st.s_s, st.s_h, st.d_b, st.d_s, st.d_h})
+                fits = fits && s % v == 0;
+            for (const void *q : {st.src, static_cast<const void *>(st.dst)})
+                fits = fits && reinterpret_cast<uintptr_t>(q) % (size_t(v) * elt) == 0;
+        }
+        if (fits)
+            return v;
+    }
+    return 1;
+}
+
+bool in_place(const View &a, const View &b)
+{
+    if (a.ptr != b.ptr)
+        return false;
+    for (int d = 0; d < a.ndim; ++d)
+        if (a.size[d] > 1 && a.stride[d] != b.stride[d])
+            return false;
+    return true;
+}
+
+// ------------------------------------------------------------------ chunks over a cache
+
+struct ChunkPlan {
+    View Q, K, V;
+    int64_t T, Hq, Hk, D, P, page;
+    size_t total;
+};
+
+fl_status chunk_plan(const fl_tensor *q, const fl_tensor *k_cache, const fl_tensor *v_cache,
+                     const fl_chunk_desc *d, ChunkPlan &pl)
+{
+    fl_status s;
+    if (!d)
+        return fail(FL_ERR_INVALID_ARG, "desc is NULL");
+    if ((s = check_tensor(q, "q", 3, FL_BF16, pl.Q)) != FL_OK) return s;
+    if ((s = check_tensor(k_cache, "k_cache", 4, FL_BF16, pl.K)) != FL_OK) return s;
+    if (v_cache) {
+        if ((s = check_tensor(v_cache, "v_cache", 4, FL_BF16, pl.V)) != FL_OK) return s;
+        if (!same(pl.V, {pl.K.size[0], pl.K.size[1], pl.K.size[2], pl.K.size[3]}))
+            return fail(FL_ERR_INVALID_ARG, "v_cache must have the shape of k_cache");
+    }
+    pl.T = pl.Q.size[0];
+    pl.Hq = pl.Q.size[1];
+    pl.D = pl.Q.size[2];
+    pl.P = pl.K.size[0];
+    pl.page = pl.K.size[1];
+    pl.Hk = pl.K.size[2];
+    if (pl.K.size[3] != pl.D)
+        return fail(FL_ERR_INVALID_ARG, "the caches must have q's head dimension");
+    if (pl.D != 64 && pl.D != 128)
+        return fail(FL_ERR_UNSUPPORTED, "chunks support head dimension 64 or 128 (got %lld)", (long long)pl.D);
+    if (pl.Hq % pl.Hk != 0)
+        return fail(FL_ERR_INVALID_ARG, "Hq (%lld) must be a multiple of Hk (%lld)", (long long)pl.Hq,
+                    (long long)pl.Hk);
+    if (pl.Hq / pl.Hk > fl::BM)
+        return fail(FL_ERR_UNSUPPORTED, "Hq / Hk = %lld exceeds %d", (long long)(pl.Hq / pl.Hk), fl::BM);
+    if (d->batch < 1)
+        return fail(FL_ERR_INVALID_ARG, "batch must be >= 1");
+    if (d->max_kv_len < 1)
+        return fail(FL_ERR_INVALID_ARG, "max_kv_len must be >= 1");
+    if (d->window < 0 || (d->window > 0 && !d->causal))
+        return fail(FL_ERR_INVALID_ARG, "window must be >= 0, and 0 without causal");
+    if (d->score_mod != FL_MOD_NONE && d->score_mod != FL_MOD_SOFTCAP)
+        return fail(FL_ERR_UNSUPPORTED, "chunks support score_mod none or softcap");
+    if (d->score_mod == FL_MOD_SOFTCAP && !(d->softcap > 0.f && std::isfinite(d->softcap)))
+        return fail(FL_ERR_INVALID_ARG, "softcap must be positive and finite");
+    if (!std::isfinite(d->scale) || d->scale < 0.f)
+        return fail(FL_ERR_INVALID_ARG, "scale must be finite and positive (0 selects 1/sqrt(D))");
+    if (!d->block_table) {
+        if (pl.P != d->batch)
+            return fail(FL_ERR_INVALID_ARG, "a contiguous cache is [batch, S_max, Hk, D]");
+        if (d->max_kv_len > pl.page)
+            return fail(FL_ERR_INVALID_ARG, "max_kv_len %d exceeds the cache length %lld", d->max_kv_len,
+                        (long long)pl.page);
+    } else {
+        if (pl.page != 16 && pl.page != 32 && pl.page != 64 && pl.page != 128 && pl.page != 256)
+            return fail(FL_ERR_UNSUPPORTED, "page size %lld: must be 16, 32, 64, 128 or 256",
+                        (long long)pl.page);
+        if (int64_t(d->block_table_stride) * pl.page < d->max_kv_len)
+            return fail(FL_ERR_INVALID_ARG, "block_table_stride %d pages cannot hold %d keys",
+                        d->block_table_stride, d->max_kv_len);
+        if (reinterpret_cast<uintptr_t>(d->block_table) % 4)
+            return fail(FL_ERR_ALIGNMENT, "block_table is not 4-byte aligned");
+    }
+    pl.total = kWsAlign;
+    return FL_OK;
+}
+
+// [a, a + n) and [b, b + m) share bytes
+bool overlap(const void *a, size_t n, const void *b, size_t m)
+{
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + m && y < x + n;
+}
+
 } // namespace
 
 extern "C" {
@@ -1506,5 +1691,359 @@ const char *fl_attn_status_string(fl_status s)
 const char *fl_attn_last_error(void) { return g_last_error; }
 
 int32_t fl_attn_version(void) { return FL_ATTN_VERSION; }
+
+// ------------------------------------------------------------------ rotary positions and serving steps
+
+fl_status fl_rope_make_table(const fl_rope_config *config, fl_rope_table *table)
+{
+    if (!config || !table)
+        return fail(FL_ERR_INVALID_ARG, "NULL argument");
+    const fl_rope_config &c = *config;
+    if (c.rot_dim < 2 || c.rot_dim % 2 || c.rot_dim > 2 * FL_ROPE_MAX_PAIRS)
+        return fail(FL_ERR_INVALID_ARG, "rot_dim must be even and within 2 .. %d", 2 * FL_ROPE_MAX_PAIRS);
+    if (c.layout != FL_ROPE_HALF && c.layout != FL_ROPE_INTERLEAVED)
+        return fail(FL_ERR_INVALID_ARG, "unknown layout %d", c.layout);
+    if (c.scaling < FL_ROPE_SCALE_NONE || c.scaling > FL_ROPE_SCALE_RAMP)
+        return fail(FL_ERR_INVALID_ARG, "unknown scaling %d", c.scaling);
+    if (!(c.base > 1.0) || !std::isfinite(c.base))
+        return fail(FL_ERR_INVALID_ARG, "base must be finite and above 1");
+    if (c.scaling != FL_ROPE_SCALE_NONE && (!(c.factor > 0.0) || !std::isfinite(c.factor)))
+        return fail(FL_ERR_INVALID_ARG, "factor must be positive and finite");
+    if (c.scaling == FL_ROPE_SCALE_BASE && c.rot_dim == 2)
+        return fail(FL_ERR_INVALID_ARG, "base scaling needs rot_dim > 2");
+    const bool blend = c.scaling == FL_ROPE_SCALE_BANDS || c.scaling == FL_ROPE_SCALE_RAMP;
+    double low = c.low, high = c.high;
+    if (low == 0.0 && high == 0.0) {
+        low = 1.0;
+        high = c.scaling == FL_ROPE_SCALE_RAMP ? 32.0 : 4.0;
+    }
+    if (blend && (!(c.context > 0.0) || !std::isfinite(c.context)))
+        return fail(FL_ERR_INVALID_ARG, "context must be positive and finite");
+    if (blend && !(low > 0.0 && low < high && std::isfinite(high)))
+        return fail(FL_ERR_INVALID_ARG, "low and high must satisfy 0 < low < high");
+    if (!std::isfinite(c.magnitude) || c.magnitude < 0.0)
+        return fail(FL_ERR_INVALID_ARG, "magnitude must be finite and positive (0 selects the default)");
+    const double two_pi = 6.283185307179586476925;
+    double base = c.base;
+    if (c.scaling == FL_ROPE_SCALE_BASE)
+        base *= std::pow(c.factor, double(c.rot_dim) / double(c.rot_dim - 2));
+    if (!(base > 1.0) || !std::isfinite(base))
+        return fail(FL_ERR_INVALID_ARG, "the scaled base must be finite and above 1");
+    double ramp_lo = 0.0, ramp_hi = 1.0;
+    if (c.scaling == FL_ROPE_SCALE_RAMP) {
+        const auto index = [&](double turns) {
+            return c.rot_dim * std::log(c.context / (turns * two_pi)) / (2.0 * std::log(base));
+        };
+        ramp_lo = std::fmax(std::floor(index(high)), 0.0);
+        ramp_hi = std::fmin(std::ceil(index(low)), double(c.rot_dim - 1));
+    }
+    fl_rope_table t{};
+    t.rot_dim = c.rot_dim;
+    t.layout = c.layout;
+    t.magnitude = static_cast<float>(c.magnitude != 0.0                  ? c.magnitude
+                                     : c.scaling == FL_ROPE_SCALE_RAMP ? 0.1 * std::log(c.factor) + 1.0
+                                                                        : 1.0);
+    for (int i = 0; i < c.rot_dim / 2; ++i) {
+        double f = std::pow(base, -2.0 * i / c.rot_dim);
+        double keep = 1.0; // share of the unscaled frequency
+        if (c.scaling == FL_ROPE_SCALE_LINEAR)
+            keep = 0.0;
+        else if (c.scaling == FL_ROPE_SCALE_BANDS)
+            keep = (c.context * f / two_pi - low) / (high - low);
+        else if (c.scaling == FL_ROPE_SCALE_RAMP)
+            keep = 1.0 - (i - ramp_lo) / std::fmax(ramp_hi - ramp_lo, 0.001);
+        keep = std::fmin(std::fmax(keep, 0.0), 1.0);
+        if (keep < 1.0)
+            f = keep * f + (1.0 - keep) * f / c.factor;
+        const double turns = std::fmod(f / two_pi, 1.0);
+        if (!std::isfinite(turns))
+            return fail(FL_ERR_INVALID_ARG, "frequency %d is not finite", i);
+        const double scaled = std::nearbyint(std::ldexp(turns, 64));
+        t.turns[i] = scaled >= 18446744073709551616.0 ? 0u : static_cast<uint64_t>(scaled);
+    }
+    t.valid = kRopeTableValid;
+    *table = t;
+    return ok();
+}
+
+fl_status fl_rope(const fl_tensor *q, const fl_tensor *k, const fl_tensor *q_out, const fl_tensor *k_out,
+                  const fl_rope_desc *desc, fl_stream_t stream)
+{
+    View Q, K, QO, KO;
+    fl_status s;
+    const int dtype = q && q->dtype == FL_F32 ? FL_F32 : FL_BF16;
+    if ((s = check_rows(q, "q", dtype, Q)) != FL_OK) return s;
+    if ((s = check_rows(q_out, "q_out", dtype, QO)) != FL_OK) return s;
+    if (!same(QO, {Q.size[0], Q.size[1], Q.size[2], Q.size[3]}) || q_out->ndim != q->ndim)
+        return fail(FL_ERR_INVALID_ARG, "q_out must have the shape of q");
+    if ((k == nullptr) != (k_out == nullptr))
+        return fail(FL_ERR_INVALID_ARG, "k and k_out must be given together");
+    if (k) {
+        if ((s = check_rows(k, "k", dtype, K)) != FL_OK) return s;
+        if ((s = check_rows(k_out, "k_out", dtype, KO)) != FL_OK) return s;
+        if (k->ndim != q->ndim || K.size[0] != Q.size[0] || K.size[1] != Q.size[1] || K.size[3] != Q.size[3])
+            return fail(FL_ERR_INVALID_ARG, "k must match q but for the number of heads");
+        if (!same(KO, {K.size[0], K.size[1], K.size[2], K.size[3]}) || k_out->ndim != k->ndim)
+            return fail(FL_ERR_INVALID_ARG, "k_out must have the shape of k");
+    }
+    const int64_t D = Q.size[3], heads = Q.size[2] + (k ? K.size[2] : 0);
+    if ((s = check_rope(desc, D)) != FL_OK) return s;
+    if (Q.size[0] * Q.size[1] >= (int64_t(1) << 31) || heads * D >= (int64_t(1) << 24))
+        return fail(FL_ERR_UNSUPPORTED, "2^31 tokens or 2^24 elements of a token, or more");
+    int dev;
+    DeviceInfo info;
+    if ((s = device_info(dev, info)) != FL_OK) return s;
+    fl::RopeParams p{};
+    set_rope(p, desc, D);
+    p.tokens = int(Q.size[0] * Q.size[1]);
+    p.div_seq = fl::make_fastdiv(int32_t(Q.size[1]));
+    add_stream(p, Q, QO, true, false);
+    if (k)
+        add_stream(p, K, KO, true, false);
+    const bool interleaved = desc->table->layout == FL_ROPE_INTERLEAVED, fp32 = dtype == FL_F32;
+    const int vec = rope_vec(p, fp32 ? 4 : 2, interleaved);
+    if (in_place(Q, QO) && (!k || in_place(K, KO)))
+        p.pass = 0; // the copied elements are where they belong
+    const cudaError_t e = fl::launch_rope(p, fp32, interleaved, vec, info.sm_count,
+                                          reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess)
+        return fail(FL_ERR_CUDA, "kernel launch failed: %s", cudaGetErrorString(e));
+    return ok();
+}
+
+fl_status fl_kv_append(const fl_tensor *q, const fl_tensor *k, const fl_tensor *v, const fl_tensor *q_out,
+                       const fl_tensor *k_cache, const fl_tensor *v_cache, const int64_t *slots,
+                       const fl_rope_desc *rope, fl_stream_t stream)
+{
+    View Q, K, V, QO, KC, VC;
+    fl_status s;
+    if ((s = check_tensor(k, "k", 3, FL_BF16, K)) != FL_OK) return s;
+    if ((s = check_tensor(v, "v", 3, FL_BF16, V)) != FL_OK) return s;
+    if ((s = check_tensor(k_cache, "k_cache", 4, FL_BF16, KC)) != FL_OK) return s;
+    if ((s = check_tensor(v_cache, "v_cache", 4, FL_BF16, VC)) != FL_OK) return s;
+    const int64_t T = K.size[0], Hk = K.size[1], D = K.size[2];
+    if (!same(V, {T, Hk, D}))
+        return fail(FL_ERR_INVALID_ARG, "v must have the shape of k");
+    if (KC.size[2] != Hk || KC.size[3] != D)
+        return fail(FL_ERR_INVALID_ARG, "k_cache must be [num_pages, page_size, Hk, D] matching k");
+    if (!same(VC, {KC.size[0], KC.size[1], Hk, D}))
+        return fail(FL_ERR_INVALID_ARG, "v_cache must have the shape of k_cache");
+    if ((q == nullptr) != (q_out == nullptr))
+        return fail(FL_ERR_INVALID_ARG, "q and q_out must be given together");
+    if (q) {
+        if ((s = check_rows(q, "q", FL_BF16, Q)) != FL_OK) return s;
+        if ((s = check_rows(q_out, "q_out", FL_BF16, QO)) != FL_OK) return s;
+        if (q->ndim != 3 || q_out->ndim != 3 || Q.size[1] != T || Q.size[3] != D)
+            return fail(FL_ERR_INVALID_ARG, "q must be [T, Hq, D] matching k");
+        if (!same(QO, {1, T, Q.size[2], D}))
+            return fail(FL_ERR_INVALID_ARG, "q_out must have the shape of q");
+    }
+    if (!slots)
+        return fail(FL_ERR_INVALID_ARG, "slots is NULL");
+    if (reinterpret_cast<uintptr_t>(slots) % 8)
+        return fail(FL_ERR_ALIGNMENT, "slots is not 8-byte aligned");
+    if (rope) {
+        if ((s = check_rope(rope, D)) != FL_OK) return s;
+        if (!rope->positions)
+            return fail(FL_ERR_INVALID_ARG, "rope->positions is NULL");
+        if (rope->backward)
+            return fail(FL_ERR_INVALID_ARG, "the append rotates forward only");
+    }
+    if (((q ? Q.size[2] : 0) + 2 * Hk) * D >= (int64_t(1) << 24))
+        return fail(FL_ERR_UNSUPPORTED, "2^24 elements of a token, or more");
+    int dev;
+    DeviceInfo info;
+    if ((s = device_info(dev, info)) != FL_OK) return s;
+    View K4 = K, V4 = V; // as one batch
+    for (View *x : {&K4, &V4}) {
+        for (int d = 3; d > 0; --d) {
+            x->size[d] = x->size[d - 1];
+            x->stride[d] = x->stride[d - 1];
+        }
+        x->size[0] = 1;
+        x->stride[0] = 0;
+        x->ndim = 4;
+    }
+    fl::RopeParams p{};
+    set_rope(p, rope, D);
+    p.tokens = int(T);
+    p.div_seq = fl::make_fastdiv(int32_t(T));
+    p.div_tile_page = fl::make_fastdiv(int32_t(KC.size[1]));
+    p.slots = slots;
+    p.n_slots = KC.size[0] * KC.size[1];
+    if (q)
+        add_stream(p, Q, QO, rope != nullptr, false);
+    add_stream(p, K4, KC, rope != nullptr, true);
+    add_stream(p, V4, VC, false, true);
+    const bool interleaved = rope && rope->table->layout == FL_ROPE_INTERLEAVED;
+    const int vec = rope_vec(p, 2, interleaved);
+    const cudaError_t e = fl::launch_rope(p, false, interleaved, vec, info.sm_count,
+                                          reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess)
+        return fail(FL_ERR_CUDA, "kernel launch failed: %s", cudaGetErrorString(e));
+    return ok();
+}
+
+fl_status fl_kv_plan(const fl_kv_plan_desc *d, fl_stream_t stream)
+{
+    if (!d)
+        return fail(FL_ERR_INVALID_ARG, "desc is NULL");
+    if (d->batch < 1)
+        return fail(FL_ERR_INVALID_ARG, "batch must be >= 1");
+    if (d->max_tokens < 0 || d->n_free < 0 || d->block_table_stride < 1)
+        return fail(FL_ERR_INVALID_ARG, "max_tokens and n_free must be >= 0, block_table_stride >= 1");
+    int shift = 4;
+    while (shift < 8 && (1 << shift) != d->page_size)
+        ++shift;
+    if ((1 << shift) != d->page_size)
+        return fail(FL_ERR_UNSUPPORTED, "page size %d: must be 16, 32, 64, 128 or 256", d->page_size);
+    const struct {
+        const void *ptr;
+        const char *name;
+        bool optional;
+    } args[] = {{d->q_lens, "q_lens", false},
+                {d->kv_lens, "kv_lens", false},
+                {d->free_pages, "free_pages", d->n_free == 0},
+                {d->free_head, "free_head", false},
+                {d->block_table, "block_table", false},
+                {d->kv_lens_out, "kv_lens_out", false},
+                {d->cu_q, "cu_q", false},
+                {d->positions, "positions", d->max_tokens == 0},
+                {d->free_head_out, "free_head_out", false}};
+    for (const auto &a : args) {
+        if (!a.ptr && !a.optional)
+            return fail(FL_ERR_INVALID_ARG, "%s is NULL", a.name);
+        if (reinterpret_cast<uintptr_t>(a.ptr) % 4)
+            return fail(FL_ERR_ALIGNMENT, "%s is not 4-byte aligned", a.name);
+    }
+    if (reinterpret_cast<uintptr_t>(d->slots) % 8)
+        return fail(FL_ERR_ALIGNMENT, "slots is not 8-byte aligned");
+    // every block reads the lengths and the head while one of them writes the new ones
+    const size_t lens = size_t(d->batch) * 4;
+    if (overlap(d->kv_lens, lens, d->kv_lens_out, lens) || overlap(d->q_lens, lens, d->kv_lens_out, lens))
+        return fail(FL_ERR_INVALID_ARG, "kv_lens_out must not overlap kv_lens or q_lens");
+    if (overlap(d->kv_lens, lens, d->cu_q, lens + 4) || overlap(d->q_lens, lens, d->cu_q, lens + 4))
+        return fail(FL_ERR_INVALID_ARG, "cu_q must not overlap kv_lens or q_lens");
+    if (d->free_head == d->free_head_out)
+        return fail(FL_ERR_INVALID_ARG, "free_head_out must not be free_head");
+    int dev;
+    DeviceInfo info;
+    fl_status s;
+    if ((s = device_info(dev, info)) != FL_OK) return s;
+    fl::KvPlanParams p{};
+    p.batch = d->batch;
+    p.max_tokens = d->max_tokens;
+    p.n_free = d->n_free;
+    p.bt_stride = d->block_table_stride;
+    p.page_shift = shift;
+    p.q_lens = d->q_lens;
+    p.kv_lens = d->kv_lens;
+    p.free_pages = d->free_pages;
+    p.free_head = d->free_head;
+    p.block_table = d->block_table;
+    p.kv_out = d->kv_lens_out;
+    p.cu_q = d->cu_q;
+    p.positions = d->positions;
+    p.head_out = d->free_head_out;
+    p.slots = d->slots;
+    p.err_user = d->error_word;
+    const cudaError_t e = fl::launch_kv_plan(p, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess)
+        return fail(FL_ERR_CUDA, "kernel launch failed: %s", cudaGetErrorString(e));
+    return ok();
+}
+
+fl_status fl_attn_chunk_workspace_size(const fl_tensor *q, const fl_tensor *k_cache, const fl_chunk_desc *desc,
+                                       size_t *bytes)
+{
+    if (!bytes)
+        return fail(FL_ERR_INVALID_ARG, "bytes is NULL");
+    ChunkPlan pl;
+    const fl_status s = chunk_plan(q, k_cache, nullptr, desc, pl);
+    if (s != FL_OK)
+        return s;
+    *bytes = pl.total;
+    return ok();
+}
+
+fl_status fl_attn_chunk(const fl_tensor *q, const fl_tensor *k_cache, const fl_tensor *v_cache,
+                        const fl_tensor *out, const fl_tensor *lse, const fl_chunk_desc *desc,
+                        void *workspace, size_t workspace_bytes, fl_stream_t stream)
+{
+    if (!v_cache)
+        return fail(FL_ERR_INVALID_ARG, "v_cache is NULL");
+    ChunkPlan pl;
+    fl_status s = chunk_plan(q, k_cache, v_cache, desc, pl);
+    if (s != FL_OK)
+        return s;
+    View O, L{};
+    if ((s = check_tensor(out, "out", 3, FL_BF16, O)) != FL_OK) return s;
+    if (!same(O, {pl.T, pl.Hq, pl.D}))
+        return fail(FL_ERR_INVALID_ARG, "out must have the shape of q");
+    if (lse) {
+        if ((s = check_tensor(lse, "lse", 2, FL_F32, L)) != FL_OK) return s;
+        if (!same(L, {pl.Hq, pl.T}))
+            return fail(FL_ERR_INVALID_ARG, "lse must be [Hq, T]");
+    }
+    if (!desc->cu_q || !desc->kv_lens)
+        return fail(FL_ERR_INVALID_ARG, "cu_q or kv_lens is NULL");
+    if (reinterpret_cast<uintptr_t>(desc->cu_q) % 4 || reinterpret_cast<uintptr_t>(desc->kv_lens) % 4)
+        return fail(FL_ERR_ALIGNMENT, "cu_q or kv_lens is not 4-byte aligned");
+    if (!workspace)
+        return fail(FL_ERR_INVALID_ARG, "workspace is NULL");
+    if (reinterpret_cast<uintptr_t>(workspace) % kWsAlign)
+        return fail(FL_ERR_ALIGNMENT, "workspace is not %zu-byte aligned", kWsAlign);
+    if (workspace_bytes < pl.total)
+        return fail(FL_ERR_INVALID_ARG, "workspace holds %zu bytes, %zu needed", workspace_bytes, pl.total);
+    int dev;
+    DeviceInfo info;
+    if ((s = device_info(dev, info)) != FL_OK) return s;
+    fl::ChunkParams p{};
+    p.T = int(pl.T);
+    p.batch = desc->batch;
+    p.Hq = int(pl.Hq);
+    p.Hk = int(pl.Hk);
+    p.G = int(pl.Hq / pl.Hk);
+    p.head_dim = int(pl.D);
+    p.max_kv = desc->max_kv_len;
+    p.page_shift = -1;
+    if (desc->block_table)
+        for (p.page_shift = 4; (1 << p.page_shift) != pl.page;)
+            ++p.page_shift;
+    p.bt_stride = desc->block_table_stride;
+    p.cu_q = desc->cu_q;
+    p.kv_lens = desc->kv_lens;
+    p.block_table = desc->block_table;
+    p.causal = desc->causal ? 1 : 0;
+    p.window = desc->window;
+    p.score_mod = desc->score_mod;
+    p.scale = desc->scale != 0.f ? desc->scale : 1.0f / std::sqrt(float(pl.D));
+    p.softcap = desc->softcap;
+    p.q = static_cast<const __nv_bfloat16 *>(pl.Q.ptr);
+    p.q_st = pl.Q.stride[0];
+    p.q_sh = pl.Q.stride[1];
+    p.k = static_cast<const __nv_bfloat16 *>(pl.K.ptr);
+    p.k_sp = pl.K.stride[0];
+    p.k_sr = pl.K.stride[1];
+    p.k_sh = pl.K.stride[2];
+    p.v = static_cast<const __nv_bfloat16 *>(pl.V.ptr);
+    p.v_sp = pl.V.stride[0];
+    p.v_sr = pl.V.stride[1];
+    p.v_sh = pl.V.stride[2];
+    p.n_pages = pl.P;
+    p.out = static_cast<__nv_bfloat16 *>(O.ptr);
+    p.o_st = O.stride[0];
+    p.o_sh = O.stride[1];
+    if (lse) {
+        p.lse = static_cast<float *>(L.ptr);
+        p.l_sh = L.stride[0];
+    }
+    p.err_user = desc->error_word;
+    p.timeout_ns = uint64_t(desc->wait_timeout_us ? desc->wait_timeout_us : 2000000u) * 1000ull;
+    const cudaError_t e = fl::launch_chunk(p, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess)
+        return fail(FL_ERR_CUDA, "kernel launch failed: %s", cudaGetErrorString(e));
+    return ok();
+}
 
 } // extern "C"

@@ -226,4 +226,75 @@ cudaError_t launch_standard_expr(const CUtensorMap &tq, const CUtensorMap &tk, c
                                  char *err, size_t err_n);
 #endif
 
+// ---- rotary positions and the cache append (rope.cu)
+// One tensor's way through the kernel: `heads` heads of every token from src
+// to dst (element strides; the batch and sequence strides of dst are the page
+// and row strides for a tensor that goes to the cache).
+struct RopeStream {
+    const void *src;
+    void *dst;
+    int64_t s_b, s_s, s_h;
+    int64_t d_b, d_s, d_h;
+    int heads;
+    int rotate;   // 0: copied
+    int to_cache; // dst row by slot instead of by token
+};
+
+struct RopeParams {
+    RopeStream st[3];
+    int n_streams, heads;      // heads: of all streams
+    int tokens;                // B * S
+    int tile;                  // tokens per block
+    int pairs, pass;           // rotated pairs and copied elements of a head
+    int rot;
+    int units;                 // vector units of a head
+    FastDiv div_units, div_head_units, div_seq, div_tile_page;
+    const int32_t *positions;  // [B][positions_stride] or null
+    int64_t positions_stride;
+    int64_t offset;
+    const int64_t *slots;      // [tokens] or null
+    int64_t n_slots;           // rows of the cache
+    int backward;
+    float magnitude;
+    uint64_t turns[128];
+};
+
+// ---- the book-keeping of a serving step (kv_plan.cu)
+struct KvPlanParams {
+    int batch, max_tokens, n_free, bt_stride;
+    int page_shift;
+    const int32_t *q_lens, *kv_lens, *free_pages, *free_head;
+    int32_t *block_table, *kv_out, *cu_q, *positions, *head_out;
+    int64_t *slots;
+    uint32_t *err_user;
+};
+
+// ---- attention of ragged chunks over the cache (fwd_chunk.cu)
+struct ChunkParams {
+    int T, batch, Hq, Hk, G, head_dim;
+    int max_kv, page_shift;    // page_shift < 0: contiguous cache
+    int64_t bt_stride;
+    const int32_t *cu_q, *kv_lens, *block_table;
+    int causal, window;        // window 0: none
+    int score_mod;
+    float scale, softcap;
+    const __nv_bfloat16 *q, *k, *v; // element strides: q (token, head), caches (page, row, head)
+    int64_t q_st, q_sh, k_sp, k_sr, k_sh, v_sp, v_sr, v_sh;
+    int64_t n_pages;
+    __nv_bfloat16 *out;
+    int64_t o_st, o_sh;
+    float *lse;                // [Hq, T] or null
+    int64_t l_sh;
+    uint32_t *err_user;
+    uint64_t timeout_ns;
+};
+
+#ifndef __CUDACC_RTC__
+// vec: elements per vector access (a power of two up to 16 bytes' worth)
+cudaError_t launch_rope(const RopeParams &p, bool fp32, bool interleaved, int vec, int sm_count,
+                        cudaStream_t stream);
+cudaError_t launch_kv_plan(const KvPlanParams &p, cudaStream_t stream);
+cudaError_t launch_chunk(const ChunkParams &p, cudaStream_t stream);
+#endif
+
 }  // namespace fl

@@ -132,6 +132,8 @@ typedef enum {
 
 /* Bits the kernel ORs into error_word. */
 #define FL_DEVERR_TIMEOUT 0x1u        /* a bounded wait ran out; the CTA quit cleanly */
+#define FL_DEVERR_PAGES 0x2u          /* fl_kv_plan: a new token got no page (slot -1) */
+#define FL_DEVERR_LENGTHS 0x4u        /* lengths on the device exceed what the host stated */
 #define FL_DEVERR_WHERE_SHIFT 8       /* bits 8..15: which wait (diagnostic) */
 
 typedef struct {
@@ -380,6 +382,185 @@ fl_status fl_attn_decode_static(const fl_tensor *q, const fl_tensor *k_cache,
                                 const fl_tensor *v_cache, const fl_tensor *out,
                                 const fl_tensor *lse, const fl_decode_desc *desc,
                                 fl_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Rotary positions.
+ *
+ * Pair i of a head's first rot_dim elements turns by the angle pos * f_i and
+ * is multiplied by a magnitude m:
+ *     y_a = m (x_a cos t - x_b sin t),  y_b = m (x_a sin t + x_b cos t),  t = pos f_i
+ * with (a, b) = (i, i + rot_dim / 2) (FL_ROPE_HALF) or (2 i, 2 i + 1)
+ * (FL_ROPE_INTERLEAVED); elements from rot_dim on are copied.  The backward
+ * turns the other way, with the same m.  The frequencies are
+ * f_i = base^(-2 i / rot_dim), stretched for contexts longer than the trained
+ * `context` by one of
+ *     LINEAR  f_i / factor
+ *     BASE    base replaced by base * factor^(rot_dim / (rot_dim - 2))
+ *     BANDS   by the turns n_i = context f_i / 2 pi a pair makes in the
+ *             trained context: f_i where n_i >= high, f_i / factor where
+ *             n_i <= low, w f_i + (1 - w) f_i / factor between, with
+ *             w = (n_i - low) / (high - low)
+ *     RAMP    by the pair's index: the same blend, w falling linearly from 1
+ *             at index floor(d(high)) to 0 at ceil(d(low)) (clamped to
+ *             [0, rot_dim - 1]), d(n) = rot_dim ln(context / 2 pi n) / (2 ln base);
+ *             m is 0.1 ln(factor) + 1 unless given
+ * Angles are exact modulo a turn at any int32 position: f_i / 2 pi is kept as
+ * a 64-bit fraction of a turn, so that pos times it wraps by itself.
+ */
+typedef enum { FL_ROPE_HALF = 0, FL_ROPE_INTERLEAVED = 1 } fl_rope_layout;
+typedef enum {
+    FL_ROPE_SCALE_NONE = 0,
+    FL_ROPE_SCALE_LINEAR = 1,
+    FL_ROPE_SCALE_BASE = 2,
+    FL_ROPE_SCALE_BANDS = 3,
+    FL_ROPE_SCALE_RAMP = 4
+} fl_rope_scaling;
+
+typedef struct {
+    int32_t rot_dim;   /* even, 2 .. 256 */
+    int32_t layout;    /* fl_rope_layout */
+    int32_t scaling;   /* fl_rope_scaling */
+    double base;       /* > 1 */
+    double factor;     /* > 0; every scaling but NONE */
+    double context;    /* trained context length (> 0); BANDS and RAMP */
+    double low, high;  /* turns, 0 < low < high; 0, 0 means 1, 4 (BANDS) or 1, 32 (RAMP) */
+    double magnitude;  /* 0 means 1, or RAMP's default */
+} fl_rope_config;
+
+#define FL_ROPE_MAX_PAIRS 128
+/* Host memory, filled by fl_rope_make_table; the caller keeps it (one per
+ * model) and every call copies it. */
+typedef struct {
+    int32_t rot_dim, layout;
+    float magnitude;
+    uint32_t valid;                    /* set by fl_rope_make_table */
+    uint64_t turns[FL_ROPE_MAX_PAIRS]; /* f_i / 2 pi modulo 1, in units of 2^-64 */
+} fl_rope_table;
+
+/* Never touches the device. */
+fl_status fl_rope_make_table(const fl_rope_config *config, fl_rope_table *table);
+
+typedef struct {
+    const fl_rope_table *table;
+    const int32_t *positions; /* NULL, or device int32: [B, S] with positions_stride elements
+                                 between the rows (0: one row for all), [T] for 3-D tensors */
+    int64_t positions_stride;
+    int32_t offset;           /* position = offset + (positions ? positions[b][s] : s) */
+    int32_t backward;         /* 1: the transposed map, for gradients of the outputs */
+} fl_rope_desc;
+
+/*
+ * fl_rope -- rotary positions of q and, unless NULL, k in one launch.
+ *   q, q_out [B, S, Hq, D], k, k_out [B, S, Hk, D], or [T, Hq, D] and
+ *   [T, Hk, D] (rows of any batch one after another); bf16 or fp32, all the
+ *   same; rot_dim <= D.  An output may be its input (same pointer and
+ *   strides); other overlaps are undefined.  Arithmetic is fp32 on the fp32
+ *   sine and cosine, rounded once.
+ */
+fl_status fl_rope(const fl_tensor *q, const fl_tensor *k, const fl_tensor *q_out,
+                  const fl_tensor *k_out, const fl_rope_desc *desc, fl_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * A serving step over a paged KV cache: fl_kv_plan once per step, then per
+ * layer fl_kv_append and fl_attn_chunk (or fl_attn_decode).
+ *
+ * fl_kv_plan -- the step's book-keeping on the GPU, from request lengths.
+ * Request b holds kv_lens[b] keys and brings q_lens[b] new tokens (entries
+ * below 0 count as 0).  Its pages are block_table[b][0 .. ceil(kv_lens[b] /
+ * page_size)); further pages are taken from free_pages[free_head[0] ...] in
+ * the order of the requests and written to the block table.  All pointers are
+ * device memory:
+ */
+typedef struct {
+    int32_t batch;              /* B >= 1 requests */
+    int32_t page_size;          /* 16, 32, 64, 128 or 256 keys */
+    int32_t max_tokens;         /* entries of positions and slots (0: none wanted) */
+    int32_t n_free;             /* entries of free_pages */
+    int32_t block_table_stride; /* entries per row of block_table */
+    const int32_t *q_lens;      /* [B] */
+    const int32_t *kv_lens;     /* [B] */
+    const int32_t *free_pages;  /* [n_free]; may be NULL when n_free is 0 */
+    const int32_t *free_head;   /* [1]: pages of free_pages taken so far */
+    int32_t *block_table;       /* [B][block_table_stride]: new pages are written, the rest kept */
+    int32_t *kv_lens_out;       /* [B]: kv_lens + q_lens; must not overlap kv_lens */
+    int32_t *cu_q;              /* [B + 1]: first token of each request, then their number */
+    int32_t *positions;         /* [max_tokens]: position of each token in its sequence */
+    int64_t *slots;             /* [max_tokens]: page * page_size + row of its key; NULL: none */
+    int32_t *free_head_out;     /* [1]: free_head plus the pages asked for; must not be free_head */
+    uint32_t *error_word;       /* NULL, or a device word FL_DEVERR_* is ORed into */
+} fl_kv_plan_desc;
+/*
+ * Entries of positions and slots past the last token are -1 (so a captured
+ * step may be padded).  A token without a page (the free list ran out, or the
+ * block table's row is full) gets slot -1, its table entry -1, and
+ * FL_DEVERR_PAGES; tokens past max_tokens are dropped with FL_DEVERR_LENGTHS.
+ * Requests' block-table entries are taken as they are.
+ */
+fl_status fl_kv_plan(const fl_kv_plan_desc *desc, fl_stream_t stream);
+
+/*
+ * fl_kv_append -- writes the new keys and values to their slots of a paged
+ * cache, rotating q and k on the way.
+ *   q, q_out  [T, Hq, D] or both NULL; k, v [T, Hk, D]; bf16
+ *   k_cache, v_cache [num_pages, page_size, Hk, D]; any page_size
+ *   slots     device int64 [T] (fl_kv_plan's): row slots[t] % page_size of page
+ *             slots[t] / page_size; a token whose slot is outside
+ *             [0, num_pages * page_size) is skipped: nothing is written for it
+ *   rope      NULL (copies), or as in fl_rope, with positions [T] required
+ *             and not backward
+ * Slots must differ from one another: of two tokens with one slot either may
+ * win, element by element.  q_out may be q.
+ */
+fl_status fl_kv_append(const fl_tensor *q, const fl_tensor *k, const fl_tensor *v,
+                       const fl_tensor *q_out, const fl_tensor *k_cache, const fl_tensor *v_cache,
+                       const int64_t *slots, const fl_rope_desc *rope, fl_stream_t stream);
+
+/*
+ * fl_attn_chunk -- attention of ragged chunks of new tokens over the cache
+ * that holds them: prompts, parts of prompts and single tokens in one call.
+ * Request b's queries are rows cu_q[b] .. cu_q[b + 1] - 1 of q and are its
+ * last tokens: row cu_q[b] + s sits at position kv_lens[b] - n_b + s (n_b its
+ * number of rows) and sees the keys j <= that position (causal) that are less
+ * than `window` before it (window > 0), or every key j < kv_lens[b].
+ */
+typedef struct {
+    int32_t score_mod;          /* FL_MOD_NONE or FL_MOD_SOFTCAP */
+    float softcap;              /* FL_MOD_SOFTCAP: the cap (> 0) */
+    int32_t causal;             /* 1: as above; 0: every cached key */
+    int32_t window;             /* 0: no window; else needs causal */
+    float scale;                /* 0 means 1 / sqrt(D) */
+    int32_t batch;              /* B requests */
+    const int32_t *cu_q;        /* device int32 [B + 1], ascending, within 0 .. T */
+    const int32_t *kv_lens;     /* device int32 [B]: cached keys, the new ones included */
+    int32_t max_kv_len;         /* host bound on kv_lens[]; larger entries are clamped to it */
+    const int32_t *block_table; /* as in fl_decode_desc; NULL: contiguous cache */
+    int32_t block_table_stride;
+    uint32_t *error_word;       /* NULL, or a device word the kernel ORs FL_DEVERR_* into */
+    uint32_t wait_timeout_us;   /* bound of every device-side wait; 0 means 2,000,000 */
+} fl_chunk_desc;
+/*
+ * Layouts (bf16 except lse):
+ *   q, out    [T, Hq, D], D = 64 or 128, Hq a multiple of Hk, Hq / Hk <= 128
+ *   k_cache, v_cache
+ *             paged: [num_pages, page_size, Hk, D], page_size in {16, 32, 64, 128, 256};
+ *             contiguous (block_table NULL): [B, S_max, Hk, D], S_max >= max_kv_len
+ *   lse       [Hq, T] fp32 (natural log) or NULL
+ * Rows of no request (past cu_q[B]) are neither read into a result nor
+ * written.  A row that sees no key gives O = 0, LSE = -inf.  Keys and values
+ * that no row of their request sees (rows kv_lens[b] and later of the last
+ * page, keys the window has left) may hold anything; the values of the others
+ * must be finite, also where the mask hides them from some rows.
+ * Page indices outside the cache read as zero keys and values.
+ * `workspace` as for fl_attn_decode (its size depends on the shapes and on
+ * the GPU): partial results of rows whose keys were split over several SMs,
+ * merged in a fixed order, so that results do not depend on scheduling.
+ * Calls sharing one workspace must not overlap on the GPU.
+ */
+fl_status fl_attn_chunk_workspace_size(const fl_tensor *q, const fl_tensor *k_cache,
+                                       const fl_chunk_desc *desc, size_t *bytes);
+fl_status fl_attn_chunk(const fl_tensor *q, const fl_tensor *k_cache, const fl_tensor *v_cache,
+                        const fl_tensor *out, const fl_tensor *lse, const fl_chunk_desc *desc,
+                        void *workspace, size_t workspace_bytes, fl_stream_t stream);
 
 #ifdef __cplusplus
 }
