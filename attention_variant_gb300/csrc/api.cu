@@ -1079,7 +1079,8 @@ bool in_place(const View &a, const View &b)
 struct ChunkPlan {
     View Q, K, V;
     int64_t T, Hq, Hk, D, P, page;
-    size_t total;
+    int TQ, max_entries;
+    size_t starts, tickets, entries, partials, total; // offsets in the workspace, its size
 };
 
 fl_status chunk_plan(const fl_tensor *q, const fl_tensor *k_cache, const fl_tensor *v_cache,
@@ -1138,7 +1139,17 @@ fl_status chunk_plan(const fl_tensor *q, const fl_tensor *k_cache, const fl_tens
         if (reinterpret_cast<uintptr_t>(d->block_table) % 4)
             return fail(FL_ERR_ALIGNMENT, "block_table is not 4-byte aligned");
     }
-    pl.total = kWsAlign;
+    pl.TQ = fl::BM / int(pl.Hq / pl.Hk);
+    // sum over requests of ceil(n_b / 2 TQ) <= B + T / (2 TQ)
+    const int64_t entries = d->batch + pl.T / (2 * pl.TQ);
+    if (entries > (int64_t(1) << 30))
+        return fail(FL_ERR_UNSUPPORTED, "batch and tokens give more than 2^30 row blocks");
+    pl.max_entries = int(entries);
+    pl.starts = align_up(sizeof(fl::ChunkHead));
+    pl.tickets = pl.starts + align_up(fl::kChunkMaxCtas * sizeof(fl::ChunkStart));
+    pl.entries = pl.tickets + align_up(fl::kChunkMaxCtas * 8 * sizeof(int));
+    pl.partials = pl.entries + align_up(size_t(entries) * sizeof(fl::ChunkEntry));
+    pl.total = pl.partials + align_up(size_t(fl::kChunkMaxCtas) * 4 * size_t(pl.D + 4) * 128 * sizeof(float));
     return FL_OK;
 }
 
@@ -1998,13 +2009,38 @@ fl_status fl_attn_chunk(const fl_tensor *q, const fl_tensor *k_cache, const fl_t
     int dev;
     DeviceInfo info;
     if ((s = device_info(dev, info)) != FL_OK) return s;
+    const int64_t G = pl.Hq / pl.Hk;
+    CUtensorMap tq, tk, tv;
+    {
+        // TQ tokens by G heads of a KV head: the rows of a block
+        const uint64_t dims[4] = {uint64_t(pl.D), uint64_t(G), uint64_t(pl.Hk), uint64_t(pl.T)};
+        const uint64_t st[3] = {uint64_t(pl.Q.stride[1]) * 2, uint64_t(pl.Q.stride[1]) * 2 * uint64_t(G),
+                                uint64_t(pl.Q.stride[0]) * 2};
+        const uint32_t box[4] = {64, uint32_t(G), 1, uint32_t(pl.TQ)};
+        if ((s = make_map(tq, pl.Q.ptr, 4, dims, st, box, CU_TENSOR_MAP_SWIZZLE_128B, "q")) != FL_OK)
+            return s;
+    }
+    const View *src[2] = {&pl.K, &pl.V};
+    CUtensorMap *dst[2] = {&tk, &tv};
+    const char *names[2] = {"k_cache", "v_cache"};
+    for (int m = 0; m < 2; ++m) {
+        const View &C = *src[m];
+        const uint64_t dims[4] = {uint64_t(pl.D), uint64_t(pl.page), uint64_t(pl.Hk), uint64_t(pl.P)};
+        const uint64_t st[3] = {uint64_t(C.stride[1]) * 2, uint64_t(C.stride[2]) * 2, uint64_t(C.stride[0]) * 2};
+        const uint32_t box[4] = {64, 16, 1, 1};
+        if ((s = make_map(*dst[m], C.ptr, 4, dims, st, box, CU_TENSOR_MAP_SWIZZLE_128B, names[m])) != FL_OK)
+            return s;
+    }
     fl::ChunkParams p{};
     p.T = int(pl.T);
     p.batch = desc->batch;
     p.Hq = int(pl.Hq);
     p.Hk = int(pl.Hk);
-    p.G = int(pl.Hq / pl.Hk);
+    p.G = int(G);
     p.head_dim = int(pl.D);
+    p.TQ = pl.TQ;
+    p.div_g = fl::make_fastdiv(int32_t(G));
+    p.key_tile = fl::chunk_key_tile(int(pl.D));
     p.max_kv = desc->max_kv_len;
     p.page_shift = -1;
     if (desc->block_table)
@@ -2017,20 +2053,13 @@ fl_status fl_attn_chunk(const fl_tensor *q, const fl_tensor *k_cache, const fl_t
     p.causal = desc->causal ? 1 : 0;
     p.window = desc->window;
     p.score_mod = desc->score_mod;
-    p.scale = desc->scale != 0.f ? desc->scale : 1.0f / std::sqrt(float(pl.D));
-    p.softcap = desc->softcap;
-    p.q = static_cast<const __nv_bfloat16 *>(pl.Q.ptr);
-    p.q_st = pl.Q.stride[0];
-    p.q_sh = pl.Q.stride[1];
-    p.k = static_cast<const __nv_bfloat16 *>(pl.K.ptr);
-    p.k_sp = pl.K.stride[0];
-    p.k_sr = pl.K.stride[1];
-    p.k_sh = pl.K.stride[2];
-    p.v = static_cast<const __nv_bfloat16 *>(pl.V.ptr);
-    p.v_sp = pl.V.stride[0];
-    p.v_sr = pl.V.stride[1];
-    p.v_sh = pl.V.stride[2];
-    p.n_pages = pl.P;
+    const float scale = desc->scale != 0.f ? desc->scale : 1.0f / std::sqrt(float(pl.D));
+    const float log2e = 1.4426950408889634f;
+    p.qk_log2 = scale * log2e;
+    if (desc->score_mod == FL_MOD_SOFTCAP) {
+        p.softcap_in = 2.f * scale * log2e / desc->softcap;
+        p.softcap_out = desc->softcap * log2e;
+    }
     p.out = static_cast<__nv_bfloat16 *>(O.ptr);
     p.o_st = O.stride[0];
     p.o_sh = O.stride[1];
@@ -2038,9 +2067,23 @@ fl_status fl_attn_chunk(const fl_tensor *q, const fl_tensor *k_cache, const fl_t
         p.lse = static_cast<float *>(L.ptr);
         p.l_sh = L.stride[0];
     }
+    p.n_cta = info.sm_count < fl::kChunkMaxCtas ? info.sm_count : fl::kChunkMaxCtas;
+    // cost units for the even split: a key tile of two row blocks, of one, an
+    // item's start and end, and the least a CTA is woken for
+    p.cost_pair = 4;
+    p.cost_single = 2;
+    p.cost_item = 4;
+    p.cost_least = 4;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    p.max_entries = pl.max_entries;
+    p.head = reinterpret_cast<fl::ChunkHead *>(ws);
+    p.starts = reinterpret_cast<fl::ChunkStart *>(ws + pl.starts);
+    p.tickets = reinterpret_cast<int *>(ws + pl.tickets);
+    p.entries = reinterpret_cast<fl::ChunkEntry *>(ws + pl.entries);
+    p.partials = reinterpret_cast<float *>(ws + pl.partials);
     p.err_user = desc->error_word;
     p.timeout_ns = uint64_t(desc->wait_timeout_us ? desc->wait_timeout_us : 2000000u) * 1000ull;
-    const cudaError_t e = fl::launch_chunk(p, reinterpret_cast<cudaStream_t>(stream));
+    const cudaError_t e = fl::launch_chunk(tq, tk, tv, p, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess)
         return fail(FL_ERR_CUDA, "kernel launch failed: %s", cudaGetErrorString(e));
     return ok();

@@ -270,21 +270,51 @@ struct KvPlanParams {
 };
 
 // ---- attention of ragged chunks over the cache (fwd_chunk.cu)
+constexpr int kChunkMaxCtas = 160; // persistent CTAs the workspace has room for
+// Keys per K/V tile (the standard kernel's, for the same TMEM budget).
+__host__ __device__ constexpr int chunk_key_tile(int D) { return D == 128 ? 64 : 112; }
+
+// One or two row blocks of a request, as the planning kernel lists them.
+struct ChunkEntry {
+    int b, t0, n_tok, pos0;    // request, first token row, tokens, position of the first
+    int L, key_lo;             // cached keys; lowest key that the rows see
+    int lo, n_tiles;           // key tiles [lo, lo + n_tiles)
+    int tile_cost, pad;
+    int64_t cum;               // cost of everything before it, all heads
+};
+struct ChunkStart {
+    int entry, head, tile, pad; // where a CTA's part begins
+};
+struct ChunkHead {
+    int64_t total;             // cost of everything
+    int n_entries, parts;      // entries; CTAs with work
+};
+
 struct ChunkParams {
     int T, batch, Hq, Hk, G, head_dim;
+    int TQ;                    // tokens per 128-row block: 128 / G
+    FastDiv div_g;
+    int key_tile;
     int max_kv, page_shift;    // page_shift < 0: contiguous cache
     int64_t bt_stride;
     const int32_t *cu_q, *kv_lens, *block_table;
     int causal, window;        // window 0: none
     int score_mod;
-    float scale, softcap;
-    const __nv_bfloat16 *q, *k, *v; // element strides: q (token, head), caches (page, row, head)
-    int64_t q_st, q_sh, k_sp, k_sr, k_sh, v_sp, v_sr, v_sh;
-    int64_t n_pages;
-    __nv_bfloat16 *out;
+    float qk_log2;             // scale * log2(e)
+    float softcap_in;          // 2 * scale * log2(e) / cap
+    float softcap_out;         // cap * log2(e)
+    __nv_bfloat16 *out;        // element strides (token, head)
     int64_t o_st, o_sh;
     float *lse;                // [Hq, T] or null
     int64_t l_sh;
+    int n_cta;
+    int cost_pair, cost_single, cost_item, cost_least; // see api.cu
+    int max_entries;
+    ChunkHead *head;           // the workspace
+    ChunkStart *starts;        // [n_cta]
+    int *tickets;              // [n_cta][2][4]
+    ChunkEntry *entries;       // [max_entries]
+    float *partials;           // [n_cta][2][2][D + 4][128]
     uint32_t *err_user;
     uint64_t timeout_ns;
 };
@@ -294,7 +324,8 @@ struct ChunkParams {
 cudaError_t launch_rope(const RopeParams &p, bool fp32, bool interleaved, int vec, int sm_count,
                         cudaStream_t stream);
 cudaError_t launch_kv_plan(const KvPlanParams &p, cudaStream_t stream);
-cudaError_t launch_chunk(const ChunkParams &p, cudaStream_t stream);
+cudaError_t launch_chunk(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, const ChunkParams &p,
+                         cudaStream_t stream);
 #endif
 
 }  // namespace fl

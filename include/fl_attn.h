@@ -530,7 +530,8 @@ typedef struct {
     int32_t window;             /* 0: no window; else needs causal */
     float scale;                /* 0 means 1 / sqrt(D) */
     int32_t batch;              /* B requests */
-    const int32_t *cu_q;        /* device int32 [B + 1], ascending, within 0 .. T */
+    const int32_t *cu_q;        /* device int32 [B + 1], ascending, within 0 .. T (entries that are
+                                   not are clamped, with FL_DEVERR_LENGTHS) */
     const int32_t *kv_lens;     /* device int32 [B]: cached keys, the new ones included */
     int32_t max_kv_len;         /* host bound on kv_lens[]; larger entries are clamped to it */
     const int32_t *block_table; /* as in fl_decode_desc; NULL: contiguous cache */
@@ -551,8 +552,7 @@ typedef struct {
  * page, keys the window has left) may hold anything; the values of the others
  * must be finite, also where the mask hides them from some rows.
  * Page indices outside the cache read as zero keys and values.
- * `workspace` as for fl_attn_decode (its size depends on the shapes and on
- * the GPU): partial results of rows whose keys were split over several SMs,
+ * `workspace` as for fl_attn_decode: the call's plan and partial results of rows whose keys were split over several SMs,
  * merged in a fixed order, so that results do not depend on scheduling.
  * Calls sharing one workspace must not overlap on the GPU.
  */
