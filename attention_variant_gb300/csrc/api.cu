@@ -164,7 +164,7 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
 // A bf16 tensor map over dims (innermost first) with byte strides of dims 1..rank-1.
 fl_status make_map(CUtensorMap &map, void *ptr, int rank, const uint64_t *dims,
                    const uint64_t *strides_bytes, const uint32_t *box, CUtensorMapSwizzle swz,
-                   const char *what)
+                   const char *what, CUtensorMapL2promotion l2 = CU_TENSOR_MAP_L2_PROMOTION_L2_256B)
 {
     auto fn = encode_fn();
     if (!fn)
@@ -180,7 +180,7 @@ fl_status make_map(CUtensorMap &map, void *ptr, int rank, const uint64_t *dims,
     for (int d = 0; d < rank - 1; ++d)
         gs[d] = strides_bytes[d];
     CUresult r = fn(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, ptr, gd, gs, bx, es,
-                    CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, swz, l2,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS)
         return fail(FL_ERR_CUDA, "cuTensorMapEncodeTiled(%s) failed with %d", what, (int)r);
@@ -1080,7 +1080,7 @@ struct ChunkPlan {
     View Q, K, V;
     int64_t T, Hq, Hk, D, P, page;
     int TQ, max_entries;
-    size_t starts, tickets, entries, partials, total; // offsets in the workspace, its size
+    size_t joins, entries, partials, total; // offsets in the workspace (the parts come first), its size
 };
 
 fl_status chunk_plan(const fl_tensor *q, const fl_tensor *k_cache, const fl_tensor *v_cache,
@@ -1145,10 +1145,9 @@ fl_status chunk_plan(const fl_tensor *q, const fl_tensor *k_cache, const fl_tens
     if (entries > (int64_t(1) << 30))
         return fail(FL_ERR_UNSUPPORTED, "batch and tokens give more than 2^30 row blocks");
     pl.max_entries = int(entries);
-    pl.starts = align_up(sizeof(fl::ChunkHead));
-    pl.tickets = pl.starts + align_up(fl::kChunkMaxCtas * sizeof(fl::ChunkStart));
-    pl.entries = pl.tickets + align_up(fl::kChunkMaxCtas * 8 * sizeof(int));
-    pl.partials = pl.entries + align_up(size_t(entries) * sizeof(fl::ChunkEntry));
+    pl.joins = align_up(fl::kChunkMaxCtas * sizeof(fl::ChunkPart));
+    pl.entries = pl.joins + align_up(fl::kChunkMaxCtas * sizeof(fl::ChunkJoin));
+    pl.partials = pl.entries + align_up(2 * size_t(entries) * sizeof(fl::ChunkEntry));
     pl.total = pl.partials + align_up(size_t(fl::kChunkMaxCtas) * 4 * size_t(pl.D + 4) * 128 * sizeof(float));
     return FL_OK;
 }
@@ -2010,25 +2009,27 @@ fl_status fl_attn_chunk(const fl_tensor *q, const fl_tensor *k_cache, const fl_t
     DeviceInfo info;
     if ((s = device_info(dev, info)) != FL_OK) return s;
     const int64_t G = pl.Hq / pl.Hk;
-    CUtensorMap tq, tk, tv;
-    {
-        // TQ tokens by G heads of a KV head: the rows of a block
+    const int few_tq = G <= fl::kFewRows ? int(fl::kFewRows / G) : 1;
+    const int few_box = desc->block_table && pl.page < fl::kFewTile ? int(pl.page) : fl::kFewTile;
+    fl::ChunkMaps maps;
+    for (int few = 0; few < 2; ++few) {
+        // tokens by the G heads of a KV head: the rows of a block
         const uint64_t dims[4] = {uint64_t(pl.D), uint64_t(G), uint64_t(pl.Hk), uint64_t(pl.T)};
         const uint64_t st[3] = {uint64_t(pl.Q.stride[1]) * 2, uint64_t(pl.Q.stride[1]) * 2 * uint64_t(G),
                                 uint64_t(pl.Q.stride[0]) * 2};
-        const uint32_t box[4] = {64, uint32_t(G), 1, uint32_t(pl.TQ)};
-        if ((s = make_map(tq, pl.Q.ptr, 4, dims, st, box, CU_TENSOR_MAP_SWIZZLE_128B, "q")) != FL_OK)
+        const uint32_t box[4] = {64, uint32_t(G), 1, uint32_t(few ? few_tq : pl.TQ)};
+        if ((s = make_map(few ? maps.few_q : maps.q, pl.Q.ptr, 4, dims, st, box, CU_TENSOR_MAP_SWIZZLE_128B,
+                          "q")) != FL_OK)
             return s;
     }
-    const View *src[2] = {&pl.K, &pl.V};
-    CUtensorMap *dst[2] = {&tk, &tv};
-    const char *names[2] = {"k_cache", "v_cache"};
-    for (int m = 0; m < 2; ++m) {
-        const View &C = *src[m];
+    for (int m = 0; m < 4; ++m) {
+        const View &C = m % 2 ? pl.V : pl.K;
+        CUtensorMap *dst[4] = {&maps.k, &maps.v, &maps.few_k, &maps.few_v};
         const uint64_t dims[4] = {uint64_t(pl.D), uint64_t(pl.page), uint64_t(pl.Hk), uint64_t(pl.P)};
         const uint64_t st[3] = {uint64_t(C.stride[1]) * 2, uint64_t(C.stride[2]) * 2, uint64_t(C.stride[0]) * 2};
-        const uint32_t box[4] = {64, 16, 1, 1};
-        if ((s = make_map(*dst[m], C.ptr, 4, dims, st, box, CU_TENSOR_MAP_SWIZZLE_128B, names[m])) != FL_OK)
+        const uint32_t box[4] = {64, m < 2 ? 16u : uint32_t(few_box), 1, 1};
+        if ((s = make_map(*dst[m], C.ptr, 4, dims, st, box, CU_TENSOR_MAP_SWIZZLE_128B,
+                          m % 2 ? "v_cache" : "k_cache")) != FL_OK)
             return s;
     }
     fl::ChunkParams p{};
@@ -2040,7 +2041,8 @@ fl_status fl_attn_chunk(const fl_tensor *q, const fl_tensor *k_cache, const fl_t
     p.head_dim = int(pl.D);
     p.TQ = pl.TQ;
     p.div_g = fl::make_fastdiv(int32_t(G));
-    p.key_tile = fl::chunk_key_tile(int(pl.D));
+    p.few_tq = few_tq;
+    p.few_box = few_box;
     p.max_kv = desc->max_kv_len;
     p.page_shift = -1;
     if (desc->block_table)
@@ -2068,22 +2070,22 @@ fl_status fl_attn_chunk(const fl_tensor *q, const fl_tensor *k_cache, const fl_t
         p.l_sh = L.stride[0];
     }
     p.n_cta = info.sm_count < fl::kChunkMaxCtas ? info.sm_count : fl::kChunkMaxCtas;
-    // cost units for the even split: a key tile of two row blocks, of one, an
-    // item's start and end, and the least a CTA is woken for
+    // cost units for the even split: a key tile of two row blocks, of one, of
+    // few rows, an item's start and end, and the least a CTA is woken for
     p.cost_pair = 4;
-    p.cost_single = 2;
+    p.cost_single = 3;
+    p.cost_few = 2;
     p.cost_item = 4;
     p.cost_least = 4;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     p.max_entries = pl.max_entries;
-    p.head = reinterpret_cast<fl::ChunkHead *>(ws);
-    p.starts = reinterpret_cast<fl::ChunkStart *>(ws + pl.starts);
-    p.tickets = reinterpret_cast<int *>(ws + pl.tickets);
+    p.parts = reinterpret_cast<fl::ChunkPart *>(ws);
+    p.joins = reinterpret_cast<fl::ChunkJoin *>(ws + pl.joins);
     p.entries = reinterpret_cast<fl::ChunkEntry *>(ws + pl.entries);
     p.partials = reinterpret_cast<float *>(ws + pl.partials);
     p.err_user = desc->error_word;
     p.timeout_ns = uint64_t(desc->wait_timeout_us ? desc->wait_timeout_us : 2000000u) * 1000ull;
-    const cudaError_t e = fl::launch_chunk(tq, tk, tv, p, reinterpret_cast<cudaStream_t>(stream));
+    const cudaError_t e = fl::launch_chunk(maps, p, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess)
         return fail(FL_ERR_CUDA, "kernel launch failed: %s", cudaGetErrorString(e));
     return ok();

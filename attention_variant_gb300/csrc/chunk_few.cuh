@@ -1,0 +1,767 @@
+// chunk_few.cuh -- the few-row path of fwd_chunk.cu: a request whose new
+// tokens times the heads of a KV group are at most 16 rows (single tokens,
+// drafts) against all of its keys.
+//
+// Bound by HBM: every key and value is read once and meets a handful of rows.
+// So the products are turned round: S^T = K Q^T puts a key in each of the 128
+// TMEM lanes and a query row in each of 16 columns, and all lanes of the
+// softmax exponentiate however few the rows are (rows in lanes would leave
+// 124 of 128 idle for a token of a group of four heads; measured at 64
+// requests of 512 to 8192 keys: 131 us).  P^T goes to shared memory as the B
+// operand of O^T = V^T P^T, which accumulates a dimension per lane and a row
+// per column.
+//
+// What matters is bytes in flight: K and V have rings of their own (192 KB in
+// all; a K stage is free as soon as S is computed), and the two slots (a
+// softmax warpgroup each) take the tiles of two neighbouring KV heads in
+// turn, whose rows share DRAM pages and 256-byte L2 fetches (one head after
+// the other read 1.48 times the bytes).  An odd last head is slot 0's alone.
+//
+// Weights are 2^z relative to a fixed reference, 2^0: floating point keeps
+// their relative precision wherever they lie, so a running maximum is needed
+// against overflow and underflow alone.  A row starts without a reference and
+// gets 0 from the first tile that holds a key of it with z >= -kFewRange (one
+// bit a row, ORed over the slot's warps); only where a logit exceeds its
+// reference by kFewRange, or a row's first keys all lie below, do the warps
+// agree on the tile's maximum, rescale and do the tile again.  2^+-60 leaves
+// fp32 sums of 2^60 such weights in range, and what lies 2^-66 below a row's
+// largest weight does not reach its bf16 output or its LSE.
+//
+//   warp  0     walks the CTA's items, publishes them, loads Q, K, V by TMA
+//   warp  1     issues S^T of both slots
+//   warps 2, 3  issue O^T of slot 0, slot 1, after zeroing V rows that no row sees
+//   warps 4-11  the slots' softmax warpgroups
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "chunk_plan.cuh"
+#include "softmax_tile.cuh"
+
+namespace fl {
+namespace {
+
+constexpr float kFewRange = 60.f; // log2 units
+
+template <int D>
+struct FewCfg {
+    static constexpr int kBN = kFewTile;
+    static constexpr int kHalves = D / 64;
+    static constexpr int kStages = D == 128 ? 3 : 6;        // of K, and of V
+    static constexpr int kLag = D == 128 ? 1 : 2;           // tiles that V is loaded behind K
+    static_assert(kLag < kStages, "K of the lag's tiles is loaded before V frees anything");
+    static constexpr uint32_t kRowBytes = 128;              // a 64-column half row
+    static constexpr uint32_t kGroupBytes = 8 * kRowBytes;
+    static constexpr uint32_t kQHalf = kFewRows * kRowBytes;
+    static constexpr uint32_t kQBytes = kHalves * kQHalf;
+    static constexpr uint32_t kHalf = kBN * kRowBytes;      // half a K or V tile
+    static constexpr uint32_t kTileBytes = kHalves * kHalf;
+    static constexpr uint32_t kPRow = 64;                   // bytes of a key's row of P (32 rows, 16 used)
+    static constexpr uint32_t kColS = 0, kColO = 64, kStride = 32; // TMEM columns of slot t: + 32 t
+};
+
+// A CTA's part of an item.  Tiles are numbered as they pass through the
+// rings: key tile v >> shift, of head kvh + (v & 1) where shift is 1.
+struct FewItem {
+    int stop;
+    int shift;
+    int u_lo, u_hi;       // tiles of this part
+    int lo, hi;           // key tiles that any row sees
+    int heads;            // KV heads: slots in use
+    int t0, rows, pos0;   // first token row, rows, first position
+    int L, key_lo;        // cached keys; lowest key that any row sees
+    int kvh;
+    int n_parts;          // CTAs that share the item
+    int mine;             // this part's buffer: 1 if the item begins here
+};
+
+// The slot's tiles: first, first + step, ... < hi.
+struct FewTiles {
+    int first, hi, step;
+};
+__device__ __forceinline__ FewTiles few_tiles(const FewItem &it, int t)
+{
+    FewTiles f;
+    f.first = max(it.u_lo, it.lo << it.shift);
+    f.step = 1 << it.shift;
+    if (it.shift)
+        f.first += (f.first ^ t) & 1;
+    f.hi = t < it.heads ? min(it.u_hi, it.hi << it.shift) : 0;
+    return f;
+}
+
+template <int D>
+struct __align__(1024) FewSmem {
+    using C = FewCfg<D>;
+    uint8_t k[C::kStages][C::kTileBytes];
+    uint8_t v[C::kStages][C::kTileBytes];
+    uint8_t q[2][2][C::kQBytes];     // [Q buffer][slot]
+    uint8_t p[2][C::kBN * C::kPRow]; // [slot]
+    uint64_t q_full[2], q_empty[2];
+    uint64_t k_full[C::kStages], k_empty[C::kStages];
+    uint64_t v_full[C::kStages], v_empty[C::kStages];
+    uint64_t s_full[2], s_free[2], p_full[2], pv_done[2];
+    uint64_t group[2];               // the slot's softmax warps among themselves
+    uint64_t final_bar[3];
+    uint64_t info_full[kInfo], info_empty[kInfo];
+    FewItem info[kInfo];
+    float red[2][4][2 * kFewRows];   // maxima or sums of each softmax warp
+    uint32_t rows[2][2][4];          // by tile parity, of each softmax warp: see few_softmax
+    uint32_t tmem_base;
+    uint32_t abort_flag;
+};
+
+template <int D>
+struct FewCtx {
+    FewSmem<D> *sm;
+    uint32_t tmem;
+    WaitCtl wc;
+};
+
+// ------------------------------------------------------------------ producer
+
+template <int D>
+__device__ void few_producer(const FewCtx<D> &cx, const ChunkParams &p, const CUtensorMap *tm_q,
+                             const CUtensorMap *tm_k, const CUtensorMap *tm_v)
+{
+    using C = FewCfg<D>;
+    constexpr int kBN = C::kBN, kStages = C::kStages;
+    FewSmem<D> &sm = *cx.sm;
+    const uint32_t lane = ptx::lane_id();
+    uint32_t k_count = 0, v_count = 0, item_count = 0;
+    bool ok = true;
+    const ChunkPart me = p.parts[blockIdx.x];
+    const ChunkEntry *entries = p.entries + p.max_entries;
+    const int cta = static_cast<int>(blockIdx.x) - me.cta;
+    int e = me.entry, h = me.item, k = me.tile; // entry, item of it, tile of that
+    const int boxes_tile = kBN / p.few_box;
+    // lane g loads the g-th box of few_box keys of tile v into the ring's next stage
+    auto load = [&](const CUtensorMap *map, uint8_t (*ring)[C::kTileBytes], uint64_t *full, uint64_t *empty,
+                    uint32_t count, const FewItem &it, int v, int page) {
+        const uint32_t s = count % kStages;
+        if (!warp_wait(bar(empty[s]), ((count / kStages) & 1) ^ 1, cx.wc, W_KV_EMPTY))
+            return false;
+        const int key0 = (v >> it.shift) * kBN, left = it.L - key0;
+        const int boxes = left <= 0 ? 0 : min(boxes_tile, (left + p.few_box - 1) / p.few_box);
+        if (lane == 0)
+            ptx::mbar_arrive_expect_tx(bar(full[s]),
+                                       static_cast<uint32_t>(C::kHalves * boxes * p.few_box) * C::kRowBytes);
+        __syncwarp();
+        if (static_cast<int>(lane) < boxes) {
+            const int key = key0 + static_cast<int>(lane) * p.few_box;
+            const int at = p.page_shift < 0 ? key : key & ((1 << p.page_shift) - 1);
+#pragma unroll
+            for (int hf = 0; hf < C::kHalves; ++hf)
+                ptx::tma_load_4d(ptx::smem_u32(ring[s]) + hf * C::kHalf + lane * p.few_box * C::kRowBytes, map,
+                                 bar(full[s]), hf * 64, at, it.kvh + (it.shift ? v & 1 : 0), page);
+        }
+        __syncwarp();
+        return true;
+    };
+    for (;;) {
+        // ---- the next part
+        FewItem it;
+        it.stop = 1;
+        ChunkEntry en{};
+        int k_end = 0;
+        while (e < me.n_entries) {
+            en = entries[e];
+            const int full = item_heads(p, en), heads = min(full, p.Hk - h * full), n_tiles = en.n_tiles * heads;
+            const int64_t x0 = en.cum + h * item_cost(p, en);
+            if (x0 + static_cast<int64_t>(k) * en.tile_cost >= me.end) {
+                e = me.n_entries; // the cut falls before this tile
+                break;
+            }
+            if (k < n_tiles) {
+                const PartRange r = part_range(x0, n_tiles, en.tile_cost, k, me.end, me.total, cta, me.parts);
+                k_end = r.k_end;
+                it.n_parts = r.n_parts;
+                it.mine = r.first == cta ? 1 : 0;
+                it.heads = heads;
+                it.kvh = h * full;
+                it.stop = 0;
+                break;
+            }
+            k = 0; // the cut fell into the item's closing cost
+            if (++h * full >= p.Hk) {
+                h = 0;
+                ++e;
+            }
+        }
+        if (!it.stop) {
+            it.shift = it.heads - 1;
+            it.u_lo = (en.lo << it.shift) + k;
+            it.u_hi = (en.lo << it.shift) + k_end;
+            it.t0 = en.t0;
+            it.rows = en.n_tok * p.G;
+            it.pos0 = en.pos0;
+            it.L = en.L;
+            it.key_lo = en.key_lo;
+            int k0, k1;
+            key_range(p, en.L, en.pos0, en.pos0 + en.n_tok - 1, k0, k1);
+            it.lo = k0 / kBN;
+            it.hi = (max(k1, 0) + kBN - 1) / kBN;
+        }
+        const uint32_t ring = item_count & 1, slot = item_count % kInfo;
+        ok = warp_wait(bar(sm.info_empty[slot]), ((item_count / kInfo) & 1) ^ 1, cx.wc, W_INFO_EMPTY);
+        if (!ok)
+            break;
+        if (lane == 0) {
+            sm.info[slot] = it;
+            ptx::mbar_arrive(bar(sm.info_full[slot])); // release: the fields above first
+            if (!it.stop && it.mine && it.n_parts > 1)
+                p.joins[blockIdx.x] = ChunkJoin{it.n_parts, JOIN_FEW, it.kvh, {it.t0, it.t0},
+                                                {it.rows, it.heads == 2 ? it.rows : 0}, 0};
+        }
+        __syncwarp();
+        if (it.stop)
+            break;
+        // ---- Q: the rows of each head
+        ok = warp_wait(bar(sm.q_empty[ring]), ((item_count >> 1) & 1) ^ 1, cx.wc, W_Q_EMPTY);
+        if (!ok)
+            break;
+        if (lane == 0) {
+            ptx::mbar_arrive_expect_tx(bar(sm.q_full[ring]),
+                                       static_cast<uint32_t>(it.heads * C::kHalves * p.few_tq * p.G) * C::kRowBytes);
+            for (int t = 0; t < it.heads; ++t)
+#pragma unroll
+                for (int hf = 0; hf < C::kHalves; ++hf)
+                    ptx::tma_load_4d(ptx::smem_u32(sm.q[ring][t]) + hf * C::kQHalf, tm_q, bar(sm.q_full[ring]),
+                                     hf * 64, 0, it.kvh + t, it.t0);
+        }
+        __syncwarp();
+        ++item_count;
+        // ---- K and V: V trails by kLag tiles, as P V trails S, so that it does
+        // not wait in shared memory for its weights (not past the item: the next
+        // item's buffers may wait for the V of its last tile).  Pages are fetched a tile ahead.
+        const int64_t row = static_cast<int64_t>(en.b) * p.bt_stride;
+        auto page_of = [&](int j) {
+            const int key = j * kBN + static_cast<int>(lane) * p.few_box;
+            if (static_cast<int>(lane) >= boxes_tile || key >= it.L)
+                return 0;
+            return p.page_shift < 0 ? en.b : __ldg(p.block_table + row + (key >> p.page_shift));
+        };
+        int page_next = page_of(it.u_lo >> it.shift);
+        int page_v[C::kLag + 1]; // pages of the last kLag + 1 tiles, the latest first
+        for (int v = it.u_lo; v < it.u_hi + C::kLag; ++v) {
+            // K of tile v, V of tile v - kLag
+#pragma unroll
+            for (int i = C::kLag; i > 0; --i)
+                page_v[i] = page_v[i - 1];
+            page_v[0] = page_next;
+            if (v + 1 < it.u_hi)
+                page_next = page_of((v + 1) >> it.shift);
+            if (v < it.u_hi) {
+                ok = load(tm_k, sm.k, sm.k_full, sm.k_empty, k_count, it, v, page_v[0]);
+                if (!ok)
+                    break;
+                ++k_count;
+            }
+            if (v - C::kLag >= it.u_lo) {
+                ok = load(tm_v, sm.v, sm.v_full, sm.v_empty, v_count, it, v - C::kLag, page_v[C::kLag]);
+                if (!ok)
+                    break;
+                ++v_count;
+            }
+        }
+        if (!ok)
+            break;
+        // ---- on to the next item
+        k = 0;
+        if (++h * item_heads(p, en) >= p.Hk) {
+            h = 0;
+            ++e;
+        }
+    }
+    if (!ok) {
+        // wait (bounded, ignoring the abort) for this warp's own loads in flight
+        for (uint32_t idx = k_count > kStages ? k_count - kStages : 0; idx < k_count; ++idx)
+            mbar_wait_drain(bar(sm.k_full[idx % kStages]), (idx / kStages) & 1, cx.wc, W_DRAIN);
+        for (uint32_t idx = v_count > kStages ? v_count - kStages : 0; idx < v_count; ++idx)
+            mbar_wait_drain(bar(sm.v_full[idx % kStages]), (idx / kStages) & 1, cx.wc, W_DRAIN);
+        for (uint32_t n = item_count > 2 ? item_count - 2 : 0; n < item_count; ++n)
+            mbar_wait_drain(bar(sm.q_full[n & 1]), (n >> 1) & 1, cx.wc, W_DRAIN);
+    }
+}
+
+// ------------------------------------------------------------------ MMA issuers
+
+template <int D>
+__device__ void few_s_role(const FewCtx<D> &cx)
+{
+    using C = FewCfg<D>;
+    constexpr int kBN = C::kBN, kStages = C::kStages;
+    FewSmem<D> &sm = *cx.sm;
+    const uint32_t lane = ptx::lane_id();
+    constexpr uint32_t idesc = umma_idesc_bf16(kBN, kFewRows, false);
+    constexpr uint64_t kHi = umma_desc_hi(16, C::kGroupBytes, kSwizzle128B); // Q, K: K-major
+    const uint32_t q_lo0 = ptx::smem_u32(sm.q[0][0]) >> 4, k_lo0 = ptx::smem_u32(sm.k[0]) >> 4;
+    uint32_t idx = 0, issued[2] = {0u, 0u};
+    bool ok = true;
+    for (uint32_t n = 0; ok; ++n) {
+        const uint32_t ring = n & 1, slot = n % kInfo;
+        ok = warp_wait(bar(sm.info_full[slot]), (n / kInfo) & 1, cx.wc, W_INFO_FULL);
+        if (!ok)
+            break;
+        const FewItem &inf = sm.info[slot];
+        const int stop = inf.stop, shift = inf.shift, u_lo = inf.u_lo, u_hi = inf.u_hi;
+        const int lo = inf.lo << shift, hi = inf.hi << shift;
+        __syncwarp();
+        if (lane == 0)
+            ptx::mbar_arrive(bar(sm.info_empty[slot]));
+        if (stop)
+            break;
+        ok = warp_wait(bar(sm.q_full[ring]), (n >> 1) & 1, cx.wc, W_Q_FULL);
+        if (!ok)
+            break;
+        for (int v = u_lo; v < u_hi; ++v, ++idx) {
+            const uint32_t stage = idx % kStages, phase = (idx / kStages) & 1;
+            const int t = shift ? v & 1 : 0;
+            ok = warp_wait(bar(sm.k_full[stage]), phase, cx.wc, W_KV_FULL);
+            if (!ok)
+                break;
+            if (v < lo || v >= hi) { // a tile that no row sees
+                if (lane == 0)
+                    ptx::mbar_arrive(bar(sm.k_empty[stage]));
+                __syncwarp();
+                continue;
+            }
+            if (issued[t] > 0) {
+                // the softmax has copied the slot's previous S out of TMEM
+                ok = warp_wait(bar(sm.s_free[t]), (issued[t] - 1) & 1, cx.wc, W_S_FULL);
+                if (!ok)
+                    break;
+            }
+            ++issued[t];
+            ptx::tc_fence_after();
+            if (lane == 0) {
+                const uint32_t qlo = q_lo0 + (2 * ring + t) * (C::kQBytes >> 4);
+                const uint32_t klo = k_lo0 + stage * (C::kTileBytes >> 4);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk)
+                    ptx::mma_ss(cx.tmem + C::kColS + C::kStride * t,
+                                kHi | (klo + (kk / 4) * (C::kHalf >> 4) + 2 * (kk % 4)),
+                                kHi | (qlo + (kk / 4) * (C::kQHalf >> 4) + 2 * (kk % 4)), idesc, kk > 0 ? 1u : 0u);
+                ptx::mma_commit(bar(sm.s_full[t]));
+                ptx::mma_commit(bar(sm.k_empty[stage]));
+            }
+            __syncwarp();
+        }
+        if (!ok)
+            break;
+        if (lane == 0)
+            ptx::mma_commit(bar(sm.q_empty[ring])); // every read of this Q buffer issued so far
+        __syncwarp();
+    }
+    // every MMA this thread issued has completed before TMEM is released
+    const uint32_t b_final = bar(sm.final_bar[0]);
+    if (lane == 0)
+        ptx::mma_commit(b_final);
+    __syncwarp();
+    mbar_wait_drain(b_final, 0, cx.wc, W_FINAL);
+}
+
+template <int D>
+__device__ void few_pv_role(const FewCtx<D> &cx, int t)
+{
+    using C = FewCfg<D>;
+    constexpr int kBN = C::kBN, kStages = C::kStages;
+    FewSmem<D> &sm = *cx.sm;
+    const uint32_t lane = ptx::lane_id();
+    // O^T = V^T P^T: both operands with their long index contiguous.  V^T has
+    // 128 rows: at D = 64 the second 64 repeat the first (block stride 0).  P
+    // has 64-byte rows of a key, 64-byte swizzle.
+    constexpr uint32_t idesc = umma_idesc_bf16(128, kFewRows, true) | (1u << 15);
+    constexpr uint64_t kHiV = umma_desc_hi(D == 128 ? C::kHalf : 0, C::kGroupBytes, kSwizzle128B);
+    constexpr uint64_t kHiP = umma_desc_hi(16, 8 * C::kPRow, kSwizzle64B);
+    const uint32_t v_lo0 = ptx::smem_u32(sm.v[0]) >> 4, p_lo = ptx::smem_u32(sm.p[t]) >> 4;
+    const uint32_t tO = cx.tmem + C::kColO + C::kStride * t;
+    uint32_t idx = 0, pcount = 0;
+    bool ok = true;
+    for (uint32_t n = 0; ok; ++n) {
+        const uint32_t slot = n % kInfo;
+        ok = warp_wait(bar(sm.info_full[slot]), (n / kInfo) & 1, cx.wc, W_INFO_FULL);
+        if (!ok)
+            break;
+        const FewItem &inf = sm.info[slot];
+        const int stop = inf.stop, shift = inf.shift, u_lo = inf.u_lo, u_hi = inf.u_hi;
+        const int L = inf.L, key_lo = inf.key_lo;
+        const FewTiles f = few_tiles(inf, t);
+        __syncwarp();
+        if (lane == 0)
+            ptx::mbar_arrive(bar(sm.info_empty[slot]));
+        if (stop)
+            break;
+        for (int v = u_lo; v < u_hi; ++v, ++idx) {
+            const uint32_t stage = idx % kStages;
+            if ((shift ? v & 1 : 0) != t || v < f.first || v >= f.hi) {
+                // the other slot's tile, or one that no row sees: released by this
+                // warp once it has landed.  Both warps pass every tile in order, so
+                // that neither is ever a whole turn of the ring away from a barrier
+                // whose parity it waits for.
+                ok = warp_wait(bar(sm.v_full[stage]), (idx / kStages) & 1, cx.wc, W_KV_FULL);
+                if (!ok)
+                    break;
+                if (lane == 0)
+                    ptx::mbar_arrive(bar(sm.v_empty[stage]));
+                __syncwarp();
+                continue;
+            }
+            ok = warp_wait(bar(sm.v_full[stage]), (idx / kStages) & 1, cx.wc, W_KV_FULL);
+            if (!ok)
+                break;
+            // rows of V that no query row sees: zero (their P is 0, but the bytes
+            // may be anything)
+            const int j0 = (v >> shift) * kBN;
+            const int dead_lo = min(kBN, max(0, key_lo - j0)), dead_hi = min(kBN, max(0, L - j0));
+            if (dead_lo > 0 || dead_hi < kBN) {
+#pragma unroll
+                for (int hf = 0; hf < C::kHalves; ++hf) {
+                    uint4 *dst = reinterpret_cast<uint4 *>(sm.v[stage] + hf * C::kHalf);
+                    for (int c = lane; c < dead_lo * 8; c += 32)
+                        dst[c] = make_uint4(0, 0, 0, 0);
+                    for (int c = dead_hi * 8 + lane; c < kBN * 8; c += 32)
+                        dst[c] = make_uint4(0, 0, 0, 0);
+                }
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+            }
+            ok = warp_wait(bar(sm.p_full[t]), pcount & 1, cx.wc, W_P_FULL);
+            if (!ok)
+                break;
+            ++pcount;
+            ptx::tc_fence_after();
+            if (lane == 0) {
+                const uint32_t vlo = v_lo0 + stage * (C::kTileBytes >> 4);
+#pragma unroll
+                for (int kk = 0; kk < kBN / 16; ++kk)
+                    ptx::mma_ss(tO, kHiV | (vlo + kk * (16 * C::kRowBytes >> 4)),
+                                kHiP | (p_lo + kk * (16 * C::kPRow >> 4)), idesc, (v > f.first || kk > 0) ? 1u : 0u);
+                ptx::mma_commit(bar(sm.pv_done[t]));
+                ptx::mma_commit(bar(sm.v_empty[stage]));
+            }
+            __syncwarp();
+        }
+    }
+    const uint32_t b_final = bar(sm.final_bar[1 + t]);
+    if (lane == 0)
+        ptx::mma_commit(b_final);
+    __syncwarp();
+    mbar_wait_drain(b_final, 0, cx.wc, W_FINAL);
+}
+
+// ------------------------------------------------------------------ softmax
+
+// This thread's weights: 2^(c x - m), and rounded to bf16 in pairs.
+__device__ __forceinline__ void few_exp(const float (&x)[kFewRows], float c, const float (&m)[kFewRows],
+                                        float (&w)[kFewRows], uint32_t (&pk)[kFewRows / 2])
+{
+#pragma unroll
+    for (int n = 0; n < kFewRows; ++n)
+        w[n] = ptx::ex2(fmaf(x[n], c, m[n] == kNegInf ? 0.f : -m[n]));
+#pragma unroll
+    for (int n = 0; n < kFewRows; n += 2)
+        pk[n / 2] = ptx::pack_bf16(w[n], w[n + 1]);
+}
+
+// A float's order as a signed integer's.
+__device__ __forceinline__ int ordered(float x)
+{
+    const int i = __float_as_int(x);
+    return i ^ ((i >> 31) & 0x7fffffff);
+}
+__device__ __forceinline__ float unordered(int i) { return __int_as_float(i ^ ((i >> 31) & 0x7fffffff)); }
+
+template <int MOD, int D>
+__device__ void few_softmax(const FewCtx<D> &cx, const ChunkParams &p, int t)
+{
+    using C = FewCfg<D>;
+    constexpr int kBN = C::kBN, R = kFewRows;
+    FewSmem<D> &sm = *cx.sm;
+    const int r = threadIdx.x & 127; // key of the tile = TMEM lane of S^T; of O^T: dimension
+    const int wq = (threadIdx.x >> 5) & 3, lane = static_cast<int>(ptx::lane_id());
+    const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
+    const uint32_t tS = cx.tmem + lanes + C::kColS + C::kStride * t;
+    const uint32_t tO = cx.tmem + lanes + C::kColO + C::kStride * t;
+    const uint32_t b_group = bar(sm.group[t]);
+    const float c = MOD == MOD_NONE ? p.qk_log2 : 1.f;
+    // 64-byte swizzle: 16-byte unit u of key r at u ^ (r / 2 mod 4)
+    uint4 *const pdst = reinterpret_cast<uint4 *>(sm.p[t] + r * C::kPRow);
+    const int sw = (r >> 1) & 3;
+    uint32_t scount = 0, pvcount = 0, group = 0, tiles = 0;
+    ScoreMod smod;
+    smod.qk_log2 = p.qk_log2;
+    smod.softcap_in = p.softcap_in;
+    smod.softcap_out = p.softcap_out;
+    smod.alibi_c = smod.scale = smod.b = smod.h = 0.f;
+    auto group_sync = [&]() {
+        ptx::mbar_arrive(b_group);
+        return warp_wait(b_group, group++ & 1, cx.wc, W_JOIN);
+    };
+
+    for (uint32_t item = 0;; ++item) {
+        if (!warp_wait(bar(sm.info_full[item % kInfo]), (item / kInfo) & 1, cx.wc, W_INFO_FULL))
+            return;
+        const FewItem &inf = sm.info[item % kInfo];
+        if (inf.stop)
+            return;
+        if (t >= inf.heads) { // an odd head's item has no second slot
+            __syncwarp();
+            if (lane == 0)
+                ptx::mbar_arrive(bar(sm.info_empty[item % kInfo]));
+            continue;
+        }
+        const FewTiles f = few_tiles(inf, t);
+        const int n_mine = f.hi > f.first ? (f.hi - f.first + f.step - 1) / f.step : 0;
+        const int rows = inf.rows, pos0 = inf.pos0;
+        int full_lo, full_hi, unused;
+        {
+            const int last = pos0 + fast_div(rows - 1, p.div_g);
+            key_range(p, inf.L, last, last, full_lo, unused);
+            key_range(p, inf.L, pos0, pos0, unused, full_hi);
+        }
+        float m[R], l[R], lr[R];
+#pragma unroll
+        for (int n = 0; n < R; ++n) {
+            m[n] = kNegInf;
+            l[n] = lr[n] = 0.f;
+        }
+        for (int kk = 0; kk < n_mine; ++kk) {
+            if (!warp_wait(bar(sm.s_full[t]), scount & 1, cx.wc, W_S_FULL))
+                return;
+            ++scount;
+            ++tiles;
+            ptx::tc_fence_after();
+            float x[R];
+            load_scores<R>(tS, x);
+            ptx::tc_fence_before();
+            ptx::mbar_arrive(bar(sm.s_free[t]));
+            const int j0 = ((f.first + kk * f.step) >> inf.shift) * kBN;
+            apply_score_mod<MOD, R>(x, smod, 0, j0);
+            if (!(j0 >= full_lo && j0 + kBN <= full_hi)) {
+#pragma unroll
+                for (int n = 0; n < R; ++n) {
+                    int lo, hi;
+                    const int pos = pos0 + fast_div(n, p.div_g);
+                    key_range(p, inf.L, pos, pos, lo, hi);
+                    if (j0 + r < lo || j0 + r >= hi)
+                        x[n] = kNegInf;
+                }
+            }
+            // bit n: row n has a key here with z >= -kFewRange; bit 16 + n: one too large
+            // for the row's reference, or too small to be its first
+            uint32_t bits = 0;
+#pragma unroll
+            for (int n = 0; n < R; ++n) {
+                const float z = x[n] * c;
+                const bool unset = m[n] == kNegInf, large = z > (unset ? 0.f : m[n]) + kFewRange;
+                if (z >= -kFewRange)
+                    bits |= 1u << n;
+                if (large || (unset && z < -kFewRange && z > kNegInf))
+                    bits |= 0x10000u << n;
+            }
+            bits = __reduce_or_sync(0xffffffffu, bits);
+            if (lane == 0)
+                sm.rows[t][tiles & 1][wq] = bits;
+            float w[R];
+            uint32_t pk[R / 2];
+            few_exp(x, c, m, w, pk);
+            if (!group_sync())
+                return;
+            {
+                const volatile uint32_t *all = sm.rows[t][tiles & 1];
+                bits = all[0] | all[1] | all[2] | all[3];
+            }
+            if (kk > 0) {
+                // the previous tile's product has read P and landed in O^T
+                if (!warp_wait(bar(sm.pv_done[t]), pvcount & 1, cx.wc, W_O_FULL))
+                    return;
+                ++pvcount;
+                ptx::tc_fence_after();
+            }
+            // columns past the item's rows may hold anything and ask for nothing
+            const uint32_t ask = (bits >> 16) & ((1u << rows) - 1);
+            if (ask) {
+#pragma unroll
+                for (int n = 0; n < R; ++n) {
+                    const int mx = __reduce_max_sync(0xffffffffu, ordered(x[n] * c));
+                    if (lane == n)
+                        sm.red[t][wq][n] = unordered(mx);
+                }
+                if (!group_sync())
+                    return;
+                float alpha[R];
+#pragma unroll
+                for (int n = 0; n < R; ++n) {
+                    const volatile float *red = &sm.red[t][0][n];
+                    const float mx = fmaxf(fmaxf(red[0], red[2 * R]), fmaxf(red[4 * R], red[6 * R]));
+                    const float other = m[n] == kNegInf && (bits >> n & 1u) ? 0.f : m[n];
+                    const float m_new = (ask >> n & 1u) ? fmaxf(m[n], mx) : other;
+                    alpha[n] = m[n] == kNegInf ? 0.f : ptx::ex2(m[n] - m_new);
+                    m[n] = m_new;
+                    l[n] *= alpha[n];
+                    lr[n] *= alpha[n];
+                }
+                if (kk > 0) {
+                    uint32_t o[R];
+                    ptx::tmem_ld16(tO, o);
+                    ptx::tmem_wait_ld();
+                    ptx::reg_fence<16>(o);
+#pragma unroll
+                    for (int n = 0; n < R; ++n) // a row without a key so far holds zeros
+                        o[n] = __float_as_uint(__uint_as_float(o[n]) * alpha[n]);
+                    ptx::tmem_st16(tO, o);
+                    ptx::tmem_wait_st();
+                }
+                few_exp(x, c, m, w, pk);
+            } else {
+#pragma unroll
+                for (int n = 0; n < R; ++n)
+                    if (m[n] == kNegInf && (bits >> n & 1u))
+                        m[n] = 0.f;
+            }
+            pdst[0 ^ sw] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+            pdst[1 ^ sw] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+            ptx::fence_proxy_async_smem();
+            ptx::tc_fence_before();
+            ptx::mbar_arrive(bar(sm.p_full[t]));
+#pragma unroll
+            for (int n = 0; n < R; n += 2) { // the exact sum (LSE) and that of the rounded P (O)
+                ptx::add2(l[n], l[n + 1], w[n], w[n + 1]);
+                ptx::add_bf16x2_to_f32(lr[n], lr[n + 1], pk[n / 2]);
+            }
+        }
+        if (n_mine) {
+            if (!warp_wait(bar(sm.pv_done[t]), pvcount & 1, cx.wc, W_O_FULL))
+                return;
+            ++pvcount;
+            ptx::tc_fence_after();
+        }
+        // ---- the slot's sums over the warp: lane i ends with l (i < 16) or the
+        // rounded sum of row i mod 16, halving the values at each exchange
+        float v[2 * R];
+#pragma unroll
+        for (int n = 0; n < R; ++n) {
+            v[n] = l[n];
+            v[R + n] = lr[n];
+        }
+#pragma unroll
+        for (int h = R; h; h >>= 1) {
+            const bool up = lane & h;
+#pragma unroll
+            for (int i = 0; i < h; ++i)
+                v[i] = (up ? v[i + h] : v[i]) + __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i + h], h);
+        }
+        uint32_t raw[R];
+        if (n_mine) {
+            ptx::tmem_ld16(tO, raw);
+            ptx::tmem_wait_ld();
+            ptx::reg_fence<16>(raw);
+        }
+        // lane = dimension; at D = 64 the upper 64 lanes repeat the lower ones
+        // and take the odd rows
+        const int dim = D == 128 ? r : r & 63;
+        if (inf.n_parts > 1) {
+            float *mine = partial<D>(p, blockIdx.x, inf.mine, t), *sums = mine + R * 128;
+#pragma unroll
+            for (int n = 0; n < R; ++n) {
+                if (n < rows && (D == 128 || (n & 1) == r >> 6))
+                    mine[n * 128 + dim] = n_mine ? __uint_as_float(raw[n]) : 0.f;
+                if (r == n)
+                    sums[n] = m[n];
+            }
+            sums[R + wq * 2 * R + lane] = v[0];
+        } else {
+            if (!n_mine && !group_sync()) // the last item's sums have been read
+                return;
+            sm.red[t][wq][lane] = v[0];
+            if (!group_sync())
+                return;
+            const volatile float *red = sm.red[t][0];
+#pragma unroll
+            for (int n = 0; n < R; ++n) {
+                if (n >= rows || (D == 64 && (n & 1) != r >> 6))
+                    continue;
+                const float sl = red[n] + red[n + 2 * R] + red[n + 4 * R] + red[n + 6 * R];
+                const float slr = red[n + R] + red[n + 3 * R] + red[n + 5 * R] + red[n + 7 * R];
+                const int s = fast_div(n, p.div_g);
+                const int64_t tok = inf.t0 + s, head = (inf.kvh + t) * p.G + n - s * p.G;
+                join_write(p, tok, head, dim, n_mine ? __uint_as_float(raw[n]) : 0.f, slr);
+                if (dim == 0)
+                    join_lse(p, tok, head, m[n], sl);
+            }
+        }
+        __syncwarp();
+        if (lane == 0)
+            ptx::mbar_arrive(bar(sm.info_empty[item % kInfo]));
+    }
+}
+
+template <int MOD, int D>
+__device__ __forceinline__ void few_path(const ChunkMaps &maps, const ChunkParams &p, uint8_t *smem)
+{
+    using C = FewCfg<D>;
+    FewSmem<D> *sm = reinterpret_cast<FewSmem<D> *>(smem);
+    const int warp = threadIdx.x >> 5;
+    if (threadIdx.x == 0) {
+        for (int b = 0; b < 2; ++b) {
+            ptx::mbar_init(bar(sm->q_full[b]), 1);
+            ptx::mbar_init(bar(sm->q_empty[b]), 1);
+        }
+        for (int b = 0; b < kInfo; ++b) {
+            ptx::mbar_init(bar(sm->info_full[b]), 1);
+            ptx::mbar_init(bar(sm->info_empty[b]), 11); // S, two P V and eight softmax warps
+        }
+        for (int s = 0; s < C::kStages; ++s) {
+            ptx::mbar_init(bar(sm->k_full[s]), 1);
+            ptx::mbar_init(bar(sm->k_empty[s]), 1);
+            ptx::mbar_init(bar(sm->v_full[s]), 1);
+            ptx::mbar_init(bar(sm->v_empty[s]), 2); // both P V warps
+        }
+        for (int t = 0; t < 2; ++t) {
+            ptx::mbar_init(bar(sm->s_full[t]), 1);
+            ptx::mbar_init(bar(sm->s_free[t]), 128);
+            ptx::mbar_init(bar(sm->p_full[t]), 128);
+            ptx::mbar_init(bar(sm->pv_done[t]), 1);
+            ptx::mbar_init(bar(sm->group[t]), 128);
+        }
+        for (int b = 0; b < 3; ++b)
+            ptx::mbar_init(bar(sm->final_bar[b]), 1);
+        sm->abort_flag = 0;
+        ptx::fence_mbarrier_init();
+        ptx::fence_proxy_async_smem();
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc(ptx::smem_u32(&sm->tmem_base), 128);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+
+    FewCtx<D> cx;
+    cx.sm = sm;
+    cx.tmem = sm->tmem_base;
+    cx.wc = wait_ctl(p, &sm->abort_flag);
+    if (warp >= 4) {
+        few_softmax<MOD, D>(cx, p, (warp >> 2) - 1);
+        ptx::tc_fence_before();
+        ptx::named_barrier_sync(1, kThreads);
+    } else {
+        if (warp == 0)
+            few_producer(cx, p, &maps.few_q, &maps.few_k, &maps.few_v);
+        else if (warp == 1)
+            few_s_role(cx);
+        else
+            few_pv_role(cx, warp - 2);
+        ptx::tc_fence_before();
+        ptx::named_barrier_sync(1, kThreads);
+        if (warp == 1) {
+            ptx::tc_fence_after();
+            ptx::tmem_dealloc(cx.tmem, 128);
+        }
+    }
+}
+
+} // namespace
+} // namespace fl

@@ -1,0 +1,455 @@
+// chunk_plan.cuh -- how the work of a ragged chunk call is cut up
+// (fwd_chunk.cu): the planning kernel, and what both attention paths share.
+//
+// Two lists: row blocks (entries of one or two blocks of TQ = 128 / G tokens)
+// and few rows (requests whose tokens times G are at most kFewRows).  An
+// entry's items are its KV heads -- pairs of KV heads on the few-row list,
+// the last of an odd number by itself -- and an item's tiles its key tiles
+// (times heads).  A list is one long line of tiles with a cost each; it is cut
+// into equal parts, one a CTA, and the CTAs are shared between the lists by
+// cost.
+#pragma once
+
+#include "common.cuh"
+#include "fl_attn.h"
+#include "launch.h"
+
+namespace fl {
+namespace {
+
+constexpr int kThreads = 384;
+constexpr uint32_t kRegsLaunch = 168;
+constexpr uint32_t kRegsSoftmax = 200;
+constexpr uint32_t kRegsOther = 104;
+static_assert(2 * 128 * kRegsSoftmax + 128 * kRegsOther == kThreads * kRegsLaunch,
+              "register split must equal the launch allocation");
+constexpr int kInfo = 4; // items published ahead of the slowest role
+
+__device__ uint32_t g_lib_error_word;
+
+__device__ __forceinline__ uint32_t bar(const uint64_t &b) { return ptx::smem_u32(&b); }
+
+__device__ __forceinline__ WaitCtl wait_ctl(const ChunkParams &p, uint32_t *abort_flag)
+{
+    WaitCtl wc;
+    wc.abort_flag = abort_flag;
+    wc.timeout_cycles = p.timeout_ns * 21 / 10; // 2.1 cycles per ns at the maximum clock
+    wc.err_user = p.err_user;
+    wc.err_lib = &g_lib_error_word;
+    return wc;
+}
+
+// Keys [lo, hi) that the tokens at positions first .. last see.
+__device__ __forceinline__ void key_range(const ChunkParams &p, int L, int first, int last, int &lo, int &hi)
+{
+    lo = p.window ? max(0, first - p.window + 1) : 0;
+    hi = p.causal ? min(L, last + 1) : L;
+}
+
+__device__ __forceinline__ bool is_few(const ChunkParams &p, int n_tok) { return n_tok * p.G <= kFewRows; }
+
+// KV heads of an entry's items (the last may have fewer).
+__device__ __forceinline__ int item_heads(const ChunkParams &p, const ChunkEntry &en)
+{
+    return is_few(p, en.n_tok) && p.Hk > 1 ? 2 : 1;
+}
+
+// Cost of an item with its full number of heads; an odd head's is less, but
+// it comes last in its entry, so positions divide by this.
+__device__ __forceinline__ int64_t item_cost(const ChunkParams &p, const ChunkEntry &en)
+{
+    return static_cast<int64_t>(en.n_tiles) * item_heads(p, en) * en.tile_cost + p.cost_item;
+}
+
+__device__ __forceinline__ int64_t entry_cost(const ChunkParams &p, const ChunkEntry &en)
+{
+    const int heads = item_heads(p, en);
+    return static_cast<int64_t>(en.n_tiles) * p.Hk * en.tile_cost +
+           static_cast<int64_t>((p.Hk + heads - 1) / heads) * p.cost_item;
+}
+
+// Part c of `parts` covers the cost units x with c total / parts <= x <
+// (c + 1) total / parts, and a tile belongs to the part of its first unit.
+struct PartRange {
+    int k_end;          // the part's tiles of the item: k .. k_end - 1
+    int first, n_parts; // the item's first part and number of parts
+};
+
+__device__ __forceinline__ PartRange part_range(int64_t x0, int n_tiles, int tile_cost, int k, int64_t x_end,
+                                                int64_t total, int part, int parts)
+{
+    PartRange r;
+    r.k_end = static_cast<int>(min(static_cast<int64_t>(n_tiles), (x_end - x0 + tile_cost - 1) / tile_cost));
+    r.first = k == 0 ? part : static_cast<int>(x0 * parts / total);
+    const int last = r.k_end == n_tiles
+                         ? part
+                         : static_cast<int>((x0 + static_cast<int64_t>(n_tiles - 1) * tile_cost) * parts / total);
+    r.n_parts = last - r.first + 1;
+    return r;
+}
+
+// Layouts of an item's partial results (one buffer a slot):
+//   JOIN_PAIR   the slot's own rows: [D columns][128 rows]
+//   JOIN_HALF   one row block, the slot's half of the columns: [D / 2][128]
+//               then, for both, m, l and the sum of the rounded P: [3][128]
+//   JOIN_FEW    [16 rows][128 dimensions], m [16], then a warp's sums of l and
+//               of the rounded P: [4 warps][2][16]
+enum : int { JOIN_PAIR = 0, JOIN_HALF = 1, JOIN_FEW = 2 };
+
+// Floats of one slot's buffer, and the place of a slot's buffer of a CTA
+// (buffer 1: the item begins in that CTA, 0: it began before).
+template <int D>
+__device__ __forceinline__ float *partial(const ChunkParams &p, int cta, int buf, int slot)
+{
+    return p.partials + (static_cast<int64_t>(cta * 2 + buf) * 2 + slot) * ((D + 4) * 128);
+}
+
+// ------------------------------------------------------------------ planning
+
+constexpr int kPlanThreads = 1024;
+
+// What one scan of the planning kernel adds up: places on the two lists
+// (16 bits each; at most kPlanThreads a round) and costs.
+struct PlanSum {
+    int places;
+    int64_t cost[2];
+};
+__device__ __forceinline__ PlanSum operator+(const PlanSum &a, const PlanSum &b)
+{
+    return PlanSum{a.places + b.places, {a.cost[0] + b.cost[0], a.cost[1] + b.cost[1]}};
+}
+__device__ __forceinline__ int shfl_up(int x, int d) { return __shfl_up_sync(0xffffffffu, x, d); }
+__device__ __forceinline__ PlanSum shfl_up(const PlanSum &x, int d)
+{
+    return PlanSum{__shfl_up_sync(0xffffffffu, x.places, d),
+                   {__shfl_up_sync(0xffffffffu, x.cost[0], d), __shfl_up_sync(0xffffffffu, x.cost[1], d)}};
+}
+
+// Inclusive sum over the block (a power of two of warps, at most 32); the
+// total is left in s_warp[31].
+template <class T>
+__device__ __forceinline__ T block_scan(T x, T *s_warp)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+        const T y = shfl_up(x, d);
+        if (lane >= d)
+            x = x + y;
+    }
+    __syncthreads(); // the last scan's sums have been read
+    if (lane == 31)
+        s_warp[warp] = x;
+    __syncthreads();
+    if (warp == 0) {
+        T w = lane < warps ? s_warp[lane] : T{};
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const T y = shfl_up(w, d);
+            if (lane >= d)
+                w = w + y;
+        }
+        s_warp[lane] = w;
+    }
+    __syncthreads();
+    return warp ? s_warp[warp - 1] + x : x;
+}
+
+// One block of up to kPlanThreads threads (fewer for small batches: the
+// barriers cost what they have to wait for).
+template <int D>
+__global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_constant__ ChunkParams p)
+{
+    __shared__ int s_scan[32];
+    __shared__ PlanSum s_sum[32];
+    __shared__ int s_ent[kPlanThreads + 1]; // first entry of each request of the round
+    __shared__ int s_t0[kPlanThreads], s_n[kPlanThreads], s_len[kPlanThreads];
+    __shared__ int64_t s_cum[2][kPlanThreads]; // cost before each of the first entries
+    __shared__ int s_most;                     // cost of the dearest tile of a row block
+    ptx::launch_dependents();
+    const int tid = threadIdx.x, threads = blockDim.x;
+    const int per = 2 * p.TQ; // tokens per entry
+    int count[2] = {0, 0};
+    int64_t cum[2] = {0, 0};
+    uint32_t err = 0;
+    for (int c = tid; c < p.n_cta; c += threads)
+        p.joins[c].n_parts = 0;
+    if (tid == 0)
+        s_most = 0;
+    for (int b0 = 0; b0 < p.batch; b0 += threads) {
+        const int b = b0 + tid;
+        int n = 0, t0 = 0, L = 0;
+        if (b < p.batch) {
+            t0 = __ldg(p.cu_q + b);
+            int t1 = __ldg(p.cu_q + b + 1);
+            L = __ldg(p.kv_lens + b);
+            if (t0 < 0 || t1 > p.T || t1 < t0)
+                err |= FL_DEVERR_LENGTHS;
+            t0 = min(max(t0, 0), p.T);
+            t1 = min(max(t1, t0), p.T);
+            n = t1 - t0;
+            L = min(max(L, 0), p.max_kv);
+        }
+        const int ent = (n + per - 1) / per;
+        const int end = block_scan(ent, s_scan);
+        s_ent[tid] = end - ent;
+        if (tid == threads - 1)
+            s_ent[threads] = end;
+        s_t0[tid] = t0;
+        s_n[tid] = n;
+        s_len[tid] = L;
+        __syncthreads();
+        const int n_round = s_ent[threads];
+        for (int e0 = 0; e0 < n_round; e0 += threads) {
+            const int e = e0 + tid;
+            ChunkEntry en{};
+            PlanSum add{};
+            int kind = -1;
+            if (e < n_round) {
+                int lo = 0, hi = threads - 1; // the last request that starts at or before e
+                while (lo < hi) {
+                    const int mid = (lo + hi + 1) >> 1;
+                    if (s_ent[mid] <= e)
+                        lo = mid;
+                    else
+                        hi = mid - 1;
+                }
+                const int at = (e - s_ent[lo]) * per;
+                en.b = b0 + lo;
+                en.t0 = s_t0[lo] + at;
+                en.n_tok = min(per, s_n[lo] - at);
+                en.L = s_len[lo];
+                en.pos0 = en.L - s_n[lo] + at;
+                int k0, k1;
+                key_range(p, en.L, en.pos0, en.pos0 + en.n_tok - 1, k0, k1);
+                en.key_lo = k0;
+                kind = is_few(p, en.n_tok) ? 1 : 0;
+                const int tile = kind ? kFewTile : chunk_key_tile(D);
+                en.lo = k0 / tile;
+                en.n_tiles = max(1, (max(k1, 0) + tile - 1) / tile - en.lo);
+                en.tile_cost = kind ? p.cost_few : en.n_tok > p.TQ ? p.cost_pair : p.cost_single;
+                add.places = kind ? 1 << 16 : 1;
+                add.cost[kind] = entry_cost(p, en);
+                if (!kind)
+                    atomicMax(&s_most, en.tile_cost);
+            }
+            const PlanSum sum = block_scan(add, s_sum);
+            if (kind >= 0) {
+                const int at = count[kind] + (kind ? sum.places >> 16 : sum.places & 0xffff) - 1;
+                en.cum = cum[kind] + sum.cost[kind] - add.cost[kind];
+                // overlapping requests may give more than fit: those are dropped
+                if (at < p.max_entries) {
+                    p.entries[kind * p.max_entries + at] = en;
+                    if (at < kPlanThreads)
+                        s_cum[kind][at] = en.cum;
+                }
+            }
+            count[0] += s_sum[31].places & 0xffff;
+            count[1] += s_sum[31].places >> 16;
+            cum[0] += s_sum[31].cost[0];
+            cum[1] += s_sum[31].cost[1];
+        }
+        __syncthreads(); // the next round overwrites the requests
+    }
+#pragma unroll
+    for (int kind = 0; kind < 2; ++kind)
+        if (count[kind] > p.max_entries) {
+            err |= FL_DEVERR_LENGTHS;
+            count[kind] = p.max_entries;
+            const ChunkEntry &last = p.entries[(kind + 1) * p.max_entries - 1];
+            cum[kind] = last.cum + entry_cost(p, last);
+        }
+    if (err && p.err_user)
+        atomicOr(p.err_user, err);
+    // CTAs of each list by its share of the cost; a part is at least one tile
+    // long, so that every CTA between the first and the last of an item holds
+    // one of its tiles
+    int parts[2];
+    {
+        const int64_t both = cum[0] + cum[1];
+        int share = both ? static_cast<int>((cum[0] * p.n_cta + both / 2) / both) : 0;
+        if (cum[0] && cum[1])
+            share = min(max(share, 1), p.n_cta - 1);
+#pragma unroll
+        for (int kind = 0; kind < 2; ++kind) {
+            const int64_t tile = kind ? p.cost_few : s_most, least = max(tile, static_cast<int64_t>(p.cost_least));
+            int g = static_cast<int>(
+                min(static_cast<int64_t>(kind ? p.n_cta - share : share), (cum[kind] + least - 1) / least));
+            if (g > 1 && cum[kind] / g < tile)
+                --g;
+            parts[kind] = g;
+        }
+    }
+    for (int c = tid; c < p.n_cta; c += threads) {
+        ChunkPart out{};
+        if (c < parts[0] + parts[1]) {
+            const int kind = c >= parts[0] ? 1 : 0;
+            const int part = kind ? c - parts[0] : c, g = kind ? parts[1] : parts[0];
+            const int64_t total = kind ? cum[1] : cum[0];
+            const int64_t x = (total * part + g - 1) / g;      // first cost unit of this part
+            int lo = 0, hi = (kind ? count[1] : count[0]) - 1; // the last entry that starts at or before x
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                const int64_t at =
+                    mid < kPlanThreads ? s_cum[kind][mid] : p.entries[kind * p.max_entries + mid].cum;
+                if (at <= x)
+                    lo = mid;
+                else
+                    hi = mid - 1;
+            }
+            const ChunkEntry &en = p.entries[kind * p.max_entries + lo];
+            const int64_t cost = item_cost(p, en);
+            out.total = total;
+            out.end = (total * (part + 1) + g - 1) / g;
+            out.few = kind;
+            out.cta = kind ? parts[0] : 0;
+            out.parts = g;
+            out.n_entries = kind ? count[1] : count[0];
+            out.entry = lo;
+            out.item = static_cast<int>((x - en.cum) / cost);
+            const int64_t in = x - en.cum - out.item * cost;
+            out.tile = static_cast<int>((in + en.tile_cost - 1) / en.tile_cost);
+        }
+        p.parts[c] = out;
+    }
+}
+
+// ------------------------------------------------------------------ joining
+//
+// Items whose keys were cut: O = sum 2^(m_q - M) O_q / sum 2^(m_q - M) l_q over
+// the parts q, in their order.  A kernel of its own: joining inside the
+// attention kernel (by the last CTA to come) put a fence, an atomic and three
+// rounds of loads on one CTA's path, 5 to 8 us at the end of the step; here
+// they are spread over 8 blocks an item.
+
+constexpr int kJoinThreads = 128, kJoinSplit = 4;
+
+__device__ __forceinline__ void join_write(const ChunkParams &p, int64_t tok, int64_t head, int dim, float o,
+                                           float l_round)
+{
+    p.out[tok * p.o_st + head * p.o_sh + dim] = __float2bfloat16(l_round == 0.f ? 0.f : o * ptx::rcp_approx(l_round));
+}
+
+__device__ __forceinline__ void join_lse(const ChunkParams &p, int64_t tok, int64_t head, float m, float l)
+{
+    if (p.lse)
+        p.lse[head * p.l_sh + tok] = l == 0.f ? kNegInf : (m + log2f(l)) * kLn2;
+}
+
+// Row-block layouts: a row per thread, N / kJoinSplit columns.
+template <int N, int D>
+__device__ __forceinline__ void join_block(const ChunkParams &p, const ChunkJoin &jn, int cta, int slot, int z)
+{
+    constexpr int C = N / kJoinSplit;
+    const int r = threadIdx.x, n_parts = jn.n_parts;
+    if (r >= jn.rows[slot])
+        return;
+    float M = kNegInf, l = 0.f, lr = 0.f, o[C];
+#pragma unroll
+    for (int i = 0; i < C; ++i)
+        o[i] = 0.f;
+    const float *b0 = partial<D>(p, cta, 1, slot) + r;
+#pragma unroll 4
+    for (int q = 0; q < n_parts; ++q)
+        M = fmaxf(M, __ldg((q ? partial<D>(p, cta + q, 0, slot) + r : b0) + N * 128));
+    const float M0 = M == kNegInf ? 0.f : M;
+#pragma unroll 2
+    for (int q = 0; q < n_parts; ++q) {
+        const float *b = q ? partial<D>(p, cta + q, 0, slot) + r : b0;
+        const float m = __ldg(b + N * 128), w = ptx::ex2(m - M0);
+        l = fmaf(w, __ldg(b + (N + 1) * 128), l);
+        lr = fmaf(w, __ldg(b + (N + 2) * 128), lr);
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            // the O of a part without a key of this row was not written
+            const float v = __ldg(b + (z * C + i) * 128);
+            o[i] = m == kNegInf ? o[i] : fmaf(w, v, o[i]);
+        }
+    }
+    const int r_tok = fast_div(r, p.div_g);
+    const int64_t tok = jn.t0[slot] + r_tok, head = jn.kvh * p.G + r - r_tok * p.G;
+    const float inv = lr == 0.f ? 0.f : ptx::rcp_approx(lr);
+    const int col = (N < D ? slot * N : 0) + z * C;
+    uint4 *dst = reinterpret_cast<uint4 *>(p.out + tok * p.o_st + head * p.o_sh + col);
+#pragma unroll
+    for (int i = 0; i < C; i += 8)
+        dst[i / 8] = make_uint4(ptx::pack_bf16(o[i] * inv, o[i + 1] * inv), ptx::pack_bf16(o[i + 2] * inv, o[i + 3] * inv),
+                                ptx::pack_bf16(o[i + 4] * inv, o[i + 5] * inv),
+                                ptx::pack_bf16(o[i + 6] * inv, o[i + 7] * inv));
+    if (z == 0 && (N == D || slot == 0))
+        join_lse(p, tok, head, M, l);
+}
+
+// Few rows: a dimension per thread (at D = 64 half the threads a row), a part
+// per lane while the weights are made.
+template <int D>
+__device__ __forceinline__ void join_few(const ChunkParams &p, const ChunkJoin &jn, int cta, int slot, int z)
+{
+    constexpr int R = kFewRows, kDepth = 16, kPerBlock = 128 / D;
+    const int lane = threadIdx.x & 31, dim = threadIdx.x & (D - 1), n_parts = jn.n_parts;
+    auto part = [&](int q) { return partial<D>(p, cta + q, q == 0 ? 1 : 0, slot); };
+    for (int n = z * kPerBlock + static_cast<int>(threadIdx.x) / D; n < jn.rows[slot]; n += kJoinSplit * kPerBlock) {
+        float M = kNegInf;
+        for (int q = lane; q < n_parts; q += 32)
+            M = fmaxf(M, __ldg(part(q) + R * 128 + n));
+#pragma unroll
+        for (int d = 16; d; d >>= 1)
+            M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+        const float M0 = M == kNegInf ? 0.f : M;
+        float l = 0.f, lr = 0.f, o = 0.f;
+        for (int q0 = 0; q0 < n_parts; q0 += 32) {
+            float w = 0.f, a = 0.f, b = 0.f;
+            if (q0 + lane < n_parts) {
+                const float *s = part(q0 + lane) + R * 128 + n;
+                w = ptx::ex2(__ldg(s) - M0);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    a += __ldg(s + R + 2 * R * k);
+                    b += __ldg(s + 2 * R + 2 * R * k);
+                }
+                a *= w;
+                b *= w;
+            }
+#pragma unroll
+            for (int d = 16; d; d >>= 1) {
+                a += __shfl_xor_sync(0xffffffffu, a, d);
+                b += __shfl_xor_sync(0xffffffffu, b, d);
+            }
+            l += a;
+            lr += b;
+            for (int q = q0; q < min(q0 + 32, n_parts); q += kDepth) {
+                float v[kDepth];
+#pragma unroll
+                for (int i = 0; i < kDepth; ++i)
+                    v[i] = q + i < n_parts ? __ldg(part(q + i) + n * 128 + dim) : 0.f;
+#pragma unroll
+                for (int i = 0; i < kDepth; ++i)
+                    o = fmaf(__shfl_sync(0xffffffffu, w, (q + i) & 31), v[i], o);
+            }
+        }
+        const int s = fast_div(n, p.div_g);
+        const int64_t tok = jn.t0[slot] + s, head = (jn.kvh + slot) * p.G + n - s * p.G;
+        join_write(p, tok, head, dim, o, lr);
+        if (dim == 0)
+            join_lse(p, tok, head, M, l);
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const __grid_constant__ ChunkParams p)
+{
+    ptx::wait_dependency();
+    const int cta = blockIdx.x, slot = blockIdx.y, z = blockIdx.z;
+    const ChunkJoin jn = p.joins[cta];
+    if (jn.n_parts < 2)
+        return;
+    if (jn.mode == JOIN_FEW)
+        join_few<D>(p, jn, cta, slot, z);
+    else if (jn.mode == JOIN_PAIR)
+        join_block<D, D>(p, jn, cta, slot, z);
+    else
+        join_block<D / 2, D>(p, jn, cta, slot, z);
+}
+
+} // namespace
+} // namespace fl

@@ -42,22 +42,16 @@
 #include <cuda_bf16.h>
 #include <cstdint>
 
+#include "chunk_few.cuh"
+#include "chunk_plan.cuh"
 #include "common.cuh"
-#include "fl_attn.h"
 #include "launch.h"
 #include "softmax_tile.cuh"
 
 namespace fl {
 namespace {
 
-constexpr int kThreads = 384;
-constexpr uint32_t kRegsLaunch = 168;
-constexpr uint32_t kRegsSoftmax = 200;
-constexpr uint32_t kRegsOther = 104;
-static_assert(2 * 128 * kRegsSoftmax + 128 * kRegsOther == kThreads * kRegsLaunch,
-              "register split must equal the launch allocation");
 constexpr int kBox = 16; // keys per TMA box
-constexpr int kInfo = 4; // items published ahead of the slowest role
 
 template <int D>
 struct ChunkCfg {
@@ -93,8 +87,8 @@ struct Item {
     int t0[2], rows[2], pos0[2]; // slot's first token row, rows, first position
     int L, key_lo;               // cached keys; lowest key that any row of the item sees
     int kvh;
-    int part, n_parts;           // first CTA of the item, number of CTAs
-    int mine;                    // this part's buffer: 0 or 1
+    int n_parts;                 // CTAs that share the item
+    int mine;                    // this part's buffer: 1 if the item begins here
 };
 
 template <int D>
@@ -116,180 +110,12 @@ struct __align__(1024) ChunkSmem {
     uint32_t abort_flag;
 };
 
-__device__ uint32_t g_lib_error_word;
-
 template <int D>
 struct KernelCtx {
     ChunkSmem<D> *sm;
     uint32_t tmem;
     WaitCtl wc;
 };
-
-__device__ __forceinline__ uint32_t bar(const uint64_t &b) { return ptx::smem_u32(&b); }
-
-// Keys [lo, hi) that the tokens at positions first .. last see.
-__device__ __forceinline__ void key_range(const ChunkParams &p, int L, int first, int last, int &lo, int &hi)
-{
-    lo = p.window ? max(0, first - p.window + 1) : 0;
-    hi = p.causal ? min(L, last + 1) : L;
-}
-
-// ------------------------------------------------------------------ planning
-
-constexpr int kPlanThreads = 1024;
-
-template <class T>
-__device__ __forceinline__ T block_scan(T x, T *s_warp)
-{
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-    for (int d = 1; d < 32; d *= 2) {
-        const T y = __shfl_up_sync(0xffffffffu, x, d);
-        if (lane >= d)
-            x += y;
-    }
-    __syncthreads(); // the last scan's sums have been read
-    if (lane == 31)
-        s_warp[warp] = x;
-    __syncthreads();
-    if (warp == 0) {
-        T w = s_warp[lane];
-#pragma unroll
-        for (int d = 1; d < 32; d *= 2) {
-            const T y = __shfl_up_sync(0xffffffffu, w, d);
-            if (lane >= d)
-                w += y;
-        }
-        s_warp[lane] = w;
-    }
-    __syncthreads();
-    return x + (warp ? s_warp[warp - 1] : T(0));
-}
-
-__global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkParams p)
-{
-    __shared__ int s_scan[32];
-    __shared__ int64_t s_scan64[32];
-    __shared__ int s_ent[kPlanThreads + 1]; // first entry of each request of the round
-    __shared__ int s_t0[kPlanThreads], s_n[kPlanThreads], s_len[kPlanThreads];
-    __shared__ int64_t s_cum[kPlanThreads]; // cost before each of the first entries
-    __shared__ int s_wide;
-    const int tid = threadIdx.x;
-    const int per = 2 * p.TQ; // tokens per entry
-    int n_entries = 0;
-    int64_t cum = 0;
-    uint32_t err = 0;
-    for (int c = tid; c < 8 * p.n_cta; c += kPlanThreads)
-        p.tickets[c] = 0;
-    if (tid == 0)
-        s_wide = 0;
-    for (int b0 = 0; b0 < p.batch; b0 += kPlanThreads) {
-        const int b = b0 + tid;
-        int n = 0, t0 = 0, L = 0;
-        if (b < p.batch) {
-            t0 = __ldg(p.cu_q + b);
-            int t1 = __ldg(p.cu_q + b + 1);
-            L = __ldg(p.kv_lens + b);
-            if (t0 < 0 || t1 > p.T || t1 < t0)
-                err |= FL_DEVERR_LENGTHS;
-            t0 = min(max(t0, 0), p.T);
-            t1 = min(max(t1, t0), p.T);
-            n = t1 - t0;
-            L = min(max(L, 0), p.max_kv);
-        }
-        const int ent = (n + per - 1) / per;
-        const int end = block_scan(ent, s_scan);
-        s_ent[tid] = end - ent;
-        if (tid == kPlanThreads - 1)
-            s_ent[kPlanThreads] = end;
-        s_t0[tid] = t0;
-        s_n[tid] = n;
-        s_len[tid] = L;
-        __syncthreads();
-        const int n_round = s_ent[kPlanThreads];
-        for (int e0 = 0; e0 < n_round; e0 += kPlanThreads) {
-            const int e = e0 + tid;
-            ChunkEntry en{};
-            int64_t cost = 0;
-            if (e < n_round) {
-                int lo = 0, hi = kPlanThreads - 1; // the last request that starts at or before e
-                while (lo < hi) {
-                    const int mid = (lo + hi + 1) >> 1;
-                    if (s_ent[mid] <= e)
-                        lo = mid;
-                    else
-                        hi = mid - 1;
-                }
-                const int at = (e - s_ent[lo]) * per;
-                en.b = b0 + lo;
-                en.t0 = s_t0[lo] + at;
-                en.n_tok = min(per, s_n[lo] - at);
-                en.L = s_len[lo];
-                en.pos0 = en.L - s_n[lo] + at;
-                int k0, k1;
-                key_range(p, en.L, en.pos0, en.pos0 + en.n_tok - 1, k0, k1);
-                en.key_lo = k0;
-                en.lo = k0 / p.key_tile;
-                en.n_tiles = max(1, (max(k1, 0) + p.key_tile - 1) / p.key_tile - en.lo);
-                en.tile_cost = en.n_tok > p.TQ ? p.cost_pair : p.cost_single;
-                cost = (static_cast<int64_t>(en.n_tiles) * en.tile_cost + p.cost_item) * p.Hk;
-                if (en.n_tok > p.TQ)
-                    s_wide = 1; // every writer writes 1
-            }
-            const int64_t incl = block_scan(cost, s_scan64);
-            en.cum = cum + incl - cost;
-            const int at = n_entries + e;
-            if (e < n_round && at < p.max_entries) {
-                p.entries[at] = en;
-                if (at < kPlanThreads)
-                    s_cum[at] = en.cum;
-            }
-            cum += s_scan64[31];
-        }
-        n_entries += n_round;
-        __syncthreads(); // the next round overwrites the requests
-    }
-    if (n_entries > p.max_entries) { // overlapping requests: drop what does not fit
-        err |= FL_DEVERR_LENGTHS;
-        n_entries = p.max_entries;
-        const ChunkEntry &last = p.entries[n_entries - 1];
-        cum = last.cum + (static_cast<int64_t>(last.n_tiles) * last.tile_cost + p.cost_item) * p.Hk;
-    }
-    if (err && p.err_user)
-        atomicOr(p.err_user, err);
-    // parts: each at least one tile long, so that every CTA between the first
-    // and the last of an item holds one of its tiles
-    const int64_t least = max(s_wide ? p.cost_pair : p.cost_single, p.cost_least);
-    const int parts = static_cast<int>(min(static_cast<int64_t>(p.n_cta), (cum + least - 1) / least));
-    const bool short_part = parts > 1 && cum / parts < (s_wide ? p.cost_pair : p.cost_single);
-    const int g = short_part ? parts - 1 : parts;
-    if (tid == 0) {
-        p.head->total = cum;
-        p.head->n_entries = n_entries;
-        p.head->parts = g;
-    }
-    if (tid >= g)
-        return;
-    const int64_t x = (cum * tid + g - 1) / g; // first cost unit of this part
-    int lo = 0, hi = n_entries - 1;            // the last entry that starts at or before x
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        const int64_t at = mid < kPlanThreads ? s_cum[mid] : p.entries[mid].cum;
-        if (at <= x)
-            lo = mid;
-        else
-            hi = mid - 1;
-    }
-    const ChunkEntry &en = p.entries[lo];
-    const int64_t cost = static_cast<int64_t>(en.n_tiles) * en.tile_cost + p.cost_item;
-    ChunkStart st;
-    st.entry = lo;
-    st.head = static_cast<int>((x - en.cum) / cost);
-    const int64_t in = x - en.cum - st.head * cost;
-    st.tile = static_cast<int>(min((in + en.tile_cost - 1) / en.tile_cost, static_cast<int64_t>(en.n_tiles)));
-    st.pad = 0;
-    p.starts[tid] = st;
-}
 
 // ------------------------------------------------------------------ producer
 
@@ -301,44 +127,29 @@ __device__ void producer_role(const KernelCtx<D> &cx, const ChunkParams &p, cons
     constexpr int kBN = C::kBN, kStages = C::kStages, kBoxes = kBN / kBox;
     ChunkSmem<D> &sm = *cx.sm;
     const uint32_t lane = ptx::lane_id();
-    const int cta = blockIdx.x;
     uint32_t kv_count = 0, item_count = 0;
     bool ok = true;
-    const int64_t total = p.head->total;
-    const int parts = p.head->parts, n_entries = p.head->n_entries;
-    int e = n_entries, h = 0, k = 0;
-    int64_t x_end = 0;
-    if (cta < parts) {
-        const ChunkStart st = p.starts[cta];
-        e = st.entry;
-        h = st.head;
-        k = st.tile;
-        x_end = (total * (cta + 1) + parts - 1) / parts;
-    }
+    const ChunkPart me = p.parts[blockIdx.x];
+    const int cta = static_cast<int>(blockIdx.x) - me.cta;
+    int e = me.entry, h = me.item, k = me.tile; // entry, item of it, tile of that
     for (;;) {
         // ---- the next part
         Item it;
         it.stop = 1;
         ChunkEntry en{};
         int k_end = 0;
-        while (e < n_entries) {
+        while (e < me.n_entries) {
             en = p.entries[e];
-            const int64_t cost = static_cast<int64_t>(en.n_tiles) * en.tile_cost + p.cost_item;
-            const int64_t x0 = en.cum + h * cost;
-            if (x0 + static_cast<int64_t>(k) * en.tile_cost >= x_end) {
-                e = n_entries; // the cut falls before this tile
+            const int64_t x0 = en.cum + h * item_cost(p, en);
+            if (x0 + static_cast<int64_t>(k) * en.tile_cost >= me.end) {
+                e = me.n_entries; // the cut falls before this tile
                 break;
             }
             if (k < en.n_tiles) {
-                k_end = static_cast<int>(
-                    min(static_cast<int64_t>(en.n_tiles), (x_end - x0 + en.tile_cost - 1) / en.tile_cost));
-                it.part = k == 0 ? cta : static_cast<int>(x0 * parts / total);
-                const int last = k_end == en.n_tiles
-                                     ? cta
-                                     : static_cast<int>((x0 + static_cast<int64_t>(en.n_tiles - 1) * en.tile_cost) *
-                                                        parts / total);
-                it.n_parts = last - it.part + 1;
-                it.mine = it.part == cta ? 1 : 0;
+                const PartRange r = part_range(x0, en.n_tiles, en.tile_cost, k, me.end, me.total, cta, me.parts);
+                k_end = r.k_end;
+                it.n_parts = r.n_parts;
+                it.mine = r.first == cta ? 1 : 0;
                 it.stop = 0;
                 break;
             }
@@ -376,6 +187,9 @@ __device__ void producer_role(const KernelCtx<D> &cx, const ChunkParams &p, cons
         if (lane == 0) {
             sm.info[slot] = it;
             ptx::mbar_arrive(bar(sm.info_full[slot])); // release: the fields above first
+            if (!it.stop && it.mine && it.n_parts > 1)
+                p.joins[blockIdx.x] = ChunkJoin{it.n_parts, it.pair ? JOIN_PAIR : JOIN_HALF, it.kvh,
+                                                {it.t0[0], it.t0[1]}, {it.rows[0], it.rows[1]}, 0};
         }
         __syncwarp();
         if (it.stop)
@@ -643,73 +457,6 @@ __device__ __forceinline__ void store16(__nv_bfloat16 *dst, const float (&o)[16]
                           ptx::pack_bf16(o[8 * c + 6] * inv, o[8 * c + 7] * inv));
 }
 
-// Joins the parts of the item's rows 32 w .. 32 w + 31 (columns [col0, col0 +
-// N) of the output; each part holds them as N fp32 columns of 128 rows, then
-// m, l and the sum of the rounded P).  Whole warp.  Lanes are spread over rows
-// first and columns with what is left, so that a single token's few rows use
-// the warp as well as 32 rows do.
-template <int N, int D>
-__device__ __forceinline__ void join_parts(const ChunkParams &p, int slot, int part, int n_parts, int rows, int w,
-                                           int t0, int kvh, int col0, bool with_lse)
-{
-    const int lane = static_cast<int>(ptx::lane_id());
-    const int n = min(32, rows - 32 * w);
-    int span = 1;
-    while (span < n)
-        span *= 2;
-    const int r = 32 * w + (lane & (span - 1));
-    const int cstep = 32 / span, c_first = lane / span;
-    const bool live = r < rows;
-    // part q (of CTA part + q) is in that CTA's buffer 1 if the item began there, else 0
-    auto base = [&](int q) {
-        return p.partials + (static_cast<int64_t>((part + q) * 2 + (q == 0 ? 1 : 0)) * 2 + slot) * ((D + 4) * 128) + r;
-    };
-    float M = kNegInf, l = 0.f, lr = 0.f;
-    if (live)
-        for (int q = 0; q < n_parts; ++q)
-            M = fmaxf(M, __ldcg(base(q) + N * 128));
-    if (live && M != kNegInf)
-        for (int q = 0; q < n_parts; ++q) {
-            const float *b = base(q) + N * 128;
-            const float wq = ptx::ex2(__ldcg(b) - M);
-            l = fmaf(wq, __ldcg(b + 128), l);
-            lr = fmaf(wq, __ldcg(b + 256), lr);
-        }
-    const float inv = lr > 0.f ? ptx::rcp_approx(lr) : 0.f;
-    const int tok = t0 + fast_div(r, p.div_g), head = kvh * p.G + (r - fast_div(r, p.div_g) * p.G);
-    __nv_bfloat16 *out = p.out + static_cast<int64_t>(tok) * p.o_st + static_cast<int64_t>(head) * p.o_sh + col0;
-    for (int c0 = c_first; c0 < N; c0 += 16 * cstep) {
-        float o[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-            o[i] = 0.f;
-        if (live && M != kNegInf)
-            for (int q = 0; q < n_parts; ++q) {
-                const float *b = base(q);
-                const float m = __ldcg(b + N * 128);
-                if (m == kNegInf)
-                    continue; // a part without a key of this row: its O was not written
-                const float wq = ptx::ex2(m - M);
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (c0 + i * cstep < N)
-                        o[i] = fmaf(wq, __ldcg(b + (c0 + i * cstep) * 128), o[i]);
-            }
-        if (!live)
-            continue;
-        if (cstep == 1) {
-            store16(out + c0, o, inv);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                if (c0 + i * cstep < N)
-                    out[c0 + i * cstep] = __float2bfloat16(o[i] * inv);
-        }
-    }
-    if (with_lse && live && c_first == 0 && p.lse)
-        p.lse[static_cast<int64_t>(head) * p.l_sh + tok] = l > 0.f ? (M + log2f(l)) * kLn2 : kNegInf;
-}
-
 // A row's finished sums and, per part, where it goes.
 template <int D>
 struct RowOut {
@@ -726,24 +473,8 @@ __device__ __forceinline__ RowOut<D> row_out(const ChunkParams &p, const Item &i
     RowOut<D> w;
     w.out = p.out + tok * p.o_st + head * p.o_sh;
     w.lse = p.lse ? p.lse + head * p.l_sh + tok : nullptr;
-    w.mine = p.partials + (static_cast<int64_t>(blockIdx.x * 2 + inf.mine) * 2 + t) * ((D + 4) * 128) + r;
+    w.mine = partial<D>(p, blockIdx.x, inf.mine, t) + r;
     return w;
-}
-
-// After a warp's partials: the last CTA to come joins the item's parts.
-template <int N, int D>
-__device__ __forceinline__ void arrive_and_join(const ChunkParams &p, const Item &inf, int t, int wq, int col0,
-                                                bool with_lse)
-{
-    __threadfence();
-    __syncwarp();
-    int old = 0;
-    if (ptx::lane_id() == 0)
-        old = atomicAdd(p.tickets + (inf.part * 2 + t) * 4 + wq, 1);
-    if (__shfl_sync(0xffffffffu, old, 0) != inf.n_parts - 1)
-        return;
-    __threadfence();
-    join_parts<N, D>(p, t, inf.part, inf.n_parts, inf.rows[t], wq, inf.t0[t], inf.kvh, col0, with_lse);
 }
 
 // Epilogue of a pair: the slot's own rows, every column.  An active warp.
@@ -778,7 +509,7 @@ __device__ __forceinline__ void write_slot(const ChunkParams &p, const Item &inf
         } else if (keys) {
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-                __stcg(w.mine + (c + i) * 128, __uint_as_float(raw[i]));
+                w.mine[(c + i) * 128] = __uint_as_float(raw[i]);
         }
     }
     if (whole) {
@@ -787,9 +518,9 @@ __device__ __forceinline__ void write_slot(const ChunkParams &p, const Item &inf
         return;
     }
     if (live) {
-        __stcg(w.mine + D * 128, st.m_ref);
-        __stcg(w.mine + (D + 1) * 128, st.l);
-        __stcg(w.mine + (D + 2) * 128, st.l_round);
+        w.mine[D * 128] = st.m_ref;
+        w.mine[(D + 1) * 128] = st.l;
+        w.mine[(D + 2) * 128] = st.l_round;
     }
 }
 
@@ -831,7 +562,7 @@ __device__ __forceinline__ void write_joined(const ChunkParams &p, const Item &i
         } else if (m != kNegInf) {
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-                __stcg(w.mine + (c + i) * 128, o[i]);
+                w.mine[(c + i) * 128] = o[i];
         }
     }
     if (!live)
@@ -840,9 +571,9 @@ __device__ __forceinline__ void write_joined(const ChunkParams &p, const Item &i
         if (t == 0 && w.lse)
             *w.lse = l > 0.f ? (m + log2f(l)) * kLn2 : kNegInf;
     } else {
-        __stcg(w.mine + H * 128, m);
-        __stcg(w.mine + (H + 1) * 128, l);
-        __stcg(w.mine + (H + 2) * 128, lr);
+        w.mine[H * 128] = m;
+        w.mine[(H + 1) * 128] = l;
+        w.mine[(H + 2) * 128] = lr;
     }
 }
 
@@ -980,11 +711,8 @@ __device__ void softmax_role(const KernelCtx<D> &cx, const ChunkParams &p, int t
             }
         }
         if (inf.pair) {
-            if (active) {
+            if (active)
                 write_slot<D>(p, inf, t, r, tO, st, n_mine > 0);
-                if (inf.n_parts > 1)
-                    arrive_and_join<D, D>(p, inf, t, wq, 0, true);
-            }
         } else {
             const uint32_t tX = cx.tmem + lanes + C::kColX;
             if (active) {
@@ -1003,8 +731,6 @@ __device__ void softmax_role(const KernelCtx<D> &cx, const ChunkParams &p, int t
                                 tX + C::kStrideX * (t ^ 1), st);
             ptx::tc_fence_before();
             ptx::mbar_arrive(bar(sm.x_free[t ^ 1])); // the other slot's O and sums have been read
-            if (active && inf.n_parts > 1)
-                arrive_and_join<D / 2, D>(p, inf, t, wq, t * (D / 2), t == 0);
             // the other warpgroup has read this slot's O before the next item's P V
             if (!warp_wait(bar(sm.x_free[t]), joins & 1, cx.wc, W_JOIN))
                 return;
@@ -1017,16 +743,14 @@ __device__ void softmax_role(const KernelCtx<D> &cx, const ChunkParams &p, int t
     }
 }
 
+// ------------------------------------------------------------------ kernel
+
 template <int MOD, int D>
-__global__ void __launch_bounds__(kThreads, 1)
-    chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                 const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ ChunkParams p)
+__device__ __forceinline__ void block_path(const ChunkMaps &maps, const ChunkParams &p, uint8_t *smem)
 {
     using C = ChunkCfg<D>;
     constexpr int kStages = C::kStages;
-    extern __shared__ uint8_t smem_raw[];
-    const uint32_t base = ptx::smem_u32(smem_raw);
-    ChunkSmem<D> *sm = reinterpret_cast<ChunkSmem<D> *>(smem_raw + ((1024u - (base & 1023u)) & 1023u));
+    ChunkSmem<D> *sm = reinterpret_cast<ChunkSmem<D> *>(smem);
     const int warp = threadIdx.x >> 5;
 
     for (uint32_t w = threadIdx.x; w < C::kOnesBytes / 4; w += kThreads)
@@ -1060,11 +784,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::fence_mbarrier_init();
         ptx::fence_proxy_async_smem();
     }
-    if (warp == 0 && ptx::lane_id() == 0) {
-        ptx::prefetch_tensormap(&tm_q);
-        ptx::prefetch_tensormap(&tm_k);
-        ptx::prefetch_tensormap(&tm_v);
-    }
     if (warp == 1) {
         ptx::tmem_alloc(ptx::smem_u32(&sm->tmem_base), 512);
         ptx::tmem_relinquish();
@@ -1076,10 +795,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     KernelCtx<D> cx;
     cx.sm = sm;
     cx.tmem = sm->tmem_base;
-    cx.wc.abort_flag = &sm->abort_flag;
-    cx.wc.timeout_cycles = p.timeout_ns * 21 / 10; // 2.1 cycles per ns at the maximum clock
-    cx.wc.err_user = p.err_user;
-    cx.wc.err_lib = &g_lib_error_word;
+    cx.wc = wait_ctl(p, &sm->abort_flag);
 
     // each branch ends with its own copy of the teardown barrier, so no code
     // runs under both register limits
@@ -1091,7 +807,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         ptx::setmaxnreg_dec<kRegsOther>();
         if (warp == 0)
-            producer_role(cx, p, &tm_q, &tm_k, &tm_v);
+            producer_role(cx, p, &maps.q, &maps.k, &maps.v);
         else if (warp == 1)
             s_role(cx);
         else
@@ -1105,13 +821,59 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
+// The first CTAs walk the row blocks, the others the few rows.
 template <int MOD, int D>
-cudaError_t launch_mod(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, const ChunkParams &p,
-                       cudaStream_t stream)
+__global__ void __launch_bounds__(kThreads, 1)
+    chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constant__ ChunkParams p)
 {
-    // the layout plus the worst-case alignment pad within 227 KB per CTA
-    static_assert(sizeof(ChunkSmem<D>) + 1024 <= 232448, "shared memory per CTA");
-    const size_t smem = sizeof(ChunkSmem<D>) + 1024;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t base = ptx::smem_u32(smem_raw);
+    uint8_t *smem = smem_raw + ((1024u - (base & 1023u)) & 1023u);
+    if (threadIdx.x == 0) {
+        ptx::prefetch_tensormap(&maps.q);
+        ptx::prefetch_tensormap(&maps.k);
+        ptx::prefetch_tensormap(&maps.v);
+        ptx::prefetch_tensormap(&maps.few_q);
+        ptx::prefetch_tensormap(&maps.few_k);
+        ptx::prefetch_tensormap(&maps.few_v);
+    }
+    ptx::launch_dependents();
+    ptx::wait_dependency(); // the plan
+    const int parts = p.parts[blockIdx.x].parts, few = p.parts[blockIdx.x].few;
+    if (parts == 0)
+        return; // no work for this CTA
+    if (!few)
+        block_path<MOD, D>(maps, p, smem);
+    else
+        few_path<MOD, D>(maps, p, smem);
+}
+
+// A launch that may start while the kernel before it in the stream runs (it
+// waits for that one itself: ptx::wait_dependency).
+template <class... Params, class... Args>
+cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                         const Args &...args)
+{
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <int MOD, int D>
+cudaError_t launch_mod(const ChunkMaps &maps, const ChunkParams &p, cudaStream_t stream)
+{
+    // the larger layout plus the worst-case alignment pad within 227 KB per CTA
+    constexpr size_t smem =
+        (sizeof(ChunkSmem<D>) > sizeof(FewSmem<D>) ? sizeof(ChunkSmem<D>) : sizeof(FewSmem<D>)) + 1024;
+    static_assert(smem <= 232448, "shared memory per CTA");
     static bool configured = false; // benign race: both calls are idempotent
     if (!configured) {
         cudaFuncAttributes attr;
@@ -1127,24 +889,30 @@ cudaError_t launch_mod(const CUtensorMap &tq, const CUtensorMap &tk, const CUten
             return e;
         configured = true;
     }
-    chunk_plan_kernel<<<1, kPlanThreads, 0, stream>>>(p);
+    // one round of the planning kernel for the requests and their entries, as
+    // long as its block allows
+    int threads = 128;
+    while (threads < kPlanThreads && (threads < p.batch || threads < p.max_entries))
+        threads *= 2;
+    chunk_plan_kernel<D><<<1, threads, 0, stream>>>(p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess)
         return e;
-    chunk_kernel<MOD, D><<<p.n_cta, kThreads, smem, stream>>>(tq, tk, tv, p);
-    return cudaGetLastError();
+    e = launch_after(chunk_kernel<MOD, D>, dim3(p.n_cta), kThreads, smem, stream, maps, p);
+    if (e != cudaSuccess)
+        return e;
+    return launch_after(chunk_join_kernel<D>, dim3(p.n_cta, 2, kJoinSplit), kJoinThreads, 0, stream, p);
 }
 
 } // namespace
 
-cudaError_t launch_chunk(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, const ChunkParams &p,
-                         cudaStream_t stream)
+cudaError_t launch_chunk(const ChunkMaps &maps, const ChunkParams &p, cudaStream_t stream)
 {
     if (p.head_dim == 64)
-        return p.score_mod == MOD_SOFTCAP ? launch_mod<MOD_SOFTCAP, 64>(tq, tk, tv, p, stream)
-                                          : launch_mod<MOD_NONE, 64>(tq, tk, tv, p, stream);
-    return p.score_mod == MOD_SOFTCAP ? launch_mod<MOD_SOFTCAP, 128>(tq, tk, tv, p, stream)
-                                      : launch_mod<MOD_NONE, 128>(tq, tk, tv, p, stream);
+        return p.score_mod == MOD_SOFTCAP ? launch_mod<MOD_SOFTCAP, 64>(maps, p, stream)
+                                          : launch_mod<MOD_NONE, 64>(maps, p, stream);
+    return p.score_mod == MOD_SOFTCAP ? launch_mod<MOD_SOFTCAP, 128>(maps, p, stream)
+                                      : launch_mod<MOD_NONE, 128>(maps, p, stream);
 }
 
 } // namespace fl

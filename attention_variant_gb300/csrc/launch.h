@@ -271,8 +271,11 @@ struct KvPlanParams {
 
 // ---- attention of ragged chunks over the cache (fwd_chunk.cu)
 constexpr int kChunkMaxCtas = 160; // persistent CTAs the workspace has room for
-// Keys per K/V tile (the standard kernel's, for the same TMEM budget).
+// Keys per K/V tile (the standard kernel's, for the same TMEM budget), and of
+// the few-row path.
 __host__ __device__ constexpr int chunk_key_tile(int D) { return D == 128 ? 64 : 112; }
+constexpr int kFewTile = 128;
+constexpr int kFewRows = 16; // query rows of a request and KV head, at most
 
 // One or two row blocks of a request, as the planning kernel lists them.
 struct ChunkEntry {
@@ -280,21 +283,31 @@ struct ChunkEntry {
     int L, key_lo;             // cached keys; lowest key that the rows see
     int lo, n_tiles;           // key tiles [lo, lo + n_tiles)
     int tile_cost, pad;
-    int64_t cum;               // cost of everything before it, all heads
+    int64_t cum;               // cost of everything before it on its list, all heads
 };
-struct ChunkStart {
-    int entry, head, tile, pad; // where a CTA's part begins
+// A CTA's part of the work: [first, end) of the cost units of its list.
+struct ChunkPart {
+    int64_t total, end;        // cost of the whole list; the part's end
+    int few;                   // which list: row blocks or few rows
+    int cta, parts;            // the list's first CTA and number of parts
+    int n_entries;
+    int entry, item, tile, pad; // where the part begins
 };
-struct ChunkHead {
-    int64_t total;             // cost of everything
-    int n_entries, parts;      // entries; CTAs with work
+// An item whose keys were cut, by the CTA it begins in.
+struct ChunkJoin {
+    int n_parts;               // 0 or 1: nothing to join
+    int mode;                  // how its parts are laid out (chunk_plan.cuh)
+    int kvh;
+    int t0[2], rows[2];        // per slot: first token row, rows
+    int pad;
 };
 
 struct ChunkParams {
     int T, batch, Hq, Hk, G, head_dim;
     int TQ;                    // tokens per 128-row block: 128 / G
     FastDiv div_g;
-    int key_tile;
+    int few_tq;                // tokens of few rows: kFewRows / G
+    int few_box;               // keys per TMA box of the few-row path
     int max_kv, page_shift;    // page_shift < 0: contiguous cache
     int64_t bt_stride;
     const int32_t *cu_q, *kv_lens, *block_table;
@@ -308,12 +321,11 @@ struct ChunkParams {
     float *lse;                // [Hq, T] or null
     int64_t l_sh;
     int n_cta;
-    int cost_pair, cost_single, cost_item, cost_least; // see api.cu
+    int cost_pair, cost_single, cost_few, cost_item, cost_least; // see api.cu
     int max_entries;
-    ChunkHead *head;           // the workspace
-    ChunkStart *starts;        // [n_cta]
-    int *tickets;              // [n_cta][2][4]
-    ChunkEntry *entries;       // [max_entries]
+    ChunkPart *parts;          // the workspace: [n_cta]
+    ChunkJoin *joins;          // [n_cta]
+    ChunkEntry *entries;       // [2][max_entries]
     float *partials;           // [n_cta][2][2][D + 4][128]
     uint32_t *err_user;
     uint64_t timeout_ns;
@@ -324,8 +336,12 @@ struct ChunkParams {
 cudaError_t launch_rope(const RopeParams &p, bool fp32, bool interleaved, int vec, int sm_count,
                         cudaStream_t stream);
 cudaError_t launch_kv_plan(const KvPlanParams &p, cudaStream_t stream);
-cudaError_t launch_chunk(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, const ChunkParams &p,
-                         cudaStream_t stream);
+// Tensor maps: a row block of q and boxes of 16 keys; few rows of q and boxes
+// of few_box keys.
+struct ChunkMaps {
+    CUtensorMap q, k, v, few_q, few_k, few_v;
+};
+cudaError_t launch_chunk(const ChunkMaps &maps, const ChunkParams &p, cudaStream_t stream);
 #endif
 
 }  // namespace fl

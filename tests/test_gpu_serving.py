@@ -268,9 +268,40 @@ def test_chunk_pages(D, page):
     _case([70, 1, 9], [517, 258, 9], D=D, page=page)
 
 
-@pytest.mark.parametrize("Hq,Hk", [(1, 1), (4, 4), (6, 2), (14, 2), (5, 1), (32, 8), (16, 1), (100, 1), (128, 1)])
-def test_chunk_head_groups(Hq, Hk):
-    _case([19, 1, 40], [150, 77, 260], Hq=Hq, Hk=Hk, page=32)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Hq,Hk", [(1, 1), (4, 4), (6, 2), (14, 2), (5, 1), (32, 8), (16, 1), (9, 3), (5, 5),
+                                   (100, 1), (128, 1)])
+def test_chunk_head_groups(Hq, Hk, D):
+    _case([19, 1, 40], [150, 77, 260], Hq=Hq, Hk=Hk, D=D, page=32)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n", [1, 2, 3, 4, 5, 8, 9, 16, 17, 31, 32, 33])
+def test_chunk_few_rows(n, D):
+    # every way of filling the row blocks, on both sides of their limits
+    _case([n, n], [700, n], Hq=8, Hk=2, D=D, page=64)
+    _case([n], [301], Hq=3, Hk=3, D=D, page=16, softcap=10.0, window=150)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_chunk_few_loud_rows(D):
+    # the maximum of single tokens' rows moves far between tiles, rows apart
+    # from one another; the largest key may come last
+    p = _problem([1, 2], [900, 1300], 6, 3, D, 16, loud=1.0)
+    for b, n in ((0, 900), (1, 1300)):
+        ramp = torch.linspace(0, 30, n)[:, None, None]
+        p["k"][b] = (p["k"][b].float() * ramp).to(torch.bfloat16)
+        for j in range(n):
+            pg, r = int(p["table"][b, j // 16]), j % 16
+            p["kc"][pg, r] = p["k"][b][j]
+    want = _expected(p)
+    got, = _launch(p)
+    out, lse, tol = want
+    # scores of up to ~150, summed in fp32: off by at most (D + 2) 2^-24 sum |q k| / sqrt(D)
+    # < 130 * 2^-24 * 128 * 4 * 120 / 11 = 4e-2 at the very worst, typically 1e-5; a weight by
+    # as much, and 2^-22 of the exponent's argument (up to 220): 5e-5
+    assert ((got[0].double().cpu() - out).abs() <= tol + 5e-3).all()
+    assert (got[1].double().cpu() - lse).abs().max() <= 5e-3
 
 
 @pytest.mark.parametrize("D", [64, 128])
@@ -306,11 +337,23 @@ def test_chunk_long_prompts(D, Hq, Hk):
     _case([700, 1, 333], [1500, 2000, 333], Hq=Hq, Hk=Hk, D=D, page=128, calls=2)
 
 
-def test_chunk_many_requests():
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Hq,Hk", [(4, 2), (3, 3), (6, 1)])
+def test_chunk_many_requests(D, Hq, Hk):
     rng = random.Random(4)
     q_lens = [rng.choice((0, 1, 1, 1, 2, 5)) for _ in range(300)]
     kv_lens = [n + rng.randrange(0, 200) for n in q_lens]
-    _case(q_lens, kv_lens, Hq=4, Hk=2, page=16, pad=9)
+    _case(q_lens, kv_lens, Hq=Hq, Hk=Hk, D=D, page=16, pad=9)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Hq,Hk,page", [(16, 2, 64), (5, 5, 128), (4, 1, 16)])
+def test_chunk_many_long_requests(D, Hq, Hk, page):
+    # tens of key tiles per CTA, of neighbouring heads and across requests, so
+    # that the rings of tiles turn many times, at every offset to the heads
+    rng = random.Random(9)
+    kv_lens = [rng.randrange(300, 6000) for _ in range(40)]
+    _case([1] * 40, kv_lens, Hq=Hq, Hk=Hk, D=D, page=page, calls=2)
 
 
 def test_chunk_loud_scores():
