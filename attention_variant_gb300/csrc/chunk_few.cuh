@@ -165,7 +165,7 @@ __device__ void few_producer(const FewCtx<D> &cx, const ChunkParams &p, const CU
         ChunkEntry en{};
         int k_end = 0;
         while (e < me.n_entries) {
-            en = entries[e];
+            en = e == me.entry ? me.at : entries[e];
             const int full = item_heads(p, en), heads = min(full, p.Hk - h * full), n_tiles = en.n_tiles * heads;
             const int64_t x0 = en.cum + h * item_cost(p, en);
             if (x0 + static_cast<int64_t>(k) * en.tile_cost >= me.end) {
@@ -452,18 +452,6 @@ __device__ void few_pv_role(const FewCtx<D> &cx, int t)
 
 // ------------------------------------------------------------------ softmax
 
-// This thread's weights: 2^(c x - m), and rounded to bf16 in pairs.
-__device__ __forceinline__ void few_exp(const float (&x)[kFewRows], float c, const float (&m)[kFewRows],
-                                        float (&w)[kFewRows], uint32_t (&pk)[kFewRows / 2])
-{
-#pragma unroll
-    for (int n = 0; n < kFewRows; ++n)
-        w[n] = ptx::ex2(fmaf(x[n], c, m[n] == kNegInf ? 0.f : -m[n]));
-#pragma unroll
-    for (int n = 0; n < kFewRows; n += 2)
-        pk[n / 2] = ptx::pack_bf16(w[n], w[n + 1]);
-}
-
 // A float's order as a signed integer's.
 __device__ __forceinline__ int ordered(float x)
 {
@@ -472,11 +460,38 @@ __device__ __forceinline__ int ordered(float x)
 }
 __device__ __forceinline__ float unordered(int i) { return __int_as_float(i ^ ((i >> 31) & 0x7fffffff)); }
 
-template <int MOD, int D>
-__device__ void few_softmax(const FewCtx<D> &cx, const ChunkParams &p, int t)
+// This thread's weights, 2^(c x - m) (an unset reference counts as 0), and
+// rounded to bf16 in pairs.
+template <int R>
+__device__ __forceinline__ void few_exp(const float (&x)[R], float c, const float (&m)[R], bool zero, float (&w)[R],
+                                        uint32_t (&pk)[R / 2])
+{
+    if (zero) { // every reference is 0
+#pragma unroll
+        for (int n = 0; n < R; ++n)
+            w[n] = ptx::ex2(x[n] * c);
+    } else {
+#pragma unroll
+        for (int n = 0; n < R; ++n)
+            w[n] = ptx::ex2(fmaf(x[n], c, m[n] == kNegInf ? 0.f : -m[n]));
+    }
+#pragma unroll
+    for (int n = 0; n < R; n += 2)
+        pk[n / 2] = ptx::pack_bf16(w[n], w[n + 1]);
+}
+
+// What a softmax thread carries from item to item.
+struct FewState {
+    uint32_t s, pv, group, tiles; // phases of s_full, pv_done, group; tiles so far
+};
+
+// One item of at most R rows.  False when a wait ran out.
+template <int MOD, int D, int R>
+__device__ __forceinline__ bool few_item(const FewCtx<D> &cx, const ChunkParams &p, const FewItem &inf, int t,
+                                         FewState &ct)
 {
     using C = FewCfg<D>;
-    constexpr int kBN = C::kBN, R = kFewRows;
+    constexpr int kBN = C::kBN;
     FewSmem<D> &sm = *cx.sm;
     const int r = threadIdx.x & 127; // key of the tile = TMEM lane of S^T; of O^T: dimension
     const int wq = (threadIdx.x >> 5) & 3, lane = static_cast<int>(ptx::lane_id());
@@ -485,72 +500,79 @@ __device__ void few_softmax(const FewCtx<D> &cx, const ChunkParams &p, int t)
     const uint32_t tO = cx.tmem + lanes + C::kColO + C::kStride * t;
     const uint32_t b_group = bar(sm.group[t]);
     const float c = MOD == MOD_NONE ? p.qk_log2 : 1.f;
-    // 64-byte swizzle: 16-byte unit u of key r at u ^ (r / 2 mod 4)
-    uint4 *const pdst = reinterpret_cast<uint4 *>(sm.p[t] + r * C::kPRow);
-    const int sw = (r >> 1) & 3;
-    uint32_t scount = 0, pvcount = 0, group = 0, tiles = 0;
     ScoreMod smod;
     smod.qk_log2 = p.qk_log2;
     smod.softcap_in = p.softcap_in;
     smod.softcap_out = p.softcap_out;
     smod.alibi_c = smod.scale = smod.b = smod.h = 0.f;
+    // 64-byte swizzle: 16-byte unit u of key r at u ^ (r / 2 mod 4)
+    uint4 *const pdst = reinterpret_cast<uint4 *>(sm.p[t] + r * C::kPRow);
+    const int sw = (r >> 1) & 3;
     auto group_sync = [&]() {
         ptx::mbar_arrive(b_group);
-        return warp_wait(b_group, group++ & 1, cx.wc, W_JOIN);
+        return warp_wait(b_group, ct.group++ & 1, cx.wc, W_JOIN);
     };
-
-    for (uint32_t item = 0;; ++item) {
-        if (!warp_wait(bar(sm.info_full[item % kInfo]), (item / kInfo) & 1, cx.wc, W_INFO_FULL))
-            return;
-        const FewItem &inf = sm.info[item % kInfo];
-        if (inf.stop)
-            return;
-        if (t >= inf.heads) { // an odd head's item has no second slot
-            __syncwarp();
-            if (lane == 0)
-                ptx::mbar_arrive(bar(sm.info_empty[item % kInfo]));
-            continue;
-        }
-        const FewTiles f = few_tiles(inf, t);
-        const int n_mine = f.hi > f.first ? (f.hi - f.first + f.step - 1) / f.step : 0;
-        const int rows = inf.rows, pos0 = inf.pos0;
-        int full_lo, full_hi, unused;
+    const FewTiles f = few_tiles(inf, t);
+    const int n_mine = f.hi > f.first ? (f.hi - f.first + f.step - 1) / f.step : 0;
+    const int rows = inf.rows, pos0 = inf.pos0;
+    const uint32_t row_bits = (1u << rows) - 1;
+    int full_lo, full_hi, unused;
+    {
+        const int last = pos0 + fast_div(rows - 1, p.div_g);
+        key_range(p, inf.L, last, last, full_lo, unused);
+        key_range(p, inf.L, pos0, pos0, unused, full_hi);
+    }
+    float m[R], l[R], lr[R];
+#pragma unroll
+    for (int n = 0; n < R; ++n) {
+        m[n] = kNegInf;
+        l[n] = lr[n] = 0.f;
+    }
+    uint32_t set = 0;  // rows that have a reference
+    bool moved = false; // some reference is not 0
+    for (int kk = 0; kk < n_mine; ++kk) {
+        if (!warp_wait(bar(sm.s_full[t]), ct.s & 1, cx.wc, W_S_FULL))
+            return false;
+        ++ct.s;
+        ++ct.tiles;
+        ptx::tc_fence_after();
+        float x[R];
         {
-            const int last = pos0 + fast_div(rows - 1, p.div_g);
-            key_range(p, inf.L, last, last, full_lo, unused);
-            key_range(p, inf.L, pos0, pos0, unused, full_hi);
-        }
-        float m[R], l[R], lr[R];
+            uint32_t raw[R];
+            if constexpr (R == 8)
+                ptx::tmem_ld8(tS, raw);
+            else
+                ptx::tmem_ld16(tS, raw);
+            ptx::tmem_wait_ld();
+            ptx::reg_fence<R>(raw);
 #pragma unroll
-        for (int n = 0; n < R; ++n) {
-            m[n] = kNegInf;
-            l[n] = lr[n] = 0.f;
+            for (int n = 0; n < R; ++n)
+                x[n] = __uint_as_float(raw[n]);
         }
-        for (int kk = 0; kk < n_mine; ++kk) {
-            if (!warp_wait(bar(sm.s_full[t]), scount & 1, cx.wc, W_S_FULL))
-                return;
-            ++scount;
-            ++tiles;
-            ptx::tc_fence_after();
-            float x[R];
-            load_scores<R>(tS, x);
-            ptx::tc_fence_before();
-            ptx::mbar_arrive(bar(sm.s_free[t]));
-            const int j0 = ((f.first + kk * f.step) >> inf.shift) * kBN;
-            apply_score_mod<MOD, R>(x, smod, 0, j0);
-            if (!(j0 >= full_lo && j0 + kBN <= full_hi)) {
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(bar(sm.s_free[t]));
+        const int j0 = ((f.first + kk * f.step) >> inf.shift) * kBN;
+        apply_score_mod<MOD, R>(x, smod, 0, j0);
+        if (!(j0 >= full_lo && j0 + kBN <= full_hi)) {
 #pragma unroll
-                for (int n = 0; n < R; ++n) {
-                    int lo, hi;
-                    const int pos = pos0 + fast_div(n, p.div_g);
-                    key_range(p, inf.L, pos, pos, lo, hi);
-                    if (j0 + r < lo || j0 + r >= hi)
-                        x[n] = kNegInf;
-                }
+            for (int n = 0; n < R; ++n) {
+                int lo, hi;
+                const int pos = pos0 + fast_div(n, p.div_g);
+                key_range(p, inf.L, pos, pos, lo, hi);
+                if (j0 + r < lo || j0 + r >= hi)
+                    x[n] = kNegInf;
             }
-            // bit n: row n has a key here with z >= -kFewRange; bit 16 + n: one too large
-            // for the row's reference, or too small to be its first
-            uint32_t bits = 0;
+        }
+        // bit n: row n has a key here with z >= -kFewRange; bit 16 + n: one too large
+        // for the row's reference, or too small to be its first.  Once every row
+        // has the reference 0, only a logit above kFewRange asks for more.
+        const bool zero = set == row_bits && !moved;
+        uint32_t bits = 0;
+        float top = x[0];
+#pragma unroll
+        for (int n = 1; n < R; ++n)
+            top = fmaxf(top, x[n]);
+        if (!zero || top * c > kFewRange) {
 #pragma unroll
             for (int n = 0; n < R; ++n) {
                 const float z = x[n] * c;
@@ -560,27 +582,29 @@ __device__ void few_softmax(const FewCtx<D> &cx, const ChunkParams &p, int t)
                 if (large || (unset && z < -kFewRange && z > kNegInf))
                     bits |= 0x10000u << n;
             }
-            bits = __reduce_or_sync(0xffffffffu, bits);
-            if (lane == 0)
-                sm.rows[t][tiles & 1][wq] = bits;
-            float w[R];
-            uint32_t pk[R / 2];
-            few_exp(x, c, m, w, pk);
-            if (!group_sync())
-                return;
-            {
-                const volatile uint32_t *all = sm.rows[t][tiles & 1];
-                bits = all[0] | all[1] | all[2] | all[3];
-            }
-            if (kk > 0) {
-                // the previous tile's product has read P and landed in O^T
-                if (!warp_wait(bar(sm.pv_done[t]), pvcount & 1, cx.wc, W_O_FULL))
-                    return;
-                ++pvcount;
-                ptx::tc_fence_after();
-            }
+        }
+        bits = __reduce_or_sync(0xffffffffu, bits);
+        if (lane == 0)
+            sm.rows[t][ct.tiles & 1][wq] = bits;
+        float w[R];
+        uint32_t pk[R / 2];
+        few_exp(x, c, m, !moved, w, pk);
+        if (!group_sync())
+            return false;
+        {
+            const volatile uint32_t *all = sm.rows[t][ct.tiles & 1];
+            bits = all[0] | all[1] | all[2] | all[3];
+        }
+        if (kk > 0) {
+            // the previous tile's product has read P and landed in O^T
+            if (!warp_wait(bar(sm.pv_done[t]), ct.pv & 1, cx.wc, W_O_FULL))
+                return false;
+            ++ct.pv;
+            ptx::tc_fence_after();
+        }
+        if (bits) {
             // columns past the item's rows may hold anything and ask for nothing
-            const uint32_t ask = (bits >> 16) & ((1u << rows) - 1);
+            const uint32_t ask = (bits >> 16) & row_bits;
             if (ask) {
 #pragma unroll
                 for (int n = 0; n < R; ++n) {
@@ -589,110 +613,150 @@ __device__ void few_softmax(const FewCtx<D> &cx, const ChunkParams &p, int t)
                         sm.red[t][wq][n] = unordered(mx);
                 }
                 if (!group_sync())
-                    return;
-                float alpha[R];
+                    return false;
+            }
+            float alpha[R];
 #pragma unroll
-                for (int n = 0; n < R; ++n) {
+            for (int n = 0; n < R; ++n) {
+                float m_new = !(set >> n & 1u) && (bits >> n & 1u) ? 0.f : m[n];
+                if (ask >> n & 1u) {
                     const volatile float *red = &sm.red[t][0][n];
-                    const float mx = fmaxf(fmaxf(red[0], red[2 * R]), fmaxf(red[4 * R], red[6 * R]));
-                    const float other = m[n] == kNegInf && (bits >> n & 1u) ? 0.f : m[n];
-                    const float m_new = (ask >> n & 1u) ? fmaxf(m[n], mx) : other;
-                    alpha[n] = m[n] == kNegInf ? 0.f : ptx::ex2(m[n] - m_new);
-                    m[n] = m_new;
-                    l[n] *= alpha[n];
-                    lr[n] *= alpha[n];
+                    m_new = fmaxf(fmaxf(fmaxf(red[0], red[2 * kFewRows]), fmaxf(red[4 * kFewRows], red[6 * kFewRows])),
+                                  m[n]);
+                    moved = true;
                 }
+                alpha[n] = m[n] == kNegInf ? 0.f : ptx::ex2(m[n] - m_new);
+                m[n] = m_new;
+            }
+            set |= (bits | bits >> 16) & row_bits;
+            if (ask) {
                 if (kk > 0) {
                     uint32_t o[R];
-                    ptx::tmem_ld16(tO, o);
+                    if constexpr (R == 8)
+                        ptx::tmem_ld8(tO, o);
+                    else
+                        ptx::tmem_ld16(tO, o);
                     ptx::tmem_wait_ld();
-                    ptx::reg_fence<16>(o);
+                    ptx::reg_fence<R>(o);
 #pragma unroll
-                    for (int n = 0; n < R; ++n) // a row without a key so far holds zeros
+                    for (int n = 0; n < R; ++n) { // a row without a key so far holds zeros
                         o[n] = __float_as_uint(__uint_as_float(o[n]) * alpha[n]);
-                    ptx::tmem_st16(tO, o);
+                        l[n] *= alpha[n];
+                        lr[n] *= alpha[n];
+                    }
+                    if constexpr (R == 8)
+                        ptx::tmem_st8(tO, o);
+                    else
+                        ptx::tmem_st16(tO, o);
                     ptx::tmem_wait_st();
                 }
-                few_exp(x, c, m, w, pk);
-            } else {
-#pragma unroll
-                for (int n = 0; n < R; ++n)
-                    if (m[n] == kNegInf && (bits >> n & 1u))
-                        m[n] = 0.f;
+                few_exp(x, c, m, false, w, pk);
             }
-            pdst[0 ^ sw] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+        }
+        // rows from R on (R = 8) are left as they are: columns of their own
+        pdst[0 ^ sw] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+        if constexpr (R == 16)
             pdst[1 ^ sw] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
-            ptx::fence_proxy_async_smem();
-            ptx::tc_fence_before();
-            ptx::mbar_arrive(bar(sm.p_full[t]));
+        ptx::fence_proxy_async_smem();
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(bar(sm.p_full[t]));
 #pragma unroll
-            for (int n = 0; n < R; n += 2) { // the exact sum (LSE) and that of the rounded P (O)
-                ptx::add2(l[n], l[n + 1], w[n], w[n + 1]);
-                ptx::add_bf16x2_to_f32(lr[n], lr[n + 1], pk[n / 2]);
-            }
+        for (int n = 0; n < R; n += 2) { // the exact sum (LSE) and that of the rounded P (O)
+            ptx::add2(l[n], l[n + 1], w[n], w[n + 1]);
+            ptx::add_bf16x2_to_f32(lr[n], lr[n + 1], pk[n / 2]);
         }
-        if (n_mine) {
-            if (!warp_wait(bar(sm.pv_done[t]), pvcount & 1, cx.wc, W_O_FULL))
-                return;
-            ++pvcount;
-            ptx::tc_fence_after();
-        }
-        // ---- the slot's sums over the warp: lane i ends with l (i < 16) or the
-        // rounded sum of row i mod 16, halving the values at each exchange
-        float v[2 * R];
+    }
+    if (n_mine) {
+        if (!warp_wait(bar(sm.pv_done[t]), ct.pv & 1, cx.wc, W_O_FULL))
+            return false;
+        ++ct.pv;
+        ptx::tc_fence_after();
+    }
+    // ---- the slot's sums over the warp: values l, then the rounded sums, halved
+    // at each exchange until lane i holds value i (mod 2 R)
+    float v[2 * R];
+#pragma unroll
+    for (int n = 0; n < R; ++n) {
+        v[n] = l[n];
+        v[R + n] = lr[n];
+    }
+#pragma unroll
+    for (int h = R; h; h >>= 1) {
+        const bool up = lane & h;
+#pragma unroll
+        for (int i = 0; i < h; ++i)
+            v[i] = (up ? v[i + h] : v[i]) + __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i + h], h);
+    }
+    if constexpr (R == 8)
+        v[0] += __shfl_xor_sync(0xffffffffu, v[0], 16);
+    // its place among the sums of 16 rows
+    const int place = R == 8 ? (lane & 7) + 2 * (lane & 8) : lane;
+    const bool store = R == 16 || lane < 16;
+    uint32_t raw[R];
+    if (n_mine) {
+        if constexpr (R == 8)
+            ptx::tmem_ld8(tO, raw);
+        else
+            ptx::tmem_ld16(tO, raw);
+        ptx::tmem_wait_ld();
+        ptx::reg_fence<R>(raw);
+    }
+    // lane = dimension; at D = 64 the upper 64 lanes repeat the lower ones and
+    // take the odd rows
+    const int dim = D == 128 ? r : r & 63;
+    if (inf.n_parts > 1) {
+        float *mine = partial<D>(p, blockIdx.x, inf.mine, t), *sums = mine + kFewRows * 128;
 #pragma unroll
         for (int n = 0; n < R; ++n) {
-            v[n] = l[n];
-            v[R + n] = lr[n];
+            if (n < rows && (D == 128 || (n & 1) == r >> 6))
+                mine[n * 128 + dim] = n_mine ? __uint_as_float(raw[n]) : 0.f;
+            if (r == n)
+                sums[n] = m[n];
         }
+        if (store)
+            sums[kFewRows + wq * 2 * kFewRows + place] = v[0];
+        return true;
+    }
+    if (!n_mine && !group_sync()) // the last item's sums have been read
+        return false;
+    if (store)
+        sm.red[t][wq][place] = v[0];
+    if (!group_sync())
+        return false;
+    const volatile float *red = sm.red[t][0];
 #pragma unroll
-        for (int h = R; h; h >>= 1) {
-            const bool up = lane & h;
-#pragma unroll
-            for (int i = 0; i < h; ++i)
-                v[i] = (up ? v[i + h] : v[i]) + __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i + h], h);
-        }
-        uint32_t raw[R];
-        if (n_mine) {
-            ptx::tmem_ld16(tO, raw);
-            ptx::tmem_wait_ld();
-            ptx::reg_fence<16>(raw);
-        }
-        // lane = dimension; at D = 64 the upper 64 lanes repeat the lower ones
-        // and take the odd rows
-        const int dim = D == 128 ? r : r & 63;
-        if (inf.n_parts > 1) {
-            float *mine = partial<D>(p, blockIdx.x, inf.mine, t), *sums = mine + R * 128;
-#pragma unroll
-            for (int n = 0; n < R; ++n) {
-                if (n < rows && (D == 128 || (n & 1) == r >> 6))
-                    mine[n * 128 + dim] = n_mine ? __uint_as_float(raw[n]) : 0.f;
-                if (r == n)
-                    sums[n] = m[n];
-            }
-            sums[R + wq * 2 * R + lane] = v[0];
-        } else {
-            if (!n_mine && !group_sync()) // the last item's sums have been read
-                return;
-            sm.red[t][wq][lane] = v[0];
-            if (!group_sync())
-                return;
-            const volatile float *red = sm.red[t][0];
-#pragma unroll
-            for (int n = 0; n < R; ++n) {
-                if (n >= rows || (D == 64 && (n & 1) != r >> 6))
-                    continue;
-                const float sl = red[n] + red[n + 2 * R] + red[n + 4 * R] + red[n + 6 * R];
-                const float slr = red[n + R] + red[n + 3 * R] + red[n + 5 * R] + red[n + 7 * R];
-                const int s = fast_div(n, p.div_g);
-                const int64_t tok = inf.t0 + s, head = (inf.kvh + t) * p.G + n - s * p.G;
-                join_write(p, tok, head, dim, n_mine ? __uint_as_float(raw[n]) : 0.f, slr);
-                if (dim == 0)
-                    join_lse(p, tok, head, m[n], sl);
-            }
-        }
+    for (int n = 0; n < R; ++n) {
+        if (n >= rows || (D == 64 && (n & 1) != r >> 6))
+            continue;
+        constexpr int W = 2 * kFewRows;
+        const float sl = red[n] + red[n + W] + red[n + 2 * W] + red[n + 3 * W];
+        const float slr = red[n + kFewRows] + red[n + kFewRows + W] + red[n + kFewRows + 2 * W] + red[n + kFewRows + 3 * W];
+        const int s = fast_div(n, p.div_g);
+        const int64_t tok = inf.t0 + s, head = (inf.kvh + t) * p.G + n - s * p.G;
+        join_write(p, tok, head, dim, n_mine ? __uint_as_float(raw[n]) : 0.f, slr);
+        if (dim == 0)
+            join_lse(p, tok, head, m[n], sl);
+    }
+    return true;
+}
+
+template <int MOD, int D>
+__device__ void few_softmax(const FewCtx<D> &cx, const ChunkParams &p, int t)
+{
+    FewSmem<D> &sm = *cx.sm;
+    FewState ct{0u, 0u, 0u, 0u};
+    for (uint32_t item = 0;; ++item) {
+        if (!warp_wait(bar(sm.info_full[item % kInfo]), (item / kInfo) & 1, cx.wc, W_INFO_FULL))
+            return;
+        const FewItem &inf = sm.info[item % kInfo];
+        if (inf.stop)
+            return;
+        // an odd head's item has no second slot; half the rows, half the work
+        if (t < inf.heads && !(inf.rows <= 8 ? few_item<MOD, D, 8>(cx, p, inf, t, ct)
+                                             : few_item<MOD, D, 16>(cx, p, inf, t, ct)))
+            return;
         __syncwarp();
-        if (lane == 0)
+        if (ptx::lane_id() == 0)
             ptx::mbar_arrive(bar(sm.info_empty[item % kInfo]));
     }
 }

@@ -297,7 +297,8 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
                 else
                     hi = mid - 1;
             }
-            const ChunkEntry &en = p.entries[kind * p.max_entries + lo];
+            const ChunkEntry en = p.entries[kind * p.max_entries + lo];
+            out.at = en;
             const int64_t cost = item_cost(p, en);
             out.total = total;
             out.end = (total * (part + 1) + g - 1) / g;

@@ -139,7 +139,7 @@ __device__ void producer_role(const KernelCtx<D> &cx, const ChunkParams &p, cons
         ChunkEntry en{};
         int k_end = 0;
         while (e < me.n_entries) {
-            en = p.entries[e];
+            en = e == me.entry ? me.at : p.entries[e];
             const int64_t x0 = en.cum + h * item_cost(p, en);
             if (x0 + static_cast<int64_t>(k) * en.tile_cost >= me.end) {
                 e = me.n_entries; // the cut falls before this tile

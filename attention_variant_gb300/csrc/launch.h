@@ -292,6 +292,7 @@ struct ChunkPart {
     int cta, parts;            // the list's first CTA and number of parts
     int n_entries;
     int entry, item, tile, pad; // where the part begins
+    ChunkEntry at;             // that entry
 };
 // An item whose keys were cut, by the CTA it begins in.
 struct ChunkJoin {
