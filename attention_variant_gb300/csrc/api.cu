@@ -2041,8 +2041,10 @@ fl_status fl_attn_chunk(const fl_tensor *q, const fl_tensor *k_cache, const fl_t
     p.head_dim = int(pl.D);
     p.TQ = pl.TQ;
     p.div_g = fl::make_fastdiv(int32_t(G));
+    p.div_per = fl::make_fastdiv(int32_t(2 * pl.TQ));
     p.few_tq = few_tq;
-    p.few_box = few_box;
+    for (p.few_shift = 4; (1 << p.few_shift) != few_box;)
+        ++p.few_shift;
     p.max_kv = desc->max_kv_len;
     p.page_shift = -1;
     if (desc->block_table)
@@ -2070,13 +2072,18 @@ fl_status fl_attn_chunk(const fl_tensor *q, const fl_tensor *k_cache, const fl_t
         p.l_sh = L.stride[0];
     }
     p.n_cta = info.sm_count < fl::kChunkMaxCtas ? info.sm_count : fl::kChunkMaxCtas;
-    // cost units for the even split: a key tile of two row blocks, of one, of
-    // few rows, an item's start and end, and the least a CTA is woken for
-    p.cost_pair = 4;
-    p.cost_single = 3;
-    p.cost_few = 2;
-    p.cost_item = 4;
-    p.cost_least = 4;
+    // costs for the even split, in tenths of a microsecond as measured: a key
+    // tile of two row blocks (1.0 us, with softcap 2.5 at D = 64), of one, a
+    // tile of few rows (32 KB a 64 of head dimension at the SM's share of the
+    // HBM bandwidth), an item's start and end; and the least work a CTA is
+    // woken for
+    const bool capped = desc->score_mod == FL_MOD_SOFTCAP;
+    p.cost_pair = capped ? (pl.D == 64 ? 25 : 16) : 10;
+    p.cost_single = capped ? (pl.D == 64 ? 14 : 9) : 8;
+    p.cost_few = (capped ? 10 : 7) * int(pl.D / 64);
+    p.cost_item = 25;
+    p.cost_few_item = 20;
+    p.cost_least = 20;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     p.max_entries = pl.max_entries;
     p.parts = reinterpret_cast<fl::ChunkPart *>(ws);

@@ -27,9 +27,10 @@
 // fp32 sums of 2^60 such weights in range, and what lies 2^-66 below a row's
 // largest weight does not reach its bf16 output or its LSE.
 //
-//   warp  0     walks the CTA's items, publishes them, loads Q, K, V by TMA
+//   warp  0     walks the CTA's items, publishes them, loads Q, K and V by TMA
 //   warp  1     issues S^T of both slots
 //   warps 2, 3  issue O^T of slot 0, slot 1, after zeroing V rows that no row sees
+//               (or warp 2 both, and warp 3 loads V: few_split_loads)
 //   warps 4-11  the slots' softmax warpgroups
 #pragma once
 
@@ -70,7 +71,7 @@ struct FewItem {
     int heads;            // KV heads: slots in use
     int t0, rows, pos0;   // first token row, rows, first position
     int L, key_lo;        // cached keys; lowest key that any row sees
-    int kvh;
+    int b, kvh;           // request, (first) KV head
     int n_parts;          // CTAs that share the item
     int mine;             // this part's buffer: 1 if the item begins here
 };
@@ -118,46 +119,83 @@ struct FewCtx {
     WaitCtl wc;
 };
 
-// ------------------------------------------------------------------ producer
+// ------------------------------------------------------------------ producers
 
+// A ring of K or V tiles and the one warp that fills it.
+template <int D>
+struct FewRing {
+    using C = FewCfg<D>;
+    const CUtensorMap *map;
+    uint8_t (*tile)[C::kTileBytes];
+    uint64_t *full, *empty;
+    uint32_t count;
+
+    // Tile v of an item into the next stage: lane g loads the g-th box, of its page.
+    __device__ __forceinline__ bool load(const FewCtx<D> &cx, const ChunkParams &p, const FewItem &it, int v, int page)
+    {
+        const int lane = static_cast<int>(ptx::lane_id());
+        const int box = 1 << p.few_shift, key0 = (v >> it.shift) * C::kBN, left = it.L - key0;
+        const uint32_t s = count % C::kStages;
+        if (!warp_wait(bar(empty[s]), ((count / C::kStages) & 1) ^ 1, cx.wc, W_KV_EMPTY))
+            return false;
+        const int boxes = left <= 0 ? 0 : min(C::kBN >> p.few_shift, (left + box - 1) >> p.few_shift);
+        if (lane == 0)
+            ptx::mbar_arrive_expect_tx(bar(full[s]), static_cast<uint32_t>(C::kHalves * boxes * box) * C::kRowBytes);
+        __syncwarp();
+        if (lane < boxes) {
+            const int key = key0 + lane * box;
+            const int at = p.page_shift < 0 ? key : key & ((1 << p.page_shift) - 1);
+#pragma unroll
+            for (int hf = 0; hf < C::kHalves; ++hf)
+                ptx::tma_load_4d(ptx::smem_u32(tile[s]) + hf * C::kHalf + lane * box * C::kRowBytes, map,
+                                 bar(full[s]), hf * 64, at, it.kvh + (it.shift ? v & 1 : 0), page);
+        }
+        __syncwarp();
+        ++count;
+        return true;
+    }
+
+    // Waits (bounded, ignoring the abort) for the warp's loads in flight.
+    __device__ __forceinline__ void drain(const FewCtx<D> &cx) const
+    {
+        for (uint32_t idx = count > C::kStages ? count - C::kStages : 0; idx < count; ++idx)
+            mbar_wait_drain(bar(full[idx % C::kStages]), (idx / C::kStages) & 1, cx.wc, W_DRAIN);
+    }
+};
+
+// The page of this lane's box of key tile j.
+template <int D>
+__device__ __forceinline__ int few_page(const ChunkParams &p, const FewItem &it, int j)
+{
+    const int lane = static_cast<int>(ptx::lane_id()), key = j * FewCfg<D>::kBN + (lane << p.few_shift);
+    if (lane >= FewCfg<D>::kBN >> p.few_shift || key >= it.L)
+        return 0; // never loaded
+    return p.page_shift < 0 ? it.b : __ldg(p.block_table + static_cast<int64_t>(it.b) * p.bt_stride + (key >> p.page_shift));
+}
+
+// Who loads V: with boxes of 64 keys or more the warp that loads K; with
+// smaller ones their number is too much for one warp (pages of 16 keys: 264
+// against 184 us for 64 requests of 8192 keys), and V gets the warp that
+// otherwise issues O^T of slot 1 (which costs 5% where it is not needed).
+__device__ __forceinline__ bool few_split_loads(const ChunkParams &p) { return p.few_shift < 6; }
+
+// Walks the CTA's items, publishes them, loads Q, K and, mostly, V.
 template <int D>
 __device__ void few_producer(const FewCtx<D> &cx, const ChunkParams &p, const CUtensorMap *tm_q,
                              const CUtensorMap *tm_k, const CUtensorMap *tm_v)
 {
     using C = FewCfg<D>;
-    constexpr int kBN = C::kBN, kStages = C::kStages;
+    constexpr int kBN = C::kBN;
     FewSmem<D> &sm = *cx.sm;
     const uint32_t lane = ptx::lane_id();
-    uint32_t k_count = 0, v_count = 0, item_count = 0;
+    FewRing<D> keys{tm_k, sm.k, sm.k_full, sm.k_empty, 0u}, values{tm_v, sm.v, sm.v_full, sm.v_empty, 0u};
+    const bool split = few_split_loads(p);
+    uint32_t item_count = 0;
     bool ok = true;
-    const ChunkPart me = p.parts[blockIdx.x];
+    const ChunkPart me = p.parts[part_of()];
     const ChunkEntry *entries = p.entries + p.max_entries;
-    const int cta = static_cast<int>(blockIdx.x) - me.cta;
+    const int cta = part_of() - me.cta;
     int e = me.entry, h = me.item, k = me.tile; // entry, item of it, tile of that
-    const int boxes_tile = kBN / p.few_box;
-    // lane g loads the g-th box of few_box keys of tile v into the ring's next stage
-    auto load = [&](const CUtensorMap *map, uint8_t (*ring)[C::kTileBytes], uint64_t *full, uint64_t *empty,
-                    uint32_t count, const FewItem &it, int v, int page) {
-        const uint32_t s = count % kStages;
-        if (!warp_wait(bar(empty[s]), ((count / kStages) & 1) ^ 1, cx.wc, W_KV_EMPTY))
-            return false;
-        const int key0 = (v >> it.shift) * kBN, left = it.L - key0;
-        const int boxes = left <= 0 ? 0 : min(boxes_tile, (left + p.few_box - 1) / p.few_box);
-        if (lane == 0)
-            ptx::mbar_arrive_expect_tx(bar(full[s]),
-                                       static_cast<uint32_t>(C::kHalves * boxes * p.few_box) * C::kRowBytes);
-        __syncwarp();
-        if (static_cast<int>(lane) < boxes) {
-            const int key = key0 + static_cast<int>(lane) * p.few_box;
-            const int at = p.page_shift < 0 ? key : key & ((1 << p.page_shift) - 1);
-#pragma unroll
-            for (int hf = 0; hf < C::kHalves; ++hf)
-                ptx::tma_load_4d(ptx::smem_u32(ring[s]) + hf * C::kHalf + lane * p.few_box * C::kRowBytes, map,
-                                 bar(full[s]), hf * 64, at, it.kvh + (it.shift ? v & 1 : 0), page);
-        }
-        __syncwarp();
-        return true;
-    };
     for (;;) {
         // ---- the next part
         FewItem it;
@@ -192,6 +230,7 @@ __device__ void few_producer(const FewCtx<D> &cx, const ChunkParams &p, const CU
             it.shift = it.heads - 1;
             it.u_lo = (en.lo << it.shift) + k;
             it.u_hi = (en.lo << it.shift) + k_end;
+            it.b = en.b;
             it.t0 = en.t0;
             it.rows = en.n_tok * p.G;
             it.pos0 = en.pos0;
@@ -210,7 +249,7 @@ __device__ void few_producer(const FewCtx<D> &cx, const ChunkParams &p, const CU
             sm.info[slot] = it;
             ptx::mbar_arrive(bar(sm.info_full[slot])); // release: the fields above first
             if (!it.stop && it.mine && it.n_parts > 1)
-                p.joins[blockIdx.x] = ChunkJoin{it.n_parts, JOIN_FEW, it.kvh, {it.t0, it.t0},
+                p.joins[part_of()] = ChunkJoin{it.n_parts, JOIN_FEW, it.kvh, {it.t0, it.t0},
                                                 {it.rows, it.heads == 2 ? it.rows : 0}, 0};
         }
         __syncwarp();
@@ -233,36 +272,21 @@ __device__ void few_producer(const FewCtx<D> &cx, const ChunkParams &p, const CU
         ++item_count;
         // ---- K and V: V trails by kLag tiles, as P V trails S, so that it does
         // not wait in shared memory for its weights (not past the item: the next
-        // item's buffers may wait for the V of its last tile).  Pages are fetched a tile ahead.
-        const int64_t row = static_cast<int64_t>(en.b) * p.bt_stride;
-        auto page_of = [&](int j) {
-            const int key = j * kBN + static_cast<int>(lane) * p.few_box;
-            if (static_cast<int>(lane) >= boxes_tile || key >= it.L)
-                return 0;
-            return p.page_shift < 0 ? en.b : __ldg(p.block_table + row + (key >> p.page_shift));
-        };
-        int page_next = page_of(it.u_lo >> it.shift);
-        int page_v[C::kLag + 1]; // pages of the last kLag + 1 tiles, the latest first
-        for (int v = it.u_lo; v < it.u_hi + C::kLag; ++v) {
-            // K of tile v, V of tile v - kLag
+        // item's buffers may wait for the V of its last tile).  Pages are fetched
+        // a tile ahead.
+        int page_next = few_page<D>(p, it, it.u_lo >> it.shift);
+        int page[C::kLag + 1]; // of the last kLag + 1 tiles, the latest first
+        for (int v = it.u_lo; v < it.u_hi + (split ? 0 : C::kLag) && ok; ++v) {
 #pragma unroll
             for (int i = C::kLag; i > 0; --i)
-                page_v[i] = page_v[i - 1];
-            page_v[0] = page_next;
+                page[i] = page[i - 1];
+            page[0] = page_next;
             if (v + 1 < it.u_hi)
-                page_next = page_of((v + 1) >> it.shift);
-            if (v < it.u_hi) {
-                ok = load(tm_k, sm.k, sm.k_full, sm.k_empty, k_count, it, v, page_v[0]);
-                if (!ok)
-                    break;
-                ++k_count;
-            }
-            if (v - C::kLag >= it.u_lo) {
-                ok = load(tm_v, sm.v, sm.v_full, sm.v_empty, v_count, it, v - C::kLag, page_v[C::kLag]);
-                if (!ok)
-                    break;
-                ++v_count;
-            }
+                page_next = few_page<D>(p, it, (v + 1) >> it.shift);
+            if (v < it.u_hi)
+                ok = keys.load(cx, p, it, v, page[0]);
+            if (ok && !split && v - C::kLag >= it.u_lo)
+                ok = values.load(cx, p, it, v - C::kLag, page[C::kLag]);
         }
         if (!ok)
             break;
@@ -274,14 +298,40 @@ __device__ void few_producer(const FewCtx<D> &cx, const ChunkParams &p, const CU
         }
     }
     if (!ok) {
-        // wait (bounded, ignoring the abort) for this warp's own loads in flight
-        for (uint32_t idx = k_count > kStages ? k_count - kStages : 0; idx < k_count; ++idx)
-            mbar_wait_drain(bar(sm.k_full[idx % kStages]), (idx / kStages) & 1, cx.wc, W_DRAIN);
-        for (uint32_t idx = v_count > kStages ? v_count - kStages : 0; idx < v_count; ++idx)
-            mbar_wait_drain(bar(sm.v_full[idx % kStages]), (idx / kStages) & 1, cx.wc, W_DRAIN);
+        keys.drain(cx);
+        values.drain(cx);
         for (uint32_t n = item_count > 2 ? item_count - 2 : 0; n < item_count; ++n)
             mbar_wait_drain(bar(sm.q_full[n & 1]), (n >> 1) & 1, cx.wc, W_DRAIN);
     }
+}
+
+// Loads V alone (few_split_loads).
+template <int D>
+__device__ void few_v_producer(const FewCtx<D> &cx, const ChunkParams &p, const CUtensorMap *tm_v)
+{
+    FewSmem<D> &sm = *cx.sm;
+    FewRing<D> values{tm_v, sm.v, sm.v_full, sm.v_empty, 0u};
+    bool ok = true;
+    for (uint32_t n = 0; ok; ++n) {
+        const uint32_t slot = n % kInfo;
+        ok = warp_wait(bar(sm.info_full[slot]), (n / kInfo) & 1, cx.wc, W_INFO_FULL);
+        if (!ok)
+            break;
+        const FewItem it = sm.info[slot];
+        __syncwarp();
+        if (ptx::lane_id() == 0)
+            ptx::mbar_arrive(bar(sm.info_empty[slot]));
+        if (it.stop)
+            return;
+        int page_next = few_page<D>(p, it, it.u_lo >> it.shift);
+        for (int v = it.u_lo; v < it.u_hi && ok; ++v) {
+            const int page = page_next;
+            if (v + 1 < it.u_hi)
+                page_next = few_page<D>(p, it, (v + 1) >> it.shift);
+            ok = values.load(cx, p, it, v, page);
+        }
+    }
+    values.drain(cx);
 }
 
 // ------------------------------------------------------------------ MMA issuers
@@ -361,8 +411,11 @@ __device__ void few_s_role(const FewCtx<D> &cx)
     mbar_wait_drain(b_final, 0, cx.wc, W_FINAL);
 }
 
+// Issues O^T of the slots from `slot` on: both, or one.  Every warp of this role
+// passes every tile in order (and releases what is not its own), so that none
+// is ever a turn of the ring away from a barrier whose parity it waits for.
 template <int D>
-__device__ void few_pv_role(const FewCtx<D> &cx, int t)
+__device__ void few_pv_role(const FewCtx<D> &cx, int slot_lo, int slot_hi)
 {
     using C = FewCfg<D>;
     constexpr int kBN = C::kBN, kStages = C::kStages;
@@ -374,9 +427,8 @@ __device__ void few_pv_role(const FewCtx<D> &cx, int t)
     constexpr uint32_t idesc = umma_idesc_bf16(128, kFewRows, true) | (1u << 15);
     constexpr uint64_t kHiV = umma_desc_hi(D == 128 ? C::kHalf : 0, C::kGroupBytes, kSwizzle128B);
     constexpr uint64_t kHiP = umma_desc_hi(16, 8 * C::kPRow, kSwizzle64B);
-    const uint32_t v_lo0 = ptx::smem_u32(sm.v[0]) >> 4, p_lo = ptx::smem_u32(sm.p[t]) >> 4;
-    const uint32_t tO = cx.tmem + C::kColO + C::kStride * t;
-    uint32_t idx = 0, pcount = 0;
+    const uint32_t v_lo0 = ptx::smem_u32(sm.v[0]) >> 4, p_lo0 = ptx::smem_u32(sm.p[0]) >> 4;
+    uint32_t idx = 0, pcount[2] = {0u, 0u};
     bool ok = true;
     for (uint32_t n = 0; ok; ++n) {
         const uint32_t slot = n % kInfo;
@@ -385,8 +437,8 @@ __device__ void few_pv_role(const FewCtx<D> &cx, int t)
             break;
         const FewItem &inf = sm.info[slot];
         const int stop = inf.stop, shift = inf.shift, u_lo = inf.u_lo, u_hi = inf.u_hi;
-        const int L = inf.L, key_lo = inf.key_lo;
-        const FewTiles f = few_tiles(inf, t);
+        const int lo = inf.lo << shift, hi = inf.hi << shift, L = inf.L, key_lo = inf.key_lo;
+        const int first = max(u_lo, lo);
         __syncwarp();
         if (lane == 0)
             ptx::mbar_arrive(bar(sm.info_empty[slot]));
@@ -394,25 +446,19 @@ __device__ void few_pv_role(const FewCtx<D> &cx, int t)
             break;
         for (int v = u_lo; v < u_hi; ++v, ++idx) {
             const uint32_t stage = idx % kStages;
-            if ((shift ? v & 1 : 0) != t || v < f.first || v >= f.hi) {
-                // the other slot's tile, or one that no row sees: released by this
-                // warp once it has landed.  Both warps pass every tile in order, so
-                // that neither is ever a whole turn of the ring away from a barrier
-                // whose parity it waits for.
-                ok = warp_wait(bar(sm.v_full[stage]), (idx / kStages) & 1, cx.wc, W_KV_FULL);
-                if (!ok)
-                    break;
+            const int t = shift ? v & 1 : 0, j0 = (v >> shift) * kBN;
+            ok = warp_wait(bar(sm.v_full[stage]), (idx / kStages) & 1, cx.wc, W_KV_FULL);
+            if (!ok)
+                break;
+            if (v < lo || v >= hi || t < slot_lo || t > slot_hi) {
+                // no row sees it, or another warp's
                 if (lane == 0)
                     ptx::mbar_arrive(bar(sm.v_empty[stage]));
                 __syncwarp();
                 continue;
             }
-            ok = warp_wait(bar(sm.v_full[stage]), (idx / kStages) & 1, cx.wc, W_KV_FULL);
-            if (!ok)
-                break;
             // rows of V that no query row sees: zero (their P is 0, but the bytes
             // may be anything)
-            const int j0 = (v >> shift) * kBN;
             const int dead_lo = min(kBN, max(0, key_lo - j0)), dead_hi = min(kBN, max(0, L - j0));
             if (dead_lo > 0 || dead_hi < kBN) {
 #pragma unroll
@@ -426,24 +472,25 @@ __device__ void few_pv_role(const FewCtx<D> &cx, int t)
                 ptx::fence_proxy_async_smem();
                 __syncwarp();
             }
-            ok = warp_wait(bar(sm.p_full[t]), pcount & 1, cx.wc, W_P_FULL);
+            ok = warp_wait(bar(sm.p_full[t]), pcount[t] & 1, cx.wc, W_P_FULL);
             if (!ok)
                 break;
-            ++pcount;
+            ++pcount[t];
             ptx::tc_fence_after();
             if (lane == 0) {
-                const uint32_t vlo = v_lo0 + stage * (C::kTileBytes >> 4);
+                const uint32_t vlo = v_lo0 + stage * (C::kTileBytes >> 4), plo = p_lo0 + t * (kBN * C::kPRow >> 4);
+                const bool begun = v - first >= 1 << shift; // not the slot's first tile
 #pragma unroll
                 for (int kk = 0; kk < kBN / 16; ++kk)
-                    ptx::mma_ss(tO, kHiV | (vlo + kk * (16 * C::kRowBytes >> 4)),
-                                kHiP | (p_lo + kk * (16 * C::kPRow >> 4)), idesc, (v > f.first || kk > 0) ? 1u : 0u);
+                    ptx::mma_ss(cx.tmem + C::kColO + C::kStride * t, kHiV | (vlo + kk * (16 * C::kRowBytes >> 4)),
+                                kHiP | (plo + kk * (16 * C::kPRow >> 4)), idesc, (begun || kk > 0) ? 1u : 0u);
                 ptx::mma_commit(bar(sm.pv_done[t]));
                 ptx::mma_commit(bar(sm.v_empty[stage]));
             }
             __syncwarp();
         }
     }
-    const uint32_t b_final = bar(sm.final_bar[1 + t]);
+    const uint32_t b_final = bar(sm.final_bar[1 + slot_lo]);
     if (lane == 0)
         ptx::mma_commit(b_final);
     __syncwarp();
@@ -705,7 +752,7 @@ __device__ __forceinline__ bool few_item(const FewCtx<D> &cx, const ChunkParams 
     // take the odd rows
     const int dim = D == 128 ? r : r & 63;
     if (inf.n_parts > 1) {
-        float *mine = partial<D>(p, blockIdx.x, inf.mine, t), *sums = mine + kFewRows * 128;
+        float *mine = partial<D>(p, part_of(), inf.mine, t), *sums = mine + kFewRows * 128;
 #pragma unroll
         for (int n = 0; n < R; ++n) {
             if (n < rows && (D == 128 || (n & 1) == r >> 6))
@@ -774,13 +821,13 @@ __device__ __forceinline__ void few_path(const ChunkMaps &maps, const ChunkParam
         }
         for (int b = 0; b < kInfo; ++b) {
             ptx::mbar_init(bar(sm->info_full[b]), 1);
-            ptx::mbar_init(bar(sm->info_empty[b]), 11); // S, two P V and eight softmax warps
+            ptx::mbar_init(bar(sm->info_empty[b]), 11); // all but the producer
         }
         for (int s = 0; s < C::kStages; ++s) {
             ptx::mbar_init(bar(sm->k_full[s]), 1);
             ptx::mbar_init(bar(sm->k_empty[s]), 1);
             ptx::mbar_init(bar(sm->v_full[s]), 1);
-            ptx::mbar_init(bar(sm->v_empty[s]), 2); // both P V warps
+            ptx::mbar_init(bar(sm->v_empty[s]), few_split_loads(p) ? 1 : 2); // the warps that issue O^T
         }
         for (int t = 0; t < 2; ++t) {
             ptx::mbar_init(bar(sm->s_full[t]), 1);
@@ -816,8 +863,12 @@ __device__ __forceinline__ void few_path(const ChunkMaps &maps, const ChunkParam
             few_producer(cx, p, &maps.few_q, &maps.few_k, &maps.few_v);
         else if (warp == 1)
             few_s_role(cx);
+        else if (!few_split_loads(p))
+            few_pv_role(cx, warp - 2, warp - 2);
+        else if (warp == 2)
+            few_pv_role(cx, 0, 1);
         else
-            few_pv_role(cx, warp - 2);
+            few_v_producer(cx, p, &maps.few_v);
         ptx::tc_fence_before();
         ptx::named_barrier_sync(1, kThreads);
         if (warp == 1) {

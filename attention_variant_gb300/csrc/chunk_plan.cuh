@@ -48,6 +48,14 @@ __device__ __forceinline__ void key_range(const ChunkParams &p, int L, int first
 
 __device__ __forceinline__ bool is_few(const ChunkParams &p, int n_tok) { return n_tok * p.G <= kFewRows; }
 
+// a / b for a >= 0, b > 0: costs are 64-bit, but their division is only where it has to be.
+__device__ __forceinline__ int64_t div64(int64_t a, int64_t b)
+{
+    if (((a | b) >> 32) == 0)
+        return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return a / b;
+}
+
 // KV heads of an entry's items (the last may have fewer).
 __device__ __forceinline__ int item_heads(const ChunkParams &p, const ChunkEntry &en)
 {
@@ -58,15 +66,24 @@ __device__ __forceinline__ int item_heads(const ChunkParams &p, const ChunkEntry
 // it comes last in its entry, so positions divide by this.
 __device__ __forceinline__ int64_t item_cost(const ChunkParams &p, const ChunkEntry &en)
 {
-    return static_cast<int64_t>(en.n_tiles) * item_heads(p, en) * en.tile_cost + p.cost_item;
+    return static_cast<int64_t>(en.n_tiles) * item_heads(p, en) * en.tile_cost +
+           (is_few(p, en.n_tok) ? p.cost_few_item : p.cost_item);
 }
 
 __device__ __forceinline__ int64_t entry_cost(const ChunkParams &p, const ChunkEntry &en)
 {
     const int heads = item_heads(p, en);
     return static_cast<int64_t>(en.n_tiles) * p.Hk * en.tile_cost +
-           static_cast<int64_t>((p.Hk + heads - 1) / heads) * p.cost_item;
+           static_cast<int64_t>(heads == 2 ? (p.Hk + 1) >> 1 : p.Hk) *
+               (is_few(p, en.n_tok) ? p.cost_few_item : p.cost_item);
 }
+
+// The part of this CTA.  The two SMs of a pair run one path at their best: the
+// instructions of both do not fit what they share (a pair that ran both took
+// 20% longer).  CTAs go to SMs in order, two by two, but for the first one,
+// whose neighbour is the SM that the planning kernel still held; it gets the
+// last.  Where CTAs are placed otherwise the results are the same.
+__device__ __forceinline__ int part_of() { return blockIdx.x + 1 == gridDim.x ? 0 : blockIdx.x + 1; }
 
 // Part c of `parts` covers the cost units x with c total / parts <= x <
 // (c + 1) total / parts, and a tile belongs to the part of its first unit.
@@ -190,7 +207,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
             n = t1 - t0;
             L = min(max(L, 0), p.max_kv);
         }
-        const int ent = (n + per - 1) / per;
+        const int ent = fast_div(n + per - 1, p.div_per);
         const int end = block_scan(ent, s_scan);
         s_ent[tid] = end - ent;
         if (tid == threads - 1)
@@ -261,21 +278,22 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
         }
     if (err && p.err_user)
         atomicOr(p.err_user, err);
-    // CTAs of each list by its share of the cost; a part is at least one tile
-    // long, so that every CTA between the first and the last of an item holds
+    // CTAs of each list by its share of the cost, in pairs (see part_of); a part
+    // is at least one tile long, so that every CTA between the first and the last of an item holds
     // one of its tiles
     int parts[2];
     {
         const int64_t both = cum[0] + cum[1];
-        int share = both ? static_cast<int>((cum[0] * p.n_cta + both / 2) / both) : 0;
+        int share = cum[0] ? p.n_cta : 0;
         if (cum[0] && cum[1])
-            share = min(max(share, 1), p.n_cta - 1);
+            share = min(max(static_cast<int>(div64(cum[0] * p.n_cta + both, 2 * both)) * 2, 2), p.n_cta - 2);
 #pragma unroll
         for (int kind = 0; kind < 2; ++kind) {
             const int64_t tile = kind ? p.cost_few : s_most, least = max(tile, static_cast<int64_t>(p.cost_least));
-            int g = static_cast<int>(
-                min(static_cast<int64_t>(kind ? p.n_cta - share : share), (cum[kind] + least - 1) / least));
-            if (g > 1 && cum[kind] / g < tile)
+            int g = kind ? p.n_cta - share : share;
+            if (cum[kind] < least * g)
+                g = static_cast<int>(div64(cum[kind] + least - 1, least));
+            if (g > 1 && cum[kind] < tile * g)
                 --g;
             parts[kind] = g;
         }
@@ -286,7 +304,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
             const int kind = c >= parts[0] ? 1 : 0;
             const int part = kind ? c - parts[0] : c, g = kind ? parts[1] : parts[0];
             const int64_t total = kind ? cum[1] : cum[0];
-            const int64_t x = (total * part + g - 1) / g;      // first cost unit of this part
+            const int64_t x = div64(total * part + g - 1, g);  // first cost unit of this part
             int lo = 0, hi = (kind ? count[1] : count[0]) - 1; // the last entry that starts at or before x
             while (lo < hi) {
                 const int mid = (lo + hi + 1) >> 1;
@@ -301,15 +319,15 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
             out.at = en;
             const int64_t cost = item_cost(p, en);
             out.total = total;
-            out.end = (total * (part + 1) + g - 1) / g;
+            out.end = div64(total * (part + 1) + g - 1, g);
             out.few = kind;
             out.cta = kind ? parts[0] : 0;
             out.parts = g;
             out.n_entries = kind ? count[1] : count[0];
             out.entry = lo;
-            out.item = static_cast<int>((x - en.cum) / cost);
+            out.item = static_cast<int>(div64(x - en.cum, cost));
             const int64_t in = x - en.cum - out.item * cost;
-            out.tile = static_cast<int>((in + en.tile_cost - 1) / en.tile_cost);
+            out.tile = static_cast<int>(div64(in + en.tile_cost - 1, en.tile_cost));
         }
         p.parts[c] = out;
     }

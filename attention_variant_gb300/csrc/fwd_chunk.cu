@@ -129,8 +129,8 @@ __device__ void producer_role(const KernelCtx<D> &cx, const ChunkParams &p, cons
     const uint32_t lane = ptx::lane_id();
     uint32_t kv_count = 0, item_count = 0;
     bool ok = true;
-    const ChunkPart me = p.parts[blockIdx.x];
-    const int cta = static_cast<int>(blockIdx.x) - me.cta;
+    const ChunkPart me = p.parts[part_of()];
+    const int cta = part_of() - me.cta;
     int e = me.entry, h = me.item, k = me.tile; // entry, item of it, tile of that
     for (;;) {
         // ---- the next part
@@ -188,7 +188,7 @@ __device__ void producer_role(const KernelCtx<D> &cx, const ChunkParams &p, cons
             sm.info[slot] = it;
             ptx::mbar_arrive(bar(sm.info_full[slot])); // release: the fields above first
             if (!it.stop && it.mine && it.n_parts > 1)
-                p.joins[blockIdx.x] = ChunkJoin{it.n_parts, it.pair ? JOIN_PAIR : JOIN_HALF, it.kvh,
+                p.joins[part_of()] = ChunkJoin{it.n_parts, it.pair ? JOIN_PAIR : JOIN_HALF, it.kvh,
                                                 {it.t0[0], it.t0[1]}, {it.rows[0], it.rows[1]}, 0};
         }
         __syncwarp();
@@ -473,7 +473,7 @@ __device__ __forceinline__ RowOut<D> row_out(const ChunkParams &p, const Item &i
     RowOut<D> w;
     w.out = p.out + tok * p.o_st + head * p.o_sh;
     w.lse = p.lse ? p.lse + head * p.l_sh + tok : nullptr;
-    w.mine = partial<D>(p, blockIdx.x, inf.mine, t) + r;
+    w.mine = partial<D>(p, part_of(), inf.mine, t) + r;
     return w;
 }
 
@@ -821,7 +821,7 @@ __device__ __forceinline__ void block_path(const ChunkMaps &maps, const ChunkPar
     }
 }
 
-// The first CTAs walk the row blocks, the others the few rows.
+// The first parts are of the row blocks, the others of the few rows.
 template <int MOD, int D>
 __global__ void __launch_bounds__(kThreads, 1)
     chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constant__ ChunkParams p)
@@ -839,7 +839,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     ptx::launch_dependents();
     ptx::wait_dependency(); // the plan
-    const int parts = p.parts[blockIdx.x].parts, few = p.parts[blockIdx.x].few;
+    const int parts = p.parts[part_of()].parts, few = p.parts[part_of()].few;
     if (parts == 0)
         return; // no work for this CTA
     if (!few)

@@ -307,8 +307,9 @@ struct ChunkParams {
     int T, batch, Hq, Hk, G, head_dim;
     int TQ;                    // tokens per 128-row block: 128 / G
     FastDiv div_g;
+    FastDiv div_per;           // 2 TQ, tokens per entry
     int few_tq;                // tokens of few rows: kFewRows / G
-    int few_box;               // keys per TMA box of the few-row path
+    int few_shift;             // log2 of the keys per TMA box of the few-row path
     int max_kv, page_shift;    // page_shift < 0: contiguous cache
     int64_t bt_stride;
     const int32_t *cu_q, *kv_lens, *block_table;
@@ -322,7 +323,7 @@ struct ChunkParams {
     float *lse;                // [Hq, T] or null
     int64_t l_sh;
     int n_cta;
-    int cost_pair, cost_single, cost_few, cost_item, cost_least; // see api.cu
+    int cost_pair, cost_single, cost_few, cost_item, cost_few_item, cost_least; // see api.cu
     int max_entries;
     ChunkPart *parts;          // the workspace: [n_cta]
     ChunkJoin *joins;          // [n_cta]
