@@ -478,39 +478,57 @@ def fl_attn_decode_static(q, k_cache, v_cache, out, lse, desc: FlDecodeDesc, str
 # Rotary positions and serving steps.  These calls are a few microseconds of
 # GPU work, so their marshalling is kept short: a tensor travels as the packed
 # bytes of its fl_tensor (one struct.pack; a ctypes structure filled field by
-# field takes three times as long).
+# field takes three times as long), and what is needed of torch is looked up once.
 
-_PACK = {n: struct.Struct(f"<Qii{n}q{8 * (5 - n)}x{n}q{8 * (5 - n)}x") for n in range(1, 6)}
-_CODES: dict = {}
+_PACK = [None] + [struct.Struct(f"<Qii{n}q{8 * (5 - n)}x{n}q{8 * (5 - n)}x").pack for n in range(1, 6)]
+
+
+class _Torch:
+    """What these calls use of torch."""
+
+    def __init__(self):
+        import torch
+        self.codes = {torch.bfloat16: FL_BF16, torch.float32: FL_F32}
+        self.types = {"int32": torch.int32, "int64": torch.int64}
+        self.int32, self.int64 = torch.int32, torch.int64
+        self.device = torch.cuda.current_device
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        self.stream = raw or (lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
+_torch = None
+
+
+def _tools() -> _Torch:
+    global _torch
+    if _torch is None:
+        _torch = _Torch()
+    return _torch
 
 
 def _pack(t, device: int):
     """A torch tensor (or None) of CUDA device `device` -> the bytes of its fl_tensor."""
     if t is None:
         return None
-    if t.get_device() != device:
-        raise ValueError(f"tensor on {t.device}: the current device is cuda:{device}")
-    if not _CODES:
-        import torch
-        _CODES.update({torch.bfloat16: FL_BF16, torch.float32: FL_F32})
-    code = _CODES.get(t.dtype)
-    if code is None:
-        raise TypeError(f"unsupported dtype {t.dtype}")
     shape = t.shape
-    if not 1 <= len(shape) <= 5:
-        raise ValueError(f"tensors have 1 to 5 dimensions, got {len(shape)}")
-    return _PACK[len(shape)].pack(t.data_ptr(), code, len(shape), *shape, *t.stride())
+    n = len(shape)
+    code = _torch.codes.get(t.dtype)
+    if code is None or t.get_device() != device or not 1 <= n <= 5:
+        if t.get_device() != device:
+            raise ValueError(f"tensor on {t.device}: the current device is cuda:{device}")
+        if code is None:
+            raise TypeError(f"unsupported dtype {t.dtype}")
+        raise ValueError(f"tensors have 1 to 5 dimensions, got {n}")
+    return _PACK[n](t.data_ptr(), code, n, *shape, *t.stride())
 
 
 def _device() -> int:
-    import torch
-    return torch.cuda.current_device()
+    return _tools().device()
 
 
-def _stream_of(stream) -> int:
+def _stream_of(stream, device: int) -> int:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _torch.stream(device)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 
 
@@ -521,10 +539,10 @@ def _check(st: int) -> None:
 
 def _index(t, name: str, shape, dtype="int32", device=None) -> int:
     """The address of a contiguous integer tensor of the given shape (None entries: any size)."""
-    import torch
-    if t.dtype != getattr(torch, dtype):
+    if t.dtype is not _tools().types[dtype]:
         raise TypeError(f"{name} must be {dtype}, is {t.dtype}")
-    if t.dim() != len(shape) or any(s is not None and s != n for s, n in zip(shape, t.shape)):
+    if t.shape != shape and (t.dim() != len(shape) or
+                             any(s is not None and s != n for s, n in zip(shape, t.shape))):
         raise ValueError(f"{name} must have shape {tuple(shape)}, has {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -562,13 +580,14 @@ def fl_rope(q, k, q_out, k_out, table: FlRopeTable, positions=None, offset=0, ba
     dev = _device()
     at = rows = 0
     if positions is not None:
+        shape = q.shape
         if positions.dim() == 2:
-            at, rows = _index(positions, "positions", q.shape[:2], device=dev), q.shape[1]
+            at, rows = _index(positions, "positions", shape[:2], device=dev), shape[1]
         else:
-            at = _index(positions, "positions", q.shape[-3:-2], device=dev)
+            at = _index(positions, "positions", shape[-3:-2], device=dev)
     desc = _ROPE_DESC.pack(ctypes.addressof(table), at, rows, int(offset), 1 if backward else 0)
     _check(lib.fl_rope(_pack(q, dev), _pack(k, dev), _pack(q_out, dev), _pack(k_out, dev), desc,
-                       _stream_of(stream)))
+                       _stream_of(stream, dev)))
 
 
 def make_kv_plan_desc(q_lens, kv_lens, free_pages, free_head, block_table, kv_lens_out, cu_q, positions,
@@ -601,7 +620,7 @@ def make_kv_plan_desc(q_lens, kv_lens, free_pages, free_head, block_table, kv_le
 
 def fl_kv_plan(desc: FlKvPlanDesc, stream=None) -> None:
     """Enqueue a serving step's book-keeping (see include/fl_attn.h)."""
-    _check(load_library().fl_kv_plan(ctypes.byref(desc), _stream_of(stream)))
+    _check(load_library().fl_kv_plan(ctypes.byref(desc), _stream_of(stream, _device())))
 
 
 def fl_kv_append(q, k, v, q_out, k_cache, v_cache, slots, *, rope: FlRopeTable | None = None,
@@ -621,7 +640,7 @@ def fl_kv_append(q, k, v, q_out, k_cache, v_cache, slots, *, rope: FlRopeTable |
     _check(lib.fl_kv_append(_pack(q, dev), _pack(k, dev), _pack(v, dev), _pack(q_out, dev),
                             _pack(k_cache, dev), _pack(v_cache, dev),
                             _index(slots, "slots", k.shape[:1], "int64", device=dev), desc,
-                            _stream_of(stream)))
+                            _stream_of(stream, dev)))
 
 
 def make_chunk_desc(cu_q, kv_lens, block_table, max_kv_len: int, *, score_mod="none", softcap=20.0,
@@ -667,4 +686,4 @@ def fl_attn_chunk(q, k_cache, v_cache, out, lse, desc: FlChunkDesc, workspace, s
     dev = _device()
     _check(lib.fl_attn_chunk(_pack(q, dev), _pack(k_cache, dev), _pack(v_cache, dev), _pack(out, dev),
                              _pack(lse, dev), ctypes.byref(desc), workspace.data_ptr(),
-                             workspace.numel() * workspace.element_size(), _stream_of(stream)))
+                             workspace.numel() * workspace.element_size(), _stream_of(stream, dev)))

@@ -1007,12 +1007,13 @@ fl_status check_rope(const fl_rope_desc *d, int64_t D)
 
 void set_rope(fl::RopeParams &p, const fl_rope_desc *d, int64_t D)
 {
-    p.div_seq = fl::make_fastdiv(1);
-    p.div_tile_page = fl::make_fastdiv(1);
+    p.div_pairs = fl::make_fastdiv(1);
+    p.page_rows = 1;
     if (d) {
         const fl_rope_table &t = *d->table;
         p.rot = t.rot_dim;
         p.pairs = t.rot_dim / 2;
+        p.div_pairs = fl::make_fastdiv(p.pairs);
         p.magnitude = t.magnitude;
         p.positions = d->positions;
         p.positions_stride = d->positions_stride;
@@ -1035,9 +1036,9 @@ void add_stream(fl::RopeParams &p, const View &src, const View &dst, bool rotate
     st.d_s = dst.stride[1];
     st.d_h = dst.stride[2];
     st.heads = int(src.size[2]);
+    st.div_heads = fl::make_fastdiv(st.heads);
     st.rotate = rotate ? 1 : 0;
     st.to_cache = to_cache ? 1 : 0;
-    p.heads += st.heads;
 }
 
 // The widest vector (in elements) that divides the rotated halves and the
@@ -1798,8 +1799,8 @@ fl_status fl_rope(const fl_tensor *q, const fl_tensor *k, const fl_tensor *q_out
     }
     const int64_t D = Q.size[3], heads = Q.size[2] + (k ? K.size[2] : 0);
     if ((s = check_rope(desc, D)) != FL_OK) return s;
-    if (Q.size[0] * Q.size[1] >= (int64_t(1) << 31) || heads * D >= (int64_t(1) << 24))
-        return fail(FL_ERR_UNSUPPORTED, "2^31 tokens or 2^24 elements of a token, or more");
+    if (Q.size[0] * Q.size[1] >= (int64_t(1) << 29) || heads * D >= (int64_t(1) << 24))
+        return fail(FL_ERR_UNSUPPORTED, "2^29 tokens or 2^24 elements of a token, or more");
     int dev;
     DeviceInfo info;
     if ((s = device_info(dev, info)) != FL_OK) return s;
@@ -1859,8 +1860,8 @@ fl_status fl_kv_append(const fl_tensor *q, const fl_tensor *k, const fl_tensor *
         if (rope->backward)
             return fail(FL_ERR_INVALID_ARG, "the append rotates forward only");
     }
-    if (((q ? Q.size[2] : 0) + 2 * Hk) * D >= (int64_t(1) << 24))
-        return fail(FL_ERR_UNSUPPORTED, "2^24 elements of a token, or more");
+    if (T >= (int64_t(1) << 29) || ((q ? Q.size[2] : 0) + 2 * Hk) * D >= (int64_t(1) << 24))
+        return fail(FL_ERR_UNSUPPORTED, "2^29 tokens or 2^24 elements of a token, or more");
     int dev;
     DeviceInfo info;
     if ((s = device_info(dev, info)) != FL_OK) return s;
@@ -1878,7 +1879,7 @@ fl_status fl_kv_append(const fl_tensor *q, const fl_tensor *k, const fl_tensor *
     set_rope(p, rope, D);
     p.tokens = int(T);
     p.div_seq = fl::make_fastdiv(int32_t(T));
-    p.div_tile_page = fl::make_fastdiv(int32_t(KC.size[1]));
+    p.page_rows = KC.size[1];
     p.slots = slots;
     p.n_slots = KC.size[0] * KC.size[1];
     if (q)

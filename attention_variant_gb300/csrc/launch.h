@@ -236,19 +236,21 @@ struct RopeStream {
     int64_t s_b, s_s, s_h;
     int64_t d_b, d_s, d_h;
     int heads;
+    FastDiv div_heads;
     int rotate;   // 0: copied
     int to_cache; // dst row by slot instead of by token
+    int tile;     // tokens per block (set by launch_rope)
 };
 
 struct RopeParams {
     RopeStream st[3];
-    int n_streams, heads;      // heads: of all streams
+    int n_streams;
     int tokens;                // B * S
-    int tile;                  // tokens per block
     int pairs, pass;           // rotated pairs and copied elements of a head
     int rot;
-    int units;                 // vector units of a head
-    FastDiv div_units, div_head_units, div_seq, div_tile_page;
+    int units, uy;             // vector units of a head; rows a block walks at a time
+    FastDiv div_ux, div_pairs, div_seq;
+    int64_t page_rows;
     const int32_t *positions;  // [B][positions_stride] or null
     int64_t positions_stride;
     int64_t offset;

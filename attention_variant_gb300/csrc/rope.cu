@@ -10,10 +10,14 @@
 // the remainder, in [-1/8, 1/8] turn, goes to sincospif.
 //
 // Bound by HBM: every element is read and written once.  A block takes `tile`
-// tokens, puts their sines and cosines in shared memory (one sincos for all
-// heads of a token) and streams all heads of all tensors through, a thread
-// moving the two vectors of up to 16 bytes that hold its pairs' halves.  The
-// vectors are loaded before the sines are ready, so both latencies overlap.
+// tokens of one tensor and puts their sines and cosines (one sincos for all
+// heads of a token) and row offsets in shared memory.  A thread keeps its
+// place within a head -- the two vectors of up to 16 bytes that hold its V
+// pairs -- and walks the (token, head) rows with it, so that a unit costs an
+// address, two loads, the rotation and two stores (about 90 instructions for
+// 8 bf16 pairs; with the place and the tensor worked out for every unit it
+// was 290, in 116 registers, and 45 us where this takes 26 for q and k of 8 x
+// 2048 tokens of 16 heads of 64).
 #include <cuda_bf16.h>
 #include <cstdint>
 
@@ -24,8 +28,9 @@ namespace fl {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnroll = 4;      // units in flight per thread
+constexpr int kRows = 8;         // (token, head) rows per thread, where there are enough
 constexpr int kMaxAngles = 1024; // tokens of a tile times pairs
+constexpr int kMaxTile = 64;
 
 template <class T, int V>
 struct alignas(sizeof(T) * V) Vec {
@@ -53,116 +58,108 @@ __device__ __forceinline__ float2 turn_cos_sin(uint64_t turn)
     }
 }
 
-// A unit: the two vectors that hold V rotated pairs (a, b), or one vector of
-// V elements that are copied (b unused).
-template <class T, int V>
-struct Unit {
-    Vec<T, V> a, b;
-    T *dst;      // of a; null: nothing to store
-    int b_at;    // b's distance from a; 0: a copied unit
-    int angle;   // first pair's place in the table of the tile; < 0: not rotated
-};
-
+// Rotates the V pairs of (a, b) by cs[0 .. V): pair e is (a, b)[e], or, where
+// INTER, neighbours of the 2 V elements a, b.
 template <class T, int V, bool INTER>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeParams p)
+__device__ __forceinline__ void rotate_pairs(Vec<T, V> &a, Vec<T, V> &b, const float2 *cs)
 {
-    __shared__ float2 s_cs[kMaxAngles];
-    const int tid = threadIdx.x;
-    const int t0 = blockIdx.x * p.tile;
-    const int n_tok = min(p.tile, p.tokens - t0);
-    const int total = n_tok * p.heads * p.units;
-    const int rot_units = p.pairs / V;
-
-    auto load = [&](int u, Unit<T, V> &w) {
-        w.dst = nullptr;
-        if (u >= total)
-            return;
-        const int tl = fast_div(u, p.div_head_units);
-        const int in_tok = u - tl * p.div_head_units.d;
-        int h = fast_div(in_tok, p.div_units);
-        const int un = in_tok - h * p.units;
-        int si = 0;
-        while (si + 1 < p.n_streams && h >= p.st[si].heads)
-            h -= p.st[si++].heads;
-        const RopeStream &st = p.st[si];
-        const int t = t0 + tl;
-        const int b = fast_div(t, p.div_seq), s = t - b * p.div_seq.d;
-        int64_t d_row;
-        if (st.to_cache) {
-            const int64_t slot = __ldg(p.slots + t);
-            if (slot < 0 || slot >= p.n_slots)
-                return;
-            const int64_t page = slot / p.div_tile_page.d;
-            d_row = page * st.d_b + (slot - page * p.div_tile_page.d) * st.d_s;
-        } else {
-            if (p.slots) {
-                const int64_t slot = __ldg(p.slots + t);
-                if (slot < 0 || slot >= p.n_slots)
-                    return;
-            }
-            d_row = b * st.d_b + s * st.d_s;
-        }
-        int at; // element of the head where a starts
-        w.angle = -1;
-        if (un < rot_units) {
-            at = INTER ? un * 2 * V : un * V;
-            w.b_at = INTER ? V : p.pairs;
-            if (st.rotate)
-                w.angle = tl * p.pairs + un * V;
-        } else {
-            at = p.rot + (un - rot_units) * V;
-            w.b_at = 0;
-        }
-        const T *src = static_cast<const T *>(st.src) + b * st.s_b + s * st.s_s + h * st.s_h + at;
-        w.a = *reinterpret_cast<const Vec<T, V> *>(src);
-        if (w.b_at)
-            w.b = *reinterpret_cast<const Vec<T, V> *>(src + w.b_at);
-        w.dst = static_cast<T *>(st.dst) + d_row + h * st.d_h + at;
-    };
-    auto store = [&](Unit<T, V> &w) {
-        if (!w.dst)
-            return;
-        if (w.angle >= 0) {
+    if constexpr (sizeof(T) == 2 && V >= 2) {
+        // bf16 two at a time: a word holds pairs e, e + 1 of one half, or both
+        // elements of a pair; widening is a shift or a mask, narrowing one cvt
+        uint32_t *wa = reinterpret_cast<uint32_t *>(&a), *wb = reinterpret_cast<uint32_t *>(&b);
+        auto lo = [](uint32_t w) { return __uint_as_float(w << 16); };
+        auto hi = [](uint32_t w) { return __uint_as_float(w & 0xffff0000u); };
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                const float2 cs = s_cs[w.angle + e];
-                T &ra = INTER ? (2 * e < V ? w.a.e[(2 * e) % V] : w.b.e[(2 * e) % V]) : w.a.e[e];
-                T &rb = INTER ? (2 * e + 1 < V ? w.a.e[(2 * e + 1) % V] : w.b.e[(2 * e + 1) % V]) : w.b.e[e];
-                const float xa = widen(ra), xb = widen(rb);
-                narrow(ra, xa * cs.x - xb * cs.y);
-                narrow(rb, xa * cs.y + xb * cs.x);
-            }
+        for (int e = 0; e < V; e += 2) {
+            const float4 f = *reinterpret_cast<const float4 *>(cs + e); // cos, sin of pairs e, e + 1
+            uint32_t &w0 = INTER ? (e < V / 2 ? wa[e % (V / 2)] : wb[e % (V / 2)]) : wa[e / 2];
+            uint32_t &w1 = INTER ? (e + 1 < V / 2 ? wa[(e + 1) % (V / 2)] : wb[(e + 1) % (V / 2)]) : wb[e / 2];
+            const float a0 = lo(w0), b0 = INTER ? hi(w0) : lo(w1);
+            const float a1 = INTER ? lo(w1) : hi(w0), b1 = hi(w1);
+            const float ya0 = a0 * f.x - b0 * f.y, yb0 = a0 * f.y + b0 * f.x;
+            const float ya1 = a1 * f.z - b1 * f.w, yb1 = a1 * f.w + b1 * f.z;
+            w0 = INTER ? ptx::pack_bf16(ya0, yb0) : ptx::pack_bf16(ya0, ya1);
+            w1 = INTER ? ptx::pack_bf16(ya1, yb1) : ptx::pack_bf16(yb0, yb1);
         }
-        *reinterpret_cast<Vec<T, V> *>(w.dst) = w.a;
-        if (w.b_at)
-            *reinterpret_cast<Vec<T, V> *>(w.dst + w.b_at) = w.b;
-    };
-
-    Unit<T, V> w[kUnroll];
+    } else {
 #pragma unroll
-    for (int k = 0; k < kUnroll; ++k)
-        load(tid + k * kThreads, w[k]);
-    for (int e = tid; e < n_tok * p.pairs; e += kThreads) {
-        const int tl = e / p.pairs, i = e - tl * p.pairs;
-        const int t = t0 + tl;
-        const int b = fast_div(t, p.div_seq), s = t - b * p.div_seq.d;
-        const int64_t pos = p.offset + (p.positions ? __ldg(p.positions + b * p.positions_stride + s) : s);
-        float2 cs = turn_cos_sin(static_cast<uint64_t>(pos) * p.turns[i]);
-        cs.x *= p.magnitude;
-        cs.y *= p.backward ? -p.magnitude : p.magnitude;
-        s_cs[e] = cs;
+        for (int e = 0; e < V; ++e) {
+            T &ra = INTER ? (2 * e < V ? a.e[(2 * e) % V] : b.e[(2 * e) % V]) : a.e[e];
+            T &rb = INTER ? (2 * e + 1 < V ? a.e[(2 * e + 1) % V] : b.e[(2 * e + 1) % V]) : b.e[e];
+            const float2 f = cs[e];
+            const float xa = widen(ra), xb = widen(rb);
+            narrow(ra, xa * f.x - xb * f.y);
+            narrow(rb, xa * f.y + xb * f.x);
+        }
     }
+}
+
+// Occupancy carries the latency (one row in flight a thread, 8 blocks a
+// SM): two rows in flight and 4 blocks took 31.8 us, four and 3 42.7.
+template <class T, int V, bool INTER>
+__global__ void __launch_bounds__(kThreads, 8) rope_kernel(const __grid_constant__ RopeParams p)
+{
+    __shared__ __align__(16) float2 s_cs[kMaxAngles];
+    __shared__ int64_t s_src[kMaxTile], s_dst[kMaxTile]; // rows of the tile's tokens; s_dst < 0: skipped
+    const RopeStream &st = p.st[blockIdx.y];
+    const int tid = threadIdx.x, t0 = blockIdx.x * st.tile, n_tok = min(st.tile, p.tokens - t0);
+    if (n_tok <= 0)
+        return; // the grid is as wide as the tensor with the smallest tiles needs
+
+    if (tid < n_tok) {
+        const int t = t0 + tid, b = fast_div(t, p.div_seq), s = t - b * p.div_seq.d;
+        int64_t dst = b * st.d_b + s * st.d_s;
+        if (p.slots) {
+            const int64_t slot = __ldg(p.slots + t);
+            if (slot < 0 || slot >= p.n_slots) {
+                dst = -1;
+            } else if (st.to_cache) {
+                const int64_t page = slot / p.page_rows;
+                dst = page * st.d_b + (slot - page * p.page_rows) * st.d_s;
+            }
+        }
+        s_src[tid] = b * st.s_b + s * st.s_s;
+        s_dst[tid] = dst;
+    }
+    if (st.rotate)
+        for (int e = tid; e < n_tok * p.pairs; e += kThreads) {
+            const int tl = fast_div(e, p.div_pairs), i = e - tl * p.pairs;
+            const int t = t0 + tl, b = fast_div(t, p.div_seq), s = t - b * p.div_seq.d;
+            const int64_t pos = p.offset + (p.positions ? __ldg(p.positions + b * p.positions_stride + s) : s);
+            float2 cs = turn_cos_sin(static_cast<uint64_t>(pos) * p.turns[i]);
+            cs.x *= p.magnitude;
+            cs.y *= p.backward ? -p.magnitude : p.magnitude;
+            s_cs[e] = cs;
+        }
     __syncthreads();
-    for (int u = tid;;) {
-#pragma unroll
-        for (int k = 0; k < kUnroll; ++k)
-            store(w[k]);
-        u += kUnroll * kThreads;
-        if (u >= total)
-            break;
-#pragma unroll
-        for (int k = 0; k < kUnroll; ++k)
-            load(u + k * kThreads, w[k]);
+
+    // unit ux of a head: the vectors a (at element `at`) and b (b_at further) of
+    // V rotated pairs, or one vector of the copied rest (b_at 0)
+    const int y = fast_div(tid, p.div_ux), x = tid - y * p.div_ux.d;
+    if (y >= p.uy)
+        return;
+    const int rot_units = p.pairs / V, rows = n_tok * st.heads;
+    for (int ux = x; ux < p.units; ux += p.div_ux.d) {
+        const bool pair = ux < rot_units;
+        const int at = !pair ? p.rot + (ux - rot_units) * V : INTER ? ux * 2 * V : ux * V;
+        const int b_at = INTER ? V : p.pairs;
+        const T *src = static_cast<const T *>(st.src) + at;
+        T *dst = static_cast<T *>(st.dst) + at;
+        for (int r = y; r < rows; r += p.uy) {
+            const int tok = fast_div(r, st.div_heads), h = r - tok * st.heads;
+            if (s_dst[tok] < 0)
+                continue;
+            const T *from = src + s_src[tok] + h * st.s_h;
+            T *to = dst + s_dst[tok] + h * st.d_h;
+            Vec<T, V> a = *reinterpret_cast<const Vec<T, V> *>(from), b;
+            if (pair) {
+                b = *reinterpret_cast<const Vec<T, V> *>(from + b_at);
+                if (st.rotate)
+                    rotate_pairs<T, V, INTER>(a, b, s_cs + tok * p.pairs + ux * V);
+                *reinterpret_cast<Vec<T, V> *>(to + b_at) = b;
+            }
+            *reinterpret_cast<Vec<T, V> *>(to) = a;
+        }
     }
 }
 
@@ -170,19 +167,25 @@ template <class T, int V>
 cudaError_t launch_vec(RopeParams &p, bool interleaved, int sm_count, cudaStream_t stream)
 {
     p.units = p.pairs / V + p.pass / V;
-    const int64_t head_units = int64_t(p.heads) * p.units;
-    if (head_units == 0 || p.tokens == 0)
+    if (p.units == 0 || p.tokens == 0)
         return cudaSuccess;
-    // tokens per block: as many as fill a block's first kUnroll rounds and its
-    // table, as long as two blocks a SM remain
-    int tile = 1;
-    while (tile < 64 && 2 * tile * head_units <= kThreads * kUnroll && 2 * tile * p.pairs <= kMaxAngles &&
-           p.tokens / (2 * tile) >= 2 * sm_count)
-        tile *= 2;
-    p.tile = tile;
-    p.div_units = make_fastdiv(p.units);
-    p.div_head_units = make_fastdiv(static_cast<int32_t>(head_units));
-    const int grid = (p.tokens + tile - 1) / tile;
+    const int ux = p.units < kThreads ? p.units : kThreads;
+    p.div_ux = make_fastdiv(ux);
+    p.uy = kThreads / ux;
+    // tokens per block: as many as give each thread its kRows rows, as long as
+    // the tensor still fills the GPU's block slots about twice
+    int blocks = 0;
+    for (int i = 0; i < p.n_streams; ++i) {
+        RopeStream &st = p.st[i];
+        int tile = 1;
+        while (tile < kMaxTile && 2 * int64_t(tile) * st.heads <= kRows * p.uy && 2 * tile * p.pairs <= kMaxAngles &&
+               p.tokens / (2 * tile) >= 4 * sm_count)
+            tile *= 2;
+        st.tile = tile;
+        const int n = (p.tokens + tile - 1) / tile;
+        blocks = n > blocks ? n : blocks;
+    }
+    const dim3 grid(blocks, p.n_streams);
     if (interleaved)
         rope_kernel<T, V, true><<<grid, kThreads, 0, stream>>>(p);
     else
