@@ -2009,6 +2009,8 @@ fl_status fl_attn_chunk(const fl_tensor *q, const fl_tensor *k_cache, const fl_t
     int dev;
     DeviceInfo info;
     if ((s = device_info(dev, info)) != FL_OK) return s;
+    if (info.sm_count < 4)
+        return fail(FL_ERR_UNSUPPORTED, "%d SMs: chunks need 4", info.sm_count);
     const int64_t G = pl.Hq / pl.Hk;
     const int few_tq = G <= fl::kFewRows ? int(fl::kFewRows / G) : 1;
     const int few_box = desc->block_table && pl.page < fl::kFewTile ? int(pl.page) : fl::kFewTile;
@@ -2072,6 +2074,7 @@ fl_status fl_attn_chunk(const fl_tensor *q, const fl_tensor *k_cache, const fl_t
         p.lse = static_cast<float *>(L.ptr);
         p.l_sh = L.stride[0];
     }
+    p.device = dev;
     p.n_cta = info.sm_count < fl::kChunkMaxCtas ? info.sm_count : fl::kChunkMaxCtas;
     // costs for the even split, in tenths of a microsecond as measured: a key
     // tile of two row blocks (1.0 us, with softcap 2.5 at D = 64), of one, a

@@ -9,7 +9,9 @@
 // 124 of 128 idle for a token of a group of four heads; measured at 64
 // requests of 512 to 8192 keys: 131 us).  P^T goes to shared memory as the B
 // operand of O^T = V^T P^T, which accumulates a dimension per lane and a row
-// per column.
+// per column.  P goes as two bf16 terms, P rounded and what the rounding left
+// (columns of their own, added at the end): with the products this small the
+// second term costs nothing, and O keeps the accuracy of an fp32 P.
 //
 // What matters is bytes in flight: K and V have rings of their own (192 KB in
 // all; a K stage is free as soon as S is computed), and the two slots (a
@@ -57,7 +59,7 @@ struct FewCfg {
     static constexpr uint32_t kQBytes = kHalves * kQHalf;
     static constexpr uint32_t kHalf = kBN * kRowBytes;      // half a K or V tile
     static constexpr uint32_t kTileBytes = kHalves * kHalf;
-    static constexpr uint32_t kPRow = 64;                   // bytes of a key's row of P (32 rows, 16 used)
+    static constexpr uint32_t kPRow = 64;                   // bytes of a key's row of P: two terms of 8 or 16 rows
     static constexpr uint32_t kColS = 0, kColO = 64, kStride = 32; // TMEM columns of slot t: + 32 t
 };
 
@@ -106,7 +108,7 @@ struct __align__(1024) FewSmem {
     uint64_t final_bar[3];
     uint64_t info_full[kInfo], info_empty[kInfo];
     FewItem info[kInfo];
-    float red[2][4][2 * kFewRows];   // maxima or sums of each softmax warp
+    float red[2][4][kFewRows];       // maxima or sums of each softmax warp
     uint32_t rows[2][2][4];          // by tile parity, of each softmax warp: see few_softmax
     uint32_t tmem_base;
     uint32_t abort_flag;
@@ -424,7 +426,8 @@ __device__ void few_pv_role(const FewCtx<D> &cx, int slot_lo, int slot_hi)
     // O^T = V^T P^T: both operands with their long index contiguous.  V^T has
     // 128 rows: at D = 64 the second 64 repeat the first (block stride 0).  P
     // has 64-byte rows of a key, 64-byte swizzle.
-    constexpr uint32_t idesc = umma_idesc_bf16(128, kFewRows, true) | (1u << 15);
+    constexpr uint32_t idesc8 = umma_idesc_bf16(128, 16, true) | (1u << 15);
+    constexpr uint32_t idesc16 = umma_idesc_bf16(128, 32, true) | (1u << 15);
     constexpr uint64_t kHiV = umma_desc_hi(D == 128 ? C::kHalf : 0, C::kGroupBytes, kSwizzle128B);
     constexpr uint64_t kHiP = umma_desc_hi(16, 8 * C::kPRow, kSwizzle64B);
     const uint32_t v_lo0 = ptx::smem_u32(sm.v[0]) >> 4, p_lo0 = ptx::smem_u32(sm.p[0]) >> 4;
@@ -439,6 +442,7 @@ __device__ void few_pv_role(const FewCtx<D> &cx, int slot_lo, int slot_hi)
         const int stop = inf.stop, shift = inf.shift, u_lo = inf.u_lo, u_hi = inf.u_hi;
         const int lo = inf.lo << shift, hi = inf.hi << shift, L = inf.L, key_lo = inf.key_lo;
         const int first = max(u_lo, lo);
+        const uint32_t idesc = inf.rows <= 8 ? idesc8 : idesc16; // two terms a row
         __syncwarp();
         if (lane == 0)
             ptx::mbar_arrive(bar(sm.info_empty[slot]));
@@ -507,11 +511,9 @@ __device__ __forceinline__ int ordered(float x)
 }
 __device__ __forceinline__ float unordered(int i) { return __int_as_float(i ^ ((i >> 31) & 0x7fffffff)); }
 
-// This thread's weights, 2^(c x - m) (an unset reference counts as 0), and
-// rounded to bf16 in pairs.
+// This thread's weights, 2^(c x - m) (an unset reference counts as 0).
 template <int R>
-__device__ __forceinline__ void few_exp(const float (&x)[R], float c, const float (&m)[R], bool zero, float (&w)[R],
-                                        uint32_t (&pk)[R / 2])
+__device__ __forceinline__ void few_exp(const float (&x)[R], float c, const float (&m)[R], bool zero, float (&w)[R])
 {
     if (zero) { // every reference is 0
 #pragma unroll
@@ -522,9 +524,18 @@ __device__ __forceinline__ void few_exp(const float (&x)[R], float c, const floa
         for (int n = 0; n < R; ++n)
             w[n] = ptx::ex2(fmaf(x[n], c, m[n] == kNegInf ? 0.f : -m[n]));
     }
-#pragma unroll
-    for (int n = 0; n < R; n += 2)
-        pk[n / 2] = ptx::pack_bf16(w[n], w[n + 1]);
+}
+
+// O^T's columns of a slot: the rows' sums of rounded weights, then those of the rests.
+template <int R>
+__device__ __forceinline__ void few_load_o(uint32_t tO, uint32_t (&o)[2 * R])
+{
+    if constexpr (R == 8)
+        ptx::tmem_ld16(tO, o);
+    else
+        ptx::tmem_ld32(tO, o);
+    ptx::tmem_wait_ld();
+    ptx::reg_fence<2 * R>(o);
 }
 
 // What a softmax thread carries from item to item.
@@ -569,11 +580,11 @@ __device__ __forceinline__ bool few_item(const FewCtx<D> &cx, const ChunkParams 
         key_range(p, inf.L, last, last, full_lo, unused);
         key_range(p, inf.L, pos0, pos0, unused, full_hi);
     }
-    float m[R], l[R], lr[R];
+    float m[R], l[R];
 #pragma unroll
     for (int n = 0; n < R; ++n) {
         m[n] = kNegInf;
-        l[n] = lr[n] = 0.f;
+        l[n] = 0.f;
     }
     uint32_t set = 0;  // rows that have a reference
     bool moved = false; // some reference is not 0
@@ -634,8 +645,7 @@ __device__ __forceinline__ bool few_item(const FewCtx<D> &cx, const ChunkParams 
         if (lane == 0)
             sm.rows[t][ct.tiles & 1][wq] = bits;
         float w[R];
-        uint32_t pk[R / 2];
-        few_exp(x, c, m, !moved, w, pk);
+        few_exp(x, c, m, !moved, w);
         if (!group_sync())
             return false;
         {
@@ -668,7 +678,7 @@ __device__ __forceinline__ bool few_item(const FewCtx<D> &cx, const ChunkParams 
                 float m_new = !(set >> n & 1u) && (bits >> n & 1u) ? 0.f : m[n];
                 if (ask >> n & 1u) {
                     const volatile float *red = &sm.red[t][0][n];
-                    m_new = fmaxf(fmaxf(fmaxf(red[0], red[2 * kFewRows]), fmaxf(red[4 * kFewRows], red[6 * kFewRows])),
+                    m_new = fmaxf(fmaxf(fmaxf(red[0], red[kFewRows]), fmaxf(red[2 * kFewRows], red[3 * kFewRows])),
                                   m[n]);
                     moved = true;
                 }
@@ -678,40 +688,42 @@ __device__ __forceinline__ bool few_item(const FewCtx<D> &cx, const ChunkParams 
             set |= (bits | bits >> 16) & row_bits;
             if (ask) {
                 if (kk > 0) {
-                    uint32_t o[R];
-                    if constexpr (R == 8)
-                        ptx::tmem_ld8(tO, o);
-                    else
-                        ptx::tmem_ld16(tO, o);
-                    ptx::tmem_wait_ld();
-                    ptx::reg_fence<R>(o);
+                    uint32_t o[2 * R];
+                    few_load_o<R>(tO, o);
 #pragma unroll
                     for (int n = 0; n < R; ++n) { // a row without a key so far holds zeros
                         o[n] = __float_as_uint(__uint_as_float(o[n]) * alpha[n]);
+                        o[R + n] = __float_as_uint(__uint_as_float(o[R + n]) * alpha[n]);
                         l[n] *= alpha[n];
-                        lr[n] *= alpha[n];
                     }
                     if constexpr (R == 8)
-                        ptx::tmem_st8(tO, o);
-                    else
                         ptx::tmem_st16(tO, o);
+                    else
+                        ptx::tmem_st32(tO, o);
                     ptx::tmem_wait_st();
                 }
-                few_exp(x, c, m, false, w, pk);
+                few_exp(x, c, m, false, w);
             }
         }
-        // rows from R on (R = 8) are left as they are: columns of their own
-        pdst[0 ^ sw] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-        if constexpr (R == 16)
-            pdst[1 ^ sw] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+        // the key's row of P: R rounded weights, then R rests
+        uint32_t hi[R / 2], lo[R / 2];
+#pragma unroll
+        for (int n = 0; n < R; n += 2) {
+            hi[n / 2] = ptx::pack_bf16(w[n], w[n + 1]);
+            lo[n / 2] = ptx::pack_bf16(w[n] - __uint_as_float(hi[n / 2] << 16),
+                                       w[n + 1] - __uint_as_float(hi[n / 2] & 0xffff0000u));
+        }
+#pragma unroll
+        for (int u = 0; u < R / 8; ++u) {
+            pdst[u ^ sw] = make_uint4(hi[4 * u], hi[4 * u + 1], hi[4 * u + 2], hi[4 * u + 3]);
+            pdst[(R / 8 + u) ^ sw] = make_uint4(lo[4 * u], lo[4 * u + 1], lo[4 * u + 2], lo[4 * u + 3]);
+        }
         ptx::fence_proxy_async_smem();
         ptx::tc_fence_before();
         ptx::mbar_arrive(bar(sm.p_full[t]));
 #pragma unroll
-        for (int n = 0; n < R; n += 2) { // the exact sum (LSE) and that of the rounded P (O)
+        for (int n = 0; n < R; n += 2)
             ptx::add2(l[n], l[n + 1], w[n], w[n + 1]);
-            ptx::add_bf16x2_to_f32(lr[n], lr[n + 1], pk[n / 2]);
-        }
     }
     if (n_mine) {
         if (!warp_wait(bar(sm.pv_done[t]), ct.pv & 1, cx.wc, W_O_FULL))
@@ -719,34 +731,29 @@ __device__ __forceinline__ bool few_item(const FewCtx<D> &cx, const ChunkParams 
         ++ct.pv;
         ptx::tc_fence_after();
     }
-    // ---- the slot's sums over the warp: values l, then the rounded sums, halved
-    // at each exchange until lane i holds value i (mod 2 R)
-    float v[2 * R];
+    // ---- the slot's sums over the warp, halved at each exchange until lane i
+    // holds row i mod R
 #pragma unroll
-    for (int n = 0; n < R; ++n) {
-        v[n] = l[n];
-        v[R + n] = lr[n];
-    }
-#pragma unroll
-    for (int h = R; h; h >>= 1) {
+    for (int h = R / 2; h; h >>= 1) {
         const bool up = lane & h;
 #pragma unroll
         for (int i = 0; i < h; ++i)
-            v[i] = (up ? v[i + h] : v[i]) + __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i + h], h);
+            l[i] = (up ? l[i + h] : l[i]) + __shfl_xor_sync(0xffffffffu, up ? l[i] : l[i + h], h);
     }
-    if constexpr (R == 8)
-        v[0] += __shfl_xor_sync(0xffffffffu, v[0], 16);
-    // its place among the sums of 16 rows
-    const int place = R == 8 ? (lane & 7) + 2 * (lane & 8) : lane;
-    const bool store = R == 16 || lane < 16;
-    uint32_t raw[R];
+#pragma unroll
+    for (int d = R; d < 32; d *= 2)
+        l[0] += __shfl_xor_sync(0xffffffffu, l[0], d);
+    float o[R];
     if (n_mine) {
-        if constexpr (R == 8)
-            ptx::tmem_ld8(tO, raw);
-        else
-            ptx::tmem_ld16(tO, raw);
-        ptx::tmem_wait_ld();
-        ptx::reg_fence<R>(raw);
+        uint32_t raw[2 * R];
+        few_load_o<R>(tO, raw);
+#pragma unroll
+        for (int n = 0; n < R; ++n)
+            o[n] = __uint_as_float(raw[n]) + __uint_as_float(raw[R + n]);
+    } else {
+#pragma unroll
+        for (int n = 0; n < R; ++n)
+            o[n] = 0.f;
     }
     // lane = dimension; at D = 64 the upper 64 lanes repeat the lower ones and
     // take the odd rows
@@ -756,18 +763,18 @@ __device__ __forceinline__ bool few_item(const FewCtx<D> &cx, const ChunkParams 
 #pragma unroll
         for (int n = 0; n < R; ++n) {
             if (n < rows && (D == 128 || (n & 1) == r >> 6))
-                mine[n * 128 + dim] = n_mine ? __uint_as_float(raw[n]) : 0.f;
+                mine[n * 128 + dim] = o[n];
             if (r == n)
                 sums[n] = m[n];
         }
-        if (store)
-            sums[kFewRows + wq * 2 * kFewRows + place] = v[0];
+        if (lane < R)
+            sums[kFewRows + wq * kFewRows + lane] = l[0];
         return true;
     }
     if (!n_mine && !group_sync()) // the last item's sums have been read
         return false;
-    if (store)
-        sm.red[t][wq][place] = v[0];
+    if (lane < R)
+        sm.red[t][wq][lane] = l[0];
     if (!group_sync())
         return false;
     const volatile float *red = sm.red[t][0];
@@ -775,14 +782,12 @@ __device__ __forceinline__ bool few_item(const FewCtx<D> &cx, const ChunkParams 
     for (int n = 0; n < R; ++n) {
         if (n >= rows || (D == 64 && (n & 1) != r >> 6))
             continue;
-        constexpr int W = 2 * kFewRows;
-        const float sl = red[n] + red[n + W] + red[n + 2 * W] + red[n + 3 * W];
-        const float slr = red[n + kFewRows] + red[n + kFewRows + W] + red[n + kFewRows + 2 * W] + red[n + kFewRows + 3 * W];
+        const float sum = red[n] + red[n + kFewRows] + red[n + 2 * kFewRows] + red[n + 3 * kFewRows];
         const int s = fast_div(n, p.div_g);
         const int64_t tok = inf.t0 + s, head = (inf.kvh + t) * p.G + n - s * p.G;
-        join_write(p, tok, head, dim, n_mine ? __uint_as_float(raw[n]) : 0.f, slr);
+        join_write(p, tok, head, dim, o[n], sum);
         if (dim == 0)
-            join_lse(p, tok, head, m[n], sl);
+            join_lse(p, tok, head, m[n], sum);
     }
     return true;
 }

@@ -109,8 +109,8 @@ __device__ __forceinline__ PartRange part_range(int64_t x0, int n_tiles, int til
 //   JOIN_PAIR   the slot's own rows: [D columns][128 rows]
 //   JOIN_HALF   one row block, the slot's half of the columns: [D / 2][128]
 //               then, for both, m, l and the sum of the rounded P: [3][128]
-//   JOIN_FEW    [16 rows][128 dimensions], m [16], then a warp's sums of l and
-//               of the rounded P: [4 warps][2][16]
+//   JOIN_FEW    [16 rows][128 dimensions], m [16], then each warp's sums of l:
+//               [4 warps][16]
 enum : int { JOIN_PAIR = 0, JOIN_HALF = 1, JOIN_FEW = 2 };
 
 // Floats of one slot's buffer, and the place of a slot's buffer of a CTA
@@ -124,6 +124,7 @@ __device__ __forceinline__ float *partial(const ChunkParams &p, int cta, int buf
 // ------------------------------------------------------------------ planning
 
 constexpr int kPlanThreads = 1024;
+constexpr int kPlanNear = 128; // entries of each list kept at hand
 
 // What one scan of the planning kernel adds up: places on the two lists
 // (16 bits each; at most kPlanThreads a round) and costs.
@@ -155,6 +156,12 @@ __device__ __forceinline__ T block_scan(T x, T *s_warp)
             x = x + y;
     }
     __syncthreads(); // the last scan's sums have been read
+    if (warps == 1) {
+        if (lane == 31)
+            s_warp[31] = x;
+        __syncthreads();
+        return x;
+    }
     if (lane == 31)
         s_warp[warp] = x;
     __syncthreads();
@@ -182,6 +189,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
     __shared__ int s_ent[kPlanThreads + 1]; // first entry of each request of the round
     __shared__ int s_t0[kPlanThreads], s_n[kPlanThreads], s_len[kPlanThreads];
     __shared__ int64_t s_cum[2][kPlanThreads]; // cost before each of the first entries
+    __shared__ ChunkEntry s_entry[2][kPlanNear]; // and the very first ones
     __shared__ int s_most;                     // cost of the dearest tile of a row block
     ptx::launch_dependents();
     const int tid = threadIdx.x, threads = blockDim.x;
@@ -259,6 +267,8 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
                     p.entries[kind * p.max_entries + at] = en;
                     if (at < kPlanThreads)
                         s_cum[kind][at] = en.cum;
+                    if (at < kPlanNear)
+                        s_entry[kind][at] = en;
                 }
             }
             count[0] += s_sum[31].places & 0xffff;
@@ -315,7 +325,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
                 else
                     hi = mid - 1;
             }
-            const ChunkEntry en = p.entries[kind * p.max_entries + lo];
+            const ChunkEntry en = lo < kPlanNear ? s_entry[kind][lo] : p.entries[kind * p.max_entries + lo];
             out.at = en;
             const int64_t cost = item_cost(p, en);
             out.total = total;
@@ -343,10 +353,9 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
 
 constexpr int kJoinThreads = 128, kJoinSplit = 4;
 
-__device__ __forceinline__ void join_write(const ChunkParams &p, int64_t tok, int64_t head, int dim, float o,
-                                           float l_round)
+__device__ __forceinline__ void join_write(const ChunkParams &p, int64_t tok, int64_t head, int dim, float o, float l)
 {
-    p.out[tok * p.o_st + head * p.o_sh + dim] = __float2bfloat16(l_round == 0.f ? 0.f : o * ptx::rcp_approx(l_round));
+    p.out[tok * p.o_st + head * p.o_sh + dim] = __float2bfloat16(l == 0.f ? 0.f : o * ptx::rcp_approx(l));
 }
 
 __device__ __forceinline__ void join_lse(const ChunkParams &p, int64_t tok, int64_t head, float m, float l)
@@ -415,27 +424,21 @@ __device__ __forceinline__ void join_few(const ChunkParams &p, const ChunkJoin &
         for (int d = 16; d; d >>= 1)
             M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
         const float M0 = M == kNegInf ? 0.f : M;
-        float l = 0.f, lr = 0.f, o = 0.f;
+        float l = 0.f, o = 0.f;
         for (int q0 = 0; q0 < n_parts; q0 += 32) {
-            float w = 0.f, a = 0.f, b = 0.f;
+            float w = 0.f, a = 0.f;
             if (q0 + lane < n_parts) {
                 const float *s = part(q0 + lane) + R * 128 + n;
                 w = ptx::ex2(__ldg(s) - M0);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    a += __ldg(s + R + 2 * R * k);
-                    b += __ldg(s + 2 * R + 2 * R * k);
-                }
+                for (int k = 1; k <= 4; ++k)
+                    a += __ldg(s + R * k);
                 a *= w;
-                b *= w;
             }
 #pragma unroll
-            for (int d = 16; d; d >>= 1) {
+            for (int d = 16; d; d >>= 1)
                 a += __shfl_xor_sync(0xffffffffu, a, d);
-                b += __shfl_xor_sync(0xffffffffu, b, d);
-            }
             l += a;
-            lr += b;
             for (int q = q0; q < min(q0 + 32, n_parts); q += kDepth) {
                 float v[kDepth];
 #pragma unroll
@@ -448,7 +451,7 @@ __device__ __forceinline__ void join_few(const ChunkParams &p, const ChunkJoin &
         }
         const int s = fast_div(n, p.div_g);
         const int64_t tok = jn.t0[slot] + s, head = (jn.kvh + slot) * p.G + n - s * p.G;
-        join_write(p, tok, head, dim, o, lr);
+        join_write(p, tok, head, dim, o, l);
         if (dim == 0)
             join_lse(p, tok, head, M, l);
     }

@@ -874,8 +874,8 @@ cudaError_t launch_mod(const ChunkMaps &maps, const ChunkParams &p, cudaStream_t
     constexpr size_t smem =
         (sizeof(ChunkSmem<D>) > sizeof(FewSmem<D>) ? sizeof(ChunkSmem<D>) : sizeof(FewSmem<D>)) + 1024;
     static_assert(smem <= 232448, "shared memory per CTA");
-    static bool configured = false; // benign race: both calls are idempotent
-    if (!configured) {
+    static bool configured[64] = {}; // by device; benign race: the calls are idempotent
+    if (!configured[p.device]) {
         cudaFuncAttributes attr;
         cudaError_t e = cudaFuncGetAttributes(&attr, chunk_kernel<MOD, D>);
         if (e != cudaSuccess)
@@ -887,11 +887,11 @@ cudaError_t launch_mod(const ChunkMaps &maps, const ChunkParams &p, cudaStream_t
                                  static_cast<int>(smem));
         if (e != cudaSuccess)
             return e;
-        configured = true;
+        configured[p.device] = true;
     }
     // one round of the planning kernel for the requests and their entries, as
     // long as its block allows
-    int threads = 128;
+    int threads = 32;
     while (threads < kPlanThreads && (threads < p.batch || threads < p.max_entries))
         threads *= 2;
     chunk_plan_kernel<D><<<1, threads, 0, stream>>>(p);

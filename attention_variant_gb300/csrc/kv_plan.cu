@@ -93,11 +93,12 @@ __global__ void __launch_bounds__(kThreads) kv_plan_kernel(const KvPlanParams p)
                 else
                     hi = mid - 1;
             }
-            const int pos = s_kv[lo] + (t - s_cu[lo]);
-            const int page = pos >> p.page_shift;
-            const int had = (s_kv[lo] + page_mask) >> p.page_shift;
+            // (unsigned: lengths that overflow 31 bits find no page)
+            const uint32_t pos = static_cast<uint32_t>(s_kv[lo]) + static_cast<uint32_t>(t - s_cu[lo]);
+            const int page = static_cast<int>(pos >> p.page_shift);
+            const int had = static_cast<int>((static_cast<uint32_t>(s_kv[lo]) + page_mask) >> p.page_shift);
             int id = -1;
-            if (page < p.bt_stride) {
+            if (page < p.bt_stride && b0 + lo < p.batch) {
                 int32_t *entry = p.block_table + static_cast<int64_t>(b0 + lo) * p.bt_stride + page;
                 if (page < had) {
                     id = *entry;
@@ -111,7 +112,7 @@ __global__ void __launch_bounds__(kThreads) kv_plan_kernel(const KvPlanParams p)
             }
             if (id < 0)
                 err |= FL_DEVERR_PAGES;
-            p.positions[t] = pos;
+            p.positions[t] = static_cast<int>(pos);
             if (p.slots)
                 p.slots[t] = id < 0 ? -1 : (static_cast<int64_t>(id) << p.page_shift) + (pos & page_mask);
         }

@@ -324,7 +324,7 @@ struct ChunkParams {
     int64_t o_st, o_sh;
     float *lse;                // [Hq, T] or null
     int64_t l_sh;
-    int n_cta;
+    int device, n_cta;
     int cost_pair, cost_single, cost_few, cost_item, cost_few_item, cost_least; // see api.cu
     int max_entries;
     ChunkPart *parts;          // the workspace: [n_cta]

@@ -100,6 +100,22 @@ def test_plan_more_tokens_than_stated():
     assert got & fa.FL_DEVERR_LENGTHS and got == want
 
 
+def test_plan_nonsense_lengths_stay_inside():
+    # lengths that overflow 32 bits: numbers without meaning, but nothing is
+    # read or written outside the arrays (guard rows around the table stay)
+    big = (1 << 31) - 1
+    for q, kv in (([big, 5], [0, 3]), ([7, 2], [big, big - 3]), ([big, big, big, 9], [0, 0, 0, 0])):
+        B = len(q)
+        table = _ints([[-9] * 4] * (B + 2))
+        t = [_ints(q), _ints(kv), _ints([5, 6, 7]), _ints([0]), table[1:-1]]
+        out = [_ints([0] * B), _ints([0] * (B + 1)), _ints([0] * 3000), _ints([0] * 3000, torch.int64), _ints([0])]
+        fa.fl_kv_plan(fa.make_kv_plan_desc(*t, *out, page_size=16))
+        torch.cuda.synchronize()
+        assert table[0].tolist() == [-9] * 4 == table[-1].tolist()
+        slots = out[3]
+        assert bool((slots < 8 * 16).all()) and bool((slots >= -1).all())
+
+
 # ------------------------------------------------------------------ append
 
 
