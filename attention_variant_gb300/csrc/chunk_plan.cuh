@@ -49,7 +49,7 @@ __device__ __forceinline__ void key_range(const ChunkParams &p, int L, int first
 __device__ __forceinline__ bool is_few(const ChunkParams &p, int n_tok) { return n_tok * p.G <= kFewRows; }
 
 // a / b for a >= 0, b > 0: costs are 64-bit, but their division is only where it has to be.
-__device__ __forceinline__ int64_t div64(int64_t a, int64_t b)
+__device__ __noinline__ int64_t div64(int64_t a, int64_t b)
 {
     if (((a | b) >> 32) == 0)
         return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
@@ -143,28 +143,37 @@ __device__ __forceinline__ PlanSum shfl_up(const PlanSum &x, int d)
                    {__shfl_up_sync(0xffffffffu, x.cost[0], d), __shfl_up_sync(0xffffffffu, x.cost[1], d)}};
 }
 
-// Inclusive sum over the block (a power of two of warps, at most 32); the
-// total is left in s_warp[31].
-template <class T>
-__device__ __forceinline__ T block_scan(T x, T *s_warp)
+// Barrier of the planning kernel's first `threads` threads.
+__device__ __forceinline__ void plan_sync(int threads)
 {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    if (threads == 32)
+        __syncwarp();
+    else
+        ptx::named_barrier_sync(1, threads);
+}
+
+// Inclusive sum over the first `threads` threads (a power of two of warps, at
+// most 32); the total is left in s_warp[31].
+template <class T>
+__device__ __forceinline__ T block_scan(T x, T *s_warp, int threads)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = threads >> 5;
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) {
         const T y = shfl_up(x, d);
         if (lane >= d)
             x = x + y;
     }
-    __syncthreads(); // the last scan's sums have been read
+    plan_sync(threads); // the last scan's sums have been read
     if (warps == 1) {
         if (lane == 31)
             s_warp[31] = x;
-        __syncthreads();
+        plan_sync(threads);
         return x;
     }
     if (lane == 31)
         s_warp[warp] = x;
-    __syncthreads();
+    plan_sync(threads);
     if (warp == 0) {
         T w = lane < warps ? s_warp[lane] : T{};
 #pragma unroll
@@ -175,32 +184,34 @@ __device__ __forceinline__ T block_scan(T x, T *s_warp)
         }
         s_warp[lane] = w;
     }
-    __syncthreads();
+    plan_sync(threads);
     return warp ? s_warp[warp - 1] + x : x;
 }
 
-// One block of up to kPlanThreads threads (fewer for small batches: the
-// barriers cost what they have to wait for).
+// What the planning kernel's threads share.
+struct PlanShared {
+    int scan[32];
+    PlanSum sum[32];
+    int ent[kPlanThreads + 1];                            // first entry of each request of the round
+    int t0[kPlanThreads], n[kPlanThreads], len[kPlanThreads];
+    int64_t cum[2][kPlanThreads];                         // cost before each of the first entries
+    ChunkEntry entry[2][kPlanNear];                       // and the very first ones
+    int most;                                             // cost of the dearest tile of a row block
+    int count[2];                                         // entries and cost of the lists
+    int64_t total[2];
+};
+
+// The lists of entries, by `threads` threads.
 template <int D>
-__global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_constant__ ChunkParams p)
+__device__ __forceinline__ void plan_entries(const ChunkParams &p, PlanShared &sm, int threads)
 {
-    __shared__ int s_scan[32];
-    __shared__ PlanSum s_sum[32];
-    __shared__ int s_ent[kPlanThreads + 1]; // first entry of each request of the round
-    __shared__ int s_t0[kPlanThreads], s_n[kPlanThreads], s_len[kPlanThreads];
-    __shared__ int64_t s_cum[2][kPlanThreads]; // cost before each of the first entries
-    __shared__ ChunkEntry s_entry[2][kPlanNear]; // and the very first ones
-    __shared__ int s_most;                     // cost of the dearest tile of a row block
-    ptx::launch_dependents();
-    const int tid = threadIdx.x, threads = blockDim.x;
+    const int tid = threadIdx.x;
     const int per = 2 * p.TQ; // tokens per entry
     int count[2] = {0, 0};
     int64_t cum[2] = {0, 0};
     uint32_t err = 0;
-    for (int c = tid; c < p.n_cta; c += threads)
-        p.joins[c].n_parts = 0;
     if (tid == 0)
-        s_most = 0;
+        sm.most = 0;
     for (int b0 = 0; b0 < p.batch; b0 += threads) {
         const int b = b0 + tid;
         int n = 0, t0 = 0, L = 0;
@@ -216,15 +227,15 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
             L = min(max(L, 0), p.max_kv);
         }
         const int ent = fast_div(n + per - 1, p.div_per);
-        const int end = block_scan(ent, s_scan);
-        s_ent[tid] = end - ent;
+        const int end = block_scan(ent, sm.scan, threads);
+        sm.ent[tid] = end - ent;
         if (tid == threads - 1)
-            s_ent[threads] = end;
-        s_t0[tid] = t0;
-        s_n[tid] = n;
-        s_len[tid] = L;
-        __syncthreads();
-        const int n_round = s_ent[threads];
+            sm.ent[threads] = end;
+        sm.t0[tid] = t0;
+        sm.n[tid] = n;
+        sm.len[tid] = L;
+        plan_sync(threads);
+        const int n_round = sm.ent[threads];
         for (int e0 = 0; e0 < n_round; e0 += threads) {
             const int e = e0 + tid;
             ChunkEntry en{};
@@ -234,17 +245,17 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
                 int lo = 0, hi = threads - 1; // the last request that starts at or before e
                 while (lo < hi) {
                     const int mid = (lo + hi + 1) >> 1;
-                    if (s_ent[mid] <= e)
+                    if (sm.ent[mid] <= e)
                         lo = mid;
                     else
                         hi = mid - 1;
                 }
-                const int at = (e - s_ent[lo]) * per;
+                const int at = (e - sm.ent[lo]) * per;
                 en.b = b0 + lo;
-                en.t0 = s_t0[lo] + at;
-                en.n_tok = min(per, s_n[lo] - at);
-                en.L = s_len[lo];
-                en.pos0 = en.L - s_n[lo] + at;
+                en.t0 = sm.t0[lo] + at;
+                en.n_tok = min(per, sm.n[lo] - at);
+                en.L = sm.len[lo];
+                en.pos0 = en.L - sm.n[lo] + at;
                 int k0, k1;
                 key_range(p, en.L, en.pos0, en.pos0 + en.n_tok - 1, k0, k1);
                 en.key_lo = k0;
@@ -254,29 +265,31 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
                 en.n_tiles = max(1, (max(k1, 0) + tile - 1) / tile - en.lo);
                 en.tile_cost = kind ? p.cost_few : en.n_tok > p.TQ ? p.cost_pair : p.cost_single;
                 add.places = kind ? 1 << 16 : 1;
-                add.cost[kind] = entry_cost(p, en);
+                const int64_t cost = entry_cost(p, en);
+                add.cost[0] = kind ? 0 : cost;
+                add.cost[1] = kind ? cost : 0;
                 if (!kind)
-                    atomicMax(&s_most, en.tile_cost);
+                    atomicMax(&sm.most, en.tile_cost);
             }
-            const PlanSum sum = block_scan(add, s_sum);
+            const PlanSum sum = block_scan(add, sm.sum, threads);
             if (kind >= 0) {
-                const int at = count[kind] + (kind ? sum.places >> 16 : sum.places & 0xffff) - 1;
-                en.cum = cum[kind] + sum.cost[kind] - add.cost[kind];
+                const int at = (kind ? count[1] + (sum.places >> 16) : count[0] + (sum.places & 0xffff)) - 1;
+                en.cum = kind ? cum[1] + sum.cost[1] - add.cost[1] : cum[0] + sum.cost[0] - add.cost[0];
                 // overlapping requests may give more than fit: those are dropped
                 if (at < p.max_entries) {
                     p.entries[kind * p.max_entries + at] = en;
                     if (at < kPlanThreads)
-                        s_cum[kind][at] = en.cum;
+                        sm.cum[kind][at] = en.cum;
                     if (at < kPlanNear)
-                        s_entry[kind][at] = en;
+                        sm.entry[kind][at] = en;
                 }
             }
-            count[0] += s_sum[31].places & 0xffff;
-            count[1] += s_sum[31].places >> 16;
-            cum[0] += s_sum[31].cost[0];
-            cum[1] += s_sum[31].cost[1];
+            count[0] += sm.sum[31].places & 0xffff;
+            count[1] += sm.sum[31].places >> 16;
+            cum[0] += sm.sum[31].cost[0];
+            cum[1] += sm.sum[31].cost[1];
         }
-        __syncthreads(); // the next round overwrites the requests
+        plan_sync(threads); // the next round overwrites the requests
     }
 #pragma unroll
     for (int kind = 0; kind < 2; ++kind)
@@ -288,9 +301,27 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
         }
     if (err && p.err_user)
         atomicOr(p.err_user, err);
+    if (tid < 2) {
+        sm.count[tid] = tid ? count[1] : count[0];
+        sm.total[tid] = tid ? cum[1] : cum[0];
+    }
+}
+
+// One block.  Its first `threads` threads list the entries (as few as make it
+// one round: the barriers cost what they have to wait for), then all of them
+// cut the parts, one a thread.
+template <int D>
+__global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_constant__ ChunkParams p, int threads)
+{
+    __shared__ PlanShared sm;
+    ptx::launch_dependents();
+    if (static_cast<int>(threadIdx.x) < threads)
+        plan_entries<D>(p, sm, threads);
+    __syncthreads();
     // CTAs of each list by its share of the cost, in pairs (see part_of); a part
     // is at least one tile long, so that every CTA between the first and the last of an item holds
     // one of its tiles
+    const int64_t cum[2] = {sm.total[0], sm.total[1]};
     int parts[2];
     {
         const int64_t both = cum[0] + cum[1];
@@ -299,7 +330,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
             share = min(max(static_cast<int>(div64(cum[0] * p.n_cta + both, 2 * both)) * 2, 2), p.n_cta - 2);
 #pragma unroll
         for (int kind = 0; kind < 2; ++kind) {
-            const int64_t tile = kind ? p.cost_few : s_most, least = max(tile, static_cast<int64_t>(p.cost_least));
+            const int64_t tile = kind ? p.cost_few : sm.most, least = max(tile, static_cast<int64_t>(p.cost_least));
             int g = kind ? p.n_cta - share : share;
             if (cum[kind] < least * g)
                 g = static_cast<int>(div64(cum[kind] + least - 1, least));
@@ -308,24 +339,33 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
             parts[kind] = g;
         }
     }
-    for (int c = tid; c < p.n_cta; c += threads) {
+    for (int c = threadIdx.x; c < p.n_cta; c += blockDim.x) {
         ChunkPart out{};
         if (c < parts[0] + parts[1]) {
             const int kind = c >= parts[0] ? 1 : 0;
             const int part = kind ? c - parts[0] : c, g = kind ? parts[1] : parts[0];
             const int64_t total = kind ? cum[1] : cum[0];
             const int64_t x = div64(total * part + g - 1, g);  // first cost unit of this part
-            int lo = 0, hi = (kind ? count[1] : count[0]) - 1; // the last entry that starts at or before x
+            // the last entry that starts at or before x
+            int lo = 0, hi = sm.count[kind] - 1;
+            if (hi >= kPlanThreads) {
+                const ChunkEntry *list = p.entries + kind * p.max_entries;
+                while (lo < hi) {
+                    const int mid = (lo + hi + 1) >> 1;
+                    if (list[mid].cum <= x)
+                        lo = mid;
+                    else
+                        hi = mid - 1;
+                }
+            }
             while (lo < hi) {
                 const int mid = (lo + hi + 1) >> 1;
-                const int64_t at =
-                    mid < kPlanThreads ? s_cum[kind][mid] : p.entries[kind * p.max_entries + mid].cum;
-                if (at <= x)
+                if (sm.cum[kind][mid] <= x)
                     lo = mid;
                 else
                     hi = mid - 1;
             }
-            const ChunkEntry en = lo < kPlanNear ? s_entry[kind][lo] : p.entries[kind * p.max_entries + lo];
+            const ChunkEntry en = lo < kPlanNear ? sm.entry[kind][lo] : p.entries[kind * p.max_entries + lo];
             out.at = en;
             const int64_t cost = item_cost(p, en);
             out.total = total;
@@ -333,13 +373,14 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
             out.few = kind;
             out.cta = kind ? parts[0] : 0;
             out.parts = g;
-            out.n_entries = kind ? count[1] : count[0];
+            out.n_entries = sm.count[kind];
             out.entry = lo;
             out.item = static_cast<int>(div64(x - en.cum, cost));
             const int64_t in = x - en.cum - out.item * cost;
             out.tile = static_cast<int>(div64(in + en.tile_cost - 1, en.tile_cost));
         }
         p.parts[c] = out;
+        p.joins[c].n_parts = 0;
     }
 }
 
@@ -379,18 +420,18 @@ __device__ __forceinline__ void join_block(const ChunkParams &p, const ChunkJoin
     const float *b0 = partial<D>(p, cta, 1, slot) + r;
 #pragma unroll 4
     for (int q = 0; q < n_parts; ++q)
-        M = fmaxf(M, __ldg((q ? partial<D>(p, cta + q, 0, slot) + r : b0) + N * 128));
+        M = fmaxf(M, __ldcg((q ? partial<D>(p, cta + q, 0, slot) + r : b0) + N * 128));
     const float M0 = M == kNegInf ? 0.f : M;
 #pragma unroll 2
     for (int q = 0; q < n_parts; ++q) {
         const float *b = q ? partial<D>(p, cta + q, 0, slot) + r : b0;
-        const float m = __ldg(b + N * 128), w = ptx::ex2(m - M0);
-        l = fmaf(w, __ldg(b + (N + 1) * 128), l);
-        lr = fmaf(w, __ldg(b + (N + 2) * 128), lr);
+        const float m = __ldcg(b + N * 128), w = ptx::ex2(m - M0);
+        l = fmaf(w, __ldcg(b + (N + 1) * 128), l);
+        lr = fmaf(w, __ldcg(b + (N + 2) * 128), lr);
 #pragma unroll
         for (int i = 0; i < C; ++i) {
             // the O of a part without a key of this row was not written
-            const float v = __ldg(b + (z * C + i) * 128);
+            const float v = __ldcg(b + (z * C + i) * 128);
             o[i] = m == kNegInf ? o[i] : fmaf(w, v, o[i]);
         }
     }
@@ -419,7 +460,7 @@ __device__ __forceinline__ void join_few(const ChunkParams &p, const ChunkJoin &
     for (int n = z * kPerBlock + static_cast<int>(threadIdx.x) / D; n < jn.rows[slot]; n += kJoinSplit * kPerBlock) {
         float M = kNegInf;
         for (int q = lane; q < n_parts; q += 32)
-            M = fmaxf(M, __ldg(part(q) + R * 128 + n));
+            M = fmaxf(M, part(q)[R * 128 + n]);
 #pragma unroll
         for (int d = 16; d; d >>= 1)
             M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
@@ -429,10 +470,10 @@ __device__ __forceinline__ void join_few(const ChunkParams &p, const ChunkJoin &
             float w = 0.f, a = 0.f;
             if (q0 + lane < n_parts) {
                 const float *s = part(q0 + lane) + R * 128 + n;
-                w = ptx::ex2(__ldg(s) - M0);
+                w = ptx::ex2(s[0] - M0);
 #pragma unroll
                 for (int k = 1; k <= 4; ++k)
-                    a += __ldg(s + R * k);
+                    a += s[R * k];
                 a *= w;
             }
 #pragma unroll
@@ -443,7 +484,7 @@ __device__ __forceinline__ void join_few(const ChunkParams &p, const ChunkJoin &
                 float v[kDepth];
 #pragma unroll
                 for (int i = 0; i < kDepth; ++i)
-                    v[i] = q + i < n_parts ? __ldg(part(q + i) + n * 128 + dim) : 0.f;
+                    v[i] = q + i < n_parts ? part(q + i)[n * 128 + dim] : 0.f;
 #pragma unroll
                 for (int i = 0; i < kDepth; ++i)
                     o = fmaf(__shfl_sync(0xffffffffu, w, (q + i) & 31), v[i], o);

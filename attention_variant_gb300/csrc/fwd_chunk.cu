@@ -40,6 +40,7 @@
 // are replaced by -inf, and as 0 * NaN is not 0, the S warp zeroes those rows
 // of V in shared memory (only in tiles at the ends of the cache or window).
 #include <cuda_bf16.h>
+#include <algorithm>
 #include <cstdint>
 
 #include "chunk_few.cuh"
@@ -890,11 +891,12 @@ cudaError_t launch_mod(const ChunkMaps &maps, const ChunkParams &p, cudaStream_t
         configured[p.device] = true;
     }
     // one round of the planning kernel for the requests and their entries, as
-    // long as its block allows
+    // long as its block allows, and a thread for each part
     int threads = 32;
     while (threads < kPlanThreads && (threads < p.batch || threads < p.max_entries))
         threads *= 2;
-    chunk_plan_kernel<D><<<1, threads, 0, stream>>>(p);
+    const int block = std::min(std::max(threads, (p.n_cta + 31) & ~31), kPlanThreads);
+    chunk_plan_kernel<D><<<1, block, 0, stream>>>(p, threads);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess)
         return e;

@@ -280,7 +280,7 @@ constexpr int kFewTile = 128;
 constexpr int kFewRows = 16; // query rows of a request and KV head, at most
 
 // One or two row blocks of a request, as the planning kernel lists them.
-struct ChunkEntry {
+struct alignas(16) ChunkEntry {
     int b, t0, n_tok, pos0;    // request, first token row, tokens, position of the first
     int L, key_lo;             // cached keys; lowest key that the rows see
     int lo, n_tiles;           // key tiles [lo, lo + n_tiles)
@@ -288,7 +288,7 @@ struct ChunkEntry {
     int64_t cum;               // cost of everything before it on its list, all heads
 };
 // A CTA's part of the work: [first, end) of the cost units of its list.
-struct ChunkPart {
+struct alignas(16) ChunkPart {
     int64_t total, end;        // cost of the whole list; the part's end
     int few;                   // which list: row blocks or few rows
     int cta, parts;            // the list's first CTA and number of parts
