@@ -16,7 +16,7 @@
 // pairs -- and walks the (token, head) rows with it, so that a unit costs an
 // address, two loads, the rotation and two stores (about 90 instructions for
 // 8 bf16 pairs; with the place and the tensor worked out for every unit it
-// was 290, in 116 registers, and 45 us where this takes 26 for q and k of 8 x
+// was 290, in 116 registers, and 45 us where this takes 25 for q and k of 8 x
 // 2048 tokens of 16 heads of 64).
 #include <cuda_bf16.h>
 #include <cstdint>
@@ -58,10 +58,24 @@ __device__ __forceinline__ float2 turn_cos_sin(uint64_t turn)
     }
 }
 
-// Rotates the V pairs of (a, b) by cs[0 .. V): pair e is (a, b)[e], or, where
-// INTER, neighbours of the 2 V elements a, b.
+// Where the angle of a token's pair i lies: two angles (16 bytes) of each unit
+// of V pairs, then the next two of each, so that the threads of neighbouring
+// units read neighbouring words (unit after unit, 8 threads met in two groups
+// of banks: 29.5 us for the append of 11,810 tokens of 16 + 2 + 2 heads of 128,
+// 27.8 this way).
+template <int V>
+__device__ __forceinline__ int angle_at(int i, int units)
+{
+    if constexpr (V <= 2)
+        return i;
+    const int u = i / V, e = i % V;
+    return ((e / 2) * units + u) * 2 + e % 2;
+}
+
+// Rotates the V pairs of (a, b) by the angles of their unit, cs[angle_at]:
+// pair e is (a, b)[e], or, where INTER, neighbours of the 2 V elements a, b.
 template <class T, int V, bool INTER>
-__device__ __forceinline__ void rotate_pairs(Vec<T, V> &a, Vec<T, V> &b, const float2 *cs)
+__device__ __forceinline__ void rotate_pairs(Vec<T, V> &a, Vec<T, V> &b, const float2 *cs, int units)
 {
     if constexpr (sizeof(T) == 2 && V >= 2) {
         // bf16 two at a time: a word holds pairs e, e + 1 of one half, or both
@@ -71,7 +85,8 @@ __device__ __forceinline__ void rotate_pairs(Vec<T, V> &a, Vec<T, V> &b, const f
         auto hi = [](uint32_t w) { return __uint_as_float(w & 0xffff0000u); };
 #pragma unroll
         for (int e = 0; e < V; e += 2) {
-            const float4 f = *reinterpret_cast<const float4 *>(cs + e); // cos, sin of pairs e, e + 1
+            // cos, sin of pairs e, e + 1
+            const float4 f = *reinterpret_cast<const float4 *>(cs + e * units);
             uint32_t &w0 = INTER ? (e < V / 2 ? wa[e % (V / 2)] : wb[e % (V / 2)]) : wa[e / 2];
             uint32_t &w1 = INTER ? (e + 1 < V / 2 ? wa[(e + 1) % (V / 2)] : wb[(e + 1) % (V / 2)]) : wb[e / 2];
             const float a0 = lo(w0), b0 = INTER ? hi(w0) : lo(w1);
@@ -82,14 +97,20 @@ __device__ __forceinline__ void rotate_pairs(Vec<T, V> &a, Vec<T, V> &b, const f
             w1 = INTER ? ptx::pack_bf16(ya1, yb1) : ptx::pack_bf16(yb0, yb1);
         }
     } else {
+        alignas(16) float2 f[V];
+        if constexpr (V == 1)
+            f[0] = cs[0];
+        else
+#pragma unroll
+            for (int e = 0; e < V; e += 2)
+                *reinterpret_cast<float4 *>(f + e) = *reinterpret_cast<const float4 *>(cs + e * units);
 #pragma unroll
         for (int e = 0; e < V; ++e) {
             T &ra = INTER ? (2 * e < V ? a.e[(2 * e) % V] : b.e[(2 * e) % V]) : a.e[e];
             T &rb = INTER ? (2 * e + 1 < V ? a.e[(2 * e + 1) % V] : b.e[(2 * e + 1) % V]) : b.e[e];
-            const float2 f = cs[e];
             const float xa = widen(ra), xb = widen(rb);
-            narrow(ra, xa * f.x - xb * f.y);
-            narrow(rb, xa * f.y + xb * f.x);
+            narrow(ra, xa * f[e].x - xb * f[e].y);
+            narrow(rb, xa * f[e].y + xb * f[e].x);
         }
     }
 }
@@ -102,6 +123,7 @@ __global__ void __launch_bounds__(kThreads, 8) rope_kernel(const __grid_constant
     __shared__ __align__(16) float2 s_cs[kMaxAngles];
     __shared__ int64_t s_src[kMaxTile], s_dst[kMaxTile]; // rows of the tile's tokens; s_dst < 0: skipped
     const RopeStream &st = p.st[blockIdx.y];
+    const int rot_units = p.pairs / V;
     const int tid = threadIdx.x, t0 = blockIdx.x * st.tile, n_tok = min(st.tile, p.tokens - t0);
     if (n_tok <= 0)
         return; // the grid is as wide as the tensor with the smallest tiles needs
@@ -129,7 +151,7 @@ __global__ void __launch_bounds__(kThreads, 8) rope_kernel(const __grid_constant
             float2 cs = turn_cos_sin(static_cast<uint64_t>(pos) * p.turns[i]);
             cs.x *= p.magnitude;
             cs.y *= p.backward ? -p.magnitude : p.magnitude;
-            s_cs[e] = cs;
+            s_cs[tl * p.pairs + angle_at<V>(i, rot_units)] = cs;
         }
     __syncthreads();
 
@@ -138,7 +160,7 @@ __global__ void __launch_bounds__(kThreads, 8) rope_kernel(const __grid_constant
     const int y = fast_div(tid, p.div_ux), x = tid - y * p.div_ux.d;
     if (y >= p.uy)
         return;
-    const int rot_units = p.pairs / V, rows = n_tok * st.heads;
+    const int rows = n_tok * st.heads;
     for (int ux = x; ux < p.units; ux += p.div_ux.d) {
         const bool pair = ux < rot_units;
         const int at = !pair ? p.rot + (ux - rot_units) * V : INTER ? ux * 2 * V : ux * V;
@@ -155,7 +177,7 @@ __global__ void __launch_bounds__(kThreads, 8) rope_kernel(const __grid_constant
             if (pair) {
                 b = *reinterpret_cast<const Vec<T, V> *>(from + b_at);
                 if (st.rotate)
-                    rotate_pairs<T, V, INTER>(a, b, s_cs + tok * p.pairs + ux * V);
+                    rotate_pairs<T, V, INTER>(a, b, s_cs + tok * p.pairs + ux * (V == 1 ? 1 : 2), rot_units);
                 *reinterpret_cast<Vec<T, V> *>(to + b_at) = b;
             }
             *reinterpret_cast<Vec<T, V> *>(to) = a;
