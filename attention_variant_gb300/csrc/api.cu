@@ -1146,7 +1146,7 @@ fl_status chunk_plan(const fl_tensor *q, const fl_tensor *k_cache, const fl_tens
     if (entries > (int64_t(1) << 30))
         return fail(FL_ERR_UNSUPPORTED, "batch and tokens give more than 2^30 row blocks");
     pl.max_entries = int(entries);
-    pl.joins = align_up(fl::kChunkMaxCtas * sizeof(fl::ChunkPart));
+    pl.joins = align_up(2 * fl::kChunkMaxCtas * sizeof(fl::ChunkPart));
     pl.entries = pl.joins + align_up(fl::kChunkMaxCtas * sizeof(fl::ChunkJoin));
     pl.partials = pl.entries + align_up(2 * size_t(entries) * sizeof(fl::ChunkEntry));
     pl.total = pl.partials + align_up(size_t(fl::kChunkMaxCtas) * 4 * size_t(pl.D + 4) * 128 * sizeof(float));

@@ -74,8 +74,9 @@ struct FewItem {
     int t0, rows, pos0;   // first token row, rows, first position
     int L, key_lo;        // cached keys; lowest key that any row sees
     int b, kvh;           // request, (first) KV head
-    int n_parts;          // CTAs that share the item
-    int mine;             // this part's buffer: 1 if the item begins here
+    int n_parts;          // CTAs that share the item; 0: the warm-up
+    int cta;              // this part among those of both paths
+    int mine;             // its buffer: 1 if the item begins here
 };
 
 // The slot's tiles: first, first + step, ... < hi.
@@ -118,6 +119,7 @@ template <int D>
 struct FewCtx {
     FewSmem<D> *sm;
     uint32_t tmem;
+    int part; // this CTA's place among the parts of the few rows
     WaitCtl wc;
 };
 
@@ -194,18 +196,32 @@ __device__ void few_producer(const FewCtx<D> &cx, const ChunkParams &p, const CU
     const bool split = few_split_loads(p);
     uint32_t item_count = 0;
     bool ok = true;
-    const ChunkPart me = p.parts[part_of()];
+    ChunkPart me{};
     const ChunkEntry *entries = p.entries + p.max_entries;
-    const int cta = part_of() - me.cta;
-    int e = me.entry, h = me.item, k = me.tile; // entry, item of it, tile of that
+    const int cta = cx.part;
+    int e = 0, h = 0, k = 0; // entry, item of it, tile of that
+    bool warm = p.warm;
+    if (!warm)
+        read_part(p, 1, cta, me, e, h, k);
     for (;;) {
         // ---- the next part
-        FewItem it;
+        FewItem it{};
         it.stop = 1;
         ChunkEntry en{};
         int k_end = 0;
+        // the warm-up, beside the planning kernel: a tile of no keys for each slot, of
+        // which nothing is written, so that the roles' instructions are there before
+        // the loads begin (behind those of a full GPU they took 12 us)
+        if (warm) {
+            it.stop = 0;
+            it.heads = min(p.Hk, 2);
+            it.shift = it.heads - 1;
+            it.hi = 1;
+            it.u_hi = it.heads;
+            it.rows = min(p.G, kFewRows);
+        }
         while (e < me.n_entries) {
-            en = e == me.entry ? me.at : entries[e];
+            en = e == me.entry ? me.at : load_plan(entries + e);
             const int full = item_heads(p, en), heads = min(full, p.Hk - h * full), n_tiles = en.n_tiles * heads;
             const int64_t x0 = en.cum + h * item_cost(p, en);
             if (x0 + static_cast<int64_t>(k) * en.tile_cost >= me.end) {
@@ -228,8 +244,9 @@ __device__ void few_producer(const FewCtx<D> &cx, const ChunkParams &p, const CU
                 ++e;
             }
         }
-        if (!it.stop) {
+        if (!it.stop && !warm) {
             it.shift = it.heads - 1;
+            it.cta = me.cta;
             it.u_lo = (en.lo << it.shift) + k;
             it.u_hi = (en.lo << it.shift) + k_end;
             it.b = en.b;
@@ -251,7 +268,7 @@ __device__ void few_producer(const FewCtx<D> &cx, const ChunkParams &p, const CU
             sm.info[slot] = it;
             ptx::mbar_arrive(bar(sm.info_full[slot])); // release: the fields above first
             if (!it.stop && it.mine && it.n_parts > 1)
-                p.joins[part_of()] = ChunkJoin{it.n_parts, JOIN_FEW, it.kvh, {it.t0, it.t0},
+                p.joins[me.cta] = ChunkJoin{it.n_parts, JOIN_FEW, it.kvh, {it.t0, it.t0},
                                                 {it.rows, it.heads == 2 ? it.rows : 0}, 0};
         }
         __syncwarp();
@@ -262,9 +279,10 @@ __device__ void few_producer(const FewCtx<D> &cx, const ChunkParams &p, const CU
         if (!ok)
             break;
         if (lane == 0) {
+            const int slots = warm ? 0 : it.heads;
             ptx::mbar_arrive_expect_tx(bar(sm.q_full[ring]),
-                                       static_cast<uint32_t>(it.heads * C::kHalves * p.few_tq * p.G) * C::kRowBytes);
-            for (int t = 0; t < it.heads; ++t)
+                                       static_cast<uint32_t>(slots * C::kHalves * p.few_tq * p.G) * C::kRowBytes);
+            for (int t = 0; t < slots; ++t)
 #pragma unroll
                 for (int hf = 0; hf < C::kHalves; ++hf)
                     ptx::tma_load_4d(ptx::smem_u32(sm.q[ring][t]) + hf * C::kQHalf, tm_q, bar(sm.q_full[ring]),
@@ -292,6 +310,11 @@ __device__ void few_producer(const FewCtx<D> &cx, const ChunkParams &p, const CU
         }
         if (!ok)
             break;
+        if (warm) {
+            warm = false;
+            read_part(p, 1, cta, me, e, h, k);
+            continue;
+        }
         // ---- on to the next item
         k = 0;
         if (++h * item_heads(p, en) >= p.Hk) {
@@ -659,7 +682,7 @@ __device__ __forceinline__ bool few_item(const FewCtx<D> &cx, const ChunkParams 
             ++ct.pv;
             ptx::tc_fence_after();
         }
-        if (bits) {
+        if (bits || inf.n_parts == 0) {
             // columns past the item's rows may hold anything and ask for nothing
             const uint32_t ask = (bits >> 16) & row_bits;
             if (ask) {
@@ -731,6 +754,8 @@ __device__ __forceinline__ bool few_item(const FewCtx<D> &cx, const ChunkParams 
         ++ct.pv;
         ptx::tc_fence_after();
     }
+    if (inf.n_parts == 0) // the warm-up
+        return true;
     // ---- the slot's sums over the warp, halved at each exchange until lane i
     // holds row i mod R
 #pragma unroll
@@ -759,7 +784,7 @@ __device__ __forceinline__ bool few_item(const FewCtx<D> &cx, const ChunkParams 
     // take the odd rows
     const int dim = D == 128 ? r : r & 63;
     if (inf.n_parts > 1) {
-        float *mine = partial<D>(p, part_of(), inf.mine, t), *sums = mine + kFewRows * 128;
+        float *mine = partial<D>(p, inf.cta, inf.mine, t), *sums = mine + kFewRows * 128;
 #pragma unroll
         for (int n = 0; n < R; ++n) {
             if (n < rows && (D == 128 || (n & 1) == r >> 6))
@@ -813,13 +838,24 @@ __device__ void few_softmax(const FewCtx<D> &cx, const ChunkParams &p, int t)
     }
 }
 
+// The kernel of the few rows (see chunk_kernel for what runs beside it).
 template <int MOD, int D>
-__device__ __forceinline__ void few_path(const ChunkMaps &maps, const ChunkParams &p, uint8_t *smem)
+__global__ void __launch_bounds__(kThreads, 1)
+    chunk_few_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constant__ ChunkParams p)
 {
     using C = FewCfg<D>;
-    FewSmem<D> *sm = reinterpret_cast<FewSmem<D> *>(smem);
+    extern __shared__ uint8_t smem_raw[];
+    FewSmem<D> *sm = reinterpret_cast<FewSmem<D> *>(smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u));
     const int warp = threadIdx.x >> 5;
+    FewCtx<D> cx;
+    cx.part = part_of(p);
+    if (idle_second(p, 1, cx.part))
+        return;
+
     if (threadIdx.x == 0) {
+        ptx::prefetch_tensormap(&maps.few_q);
+        ptx::prefetch_tensormap(&maps.few_k);
+        ptx::prefetch_tensormap(&maps.few_v);
         for (int b = 0; b < 2; ++b) {
             ptx::mbar_init(bar(sm->q_full[b]), 1);
             ptx::mbar_init(bar(sm->q_empty[b]), 1);
@@ -855,7 +891,6 @@ __device__ __forceinline__ void few_path(const ChunkMaps &maps, const ChunkParam
     __syncthreads();
     ptx::tc_fence_after();
 
-    FewCtx<D> cx;
     cx.sm = sm;
     cx.tmem = sm->tmem_base;
     cx.wc = wait_ctl(p, &sm->abort_flag);
@@ -880,6 +915,7 @@ __device__ __forceinline__ void few_path(const ChunkMaps &maps, const ChunkParam
             ptx::tc_fence_after();
             ptx::tmem_dealloc(cx.tmem, 128);
         }
+        ptx::wait_dependency(); // see chunk_plan.cuh
     }
 }
 

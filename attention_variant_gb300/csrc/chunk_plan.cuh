@@ -78,12 +78,68 @@ __device__ __forceinline__ int64_t entry_cost(const ChunkParams &p, const ChunkE
                (is_few(p, en.n_tok) ? p.cost_few_item : p.cost_item);
 }
 
-// The part of this CTA.  The two SMs of a pair run one path at their best: the
+// What the planning kernel wrote, read past L1: a second kernel may have
+// started before it (below).
+template <class T>
+__device__ __forceinline__ T load_plan(const T *src)
+{
+    static_assert(sizeof(T) % 16 == 0, "16-byte words");
+    union {
+        T value;
+        uint4 word[sizeof(T) / 16];
+    } u;
+#pragma unroll
+    for (size_t i = 0; i < sizeof(T) / 16; ++i)
+        u.word[i] = __ldcg(reinterpret_cast<const uint4 *>(src) + i);
+    return u.value;
+}
+
+// The kernels of the two paths.  The first one's CTAs start beside the planning
+// kernel: they set up and then wait for the plan.  The second one is launched
+// when every CTA of the first has seen the plan, so it reads it without a
+// wait; its CTAs take the SMs as those without work leave them.  Both end with a
+// wait for the one before: the second stands for the first to what follows, and
+// a CTA of the first that gave up early is not gone before the plan is there.  (One kernel for both: the path
+// laid out second started 6 to 9 us late, its instructions fetched from
+// memory.)
+
+// A CTA's place among its kernel's parts.  CTAs go to SMs in order, two by two,
+// but for the first one, whose neighbour is the SM that the planning kernel
+// still held; it gets the last, so that the two SMs of a pair run one path: the
 // instructions of both do not fit what they share (a pair that ran both took
-// 20% longer).  CTAs go to SMs in order, two by two, but for the first one,
-// whose neighbour is the SM that the planning kernel still held; it gets the
-// last.  Where CTAs are placed otherwise the results are the same.
-__device__ __forceinline__ int part_of() { return blockIdx.x + 1 == gridDim.x ? 0 : blockIdx.x + 1; }
+// 20% longer).  Where CTAs are placed otherwise the results are the same.
+__device__ __forceinline__ int part_of(const ChunkParams &p)
+{
+    const int c = blockIdx.x;
+    return p.second ? c : c + 1 == p.n_cta ? 0 : c + 1;
+}
+
+// At the start: a CTA of the second kernel without work (kind 0: row blocks, 1:
+// few rows) has only to wait for the first.
+__device__ __forceinline__ bool idle_second(const ChunkParams &p, int kind, int part)
+{
+    if (!p.second)
+        return false;
+    ptx::launch_dependents();
+    if (__ldcg(&p.parts[kind * p.n_cta + part].parts))
+        return false;
+    ptx::wait_dependency();
+    return true;
+}
+
+// The CTA's part, which begins at tile k of item h of entry e.  A warp.
+__device__ __forceinline__ void read_part(const ChunkParams &p, int kind, int part, ChunkPart &me, int &e, int &h,
+                                          int &k)
+{
+    if (!p.second) {
+        ptx::wait_dependency();
+        ptx::launch_dependents();
+    }
+    me = load_plan(p.parts + kind * p.n_cta + part);
+    e = me.entry;
+    h = me.item;
+    k = me.tile;
+}
 
 // Part c of `parts` covers the cost units x with c total / parts <= x <
 // (c + 1) total / parts, and a tile belongs to the part of its first unit.
@@ -318,9 +374,9 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
     if (static_cast<int>(threadIdx.x) < threads)
         plan_entries<D>(p, sm, threads);
     __syncthreads();
-    // CTAs of each list by its share of the cost, in pairs (see part_of); a part
-    // is at least one tile long, so that every CTA between the first and the last of an item holds
-    // one of its tiles
+    // parts of each list by its share of the cost, in pairs (see part_of); a part is
+    // at least one tile long, so that every part between the first and the last
+    // of an item holds one of its tiles
     const int64_t cum[2] = {sm.total[0], sm.total[1]};
     int parts[2];
     {
@@ -339,11 +395,10 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
             parts[kind] = g;
         }
     }
-    for (int c = threadIdx.x; c < p.n_cta; c += blockDim.x) {
+    for (int c = threadIdx.x; c < 2 * p.n_cta; c += blockDim.x) {
         ChunkPart out{};
-        if (c < parts[0] + parts[1]) {
-            const int kind = c >= parts[0] ? 1 : 0;
-            const int part = kind ? c - parts[0] : c, g = kind ? parts[1] : parts[0];
+        const int kind = c >= p.n_cta ? 1 : 0, part = kind ? c - p.n_cta : c, g = kind ? parts[1] : parts[0];
+        if (part < g) {
             const int64_t total = kind ? cum[1] : cum[0];
             const int64_t x = div64(total * part + g - 1, g);  // first cost unit of this part
             // the last entry that starts at or before x
@@ -370,8 +425,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
             const int64_t cost = item_cost(p, en);
             out.total = total;
             out.end = div64(total * (part + 1) + g - 1, g);
-            out.few = kind;
-            out.cta = kind ? parts[0] : 0;
+            out.cta = (kind ? parts[0] : 0) + part;
             out.parts = g;
             out.n_entries = sm.count[kind];
             out.entry = lo;
@@ -380,7 +434,8 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
             out.tile = static_cast<int>(div64(in + en.tile_cost - 1, en.tile_cost));
         }
         p.parts[c] = out;
-        p.joins[c].n_parts = 0;
+        if (!kind)
+            p.joins[part].n_parts = 0;
     }
 }
 

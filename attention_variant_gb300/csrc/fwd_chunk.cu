@@ -89,7 +89,8 @@ struct Item {
     int L, key_lo;               // cached keys; lowest key that any row of the item sees
     int kvh;
     int n_parts;                 // CTAs that share the item
-    int mine;                    // this part's buffer: 1 if the item begins here
+    int cta;                     // this part among those of both paths
+    int mine;                    // its buffer: 1 if the item begins here
 };
 
 template <int D>
@@ -115,6 +116,7 @@ template <int D>
 struct KernelCtx {
     ChunkSmem<D> *sm;
     uint32_t tmem;
+    int part;
     WaitCtl wc;
 };
 
@@ -130,9 +132,10 @@ __device__ void producer_role(const KernelCtx<D> &cx, const ChunkParams &p, cons
     const uint32_t lane = ptx::lane_id();
     uint32_t kv_count = 0, item_count = 0;
     bool ok = true;
-    const ChunkPart me = p.parts[part_of()];
-    const int cta = part_of() - me.cta;
-    int e = me.entry, h = me.item, k = me.tile; // entry, item of it, tile of that
+    ChunkPart me{};
+    const int cta = cx.part;
+    int e = 0, h = 0, k = 0; // entry, item of it, tile of that
+    read_part(p, 0, cta, me, e, h, k);
     for (;;) {
         // ---- the next part
         Item it;
@@ -140,7 +143,7 @@ __device__ void producer_role(const KernelCtx<D> &cx, const ChunkParams &p, cons
         ChunkEntry en{};
         int k_end = 0;
         while (e < me.n_entries) {
-            en = e == me.entry ? me.at : p.entries[e];
+            en = e == me.entry ? me.at : load_plan(p.entries + e);
             const int64_t x0 = en.cum + h * item_cost(p, en);
             if (x0 + static_cast<int64_t>(k) * en.tile_cost >= me.end) {
                 e = me.n_entries; // the cut falls before this tile
@@ -161,6 +164,7 @@ __device__ void producer_role(const KernelCtx<D> &cx, const ChunkParams &p, cons
             }
         }
         if (!it.stop) {
+            it.cta = me.cta;
             it.kvh = h;
             it.L = en.L;
             it.key_lo = en.key_lo;
@@ -189,7 +193,7 @@ __device__ void producer_role(const KernelCtx<D> &cx, const ChunkParams &p, cons
             sm.info[slot] = it;
             ptx::mbar_arrive(bar(sm.info_full[slot])); // release: the fields above first
             if (!it.stop && it.mine && it.n_parts > 1)
-                p.joins[part_of()] = ChunkJoin{it.n_parts, it.pair ? JOIN_PAIR : JOIN_HALF, it.kvh,
+                p.joins[me.cta] = ChunkJoin{it.n_parts, it.pair ? JOIN_PAIR : JOIN_HALF, it.kvh,
                                                 {it.t0[0], it.t0[1]}, {it.rows[0], it.rows[1]}, 0};
         }
         __syncwarp();
@@ -474,7 +478,7 @@ __device__ __forceinline__ RowOut<D> row_out(const ChunkParams &p, const Item &i
     RowOut<D> w;
     w.out = p.out + tok * p.o_st + head * p.o_sh;
     w.lse = p.lse ? p.lse + head * p.l_sh + tok : nullptr;
-    w.mine = partial<D>(p, part_of(), inf.mine, t) + r;
+    w.mine = partial<D>(p, inf.cta, inf.mine, t) + r;
     return w;
 }
 
@@ -746,18 +750,29 @@ __device__ void softmax_role(const KernelCtx<D> &cx, const ChunkParams &p, int t
 
 // ------------------------------------------------------------------ kernel
 
+// The kernel of the row blocks.
 template <int MOD, int D>
-__device__ __forceinline__ void block_path(const ChunkMaps &maps, const ChunkParams &p, uint8_t *smem)
+__global__ void __launch_bounds__(kThreads, 1)
+    chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constant__ ChunkParams p)
 {
     using C = ChunkCfg<D>;
     constexpr int kStages = C::kStages;
-    ChunkSmem<D> *sm = reinterpret_cast<ChunkSmem<D> *>(smem);
+    extern __shared__ uint8_t smem_raw[];
+    ChunkSmem<D> *sm =
+        reinterpret_cast<ChunkSmem<D> *>(smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u));
     const int warp = threadIdx.x >> 5;
+    KernelCtx<D> cx;
+    cx.part = part_of(p);
+    if (idle_second(p, 0, cx.part))
+        return;
 
     for (uint32_t w = threadIdx.x; w < C::kOnesBytes / 4; w += kThreads)
         reinterpret_cast<uint32_t *>(sm->ones)[w] = 0x3F803F80u; // bf16 1.0 pairs
     ptx::fence_proxy_async_smem();
     if (threadIdx.x == 0) {
+        ptx::prefetch_tensormap(&maps.q);
+        ptx::prefetch_tensormap(&maps.k);
+        ptx::prefetch_tensormap(&maps.v);
         for (int b = 0; b < 2; ++b) {
             ptx::mbar_init(bar(sm->q_full[b]), 1);
             ptx::mbar_init(bar(sm->q_empty[b]), 1);
@@ -793,7 +808,6 @@ __device__ __forceinline__ void block_path(const ChunkMaps &maps, const ChunkPar
     __syncthreads();
     ptx::tc_fence_after();
 
-    KernelCtx<D> cx;
     cx.sm = sm;
     cx.tmem = sm->tmem_base;
     cx.wc = wait_ctl(p, &sm->abort_flag);
@@ -819,34 +833,8 @@ __device__ __forceinline__ void block_path(const ChunkMaps &maps, const ChunkPar
             ptx::tc_fence_after();
             ptx::tmem_dealloc(cx.tmem, 512);
         }
+        ptx::wait_dependency(); // see chunk_plan.cuh
     }
-}
-
-// The first parts are of the row blocks, the others of the few rows.
-template <int MOD, int D>
-__global__ void __launch_bounds__(kThreads, 1)
-    chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constant__ ChunkParams p)
-{
-    extern __shared__ uint8_t smem_raw[];
-    const uint32_t base = ptx::smem_u32(smem_raw);
-    uint8_t *smem = smem_raw + ((1024u - (base & 1023u)) & 1023u);
-    if (threadIdx.x == 0) {
-        ptx::prefetch_tensormap(&maps.q);
-        ptx::prefetch_tensormap(&maps.k);
-        ptx::prefetch_tensormap(&maps.v);
-        ptx::prefetch_tensormap(&maps.few_q);
-        ptx::prefetch_tensormap(&maps.few_k);
-        ptx::prefetch_tensormap(&maps.few_v);
-    }
-    ptx::launch_dependents();
-    ptx::wait_dependency(); // the plan
-    const int parts = p.parts[part_of()].parts, few = p.parts[part_of()].few;
-    if (parts == 0)
-        return; // no work for this CTA
-    if (!few)
-        block_path<MOD, D>(maps, p, smem);
-    else
-        few_path<MOD, D>(maps, p, smem);
 }
 
 // A launch that may start while the kernel before it in the stream runs (it
@@ -868,39 +856,70 @@ cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, int threads, size
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-template <int MOD, int D>
-cudaError_t launch_mod(const ChunkMaps &maps, const ChunkParams &p, cudaStream_t stream)
+// Shared memory of a CTA, and the worst-case pad of its alignment.
+template <class Smem>
+constexpr size_t smem_bytes()
 {
-    // the larger layout plus the worst-case alignment pad within 227 KB per CTA
-    constexpr size_t smem =
-        (sizeof(ChunkSmem<D>) > sizeof(FewSmem<D>) ? sizeof(ChunkSmem<D>) : sizeof(FewSmem<D>)) + 1024;
-    static_assert(smem <= 232448, "shared memory per CTA");
+    static_assert(sizeof(Smem) + 1024 <= 232448, "shared memory per CTA");
+    return sizeof(Smem) + 1024;
+}
+
+template <int MOD, int D>
+cudaError_t configure(int device)
+{
     static bool configured[64] = {}; // by device; benign race: the calls are idempotent
-    if (!configured[p.device]) {
-        cudaFuncAttributes attr;
-        cudaError_t e = cudaFuncGetAttributes(&attr, chunk_kernel<MOD, D>);
-        if (e != cudaSuccess)
-            return e;
-        // the setmaxnreg split assumes exactly kRegsLaunch registers at launch
-        if (attr.numRegs != static_cast<int>(kRegsLaunch))
-            return cudaErrorInvalidConfiguration;
-        e = cudaFuncSetAttribute(chunk_kernel<MOD, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(smem));
-        if (e != cudaSuccess)
-            return e;
-        configured[p.device] = true;
-    }
+    if (configured[device])
+        return cudaSuccess;
+    cudaFuncAttributes attr;
+    cudaError_t e = cudaFuncGetAttributes(&attr, chunk_kernel<MOD, D>);
+    if (e != cudaSuccess)
+        return e;
+    // the setmaxnreg split assumes exactly kRegsLaunch registers at launch
+    if (attr.numRegs != static_cast<int>(kRegsLaunch))
+        return cudaErrorInvalidConfiguration;
+    e = cudaFuncSetAttribute(chunk_kernel<MOD, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(smem_bytes<ChunkSmem<D>>()));
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(chunk_few_kernel<MOD, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(smem_bytes<FewSmem<D>>()));
+    configured[device] = e == cudaSuccess;
+    return e;
+}
+
+template <int MOD, int D>
+cudaError_t launch_mod(const ChunkMaps &maps, ChunkParams &p, cudaStream_t stream)
+{
+    cudaError_t e = configure<MOD, D>(p.device);
+    if (e != cudaSuccess)
+        return e;
     // one round of the planning kernel for the requests and their entries, as
     // long as its block allows, and a thread for each part
     int threads = 32;
     while (threads < kPlanThreads && (threads < p.batch || threads < p.max_entries))
         threads *= 2;
-    const int block = std::min(std::max(threads, (p.n_cta + 31) & ~31), kPlanThreads);
+    const int block = std::min(std::max(threads, (2 * p.n_cta + 31) & ~31), kPlanThreads);
     chunk_plan_kernel<D><<<1, block, 0, stream>>>(p, threads);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess)
-        return e;
-    e = launch_after(chunk_kernel<MOD, D>, dim3(p.n_cta), kThreads, smem, stream, maps, p);
+    e = cudaGetLastError();
+    // groups of more than kFewRows heads have row blocks alone, and no more
+    // tokens than few rows hold make no row block.  Where both may have work the
+    // likelier one is first.
+    const bool few = p.G <= kFewRows, blocks = !few || p.T > p.few_tq;
+    const bool few_first = few && (!blocks || p.T <= static_cast<int64_t>(p.batch) * p.few_tq);
+    // the warm-up pays where the loads queue up: more keys than all rings hold
+    p.warm = few_first && static_cast<int64_t>(p.batch) * p.max_kv * p.Hk >
+                              static_cast<int64_t>(p.n_cta) * FewCfg<D>::kStages * FewCfg<D>::kBN;
+    auto launch = [&](bool few_kernel) {
+        const cudaError_t err = few_kernel
+            ? launch_after(chunk_few_kernel<MOD, D>, dim3(p.n_cta), kThreads, smem_bytes<FewSmem<D>>(), stream, maps, p)
+            : launch_after(chunk_kernel<MOD, D>, dim3(p.n_cta), kThreads, smem_bytes<ChunkSmem<D>>(), stream, maps, p);
+        p.second = 1;
+        p.warm = 0;
+        return err;
+    };
+    if (e == cudaSuccess)
+        e = launch(few_first);
+    if (e == cudaSuccess && few && blocks)
+        e = launch(!few_first);
     if (e != cudaSuccess)
         return e;
     return launch_after(chunk_join_kernel<D>, dim3(p.n_cta, 2, kJoinSplit), kJoinThreads, 0, stream, p);
@@ -908,8 +927,9 @@ cudaError_t launch_mod(const ChunkMaps &maps, const ChunkParams &p, cudaStream_t
 
 } // namespace
 
-cudaError_t launch_chunk(const ChunkMaps &maps, const ChunkParams &p, cudaStream_t stream)
+cudaError_t launch_chunk(const ChunkMaps &maps, const ChunkParams &params, cudaStream_t stream)
 {
+    ChunkParams p = params;
     if (p.head_dim == 64)
         return p.score_mod == MOD_SOFTCAP ? launch_mod<MOD_SOFTCAP, 64>(maps, p, stream)
                                           : launch_mod<MOD_NONE, 64>(maps, p, stream);

@@ -290,10 +290,9 @@ struct alignas(16) ChunkEntry {
 // A CTA's part of the work: [first, end) of the cost units of its list.
 struct alignas(16) ChunkPart {
     int64_t total, end;        // cost of the whole list; the part's end
-    int few;                   // which list: row blocks or few rows
-    int cta, parts;            // the list's first CTA and number of parts
+    int parts, cta;            // parts of the list (0: none); this part among those of both
     int n_entries;
-    int entry, item, tile, pad; // where the part begins
+    int entry, item, tile, pad[2]; // where the part begins
     ChunkEntry at;             // that entry
 };
 // An item whose keys were cut, by the CTA it begins in.
@@ -327,7 +326,9 @@ struct ChunkParams {
     int device, n_cta;
     int cost_pair, cost_single, cost_few, cost_item, cost_few_item, cost_least; // see api.cu
     int max_entries;
-    ChunkPart *parts;          // the workspace: [n_cta]
+    int second;                // the other path's kernel comes first (chunk_plan.cuh)
+    int warm;                  // few rows: run a tile of no keys first
+    ChunkPart *parts;          // the workspace: [2][n_cta], row blocks and few rows
     ChunkJoin *joins;          // [n_cta]
     ChunkEntry *entries;       // [2][max_entries]
     float *partials;           // [n_cta][2][2][D + 4][128]
