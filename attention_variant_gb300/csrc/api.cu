@@ -4,6 +4,7 @@
 // Validation runs before any CUDA call, so a rejected request touches no
 // device state.  The library allocates no device memory: TMA descriptors are
 // passed to the kernel as __grid_constant__ parameters.
+#include <algorithm>
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
@@ -2095,7 +2096,8 @@ fl_status fl_attn_chunk(const fl_tensor *q, const fl_tensor *k_cache, const fl_t
     p.entries = reinterpret_cast<fl::ChunkEntry *>(ws + pl.entries);
     p.partials = reinterpret_cast<float *>(ws + pl.partials);
     p.err_user = desc->error_word;
-    p.timeout_ns = uint64_t(desc->wait_timeout_us ? desc->wait_timeout_us : 2000000u) * 1000ull;
+    // a millisecond at least: a wait that gives up sooner could leave a copy on its way
+    p.timeout_ns = std::max<uint64_t>(desc->wait_timeout_us ? desc->wait_timeout_us : 2000000u, 1000u) * 1000ull;
     const cudaError_t e = fl::launch_chunk(maps, p, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess)
         return fail(FL_ERR_CUDA, "kernel launch failed: %s", cudaGetErrorString(e));

@@ -537,7 +537,8 @@ typedef struct {
     const int32_t *block_table; /* as in fl_decode_desc; NULL: contiguous cache */
     int32_t block_table_stride;
     uint32_t *error_word;       /* NULL, or a device word the kernel ORs FL_DEVERR_* into */
-    uint32_t wait_timeout_us;   /* bound of every device-side wait; 0 means 2,000,000 */
+    uint32_t wait_timeout_us;   /* bound of every device-side wait, at least 1,000; 0 means
+                                   2,000,000 */
 } fl_chunk_desc;
 /*
  * Layouts (bf16 except lse):

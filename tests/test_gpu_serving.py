@@ -372,6 +372,27 @@ def test_chunk_many_long_requests(D, Hq, Hk, page):
     _case([1] * 40, kv_lens, Hq=Hq, Hk=Hk, D=D, page=page, calls=2)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Hq,Hk", [(8, 2), (16, 1), (6, 3), (20, 1)])
+@pytest.mark.parametrize("q_lens", [
+    [1] * 37 + [60],                # few tokens a request: few rows first, then a row block
+    [150] + [1] * 20 + [0, 90, 2],  # row blocks first
+    [1, 2, 1, 1],                   # few rows alone (groups of up to 8 heads)
+])
+def test_chunk_both_kinds_of_work(q_lens, Hq, Hk, D):
+    # a cache that may hold far more than it does, so that the loads are taken
+    # for many, and the same with a tight bound
+    rng = random.Random(len(q_lens))
+    kv_lens = [n + rng.randrange(0, 400) for n in q_lens]
+    p = _problem(q_lens, kv_lens, Hq, Hk, D, 32, width_extra=10000)
+    want = _expected(p)
+    for max_kv in (max(kv_lens), 300000):
+        got = _launch(p, max_kv=max_kv, calls=3)
+        for g in got:
+            _compare(g, want, f"q {q_lens} max_kv {max_kv}")
+            assert torch.equal(g[0], got[0][0]) and torch.equal(g[1], got[0][1])
+
+
 def test_chunk_loud_scores():
     # logits of several hundred: the maximum moves far between tiles
     p = _problem([40, 1], [500, 400], 8, 2, 64, 32, loud=40.0)
