@@ -117,6 +117,7 @@ class FlRopeTable(ctypes.Structure):
 
 
 class FlKvPlanDesc(ctypes.Structure):
+    _device = None  # of the tensors whose addresses it holds
     _fields_ = [
         ("batch", ctypes.c_int32), ("page_size", ctypes.c_int32), ("max_tokens", ctypes.c_int32),
         ("n_free", ctypes.c_int32), ("block_table_stride", ctypes.c_int32),
@@ -128,6 +129,7 @@ class FlKvPlanDesc(ctypes.Structure):
 
 
 class FlChunkDesc(ctypes.Structure):
+    _device = None  # of the tensors whose addresses it holds
     _fields_ = [
         ("score_mod", ctypes.c_int32), ("softcap", ctypes.c_float), ("causal", ctypes.c_int32),
         ("window", ctypes.c_int32), ("scale", ctypes.c_float), ("batch", ctypes.c_int32),
@@ -551,6 +553,17 @@ def _index(t, name: str, shape, dtype="int32", device=None) -> int:
     return t.data_ptr()
 
 
+def _error_word(t, device: int):
+    if t is not None and t.get_device() != device:
+        raise ValueError(f"error_word on {t.device}: the other tensors are on cuda:{device}")
+    return t.data_ptr() if t is not None else None
+
+
+def _check_device(desc, device: int) -> None:
+    if desc._device not in (None, device):
+        raise ValueError(f"the desc's tensors are on cuda:{desc._device}: the current device is cuda:{device}")
+
+
 def make_rope_table(rot_dim: int, *, base=10000.0, layout="half", scaling="none", factor=1.0,
                     context=8192, low=0.0, high=0.0, magnitude=0.0) -> FlRopeTable:
     """The frequencies of a model's rotary positions (see include/fl_attn.h);
@@ -581,7 +594,7 @@ def fl_rope(q, k, q_out, k_out, table: FlRopeTable, positions=None, offset=0, ba
     at = rows = 0
     if positions is not None:
         shape = q.shape
-        if positions.dim() == 2:
+        if positions.dim() == 2 and len(shape) == 4:
             at, rows = _index(positions, "positions", shape[:2], device=dev), shape[1]
         else:
             at = _index(positions, "positions", shape[-3:-2], device=dev)
@@ -612,7 +625,8 @@ def make_kv_plan_desc(q_lens, kv_lens, free_pages, free_head, block_table, kv_le
     d.positions = _index(positions, "positions", (None,), device=dev)
     d.slots = _index(slots, "slots", positions.shape, "int64", device=dev) if slots is not None else None
     d.free_head_out = _index(free_head_out, "free_head_out", (1,), device=dev)
-    d.error_word = error_word.data_ptr() if error_word is not None else None
+    d.error_word = _error_word(error_word, dev)
+    d._device = dev
     d._keep = (q_lens, kv_lens, free_pages, free_head, block_table, kv_lens_out, cu_q, positions, slots,
                free_head_out, error_word)
     return d
@@ -620,7 +634,9 @@ def make_kv_plan_desc(q_lens, kv_lens, free_pages, free_head, block_table, kv_le
 
 def fl_kv_plan(desc: FlKvPlanDesc, stream=None) -> None:
     """Enqueue a serving step's book-keeping (see include/fl_attn.h)."""
-    _check(load_library().fl_kv_plan(ctypes.byref(desc), _stream_of(stream, _device())))
+    dev = _device()
+    _check_device(desc, dev)
+    _check(load_library().fl_kv_plan(ctypes.byref(desc), _stream_of(stream, dev)))
 
 
 def fl_kv_append(q, k, v, q_out, k_cache, v_cache, slots, *, rope: FlRopeTable | None = None,
@@ -662,8 +678,9 @@ def make_chunk_desc(cu_q, kv_lens, block_table, max_kv_len: int, *, score_mod="n
     if block_table is not None:
         d.block_table = _index(block_table, "block_table", (B, None), device=dev)
         d.block_table_stride = block_table.shape[1]
-    d.error_word = error_word.data_ptr() if error_word is not None else None
+    d.error_word = _error_word(error_word, dev)
     d.wait_timeout_us = int(wait_timeout_us)
+    d._device = dev
     d._keep = (cu_q, kv_lens, block_table, error_word)
     return d
 
@@ -684,6 +701,9 @@ def fl_attn_chunk(q, k_cache, v_cache, out, lse, desc: FlChunkDesc, workspace, s
     fl_attn_chunk_workspace_size bytes."""
     lib = load_library()
     dev = _device()
+    _check_device(desc, dev)
+    if workspace.get_device() != dev:
+        raise ValueError(f"workspace on {workspace.device}: the current device is cuda:{dev}")
     _check(lib.fl_attn_chunk(_pack(q, dev), _pack(k_cache, dev), _pack(v_cache, dev), _pack(out, dev),
                              _pack(lse, dev), ctypes.byref(desc), workspace.data_ptr(),
                              workspace.numel() * workspace.element_size(), _stream_of(stream, dev)))

@@ -5,9 +5,9 @@
 // Bound by HBM: every key and value is read once and meets a handful of rows.
 // So the products are turned round: S^T = K Q^T puts a key in each of the 128
 // TMEM lanes and a query row in each of 16 columns, and all lanes of the
-// softmax exponentiate however few the rows are (rows in lanes would leave
-// 124 of 128 idle for a token of a group of four heads; measured at 64
-// requests of 512 to 8192 keys: 131 us).  P^T goes to shared memory as the B
+// softmax exponentiate however few the rows are (rows in lanes leave 124 of
+// 128 idle for a token of a group of four heads: 131 us for 64 requests of 512
+// to 8192 keys, 32 heads over 8 of 64, where this takes 101).  P^T goes to shared memory as the B
 // operand of O^T = V^T P^T, which accumulates a dimension per lane and a row
 // per column.  P goes as two bf16 terms, P rounded and what the rounding left
 // (columns of their own, added at the end): with the products this small the
@@ -28,6 +28,10 @@
 // agree on the tile's maximum, rescale and do the tile again.  2^+-60 leaves
 // fp32 sums of 2^60 such weights in range, and what lies 2^-66 below a row's
 // largest weight does not reach its bf16 output or its LSE.
+//
+// 64 requests of 8192 keys take 174 us, 0.91 of the rate of a plain copy; what
+// shorter ones pay more is the plan (6 us until it is seen), the first loads
+// (5 us), the uneven end (5 us) and the joins (5 us).
 //
 //   warp  0     walks the CTA's items, publishes them, loads Q, K and V by TMA
 //   warp  1     issues S^T of both slots
@@ -177,11 +181,12 @@ __device__ __forceinline__ int few_page(const ChunkParams &p, const FewItem &it,
     return p.page_shift < 0 ? it.b : __ldg(p.block_table + static_cast<int64_t>(it.b) * p.bt_stride + (key >> p.page_shift));
 }
 
-// Who loads V: with boxes of 64 keys or more the warp that loads K; with
-// smaller ones their number is too much for one warp (pages of 16 keys: 264
-// against 184 us for 64 requests of 8192 keys), and V gets the warp that
-// otherwise issues O^T of slot 1 (which costs 5% where it is not needed).
-__device__ __forceinline__ bool few_split_loads(const ChunkParams &p) { return p.few_shift < 6; }
+// Who loads V: with boxes of 32 keys or more the warp that loads K; with
+// smaller ones their number is too much for one warp (pages of 16 keys: 225
+// against 178 us for 64 requests of 8192 keys, 128 against 107 of 512 to 8192),
+// and V gets the warp that otherwise issues O^T of slot 1, which costs 2 to 7%
+// with larger pages (of 32 keys: 108 against 104 us of 512 to 8192).
+__device__ __forceinline__ bool few_split_loads(const ChunkParams &p) { return p.few_shift < 5; }
 
 // Walks the CTA's items, publishes them, loads Q, K and, mostly, V.
 template <int D>

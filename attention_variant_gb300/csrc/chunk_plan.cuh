@@ -6,8 +6,8 @@
 // entry's items are its KV heads -- pairs of KV heads on the few-row list,
 // the last of an odd number by itself -- and an item's tiles its key tiles
 // (times heads).  A list is one long line of tiles with a cost each; it is cut
-// into equal parts, one a CTA, and the CTAs are shared between the lists by
-// cost.
+// into equal parts, one a CTA; each list has a kernel, and the SMs are shared
+// between the two by cost.
 #pragma once
 
 #include "common.cuh"
@@ -445,7 +445,9 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
 // the parts q, in their order.  A kernel of its own: joining inside the
 // attention kernel (by the last CTA to come) put a fence, an atomic and three
 // rounds of loads on one CTA's path, 5 to 8 us at the end of the step; here
-// they are spread over 8 blocks an item.
+// they are spread over 8 blocks an item.  The partials are not read by
+// read-only loads, which may not see what a kernel writes that still runs when
+// this one starts: row blocks, which use a line once, go past L1.
 
 constexpr int kJoinThreads = 128, kJoinSplit = 4;
 

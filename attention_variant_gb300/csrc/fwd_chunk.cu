@@ -7,18 +7,20 @@
 //     M = max m_i,  O = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i.
 //
 // Work.  The query rows of a (request, KV head) are its tokens times the G
-// query heads of the group, token by token: a block of TQ = 128 / G tokens
-// fills the 128 rows of an MMA, so that even one token of a grouped head
-// shares every key load among its heads.  An item is two such blocks (or the
-// last one) of one request and KV head, against the key tiles any of its rows
-// sees.  Lengths live on the device, so a one-block planning kernel lists the
-// items' entries with a running sum of their cost, cuts the whole sum into
-// equal parts and gives each CTA one: CTAs start and stop in the middle of an
-// item's keys, wherever the cut falls, so a single long conversation spreads
-// over the GPU as evenly as a full batch, and a batch needs no heuristics for
-// the number of splits.  At most the first and last item of a CTA are shared;
-// these leave partials in the workspace, and the last CTA to arrive (a ticket
-// per warp of rows) joins them in the order of the keys.
+// query heads of the group, token by token, so that even one token of a
+// grouped head shares every key load among its heads.  Up to 16 rows are "few
+// rows" (chunk_few.cuh); more make row blocks of TQ = 128 / G tokens, which
+// fill the 128 rows of an MMA, and are this file's.  An item is two such blocks
+// (or the last one) of one request and KV head, against the key tiles any of
+// its rows sees.  Lengths live on the device, so a one-block planning kernel
+// (chunk_plan.cuh) lists the items of both kinds with a running sum of their
+// cost, shares the SMs between the lists and cuts each list's sum into equal
+// parts, one per CTA: CTAs start and stop in the middle of an item's keys,
+// wherever the cut falls, so a single long conversation spreads over the GPU as
+// evenly as a full batch, and a batch needs no heuristics for the number of
+// splits.  At most the first and last item of a CTA are shared; these leave
+// partials in the workspace, which a kernel of their own joins in the order
+// of the keys.  The launches overlap (programmatic dependent launch).
 //
 // CTA (persistent, one per SM, 384 threads; the roles and the TMEM layout of
 // the standard forward kernel, see fwd_standard.cu):
@@ -29,16 +31,23 @@
 //   warps 4-11  two softmax warpgroups, one thread per row
 // A slot is a 128-row softmax pipeline.  An item of two row blocks gives each
 // slot a block, and they share every K/V tile (pair); an item of one block
-// (single tokens, short chunks) gives both slots the same rows and every
-// second key tile, and the slots' results are joined in the epilogue, each
-// warpgroup reading both accumulators from TMEM for half of the columns.
-// Warps that hold no row of the item skip the arithmetic.
+// (short chunks) gives both slots the same rows and every second key tile, and
+// the slots' results are joined in the epilogue, each warpgroup reading both
+// accumulators from TMEM for half of the columns.  Warps that hold no row of
+// the item skip the arithmetic.
 //
 // K/V tiles are 112 keys at D = 64 and 64 at D = 128 (TMEM budget of the
 // standard kernel), loaded as boxes of 16 keys: the largest that divides the
 // tile and every page size.  Keys no row may see never reach the sums: logits
 // are replaced by -inf, and as 0 * NaN is not 0, the S warp zeroes those rows
 // of V in shared memory (only in tiles at the ends of the cache or window).
+//
+// Bound by the exponentials and the instructions around them: the last 4096
+// tokens of 16384, 32 heads over 8 of 64, take 470 us, 1020 TFLOP/s, with the
+// tensor pipe 49% active, special functions 45% and 56% of the issue slots
+// used; D = 128 reaches 1.05 us a pair of blocks and tile, 1220 TFLOP/s.  An
+// item costs 2 to 3 us more (its last product, O out of TMEM, its rows to
+// memory), which is what short windows and chunks pay.
 #include <cuda_bf16.h>
 #include <algorithm>
 #include <cstdint>
@@ -906,8 +915,8 @@ cudaError_t launch_mod(const ChunkMaps &maps, ChunkParams &p, cudaStream_t strea
     const bool few = p.G <= kFewRows, blocks = !few || p.T > p.few_tq;
     const bool few_first = few && (!blocks || p.T <= static_cast<int64_t>(p.batch) * p.few_tq);
     // the warm-up pays where the loads queue up: more keys than all rings hold
-    p.warm = few_first && static_cast<int64_t>(p.batch) * p.max_kv * p.Hk >
-                              static_cast<int64_t>(p.n_cta) * FewCfg<D>::kStages * FewCfg<D>::kBN;
+    p.warm = few_first && static_cast<double>(p.batch) * p.max_kv * p.Hk >
+                              static_cast<double>(p.n_cta) * FewCfg<D>::kStages * FewCfg<D>::kBN;
     auto launch = [&](bool few_kernel) {
         const cudaError_t err = few_kernel
             ? launch_after(chunk_few_kernel<MOD, D>, dim3(p.n_cta), kThreads, smem_bytes<FewSmem<D>>(), stream, maps, p)

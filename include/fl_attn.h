@@ -547,14 +547,15 @@ typedef struct {
  *             paged: [num_pages, page_size, Hk, D], page_size in {16, 32, 64, 128, 256};
  *             contiguous (block_table NULL): [B, S_max, Hk, D], S_max >= max_kv_len
  *   lse       [Hq, T] fp32 (natural log) or NULL
- * Rows of no request (past cu_q[B]) are neither read into a result nor
- * written.  A row that sees no key gives O = 0, LSE = -inf.  Keys and values
+ * out and lse overlap no input.  Rows of no request (past cu_q[B]) are neither
+ * read into a result nor written.  A row that sees no key gives O = 0, LSE = -inf.  Keys and values
  * that no row of their request sees (rows kv_lens[b] and later of the last
  * page, keys the window has left) may hold anything; the values of the others
  * must be finite, also where the mask hides them from some rows.
  * Page indices outside the cache read as zero keys and values.
- * `workspace` as for fl_attn_decode: the call's plan and partial results of rows whose keys were split over several SMs,
- * merged in a fixed order, so that results do not depend on scheduling.
+ * `workspace`, as for fl_attn_decode, holds the call's plan and the partial
+ * results of rows whose keys were split over several SMs; they are joined in
+ * a fixed order, so that results do not depend on scheduling.
  * Calls sharing one workspace must not overlap on the GPU.
  */
 fl_status fl_attn_chunk_workspace_size(const fl_tensor *q, const fl_tensor *k_cache,

@@ -205,3 +205,6 @@ def test_cpu_tensors_and_wrong_positions_are_refused():
         fa.fl_rope(x, x, x, None, table)
     with pytest.raises(fa.FlAttnError):
         fa.fl_rope(x, None, torch.empty(1, 4, 2, 72, dtype=x.dtype, device="cuda"), None, table)
+    with pytest.raises(ValueError, match="shape"):
+        # rows of a batch have one position each
+        fa.fl_rope(x[0], None, x[0], None, table, positions=torch.zeros((4, 2), dtype=torch.int32, device="cuda"))

@@ -494,6 +494,30 @@ def test_chunk_without_lse_and_on_another_stream():
     _compare(got, want, "side stream")
 
 
+def test_chunk_two_calls_at_once():
+    # two streams with a workspace each: the calls' kernels share the GPU as they come
+    ps = [_problem([300, 1, 1, 7], [1500, 2000, 3, 7], 8, 2, 64, 16, seed=3),
+          _problem([1] * 24, [700 + 90 * i for i in range(24)], 8, 2, 64, 64, seed=4)]
+    wants = [_expected(p) for p in ps]
+    runs = []
+    for p in ps:
+        t = dict(q=p["q"].cuda(), kc=p["kc"].cuda(), vc=p["vc"].cuda(), cu=_ints(p["cu"]), kv=_ints(p["kv_lens"]),
+                 table=p["table"].cuda(), stream=torch.cuda.Stream())
+        t["d"] = fa.make_chunk_desc(t["cu"], t["kv"], t["table"], max(p["kv_lens"]))
+        t["ws"] = torch.empty(fa.fl_attn_chunk_workspace_size(t["q"], t["kc"], t["d"]), dtype=torch.uint8, device="cuda")
+        t["outs"] = [(torch.full_like(t["q"], 7.0), torch.full((8, p["T"]), 7.0, device="cuda")) for _ in range(20)]
+        runs.append(t)
+    torch.cuda.synchronize()
+    for i in range(20):
+        for t in runs:
+            fa.fl_attn_chunk(t["q"], t["kc"], t["vc"], *t["outs"][i], t["d"], t["ws"], stream=t["stream"])
+    torch.cuda.synchronize()
+    for t, want in zip(runs, wants):
+        for out in t["outs"]:
+            _compare(out, want, "beside another call")
+            assert torch.equal(out[0], t["outs"][0][0]) and torch.equal(out[1], t["outs"][0][1])
+
+
 def test_chunk_captured_graphs_share_a_workspace():
     # two captured steps of different shapes replay in turn over one workspace
     ps = [_problem([60, 1], [100, 3000], 8, 2, 64, 16, seed=1), _problem([1, 1, 9], [2000, 5, 9], 8, 2, 64, 16, seed=2)]
@@ -619,6 +643,13 @@ def test_refusals_of_the_binding():
         fa.fl_attn_chunk(q.cpu(), kc, vc, out, None, d, ws)
     with pytest.raises(fa.FlAttnError, match="needed"):
         fa.fl_attn_chunk(q, kc, vc, out, None, d, ws[:16])
+    with pytest.raises(ValueError, match="workspace"):
+        fa.fl_attn_chunk(q, kc, vc, out, None, d, ws.cpu())
+    with pytest.raises(ValueError, match="error_word"):
+        fa.make_chunk_desc(cu, kv, table, 20, error_word=torch.zeros(1, dtype=torch.int32))
+    with pytest.raises(ValueError, match="desc"):
+        # tensors of no GPU stand for those of another
+        fa.fl_attn_chunk(q, kc, vc, out, None, fa.make_chunk_desc(cu.cpu(), kv.cpu(), table.cpu(), 20), ws)
     with pytest.raises(TypeError):
         fa.make_chunk_desc(cu.long(), kv, table, 20)
     with pytest.raises(ValueError):
