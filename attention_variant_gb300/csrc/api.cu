@@ -2078,14 +2078,14 @@ fl_status fl_attn_chunk(const fl_tensor *q, const fl_tensor *k_cache, const fl_t
     p.device = dev;
     p.n_cta = info.sm_count < fl::kChunkMaxCtas ? info.sm_count : fl::kChunkMaxCtas;
     // costs for the even split, in tenths of a microsecond as measured: a key
-    // tile of two row blocks (1.0 us, with softcap 2.5 at D = 64), of one, a
-    // tile of few rows (32 KB a 64 of head dimension at the SM's share of the
-    // HBM bandwidth), an item's start and end; and the least work a CTA is
+    // tile of two row blocks (1.0 us, with softcap 2.2 at D = 64 and 1.6 at 128),
+    // of one, a tile of few rows (32 KB a 64 of head dimension at the SM's share
+    // of the HBM bandwidth), an item's start and end; and the least work a CTA is
     // woken for
     const bool capped = desc->score_mod == FL_MOD_SOFTCAP;
-    p.cost_pair = capped ? (pl.D == 64 ? 25 : 16) : 10;
-    p.cost_single = capped ? (pl.D == 64 ? 14 : 9) : 8;
-    p.cost_few = (capped ? 10 : 7) * int(pl.D / 64);
+    p.cost_pair = capped ? (pl.D == 64 ? 22 : 16) : 10;
+    p.cost_single = capped ? (pl.D == 64 ? 12 : 9) : 8;
+    p.cost_few = (capped ? 9 : 7) * int(pl.D / 64);
     p.cost_item = 25;
     p.cost_few_item = 20;
     p.cost_least = 20;

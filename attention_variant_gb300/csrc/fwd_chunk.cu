@@ -292,7 +292,7 @@ __device__ __forceinline__ bool uses(int j, int first, int hi, int step)
     return j >= first && j < hi && ((j - first) & (step - 1)) == 0;
 }
 
-template <int D>
+template <int MOD, int D>
 __device__ void s_role(const KernelCtx<D> &cx)
 {
     using C = ChunkCfg<D>;
@@ -330,14 +330,16 @@ __device__ void s_role(const KernelCtx<D> &cx)
             if (!ok)
                 break;
             // rows of V that no query row sees: zero (their P is 0, but the bytes
-            // may be anything).  Each lane's writes reach the tensor core through
-            // its proxy fence, s_full, p_full and the P V issue.
+            // may be anything); with softcap those of K, too (softcap_scores).  Each
+            // lane's writes reach the tensor core through its proxy fence, the S
+            // issue, s_full, p_full and the P V issue.
             const int j0 = j * kBN;
             const int dead_lo = min(kBN, max(0, key_lo - j0)), dead_hi = min(kBN, max(0, L - j0));
             if (dead_lo > 0 || dead_hi < kBN) {
 #pragma unroll
-                for (int hf = 0; hf < C::kHalves; ++hf) {
-                    uint4 *v = reinterpret_cast<uint4 *>(sm.v[stage] + hf * C::kKVHalf);
+                for (int hf = 0; hf < (MOD == MOD_SOFTCAP ? 2 : 1) * C::kHalves; ++hf) {
+                    uint4 *v = reinterpret_cast<uint4 *>((hf < C::kHalves ? sm.v[stage] : sm.k[stage]) +
+                                                         hf % C::kHalves * C::kKVHalf);
                     for (int c = lane; c < dead_lo * 8; c += 32)
                         v[c] = make_uint4(0, 0, 0, 0);
                     for (int c = dead_hi * 8 + lane; c < kBN * 8; c += 32)
@@ -591,14 +593,45 @@ __device__ __forceinline__ void write_joined(const ChunkParams &p, const Item &i
     }
 }
 
+// cap tanh(z / cap) as out (1 - 2 / (1 + 2^(in z))) in log2 units, four scores
+// to a reciprocal: 1 / a = b c d / (a b c d), with the exponent held to 30, where
+// tanh is 1 to the last bit and four factors stay in range.  (NaN stays NaN and
+// spreads to the other three, so keys that no row sees are zeroed, as V is.)
+// Special functions bound the softcap, and this takes 2.25 a score with the
+// softmax's own in place of 3 (2048 tokens on 8192 keys, 32 heads over 8 of 64:
+// 265 -> 236 us; 16 over 2 of 128: 179 -> 161; two scores to a reciprocal: 248,
+// 164).
+template <int N>
+__device__ __forceinline__ void softcap_scores(float (&x)[N], float in, float out)
+{
+    const float m2o = -2.f * out;
+#pragma unroll
+    for (int e = 0; e < N; e += 4) {
+        float d[4];
+        ptx::fma2(d[0], d[1], x[e], x[e + 1], in, in, 0.f, 0.f);
+        ptx::fma2(d[2], d[3], x[e + 2], x[e + 3], in, in, 0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            asm("min.NaN.f32 %0, %0, 0f41F00000;" : "+f"(d[i]));
+            d[i] = ptx::ex2(d[i]);
+        }
+        ptx::add2(d[0], d[1], 1.f, 1.f);
+        ptx::add2(d[2], d[3], 1.f, 1.f);
+        const float a = d[0] * d[1], b = d[2] * d[3], t = ptx::rcp_approx(a * b) * m2o, ta = t * b, tb = t * a;
+        ptx::fma2(x[e], x[e + 1], ta, ta, d[1], d[0], out, out);
+        ptx::fma2(x[e + 2], x[e + 3], tb, tb, d[3], d[2], out, out);
+    }
+}
+
 template <int MOD, int D>
 __device__ void softmax_role(const KernelCtx<D> &cx, const ChunkParams &p, int t)
 {
     using C = ChunkCfg<D>;
     constexpr int kBN = C::kBN;
-    // the warpgroups of a pair take turns on the exponentials of plain scores
-    // and run freely with softcap, as in the standard kernel
-    constexpr bool kTurns = MOD != MOD_SOFTCAP;
+    // the warpgroups of a pair take turns on the exponentials; with softcap at D =
+    // 64 they run freely, as in the standard kernel (321 us with turns, 236
+    // without; at D = 128 157 and 160)
+    constexpr bool kTurns = MOD != MOD_SOFTCAP || D == 128;
     ChunkSmem<D> &sm = *cx.sm;
     const int r = threadIdx.x & 127;            // row of the block = TMEM lane
     const int wq = (threadIdx.x >> 5) & 3;      // warp's quarter of the lanes
@@ -608,11 +641,6 @@ __device__ void softmax_role(const KernelCtx<D> &cx, const ChunkParams &p, int t
     const uint32_t tP = cx.tmem + lanes + C::kColP + C::kStrideP * t;
     const uint32_t b_turn_mine = bar(sm.turn[t]), b_turn_other = bar(sm.turn[t ^ 1]);
     uint32_t scount = 0, pvcount = 0, turns = 0, joins = 0;
-    ScoreMod smod;
-    smod.qk_log2 = p.qk_log2;
-    smod.softcap_in = p.softcap_in;
-    smod.softcap_out = p.softcap_out;
-    smod.alibi_c = smod.scale = smod.b = smod.h = 0.f;
     auto turn_wait = [&]() {
         return (t == 0 && turns == 0) || warp_wait(b_turn_mine, (t == 1 ? turns : turns - 1) & 1, cx.wc, W_TURN);
     };
@@ -655,7 +683,8 @@ __device__ void softmax_role(const KernelCtx<D> &cx, const ChunkParams &p, int t
                 if (take_turns && !turn_wait())
                     return;
                 const int j0 = (first + kk * step) * kBN;
-                apply_score_mod<MOD, kBN>(x, smod, 0, j0);
+                if constexpr (MOD == MOD_SOFTCAP)
+                    softcap_scores<kBN>(x, p.softcap_in, p.softcap_out);
                 if (!(j0 >= full_lo && j0 + kBN <= full_hi))
                     apply_row_mask<kBN>(x, j0, row_lo, row_hi);
                 uint32_t pk[kBN / 2];
@@ -833,7 +862,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (warp == 0)
             producer_role(cx, p, &maps.q, &maps.k, &maps.v);
         else if (warp == 1)
-            s_role(cx);
+            s_role<MOD>(cx);
         else
             pv_role(cx, warp - 2);
         ptx::tc_fence_before();

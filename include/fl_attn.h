@@ -550,8 +550,8 @@ typedef struct {
  * out and lse overlap no input.  Rows of no request (past cu_q[B]) are neither
  * read into a result nor written.  A row that sees no key gives O = 0, LSE = -inf.  Keys and values
  * that no row of their request sees (rows kv_lens[b] and later of the last
- * page, keys the window has left) may hold anything; the values of the others
- * must be finite, also where the mask hides them from some rows.
+ * page, keys the window has left) may hold anything; the others must be
+ * finite, also where the mask hides them from some rows.
  * Page indices outside the cache read as zero keys and values.
  * `workspace`, as for fl_attn_decode, holds the call's plan and the partial
  * results of rows whose keys were split over several SMs; they are joined in
