@@ -363,6 +363,16 @@ def test_chunk_many_requests(D, Hq, Hk):
 
 
 @pytest.mark.parametrize("D", [64, 128])
+def test_chunk_thousands_of_requests(D):
+    # both lists longer than a round of the planning kernel and than what it keeps at hand
+    rng = random.Random(12)
+    q_lens = [9] * 1030 + [1] * 1070 + [0] * 50
+    rng.shuffle(q_lens)
+    kv_lens = [n + rng.randrange(0, 40) for n in q_lens]
+    _case(q_lens, kv_lens, Hq=2, Hk=1, D=D, page=16, pad=5, calls=2)
+
+
+@pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("Hq,Hk,page", [(16, 2, 64), (5, 5, 128), (4, 1, 16)])
 def test_chunk_many_long_requests(D, Hq, Hk, page):
     # tens of key tiles per CTA, of neighbouring heads and across requests, so
