@@ -2080,15 +2080,16 @@ fl_status fl_attn_chunk(const fl_tensor *q, const fl_tensor *k_cache, const fl_t
     // costs for the even split, in tenths of a microsecond as measured: a key
     // tile of two row blocks (1.0 us, with softcap 2.2 at D = 64 and 1.6 at 128),
     // of one, a tile of few rows (32 KB a 64 of head dimension at the SM's share
-    // of the HBM bandwidth), an item's start and end; and the least work a CTA is
-    // woken for
+    // of the HBM bandwidth), an item's start and end (CTAs with many short items
+    // came in last with 2.5 and 2.0 us: 64 single tokens 104 against 101 us, seven
+    // mixed steps 736 against 717 in all); and the least work a CTA is woken for
     const bool capped = desc->score_mod == FL_MOD_SOFTCAP;
     p.cost_pair = capped ? (pl.D == 64 ? 22 : 16) : 10;
     p.cost_single = capped ? (pl.D == 64 ? 12 : 9) : 8;
     p.cost_few = (capped ? 9 : 7) * int(pl.D / 64);
-    p.cost_item = 25;
-    p.cost_few_item = 20;
-    p.cost_least = 20;
+    p.cost_item = 35;
+    p.cost_few_item = 32;
+    p.cost_least = 18;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     p.max_entries = pl.max_entries;
     p.parts = reinterpret_cast<fl::ChunkPart *>(ws);
