@@ -807,17 +807,26 @@ __device__ __forceinline__ bool few_item(const FewCtx<D> &cx, const ChunkParams 
         sm.red[t][wq][lane] = l[0];
     if (!group_sync())
         return false;
-    const volatile float *red = sm.red[t][0];
+    // a row's sum per lane, so that the reciprocals and logarithms are taken at once
+    const volatile float *red = sm.red[t][0] + (lane & (R - 1));
+    const float sum = red[0] + red[kFewRows] + red[2 * kFewRows] + red[3 * kFewRows];
+    const float inv = sum == 0.f ? 0.f : ptx::rcp_approx(sum);
 #pragma unroll
     for (int n = 0; n < R; ++n) {
+        const float norm = __shfl_sync(0xffffffffu, inv, n);
         if (n >= rows || (D == 64 && (n & 1) != r >> 6))
             continue;
-        const float sum = red[n] + red[n + kFewRows] + red[n + 2 * kFewRows] + red[n + 3 * kFewRows];
         const int s = fast_div(n, p.div_g);
         const int64_t tok = inf.t0 + s, head = (inf.kvh + t) * p.G + n - s * p.G;
-        join_write(p, tok, head, dim, o[n], sum);
-        if (dim == 0)
-            join_lse(p, tok, head, m[n], sum);
+        p.out[tok * p.o_st + head * p.o_sh + dim] = __float2bfloat16(o[n] * norm);
+    }
+    if (r < rows) {
+        float ref = m[0];
+#pragma unroll
+        for (int n = 1; n < R; ++n)
+            ref = r == n ? m[n] : ref;
+        const int s = fast_div(r, p.div_g);
+        join_lse(p, inf.t0 + s, (inf.kvh + t) * p.G + r - s * p.G, ref, sum);
     }
     return true;
 }
