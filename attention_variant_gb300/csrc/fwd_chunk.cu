@@ -193,6 +193,10 @@ __device__ void producer_role(const KernelCtx<D> &cx, const ChunkParams &p, cons
                 it.first[t] = max(it.u_lo, k0 / kBN) + (it.pair ? 0 : t);
                 it.hi[t] = min(it.u_hi, (max(k1, 0) + kBN - 1) / kBN);
             }
+            // an item whose rows see no key has no tile: one that no slot uses would be
+            // released by the P V warps alone, while the S warp may still be zeroing
+            // its rows of V
+            it.u_hi = max(it.u_lo, max(it.hi[0], it.hi[1]));
         }
         const uint32_t ring = item_count & 1, slot = item_count % kInfo;
         ok = warp_wait(bar(sm.info_empty[slot]), ((item_count / kInfo) & 1) ^ 1, cx.wc, W_INFO_EMPTY);
@@ -330,8 +334,9 @@ __device__ void s_role(const KernelCtx<D> &cx)
             if (!ok)
                 break;
             // rows of V that no query row sees: zero (their P is 0, but the bytes
-            // may be anything); with softcap those of K, too (softcap_scores).  Each
-            // lane's writes reach the tensor core through its proxy fence, the S
+            // may be anything); with softcap those of K, too (softcap_scores).  Some slot
+            // uses every tile, and its P V, which releases the stage, waits for this
+            // warp's S.  Each lane's writes reach the tensor core through its proxy fence, the S
             // issue, s_full, p_full and the P V issue.
             const int j0 = j * kBN;
             const int dead_lo = min(kBN, max(0, key_lo - j0)), dead_hi = min(kBN, max(0, L - j0));

@@ -1,0 +1,31 @@
+"""GPU parity of the serving-step entry points where lengths, offsets and windows
+are at the limits of what their documentation allows."""
+from __future__ import annotations
+
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+from tests.test_gpu_serving import _compare, _expected, _launch, _problem  # noqa: E402
+
+
+# ------------------------------------------------------------------ chunks
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("page", [0, 64])
+@pytest.mark.parametrize("softcap", [0.0, 20.0])
+def test_chunk_blocks_without_keys_between_long_ones(D, page, softcap):
+    # whole row blocks before the sequence (no key, so nothing to load), each
+    # followed in its CTA by items that fill the rings of tiles; several times
+    q_lens, kv_lens = [], []
+    for i in range(24):
+        q_lens += [200, 40, 70]
+        kv_lens += [(50, 0, 120, 3)[i % 4], 900 + 37 * i, (0, 5)[i % 2]]
+    p = _problem(q_lens, kv_lens, 4, 1, D, page, seed=7)
+    want = _expected(p, softcap=softcap)
+    got = _launch(p, calls=4, softcap=softcap)
+    for g in got:
+        _compare(g, want, "blocks without keys")
+        assert torch.equal(g[0], got[0][0]) and torch.equal(g[1], got[0][1])
