@@ -39,10 +39,11 @@ __device__ __forceinline__ WaitCtl wait_ctl(const ChunkParams &p, uint32_t *abor
     return wc;
 }
 
-// Keys [lo, hi) that the tokens at positions first .. last see.
+// Keys [lo, hi) that the tokens at positions first .. last see.  (first may be far
+// below 0, before the sequence, and the window as long as an int goes.)
 __device__ __forceinline__ void key_range(const ChunkParams &p, int L, int first, int last, int &lo, int &hi)
 {
-    lo = p.window ? max(0, first - p.window + 1) : 0;
+    lo = p.window ? max(0, max(first, 0) - p.window + 1) : 0;
     hi = p.causal ? min(L, last + 1) : L;
 }
 

@@ -29,3 +29,15 @@ def test_chunk_blocks_without_keys_between_long_ones(D, page, softcap):
     for g in got:
         _compare(g, want, "blocks without keys")
         assert torch.equal(g[0], got[0][0]) and torch.equal(g[1], got[0][1])
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("window", [2**31 - 1, 2**31 - 100, 1 << 30])
+def test_chunk_windows_as_long_as_an_int_goes(D, window):
+    # rows before the sequence and rows with keys in one entry, in row blocks and
+    # in few rows: the window hides nothing
+    p = _problem([60, 3, 300, 1], [20, 1, 290, 500], 8, 2, D, 16, seed=3)
+    want = _expected(p)
+    for kw in (dict(window=window), dict()):
+        got, = _launch(p, **kw)
+        _compare(got, want, f"window {window}")
