@@ -1078,6 +1078,8 @@ bool in_place(const View &a, const View &b)
 
 // ------------------------------------------------------------------ chunks over a cache
 
+constexpr int32_t kChunkMaxKeys = INT32_MAX - 255;
+
 struct ChunkPlan {
     View Q, K, V;
     int64_t T, Hq, Hk, D, P, page;
@@ -1117,6 +1119,8 @@ fl_status chunk_plan(const fl_tensor *q, const fl_tensor *k_cache, const fl_tens
         return fail(FL_ERR_INVALID_ARG, "batch must be >= 1");
     if (d->max_kv_len < 1)
         return fail(FL_ERR_INVALID_ARG, "max_kv_len must be >= 1");
+    if (d->max_kv_len > kChunkMaxKeys) // the end of a key tile past the last key is an int, too
+        return fail(FL_ERR_UNSUPPORTED, "max_kv_len %d exceeds %d", d->max_kv_len, kChunkMaxKeys);
     if (d->window < 0 || (d->window > 0 && !d->causal))
         return fail(FL_ERR_INVALID_ARG, "window must be >= 0, and 0 without causal");
     if (d->score_mod != FL_MOD_NONE && d->score_mod != FL_MOD_SOFTCAP)

@@ -533,7 +533,8 @@ typedef struct {
     const int32_t *cu_q;        /* device int32 [B + 1], ascending, within 0 .. T (entries that are
                                    not are clamped, with FL_DEVERR_LENGTHS) */
     const int32_t *kv_lens;     /* device int32 [B]: cached keys, the new ones included */
-    int32_t max_kv_len;         /* host bound on kv_lens[]; larger entries are clamped to it */
+    int32_t max_kv_len;         /* host bound on kv_lens[], below 2^31 - 255; larger entries are clamped
+                                   to it */
     const int32_t *block_table; /* as in fl_decode_desc; NULL: contiguous cache */
     int32_t block_table_stride;
     uint32_t *error_word;       /* NULL, or a device word the kernel ORs FL_DEVERR_* into */

@@ -1,0 +1,33 @@
+"""Refusals of the rotary and serving-step entry points at the limits of their
+arguments (no GPU: every refusal comes before any CUDA call)."""
+from __future__ import annotations
+
+import ctypes
+
+import pytest
+
+import attention_variant_gb300 as fa
+from attention_variant_gb300 import build as fbuild
+
+torch = pytest.importorskip("torch")
+from tests.test_serving_host import _chunk_desc, _t, fake_addresses  # noqa: E402
+
+
+@pytest.fixture(scope="module")
+def lib():
+    fbuild.build()
+    return fa.load_library()
+
+
+def _chunk(lib, **kw):
+    q, c = _t((9, 8, 64)), _t((20, 16, 2, 64))
+    return lib.fl_attn_chunk(q, c, c, q, None, ctypes.byref(_chunk_desc(**kw)), 0x100000, 1 << 40, None)
+
+
+@fake_addresses
+def test_chunk_caches_that_an_int_cannot_count(lib):
+    # the end of the tile that holds the last key has to be an int
+    for n in (2 ** 31 - 1, 2 ** 31 - 255):
+        assert _chunk(lib, max_kv_len=n, block_table_stride=2 ** 31 - 1) == fa.FL_ERR_UNSUPPORTED
+    # (taken up to the look for a GPU)
+    assert _chunk(lib, max_kv_len=2 ** 31 - 256, block_table_stride=2 ** 31 - 1) == fa.FL_ERR_NO_DEVICE
