@@ -493,7 +493,9 @@ typedef struct {
  * Entries of positions and slots past the last token are -1 (so a captured
  * step may be padded).  A token without a page (the free list ran out, or the
  * block table's row is full) gets slot -1, its table entry -1, and
- * FL_DEVERR_PAGES; tokens past max_tokens are dropped with FL_DEVERR_LENGTHS.
+ * FL_DEVERR_PAGES.  Tokens past max_tokens are not listed, with
+ * FL_DEVERR_LENGTHS unless max_tokens is 0; they count in everything else, and
+ * their pages are taken and written to the block table.
  * Requests' block-table entries are taken as they are.
  */
 fl_status fl_kv_plan(const fl_kv_plan_desc *desc, fl_stream_t stream);

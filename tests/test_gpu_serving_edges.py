@@ -2,12 +2,15 @@
 are at the limits of what their documentation allows."""
 from __future__ import annotations
 
+import random
+
 import pytest
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
-from tests.test_gpu_serving import _compare, _expected, _launch, _problem  # noqa: E402
+import attention_variant_gb300 as fa  # noqa: E402
+from tests.test_gpu_serving import _compare, _expected, _launch, _problem, _run_plan  # noqa: E402
 
 
 # ------------------------------------------------------------------ chunks
@@ -41,3 +44,33 @@ def test_chunk_windows_as_long_as_an_int_goes(D, window):
     for kw in (dict(window=window), dict()):
         got, = _launch(p, **kw)
         _compare(got, want, f"window {window}")
+
+
+# ------------------------------------------------------------------ book-keeping
+
+
+@pytest.mark.parametrize("max_tokens", [0, 1, 45, 46, 47, 59])
+@pytest.mark.parametrize("slots", [True, False])
+def test_plan_takes_every_page_whatever_it_lists(max_tokens, slots):
+    # pages that begin with a token past max_tokens are in the table all the same
+    got, want = _run_plan([40, 20], [0, 10], 16, max_tokens=max_tokens, slots=slots)
+    assert got == (want if max_tokens else 0)
+
+
+@pytest.mark.parametrize("B", [700, 1024, 2300])
+@pytest.mark.parametrize("max_tokens", [0, 700, 40000])
+def test_plan_takes_every_page_of_many_requests(B, max_tokens):
+    # the limit falls into any of the scans, or a request of many pages
+    rng = random.Random(B + max_tokens)
+    q = [rng.choice((0, 1, 1, 30, 300)) for _ in range(B)]
+    q[B // 2] = 30000
+    kv = [rng.randrange(0, 300) for _ in range(B)]
+    got, want = _run_plan(q, kv, 16, head=3, seed=B, max_tokens=max_tokens)
+    assert got == (want if max_tokens else 0)
+
+
+@pytest.mark.parametrize("max_tokens", [0, 5])
+def test_plan_reports_pages_that_unlisted_tokens_lack(max_tokens):
+    lengths = fa.FL_DEVERR_LENGTHS if max_tokens else 0
+    assert _run_plan([40, 20], [0, 10], 16, n_free=2, max_tokens=max_tokens)[0] == fa.FL_DEVERR_PAGES | lengths
+    assert _run_plan([40, 1], [0, 3], 16, width=2, max_tokens=max_tokens)[0] == fa.FL_DEVERR_PAGES | lengths
