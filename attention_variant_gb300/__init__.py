@@ -136,6 +136,7 @@ class FlChunkDesc(ctypes.Structure):
         ("cu_q", ctypes.c_void_p), ("kv_lens", ctypes.c_void_p), ("max_kv_len", ctypes.c_int32),
         ("block_table", ctypes.c_void_p), ("block_table_stride", ctypes.c_int32),
         ("error_word", ctypes.c_void_p), ("wait_timeout_us", ctypes.c_uint32),
+        ("strict_lengths", ctypes.c_int32),
     ]
 
 
@@ -660,9 +661,12 @@ def fl_kv_append(q, k, v, q_out, k_cache, v_cache, slots, *, rope: FlRopeTable |
 
 
 def make_chunk_desc(cu_q, kv_lens, block_table, max_kv_len: int, *, score_mod="none", softcap=20.0,
-                    causal=True, window=0, scale=0.0, error_word=None, wait_timeout_us=0) -> FlChunkDesc:
+                    causal=True, window=0, scale=0.0, error_word=None, wait_timeout_us=0,
+                    strict_lengths=False) -> FlChunkDesc:
     """Build an fl_chunk_desc; cu_q [B + 1], kv_lens [B] and block_table
-    [B, pages] (None: contiguous cache) are contiguous device int32 torch tensors."""
+    [B, pages] (None: contiguous cache) are contiguous device int32 torch tensors.
+    A loop whose lengths may outgrow ``max_kv_len`` sets ``strict_lengths``: without it they
+    are cut to it, which moves the request's rows to earlier keys, and error_word says nothing."""
     B = kv_lens.shape[0]
     dev = kv_lens.get_device()
     d = FlChunkDesc()
@@ -680,6 +684,7 @@ def make_chunk_desc(cu_q, kv_lens, block_table, max_kv_len: int, *, score_mod="n
         d.block_table_stride = block_table.shape[1]
     d.error_word = _error_word(error_word, dev)
     d.wait_timeout_us = int(wait_timeout_us)
+    d.strict_lengths = 1 if strict_lengths else 0
     d._device = dev
     d._keep = (cu_q, kv_lens, block_table, error_word)
     return d

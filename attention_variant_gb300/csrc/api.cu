@@ -2054,6 +2054,7 @@ fl_status fl_attn_chunk(const fl_tensor *q, const fl_tensor *k_cache, const fl_t
     for (p.few_shift = 4; (1 << p.few_shift) != few_box;)
         ++p.few_shift;
     p.max_kv = desc->max_kv_len;
+    p.strict = desc->strict_lengths ? 1 : 0;
     p.page_shift = -1;
     if (desc->block_table)
         for (p.page_shift = 4; (1 << p.page_shift) != pl.page;)

@@ -276,7 +276,7 @@ __device__ __forceinline__ void plan_entries(const ChunkParams &p, PlanShared &s
             t0 = __ldg(p.cu_q + b);
             int t1 = __ldg(p.cu_q + b + 1);
             L = __ldg(p.kv_lens + b);
-            if (t0 < 0 || t1 > p.T || t1 < t0)
+            if (t0 < 0 || t1 > p.T || t1 < t0 || L < 0 || (L > p.max_kv && p.strict))
                 err |= FL_DEVERR_LENGTHS;
             t0 = min(max(t0, 0), p.T);
             t1 = min(max(t1, t0), p.T);

@@ -312,6 +312,7 @@ struct ChunkParams {
     int few_tq;                // tokens of few rows: kFewRows / G
     int few_shift;             // log2 of the keys per TMA box of the few-row path
     int max_kv, page_shift;    // page_shift < 0: contiguous cache
+    int strict;                // lengths above max_kv are reported
     int64_t bt_stride;
     const int32_t *cu_q, *kv_lens, *block_table;
     int causal, window;        // window 0: none

@@ -133,7 +133,9 @@ typedef enum {
 /* Bits the kernel ORs into error_word. */
 #define FL_DEVERR_TIMEOUT 0x1u        /* a bounded wait ran out; the CTA quit cleanly */
 #define FL_DEVERR_PAGES 0x2u          /* fl_kv_plan: a new token got no page (slot -1) */
-#define FL_DEVERR_LENGTHS 0x4u        /* lengths on the device exceed what the host stated */
+#define FL_DEVERR_LENGTHS 0x4u        /* lengths on the device exceed what the host stated (fl_kv_plan's
+                                         tokens, fl_attn_chunk's offsets and, where asked for,
+                                         kv_lens) */
 #define FL_DEVERR_WHERE_SHIFT 8       /* bits 8..15: which wait (diagnostic) */
 
 typedef struct {
@@ -535,13 +537,16 @@ typedef struct {
     const int32_t *cu_q;        /* device int32 [B + 1], ascending, within 0 .. T (entries that are
                                    not are clamped, with FL_DEVERR_LENGTHS) */
     const int32_t *kv_lens;     /* device int32 [B]: cached keys, the new ones included */
-    int32_t max_kv_len;         /* host bound on kv_lens[], below 2^31 - 255; larger entries are clamped
-                                   to it */
+    int32_t max_kv_len;         /* host bound on kv_lens[], below 2^31 - 255; a larger entry counts as
+                                   this many keys, with the request's rows at the end of them */
     const int32_t *block_table; /* as in fl_decode_desc; NULL: contiguous cache */
     int32_t block_table_stride;
     uint32_t *error_word;       /* NULL, or a device word the kernel ORs FL_DEVERR_* into */
     uint32_t wait_timeout_us;   /* bound of every device-side wait, at least 1,000; 0 means
                                    2,000,000 */
+    int32_t strict_lengths;     /* 1: entries of kv_lens above max_kv_len set FL_DEVERR_LENGTHS; 0: they
+                                   are cut without a word, as fl_attn_decode does.  Entries below 0
+                                   count as 0 and set it either way */
 } fl_chunk_desc;
 /*
  * Layouts (bf16 except lse):

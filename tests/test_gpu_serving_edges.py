@@ -2,6 +2,7 @@
 are at the limits of what their documentation allows."""
 from __future__ import annotations
 
+import math
 import random
 
 import pytest
@@ -10,7 +11,7 @@ torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
 import attention_variant_gb300 as fa  # noqa: E402
-from tests.test_gpu_serving import _compare, _expected, _launch, _problem, _run_plan  # noqa: E402
+from tests.test_gpu_serving import _compare, _expected, _ints, _launch, _problem, _run_plan  # noqa: E402
 
 
 # ------------------------------------------------------------------ chunks
@@ -44,6 +45,36 @@ def test_chunk_windows_as_long_as_an_int_goes(D, window):
     for kw in (dict(window=window), dict()):
         got, = _launch(p, **kw)
         _compare(got, want, f"window {window}")
+
+
+def _error_of(p, kv_lens, max_kv, **kw):
+    err = _ints([0])
+    d = fa.make_chunk_desc(_ints(p["cu"]), _ints(kv_lens), p["table"].cuda(), max_kv, error_word=err, **kw)
+    q, kc, vc = (p[n].cuda() for n in ("q", "kc", "vc"))
+    ws = torch.empty(fa.fl_attn_chunk_workspace_size(q, kc, d), dtype=torch.uint8, device="cuda")
+    out, lse = torch.full_like(q, 7.0), torch.full((q.shape[1], q.shape[0]), 7.0, device="cuda")
+    fa.fl_attn_chunk(q, kc, vc, out, lse, d, ws)
+    torch.cuda.synchronize()
+    return int(err.item()), (out, lse)
+
+
+@pytest.mark.parametrize("n", [1, 40])
+def test_chunk_lengths_past_the_bound_are_reported(n):
+    # a request that outgrew max_kv_len: its rows are no longer where they were
+    # meant to be, and the caller can learn of it; the others are right
+    p = _problem([n, 3], [100, 60], 8, 2, 64, 16)
+    want, lse, tol = _expected(p)
+    for max_kv in (100, 99, 61):
+        err, got = _error_of(p, [100, 60], max_kv, strict_lengths=True)
+        assert err == (fa.FL_DEVERR_LENGTHS if max_kv < 100 else 0)
+        rows = slice(0 if max_kv == 100 else n, n + 3)
+        _compare((got[0][rows], got[1][:, rows]), (want[rows], lse[:, rows], tol[rows]), f"bound {max_kv}")
+    # lengths below 0 are never right
+    for strict in (False, True):
+        err, got = _error_of(p, [-5, 60], 100, strict_lengths=strict)
+        assert err == fa.FL_DEVERR_LENGTHS
+        assert not bool(got[0][:n].any()) and bool((got[1][:, :n] == -math.inf).all())
+        _compare((got[0][n:], got[1][:, n:]), (want[n:], lse[:, n:], tol[n:]), "beside a negative length")
 
 
 # ------------------------------------------------------------------ book-keeping

@@ -3,6 +3,8 @@ arguments (no GPU: every refusal comes before any CUDA call)."""
 from __future__ import annotations
 
 import ctypes
+import os
+import subprocess
 
 import pytest
 
@@ -31,3 +33,16 @@ def test_chunk_caches_that_an_int_cannot_count(lib):
         assert _chunk(lib, max_kv_len=n, block_table_stride=2 ** 31 - 1) == fa.FL_ERR_UNSUPPORTED
     # (taken up to the look for a GPU)
     assert _chunk(lib, max_kv_len=2 ** 31 - 256, block_table_stride=2 ** 31 - 1) == fa.FL_ERR_NO_DEVICE
+
+
+def test_chunk_desc_is_laid_out_as_in_c(lib, tmp_path):
+    src = tmp_path / "size.c"
+    src.write_text('#include <stddef.h>\n#include <stdio.h>\n#include "fl_attn.h"\n'
+                   'int main(void) { printf("%zu %zu %zu", sizeof(fl_chunk_desc), '
+                   'offsetof(fl_chunk_desc, wait_timeout_us), offsetof(fl_chunk_desc, strict_lengths)); return 0; }\n')
+    root = os.path.dirname(os.path.dirname(os.path.abspath(fa.__file__)))
+    exe = str(tmp_path / "size")
+    subprocess.run(["gcc", "-I", os.path.join(root, "include"), str(src), "-o", exe], check=True)
+    got = subprocess.run([exe], capture_output=True, text=True, check=True).stdout
+    d = fa.FlChunkDesc
+    assert got.split() == [str(n) for n in (ctypes.sizeof(d), d.wait_timeout_us.offset, d.strict_lengths.offset)]
