@@ -1756,9 +1756,10 @@ fl_status fl_rope_make_table(const fl_rope_config *config, fl_rope_table *table)
     fl_rope_table t{};
     t.rot_dim = c.rot_dim;
     t.layout = c.layout;
-    t.magnitude = static_cast<float>(c.magnitude != 0.0                  ? c.magnitude
-                                     : c.scaling == FL_ROPE_SCALE_RAMP ? 0.1 * std::log(c.factor) + 1.0
-                                                                        : 1.0);
+    t.magnitude = static_cast<float>(c.magnitude != 0.0 ? c.magnitude
+                                     : c.scaling == FL_ROPE_SCALE_RAMP && c.factor > 1.0
+                                         ? 0.1 * std::log(c.factor) + 1.0
+                                         : 1.0);
     for (int i = 0; i < c.rot_dim / 2; ++i) {
         double f = std::pow(base, -2.0 * i / c.rot_dim);
         double keep = 1.0; // share of the unscaled frequency

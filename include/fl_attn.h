@@ -405,7 +405,7 @@ fl_status fl_attn_decode_static(const fl_tensor *q, const fl_tensor *k_cache,
  *     RAMP    by the pair's index: the same blend, w falling linearly from 1
  *             at index floor(d(high)) to 0 at ceil(d(low)) (clamped to
  *             [0, rot_dim - 1]), d(n) = rot_dim ln(context / 2 pi n) / (2 ln base);
- *             m is 0.1 ln(factor) + 1 unless given
+ *             m is 0.1 ln(factor) + 1 for factors above 1 and 1 up to it, unless given
  * Angles are exact modulo a turn at any int32 position: f_i / 2 pi is kept as
  * a 64-bit fraction of a turn, so that pos times it wraps by itself.
  */

@@ -3,6 +3,7 @@ arguments (no GPU: every refusal comes before any CUDA call)."""
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import subprocess
 
@@ -46,3 +47,12 @@ def test_chunk_desc_is_laid_out_as_in_c(lib, tmp_path):
     got = subprocess.run([exe], capture_output=True, text=True, check=True).stdout
     d = fa.FlChunkDesc
     assert got.split() == [str(n) for n in (ctypes.sizeof(d), d.wait_timeout_us.offset, d.strict_lengths.offset)]
+
+
+@pytest.mark.parametrize("factor", [1.0, 0.5, 1e-3, 1e-6])
+def test_ramp_does_not_shrink_contexts_that_it_does_not_stretch(lib, factor):
+    # the default magnitude is 0.1 ln(factor) + 1 above 1, and 1 up to it
+    assert fa.make_rope_table(64, scaling="ramp", factor=factor).magnitude == 1.0
+    assert fa.make_rope_table(64, scaling="ramp", factor=factor, magnitude=1.25).magnitude == 1.25
+    up = fa.make_rope_table(64, scaling="ramp", factor=1.0 / factor).magnitude
+    assert up == pytest.approx(1.0 + 0.1 * math.log(1.0 / factor), rel=2.0 ** -24)
