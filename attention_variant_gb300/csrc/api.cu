@@ -1079,6 +1079,7 @@ bool in_place(const View &a, const View &b)
 // ------------------------------------------------------------------ chunks over a cache
 
 constexpr int32_t kChunkMaxKeys = INT32_MAX - 255;
+constexpr float kLog2e = 1.4426950408889634f;
 
 struct ChunkPlan {
     View Q, K, V;
@@ -1086,6 +1087,17 @@ struct ChunkPlan {
     int TQ, max_entries;
     size_t joins, entries, partials, total; // offsets in the workspace (the parts come first), its size
 };
+
+float chunk_scale(const ChunkPlan &pl, const fl_chunk_desc *d)
+{
+    return d->scale != 0.f ? d->scale : 1.0f / std::sqrt(float(pl.D));
+}
+
+// What a softcapped score is multiplied by to be the exponent x of tanh = 1 - 2 / (1 + 2^x).
+float chunk_softcap_in(const ChunkPlan &pl, const fl_chunk_desc *d)
+{
+    return 2.f * chunk_scale(pl, d) * kLog2e / d->softcap;
+}
 
 fl_status chunk_plan(const fl_tensor *q, const fl_tensor *k_cache, const fl_tensor *v_cache,
                      const fl_chunk_desc *d, ChunkPlan &pl)
@@ -1129,6 +1141,14 @@ fl_status chunk_plan(const fl_tensor *q, const fl_tensor *k_cache, const fl_tens
         return fail(FL_ERR_INVALID_ARG, "softcap must be positive and finite");
     if (!std::isfinite(d->scale) || d->scale < 0.f)
         return fail(FL_ERR_INVALID_ARG, "scale must be finite and positive (0 selects 1/sqrt(D))");
+    if (d->score_mod == FL_MOD_SOFTCAP) {
+        // cap (1 - 2 / (1 + 2^x)) is off by about 2^-22 cap whatever the score: past 2^14
+        // a weight would be off by more than its rounding to bf16
+        if (d->softcap > 16384.f)
+            return fail(FL_ERR_UNSUPPORTED, "softcap %g: chunks support up to 16384", double(d->softcap));
+        if (!std::isfinite(chunk_softcap_in(pl, d)))
+            return fail(FL_ERR_INVALID_ARG, "softcap %g is too small for the scale", double(d->softcap));
+    }
     if (!d->block_table) {
         if (pl.P != d->batch)
             return fail(FL_ERR_INVALID_ARG, "a contiguous cache is [batch, S_max, Hk, D]");
@@ -2067,12 +2087,10 @@ fl_status fl_attn_chunk(const fl_tensor *q, const fl_tensor *k_cache, const fl_t
     p.causal = desc->causal ? 1 : 0;
     p.window = desc->window;
     p.score_mod = desc->score_mod;
-    const float scale = desc->scale != 0.f ? desc->scale : 1.0f / std::sqrt(float(pl.D));
-    const float log2e = 1.4426950408889634f;
-    p.qk_log2 = scale * log2e;
+    p.qk_log2 = chunk_scale(pl, desc) * kLog2e;
     if (desc->score_mod == FL_MOD_SOFTCAP) {
-        p.softcap_in = 2.f * scale * log2e / desc->softcap;
-        p.softcap_out = desc->softcap * log2e;
+        p.softcap_in = chunk_softcap_in(pl, desc);
+        p.softcap_out = desc->softcap * kLog2e;
     }
     p.out = static_cast<__nv_bfloat16 *>(O.ptr);
     p.o_st = O.stride[0];

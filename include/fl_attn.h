@@ -529,7 +529,8 @@ fl_status fl_kv_append(const fl_tensor *q, const fl_tensor *k, const fl_tensor *
  */
 typedef struct {
     int32_t score_mod;          /* FL_MOD_NONE or FL_MOD_SOFTCAP */
-    float softcap;              /* FL_MOD_SOFTCAP: the cap (> 0) */
+    float softcap;              /* FL_MOD_SOFTCAP: the cap, > 0 and at most 16384; capped scores are off
+                                   by about 2^-22 cap */
     int32_t causal;             /* 1: as above; 0: every cached key */
     int32_t window;             /* 0: no window; else needs causal */
     float scale;                /* 0 means 1 / sqrt(D) */

@@ -77,6 +77,21 @@ def test_chunk_lengths_past_the_bound_are_reported(n):
         _compare((got[0][n:], got[1][:, n:]), (want[n:], lse[:, n:], tol[n:]), "beside a negative length")
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("cap", [0.25, 1000.0, 16384.0])
+def test_chunk_small_and_large_softcaps(D, cap):
+    p = _problem([50, 1, 3], [300, 400, 90], 8, 2, D, 32)
+    want, lse, tol = _expected(p, softcap=cap)
+    (o, l), = _launch(p, softcap=cap)
+    # cap (1 - 2 / (1 + 2^x)) in fp32: 2^x, the sum, the reciprocal and the last sum round at
+    # the size of 1, each at most 2^-22 (twice their sum allowed): a score is off by d, the
+    # LSE by as much, a weight by 2 d, and O by that times |v - O| <= 2 max |v|
+    d = 8 * 2.0 ** -22 * cap
+    v = max(x.float().abs().max().item() for x in p["v"])
+    assert ((o.double().cpu() - want).abs() <= tol + 4 * d * v).all()
+    assert (l.double().cpu() - lse).abs().max() <= 2e-4 + d
+
+
 # ------------------------------------------------------------------ book-keeping
 
 

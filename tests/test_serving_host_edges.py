@@ -56,3 +56,15 @@ def test_ramp_does_not_shrink_contexts_that_it_does_not_stretch(lib, factor):
     assert fa.make_rope_table(64, scaling="ramp", factor=factor, magnitude=1.25).magnitude == 1.25
     up = fa.make_rope_table(64, scaling="ramp", factor=1.0 / factor).magnitude
     assert up == pytest.approx(1.0 + 0.1 * math.log(1.0 / factor), rel=2.0 ** -24)
+
+
+@fake_addresses
+def test_chunk_softcaps_without_digits_left(lib):
+    mod = dict(score_mod=fa.FL_MOD_SOFTCAP)
+    for cap in (16385.0, 1e6, 1e30):  # rounding of cap tanh(z / cap) alone: 2^-8 and more of a weight
+        assert _chunk(lib, softcap=cap, **mod) == fa.FL_ERR_UNSUPPORTED
+    for kw in (dict(softcap=1e-40), dict(softcap=1e-3, scale=3e37)):  # 2 scale / cap is no float
+        assert _chunk(lib, **kw, **mod) == fa.FL_ERR_INVALID_ARG
+    for cap in (16384.0, 20.0, 1e-30):
+        assert _chunk(lib, softcap=cap, **mod) == fa.FL_ERR_NO_DEVICE
+    assert _chunk(lib, softcap=1e30) == fa.FL_ERR_NO_DEVICE  # not used
