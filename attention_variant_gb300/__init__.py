@@ -555,9 +555,13 @@ def _index(t, name: str, shape, dtype="int32", device=None) -> int:
 
 
 def _error_word(t, device: int):
-    if t is not None and t.get_device() != device:
+    if t is None:
+        return None
+    if t.get_device() != device:
         raise ValueError(f"error_word on {t.device}: the other tensors are on cuda:{device}")
-    return t.data_ptr() if t is not None else None
+    if t.numel() < 1 or t.element_size() < 4:
+        raise ValueError(f"error_word must hold 32 bits, is {tuple(t.shape)} of {t.dtype}")
+    return t.data_ptr()
 
 
 def _check_device(desc, device: int) -> None:

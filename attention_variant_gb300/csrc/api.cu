@@ -1955,6 +1955,8 @@ fl_status fl_kv_plan(const fl_kv_plan_desc *d, fl_stream_t stream)
     }
     if (reinterpret_cast<uintptr_t>(d->slots) % 8)
         return fail(FL_ERR_ALIGNMENT, "slots is not 8-byte aligned");
+    if (reinterpret_cast<uintptr_t>(d->error_word) % 4)
+        return fail(FL_ERR_ALIGNMENT, "error_word is not 4-byte aligned");
     // every block reads the lengths and the head while one of them writes the new ones
     const size_t lens = size_t(d->batch) * 4;
     if (overlap(d->kv_lens, lens, d->kv_lens_out, lens) || overlap(d->q_lens, lens, d->kv_lens_out, lens))
@@ -2026,6 +2028,8 @@ fl_status fl_attn_chunk(const fl_tensor *q, const fl_tensor *k_cache, const fl_t
         return fail(FL_ERR_INVALID_ARG, "cu_q or kv_lens is NULL");
     if (reinterpret_cast<uintptr_t>(desc->cu_q) % 4 || reinterpret_cast<uintptr_t>(desc->kv_lens) % 4)
         return fail(FL_ERR_ALIGNMENT, "cu_q or kv_lens is not 4-byte aligned");
+    if (reinterpret_cast<uintptr_t>(desc->error_word) % 4)
+        return fail(FL_ERR_ALIGNMENT, "error_word is not 4-byte aligned");
     if (!workspace)
         return fail(FL_ERR_INVALID_ARG, "workspace is NULL");
     if (reinterpret_cast<uintptr_t>(workspace) % kWsAlign)

@@ -13,7 +13,7 @@ import attention_variant_gb300 as fa
 from attention_variant_gb300 import build as fbuild
 
 torch = pytest.importorskip("torch")
-from tests.test_serving_host import _chunk_desc, _t, fake_addresses  # noqa: E402
+from tests.test_serving_host import _chunk_desc, _plan_desc, _t, fake_addresses  # noqa: E402
 
 
 @pytest.fixture(scope="module")
@@ -68,3 +68,23 @@ def test_chunk_softcaps_without_digits_left(lib):
     for cap in (16384.0, 20.0, 1e-30):
         assert _chunk(lib, softcap=cap, **mod) == fa.FL_ERR_NO_DEVICE
     assert _chunk(lib, softcap=1e30) == fa.FL_ERR_NO_DEVICE  # not used
+
+
+@fake_addresses
+def test_error_words_are_aligned(lib):
+    # the kernels OR into it: an odd address would be a fault
+    for at in (0xB001, 0xB002, 0xB003):
+        assert lib.fl_kv_plan(ctypes.byref(_plan_desc(error_word=at)), None) == fa.FL_ERR_ALIGNMENT
+        assert _chunk(lib, error_word=at) == fa.FL_ERR_ALIGNMENT
+    assert lib.fl_kv_plan(ctypes.byref(_plan_desc(error_word=0xB004)), None) == fa.FL_ERR_NO_DEVICE
+    assert _chunk(lib, error_word=0xB004) == fa.FL_ERR_NO_DEVICE
+
+
+def test_error_words_hold_32_bits(lib):
+    # (tensors of no GPU: the descs are built, not used)
+    cu, kv, table = (torch.zeros(s, dtype=torch.int32) for s in (2, 1, (1, 4)))
+    for word in (torch.zeros(1, dtype=torch.uint8), torch.zeros(1, dtype=torch.int16), torch.zeros(0, dtype=torch.int32)):
+        with pytest.raises(ValueError, match="error_word"):
+            fa.make_chunk_desc(cu, kv, table, 20, error_word=word)
+    for word in (torch.zeros(1, dtype=torch.int32), torch.zeros((), dtype=torch.int32), torch.zeros(2, dtype=torch.int64)):
+        assert fa.make_chunk_desc(cu, kv, table, 20, error_word=word).error_word == word.data_ptr()
