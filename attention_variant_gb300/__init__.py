@@ -706,13 +706,15 @@ def fl_attn_chunk_workspace_size(q, k_cache, desc: FlChunkDesc) -> int:
 def fl_attn_chunk(q, k_cache, v_cache, out, lse, desc: FlChunkDesc, workspace, stream=None) -> None:
     """Enqueue attention of ragged chunks of new tokens over the cache that
     holds them (see include/fl_attn.h); q and out are [T, Hq, D], lse [Hq, T]
-    or None, workspace a device torch tensor of at least
+    or None, workspace a contiguous device torch tensor of at least
     fl_attn_chunk_workspace_size bytes."""
     lib = load_library()
     dev = _device()
     _check_device(desc, dev)
     if workspace.get_device() != dev:
         raise ValueError(f"workspace on {workspace.device}: the current device is cuda:{dev}")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
     _check(lib.fl_attn_chunk(_pack(q, dev), _pack(k_cache, dev), _pack(v_cache, dev), _pack(out, dev),
                              _pack(lse, dev), ctypes.byref(desc), workspace.data_ptr(),
                              workspace.numel() * workspace.element_size(), _stream_of(stream, dev)))

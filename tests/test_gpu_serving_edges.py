@@ -92,6 +92,25 @@ def test_chunk_small_and_large_softcaps(D, cap):
     assert (l.double().cpu() - lse).abs().max() <= 2e-4 + d
 
 
+def test_chunk_workspaces_that_are_not_one_piece():
+    # as many elements as are needed, but not as many bytes behind the address
+    p = _problem([2], [20], 8, 2, 64, 16)
+    q, kc, vc = (p[n].cuda() for n in ("q", "kc", "vc"))
+    d = fa.make_chunk_desc(_ints(p["cu"]), _ints([20]), p["table"].cuda(), 20)
+    n = fa.fl_attn_chunk_workspace_size(q, kc, d)
+    out = torch.full_like(q, 7.0)
+    for ws in (torch.empty(1, dtype=torch.uint8, device="cuda").expand(n),
+               torch.empty(2 * n, dtype=torch.uint8, device="cuda")[::2],
+               torch.empty((64, n), dtype=torch.uint8, device="cuda").t()):
+        with pytest.raises(ValueError, match="workspace"):
+            fa.fl_attn_chunk(q, kc, vc, out, None, d, ws)
+    assert bool((out == 7).all())
+    ws = torch.empty((2, n // 8 + 1), dtype=torch.float32, device="cuda")
+    fa.fl_attn_chunk(q, kc, vc, out, None, d, ws)
+    torch.cuda.synchronize()
+    _compare((out, None), _expected(p), "workspace of floats")
+
+
 # ------------------------------------------------------------------ book-keeping
 
 
