@@ -1929,6 +1929,8 @@ fl_status fl_kv_plan(const fl_kv_plan_desc *d, fl_stream_t stream)
         return fail(FL_ERR_INVALID_ARG, "batch must be >= 1");
     if (d->max_tokens < 0 || d->n_free < 0 || d->block_table_stride < 1)
         return fail(FL_ERR_INVALID_ARG, "max_tokens and n_free must be >= 0, block_table_stride >= 1");
+    if (d->max_tokens > INT32_MAX - 1023) // a block's 1024 token numbers are ints
+        return fail(FL_ERR_UNSUPPORTED, "max_tokens %d exceeds %d", d->max_tokens, INT32_MAX - 1023);
     int shift = 4;
     while (shift < 8 && (1 << shift) != d->page_size)
         ++shift;

@@ -476,7 +476,7 @@ fl_status fl_rope(const fl_tensor *q, const fl_tensor *k, const fl_tensor *q_out
 typedef struct {
     int32_t batch;              /* B >= 1 requests */
     int32_t page_size;          /* 16, 32, 64, 128 or 256 keys */
-    int32_t max_tokens;         /* entries of positions and slots (0: none wanted) */
+    int32_t max_tokens;         /* entries of positions and slots (0: none wanted), at most 2^31 - 1024 */
     int32_t n_free;             /* entries of free_pages */
     int32_t block_table_stride; /* entries per row of block_table */
     const int32_t *q_lens;      /* [B] */

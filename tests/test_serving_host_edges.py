@@ -88,3 +88,11 @@ def test_error_words_hold_32_bits(lib):
             fa.make_chunk_desc(cu, kv, table, 20, error_word=word)
     for word in (torch.zeros(1, dtype=torch.int32), torch.zeros((), dtype=torch.int32), torch.zeros(2, dtype=torch.int64)):
         assert fa.make_chunk_desc(cu, kv, table, 20, error_word=word).error_word == word.data_ptr()
+
+
+@fake_addresses
+def test_plan_lists_that_an_int_cannot_count(lib):
+    # the threads' token numbers run to the end of the last block of 1024
+    for n in (2 ** 31 - 1, 2 ** 31 - 1023):
+        assert lib.fl_kv_plan(ctypes.byref(_plan_desc(max_tokens=n)), None) == fa.FL_ERR_UNSUPPORTED
+    assert lib.fl_kv_plan(ctypes.byref(_plan_desc(max_tokens=2 ** 31 - 1024)), None) == fa.FL_ERR_NO_DEVICE
