@@ -5,6 +5,7 @@
 // device state.  The library allocates no device memory: TMA descriptors are
 // passed to the kernel as __grid_constant__ parameters.
 #include <algorithm>
+#include <atomic>
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
@@ -1085,7 +1086,7 @@ struct ChunkPlan {
     View Q, K, V;
     int64_t T, Hq, Hk, D, P, page;
     int TQ, max_entries;
-    size_t joins, entries, partials, total; // offsets in the workspace (the parts come first), its size
+    size_t joins, entries, partials, seen, total; // offsets in the workspace (the parts come first), its size
 };
 
 float chunk_scale(const ChunkPlan &pl, const fl_chunk_desc *d)
@@ -1174,7 +1175,8 @@ fl_status chunk_plan(const fl_tensor *q, const fl_tensor *k_cache, const fl_tens
     pl.joins = align_up(2 * fl::kChunkMaxCtas * sizeof(fl::ChunkPart));
     pl.entries = pl.joins + align_up(fl::kChunkMaxCtas * sizeof(fl::ChunkJoin));
     pl.partials = pl.entries + align_up(2 * size_t(entries) * sizeof(fl::ChunkEntry));
-    pl.total = pl.partials + align_up(size_t(fl::kChunkMaxCtas) * 4 * size_t(pl.D + 4) * 128 * sizeof(float));
+    pl.seen = pl.partials + align_up(size_t(fl::kChunkMaxCtas) * 4 * size_t(pl.D + 4) * 128 * sizeof(float));
+    pl.total = pl.seen + align_up(sizeof(uint64_t));
     return FL_OK;
 }
 
@@ -2126,6 +2128,11 @@ fl_status fl_attn_chunk(const fl_tensor *q, const fl_tensor *k_cache, const fl_t
     p.joins = reinterpret_cast<fl::ChunkJoin *>(ws + pl.joins);
     p.entries = reinterpret_cast<fl::ChunkEntry *>(ws + pl.entries);
     p.partials = reinterpret_cast<float *>(ws + pl.partials);
+    // a mark that no other call has and no other data is likely to hold (the odd
+    // factor takes the numbers one to one over all 64 bits)
+    static std::atomic<uint64_t> calls{0};
+    p.seen = reinterpret_cast<uint64_t *>(ws + pl.seen);
+    p.seen_mark = ++calls * 0x9e3779b97f4a7c15ull;
     p.err_user = desc->error_word;
     // a millisecond at least: a wait that gives up sooner could leave a copy on its way
     p.timeout_ns = std::max<uint64_t>(desc->wait_timeout_us ? desc->wait_timeout_us : 2000000u, 1000u) * 1000ull;

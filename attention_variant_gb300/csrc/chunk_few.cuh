@@ -909,6 +909,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     cx.tmem = sm->tmem_base;
     cx.wc = wait_ctl(p, &sm->abort_flag);
     if (warp >= 4) {
+        tell_second(p, cx.part);
         few_softmax<MOD, D>(cx, p, (warp >> 2) - 1);
         ptx::tc_fence_before();
         ptx::named_barrier_sync(1, kThreads);

@@ -97,8 +97,11 @@ __device__ __forceinline__ T load_plan(const T *src)
 
 // The kernels of the two paths.  The first one's CTAs start beside the planning
 // kernel: they set up and then wait for the plan.  The second one is launched
-// when every CTA of the first has seen the plan, so it reads it without a
-// wait; its CTAs take the SMs as those without work leave them.  Both end with a
+// when every CTA of the first has seen the plan.  That it sees it, too, follows
+// from a word that a thread of the first releases and all of its own acquire;
+// should it not come soon, they wait for the first kernel's end.  (The release is
+// a softmax thread's, which has nothing to do yet: from the producer it cost 1 us.)
+// Its CTAs take the SMs as those without work leave them.  Both end with a
 // wait for the one before: the second stands for the first to what follows, and
 // a CTA of the first that gave up early is not gone before the plan is there.  (One kernel for both: the path
 // laid out second started 6 to 9 us late, its instructions fetched from
@@ -122,10 +125,25 @@ __device__ __forceinline__ bool idle_second(const ChunkParams &p, int kind, int 
     if (!p.second)
         return false;
     ptx::launch_dependents();
+    int tries = 32; // 20 us
+    while (ptx::load_acquire(p.seen) != p.seen_mark && --tries)
+        ;
+    if (!tries)
+        ptx::wait_dependency();
     if (__ldcg(&p.parts[kind * p.n_cta + part].parts))
         return false;
     ptx::wait_dependency();
     return true;
+}
+
+// The word of the first kernel for the second.  The softmax warps.
+__device__ __forceinline__ void tell_second(const ChunkParams &p, int part)
+{
+    if (!p.second && p.seen_mark && part == 0 && threadIdx.x == kThreads - 1) {
+        ptx::wait_dependency();
+        ptx::store_release(p.seen, p.seen_mark);
+    }
+    __syncwarp();
 }
 
 // The CTA's part, which begins at tile k of item h of entry e.  A warp.
@@ -561,6 +579,8 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const __grid_c
 {
     ptx::wait_dependency();
     const int cta = blockIdx.x, slot = blockIdx.y, z = blockIdx.z;
+    if (cta + slot + z == 0 && threadIdx.x == 0)
+        *p.seen = 0; // a replay of this call has the same mark
     const ChunkJoin jn = p.joins[cta];
     if (jn.n_parts < 2)
         return;

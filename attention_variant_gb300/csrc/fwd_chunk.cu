@@ -859,6 +859,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // runs under both register limits
     if (warp >= 4) {
         ptx::setmaxnreg_inc<kRegsSoftmax>();
+        tell_second(p, cx.part);
         softmax_role<MOD, D>(cx, p, (warp >> 2) - 1);
         ptx::tc_fence_before();
         ptx::named_barrier_sync(1, kThreads);
@@ -948,6 +949,8 @@ cudaError_t launch_mod(const ChunkMaps &maps, ChunkParams &p, cudaStream_t strea
     // likelier one is first.
     const bool few = p.G <= kFewRows, blocks = !few || p.T > p.few_tq;
     const bool few_first = few && (!blocks || p.T <= static_cast<int64_t>(p.batch) * p.few_tq);
+    if (!few || !blocks)
+        p.seen_mark = 0;
     // the warm-up pays where the loads queue up: more keys than all rings hold
     p.warm = few_first && static_cast<double>(p.batch) * p.max_kv * p.Hk >
                               static_cast<double>(p.n_cta) * FewCfg<D>::kStages * FewCfg<D>::kBN;

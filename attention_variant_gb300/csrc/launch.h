@@ -328,6 +328,8 @@ struct ChunkParams {
     int cost_pair, cost_single, cost_few, cost_item, cost_few_item, cost_least; // see api.cu
     int max_entries;
     int second;                // the other path's kernel comes first (chunk_plan.cuh)
+    uint64_t *seen;            // holds seen_mark once that one has seen the plan
+    uint64_t seen_mark;        // this call's; 0: one path alone
     int warm;                  // few rows: run a tile of no keys first
     ChunkPart *parts;          // the workspace: [2][n_cta], row blocks and few rows
     ChunkJoin *joins;          // [n_cta]

@@ -111,6 +111,50 @@ def test_chunk_workspaces_that_are_not_one_piece():
     _compare((out, None), _expected(p), "workspace of floats")
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("T,first", [(60, "blocks"), (12, "few")])
+def test_chunk_replays_follow_the_lengths(T, first, D):
+    # one captured call with work of both kinds, whose requests change from replay to
+    # replay: each has a plan of its own, in the workspace that held the last one's
+    rng = random.Random(T)
+    B = 4 if first == "blocks" else 8
+    page, Hq, Hk, width = 16, 8, 1, 64
+    fixed = dict(cu=_ints([0] * (B + 1)), kv=_ints([1] * B), table=_ints([[0] * width] * B))
+    q = torch.zeros((T, Hq, D), dtype=torch.bfloat16, device="cuda")
+    kc, vc = (torch.zeros((B * width + 2, page, Hk, D), dtype=torch.bfloat16, device="cuda") for _ in "kv")
+    out, lse = torch.empty_like(q), torch.empty((Hq, T), device="cuda")
+    err = _ints([0])
+    d = fa.make_chunk_desc(fixed["cu"], fixed["kv"], fixed["table"], 900, error_word=err)
+    n = fa.fl_attn_chunk_workspace_size(q, kc, d)
+    ws = torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda")
+    fa.fl_attn_chunk(q, kc, vc, out, lse, d, ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        fa.fl_attn_chunk(q, kc, vc, out, lse, d, ws)
+    for i in range(8):
+        q_lens = [rng.randrange(0, 2) for _ in range(B - 1)]
+        q_lens.insert(rng.randrange(B), T - sum(q_lens) - 3)
+        kv_lens = [m + rng.randrange(0, 800) for m in q_lens]
+        p = _problem(q_lens, kv_lens, Hq, Hk, D, page, seed=i)
+        m = sum(q_lens)
+        q[:m].copy_(p["q"])
+        for dst, src in ((kc, p["kc"]), (vc, p["vc"])):
+            dst[: src.shape[0]].copy_(src)
+        fixed["cu"].copy_(torch.tensor(p["cu"], dtype=torch.int32))
+        fixed["kv"].copy_(torch.tensor(kv_lens, dtype=torch.int32))
+        fixed["table"][:, : p["table"].shape[1]].copy_(p["table"])
+        want = _expected(p)
+        for _ in range(3):
+            out.fill_(7.0)
+            lse.fill_(7.0)
+            graph.replay()
+            torch.cuda.synchronize()
+            _compare((out[:m], lse[:, :m]), want, f"replay {i} q {q_lens} kv {kv_lens}")
+            assert bool((out[m:] == 7).all()) and bool((lse[:, m:] == 7).all())
+    assert int(err.item()) == 0
+
+
 # ------------------------------------------------------------------ book-keeping
 
 
