@@ -155,6 +155,42 @@ def test_chunk_replays_follow_the_lengths(T, first, D):
     assert int(err.item()) == 0
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n,Hq", [(2, 1), (2, 4), (1, 8), (4, 4), (1, 16)])
+@pytest.mark.parametrize("L", [4, 5, 7])
+def test_chunk_few_rows_keep_both_terms_of_p(n, Hq, D, L):
+    # values that cancel: O is what the weights differ by, which one bf16 per
+    # weight does not hold
+    q, k, v = torch.zeros(n, Hq, D), torch.zeros(L, 1, D), torch.zeros(L, 1, D)
+    q[..., :2] = torch.tensor([1.0, 1.5, 0.75, 2.0])[torch.arange(n * Hq) % 4].view(n, Hq, 1)
+    k[:, 0, 0], k[:, 0, 1] = -1.25, torch.tensor([(5 * j % 7 - 3) * 2.0 ** -9 for j in range(L)])
+    v[:, 0] = torch.tensor([1.0, -1.0, -1.0, 1.0, 0.0, 1.0, -1.0])[:L, None]
+    p = _problem([n], [L], Hq, 1, D, 16, causal=False)
+    for name, x in (("q", q), ("k", k), ("v", v)):
+        x = x.to(torch.bfloat16)
+        if name == "q":
+            p["q"] = x
+            continue
+        p[name][0] = x
+        p[name + "c"][int(p["table"][0, 0]), :L] = x
+    want, lse, _ = _expected(p, causal=False, scale=1.0)
+    z = q[..., :1].double() * k[:, 0].double().sum(-1)  # [n, Hq, L]
+    w = torch.exp(z)
+
+    def out_of(weights):  # of what the kernel multiplies V by; the sum is of w itself
+        return (weights @ v[:, 0, 0].double() / w.sum(-1))[..., None].expand(n, Hq, D)
+
+    first = w.float().to(torch.bfloat16).double()
+    rest = w - first
+    assert (out_of(w) - want).abs().max() < 1e-12
+    # the second term's own rounding (2^-8 of it), the output's (2^-8), and 2^x, the sums and
+    # the reciprocal in fp32: 2^-22 of weights that sum to 1, four times
+    tol = 2.0 ** -8 * (rest.abs().sum(-1) / w.sum(-1)).max() + 2.0 ** -8 * want.abs() + 4 * 2.0 ** -22
+    assert (out_of(first) - want).abs().max() > 8 * tol.max()  # the first term alone
+    (o, _), = _launch(p, causal=False, scale=1.0)
+    assert ((o.double().cpu() - want).abs() <= tol).all()
+
+
 # ------------------------------------------------------------------ book-keeping
 
 
