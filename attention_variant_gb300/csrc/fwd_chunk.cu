@@ -660,7 +660,9 @@ __device__ void softmax_role(const KernelCtx<D> &cx, const ChunkParams &p, int t
         const int n_mine = inf.hi[t] > first ? (inf.hi[t] - first + step - 1) / step : 0;
         const bool active = 32 * wq < inf.rows[t]; // warp-uniform
         const bool take_turns = kTurns && inf.pair;
-        RowState st{kNegInf, 0.f, 0.f};
+        // rows past the item's (other requests', or whatever Q's buffer held) start with a
+        // reference that nothing exceeds: they have no say in when the warp rescales
+        RowState st{r < inf.rows[t] ? kNegInf : -kNegInf, 0.f, 0.f};
         if (take_turns) // turns of tiles before this slot's
             for (int j = n_mine ? first - inf.u_lo : inf.u_hi - inf.u_lo; j > 0; --j, ++turns) {
                 if (!turn_wait())
@@ -695,9 +697,9 @@ __device__ void softmax_role(const KernelCtx<D> &cx, const ChunkParams &p, int t
                 uint32_t pk[kBN / 2];
                 bool rescale;
                 const float alpha =
-                    C::kOnes ? softmax_compute_p_exact_sum<kBN>(x, MOD == MOD_NONE ? p.qk_log2 : 1.f, st, kk == 0,
+                    C::kOnes ? softmax_compute_p_exact_sum<kBN>(x, MOD == MOD_NONE ? p.qk_log2 : 1.f, st, false,
                                                                 pk, rescale)
-                             : softmax_compute_p<kBN>(x, MOD == MOD_NONE ? p.qk_log2 : 1.f, st, kk == 0, pk,
+                             : softmax_compute_p<kBN>(x, MOD == MOD_NONE ? p.qk_log2 : 1.f, st, false, pk,
                                                       rescale);
                 if (take_turns) {
                     ptx::mbar_arrive(b_turn_other); // hand the turn over

@@ -191,6 +191,32 @@ def test_chunk_few_rows_keep_both_terms_of_p(n, Hq, D, L):
     assert ((o.double().cpu() - want).abs() <= tol).all()
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("softcap", [0.0, 20.0])
+@pytest.mark.parametrize("Hq,Hk", [(14, 2), (40, 1), (6, 2), (8, 2), (5, 1)])
+def test_chunk_rows_depend_on_their_own_request(Hq, Hk, D, softcap):
+    # groups that do not fill the 128 rows of a block, and blocks that end inside it:
+    # what else lies there (rows of loud neighbours, what Q's buffers held before) must
+    # not reach a row's bits, not even by the moment at which a warp rescales
+    q_lens, kv_lens = [45, 150, 1, 45, 2, 70], [600, 700, 800, 500, 300, 70]
+    quiet = _problem(q_lens, kv_lens, Hq, Hk, D, 32, seed=1)
+    others = [0, 2, 4, 5]  # the neighbours; 1 and 3 stay
+    kw = dict(softcap=softcap)
+    want = _expected(quiet, **kw)
+    (o0, l0), = _launch(quiet, **kw)
+    _compare((o0, l0), want, "quiet")
+    for loud in (30.0, 1e4):
+        p = dict(quiet, q=quiet["q"].clone())
+        for b in others:
+            p["q"][p["cu"][b]: p["cu"][b + 1]] *= loud
+        for o, l in _launch(p, calls=3, **kw):
+            for b in (1, 3):
+                rows = slice(p["cu"][b], p["cu"][b + 1])
+                assert torch.equal(o[rows], o0[rows]) and torch.equal(l[:, rows], l0[:, rows])
+    for o, l in _launch(quiet, calls=3, **kw):  # after the loud ones
+        assert torch.equal(o, o0) and torch.equal(l, l0)
+
+
 # ------------------------------------------------------------------ book-keeping
 
 
