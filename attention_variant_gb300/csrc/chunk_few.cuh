@@ -29,7 +29,7 @@
 // fp32 sums of 2^60 such weights in range, and what lies 2^-66 below a row's
 // largest weight does not reach its bf16 output or its LSE.
 //
-// 64 requests of 8192 keys take 174 us, 0.91 of the rate of a plain copy; what
+// 64 requests of 8192 keys take 174 to 178 us, 0.9 of the rate of a plain copy; what
 // shorter ones pay more is the plan (6 us until it is seen), the first loads
 // (5 us), the uneven end (5 us) and the joins (5 us).
 //

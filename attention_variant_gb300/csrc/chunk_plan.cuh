@@ -103,9 +103,9 @@ __device__ __forceinline__ T load_plan(const T *src)
 // a softmax thread's, which has nothing to do yet: from the producer it cost 1 us.)
 // Its CTAs take the SMs as those without work leave them.  Both end with a
 // wait for the one before: the second stands for the first to what follows, and
-// a CTA of the first that gave up early is not gone before the plan is there.  (One kernel for both: the path
-// laid out second started 6 to 9 us late, its instructions fetched from
-// memory.)
+// a CTA of the first that gave up early is not gone before the plan is there.
+// (One kernel for both: the path laid out second started 6 to 9 us late, its
+// instructions fetched from memory.)
 
 // A CTA's place among its kernel's parts.  CTAs go to SMs in order, two by two,
 // but for the first one, whose neighbour is the SM that the planning kernel

@@ -42,10 +42,11 @@
 // are replaced by -inf, and as 0 * NaN is not 0, the S warp zeroes those rows
 // of V in shared memory (only in tiles at the ends of the cache or window).
 //
-// Bound by the exponentials and the instructions around them: the last 4096
-// tokens of 16384, 32 heads over 8 of 64, take 470 us, 1020 TFLOP/s, with the
-// tensor pipe 49% active, special functions 45% and 56% of the issue slots
-// used; D = 128 reaches 1.05 us a pair of blocks and tile, 1220 TFLOP/s.  An
+// Bound by no one pipe but by the chain of dependent instructions in each of
+// the two softmax warps a scheduler has: the last 4096 tokens of 16384, 32 heads
+// over 8 of 64, take 457 us, 1050 TFLOP/s, with the tensor pipe 50% active,
+// special functions 44% and 56% of the issue slots used; 16 heads over 2 of 128
+// 410 us, 1170 TFLOP/s (1.05 us a pair of blocks and tile).  An
 // item costs 2 to 3 us more (its last product, O out of TMEM, its rows to
 // memory), which is what short windows and chunks pay.
 #include <cuda_bf16.h>
@@ -602,10 +603,11 @@ __device__ __forceinline__ void write_joined(const ChunkParams &p, const Item &i
 // to a reciprocal: 1 / a = b c d / (a b c d), with the exponent held to 30, where
 // tanh is 1 to the last bit and four factors stay in range.  (NaN stays NaN and
 // spreads to the other three, so keys that no row sees are zeroed, as V is.)
-// Special functions bound the softcap, and this takes 2.25 a score with the
-// softmax's own in place of 3 (2048 tokens on 8192 keys, 32 heads over 8 of 64:
-// 265 -> 236 us; 16 over 2 of 128: 179 -> 161; two scores to a reciprocal: 248,
-// 164).
+// This takes 2.25 special functions a score with the softmax's own in place of 3
+// (2048 tokens on 8192 keys, 32 heads over 8 of 64: 265 -> 236 us; 16 over 2 of
+// 128: 179 -> 157; two scores to a reciprocal: 248, 164).  They are not the bound:
+// the busiest SM of a mixed step uses that pipe 66% of its time; the 112 capped
+// scores of a row at D = 64 are held until their maximum is known, and spill.
 template <int N>
 __device__ __forceinline__ void softcap_scores(float (&x)[N], float in, float out)
 {

@@ -4,9 +4,9 @@
 //   y_a = m (x_a cos t - x_b sin t),  y_b = m (x_a sin t + x_b cos t),  t = pos f_i
 //
 // The angle: f_i / 2 pi is held as a 64-bit fraction of a turn, so pos times
-// it, in 64-bit integers, is the angle modulo a turn with no reduction and no
-// error that grows with the position (a 32-bit float angle is off by 0.06 rad
-// at position 10^6).  The nearest quarter turn is taken off in integers too;
+// it, in 64-bit integers, is the angle modulo a turn with no reduction, and all
+// that grows with the position is the frequency's own error, a few 2^-53 of it
+// (a 32-bit float angle is off by 0.06 rad at position 10^6).  The nearest quarter turn is taken off in integers too;
 // the remainder, in [-1/8, 1/8] turn, goes to sincospif.
 //
 // Bound by HBM: every element is read and written once.  A block takes `tile`

@@ -406,8 +406,10 @@ fl_status fl_attn_decode_static(const fl_tensor *q, const fl_tensor *k_cache,
  *             at index floor(d(high)) to 0 at ceil(d(low)) (clamped to
  *             [0, rot_dim - 1]), d(n) = rot_dim ln(context / 2 pi n) / (2 ln base);
  *             m is 0.1 ln(factor) + 1 for factors above 1 and 1 up to it, unless given
- * Angles are exact modulo a turn at any int32 position: f_i / 2 pi is kept as
- * a 64-bit fraction of a turn, so that pos times it wraps by itself.
+ * f_i / 2 pi is kept as a 64-bit fraction of a turn, so that pos times it wraps
+ * by itself: the reduction modulo a turn is exact at any int32 position.  What
+ * grows with the position is the frequency's own error, a few 2^-53 of it (about
+ * 10^-6 rad at 2^31).
  */
 typedef enum { FL_ROPE_HALF = 0, FL_ROPE_INTERLEAVED = 1 } fl_rope_layout;
 typedef enum {
@@ -455,9 +457,10 @@ typedef struct {
  * fl_rope -- rotary positions of q and, unless NULL, k in one launch.
  *   q, q_out [B, S, Hq, D], k, k_out [B, S, Hk, D], or [T, Hq, D] and
  *   [T, Hk, D] (rows of any batch one after another); bf16 or fp32, all the
- *   same; rot_dim <= D.  An output may be its input (same pointer and
- *   strides); other overlaps are undefined.  Arithmetic is fp32 on the fp32
- *   sine and cosine, rounded once.
+ *   same; rot_dim <= D.  Strides of bf16 tensors are multiples of 16 bytes,
+ *   those of fp32 ones anything; the innermost is 1.  At least one token.  An
+ *   output may be its input (same pointer and strides); other overlaps are
+ *   undefined.  Arithmetic is fp32 on the fp32 sine and cosine, rounded once.
  */
 fl_status fl_rope(const fl_tensor *q, const fl_tensor *k, const fl_tensor *q_out,
                   const fl_tensor *k_out, const fl_rope_desc *desc, fl_stream_t stream);
@@ -505,7 +508,7 @@ fl_status fl_kv_plan(const fl_kv_plan_desc *desc, fl_stream_t stream);
 /*
  * fl_kv_append -- writes the new keys and values to their slots of a paged
  * cache, rotating q and k on the way.
- *   q, q_out  [T, Hq, D] or both NULL; k, v [T, Hk, D]; bf16
+ *   q, q_out  [T, Hq, D] or both NULL; k, v [T, Hk, D]; bf16, T >= 1
  *   k_cache, v_cache [num_pages, page_size, Hk, D]; any page_size
  *   slots     device int64 [T] (fl_kv_plan's): row slots[t] % page_size of page
  *             slots[t] / page_size; a token whose slot is outside
@@ -551,7 +554,7 @@ typedef struct {
 } fl_chunk_desc;
 /*
  * Layouts (bf16 except lse):
- *   q, out    [T, Hq, D], D = 64 or 128, Hq a multiple of Hk, Hq / Hk <= 128
+ *   q, out    [T, Hq, D], T >= 1, D = 64 or 128, Hq a multiple of Hk, Hq / Hk <= 128
  *   k_cache, v_cache
  *             paged: [num_pages, page_size, Hk, D], page_size in {16, 32, 64, 128, 256};
  *             contiguous (block_table NULL): [B, S_max, Hk, D], S_max >= max_kv_len
@@ -560,12 +563,17 @@ typedef struct {
  * read into a result nor written.  A row that sees no key gives O = 0, LSE = -inf.  Keys and values
  * that no row of their request sees (rows kv_lens[b] and later of the last
  * page, keys the window has left) may hold anything; the others must be
- * finite, also where the mask hides them from some rows.
+ * finite, also where the mask hides them from some rows.  Requests of at most 16
+ * rows a KV head sum weights between 2^-60 and 2^60 times values, in fp32:
+ * values above 2^37 in size may overflow there, and below 2^-60 vanish.
  * Page indices outside the cache read as zero keys and values.
  * `workspace`, as for fl_attn_decode, holds the call's plan and the partial
  * results of rows whose keys were split over several SMs; they are joined in
- * a fixed order, so that results do not depend on scheduling.
+ * a fixed order, so that results do not depend on scheduling: a row's bits follow
+ * from its own request's data and the lengths of all.
  * Calls sharing one workspace must not overlap on the GPU.
+ * For steps of nothing but single tokens over short caches at D = 64
+ * fl_attn_decode is faster (it needs no plan); for long ones they are even.
  */
 fl_status fl_attn_chunk_workspace_size(const fl_tensor *q, const fl_tensor *k_cache,
                                        const fl_chunk_desc *desc, size_t *bytes);
