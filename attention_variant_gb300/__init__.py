@@ -9,7 +9,8 @@ The names mirror the C ABI: :func:`fl_attn_fwd`, :func:`fl_attn_tile_shape`,
 :func:`fl_attn_version`, :func:`fl_attn_decode_workspace_size`,
 :func:`fl_attn_decode`, :func:`fl_attn_decode_static`, :func:`fl_attn_bwd`,
 :func:`fl_attn_diff_bwd`, and for rotary positions and serving steps
-:func:`fl_rope`, :func:`fl_kv_plan`, :func:`fl_kv_append`, :func:`fl_attn_chunk`.
+:func:`fl_rope`, :func:`fl_kv_plan`, :func:`fl_kv_append`, :func:`fl_attn_chunk`, and for a
+cache in 8 bits :func:`fl_kv_append_fp8`, :func:`fl_kv_read_fp8`, :func:`fl_attn_chunk_fp8`.
 Tensors are torch tensors on the current CUDA device
 (PyTorch provides device memory and streams; nothing else).
 """
@@ -33,6 +34,7 @@ FL_ERR_NO_DEVICE = 6
 # fl_dtype
 FL_BF16 = 0
 FL_F32 = 1
+FL_E4M3 = 2
 # fl_kind
 FL_KIND_STANDARD = 0
 FL_KIND_DIFF = 1
@@ -214,6 +216,15 @@ def load_library(path: str = LIB_PATH):
     lib.fl_attn_chunk.restype = ctypes.c_int
     lib.fl_attn_chunk.argtypes = [B] * 5 + [P(FlChunkDesc), ctypes.c_void_p, ctypes.c_size_t,
                                             ctypes.c_void_p]
+    lib.fl_kv_append_fp8.restype = ctypes.c_int
+    lib.fl_kv_append_fp8.argtypes = [B] * 8 + [ctypes.c_void_p, B, ctypes.c_void_p]
+    lib.fl_kv_read_fp8.restype = ctypes.c_int
+    lib.fl_kv_read_fp8.argtypes = [B] * 4 + [ctypes.c_void_p, B, B, ctypes.c_void_p]
+    lib.fl_attn_chunk_fp8_workspace_size.restype = ctypes.c_int
+    lib.fl_attn_chunk_fp8_workspace_size.argtypes = [B, B, P(FlChunkDesc), P(ctypes.c_size_t)]
+    lib.fl_attn_chunk_fp8.restype = ctypes.c_int
+    lib.fl_attn_chunk_fp8.argtypes = [B] * 7 + [P(FlChunkDesc), ctypes.c_void_p, ctypes.c_size_t,
+                                                ctypes.c_void_p]
     _lib = lib
     return lib
 
@@ -491,7 +502,7 @@ class _Torch:
 
     def __init__(self):
         import torch
-        self.codes = {torch.bfloat16: FL_BF16, torch.float32: FL_F32}
+        self.codes = {torch.bfloat16: FL_BF16, torch.float32: FL_F32, torch.float8_e4m3fn: FL_E4M3}
         self.types = {"int32": torch.int32, "int64": torch.int64}
         self.int32, self.int64 = torch.int32, torch.int64
         self.device = torch.cuda.current_device
@@ -664,6 +675,34 @@ def fl_kv_append(q, k, v, q_out, k_cache, v_cache, slots, *, rope: FlRopeTable |
                             _stream_of(stream, dev)))
 
 
+def fl_kv_append_fp8(q, k, v, q_out, k_cache, v_cache, k_scale, v_scale, slots, *, rope: FlRopeTable | None = None,
+                     positions=None, stream=None) -> None:
+    """:func:`fl_kv_append` into a cache of torch.float8_e4m3fn codes with fp32 scales
+    [num_pages, page_size / block, Hk], which grow as they have to (see include/fl_attn.h)."""
+    lib = load_library()
+    dev = _device()
+    desc = None
+    if rope is not None:
+        if positions is None:
+            raise ValueError("rope needs positions")
+        desc = _ROPE_DESC.pack(ctypes.addressof(rope), _index(positions, "positions", k.shape[:1], device=dev),
+                               0, 0, 0)
+    _check(lib.fl_kv_append_fp8(_pack(q, dev), _pack(k, dev), _pack(v, dev), _pack(q_out, dev),
+                                _pack(k_cache, dev), _pack(v_cache, dev), _pack(k_scale, dev), _pack(v_scale, dev),
+                                _index(slots, "slots", k.shape[:1], "int64", device=dev), desc,
+                                _stream_of(stream, dev)))
+
+
+def fl_kv_read_fp8(k_cache, v_cache, k_scale, v_scale, slots, k_out, v_out, stream=None) -> None:
+    """Enqueue the read of the tokens at ``slots`` (int64 [T]) of an 8-bit cache into k_out
+    and v_out [T, Hk, D], bf16 or fp32 (see include/fl_attn.h)."""
+    lib = load_library()
+    dev = _device()
+    _check(lib.fl_kv_read_fp8(_pack(k_cache, dev), _pack(v_cache, dev), _pack(k_scale, dev), _pack(v_scale, dev),
+                              _index(slots, "slots", k_out.shape[:1], "int64", device=dev), _pack(k_out, dev),
+                              _pack(v_out, dev), _stream_of(stream, dev)))
+
+
 def make_chunk_desc(cu_q, kv_lens, block_table, max_kv_len: int, *, score_mod="none", softcap=20.0,
                     causal=True, window=0, scale=0.0, error_word=None, wait_timeout_us=0,
                     strict_lengths=False) -> FlChunkDesc:
@@ -718,3 +757,29 @@ def fl_attn_chunk(q, k_cache, v_cache, out, lse, desc: FlChunkDesc, workspace, s
     _check(lib.fl_attn_chunk(_pack(q, dev), _pack(k_cache, dev), _pack(v_cache, dev), _pack(out, dev),
                              _pack(lse, dev), ctypes.byref(desc), workspace.data_ptr(),
                              workspace.numel() * workspace.element_size(), _stream_of(stream, dev)))
+
+
+def fl_attn_chunk_fp8_workspace_size(q, k_cache, desc: FlChunkDesc) -> int:
+    """Bytes of workspace fl_attn_chunk_fp8 needs for these shapes."""
+    dev = _device()
+    n = ctypes.c_size_t()
+    _check(load_library().fl_attn_chunk_fp8_workspace_size(_pack(q, dev), _pack(k_cache, dev),
+                                                           ctypes.byref(desc), ctypes.byref(n)))
+    return n.value
+
+
+def fl_attn_chunk_fp8(q, k_cache, v_cache, k_scale, v_scale, out, lse, desc: FlChunkDesc, workspace,
+                      stream=None) -> None:
+    """:func:`fl_attn_chunk` over a cache in 8 bits (torch.float8_e4m3fn, fp32 scales); the
+    workspace holds at least fl_attn_chunk_fp8_workspace_size bytes (see include/fl_attn.h)."""
+    lib = load_library()
+    dev = _device()
+    _check_device(desc, dev)
+    if workspace.get_device() != dev:
+        raise ValueError(f"workspace on {workspace.device}: the current device is cuda:{dev}")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    _check(lib.fl_attn_chunk_fp8(_pack(q, dev), _pack(k_cache, dev), _pack(v_cache, dev), _pack(k_scale, dev),
+                                 _pack(v_scale, dev), _pack(out, dev), _pack(lse, dev), ctypes.byref(desc),
+                                 workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                 _stream_of(stream, dev)))

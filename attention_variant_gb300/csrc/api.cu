@@ -53,6 +53,8 @@ struct View {
     int64_t stride[5];
 };
 
+const char *dtype_name(int dtype) { return dtype == FL_BF16 ? "bf16" : dtype == FL_E4M3 ? "e4m3" : "fp32"; }
+
 fl_status check_tensor(const fl_tensor *t, const char *name, int ndim, int dtype, View &v)
 {
     if (!t)
@@ -62,7 +64,7 @@ fl_status check_tensor(const fl_tensor *t, const char *name, int ndim, int dtype
     if (t->ndim != ndim)
         return fail(FL_ERR_INVALID_ARG, "%s must have %d dimensions, has %d", name, ndim, t->ndim);
     if (t->dtype != dtype)
-        return fail(FL_ERR_INVALID_ARG, "%s must be %s", name, dtype == FL_BF16 ? "bf16" : "fp32");
+        return fail(FL_ERR_INVALID_ARG, "%s must be %s", name, dtype_name(dtype));
     v.ptr = t->ptr;
     v.ndim = ndim;
     for (int d = 0; d < ndim; ++d) {
@@ -80,19 +82,19 @@ fl_status check_tensor(const fl_tensor *t, const char *name, int ndim, int dtype
     }
     if (v.stride[ndim - 1] != 1)
         return fail(FL_ERR_INVALID_ARG, "%s innermost stride must be 1", name);
-    const int elt = dtype == FL_BF16 ? 2 : 4;
+    const int elt = dtype == FL_BF16 ? 2 : dtype == FL_E4M3 ? 1 : 4;
+    const bool vectors = dtype != FL_F32; // read in words of 16 bytes
     for (int d = 0; d < ndim - 1; ++d) {
         if (v.stride[d] <= 0)
             return fail(FL_ERR_INVALID_ARG, "%s stride[%d] must be positive", name, d);
-        if (dtype == FL_BF16 && (v.stride[d] * elt) % 16 != 0)
+        if (vectors && (v.stride[d] * elt) % 16 != 0)
             return fail(FL_ERR_ALIGNMENT, "%s stride[%d] = %lld elements is not a multiple of 16 bytes",
                         name, d, (long long)v.stride[d]);
         if (v.stride[d] * elt >= (int64_t(1) << 40))
             return fail(FL_ERR_INVALID_ARG, "%s stride[%d] too large", name, d);
     }
-    if (reinterpret_cast<uintptr_t>(v.ptr) % (dtype == FL_BF16 ? 16 : 4) != 0)
-        return fail(FL_ERR_ALIGNMENT, "%s->ptr is not %d-byte aligned", name,
-                    dtype == FL_BF16 ? 16 : 4);
+    if (reinterpret_cast<uintptr_t>(v.ptr) % (vectors ? 16 : 4) != 0)
+        return fail(FL_ERR_ALIGNMENT, "%s->ptr is not %d-byte aligned", name, vectors ? 16 : 4);
     return FL_OK;
 }
 
@@ -163,10 +165,11 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
     return fn;
 }
 
-// A bf16 tensor map over dims (innermost first) with byte strides of dims 1..rank-1.
+// A tensor map (bf16, unless `type` says so) over dims (innermost first) with byte strides of dims 1..rank-1.
 fl_status make_map(CUtensorMap &map, void *ptr, int rank, const uint64_t *dims,
                    const uint64_t *strides_bytes, const uint32_t *box, CUtensorMapSwizzle swz,
-                   const char *what, CUtensorMapL2promotion l2 = CU_TENSOR_MAP_L2_PROMOTION_L2_256B)
+                   const char *what, CUtensorMapL2promotion l2 = CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16)
 {
     auto fn = encode_fn();
     if (!fn)
@@ -181,7 +184,7 @@ fl_status make_map(CUtensorMap &map, void *ptr, int rank, const uint64_t *dims,
     }
     for (int d = 0; d < rank - 1; ++d)
         gs[d] = strides_bytes[d];
-    CUresult r = fn(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, ptr, gd, gs, bx, es,
+    CUresult r = fn(&map, type, rank, ptr, gd, gs, bx, es,
                     CU_TENSOR_MAP_INTERLEAVE_NONE, swz, l2,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS)
@@ -1043,6 +1046,43 @@ void add_stream(fl::RopeParams &p, const View &src, const View &dst, bool rotate
     st.to_cache = to_cache ? 1 : 0;
 }
 
+// q and q_out of the appends: both or neither, [T, Hq, D].
+fl_status check_append_rows(const fl_tensor *q, const fl_tensor *q_out, int64_t T, int64_t D, View &Q, View &QO)
+{
+    fl_status s;
+    if ((q == nullptr) != (q_out == nullptr))
+        return fail(FL_ERR_INVALID_ARG, "q and q_out must be given together");
+    if (q) {
+        if ((s = check_rows(q, "q", FL_BF16, Q)) != FL_OK) return s;
+        if ((s = check_rows(q_out, "q_out", FL_BF16, QO)) != FL_OK) return s;
+        if (q->ndim != 3 || q_out->ndim != 3 || Q.size[1] != T || Q.size[3] != D)
+            return fail(FL_ERR_INVALID_ARG, "q must be [T, Hq, D] matching k");
+        if (!same(QO, {1, T, Q.size[2], D}))
+            return fail(FL_ERR_INVALID_ARG, "q_out must have the shape of q");
+    }
+    return FL_OK;
+}
+
+// The other arguments that the appends and the read-back share; `heads` of a token in all.
+fl_status check_append_args(const int64_t *slots, const fl_rope_desc *rope, int64_t T, int64_t D, int64_t heads)
+{
+    fl_status s;
+    if (!slots)
+        return fail(FL_ERR_INVALID_ARG, "slots is NULL");
+    if (reinterpret_cast<uintptr_t>(slots) % 8)
+        return fail(FL_ERR_ALIGNMENT, "slots is not 8-byte aligned");
+    if (rope) {
+        if ((s = check_rope(rope, D)) != FL_OK) return s;
+        if (!rope->positions)
+            return fail(FL_ERR_INVALID_ARG, "rope->positions is NULL");
+        if (rope->backward)
+            return fail(FL_ERR_INVALID_ARG, "the append rotates forward only");
+    }
+    if (T >= (int64_t(1) << 29) || heads * D >= (int64_t(1) << 24))
+        return fail(FL_ERR_UNSUPPORTED, "2^29 tokens or 2^24 elements of a token, or more");
+    return FL_OK;
+}
+
 // The widest vector (in elements) that divides the rotated halves and the
 // copied rest, and to which every address of every tensor is aligned.
 int rope_vec(const fl::RopeParams &p, int elt, bool interleaved)
@@ -1077,6 +1117,45 @@ bool in_place(const View &a, const View &b)
     return true;
 }
 
+// ------------------------------------------------------------------ caches in 8 bits
+
+// The scales of a cache [P, page, Hk, D]: fp32 [P, page / block, Hk].
+fl_status check_scale(const fl_tensor *t, const char *name, const View &cache, View &v, int &block_shift)
+{
+    fl_status s;
+    if ((s = check_tensor(t, name, 3, FL_F32, v)) != FL_OK) return s;
+    const int64_t P = cache.size[0], page = cache.size[1], Hk = cache.size[2];
+    if (v.size[0] != P || v.size[2] != Hk || page % v.size[1] != 0)
+        return fail(FL_ERR_INVALID_ARG, "%s must be [num_pages, page_size / block, Hk] matching its cache", name);
+    const int64_t block = page / v.size[1];
+    for (block_shift = 4; block_shift < 8 && (int64_t(1) << block_shift) != block;)
+        ++block_shift;
+    if ((int64_t(1) << block_shift) != block)
+        return fail(FL_ERR_UNSUPPORTED, "a scale for %lld keys: must be 16, 32, 64, 128 or 256", (long long)block);
+    return FL_OK;
+}
+
+// Both caches and their scales, of one shape.
+struct Fp8Caches {
+    View K, V, KS, VS;
+    int block_shift;
+};
+fl_status check_caches(const fl_tensor *k_cache, const fl_tensor *v_cache, const fl_tensor *k_scale,
+                       const fl_tensor *v_scale, Fp8Caches &c)
+{
+    fl_status s;
+    int shift = 0;
+    if ((s = check_tensor(k_cache, "k_cache", 4, FL_E4M3, c.K)) != FL_OK) return s;
+    if ((s = check_tensor(v_cache, "v_cache", 4, FL_E4M3, c.V)) != FL_OK) return s;
+    if (!same(c.V, {c.K.size[0], c.K.size[1], c.K.size[2], c.K.size[3]}))
+        return fail(FL_ERR_INVALID_ARG, "v_cache must have the shape of k_cache");
+    if ((s = check_scale(k_scale, "k_scale", c.K, c.KS, c.block_shift)) != FL_OK) return s;
+    if ((s = check_scale(v_scale, "v_scale", c.V, c.VS, shift)) != FL_OK) return s;
+    if (shift != c.block_shift)
+        return fail(FL_ERR_INVALID_ARG, "v_scale must have the shape of k_scale");
+    return FL_OK;
+}
+
 // ------------------------------------------------------------------ chunks over a cache
 
 constexpr int32_t kChunkMaxKeys = INT32_MAX - 255;
@@ -1101,15 +1180,15 @@ float chunk_softcap_in(const ChunkPlan &pl, const fl_chunk_desc *d)
 }
 
 fl_status chunk_plan(const fl_tensor *q, const fl_tensor *k_cache, const fl_tensor *v_cache,
-                     const fl_chunk_desc *d, ChunkPlan &pl)
+                     const fl_chunk_desc *d, ChunkPlan &pl, int cache_type = FL_BF16)
 {
     fl_status s;
     if (!d)
         return fail(FL_ERR_INVALID_ARG, "desc is NULL");
     if ((s = check_tensor(q, "q", 3, FL_BF16, pl.Q)) != FL_OK) return s;
-    if ((s = check_tensor(k_cache, "k_cache", 4, FL_BF16, pl.K)) != FL_OK) return s;
+    if ((s = check_tensor(k_cache, "k_cache", 4, cache_type, pl.K)) != FL_OK) return s;
     if (v_cache) {
-        if ((s = check_tensor(v_cache, "v_cache", 4, FL_BF16, pl.V)) != FL_OK) return s;
+        if ((s = check_tensor(v_cache, "v_cache", 4, cache_type, pl.V)) != FL_OK) return s;
         if (!same(pl.V, {pl.K.size[0], pl.K.size[1], pl.K.size[2], pl.K.size[3]}))
             return fail(FL_ERR_INVALID_ARG, "v_cache must have the shape of k_cache");
     }
@@ -1185,6 +1264,157 @@ bool overlap(const void *a, size_t n, const void *b, size_t m)
 {
     const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
     return x < y + m && y < x + n;
+}
+
+// Both chunk calls; k_scale is NULL for a cache in bf16.
+fl_status chunk_run(const fl_tensor *q, const fl_tensor *k_cache, const fl_tensor *v_cache, const fl_tensor *k_scale,
+                    const fl_tensor *v_scale, const fl_tensor *out, const fl_tensor *lse, const fl_chunk_desc *desc,
+                    void *workspace, size_t workspace_bytes, fl_stream_t stream)
+{
+    if (!v_cache)
+        return fail(FL_ERR_INVALID_ARG, "v_cache is NULL");
+    const bool fp8 = k_scale != nullptr;
+    ChunkPlan pl;
+    fl_status s = chunk_plan(q, k_cache, v_cache, desc, pl, fp8 ? FL_E4M3 : FL_BF16);
+    if (s != FL_OK)
+        return s;
+    Fp8Caches c{};
+    if (fp8 && (s = check_caches(k_cache, v_cache, k_scale, v_scale, c)) != FL_OK)
+        return s;
+    View O, L{};
+    if ((s = check_tensor(out, "out", 3, FL_BF16, O)) != FL_OK) return s;
+    if (!same(O, {pl.T, pl.Hq, pl.D}))
+        return fail(FL_ERR_INVALID_ARG, "out must have the shape of q");
+    if (lse) {
+        if ((s = check_tensor(lse, "lse", 2, FL_F32, L)) != FL_OK) return s;
+        if (!same(L, {pl.Hq, pl.T}))
+            return fail(FL_ERR_INVALID_ARG, "lse must be [Hq, T]");
+    }
+    if (!desc->cu_q || !desc->kv_lens)
+        return fail(FL_ERR_INVALID_ARG, "cu_q or kv_lens is NULL");
+    if (reinterpret_cast<uintptr_t>(desc->cu_q) % 4 || reinterpret_cast<uintptr_t>(desc->kv_lens) % 4)
+        return fail(FL_ERR_ALIGNMENT, "cu_q or kv_lens is not 4-byte aligned");
+    if (reinterpret_cast<uintptr_t>(desc->error_word) % 4)
+        return fail(FL_ERR_ALIGNMENT, "error_word is not 4-byte aligned");
+    if (!workspace)
+        return fail(FL_ERR_INVALID_ARG, "workspace is NULL");
+    if (reinterpret_cast<uintptr_t>(workspace) % kWsAlign)
+        return fail(FL_ERR_ALIGNMENT, "workspace is not %zu-byte aligned", kWsAlign);
+    if (workspace_bytes < pl.total)
+        return fail(FL_ERR_INVALID_ARG, "workspace holds %zu bytes, %zu needed", workspace_bytes, pl.total);
+    int dev;
+    DeviceInfo info;
+    if ((s = device_info(dev, info)) != FL_OK) return s;
+    if (info.sm_count < 4)
+        return fail(FL_ERR_UNSUPPORTED, "%d SMs: chunks need 4", info.sm_count);
+    const int64_t G = pl.Hq / pl.Hk;
+    const int few_tq = G <= fl::kFewRows ? int(fl::kFewRows / G) : 1;
+    const int few_box = desc->block_table && pl.page < fl::kFewTile ? int(pl.page) : fl::kFewTile;
+    fl::ChunkMaps maps;
+    for (int few = 0; few < 2; ++few) {
+        // tokens by the G heads of a KV head: the rows of a block
+        const uint64_t dims[4] = {uint64_t(pl.D), uint64_t(G), uint64_t(pl.Hk), uint64_t(pl.T)};
+        const uint64_t st[3] = {uint64_t(pl.Q.stride[1]) * 2, uint64_t(pl.Q.stride[1]) * 2 * uint64_t(G),
+                                uint64_t(pl.Q.stride[0]) * 2};
+        const uint32_t box[4] = {64, uint32_t(G), 1, uint32_t(few ? few_tq : pl.TQ)};
+        if ((s = make_map(few ? maps.few_q : maps.q, pl.Q.ptr, 4, dims, st, box, CU_TENSOR_MAP_SWIZZLE_128B,
+                          "q")) != FL_OK)
+            return s;
+    }
+    for (int m = 0; m < 4; ++m) {
+        const View &C = m % 2 ? pl.V : pl.K;
+        CUtensorMap *dst[4] = {&maps.k, &maps.v, &maps.few_k, &maps.few_v};
+        const uint64_t dims[4] = {uint64_t(pl.D), uint64_t(pl.page), uint64_t(pl.Hk), uint64_t(pl.P)};
+        const uint64_t elt = fp8 ? 1 : 2;
+        const uint64_t st[3] = {uint64_t(C.stride[1]) * elt, uint64_t(C.stride[2]) * elt, uint64_t(C.stride[0]) * elt};
+        const uint32_t box[4] = {fp8 ? uint32_t(pl.D) : 64, m < 2 ? 16u : uint32_t(few_box), 1, 1};
+        if ((s = make_map(*dst[m], C.ptr, 4, dims, st, box,
+                          fp8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+                          m % 2 ? "v_cache" : "k_cache", CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16)) != FL_OK)
+            return s;
+    }
+    fl::ChunkParams p{};
+    p.T = int(pl.T);
+    p.batch = desc->batch;
+    p.Hq = int(pl.Hq);
+    p.Hk = int(pl.Hk);
+    p.G = int(G);
+    p.head_dim = int(pl.D);
+    p.TQ = pl.TQ;
+    p.div_g = fl::make_fastdiv(int32_t(G));
+    p.div_per = fl::make_fastdiv(int32_t(2 * pl.TQ));
+    p.few_tq = few_tq;
+    for (p.few_shift = 4; (1 << p.few_shift) != few_box;)
+        ++p.few_shift;
+    p.max_kv = desc->max_kv_len;
+    p.strict = desc->strict_lengths ? 1 : 0;
+    p.page_shift = -1;
+    if (desc->block_table)
+        for (p.page_shift = 4; (1 << p.page_shift) != pl.page;)
+            ++p.page_shift;
+    p.bt_stride = desc->block_table_stride;
+    p.cu_q = desc->cu_q;
+    p.kv_lens = desc->kv_lens;
+    p.block_table = desc->block_table;
+    p.causal = desc->causal ? 1 : 0;
+    p.window = desc->window;
+    p.score_mod = desc->score_mod;
+    p.qk_log2 = chunk_scale(pl, desc) * kLog2e;
+    if (desc->score_mod == FL_MOD_SOFTCAP) {
+        p.softcap_in = chunk_softcap_in(pl, desc);
+        p.softcap_out = desc->softcap * kLog2e;
+    }
+    p.out = static_cast<__nv_bfloat16 *>(O.ptr);
+    p.o_st = O.stride[0];
+    p.o_sh = O.stride[1];
+    if (lse) {
+        p.lse = static_cast<float *>(L.ptr);
+        p.l_sh = L.stride[0];
+    }
+    p.device = dev;
+    p.n_cta = info.sm_count < fl::kChunkMaxCtas ? info.sm_count : fl::kChunkMaxCtas;
+    // costs for the even split, in tenths of a microsecond as measured: a key
+    // tile of two row blocks (1.0 us, with softcap 2.2 at D = 64 and 1.6 at 128),
+    // of one, a tile of few rows (32 KB a 64 of head dimension at the SM's share
+    // of the HBM bandwidth), an item's start and end (CTAs with many short items
+    // came in last with 2.5 and 2.0 us: 64 single tokens 104 against 101 us, seven
+    // mixed steps 736 against 717 in all); and the least work a CTA is woken for
+    const bool capped = desc->score_mod == FL_MOD_SOFTCAP;
+    p.cost_pair = capped ? (pl.D == 64 ? 22 : 16) : 10;
+    p.cost_single = capped ? (pl.D == 64 ? 12 : 9) : 8;
+    p.cost_few = (capped ? 9 : 7) * int(pl.D / 64);
+    p.cost_item = 35;
+    p.cost_few_item = 32;
+    p.cost_least = 18;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    p.max_entries = pl.max_entries;
+    p.parts = reinterpret_cast<fl::ChunkPart *>(ws);
+    p.joins = reinterpret_cast<fl::ChunkJoin *>(ws + pl.joins);
+    p.entries = reinterpret_cast<fl::ChunkEntry *>(ws + pl.entries);
+    p.partials = reinterpret_cast<float *>(ws + pl.partials);
+    // a mark that no other call has and no other data is likely to hold (the odd
+    // factor takes the numbers one to one over all 64 bits)
+    static std::atomic<uint64_t> calls{0};
+    p.seen = reinterpret_cast<uint64_t *>(ws + pl.seen);
+    p.seen_mark = ++calls * 0x9e3779b97f4a7c15ull;
+    p.err_user = desc->error_word;
+    // a millisecond at least: a wait that gives up sooner could leave a copy on its way
+    p.timeout_ns = std::max<uint64_t>(desc->wait_timeout_us ? desc->wait_timeout_us : 2000000u, 1000u) * 1000ull;
+    if (fp8) {
+        p.k_scale = static_cast<const float *>(c.KS.ptr);
+        p.v_scale = static_cast<const float *>(c.VS.ptr);
+        p.ks_p = c.KS.stride[0];
+        p.ks_b = c.KS.stride[1];
+        p.vs_p = c.VS.stride[0];
+        p.vs_b = c.VS.stride[1];
+        p.scale_shift = c.block_shift;
+        p.n_pages = int(pl.P);
+    }
+    const cudaError_t e = (fp8 ? fl::launch_chunk_fp8 : fl::launch_chunk)(maps, p, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess)
+        return fail(FL_ERR_CUDA, "kernel launch failed: %s", cudaGetErrorString(e));
+    return ok();
 }
 
 } // namespace
@@ -1867,29 +2097,8 @@ fl_status fl_kv_append(const fl_tensor *q, const fl_tensor *k, const fl_tensor *
         return fail(FL_ERR_INVALID_ARG, "k_cache must be [num_pages, page_size, Hk, D] matching k");
     if (!same(VC, {KC.size[0], KC.size[1], Hk, D}))
         return fail(FL_ERR_INVALID_ARG, "v_cache must have the shape of k_cache");
-    if ((q == nullptr) != (q_out == nullptr))
-        return fail(FL_ERR_INVALID_ARG, "q and q_out must be given together");
-    if (q) {
-        if ((s = check_rows(q, "q", FL_BF16, Q)) != FL_OK) return s;
-        if ((s = check_rows(q_out, "q_out", FL_BF16, QO)) != FL_OK) return s;
-        if (q->ndim != 3 || q_out->ndim != 3 || Q.size[1] != T || Q.size[3] != D)
-            return fail(FL_ERR_INVALID_ARG, "q must be [T, Hq, D] matching k");
-        if (!same(QO, {1, T, Q.size[2], D}))
-            return fail(FL_ERR_INVALID_ARG, "q_out must have the shape of q");
-    }
-    if (!slots)
-        return fail(FL_ERR_INVALID_ARG, "slots is NULL");
-    if (reinterpret_cast<uintptr_t>(slots) % 8)
-        return fail(FL_ERR_ALIGNMENT, "slots is not 8-byte aligned");
-    if (rope) {
-        if ((s = check_rope(rope, D)) != FL_OK) return s;
-        if (!rope->positions)
-            return fail(FL_ERR_INVALID_ARG, "rope->positions is NULL");
-        if (rope->backward)
-            return fail(FL_ERR_INVALID_ARG, "the append rotates forward only");
-    }
-    if (T >= (int64_t(1) << 29) || ((q ? Q.size[2] : 0) + 2 * Hk) * D >= (int64_t(1) << 24))
-        return fail(FL_ERR_UNSUPPORTED, "2^29 tokens or 2^24 elements of a token, or more");
+    if ((s = check_append_rows(q, q_out, T, D, Q, QO)) != FL_OK) return s;
+    if ((s = check_append_args(slots, rope, T, D, (q ? Q.size[2] : 0) + 2 * Hk)) != FL_OK) return s;
     int dev;
     DeviceInfo info;
     if ((s = device_info(dev, info)) != FL_OK) return s;
@@ -2013,130 +2222,141 @@ fl_status fl_attn_chunk(const fl_tensor *q, const fl_tensor *k_cache, const fl_t
                         const fl_tensor *out, const fl_tensor *lse, const fl_chunk_desc *desc,
                         void *workspace, size_t workspace_bytes, fl_stream_t stream)
 {
-    if (!v_cache)
-        return fail(FL_ERR_INVALID_ARG, "v_cache is NULL");
+    return chunk_run(q, k_cache, v_cache, nullptr, nullptr, out, lse, desc, workspace, workspace_bytes, stream);
+}
+
+fl_status fl_attn_chunk_fp8_workspace_size(const fl_tensor *q, const fl_tensor *k_cache, const fl_chunk_desc *desc,
+                                           size_t *bytes)
+{
+    if (!bytes)
+        return fail(FL_ERR_INVALID_ARG, "bytes is NULL");
     ChunkPlan pl;
-    fl_status s = chunk_plan(q, k_cache, v_cache, desc, pl);
+    const fl_status s = chunk_plan(q, k_cache, nullptr, desc, pl, FL_E4M3);
     if (s != FL_OK)
         return s;
-    View O, L{};
-    if ((s = check_tensor(out, "out", 3, FL_BF16, O)) != FL_OK) return s;
-    if (!same(O, {pl.T, pl.Hq, pl.D}))
-        return fail(FL_ERR_INVALID_ARG, "out must have the shape of q");
-    if (lse) {
-        if ((s = check_tensor(lse, "lse", 2, FL_F32, L)) != FL_OK) return s;
-        if (!same(L, {pl.Hq, pl.T}))
-            return fail(FL_ERR_INVALID_ARG, "lse must be [Hq, T]");
-    }
-    if (!desc->cu_q || !desc->kv_lens)
-        return fail(FL_ERR_INVALID_ARG, "cu_q or kv_lens is NULL");
-    if (reinterpret_cast<uintptr_t>(desc->cu_q) % 4 || reinterpret_cast<uintptr_t>(desc->kv_lens) % 4)
-        return fail(FL_ERR_ALIGNMENT, "cu_q or kv_lens is not 4-byte aligned");
-    if (reinterpret_cast<uintptr_t>(desc->error_word) % 4)
-        return fail(FL_ERR_ALIGNMENT, "error_word is not 4-byte aligned");
-    if (!workspace)
-        return fail(FL_ERR_INVALID_ARG, "workspace is NULL");
-    if (reinterpret_cast<uintptr_t>(workspace) % kWsAlign)
-        return fail(FL_ERR_ALIGNMENT, "workspace is not %zu-byte aligned", kWsAlign);
-    if (workspace_bytes < pl.total)
-        return fail(FL_ERR_INVALID_ARG, "workspace holds %zu bytes, %zu needed", workspace_bytes, pl.total);
+    *bytes = pl.total;
+    return ok();
+}
+
+fl_status fl_attn_chunk_fp8(const fl_tensor *q, const fl_tensor *k_cache, const fl_tensor *v_cache,
+                            const fl_tensor *k_scale, const fl_tensor *v_scale, const fl_tensor *out,
+                            const fl_tensor *lse, const fl_chunk_desc *desc, void *workspace,
+                            size_t workspace_bytes, fl_stream_t stream)
+{
+    if (!k_scale)
+        return fail(FL_ERR_INVALID_ARG, "k_scale is NULL");
+    return chunk_run(q, k_cache, v_cache, k_scale, v_scale, out, lse, desc, workspace, workspace_bytes, stream);
+}
+
+fl_status fl_kv_append_fp8(const fl_tensor *q, const fl_tensor *k, const fl_tensor *v, const fl_tensor *q_out,
+                           const fl_tensor *k_cache, const fl_tensor *v_cache, const fl_tensor *k_scale,
+                           const fl_tensor *v_scale, const int64_t *slots, const fl_rope_desc *rope,
+                           fl_stream_t stream)
+{
+    View Q, K, V, QO;
+    Fp8Caches c;
+    fl_status s;
+    if ((s = check_tensor(k, "k", 3, FL_BF16, K)) != FL_OK) return s;
+    if ((s = check_tensor(v, "v", 3, FL_BF16, V)) != FL_OK) return s;
+    if ((s = check_caches(k_cache, v_cache, k_scale, v_scale, c)) != FL_OK) return s;
+    const int64_t T = K.size[0], Hk = K.size[1], D = K.size[2];
+    if (!same(V, {T, Hk, D}))
+        return fail(FL_ERR_INVALID_ARG, "v must have the shape of k");
+    if (c.K.size[2] != Hk || c.K.size[3] != D)
+        return fail(FL_ERR_INVALID_ARG, "k_cache must be [num_pages, page_size, Hk, D] matching k");
+    if (D != 64 && D != 128)
+        return fail(FL_ERR_UNSUPPORTED, "caches in 8 bits support head dimension 64 or 128 (got %lld)", (long long)D);
+    if (Hk > 8192)
+        return fail(FL_ERR_UNSUPPORTED, "caches in 8 bits support up to 8192 KV heads (got %lld)", (long long)Hk);
+    if ((s = check_append_rows(q, q_out, T, D, Q, QO)) != FL_OK) return s;
+    if ((s = check_append_args(slots, rope, T, D, (q ? Q.size[2] : 0) + 2 * Hk)) != FL_OK) return s;
     int dev;
     DeviceInfo info;
     if ((s = device_info(dev, info)) != FL_OK) return s;
-    if (info.sm_count < 4)
-        return fail(FL_ERR_UNSUPPORTED, "%d SMs: chunks need 4", info.sm_count);
-    const int64_t G = pl.Hq / pl.Hk;
-    const int few_tq = G <= fl::kFewRows ? int(fl::kFewRows / G) : 1;
-    const int few_box = desc->block_table && pl.page < fl::kFewTile ? int(pl.page) : fl::kFewTile;
-    fl::ChunkMaps maps;
-    for (int few = 0; few < 2; ++few) {
-        // tokens by the G heads of a KV head: the rows of a block
-        const uint64_t dims[4] = {uint64_t(pl.D), uint64_t(G), uint64_t(pl.Hk), uint64_t(pl.T)};
-        const uint64_t st[3] = {uint64_t(pl.Q.stride[1]) * 2, uint64_t(pl.Q.stride[1]) * 2 * uint64_t(G),
-                                uint64_t(pl.Q.stride[0]) * 2};
-        const uint32_t box[4] = {64, uint32_t(G), 1, uint32_t(few ? few_tq : pl.TQ)};
-        if ((s = make_map(few ? maps.few_q : maps.q, pl.Q.ptr, 4, dims, st, box, CU_TENSOR_MAP_SWIZZLE_128B,
-                          "q")) != FL_OK)
-            return s;
+    fl::Fp8AppendParams f{};
+    set_rope(f.rope, rope, D);
+    f.rope.tokens = int(T);
+    f.rope.div_seq = fl::make_fastdiv(int32_t(T));
+    f.rope.page_rows = c.K.size[1];
+    f.rope.slots = slots;
+    f.rope.n_slots = c.K.size[0] * c.K.size[1];
+    if (q)
+        add_stream(f.rope, Q, QO, rope != nullptr, false);
+    for (int i = 0; i < 2; ++i) {
+        const View &src = i ? V : K, &dst = i ? c.V : c.K, &scale = i ? c.VS : c.KS;
+        fl::Fp8Stream &st = i ? f.v : f.k;
+        st.src = static_cast<const __nv_bfloat16 *>(src.ptr);
+        st.s_s = src.stride[0];
+        st.s_h = src.stride[1];
+        st.cache = static_cast<uint8_t *>(dst.ptr);
+        st.d_p = dst.stride[0];
+        st.d_r = dst.stride[1];
+        st.d_h = dst.stride[2];
+        st.scale = static_cast<float *>(scale.ptr);
+        st.s_p = scale.stride[0];
+        st.s_b = scale.stride[1];
     }
-    for (int m = 0; m < 4; ++m) {
-        const View &C = m % 2 ? pl.V : pl.K;
-        CUtensorMap *dst[4] = {&maps.k, &maps.v, &maps.few_k, &maps.few_v};
-        const uint64_t dims[4] = {uint64_t(pl.D), uint64_t(pl.page), uint64_t(pl.Hk), uint64_t(pl.P)};
-        const uint64_t st[3] = {uint64_t(C.stride[1]) * 2, uint64_t(C.stride[2]) * 2, uint64_t(C.stride[0]) * 2};
-        const uint32_t box[4] = {64, m < 2 ? 16u : uint32_t(few_box), 1, 1};
-        if ((s = make_map(*dst[m], C.ptr, 4, dims, st, box, CU_TENSOR_MAP_SWIZZLE_128B,
-                          m % 2 ? "v_cache" : "k_cache")) != FL_OK)
-            return s;
+    f.heads = int(Hk);
+    f.lane_shift = D == 64 ? 2 : 3;
+    f.block_shift = c.block_shift;
+    const cudaError_t e = fl::launch_append_fp8(f, rope && rope->table->layout == FL_ROPE_INTERLEAVED, info.sm_count,
+                                                reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess)
+        return fail(FL_ERR_CUDA, "kernel launch failed: %s", cudaGetErrorString(e));
+    return ok();
+}
+
+fl_status fl_kv_read_fp8(const fl_tensor *k_cache, const fl_tensor *v_cache, const fl_tensor *k_scale,
+                         const fl_tensor *v_scale, const int64_t *slots, const fl_tensor *k_out,
+                         const fl_tensor *v_out, fl_stream_t stream)
+{
+    View O[2];
+    Fp8Caches c;
+    fl_status s;
+    if ((s = check_caches(k_cache, v_cache, k_scale, v_scale, c)) != FL_OK) return s;
+    const int dtype = k_out && k_out->dtype == FL_F32 ? FL_F32 : FL_BF16;
+    const int64_t Hk = c.K.size[2], D = c.K.size[3];
+    for (int i = 0; i < 2; ++i) {
+        const fl_tensor *t = i ? v_out : k_out;
+        const char *name = i ? "v_out" : "k_out";
+        if ((s = check_tensor(t, name, 3, dtype, O[i])) != FL_OK) return s;
+        if (!same(O[i], {O[0].size[0], Hk, D}))
+            return fail(FL_ERR_INVALID_ARG, "%s must be [T, Hk, D] matching the cache", name);
+        if (dtype == FL_F32 && (O[i].stride[0] % 4 || O[i].stride[1] % 4 || reinterpret_cast<uintptr_t>(O[i].ptr) % 16))
+            return fail(FL_ERR_ALIGNMENT, "%s must have its address and strides in multiples of 16 bytes", name);
     }
-    fl::ChunkParams p{};
-    p.T = int(pl.T);
-    p.batch = desc->batch;
-    p.Hq = int(pl.Hq);
-    p.Hk = int(pl.Hk);
-    p.G = int(G);
-    p.head_dim = int(pl.D);
-    p.TQ = pl.TQ;
-    p.div_g = fl::make_fastdiv(int32_t(G));
-    p.div_per = fl::make_fastdiv(int32_t(2 * pl.TQ));
-    p.few_tq = few_tq;
-    for (p.few_shift = 4; (1 << p.few_shift) != few_box;)
-        ++p.few_shift;
-    p.max_kv = desc->max_kv_len;
-    p.strict = desc->strict_lengths ? 1 : 0;
-    p.page_shift = -1;
-    if (desc->block_table)
-        for (p.page_shift = 4; (1 << p.page_shift) != pl.page;)
-            ++p.page_shift;
-    p.bt_stride = desc->block_table_stride;
-    p.cu_q = desc->cu_q;
-    p.kv_lens = desc->kv_lens;
-    p.block_table = desc->block_table;
-    p.causal = desc->causal ? 1 : 0;
-    p.window = desc->window;
-    p.score_mod = desc->score_mod;
-    p.qk_log2 = chunk_scale(pl, desc) * kLog2e;
-    if (desc->score_mod == FL_MOD_SOFTCAP) {
-        p.softcap_in = chunk_softcap_in(pl, desc);
-        p.softcap_out = desc->softcap * kLog2e;
+    if (D != 64 && D != 128)
+        return fail(FL_ERR_UNSUPPORTED, "caches in 8 bits support head dimension 64 or 128 (got %lld)", (long long)D);
+    const int64_t T = O[0].size[0];
+    if ((s = check_append_args(slots, nullptr, T, D, 2 * Hk)) != FL_OK) return s;
+    int dev;
+    DeviceInfo info;
+    if ((s = device_info(dev, info)) != FL_OK) return s;
+    fl::Fp8ReadParams f{};
+    for (int i = 0; i < 2; ++i) {
+        const View &src = i ? c.V : c.K, &scale = i ? c.VS : c.KS;
+        fl::Fp8ReadStream &st = f.st[f.n_streams++];
+        st.cache = static_cast<const uint8_t *>(src.ptr);
+        st.d_p = src.stride[0];
+        st.d_r = src.stride[1];
+        st.d_h = src.stride[2];
+        st.scale = static_cast<const float *>(scale.ptr);
+        st.s_p = scale.stride[0];
+        st.s_b = scale.stride[1];
+        st.out = O[i].ptr;
+        st.o_t = O[i].stride[0];
+        st.o_h = O[i].stride[1];
     }
-    p.out = static_cast<__nv_bfloat16 *>(O.ptr);
-    p.o_st = O.stride[0];
-    p.o_sh = O.stride[1];
-    if (lse) {
-        p.lse = static_cast<float *>(L.ptr);
-        p.l_sh = L.stride[0];
-    }
-    p.device = dev;
-    p.n_cta = info.sm_count < fl::kChunkMaxCtas ? info.sm_count : fl::kChunkMaxCtas;
-    // costs for the even split, in tenths of a microsecond as measured: a key
-    // tile of two row blocks (1.0 us, with softcap 2.2 at D = 64 and 1.6 at 128),
-    // of one, a tile of few rows (32 KB a 64 of head dimension at the SM's share
-    // of the HBM bandwidth), an item's start and end (CTAs with many short items
-    // came in last with 2.5 and 2.0 us: 64 single tokens 104 against 101 us, seven
-    // mixed steps 736 against 717 in all); and the least work a CTA is woken for
-    const bool capped = desc->score_mod == FL_MOD_SOFTCAP;
-    p.cost_pair = capped ? (pl.D == 64 ? 22 : 16) : 10;
-    p.cost_single = capped ? (pl.D == 64 ? 12 : 9) : 8;
-    p.cost_few = (capped ? 9 : 7) * int(pl.D / 64);
-    p.cost_item = 35;
-    p.cost_few_item = 32;
-    p.cost_least = 18;
-    uint8_t *ws = static_cast<uint8_t *>(workspace);
-    p.max_entries = pl.max_entries;
-    p.parts = reinterpret_cast<fl::ChunkPart *>(ws);
-    p.joins = reinterpret_cast<fl::ChunkJoin *>(ws + pl.joins);
-    p.entries = reinterpret_cast<fl::ChunkEntry *>(ws + pl.entries);
-    p.partials = reinterpret_cast<float *>(ws + pl.partials);
-    // a mark that no other call has and no other data is likely to hold (the odd
-    // factor takes the numbers one to one over all 64 bits)
-    static std::atomic<uint64_t> calls{0};
-    p.seen = reinterpret_cast<uint64_t *>(ws + pl.seen);
-    p.seen_mark = ++calls * 0x9e3779b97f4a7c15ull;
-    p.err_user = desc->error_word;
-    // a millisecond at least: a wait that gives up sooner could leave a copy on its way
-    p.timeout_ns = std::max<uint64_t>(desc->wait_timeout_us ? desc->wait_timeout_us : 2000000u, 1000u) * 1000ull;
-    const cudaError_t e = fl::launch_chunk(maps, p, reinterpret_cast<cudaStream_t>(stream));
+    f.tokens = int(T);
+    f.slots = slots;
+    f.n_slots = c.K.size[0] * c.K.size[1];
+    f.page_rows = c.K.size[1];
+    f.block_shift = c.block_shift;
+    const int per = dtype == FL_F32 ? 4 : 8; // elements of 16 bytes
+    f.div_units = fl::make_fastdiv(int32_t(Hk * D / per));
+    while ((int64_t(per) << f.head_shift) < D)
+        ++f.head_shift;
+    const cudaError_t e = fl::launch_read_fp8(f, dtype == FL_F32, info.sm_count, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess)
         return fail(FL_ERR_CUDA, "kernel launch failed: %s", cudaGetErrorString(e));
     return ok();

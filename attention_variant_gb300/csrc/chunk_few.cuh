@@ -43,6 +43,7 @@
 #include <cuda_bf16.h>
 
 #include "chunk_plan.cuh"
+#include "fp8.cuh"
 #include "softmax_tile.cuh"
 
 namespace fl {
@@ -50,12 +51,13 @@ namespace {
 
 constexpr float kFewRange = 60.f; // log2 units
 
-template <int D>
+template <int D, bool F8 = false>
 struct FewCfg {
     static constexpr int kBN = kFewTile;
     static constexpr int kHalves = D / 64;
-    static constexpr int kStages = D == 128 ? 3 : 6;        // of K, and of V
-    static constexpr int kLag = D == 128 ? 1 : 2;           // tiles that V is loaded behind K
+    static constexpr int kThreads = chunk_threads(F8);
+    static constexpr int kStages = F8 ? (D == 128 ? 2 : 3) : D == 128 ? 3 : 6; // of K, and of V
+    static constexpr int kLag = F8 ? 0 : D == 128 ? 1 : 2;  // tiles that V is loaded behind K
     static_assert(kLag < kStages, "K of the lag's tiles is loaded before V frees anything");
     static constexpr uint32_t kRowBytes = 128;              // a 64-column half row
     static constexpr uint32_t kGroupBytes = 8 * kRowBytes;
@@ -63,6 +65,9 @@ struct FewCfg {
     static constexpr uint32_t kQBytes = kHalves * kQHalf;
     static constexpr uint32_t kHalf = kBN * kRowBytes;      // half a K or V tile
     static constexpr uint32_t kTileBytes = kHalves * kHalf;
+    // what TMA loads: these tiles, or ones in 8 bits that are converted to them
+    static constexpr int kLoadStages = F8 ? (D == 128 ? 1 : 4) : kStages, kLoadHalves = F8 ? 1 : kHalves;
+    static constexpr uint32_t kLoadRow = F8 ? D : kRowBytes, kLoadHalf = kBN * kLoadRow, kLoadBytes = kLoadHalves * kLoadHalf;
     static constexpr uint32_t kPRow = 64;                   // bytes of a key's row of P: two terms of 8 or 16 rows
     static constexpr uint32_t kColS = 0, kColO = 64, kStride = 32; // TMEM columns of slot t: + 32 t
 };
@@ -98,9 +103,20 @@ __device__ __forceinline__ FewTiles few_tiles(const FewItem &it, int t)
     return f;
 }
 
+// What TMA loads of a cache in 8 bits, ahead of its conversion.
+template <int D, bool F8>
+struct FewRaw {};
 template <int D>
-struct __align__(1024) FewSmem {
-    using C = FewCfg<D>;
+struct __align__(1024) FewRaw<D, true> {
+    using C = FewCfg<D, true>;
+    uint8_t raw_k[C::kLoadStages][C::kLoadBytes], raw_v[C::kLoadStages][C::kLoadBytes];
+    uint64_t raw_k_full[C::kLoadStages], raw_k_empty[C::kLoadStages];
+    uint64_t raw_v_full[C::kLoadStages], raw_v_empty[C::kLoadStages];
+};
+
+template <int D, bool F8>
+struct __align__(1024) FewSmem : FewRaw<D, F8> {
+    using C = FewCfg<D, F8>;
     uint8_t k[C::kStages][C::kTileBytes];
     uint8_t v[C::kStages][C::kTileBytes];
     uint8_t q[2][2][C::kQBytes];     // [Q buffer][slot]
@@ -119,9 +135,9 @@ struct __align__(1024) FewSmem {
     uint32_t abort_flag;
 };
 
-template <int D>
+template <int D, bool F8>
 struct FewCtx {
-    FewSmem<D> *sm;
+    FewSmem<D, F8> *sm;
     uint32_t tmem;
     int part; // this CTA's place among the parts of the few rows
     WaitCtl wc;
@@ -130,32 +146,32 @@ struct FewCtx {
 // ------------------------------------------------------------------ producers
 
 // A ring of K or V tiles and the one warp that fills it.
-template <int D>
+template <int D, bool F8>
 struct FewRing {
-    using C = FewCfg<D>;
+    using C = FewCfg<D, F8>;
     const CUtensorMap *map;
-    uint8_t (*tile)[C::kTileBytes];
+    uint8_t (*tile)[C::kLoadBytes];
     uint64_t *full, *empty;
     uint32_t count;
 
     // Tile v of an item into the next stage: lane g loads the g-th box, of its page.
-    __device__ __forceinline__ bool load(const FewCtx<D> &cx, const ChunkParams &p, const FewItem &it, int v, int page)
+    __device__ __forceinline__ bool load(const FewCtx<D, F8> &cx, const ChunkParams &p, const FewItem &it, int v, int page)
     {
         const int lane = static_cast<int>(ptx::lane_id());
         const int box = 1 << p.few_shift, key0 = (v >> it.shift) * C::kBN, left = it.L - key0;
-        const uint32_t s = count % C::kStages;
-        if (!warp_wait(bar(empty[s]), ((count / C::kStages) & 1) ^ 1, cx.wc, W_KV_EMPTY))
+        const uint32_t s = count % C::kLoadStages;
+        if (!warp_wait(bar(empty[s]), ((count / C::kLoadStages) & 1) ^ 1, cx.wc, W_KV_EMPTY))
             return false;
         const int boxes = left <= 0 ? 0 : min(C::kBN >> p.few_shift, (left + box - 1) >> p.few_shift);
         if (lane == 0)
-            ptx::mbar_arrive_expect_tx(bar(full[s]), static_cast<uint32_t>(C::kHalves * boxes * box) * C::kRowBytes);
+            ptx::mbar_arrive_expect_tx(bar(full[s]), static_cast<uint32_t>(C::kLoadHalves * boxes * box) * C::kLoadRow);
         __syncwarp();
         if (lane < boxes) {
             const int key = key0 + lane * box;
             const int at = p.page_shift < 0 ? key : key & ((1 << p.page_shift) - 1);
 #pragma unroll
-            for (int hf = 0; hf < C::kHalves; ++hf)
-                ptx::tma_load_4d(ptx::smem_u32(tile[s]) + hf * C::kHalf + lane * box * C::kRowBytes, map,
+            for (int hf = 0; hf < C::kLoadHalves; ++hf)
+                ptx::tma_load_4d(ptx::smem_u32(tile[s]) + hf * C::kLoadHalf + lane * box * C::kLoadRow, map,
                                  bar(full[s]), hf * 64, at, it.kvh + (it.shift ? v & 1 : 0), page);
         }
         __syncwarp();
@@ -164,10 +180,10 @@ struct FewRing {
     }
 
     // Waits (bounded, ignoring the abort) for the warp's loads in flight.
-    __device__ __forceinline__ void drain(const FewCtx<D> &cx) const
+    __device__ __forceinline__ void drain(const FewCtx<D, F8> &cx) const
     {
-        for (uint32_t idx = count > C::kStages ? count - C::kStages : 0; idx < count; ++idx)
-            mbar_wait_drain(bar(full[idx % C::kStages]), (idx / C::kStages) & 1, cx.wc, W_DRAIN);
+        for (uint32_t idx = count > C::kLoadStages ? count - C::kLoadStages : 0; idx < count; ++idx)
+            mbar_wait_drain(bar(full[idx % C::kLoadStages]), (idx / C::kLoadStages) & 1, cx.wc, W_DRAIN);
     }
 };
 
@@ -188,16 +204,33 @@ __device__ __forceinline__ int few_page(const ChunkParams &p, const FewItem &it,
 // with larger pages (of 32 keys: 108 against 104 us of 512 to 8192).
 __device__ __forceinline__ bool few_split_loads(const ChunkParams &p) { return p.few_shift < 5; }
 
+template <int D, bool F8>
+__device__ __forceinline__ FewRing<D, F8> few_ring_k(FewSmem<D, F8> &sm, const CUtensorMap *map)
+{
+    if constexpr (F8)
+        return {map, sm.raw_k, sm.raw_k_full, sm.raw_k_empty, 0u};
+    else
+        return {map, sm.k, sm.k_full, sm.k_empty, 0u};
+}
+template <int D, bool F8>
+__device__ __forceinline__ FewRing<D, F8> few_ring_v(FewSmem<D, F8> &sm, const CUtensorMap *map)
+{
+    if constexpr (F8)
+        return {map, sm.raw_v, sm.raw_v_full, sm.raw_v_empty, 0u};
+    else
+        return {map, sm.v, sm.v_full, sm.v_empty, 0u};
+}
+
 // Walks the CTA's items, publishes them, loads Q, K and, mostly, V.
-template <int D>
-__device__ void few_producer(const FewCtx<D> &cx, const ChunkParams &p, const CUtensorMap *tm_q,
+template <int D, bool F8>
+__device__ void few_producer(const FewCtx<D, F8> &cx, const ChunkParams &p, const CUtensorMap *tm_q,
                              const CUtensorMap *tm_k, const CUtensorMap *tm_v)
 {
-    using C = FewCfg<D>;
+    using C = FewCfg<D, F8>;
     constexpr int kBN = C::kBN;
-    FewSmem<D> &sm = *cx.sm;
+    FewSmem<D, F8> &sm = *cx.sm;
     const uint32_t lane = ptx::lane_id();
-    FewRing<D> keys{tm_k, sm.k, sm.k_full, sm.k_empty, 0u}, values{tm_v, sm.v, sm.v_full, sm.v_empty, 0u};
+    FewRing<D, F8> keys = few_ring_k<D, F8>(sm, tm_k), values = few_ring_v<D, F8>(sm, tm_v);
     const bool split = few_split_loads(p);
     uint32_t item_count = 0;
     bool ok = true;
@@ -336,11 +369,11 @@ __device__ void few_producer(const FewCtx<D> &cx, const ChunkParams &p, const CU
 }
 
 // Loads V alone (few_split_loads).
-template <int D>
-__device__ void few_v_producer(const FewCtx<D> &cx, const ChunkParams &p, const CUtensorMap *tm_v)
+template <int D, bool F8>
+__device__ void few_v_producer(const FewCtx<D, F8> &cx, const ChunkParams &p, const CUtensorMap *tm_v)
 {
-    FewSmem<D> &sm = *cx.sm;
-    FewRing<D> values{tm_v, sm.v, sm.v_full, sm.v_empty, 0u};
+    FewSmem<D, F8> &sm = *cx.sm;
+    FewRing<D, F8> values = few_ring_v<D, F8>(sm, tm_v);
     bool ok = true;
     for (uint32_t n = 0; ok; ++n) {
         const uint32_t slot = n % kInfo;
@@ -364,14 +397,70 @@ __device__ void few_v_producer(const FewCtx<D> &cx, const ChunkParams &p, const 
     values.drain(cx);
 }
 
+// ------------------------------------------------------------------ conversion
+
+// Converts the tiles of a cache in 8 bits, keys that no row sees to zeros.  Four warps.
+template <int D>
+__device__ void few_convert_role(const FewCtx<D, true> &cx, const ChunkParams &p)
+{
+    using C = FewCfg<D, true>;
+    constexpr int kBN = C::kBN;
+    FewSmem<D, true> &sm = *cx.sm;
+    uint32_t idx = 0;
+    for (uint32_t n = 0;; ++n) {
+        const uint32_t slot = n % kInfo;
+        if (!warp_wait(bar(sm.info_full[slot]), (n / kInfo) & 1, cx.wc, W_INFO_FULL))
+            return;
+        const FewItem it = sm.info[slot];
+        __syncwarp();
+        if (ptx::lane_id() == 0)
+            ptx::mbar_arrive(bar(sm.info_empty[slot]));
+        if (it.stop)
+            return;
+        auto scales_of = [&](int v) {
+            return tile_scales(p, it.b, (v >> it.shift) * kBN, it.L, it.kvh + (it.shift ? v & 1 : 0));
+        };
+        float next = scales_of(it.u_lo);
+        for (int v = it.u_lo; v < it.u_hi; ++v, ++idx) {
+            const float scales = next;
+            if (v + 1 < it.u_hi)
+                next = scales_of(v + 1);
+            const uint32_t raw = idx % C::kLoadStages, raw_phase = (idx / C::kLoadStages) & 1;
+            const uint32_t stage = idx % C::kStages, phase = (idx / C::kStages) & 1;
+            const int j0 = (v >> it.shift) * kBN;
+            const int dead_lo = min(kBN, max(0, it.key_lo - j0)), dead_hi = min(kBN, max(0, it.L - j0));
+            if (!warp_wait(bar(sm.raw_k_full[raw]), raw_phase, cx.wc, W_KV_FULL) ||
+                !warp_wait(bar(sm.k_empty[stage]), phase ^ 1, cx.wc, W_KV_EMPTY))
+                return;
+            convert_tile<D, kBN>(sm.raw_k[raw], sm.k[stage], scales, 0, dead_lo, dead_hi);
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (ptx::lane_id() == 0) {
+                ptx::mbar_arrive(bar(sm.k_full[stage]));
+                ptx::mbar_arrive(bar(sm.raw_k_empty[raw]));
+            }
+            if (!warp_wait(bar(sm.raw_v_full[raw]), raw_phase, cx.wc, W_KV_FULL) ||
+                !warp_wait(bar(sm.v_empty[stage]), phase ^ 1, cx.wc, W_KV_EMPTY))
+                return;
+            convert_tile<D, kBN>(sm.raw_v[raw], sm.v[stage], scales, 8, dead_lo, dead_hi);
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (ptx::lane_id() == 0) {
+                ptx::mbar_arrive(bar(sm.v_full[stage]));
+                ptx::mbar_arrive(bar(sm.raw_v_empty[raw]));
+            }
+        }
+    }
+}
+
 // ------------------------------------------------------------------ MMA issuers
 
-template <int D>
-__device__ void few_s_role(const FewCtx<D> &cx)
+template <int D, bool F8>
+__device__ void few_s_role(const FewCtx<D, F8> &cx)
 {
-    using C = FewCfg<D>;
+    using C = FewCfg<D, F8>;
     constexpr int kBN = C::kBN, kStages = C::kStages;
-    FewSmem<D> &sm = *cx.sm;
+    FewSmem<D, F8> &sm = *cx.sm;
     const uint32_t lane = ptx::lane_id();
     constexpr uint32_t idesc = umma_idesc_bf16(kBN, kFewRows, false);
     constexpr uint64_t kHi = umma_desc_hi(16, C::kGroupBytes, kSwizzle128B); // Q, K: K-major
@@ -444,12 +533,12 @@ __device__ void few_s_role(const FewCtx<D> &cx)
 // Issues O^T of the slots from `slot` on: both, or one.  Every warp of this role
 // passes every tile in order (and releases what is not its own), so that none
 // is ever a turn of the ring away from a barrier whose parity it waits for.
-template <int D>
-__device__ void few_pv_role(const FewCtx<D> &cx, int slot_lo, int slot_hi)
+template <int D, bool F8>
+__device__ void few_pv_role(const FewCtx<D, F8> &cx, int slot_lo, int slot_hi)
 {
-    using C = FewCfg<D>;
+    using C = FewCfg<D, F8>;
     constexpr int kBN = C::kBN, kStages = C::kStages;
-    FewSmem<D> &sm = *cx.sm;
+    FewSmem<D, F8> &sm = *cx.sm;
     const uint32_t lane = ptx::lane_id();
     // O^T = V^T P^T: both operands with their long index contiguous.  V^T has
     // 128 rows: at D = 64 the second 64 repeat the first (block stride 0).  P
@@ -492,7 +581,7 @@ __device__ void few_pv_role(const FewCtx<D> &cx, int slot_lo, int slot_hi)
             // rows of V that no query row sees: zero (their P is 0, but the bytes
             // may be anything)
             const int dead_lo = min(kBN, max(0, key_lo - j0)), dead_hi = min(kBN, max(0, L - j0));
-            if (dead_lo > 0 || dead_hi < kBN) {
+            if (!F8 && (dead_lo > 0 || dead_hi < kBN)) { // in 8 bits the conversion has
 #pragma unroll
                 for (int hf = 0; hf < C::kHalves; ++hf) {
                     uint4 *dst = reinterpret_cast<uint4 *>(sm.v[stage] + hf * C::kHalf);
@@ -572,13 +661,13 @@ struct FewState {
 };
 
 // One item of at most R rows.  False when a wait ran out.
-template <int MOD, int D, int R>
-__device__ __forceinline__ bool few_item(const FewCtx<D> &cx, const ChunkParams &p, const FewItem &inf, int t,
+template <int MOD, int D, bool F8, int R>
+__device__ __forceinline__ bool few_item(const FewCtx<D, F8> &cx, const ChunkParams &p, const FewItem &inf, int t,
                                          FewState &ct)
 {
-    using C = FewCfg<D>;
+    using C = FewCfg<D, F8>;
     constexpr int kBN = C::kBN;
-    FewSmem<D> &sm = *cx.sm;
+    FewSmem<D, F8> &sm = *cx.sm;
     const int r = threadIdx.x & 127; // key of the tile = TMEM lane of S^T; of O^T: dimension
     const int wq = (threadIdx.x >> 5) & 3, lane = static_cast<int>(ptx::lane_id());
     const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
@@ -831,10 +920,10 @@ __device__ __forceinline__ bool few_item(const FewCtx<D> &cx, const ChunkParams 
     return true;
 }
 
-template <int MOD, int D>
-__device__ void few_softmax(const FewCtx<D> &cx, const ChunkParams &p, int t)
+template <int MOD, int D, bool F8>
+__device__ void few_softmax(const FewCtx<D, F8> &cx, const ChunkParams &p, int t)
 {
-    FewSmem<D> &sm = *cx.sm;
+    FewSmem<D, F8> &sm = *cx.sm;
     FewState ct{0u, 0u, 0u, 0u};
     for (uint32_t item = 0;; ++item) {
         if (!warp_wait(bar(sm.info_full[item % kInfo]), (item / kInfo) & 1, cx.wc, W_INFO_FULL))
@@ -843,8 +932,8 @@ __device__ void few_softmax(const FewCtx<D> &cx, const ChunkParams &p, int t)
         if (inf.stop)
             return;
         // an odd head's item has no second slot; half the rows, half the work
-        if (t < inf.heads && !(inf.rows <= 8 ? few_item<MOD, D, 8>(cx, p, inf, t, ct)
-                                             : few_item<MOD, D, 16>(cx, p, inf, t, ct)))
+        if (t < inf.heads && !(inf.rows <= 8 ? few_item<MOD, D, F8, 8>(cx, p, inf, t, ct)
+                                             : few_item<MOD, D, F8, 16>(cx, p, inf, t, ct)))
             return;
         __syncwarp();
         if (ptx::lane_id() == 0)
@@ -853,15 +942,16 @@ __device__ void few_softmax(const FewCtx<D> &cx, const ChunkParams &p, int t)
 }
 
 // The kernel of the few rows (see chunk_kernel for what runs beside it).
-template <int MOD, int D>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int MOD, int D, bool F8>
+__global__ void __launch_bounds__(chunk_threads(F8), 1)
     chunk_few_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constant__ ChunkParams p)
 {
-    using C = FewCfg<D>;
+    using C = FewCfg<D, F8>;
+    constexpr int kThreads = C::kThreads;
     extern __shared__ uint8_t smem_raw[];
-    FewSmem<D> *sm = reinterpret_cast<FewSmem<D> *>(smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u));
+    FewSmem<D, F8> *sm = reinterpret_cast<FewSmem<D, F8> *>(smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u));
     const int warp = threadIdx.x >> 5;
-    FewCtx<D> cx;
+    FewCtx<D, F8> cx;
     cx.part = part_of(p);
     if (idle_second(p, 1, cx.part))
         return;
@@ -876,14 +966,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int b = 0; b < kInfo; ++b) {
             ptx::mbar_init(bar(sm->info_full[b]), 1);
-            ptx::mbar_init(bar(sm->info_empty[b]), 11); // all but the producer
+            ptx::mbar_init(bar(sm->info_empty[b]), F8 ? 15 : 11); // all but the producer
         }
         for (int s = 0; s < C::kStages; ++s) {
-            ptx::mbar_init(bar(sm->k_full[s]), 1);
+            ptx::mbar_init(bar(sm->k_full[s]), F8 ? 4 : 1); // one arrival per converting warp
             ptx::mbar_init(bar(sm->k_empty[s]), 1);
-            ptx::mbar_init(bar(sm->v_full[s]), 1);
+            ptx::mbar_init(bar(sm->v_full[s]), F8 ? 4 : 1);
             ptx::mbar_init(bar(sm->v_empty[s]), few_split_loads(p) ? 1 : 2); // the warps that issue O^T
         }
+        if constexpr (F8)
+            for (int s = 0; s < C::kLoadStages; ++s) {
+                ptx::mbar_init(bar(sm->raw_k_full[s]), 1);
+                ptx::mbar_init(bar(sm->raw_k_empty[s]), 4);
+                ptx::mbar_init(bar(sm->raw_v_full[s]), 1);
+                ptx::mbar_init(bar(sm->raw_v_empty[s]), 4);
+            }
         for (int t = 0; t < 2; ++t) {
             ptx::mbar_init(bar(sm->s_full[t]), 1);
             ptx::mbar_init(bar(sm->s_free[t]), 128);
@@ -908,9 +1005,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     cx.sm = sm;
     cx.tmem = sm->tmem_base;
     cx.wc = wait_ctl(p, &sm->abort_flag);
-    if (warp >= 4) {
+    if (F8 && warp >= 12) {
+        if constexpr (F8)
+            few_convert_role<D>(cx, p);
+        ptx::named_barrier_sync(1, kThreads);
+    } else if (warp >= 4) {
         tell_second(p, cx.part);
-        few_softmax<MOD, D>(cx, p, (warp >> 2) - 1);
+        few_softmax<MOD, D, F8>(cx, p, (warp >> 2) - 1);
         ptx::tc_fence_before();
         ptx::named_barrier_sync(1, kThreads);
     } else {

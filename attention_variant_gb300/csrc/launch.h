@@ -261,6 +261,43 @@ struct RopeParams {
     uint64_t turns[128];
 };
 
+// ---- a cache of e4m3 codes written and read back (kv_fp8.cu)
+// One tensor's way into the cache (element strides; scales have heads innermost).
+struct Fp8Stream {
+    const __nv_bfloat16 *src;
+    int64_t s_s, s_h;
+    uint8_t *cache;
+    int64_t d_p, d_r, d_h;
+    float *scale;
+    int64_t s_p, s_b;
+};
+struct Fp8AppendParams {
+    RopeParams rope;           // of q, where given, and k; the slots
+    Fp8Stream k, v;
+    int heads, lane_shift;     // KV heads; log2 of a row's 16-element pieces
+    int block_shift;           // log2 of the keys per scale
+    FastDiv div_group;         // heads of a group, groups, tokens per chunk of a
+    int groups, chunk, tile;   // run and per thread block (set by launch_append_fp8)
+};
+struct Fp8ReadStream {
+    const uint8_t *cache;
+    int64_t d_p, d_r, d_h;
+    const float *scale;
+    int64_t s_p, s_b;
+    void *out;
+    int64_t o_t, o_h;
+};
+struct Fp8ReadParams {
+    Fp8ReadStream st[2];
+    int n_streams, tokens;
+    const int64_t *slots;
+    int64_t n_slots, page_rows;
+    int block_shift;
+    FastDiv div_units;         // 16-byte units of a token's output
+    int head_shift;            // log2 of those of a head
+    int tile;                  // tokens per thread block (set by launch_read_fp8)
+};
+
 // ---- the book-keeping of a serving step (kv_plan.cu)
 struct KvPlanParams {
     int batch, max_tokens, n_free, bt_stride;
@@ -337,12 +374,19 @@ struct ChunkParams {
     float *partials;           // [n_cta][2][2][D + 4][128]
     uint32_t *err_user;
     uint64_t timeout_ns;
+    // a cache in 8 bits: scales [page][block of keys][head], element strides
+    const float *k_scale, *v_scale;
+    int64_t ks_p, ks_b, vs_p, vs_b;
+    int scale_shift;           // log2 of the keys per block
+    int n_pages;
 };
 
 #ifndef __CUDACC_RTC__
 // vec: elements per vector access (a power of two up to 16 bytes' worth)
 cudaError_t launch_rope(const RopeParams &p, bool fp32, bool interleaved, int vec, int sm_count,
                         cudaStream_t stream);
+cudaError_t launch_append_fp8(const Fp8AppendParams &p, bool interleaved, int sm_count, cudaStream_t stream);
+cudaError_t launch_read_fp8(const Fp8ReadParams &p, bool fp32, int sm_count, cudaStream_t stream);
 cudaError_t launch_kv_plan(const KvPlanParams &p, cudaStream_t stream);
 // Tensor maps: a row block of q and boxes of 16 keys; few rows of q and boxes
 // of few_box keys.
@@ -350,6 +394,7 @@ struct ChunkMaps {
     CUtensorMap q, k, v, few_q, few_k, few_v;
 };
 cudaError_t launch_chunk(const ChunkMaps &maps, const ChunkParams &p, cudaStream_t stream);
+cudaError_t launch_chunk_fp8(const ChunkMaps &maps, const ChunkParams &p, cudaStream_t stream);
 #endif
 
 }  // namespace fl

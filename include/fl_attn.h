@@ -57,11 +57,12 @@ typedef enum {
     FL_ERR_NO_DEVICE = 6       /* no CUDA device, or not an sm_103 (GB300) device */
 } fl_status;
 
-typedef enum { FL_BF16 = 0, FL_F32 = 1 } fl_dtype;
+/* FL_E4M3: 8-bit floats of 4 exponent and 3 mantissa bits (up to 448, no infinities). */
+typedef enum { FL_BF16 = 0, FL_F32 = 1, FL_E4M3 = 2 } fl_dtype;
 
 /* A strided view.  sizes/strides are in ELEMENTS, outermost first; the
- * innermost stride must be 1.  All other strides of bf16 tensors must be
- * multiples of 8 elements (16 bytes) and every ptr 16-byte aligned. */
+ * innermost stride must be 1.  All other strides of bf16 and e4m3 tensors must be
+ * multiples of 16 bytes and every ptr 16-byte aligned. */
 typedef struct {
     void *ptr;
     int32_t dtype; /* fl_dtype */
@@ -580,6 +581,66 @@ fl_status fl_attn_chunk_workspace_size(const fl_tensor *q, const fl_tensor *k_ca
 fl_status fl_attn_chunk(const fl_tensor *q, const fl_tensor *k_cache, const fl_tensor *v_cache,
                         const fl_tensor *out, const fl_tensor *lse, const fl_chunk_desc *desc,
                         void *workspace, size_t workspace_bytes, fl_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The same cache in 8 bits: half the bytes that a decode step reads.
+ *
+ *   k_cache, v_cache  [num_pages, page_size, Hk, D] e4m3, D = 64 or 128
+ *   k_scale, v_scale  fp32 [num_pages, page_size / block, Hk], heads contiguous (other
+ *                     strides any): a scale for each `block` keys of a page and KV
+ *                     head, block 16, 32, 64, 128 or 256 and a divisor of page_size
+ *                     (both tensors the same; it follows from the shapes)
+ * Element d of key row r of page p and head h stands for
+ *     cache[p][r][h][d] * scale[p][r / block][h].
+ * Scales are positive powers of two, between 2^-100 and 2^100: code times scale is then
+ * exact in bf16.  Others are allowed where a cache comes from elsewhere and cost a rounding
+ * of the scale and of each value to bf16.
+ *
+ * fl_kv_append_fp8 -- fl_kv_append into such a cache.
+ * Arguments as there, but page_size a multiple of block.  Per KV head, k (rotated in
+ * fp32, where rope is given) and v are coded as x / s rounded to e4m3 (to nearest even),
+ * with s the block's scale.  Of the tokens that a call writes to a block, let a be the
+ * largest finite |x| and need the smallest power of two with 448 need >= a, at least
+ * 2^-100.  If the block's first row is among them the block starts anew, with s = need;
+ * other rows keep codes that mean nothing until they are written.  Otherwise s = max(the
+ * scale found, need), and where that grows, codes c of the block's other rows become
+ * c s_old / s, rounded (exact but for codes that leave e4m3's normal range).  So a block's scale
+ * does not depend on how its tokens were split over calls.  A scale found that is not
+ * positive and finite counts as none.  Values that are not finite are stored as NaN.
+ * The tokens of a call that share a block must follow one another in k, v and
+ * slots (in any order), as fl_kv_plan lists them; blocks that tokens apart from one another
+ * share hold any of their scales and codes afterwards.  Slots must differ from one
+ * another.  q_out may be q.
+ */
+fl_status fl_kv_append_fp8(const fl_tensor *q, const fl_tensor *k, const fl_tensor *v, const fl_tensor *q_out,
+                           const fl_tensor *k_cache, const fl_tensor *v_cache, const fl_tensor *k_scale,
+                           const fl_tensor *v_scale, const int64_t *slots, const fl_rope_desc *rope,
+                           fl_stream_t stream);
+
+/*
+ * fl_kv_read_fp8 -- the values of tokens of such a cache: row t of k_out and
+ * v_out [T, Hk, D] (T >= 1, both bf16 or both fp32, strides in multiples of 16
+ * bytes) becomes code times scale of slot slots[t] (device int64 [T], as in
+ * fl_kv_append), rounded once.  Slots may repeat; rows of slots outside the
+ * cache are left as they are.
+ */
+fl_status fl_kv_read_fp8(const fl_tensor *k_cache, const fl_tensor *v_cache, const fl_tensor *k_scale,
+                         const fl_tensor *v_scale, const int64_t *slots, const fl_tensor *k_out,
+                         const fl_tensor *v_out, fl_stream_t stream);
+
+/*
+ * fl_attn_chunk_fp8 -- fl_attn_chunk over such a cache (contiguous ones are
+ * [B, S_max, Hk, D] with scales [B, S_max / block, Hk]).  Everything said there holds, with
+ * the values of the cache in place of its elements.  Codes and scales of keys that no row of
+ * their request sees may be anything; those of the others must not be NaN.  The
+ * workspace is larger: ask fl_attn_chunk_fp8_workspace_size.
+ */
+fl_status fl_attn_chunk_fp8_workspace_size(const fl_tensor *q, const fl_tensor *k_cache,
+                                           const fl_chunk_desc *desc, size_t *bytes);
+fl_status fl_attn_chunk_fp8(const fl_tensor *q, const fl_tensor *k_cache, const fl_tensor *v_cache,
+                            const fl_tensor *k_scale, const fl_tensor *v_scale, const fl_tensor *out,
+                            const fl_tensor *lse, const fl_chunk_desc *desc, void *workspace,
+                            size_t workspace_bytes, fl_stream_t stream);
 
 #ifdef __cplusplus
 }
