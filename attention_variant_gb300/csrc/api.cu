@@ -1165,7 +1165,8 @@ struct ChunkPlan {
     View Q, K, V;
     int64_t T, Hq, Hk, D, P, page;
     int TQ, max_entries;
-    size_t joins, entries, partials, seen, total; // offsets in the workspace (the parts come first), its size
+    // offsets in the workspace (the parts come first), its size; the last two of a cache in 8 bits
+    size_t joins, entries, partials, seen, total, q8, q_scale;
 };
 
 float chunk_scale(const ChunkPlan &pl, const fl_chunk_desc *d)
@@ -1255,7 +1256,13 @@ fl_status chunk_plan(const fl_tensor *q, const fl_tensor *k_cache, const fl_tens
     pl.entries = pl.joins + align_up(fl::kChunkMaxCtas * sizeof(fl::ChunkJoin));
     pl.partials = pl.entries + align_up(2 * size_t(entries) * sizeof(fl::ChunkEntry));
     pl.seen = pl.partials + align_up(size_t(fl::kChunkMaxCtas) * 4 * size_t(pl.D + 4) * 128 * sizeof(float));
-    pl.total = pl.seen + align_up(sizeof(uint64_t));
+    pl.q8 = pl.q_scale = pl.total = pl.seen + align_up(sizeof(uint64_t));
+    if (cache_type == FL_E4M3) {
+        if (pl.T >= (int64_t(1) << 30)) // both terms of q are numbered
+            return fail(FL_ERR_UNSUPPORTED, "2^30 tokens or more");
+        pl.q_scale = pl.q8 + align_up(2 * size_t(pl.T) * size_t(pl.Hq) * size_t(pl.D));
+        pl.total = pl.q_scale + align_up(size_t(pl.T) * size_t(pl.Hq) * sizeof(float));
+    }
     return FL_OK;
 }
 
@@ -1310,15 +1317,19 @@ fl_status chunk_run(const fl_tensor *q, const fl_tensor *k_cache, const fl_tenso
     const int64_t G = pl.Hq / pl.Hk;
     const int few_tq = G <= fl::kFewRows ? int(fl::kFewRows / G) : 1;
     const int few_box = desc->block_table && pl.page < fl::kFewTile ? int(pl.page) : fl::kFewTile;
+    const CUtensorMapDataType type = fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const CUtensorMapSwizzle rows_swizzle = fp8 && pl.D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
     fl::ChunkMaps maps;
     for (int few = 0; few < 2; ++few) {
         // tokens by the G heads of a KV head: the rows of a block
-        const uint64_t dims[4] = {uint64_t(pl.D), uint64_t(G), uint64_t(pl.Hk), uint64_t(pl.T)};
-        const uint64_t st[3] = {uint64_t(pl.Q.stride[1]) * 2, uint64_t(pl.Q.stride[1]) * 2 * uint64_t(G),
-                                uint64_t(pl.Q.stride[0]) * 2};
-        const uint32_t box[4] = {64, uint32_t(G), 1, uint32_t(few ? few_tq : pl.TQ)};
-        if ((s = make_map(few ? maps.few_q : maps.q, pl.Q.ptr, 4, dims, st, box, CU_TENSOR_MAP_SWIZZLE_128B,
-                          "q")) != FL_OK)
+        // (in 8 bits those of q's first term, then of its second, in the workspace)
+        const uint64_t dims[4] = {uint64_t(pl.D), uint64_t(G), uint64_t(pl.Hk), uint64_t(pl.T) * (fp8 ? 2 : 1)};
+        const uint64_t sh = fp8 ? uint64_t(pl.D) : uint64_t(pl.Q.stride[1]) * 2;
+        const uint64_t st[3] = {sh, sh * uint64_t(G), fp8 ? sh * uint64_t(pl.Hq) : uint64_t(pl.Q.stride[0]) * 2};
+        const uint32_t box[4] = {fp8 ? uint32_t(pl.D) : 64, uint32_t(G), 1, uint32_t(few ? few_tq : pl.TQ)};
+        void *ptr = fp8 ? static_cast<uint8_t *>(workspace) + pl.q8 : pl.Q.ptr;
+        if ((s = make_map(few ? maps.few_q : maps.q, ptr, 4, dims, st, box, rows_swizzle, "q",
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, type)) != FL_OK)
             return s;
     }
     for (int m = 0; m < 4; ++m) {
@@ -1328,10 +1339,10 @@ fl_status chunk_run(const fl_tensor *q, const fl_tensor *k_cache, const fl_tenso
         const uint64_t elt = fp8 ? 1 : 2;
         const uint64_t st[3] = {uint64_t(C.stride[1]) * elt, uint64_t(C.stride[2]) * elt, uint64_t(C.stride[0]) * elt};
         const uint32_t box[4] = {fp8 ? uint32_t(pl.D) : 64, m < 2 ? 16u : uint32_t(few_box), 1, 1};
-        if ((s = make_map(*dst[m], C.ptr, 4, dims, st, box,
-                          fp8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
-                          m % 2 ? "v_cache" : "k_cache", CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                          fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16)) != FL_OK)
+        // V of row blocks is not multiplied as it is loaded
+        const CUtensorMapSwizzle swizzle = fp8 && m == 1 ? CU_TENSOR_MAP_SWIZZLE_NONE : rows_swizzle;
+        if ((s = make_map(*dst[m], C.ptr, 4, dims, st, box, swizzle, m % 2 ? "v_cache" : "k_cache",
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, type)) != FL_OK)
             return s;
     }
     fl::ChunkParams p{};
@@ -1410,6 +1421,12 @@ fl_status chunk_run(const fl_tensor *q, const fl_tensor *k_cache, const fl_tenso
         p.vs_b = c.VS.stride[1];
         p.scale_shift = c.block_shift;
         p.n_pages = int(pl.P);
+        p.q = static_cast<const __nv_bfloat16 *>(pl.Q.ptr);
+        p.q_st = pl.Q.stride[0];
+        p.q_sh = pl.Q.stride[1];
+        p.q8 = ws + pl.q8;
+        p.q_scale = reinterpret_cast<float *>(ws + pl.q_scale);
+        p.cost_few = (p.cost_few + 1) / 2; // half the bytes
     }
     const cudaError_t e = (fp8 ? fl::launch_chunk_fp8 : fl::launch_chunk)(maps, p, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess)

@@ -71,7 +71,8 @@ template <int D, bool F8 = false>
 struct ChunkCfg {
     static_assert(D == 64 || D == 128, "head dimension");
     static constexpr int kBN = chunk_key_tile(D);
-    static constexpr int kStages = F8 ? (D == 128 ? 2 : 3) : D == 128 ? 3 : 4;
+    static constexpr int kStages = D == 128 ? 3 : 4; // of K and V as they are loaded
+    static constexpr int kVStages = F8 ? (D == 128 ? 2 : 3) : kStages; // of V in bf16
     static constexpr int kThreads = chunk_threads(F8);
     static constexpr bool kOnes = D <= 64; // sum of the rounded P from a ones column block
     static constexpr int kHalves = D / 64;
@@ -81,7 +82,9 @@ struct ChunkCfg {
     static constexpr uint32_t kKVHalf = kBN * kRowBytes;
     static constexpr uint32_t kTileBytes = kHalves * kQHalf;
     static constexpr uint32_t kKVBytes = kHalves * kKVHalf;
-    static constexpr uint32_t kRawBytes = kBN * D; // a tile in 8 bits
+    static constexpr uint32_t kLoadBytes = F8 ? kBN * D : kKVBytes; // of a tile of K or V as it is loaded
+    static constexpr uint32_t kRowSwizzle = F8 && D == 64 ? kSwizzle64B : kSwizzle128B; // of Q and K
+    static constexpr uint32_t kRowLen = F8 ? D : kRowBytes;
     static constexpr uint32_t kOnesBytes = kOnes ? kTileBytes : 16;
     static constexpr uint32_t kDvExt = kOnes ? D + 16 : D;
     static constexpr uint32_t kColSum = D;
@@ -108,22 +111,12 @@ struct Item {
     int mine;                    // its buffer: 1 if the item begins here
 };
 
-// What TMA loads of a cache in 8 bits, ahead of its conversion.
 template <int D, bool F8>
-struct ChunkRaw {};
-template <int D>
-struct __align__(1024) ChunkRaw<D, true> {
-    using C = ChunkCfg<D, true>;
-    uint8_t raw_k[C::kStages][C::kRawBytes], raw_v[C::kStages][C::kRawBytes];
-    uint64_t raw_full[C::kStages], raw_empty[C::kStages];
-};
-
-template <int D, bool F8>
-struct __align__(1024) ChunkSmem : ChunkRaw<D, F8> {
+struct __align__(1024) ChunkSmem {
     using C = ChunkCfg<D, F8>;
-    uint8_t q[2][2][C::kTileBytes]; // [Q buffer][slot]
-    uint8_t k[C::kStages][C::kKVBytes];
-    uint8_t v[C::kStages][C::kKVBytes];
+    uint8_t q[2][2][C::kTileBytes]; // [Q buffer][slot]; in 8 bits two terms
+    uint8_t k[C::kStages][C::kLoadBytes];
+    uint8_t v[C::kVStages][C::kKVBytes];
     uint8_t ones[C::kOnesBytes];
     uint64_t q_full[2], q_empty[2];
     uint64_t kv_full[C::kStages], kv_empty[C::kStages];
@@ -135,6 +128,9 @@ struct __align__(1024) ChunkSmem : ChunkRaw<D, F8> {
     Item info[kInfo];
     uint32_t tmem_base;
     uint32_t abort_flag;
+    // a cache in 8 bits: V as it is loaded, and the stages of what it is converted to
+    uint64_t v_full[F8 ? C::kVStages : 1], v_empty[F8 ? C::kVStages : 1];
+    alignas(F8 ? 128 : 4) uint8_t raw_v[F8 ? C::kStages : 1][F8 ? C::kLoadBytes : 4];
 };
 
 template <int D, bool F8>
@@ -144,24 +140,6 @@ struct KernelCtx {
     int part;
     WaitCtl wc;
 };
-
-// The barriers of the stage that TMA fills.
-template <int D, bool F8>
-__device__ __forceinline__ uint64_t *load_full(ChunkSmem<D, F8> &sm, uint32_t s)
-{
-    if constexpr (F8)
-        return &sm.raw_full[s];
-    else
-        return &sm.kv_full[s];
-}
-template <int D, bool F8>
-__device__ __forceinline__ uint64_t *load_empty(ChunkSmem<D, F8> &sm, uint32_t s)
-{
-    if constexpr (F8)
-        return &sm.raw_empty[s];
-    else
-        return &sm.kv_empty[s];
-}
 
 // ------------------------------------------------------------------ producer
 
@@ -179,6 +157,8 @@ __device__ void producer_role(const KernelCtx<D, F8> &cx, const ChunkParams &p, 
     const int cta = cx.part;
     int e = 0, h = 0, k = 0; // entry, item of it, tile of that
     read_part(p, 0, cta, me, e, h, k);
+    if (F8)
+        ptx::fence_proxy_async_all(); // Q's terms, which the planning kernel has written
     for (;;) {
         // ---- the next part
         Item it;
@@ -257,11 +237,16 @@ __device__ void producer_role(const KernelCtx<D, F8> &cx, const ChunkParams &p, 
             const int slots = it.pair ? 2 : 1;
             ptx::mbar_arrive_expect_tx(bar(sm.q_full[ring]),
                                        static_cast<uint32_t>(slots * C::kHalves * p.TQ * p.G) * C::kRowBytes);
-            for (int t = 0; t < slots; ++t)
+            for (int t = 0; t < slots; ++t) {
 #pragma unroll
-                for (int hf = 0; hf < C::kHalves; ++hf)
+                for (int hf = 0; hf < (F8 ? 0 : C::kHalves); ++hf)
                     ptx::tma_load_4d(ptx::smem_u32(sm.q[ring][t]) + hf * C::kQHalf, tm_q, bar(sm.q_full[ring]),
                                      hf * 64, 0, it.kvh, it.t0[t]);
+#pragma unroll
+                for (int i = 0; i < (F8 ? 2 : 0); ++i) // the terms
+                    ptx::tma_load_4d(ptx::smem_u32(sm.q[ring][t]) + i * (BM * D), tm_q, bar(sm.q_full[ring]), 0, 0,
+                                     it.kvh, it.t0[t] + i * p.T);
+            }
         }
         __syncwarp();
         ++item_count;
@@ -280,12 +265,12 @@ __device__ void producer_role(const KernelCtx<D, F8> &cx, const ChunkParams &p, 
             if (j + 1 < it.u_hi)
                 page_next = page_of(j + 1);
             const uint32_t s = kv_count % kStages;
-            ok = warp_wait(bar(*load_empty(sm, s)), ((kv_count / kStages) & 1) ^ 1, cx.wc, W_KV_EMPTY);
+            ok = warp_wait(bar(sm.kv_empty[s]), ((kv_count / kStages) & 1) ^ 1, cx.wc, W_KV_EMPTY);
             if (!ok)
                 break;
             const int left = it.L - j * kBN;
             const int boxes = left <= 0 ? 0 : min(kBoxes, (left + kBox - 1) / kBox);
-            const uint32_t b_full = bar(*load_full(sm, s));
+            const uint32_t b_full = bar(sm.kv_full[s]);
             if (lane == 0)
                 ptx::mbar_arrive_expect_tx(b_full, static_cast<uint32_t>(2 * boxes * kBox) * (F8 ? 1 : 2) * D);
             __syncwarp();
@@ -293,7 +278,7 @@ __device__ void producer_role(const KernelCtx<D, F8> &cx, const ChunkParams &p, 
                 const int key = j * kBN + static_cast<int>(lane) * kBox;
                 const int at = p.page_shift < 0 ? key : key & ((1 << p.page_shift) - 1);
                 if constexpr (F8) {
-                    ptx::tma_load_4d(ptx::smem_u32(sm.raw_k[s]) + lane * kBox * D, tm_k, b_full, 0, at, it.kvh, page);
+                    ptx::tma_load_4d(ptx::smem_u32(sm.k[s]) + lane * kBox * D, tm_k, b_full, 0, at, it.kvh, page);
                     ptx::tma_load_4d(ptx::smem_u32(sm.raw_v[s]) + lane * kBox * D, tm_v, b_full, 0, at, it.kvh, page);
                 }
                 const uint32_t off = lane * kBox * C::kRowBytes;
@@ -320,7 +305,7 @@ __device__ void producer_role(const KernelCtx<D, F8> &cx, const ChunkParams &p, 
         // wait (bounded, ignoring the abort) for this warp's own loads in flight
         const uint32_t first = kv_count > kStages ? kv_count - kStages : 0;
         for (uint32_t idx = first; idx < kv_count; ++idx)
-            mbar_wait_drain(bar(*load_full(sm, idx % kStages)), (idx / kStages) & 1, cx.wc, W_DRAIN);
+            mbar_wait_drain(bar(sm.kv_full[idx % kStages]), (idx / kStages) & 1, cx.wc, W_DRAIN);
         for (uint32_t n = item_count > 2 ? item_count - 2 : 0; n < item_count; ++n)
             mbar_wait_drain(bar(sm.q_full[n & 1]), (n >> 1) & 1, cx.wc, W_DRAIN);
     }
@@ -328,12 +313,13 @@ __device__ void producer_role(const KernelCtx<D, F8> &cx, const ChunkParams &p, 
 
 // ------------------------------------------------------------------ conversion
 
-// Converts the tiles of a cache in 8 bits, keys that no row sees to zeros.  Four warps.
+// Converts the tiles of V of a cache in 8 bits, keys that no row sees to zeros.  Four
+// warps.
 template <int D>
 __device__ void convert_role(const KernelCtx<D, true> &cx, const ChunkParams &p)
 {
     using C = ChunkCfg<D, true>;
-    constexpr int kBN = C::kBN, kStages = C::kStages;
+    constexpr int kBN = C::kBN, kStages = C::kStages, kVStages = C::kVStages;
     ChunkSmem<D, true> &sm = *cx.sm;
     uint32_t idx = 0;
     for (uint32_t n = 0;; ++n) {
@@ -348,23 +334,25 @@ __device__ void convert_role(const KernelCtx<D, true> &cx, const ChunkParams &p)
             ptx::mbar_arrive(bar(sm.info_empty[slot]));
         if (stop)
             return;
-        float next = tile_scales(p, b, u_lo * kBN, L, kvh);
+        auto scales_of = [&](int j) {
+            return tile_scales(p, p.v_scale, p.vs_p, p.vs_b, b, j * kBN, key_lo, L, kvh);
+        };
+        float next = scales_of(u_lo);
         for (int j = u_lo; j < u_hi; ++j, ++idx) {
             const float scales = next;
             if (j + 1 < u_hi)
-                next = tile_scales(p, b, (j + 1) * kBN, L, kvh);
-            const uint32_t stage = idx % kStages, phase = (idx / kStages) & 1;
+                next = scales_of(j + 1);
+            const uint32_t from = idx % kStages, to = idx % kVStages;
             const int j0 = j * kBN, dead_lo = min(kBN, max(0, key_lo - j0)), dead_hi = min(kBN, max(0, L - j0));
-            if (!warp_wait(bar(sm.raw_full[stage]), phase, cx.wc, W_KV_FULL) ||
-                !warp_wait(bar(sm.kv_empty[stage]), phase ^ 1, cx.wc, W_KV_EMPTY))
+            if (!warp_wait(bar(sm.kv_full[from]), (idx / kStages) & 1, cx.wc, W_KV_FULL) ||
+                !warp_wait(bar(sm.v_empty[to]), ((idx / kVStages) & 1) ^ 1, cx.wc, W_KV_EMPTY))
                 return;
-            convert_tile<D, kBN>(sm.raw_k[stage], sm.k[stage], scales, 0, dead_lo, dead_hi);
-            convert_tile<D, kBN>(sm.raw_v[stage], sm.v[stage], scales, 8, dead_lo, dead_hi);
+            convert_tile<D, kBN>(sm.raw_v[from], sm.v[to], scales, dead_lo, dead_hi);
             ptx::fence_proxy_async_smem();
             __syncwarp();
             if (ptx::lane_id() == 0) {
-                ptx::mbar_arrive(bar(sm.kv_full[stage]));
-                ptx::mbar_arrive(bar(sm.raw_empty[stage]));
+                ptx::mbar_arrive(bar(sm.v_full[to]));
+                ptx::mbar_arrive(bar(sm.kv_empty[from]));
             }
         }
     }
@@ -385,9 +373,9 @@ __device__ void s_role(const KernelCtx<D, F8> &cx)
     constexpr int kBN = C::kBN, kStages = C::kStages;
     ChunkSmem<D, F8> &sm = *cx.sm;
     const uint32_t lane = ptx::lane_id();
-    constexpr uint32_t idesc_qk = umma_idesc_bf16(BM, kBN, false);
-    constexpr uint64_t kHiK = umma_desc_hi(16, C::kGroupBytes, kSwizzle128B); // Q, K: K-major
-    constexpr uint32_t kTileLo = C::kTileBytes >> 4, kKVLo = C::kKVBytes >> 4;
+    constexpr uint32_t idesc_qk = F8 ? umma_idesc_e4m3(BM, kBN) : umma_idesc_bf16(BM, kBN, false);
+    constexpr uint64_t kHiK = umma_desc_hi(16, 8 * C::kRowLen, C::kRowSwizzle); // Q, K: K-major
+    constexpr uint32_t kTileLo = C::kTileBytes >> 4, kKVLo = C::kLoadBytes >> 4;
     const uint32_t q_lo0 = ptx::smem_u32(sm.q[0][0]) >> 4;
     const uint32_t k_lo0 = ptx::smem_u32(sm.k[0]) >> 4;
     uint32_t idx = 0, issued[2] = {0u, 0u};
@@ -422,14 +410,17 @@ __device__ void s_role(const KernelCtx<D, F8> &cx)
             // issue, s_full, p_full and the P V issue.
             const int j0 = j * kBN;
             const int dead_lo = min(kBN, max(0, key_lo - j0)), dead_hi = min(kBN, max(0, L - j0));
-            if (!F8 && (dead_lo > 0 || dead_hi < kBN)) { // in 8 bits the conversion has
+            if ((!F8 || MOD == MOD_SOFTCAP) && (dead_lo > 0 || dead_hi < kBN)) {
+                constexpr int kUnits = C::kRowLen / 16;
 #pragma unroll
-                for (int hf = 0; hf < (MOD == MOD_SOFTCAP ? 2 : 1) * C::kHalves; ++hf) {
+                for (int hf = F8 ? C::kHalves : 0; hf < (MOD == MOD_SOFTCAP ? 2 : 1) * C::kHalves; ++hf) {
+                    if (F8 && hf > C::kHalves) // whole rows of K; V's the conversion has zeroed
+                        break;
                     uint4 *v = reinterpret_cast<uint4 *>((hf < C::kHalves ? sm.v[stage] : sm.k[stage]) +
                                                          hf % C::kHalves * C::kKVHalf);
-                    for (int c = lane; c < dead_lo * 8; c += 32)
+                    for (int c = lane; c < dead_lo * kUnits; c += 32)
                         v[c] = make_uint4(0, 0, 0, 0);
-                    for (int c = dead_hi * 8 + lane; c < kBN * 8; c += 32)
+                    for (int c = dead_hi * kUnits + lane; c < kBN * kUnits; c += 32)
                         v[c] = make_uint4(0, 0, 0, 0);
                 }
                 ptx::fence_proxy_async_smem();
@@ -451,8 +442,14 @@ __device__ void s_role(const KernelCtx<D, F8> &cx)
                 if (lane == 0) {
                     const uint32_t qlo = q_lo0 + (2 * ring + (pair ? t : 0)) * kTileLo;
                     const uint32_t tS = cx.tmem + C::kColS + C::kStrideS * t;
+                    if constexpr (F8) { // both terms of Q with the same K
 #pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
+                        for (int kk = 0; kk < D / 16; ++kk)
+                            ptx::mma_ss_f8(tS, kHiK | (qlo + kk / (D / 32) * (BM * D >> 4) + 2 * (kk % (D / 32))),
+                                           kHiK | (klo + 2 * (kk % (D / 32))), idesc_qk, kk > 0 ? 1u : 0u);
+                    }
+#pragma unroll
+                    for (int kk = 0; kk < (F8 ? 0 : D / 16); ++kk) {
                         const uint32_t qo = (kk / 4) * (C::kQHalf >> 4) + 2 * (kk % 4);
                         const uint32_t ko = (kk / 4) * (C::kKVHalf >> 4) + 2 * (kk % 4);
                         ptx::mma_ss(tS, kHiK | (qlo + qo), kHiK | (klo + ko), idesc_qk, kk > 0 ? 1u : 0u);
@@ -463,6 +460,11 @@ __device__ void s_role(const KernelCtx<D, F8> &cx)
             }
             if (!ok)
                 break;
+            if (F8) {
+                if (lane == 0)
+                    ptx::mma_commit(bar(sm.kv_empty[stage])); // K has been read
+                __syncwarp();
+            }
         }
         if (!ok)
             break;
@@ -482,9 +484,10 @@ template <int D, bool F8>
 __device__ void pv_role(const KernelCtx<D, F8> &cx, int t)
 {
     using C = ChunkCfg<D, F8>;
-    constexpr int kBN = C::kBN, kStages = C::kStages;
+    constexpr int kBN = C::kBN, kStages = C::kVStages;
     ChunkSmem<D, F8> &sm = *cx.sm;
     const uint32_t lane = ptx::lane_id();
+    uint64_t *const full = F8 ? sm.v_full : sm.kv_full, *const empty = F8 ? sm.v_empty : sm.kv_empty;
     constexpr uint32_t idesc_pv = umma_idesc_bf16(BM, C::kDvExt, true);
     constexpr uint32_t kKVLo = C::kKVBytes >> 4;
     const uint32_t v_lo0 = ptx::smem_u32(sm.v[0]) >> 4;
@@ -510,11 +513,11 @@ __device__ void pv_role(const KernelCtx<D, F8> &cx, int t)
             const uint32_t stage = idx % kStages;
             if (!uses(j, first, hi, step)) {
                 // tile not used by this slot: release it once it has landed
-                ok = warp_wait(bar(sm.kv_full[stage]), (idx / kStages) & 1, cx.wc, W_KV_FULL);
+                ok = warp_wait(bar(full[stage]), (idx / kStages) & 1, cx.wc, W_KV_FULL);
                 if (!ok)
                     break;
                 if (lane == 0)
-                    ptx::mbar_arrive(bar(sm.kv_empty[stage]));
+                    ptx::mbar_arrive(bar(empty[stage]));
                 __syncwarp();
                 continue;
             }
@@ -522,6 +525,11 @@ __device__ void pv_role(const KernelCtx<D, F8> &cx, int t)
             if (!ok)
                 break;
             ++pcount;
+            if (F8) { // S has waited for K alone
+                ok = warp_wait(bar(full[stage]), (idx / kStages) & 1, cx.wc, W_KV_FULL);
+                if (!ok)
+                    break;
+            }
             ptx::tc_fence_after();
             if (lane == 0) {
                 // D = 64: O += P [V_j | 1] (V's second column block is the ones
@@ -534,7 +542,7 @@ __device__ void pv_role(const KernelCtx<D, F8> &cx, int t)
                     ptx::mma_ts(tO, tP + 8 * kk, hi_v | (vlo + kk * (16 * C::kRowBytes >> 4)), idesc_pv,
                                 (j > first || kk > 0) ? 1u : 0u);
                 ptx::mma_commit(bar(sm.pv_done[t]));
-                ptx::mma_commit(bar(sm.kv_empty[stage]));
+                ptx::mma_commit(bar(empty[stage]));
             }
             __syncwarp();
         }
@@ -754,6 +762,19 @@ __device__ void softmax_role(const KernelCtx<D, F8> &cx, const ChunkParams &p, i
             }
         if (active) {
             const int pos0 = inf.pos0[t], L = inf.L;
+            // 8 bits: the scale of this row's Q; those of a tile's keys, 16 to a lane, a tile ahead
+            float q_scale = 1.f, next = 0.f;
+            auto scales_of = [&](int j) {
+                return tile_scales(p, p.k_scale, p.ks_p, p.ks_b, inf.b, j * kBN, inf.key_lo, L, inf.kvh);
+            };
+            if constexpr (F8) {
+                const int r_tok = fast_div(r, p.div_g);
+                if (r < inf.rows[t])
+                    q_scale = __ldcg(p.q_scale + static_cast<int64_t>(inf.t0[t] + r_tok) * p.Hq + inf.kvh * p.G + r - r_tok * p.G);
+                if (n_mine)
+                    next = scales_of(first);
+            }
+            const float qk = p.qk_log2 * q_scale, cap_in = p.softcap_in * q_scale;
             int row_lo, row_hi, full_lo, full_hi, unused;
             {
                 const int pos = pos0 + fast_div(r, p.div_g), last = pos0 + fast_div(inf.rows[t] - 1, p.div_g);
@@ -762,6 +783,9 @@ __device__ void softmax_role(const KernelCtx<D, F8> &cx, const ChunkParams &p, i
                 key_range(p, L, pos0, pos0, unused, full_hi);
             }
             for (int kk = 0; kk < n_mine; ++kk) {
+                const float scales = next;
+                if (F8 && kk + 1 < n_mine)
+                    next = scales_of(first + (kk + 1) * step);
                 if (!warp_wait(bar(sm.s_full[t]), scount & 1, cx.wc, W_S_FULL))
                     return;
                 ++scount;
@@ -770,19 +794,28 @@ __device__ void softmax_role(const KernelCtx<D, F8> &cx, const ChunkParams &p, i
                 load_scores<kBN>(tS, x);
                 ptx::tc_fence_before();
                 ptx::mbar_arrive(bar(sm.s_free[t])); // S[t] may be overwritten
+                if constexpr (F8) {
+#pragma unroll
+                    for (int g = 0; g < kBN / 16; ++g) {
+                        const float k = __shfl_sync(0xffffffffu, scales, g);
+#pragma unroll
+                        for (int e = 16 * g; e < 16 * g + 16; e += 2)
+                            ptx::fma2(x[e], x[e + 1], x[e], x[e + 1], k, k, 0.f, 0.f);
+                    }
+                }
                 if (take_turns && !turn_wait())
                     return;
                 const int j0 = (first + kk * step) * kBN;
                 if constexpr (MOD == MOD_SOFTCAP)
-                    softcap_scores<kBN>(x, p.softcap_in, p.softcap_out);
+                    softcap_scores<kBN>(x, F8 ? cap_in : p.softcap_in, p.softcap_out);
                 if (!(j0 >= full_lo && j0 + kBN <= full_hi))
                     apply_row_mask<kBN>(x, j0, row_lo, row_hi);
                 uint32_t pk[kBN / 2];
                 bool rescale;
                 const float alpha =
-                    C::kOnes ? softmax_compute_p_exact_sum<kBN>(x, MOD == MOD_NONE ? p.qk_log2 : 1.f, st, false,
+                    C::kOnes ? softmax_compute_p_exact_sum<kBN>(x, MOD == MOD_NONE ? (F8 ? qk : p.qk_log2) : 1.f, st, false,
                                                                 pk, rescale)
-                             : softmax_compute_p<kBN>(x, MOD == MOD_NONE ? p.qk_log2 : 1.f, st, false, pk,
+                             : softmax_compute_p<kBN>(x, MOD == MOD_NONE ? (F8 ? qk : p.qk_log2) : 1.f, st, false, pk,
                                                       rescale);
                 if (take_turns) {
                     ptx::mbar_arrive(b_turn_other); // hand the turn over
@@ -910,12 +943,12 @@ __global__ void __launch_bounds__(chunk_threads(F8), 1)
             ptx::mbar_init(bar(sm->info_empty[b]), F8 ? 15 : 11); // S, two P V, eight softmax and four converting warps
         }
         for (int s = 0; s < kStages; ++s) {
-            ptx::mbar_init(bar(sm->kv_full[s]), F8 ? 4 : 1); // one arrival per converting warp
-            ptx::mbar_init(bar(sm->kv_empty[s]), 2); // one arrival per P V warp
-            if constexpr (F8) {
-                ptx::mbar_init(bar(sm->raw_full[s]), 1);
-                ptx::mbar_init(bar(sm->raw_empty[s]), 4);
-            }
+            ptx::mbar_init(bar(sm->kv_full[s]), 1);
+            ptx::mbar_init(bar(sm->kv_empty[s]), F8 ? 5 : 2); // one arrival per P V warp; or S's and each converting warp's
+        }
+        for (int s = 0; s < (F8 ? C::kVStages : 0); ++s) {
+            ptx::mbar_init(bar(sm->v_full[s]), 4);
+            ptx::mbar_init(bar(sm->v_empty[s]), 2);
         }
         for (int t = 0; t < 2; ++t) {
             ptx::mbar_init(bar(sm->s_full[t]), 1);
@@ -1036,7 +1069,9 @@ cudaError_t launch_mod(const ChunkMaps &maps, ChunkParams &p, cudaStream_t strea
     while (threads < kPlanThreads && (threads < p.batch || threads < p.max_entries))
         threads *= 2;
     const int block = std::min(std::max(threads, (2 * p.n_cta + 31) & ~31), kPlanThreads);
-    chunk_plan_kernel<D><<<1, block, 0, stream>>>(p, threads);
+    // in 8 bits q is split beside it, a few rows to a thread where there are many
+    const int64_t split = F8 ? (static_cast<int64_t>(p.T) * p.Hq * (D / 8) + block - 1) / block : 0;
+    chunk_plan_kernel<D, F8><<<1 + static_cast<int>(std::min<int64_t>(split, p.n_cta - 1)), block, 0, stream>>>(p, threads);
     e = cudaGetLastError();
     // groups of more than kFewRows heads have row blocks alone, and no more
     // tokens than few rows hold make no row block.  Where both may have work the
@@ -1050,7 +1085,7 @@ cudaError_t launch_mod(const ChunkMaps &maps, ChunkParams &p, cudaStream_t strea
                               static_cast<double>(p.n_cta) * FewCfg<D, F8>::kStages * FewCfg<D, F8>::kBN;
     auto launch = [&](bool few_kernel) {
         const cudaError_t err = few_kernel
-            ? launch_after(chunk_few_kernel<MOD, D, F8>, dim3(p.n_cta), chunk_threads(F8), smem_bytes<FewSmem<D, F8>>(), stream, maps, p)
+            ? launch_after(chunk_few_kernel<MOD, D, F8>, dim3(p.n_cta), kThreads, smem_bytes<FewSmem<D, F8>>(), stream, maps, p)
             : launch_after(chunk_kernel<MOD, D, F8>, dim3(p.n_cta), chunk_threads(F8), smem_bytes<ChunkSmem<D, F8>>(), stream, maps, p);
         p.second = 1;
         p.warm = 0;

@@ -33,6 +33,14 @@
 // shorter ones pay more is the plan (6 us until it is seen), the first loads
 // (5 us), the uneven end (5 us) and the joins (5 us).
 //
+// A cache in 8 bits (F8) goes through the same rings and products as it is, half the bytes a
+// tile: tcgen05's kind::f8f6f4 multiplies its e4m3 codes.  Q comes as two e4m3 terms, which
+// hold a bf16 number exactly (split_q), and a key's scale, one number per TMEM lane, goes
+// into its scores.  V's scale goes into P, as two e4m3 terms against a reference of
+// their own (kFewPTop): off by 2^-9 of a weight down to 2^-12 of the row's largest
+// product of weight and scale, and by 2^-22 of that one below.  The sums of the weights are
+// taken from the fp32 ones.
+//
 //   warp  0     walks the CTA's items, publishes them, loads Q, K and V by TMA
 //   warp  1     issues S^T of both slots
 //   warps 2, 3  issue O^T of slot 0, slot 1, after zeroing V rows that no row sees
@@ -54,21 +62,19 @@ constexpr float kFewRange = 60.f; // log2 units
 template <int D, bool F8 = false>
 struct FewCfg {
     static constexpr int kBN = kFewTile;
-    static constexpr int kHalves = D / 64;
-    static constexpr int kThreads = chunk_threads(F8);
-    static constexpr int kStages = F8 ? (D == 128 ? 2 : 3) : D == 128 ? 3 : 6; // of K, and of V
-    static constexpr int kLag = F8 ? 0 : D == 128 ? 1 : 2;  // tiles that V is loaded behind K
+    static constexpr int kHalves = F8 ? 1 : D / 64;
+    static constexpr int kStages = F8 ? (D == 128 ? 5 : 10) : D == 128 ? 3 : 6; // of K, and of V
+    static constexpr int kLag = F8 ? (D == 128 ? 2 : 3) : D == 128 ? 1 : 2; // tiles that V is loaded behind K
     static_assert(kLag < kStages, "K of the lag's tiles is loaded before V frees anything");
-    static constexpr uint32_t kRowBytes = 128;              // a 64-column half row
+    static constexpr uint32_t kRowBytes = F8 ? D : 128;     // a row, or 64 columns of it
+    static constexpr uint32_t kRowSwizzle = kRowBytes == 64 ? kSwizzle64B : kSwizzle128B;
     static constexpr uint32_t kGroupBytes = 8 * kRowBytes;
-    static constexpr uint32_t kQHalf = kFewRows * kRowBytes;
-    static constexpr uint32_t kQBytes = kHalves * kQHalf;
-    static constexpr uint32_t kHalf = kBN * kRowBytes;      // half a K or V tile
+    static constexpr uint32_t kQPart = kFewRows * kRowBytes; // half the columns of Q, or one of its two terms
+    static constexpr int kQParts = F8 ? 2 : kHalves;
+    static constexpr uint32_t kQBytes = kQParts * kQPart;
+    static constexpr uint32_t kHalf = kBN * kRowBytes;      // half a K or V tile, or all of it
     static constexpr uint32_t kTileBytes = kHalves * kHalf;
-    // what TMA loads: these tiles, or ones in 8 bits that are converted to them
-    static constexpr int kLoadStages = F8 ? (D == 128 ? 1 : 4) : kStages, kLoadHalves = F8 ? 1 : kHalves;
-    static constexpr uint32_t kLoadRow = F8 ? D : kRowBytes, kLoadHalf = kBN * kLoadRow, kLoadBytes = kLoadHalves * kLoadHalf;
-    static constexpr uint32_t kPRow = 64;                   // bytes of a key's row of P: two terms of 8 or 16 rows
+    static constexpr uint32_t kPRow = F8 ? 32 : 64;         // bytes of a key's row of P: two terms of 8 or 16 rows
     static constexpr uint32_t kColS = 0, kColO = 64, kStride = 32; // TMEM columns of slot t: + 32 t
 };
 
@@ -103,19 +109,8 @@ __device__ __forceinline__ FewTiles few_tiles(const FewItem &it, int t)
     return f;
 }
 
-// What TMA loads of a cache in 8 bits, ahead of its conversion.
 template <int D, bool F8>
-struct FewRaw {};
-template <int D>
-struct __align__(1024) FewRaw<D, true> {
-    using C = FewCfg<D, true>;
-    uint8_t raw_k[C::kLoadStages][C::kLoadBytes], raw_v[C::kLoadStages][C::kLoadBytes];
-    uint64_t raw_k_full[C::kLoadStages], raw_k_empty[C::kLoadStages];
-    uint64_t raw_v_full[C::kLoadStages], raw_v_empty[C::kLoadStages];
-};
-
-template <int D, bool F8>
-struct __align__(1024) FewSmem : FewRaw<D, F8> {
+struct __align__(1024) FewSmem {
     using C = FewCfg<D, F8>;
     uint8_t k[C::kStages][C::kTileBytes];
     uint8_t v[C::kStages][C::kTileBytes];
@@ -131,6 +126,7 @@ struct __align__(1024) FewSmem : FewRaw<D, F8> {
     FewItem info[kInfo];
     float red[2][4][kFewRows];       // maxima or sums of each softmax warp
     uint32_t rows[2][2][4];          // by tile parity, of each softmax warp: see few_softmax
+    uint32_t large[2][2][4];         // the same of rows whose P asks for a reference (8 bits)
     uint32_t tmem_base;
     uint32_t abort_flag;
 };
@@ -150,7 +146,7 @@ template <int D, bool F8>
 struct FewRing {
     using C = FewCfg<D, F8>;
     const CUtensorMap *map;
-    uint8_t (*tile)[C::kLoadBytes];
+    uint8_t (*tile)[C::kTileBytes];
     uint64_t *full, *empty;
     uint32_t count;
 
@@ -159,19 +155,19 @@ struct FewRing {
     {
         const int lane = static_cast<int>(ptx::lane_id());
         const int box = 1 << p.few_shift, key0 = (v >> it.shift) * C::kBN, left = it.L - key0;
-        const uint32_t s = count % C::kLoadStages;
-        if (!warp_wait(bar(empty[s]), ((count / C::kLoadStages) & 1) ^ 1, cx.wc, W_KV_EMPTY))
+        const uint32_t s = count % C::kStages;
+        if (!warp_wait(bar(empty[s]), ((count / C::kStages) & 1) ^ 1, cx.wc, W_KV_EMPTY))
             return false;
         const int boxes = left <= 0 ? 0 : min(C::kBN >> p.few_shift, (left + box - 1) >> p.few_shift);
         if (lane == 0)
-            ptx::mbar_arrive_expect_tx(bar(full[s]), static_cast<uint32_t>(C::kLoadHalves * boxes * box) * C::kLoadRow);
+            ptx::mbar_arrive_expect_tx(bar(full[s]), static_cast<uint32_t>(C::kHalves * boxes * box) * C::kRowBytes);
         __syncwarp();
         if (lane < boxes) {
             const int key = key0 + lane * box;
             const int at = p.page_shift < 0 ? key : key & ((1 << p.page_shift) - 1);
 #pragma unroll
-            for (int hf = 0; hf < C::kLoadHalves; ++hf)
-                ptx::tma_load_4d(ptx::smem_u32(tile[s]) + hf * C::kLoadHalf + lane * box * C::kLoadRow, map,
+            for (int hf = 0; hf < C::kHalves; ++hf)
+                ptx::tma_load_4d(ptx::smem_u32(tile[s]) + hf * C::kHalf + lane * box * C::kRowBytes, map,
                                  bar(full[s]), hf * 64, at, it.kvh + (it.shift ? v & 1 : 0), page);
         }
         __syncwarp();
@@ -182,8 +178,8 @@ struct FewRing {
     // Waits (bounded, ignoring the abort) for the warp's loads in flight.
     __device__ __forceinline__ void drain(const FewCtx<D, F8> &cx) const
     {
-        for (uint32_t idx = count > C::kLoadStages ? count - C::kLoadStages : 0; idx < count; ++idx)
-            mbar_wait_drain(bar(full[idx % C::kLoadStages]), (idx / C::kLoadStages) & 1, cx.wc, W_DRAIN);
+        for (uint32_t idx = count > C::kStages ? count - C::kStages : 0; idx < count; ++idx)
+            mbar_wait_drain(bar(full[idx % C::kStages]), (idx / C::kStages) & 1, cx.wc, W_DRAIN);
     }
 };
 
@@ -204,23 +200,6 @@ __device__ __forceinline__ int few_page(const ChunkParams &p, const FewItem &it,
 // with larger pages (of 32 keys: 108 against 104 us of 512 to 8192).
 __device__ __forceinline__ bool few_split_loads(const ChunkParams &p) { return p.few_shift < 5; }
 
-template <int D, bool F8>
-__device__ __forceinline__ FewRing<D, F8> few_ring_k(FewSmem<D, F8> &sm, const CUtensorMap *map)
-{
-    if constexpr (F8)
-        return {map, sm.raw_k, sm.raw_k_full, sm.raw_k_empty, 0u};
-    else
-        return {map, sm.k, sm.k_full, sm.k_empty, 0u};
-}
-template <int D, bool F8>
-__device__ __forceinline__ FewRing<D, F8> few_ring_v(FewSmem<D, F8> &sm, const CUtensorMap *map)
-{
-    if constexpr (F8)
-        return {map, sm.raw_v, sm.raw_v_full, sm.raw_v_empty, 0u};
-    else
-        return {map, sm.v, sm.v_full, sm.v_empty, 0u};
-}
-
 // Walks the CTA's items, publishes them, loads Q, K and, mostly, V.
 template <int D, bool F8>
 __device__ void few_producer(const FewCtx<D, F8> &cx, const ChunkParams &p, const CUtensorMap *tm_q,
@@ -230,7 +209,7 @@ __device__ void few_producer(const FewCtx<D, F8> &cx, const ChunkParams &p, cons
     constexpr int kBN = C::kBN;
     FewSmem<D, F8> &sm = *cx.sm;
     const uint32_t lane = ptx::lane_id();
-    FewRing<D, F8> keys = few_ring_k<D, F8>(sm, tm_k), values = few_ring_v<D, F8>(sm, tm_v);
+    FewRing<D, F8> keys{tm_k, sm.k, sm.k_full, sm.k_empty, 0u}, values{tm_v, sm.v, sm.v_full, sm.v_empty, 0u};
     const bool split = few_split_loads(p);
     uint32_t item_count = 0;
     bool ok = true;
@@ -241,6 +220,8 @@ __device__ void few_producer(const FewCtx<D, F8> &cx, const ChunkParams &p, cons
     bool warm = p.warm;
     if (!warm)
         read_part(p, 1, cta, me, e, h, k);
+    if (F8)
+        ptx::fence_proxy_async_all(); // Q's terms, which the planning kernel has written
     for (;;) {
         // ---- the next part
         FewItem it{};
@@ -319,12 +300,12 @@ __device__ void few_producer(const FewCtx<D, F8> &cx, const ChunkParams &p, cons
         if (lane == 0) {
             const int slots = warm ? 0 : it.heads;
             ptx::mbar_arrive_expect_tx(bar(sm.q_full[ring]),
-                                       static_cast<uint32_t>(slots * C::kHalves * p.few_tq * p.G) * C::kRowBytes);
+                                       static_cast<uint32_t>(slots * C::kQParts * p.few_tq * p.G) * C::kRowBytes);
             for (int t = 0; t < slots; ++t)
 #pragma unroll
-                for (int hf = 0; hf < C::kHalves; ++hf)
-                    ptx::tma_load_4d(ptx::smem_u32(sm.q[ring][t]) + hf * C::kQHalf, tm_q, bar(sm.q_full[ring]),
-                                     hf * 64, 0, it.kvh + t, it.t0);
+                for (int i = 0; i < C::kQParts; ++i)
+                    ptx::tma_load_4d(ptx::smem_u32(sm.q[ring][t]) + i * C::kQPart, tm_q, bar(sm.q_full[ring]),
+                                     F8 ? 0 : i * 64, 0, it.kvh + t, it.t0 + (F8 ? i * p.T : 0));
         }
         __syncwarp();
         ++item_count;
@@ -351,6 +332,8 @@ __device__ void few_producer(const FewCtx<D, F8> &cx, const ChunkParams &p, cons
         if (warm) {
             warm = false;
             read_part(p, 1, cta, me, e, h, k);
+            if (F8)
+                ptx::fence_proxy_async_all();
             continue;
         }
         // ---- on to the next item
@@ -373,7 +356,7 @@ template <int D, bool F8>
 __device__ void few_v_producer(const FewCtx<D, F8> &cx, const ChunkParams &p, const CUtensorMap *tm_v)
 {
     FewSmem<D, F8> &sm = *cx.sm;
-    FewRing<D, F8> values = few_ring_v<D, F8>(sm, tm_v);
+    FewRing<D, F8> values{tm_v, sm.v, sm.v_full, sm.v_empty, 0u};
     bool ok = true;
     for (uint32_t n = 0; ok; ++n) {
         const uint32_t slot = n % kInfo;
@@ -397,62 +380,6 @@ __device__ void few_v_producer(const FewCtx<D, F8> &cx, const ChunkParams &p, co
     values.drain(cx);
 }
 
-// ------------------------------------------------------------------ conversion
-
-// Converts the tiles of a cache in 8 bits, keys that no row sees to zeros.  Four warps.
-template <int D>
-__device__ void few_convert_role(const FewCtx<D, true> &cx, const ChunkParams &p)
-{
-    using C = FewCfg<D, true>;
-    constexpr int kBN = C::kBN;
-    FewSmem<D, true> &sm = *cx.sm;
-    uint32_t idx = 0;
-    for (uint32_t n = 0;; ++n) {
-        const uint32_t slot = n % kInfo;
-        if (!warp_wait(bar(sm.info_full[slot]), (n / kInfo) & 1, cx.wc, W_INFO_FULL))
-            return;
-        const FewItem it = sm.info[slot];
-        __syncwarp();
-        if (ptx::lane_id() == 0)
-            ptx::mbar_arrive(bar(sm.info_empty[slot]));
-        if (it.stop)
-            return;
-        auto scales_of = [&](int v) {
-            return tile_scales(p, it.b, (v >> it.shift) * kBN, it.L, it.kvh + (it.shift ? v & 1 : 0));
-        };
-        float next = scales_of(it.u_lo);
-        for (int v = it.u_lo; v < it.u_hi; ++v, ++idx) {
-            const float scales = next;
-            if (v + 1 < it.u_hi)
-                next = scales_of(v + 1);
-            const uint32_t raw = idx % C::kLoadStages, raw_phase = (idx / C::kLoadStages) & 1;
-            const uint32_t stage = idx % C::kStages, phase = (idx / C::kStages) & 1;
-            const int j0 = (v >> it.shift) * kBN;
-            const int dead_lo = min(kBN, max(0, it.key_lo - j0)), dead_hi = min(kBN, max(0, it.L - j0));
-            if (!warp_wait(bar(sm.raw_k_full[raw]), raw_phase, cx.wc, W_KV_FULL) ||
-                !warp_wait(bar(sm.k_empty[stage]), phase ^ 1, cx.wc, W_KV_EMPTY))
-                return;
-            convert_tile<D, kBN>(sm.raw_k[raw], sm.k[stage], scales, 0, dead_lo, dead_hi);
-            ptx::fence_proxy_async_smem();
-            __syncwarp();
-            if (ptx::lane_id() == 0) {
-                ptx::mbar_arrive(bar(sm.k_full[stage]));
-                ptx::mbar_arrive(bar(sm.raw_k_empty[raw]));
-            }
-            if (!warp_wait(bar(sm.raw_v_full[raw]), raw_phase, cx.wc, W_KV_FULL) ||
-                !warp_wait(bar(sm.v_empty[stage]), phase ^ 1, cx.wc, W_KV_EMPTY))
-                return;
-            convert_tile<D, kBN>(sm.raw_v[raw], sm.v[stage], scales, 8, dead_lo, dead_hi);
-            ptx::fence_proxy_async_smem();
-            __syncwarp();
-            if (ptx::lane_id() == 0) {
-                ptx::mbar_arrive(bar(sm.v_full[stage]));
-                ptx::mbar_arrive(bar(sm.raw_v_empty[raw]));
-            }
-        }
-    }
-}
-
 // ------------------------------------------------------------------ MMA issuers
 
 template <int D, bool F8>
@@ -462,8 +389,8 @@ __device__ void few_s_role(const FewCtx<D, F8> &cx)
     constexpr int kBN = C::kBN, kStages = C::kStages;
     FewSmem<D, F8> &sm = *cx.sm;
     const uint32_t lane = ptx::lane_id();
-    constexpr uint32_t idesc = umma_idesc_bf16(kBN, kFewRows, false);
-    constexpr uint64_t kHi = umma_desc_hi(16, C::kGroupBytes, kSwizzle128B); // Q, K: K-major
+    constexpr uint32_t idesc = F8 ? umma_idesc_e4m3(kBN, kFewRows) : umma_idesc_bf16(kBN, kFewRows, false);
+    constexpr uint64_t kHi = umma_desc_hi(16, C::kGroupBytes, C::kRowSwizzle); // Q, K: K-major
     const uint32_t q_lo0 = ptx::smem_u32(sm.q[0][0]) >> 4, k_lo0 = ptx::smem_u32(sm.k[0]) >> 4;
     uint32_t idx = 0, issued[2] = {0u, 0u};
     bool ok = true;
@@ -506,11 +433,19 @@ __device__ void few_s_role(const FewCtx<D, F8> &cx)
             if (lane == 0) {
                 const uint32_t qlo = q_lo0 + (2 * ring + t) * (C::kQBytes >> 4);
                 const uint32_t klo = k_lo0 + stage * (C::kTileBytes >> 4);
+                const uint32_t tS = cx.tmem + C::kColS + C::kStride * t;
+                if constexpr (F8) { // both terms of Q with the same K
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk)
-                    ptx::mma_ss(cx.tmem + C::kColS + C::kStride * t,
-                                kHi | (klo + (kk / 4) * (C::kHalf >> 4) + 2 * (kk % 4)),
-                                kHi | (qlo + (kk / 4) * (C::kQHalf >> 4) + 2 * (kk % 4)), idesc, kk > 0 ? 1u : 0u);
+                    for (int kk = 0; kk < D / 16; ++kk)
+                        ptx::mma_ss_f8(tS, kHi | (klo + 2 * (kk % (D / 32))),
+                                       kHi | (qlo + kk / (D / 32) * (C::kQPart >> 4) + 2 * (kk % (D / 32))), idesc,
+                                       kk > 0 ? 1u : 0u);
+                } else {
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk)
+                        ptx::mma_ss(tS, kHi | (klo + (kk / 4) * (C::kHalf >> 4) + 2 * (kk % 4)),
+                                    kHi | (qlo + (kk / 4) * (C::kQPart >> 4) + 2 * (kk % 4)), idesc, kk > 0 ? 1u : 0u);
+                }
                 ptx::mma_commit(bar(sm.s_full[t]));
                 ptx::mma_commit(bar(sm.k_empty[stage]));
             }
@@ -543,10 +478,13 @@ __device__ void few_pv_role(const FewCtx<D, F8> &cx, int slot_lo, int slot_hi)
     // O^T = V^T P^T: both operands with their long index contiguous.  V^T has
     // 128 rows: at D = 64 the second 64 repeat the first (block stride 0).  P
     // has 64-byte rows of a key, 64-byte swizzle.
-    constexpr uint32_t idesc8 = umma_idesc_bf16(128, 16, true) | (1u << 15);
-    constexpr uint32_t idesc16 = umma_idesc_bf16(128, 32, true) | (1u << 15);
-    constexpr uint64_t kHiV = umma_desc_hi(D == 128 ? C::kHalf : 0, C::kGroupBytes, kSwizzle128B);
-    constexpr uint64_t kHiP = umma_desc_hi(16, 8 * C::kPRow, kSwizzle64B);
+    // In 8 bits V^T's rows are 64 or 128 bytes, P's 32, each swizzled over its length.
+    constexpr uint32_t kMajor = 1u << 15 | 1u << 16;
+    constexpr uint32_t idesc8 = (F8 ? umma_idesc_e4m3(128, 16) : umma_idesc_bf16(128, 16, true)) | kMajor;
+    constexpr uint32_t idesc16 = (F8 ? umma_idesc_e4m3(128, 32) : umma_idesc_bf16(128, 32, true)) | kMajor;
+    constexpr uint64_t kHiV = umma_desc_hi(D == 128 ? C::kHalf : 0, C::kGroupBytes, C::kRowSwizzle);
+    constexpr uint64_t kHiP = umma_desc_hi(16, 8 * C::kPRow, F8 ? kSwizzle32B : kSwizzle64B);
+    constexpr int kKeys = F8 ? 32 : 16; // of an MMA
     const uint32_t v_lo0 = ptx::smem_u32(sm.v[0]) >> 4, p_lo0 = ptx::smem_u32(sm.p[0]) >> 4;
     uint32_t idx = 0, pcount[2] = {0u, 0u};
     bool ok = true;
@@ -581,13 +519,14 @@ __device__ void few_pv_role(const FewCtx<D, F8> &cx, int slot_lo, int slot_hi)
             // rows of V that no query row sees: zero (their P is 0, but the bytes
             // may be anything)
             const int dead_lo = min(kBN, max(0, key_lo - j0)), dead_hi = min(kBN, max(0, L - j0));
-            if (!F8 && (dead_lo > 0 || dead_hi < kBN)) { // in 8 bits the conversion has
+            if (dead_lo > 0 || dead_hi < kBN) {
+                constexpr int kUnits = C::kRowBytes / 16;
 #pragma unroll
                 for (int hf = 0; hf < C::kHalves; ++hf) {
                     uint4 *dst = reinterpret_cast<uint4 *>(sm.v[stage] + hf * C::kHalf);
-                    for (int c = lane; c < dead_lo * 8; c += 32)
+                    for (int c = lane; c < dead_lo * kUnits; c += 32)
                         dst[c] = make_uint4(0, 0, 0, 0);
-                    for (int c = dead_hi * 8 + lane; c < kBN * 8; c += 32)
+                    for (int c = dead_hi * kUnits + lane; c < kBN * kUnits; c += 32)
                         dst[c] = make_uint4(0, 0, 0, 0);
                 }
                 ptx::fence_proxy_async_smem();
@@ -602,9 +541,10 @@ __device__ void few_pv_role(const FewCtx<D, F8> &cx, int slot_lo, int slot_hi)
                 const uint32_t vlo = v_lo0 + stage * (C::kTileBytes >> 4), plo = p_lo0 + t * (kBN * C::kPRow >> 4);
                 const bool begun = v - first >= 1 << shift; // not the slot's first tile
 #pragma unroll
-                for (int kk = 0; kk < kBN / 16; ++kk)
-                    ptx::mma_ss(cx.tmem + C::kColO + C::kStride * t, kHiV | (vlo + kk * (16 * C::kRowBytes >> 4)),
-                                kHiP | (plo + kk * (16 * C::kPRow >> 4)), idesc, (begun || kk > 0) ? 1u : 0u);
+                for (int kk = 0; kk < kBN / kKeys; ++kk)
+                    (F8 ? ptx::mma_ss_f8 : ptx::mma_ss)(
+                        cx.tmem + C::kColO + C::kStride * t, kHiV | (vlo + kk * (kKeys * C::kRowBytes >> 4)),
+                        kHiP | (plo + kk * (kKeys * C::kPRow >> 4)), idesc, (begun || kk > 0) ? 1u : 0u);
                 ptx::mma_commit(bar(sm.pv_done[t]));
                 ptx::mma_commit(bar(sm.v_empty[stage]));
             }
@@ -655,6 +595,12 @@ __device__ __forceinline__ void few_load_o(uint32_t tO, uint32_t (&o)[2 * R])
     ptx::reg_fence<2 * R>(o);
 }
 
+// P in 8 bits: weights times V's scale, 2^(z + log2 s - ref), as two e4m3 terms, the second 16
+// times what the first left out.  A row's reference is set to make the largest of a
+// tile 2^5, and again where one would pass e4m3's 448.
+constexpr float kFewPTop = 5.f, kFewPMost = 8.8f, kFewPRest = 16.f;
+constexpr float kFewPUnset = -1e30f;
+
 // What a softmax thread carries from item to item.
 struct FewState {
     uint32_t s, pv, group, tiles; // phases of s_full, pv_done, group; tiles so far
@@ -674,15 +620,15 @@ __device__ __forceinline__ bool few_item(const FewCtx<D, F8> &cx, const ChunkPar
     const uint32_t tS = cx.tmem + lanes + C::kColS + C::kStride * t;
     const uint32_t tO = cx.tmem + lanes + C::kColO + C::kStride * t;
     const uint32_t b_group = bar(sm.group[t]);
-    const float c = MOD == MOD_NONE ? p.qk_log2 : 1.f;
+    const float c = MOD == MOD_NONE && !F8 ? p.qk_log2 : 1.f; // in 8 bits it is in q_factor
     ScoreMod smod;
     smod.qk_log2 = p.qk_log2;
     smod.softcap_in = p.softcap_in;
     smod.softcap_out = p.softcap_out;
     smod.alibi_c = smod.scale = smod.b = smod.h = 0.f;
-    // 64-byte swizzle: 16-byte unit u of key r at u ^ (r / 2 mod 4)
+    // 64-byte swizzle: 16-byte unit u of key r at u ^ (r / 2 mod 4); 32-byte: at u ^ (r / 4 mod 2)
     uint4 *const pdst = reinterpret_cast<uint4 *>(sm.p[t] + r * C::kPRow);
-    const int sw = (r >> 1) & 3;
+    const int sw = F8 ? (r >> 2) & 1 : (r >> 1) & 3;
     auto group_sync = [&]() {
         ptx::mbar_arrive(b_group);
         return warp_wait(b_group, ct.group++ & 1, cx.wc, W_JOIN);
@@ -705,7 +651,31 @@ __device__ __forceinline__ bool few_item(const FewCtx<D, F8> &cx, const ChunkPar
     }
     uint32_t set = 0;  // rows that have a reference
     bool moved = false; // some reference is not 0
+    // 8 bits: the factor of a row's scores, the reference of its P; this thread's key's scales
+    float q_factor[F8 ? R : 1], mp[F8 ? R : 1];
+    float next_k = 0.f, next_v = 0.f;
+    auto scales_of = [&](int v) {
+        const int key = (v >> inf.shift) * kBN + r;
+        next_k = box_scale(p, p.k_scale, p.ks_p, p.ks_b, inf.b, key, inf.key_lo, inf.L, inf.kvh + t);
+        next_v = box_scale(p, p.v_scale, p.vs_p, p.vs_b, inf.b, key, inf.key_lo, inf.L, inf.kvh + t);
+    };
+    if constexpr (F8) {
+#pragma unroll
+        for (int n = 0; n < R; ++n) {
+            const int s = fast_div(n, p.div_g);
+            mp[n] = n < rows ? kFewPUnset : -kFewPUnset; // columns past the rows ask for nothing
+            q_factor[n] = n < rows && inf.n_parts
+                              ? __ldcg(p.q_scale + static_cast<int64_t>(inf.t0 + s) * p.Hq + (inf.kvh + t) * p.G + n - s * p.G) *
+                                    (MOD == MOD_NONE ? p.qk_log2 : 1.f)
+                              : 0.f;
+        }
+        if (n_mine)
+            scales_of(f.first);
+    }
     for (int kk = 0; kk < n_mine; ++kk) {
+        const float key_k = next_k, key_v = next_v;
+        if (F8 && kk + 1 < n_mine)
+            scales_of(f.first + (kk + 1) * f.step);
         if (!warp_wait(bar(sm.s_full[t]), ct.s & 1, cx.wc, W_S_FULL))
             return false;
         ++ct.s;
@@ -727,6 +697,13 @@ __device__ __forceinline__ bool few_item(const FewCtx<D, F8> &cx, const ChunkPar
         ptx::tc_fence_before();
         ptx::mbar_arrive(bar(sm.s_free[t]));
         const int j0 = ((f.first + kk * f.step) >> inf.shift) * kBN;
+        if constexpr (F8) {
+#pragma unroll
+            for (int n = 0; n < R; n += 2) {
+                ptx::fma2(x[n], x[n + 1], x[n], x[n + 1], key_k, key_k, 0.f, 0.f);
+                ptx::fma2(x[n], x[n + 1], x[n], x[n + 1], q_factor[n], q_factor[n + 1], 0.f, 0.f);
+            }
+        }
         apply_score_mod<MOD, R>(x, smod, 0, j0);
         if (!(j0 >= full_lo && j0 + kBN <= full_hi)) {
 #pragma unroll
@@ -761,6 +738,22 @@ __device__ __forceinline__ bool few_item(const FewCtx<D, F8> &cx, const ChunkPar
         bits = __reduce_or_sync(0xffffffffu, bits);
         if (lane == 0)
             sm.rows[t][ct.tiles & 1][wq] = bits;
+        uint32_t large = 0; // 8 bits: rows whose P wants another reference
+        const float log_v = F8 ? ptx::lg2(key_v) : 0.f;
+        if constexpr (F8) {
+            float most = x[0] - mp[0];
+#pragma unroll
+            for (int n = 1; n < R; ++n)
+                most = fmaxf(most, x[n] - mp[n]);
+            if (most + log_v > kFewPMost) {
+#pragma unroll
+                for (int n = 0; n < R; ++n)
+                    large |= x[n] - mp[n] + log_v > kFewPMost ? 1u << n : 0u;
+            }
+            large = __reduce_or_sync(0xffffffffu, large);
+            if (lane == 0)
+                sm.large[t][ct.tiles & 1][wq] = large;
+        }
         float w[R];
         few_exp(x, c, m, !moved, w);
         if (!group_sync())
@@ -768,6 +761,10 @@ __device__ __forceinline__ bool few_item(const FewCtx<D, F8> &cx, const ChunkPar
         {
             const volatile uint32_t *all = sm.rows[t][ct.tiles & 1];
             bits = all[0] | all[1] | all[2] | all[3];
+        }
+        if constexpr (F8) {
+            const volatile uint32_t *all = sm.large[t][ct.tiles & 1];
+            large = (all[0] | all[1] | all[2] | all[3]) & row_bits;
         }
         if (kk > 0) {
             // the previous tile's product has read P and landed in O^T
@@ -803,7 +800,12 @@ __device__ __forceinline__ bool few_item(const FewCtx<D, F8> &cx, const ChunkPar
                 m[n] = m_new;
             }
             set |= (bits | bits >> 16) & row_bits;
-            if (ask) {
+            if (ask && F8) {
+#pragma unroll
+                for (int n = 0; n < R; ++n)
+                    l[n] *= alpha[n];
+                few_exp(x, c, m, false, w);
+            } else if (ask) {
                 if (kk > 0) {
                     uint32_t o[2 * R];
                     few_load_o<R>(tO, o);
@@ -822,6 +824,65 @@ __device__ __forceinline__ bool few_item(const FewCtx<D, F8> &cx, const ChunkPar
                 few_exp(x, c, m, false, w);
             }
         }
+        if constexpr (F8) {
+            if (large || inf.n_parts == 0) {
+                // the largest of each row, and O^T to its new reference
+                if (!group_sync()) // the maxima above have been read
+                    return false;
+#pragma unroll
+                for (int n = 0; n < R; ++n) {
+                    const int mx = __reduce_max_sync(0xffffffffu, ordered(x[n] + log_v));
+                    if (lane == n)
+                        sm.red[t][wq][n] = unordered(mx);
+                }
+                if (!group_sync())
+                    return false;
+                float beta[R];
+#pragma unroll
+                for (int n = 0; n < R; ++n) {
+                    beta[n] = 1.f;
+                    if (large >> n & 1u) {
+                        const volatile float *red = &sm.red[t][0][n];
+                        const float top = fmaxf(fmaxf(red[0], red[kFewRows]), fmaxf(red[2 * kFewRows], red[3 * kFewRows])) - kFewPTop;
+                        beta[n] = mp[n] == kFewPUnset ? 0.f : ptx::ex2(mp[n] - top);
+                        mp[n] = top;
+                    }
+                }
+                if (kk > 0) {
+                    uint32_t o[2 * R];
+                    few_load_o<R>(tO, o);
+#pragma unroll
+                    for (int n = 0; n < R; ++n) { // a row without a key so far holds zeros
+                        o[n] = __float_as_uint(__uint_as_float(o[n]) * beta[n]);
+                        o[R + n] = __float_as_uint(__uint_as_float(o[R + n]) * beta[n]);
+                    }
+                    if constexpr (R == 8)
+                        ptx::tmem_st16(tO, o);
+                    else
+                        ptx::tmem_st32(tO, o);
+                    ptx::tmem_wait_st();
+                }
+            }
+            uint32_t hi[R / 4], lo[R / 4];
+#pragma unroll
+            for (int n = 0; n < R; n += 4) {
+                float e[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    e[i] = ptx::ex2(x[n + i] - mp[n + i] + log_v);
+                const uint32_t h0 = to_e4m3x2(e[0], e[1]), h1 = to_e4m3x2(e[2], e[3]);
+                const float2 a = from_e4m3x2(h0), b = from_e4m3x2(h1);
+                hi[n / 4] = h0 | h1 << 16;
+                lo[n / 4] = to_e4m3x2((e[0] - a.x) * kFewPRest, (e[1] - a.y) * kFewPRest) |
+                            to_e4m3x2((e[2] - b.x) * kFewPRest, (e[3] - b.y) * kFewPRest) << 16;
+            }
+            if constexpr (R == 8) {
+                pdst[sw] = make_uint4(hi[0], hi[1], lo[0], lo[1]);
+            } else {
+                pdst[sw] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                pdst[1 ^ sw] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            }
+        } else {
         // the key's row of P: R rounded weights, then R rests
         uint32_t hi[R / 2], lo[R / 2];
 #pragma unroll
@@ -834,6 +895,7 @@ __device__ __forceinline__ bool few_item(const FewCtx<D, F8> &cx, const ChunkPar
         for (int u = 0; u < R / 8; ++u) {
             pdst[u ^ sw] = make_uint4(hi[4 * u], hi[4 * u + 1], hi[4 * u + 2], hi[4 * u + 3]);
             pdst[(R / 8 + u) ^ sw] = make_uint4(lo[4 * u], lo[4 * u + 1], lo[4 * u + 2], lo[4 * u + 3]);
+        }
         }
         ptx::fence_proxy_async_smem();
         ptx::tc_fence_before();
@@ -868,7 +930,7 @@ __device__ __forceinline__ bool few_item(const FewCtx<D, F8> &cx, const ChunkPar
         few_load_o<R>(tO, raw);
 #pragma unroll
         for (int n = 0; n < R; ++n)
-            o[n] = __uint_as_float(raw[n]) + __uint_as_float(raw[R + n]);
+            o[n] = __uint_as_float(raw[n]) + __uint_as_float(raw[R + n]) * (F8 ? 1.f / kFewPRest : 1.f);
     } else {
 #pragma unroll
         for (int n = 0; n < R; ++n)
@@ -881,8 +943,11 @@ __device__ __forceinline__ bool few_item(const FewCtx<D, F8> &cx, const ChunkPar
         float *mine = partial<D>(p, inf.cta, inf.mine, t), *sums = mine + kFewRows * 128;
 #pragma unroll
         for (int n = 0; n < R; ++n) {
-            if (n < rows && (D == 128 || (n & 1) == r >> 6))
+            if (n < rows && (D == 128 || (n & 1) == r >> 6)) {
+                if constexpr (F8) // from P's reference to the weights'
+                    o[n] = mp[n] == kFewPUnset ? 0.f : o[n] * ptx::ex2(mp[n] - m[n]);
                 mine[n * 128 + dim] = o[n];
+            }
             if (r == n)
                 sums[n] = m[n];
         }
@@ -899,10 +964,14 @@ __device__ __forceinline__ bool few_item(const FewCtx<D, F8> &cx, const ChunkPar
     // a row's sum per lane, so that the reciprocals and logarithms are taken at once
     const volatile float *red = sm.red[t][0] + (lane & (R - 1));
     const float sum = red[0] + red[kFewRows] + red[2 * kFewRows] + red[3 * kFewRows];
-    const float inv = sum == 0.f ? 0.f : ptx::rcp_approx(sum);
+    const float inv = sum == 0.f ? 0.f : ptx::rcp_approx(sum), log_l = F8 ? ptx::lg2(sum) : 0.f;
 #pragma unroll
     for (int n = 0; n < R; ++n) {
-        const float norm = __shfl_sync(0xffffffffu, inv, n);
+        float norm;
+        if constexpr (F8) // from P's reference to the weights' and over their sum, in one exponent
+            norm = mp[n] == kFewPUnset ? 0.f : ptx::ex2(mp[n] - m[n] - __shfl_sync(0xffffffffu, log_l, n));
+        else
+            norm = __shfl_sync(0xffffffffu, inv, n);
         if (n >= rows || (D == 64 && (n & 1) != r >> 6))
             continue;
         const int s = fast_div(n, p.div_g);
@@ -943,11 +1012,10 @@ __device__ void few_softmax(const FewCtx<D, F8> &cx, const ChunkParams &p, int t
 
 // The kernel of the few rows (see chunk_kernel for what runs beside it).
 template <int MOD, int D, bool F8>
-__global__ void __launch_bounds__(chunk_threads(F8), 1)
+__global__ void __launch_bounds__(kThreads, 1)
     chunk_few_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constant__ ChunkParams p)
 {
     using C = FewCfg<D, F8>;
-    constexpr int kThreads = C::kThreads;
     extern __shared__ uint8_t smem_raw[];
     FewSmem<D, F8> *sm = reinterpret_cast<FewSmem<D, F8> *>(smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u));
     const int warp = threadIdx.x >> 5;
@@ -966,21 +1034,14 @@ __global__ void __launch_bounds__(chunk_threads(F8), 1)
         }
         for (int b = 0; b < kInfo; ++b) {
             ptx::mbar_init(bar(sm->info_full[b]), 1);
-            ptx::mbar_init(bar(sm->info_empty[b]), F8 ? 15 : 11); // all but the producer
+            ptx::mbar_init(bar(sm->info_empty[b]), 11); // all but the producer
         }
         for (int s = 0; s < C::kStages; ++s) {
-            ptx::mbar_init(bar(sm->k_full[s]), F8 ? 4 : 1); // one arrival per converting warp
+            ptx::mbar_init(bar(sm->k_full[s]), 1);
             ptx::mbar_init(bar(sm->k_empty[s]), 1);
-            ptx::mbar_init(bar(sm->v_full[s]), F8 ? 4 : 1);
+            ptx::mbar_init(bar(sm->v_full[s]), 1);
             ptx::mbar_init(bar(sm->v_empty[s]), few_split_loads(p) ? 1 : 2); // the warps that issue O^T
         }
-        if constexpr (F8)
-            for (int s = 0; s < C::kLoadStages; ++s) {
-                ptx::mbar_init(bar(sm->raw_k_full[s]), 1);
-                ptx::mbar_init(bar(sm->raw_k_empty[s]), 4);
-                ptx::mbar_init(bar(sm->raw_v_full[s]), 1);
-                ptx::mbar_init(bar(sm->raw_v_empty[s]), 4);
-            }
         for (int t = 0; t < 2; ++t) {
             ptx::mbar_init(bar(sm->s_full[t]), 1);
             ptx::mbar_init(bar(sm->s_free[t]), 128);
@@ -1005,11 +1066,7 @@ __global__ void __launch_bounds__(chunk_threads(F8), 1)
     cx.sm = sm;
     cx.tmem = sm->tmem_base;
     cx.wc = wait_ctl(p, &sm->abort_flag);
-    if (F8 && warp >= 12) {
-        if constexpr (F8)
-            few_convert_role<D>(cx, p);
-        ptx::named_barrier_sync(1, kThreads);
-    } else if (warp >= 4) {
+    if (warp >= 4) {
         tell_second(p, cx.part);
         few_softmax<MOD, D, F8>(cx, p, (warp >> 2) - 1);
         ptx::tc_fence_before();

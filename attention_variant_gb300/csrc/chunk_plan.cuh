@@ -17,7 +17,8 @@
 namespace fl {
 namespace {
 
-// A cache in 8 bits (F8) takes four warps more, which convert it.
+constexpr int kThreads = 384;
+// Row blocks of a cache in 8 bits (F8) take four warps more, which convert V.
 __host__ __device__ constexpr int chunk_threads(bool f8) { return f8 ? 512 : 384; }
 __host__ __device__ constexpr uint32_t chunk_regs_launch(bool f8) { return f8 ? 128 : 168; }
 __host__ __device__ constexpr uint32_t chunk_regs_other(bool f8) { return f8 ? 56 : 104; }
@@ -200,6 +201,9 @@ __device__ __forceinline__ float *partial(const ChunkParams &p, int cta, int buf
 }
 
 // ------------------------------------------------------------------ planning
+
+template <int D>
+__device__ __forceinline__ void split_q(const ChunkParams &p); // fp8.cuh
 
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanNear = 128; // entries of each list kept at hand
@@ -385,14 +389,20 @@ __device__ __forceinline__ void plan_entries(const ChunkParams &p, PlanShared &s
     }
 }
 
-// One block.  Its first `threads` threads list the entries (as few as make it
+// One block (for a cache in 8 bits, the others split Q).  Its first `threads` threads list the entries (as few as make it
 // one round: the barriers cost what they have to wait for), then all of them
 // cut the parts, one a thread.
-template <int D>
+template <int D, bool F8>
 __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_constant__ ChunkParams p, int threads)
 {
     __shared__ PlanShared sm;
     ptx::launch_dependents();
+    if constexpr (F8) {
+        if (blockIdx.x > 0) {
+            split_q<D>(p);
+            return;
+        }
+    }
     if (static_cast<int>(threadIdx.x) < threads)
         plan_entries<D>(p, sm, threads);
     __syncthreads();

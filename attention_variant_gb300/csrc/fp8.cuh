@@ -11,6 +11,7 @@
 #pragma once
 
 #include "chunk_plan.cuh"
+#include "e4m3.cuh"
 
 namespace fl {
 namespace {
@@ -57,12 +58,12 @@ __device__ __forceinline__ uint2 fp8_to_bf16(uint32_t w, const Fp8Scale &f)
     return make_uint2(out[0], out[1]);
 }
 
-// A scale of the cache: of the 16 keys from `key` on of request b.  Keys past the
-// last and pages outside the cache have none.
+// The scale of a key of request b.  Keys that no row sees and pages outside the
+// cache have none.
 __device__ __forceinline__ float box_scale(const ChunkParams &p, const float *scale, int64_t s_page, int64_t s_block,
-                                           int b, int key, int L, int kvh)
+                                           int b, int key, int key_lo, int L, int kvh)
 {
-    if (key >= L)
+    if (key >= L || key < key_lo)
         return 0.f;
     int page = b, at = key;
     if (p.page_shift >= 0) {
@@ -74,43 +75,44 @@ __device__ __forceinline__ float box_scale(const ChunkParams &p, const float *sc
     return __ldg(scale + page * s_page + static_cast<int64_t>(at >> p.scale_shift) * s_block + kvh);
 }
 
-// The scales of tile j in the lanes of a warp: those of K's boxes of 16 keys in
-// lanes 0 .. 7, of V's in 8 .. 15.
-__device__ __forceinline__ float tile_scales(const ChunkParams &p, int b, int key0, int L, int kvh)
+// The scales of a tile's boxes of 16 keys in the lanes of a warp.  (A box that holds
+// some key that a row sees has that key's.)
+__device__ __forceinline__ float tile_scales(const ChunkParams &p, const float *scale, int64_t s_page, int64_t s_block,
+                                             int b, int key0, int key_lo, int L, int kvh)
 {
-    const int lane = static_cast<int>(ptx::lane_id()), key = key0 + (lane & 7) * 16;
-    if (lane >= 16)
-        return 0.f;
-    return lane < 8 ? box_scale(p, p.k_scale, p.ks_p, p.ks_b, b, key, L, kvh)
-                    : box_scale(p, p.v_scale, p.vs_p, p.vs_b, b, key, L, kvh);
+    const int lane = static_cast<int>(ptx::lane_id());
+    return lane < 8 ? box_scale(p, scale, s_page, s_block, b, key0 + lane * 16, key_lo & ~15, L, kvh) : 0.f;
 }
 
 // A tile of KEYS keys from codes (a key's D bytes after another's) to bf16 in the layout
 // of the 128-byte swizzle, halves of 64 dimensions, by four warps.  Keys outside
-// [dead_lo, dead_hi) become zero.  `scales`: tile_scales, from lane `from` on.
-// 16 codes a thread and step: a 16-byte load and two 16-byte stores, 8 threads of
-// which meet in no bank.
+// [dead_lo, dead_hi) become zero.  16 codes a thread and step: a 16-byte load (all of
+// them first) and two 16-byte stores, 8 threads of which meet in no bank.
 template <int D, int KEYS>
-__device__ __forceinline__ void convert_tile(const uint8_t *raw, uint8_t *dst, float scales, int from, int dead_lo,
-                                             int dead_hi)
+__device__ __forceinline__ void convert_tile(const uint8_t *raw, uint8_t *dst, float scales, int dead_lo, int dead_hi)
 {
-    constexpr int kUnits = D / 16; // of a key
-    const int tid = threadIdx.x & (kConvertThreads - 1);
+    constexpr int kUnits = D / 16, kSteps = (KEYS * kUnits + kConvertThreads - 1) / kConvertThreads;
+    constexpr bool kRagged = KEYS * kUnits % kConvertThreads != 0; // the last step is some warps' alone
+    const int tid = threadIdx.x & (kConvertThreads - 1), u = tid % kUnits;
+    uint4 w[kSteps];
 #pragma unroll
-    for (int c0 = 0; c0 < KEYS * kUnits; c0 += kConvertThreads) {
-        const int c = c0 + tid, key = c / kUnits, u = c % kUnits;
-        if (KEYS * kUnits % kConvertThreads && c >= KEYS * kUnits) // whole warps
+    for (int i = 0; i < kSteps; ++i)
+        if (!kRagged || i + 1 < kSteps || tid + i * kConvertThreads < KEYS * kUnits)
+            w[i] = *reinterpret_cast<const uint4 *>(raw + (tid + i * kConvertThreads) * 16);
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+        const int key = tid / kUnits + i * (kConvertThreads / kUnits);
+        const Fp8Scale f = fp8_scale(__shfl_sync(0xffffffffu, scales, (key >> 4) & 7));
+        if (kRagged && i + 1 == kSteps && tid + i * kConvertThreads >= KEYS * kUnits)
             break;
-        const Fp8Scale f = fp8_scale(__shfl_sync(0xffffffffu, scales, from + (key >> 4)));
-        const uint4 w = *reinterpret_cast<const uint4 *>(raw + c * 16);
         uint4 out[2];
-        const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+        const uint32_t in[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
         uint32_t *o = reinterpret_cast<uint32_t *>(out);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint2 y = fp8_to_bf16(in[i], f);
-            o[2 * i] = y.x;
-            o[2 * i + 1] = y.y;
+        for (int c = 0; c < 4; ++c) {
+            const uint2 y = fp8_to_bf16(in[c], f);
+            o[2 * c] = y.x;
+            o[2 * c + 1] = y.y;
         }
         if (key < dead_lo || key >= dead_hi)
             out[0] = out[1] = make_uint4(0, 0, 0, 0);
@@ -119,6 +121,65 @@ __device__ __forceinline__ void convert_tile(const uint8_t *raw, uint8_t *dst, f
         row[at ^ (key & 7)] = out[0];
         row[(at + 1) ^ (key & 7)] = out[1];
     }
+}
+
+// Q as two e4m3 terms a row, relative to the row's scale: q = s (q1 + q2).  e4m3 has 4
+// significant bits, what rounding to them leaves of bf16's 8 has 4 again, so the
+// terms are exact for elements from 2^-10 of the row's largest on, and off by 2^-18 of
+// it below.  A row with an element that is not finite becomes NaN there.  By the blocks
+// of the planning kernel but the first; q8 [2][T][Hq][D], q_scale [T][Hq].
+template <int D>
+__device__ __forceinline__ void split_q(const ChunkParams &p)
+{
+    constexpr int kLanes = D / 8; // of a row, 8 elements each
+    const int per = blockDim.x / kLanes, y = threadIdx.x / kLanes, u = threadIdx.x % kLanes;
+    const int64_t rows = static_cast<int64_t>(p.T) * p.Hq;
+    for (int64_t r0 = static_cast<int64_t>(blockIdx.x - 1) * per; r0 < rows; r0 += static_cast<int64_t>(gridDim.x - 1) * per) {
+        const int64_t r = r0 + y, tok = r / p.Hq;
+        float x[8];
+        if (r < rows) {
+            const uint4 w = __ldg(reinterpret_cast<const uint4 *>(p.q + tok * p.q_st + (r - tok * p.Hq) * p.q_sh + u * 8));
+            const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x[2 * i] = __uint_as_float(in[i] << 16);
+                x[2 * i + 1] = __uint_as_float(in[i] & 0xffff0000u);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                x[i] = 0.f;
+        }
+        float m = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            m = fmaxf(m, fabsf(x[i]));
+#pragma unroll
+        for (int d = kLanes / 2; d; d >>= 1)
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+        if (r >= rows)
+            continue;
+        const uint32_t s = m < -kNegInf ? scale_bits(__float_as_uint(m)) : 0x3f800000u;
+        const float inv = __uint_as_float((254u << 23) - s); // 1 / s, s a power of two
+        uint32_t a[2] = {0, 0}, b[2] = {0, 0};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float lo = x[2 * i] * inv, hi = x[2 * i + 1] * inv;
+            // an infinity saturates; its difference from that makes the second term's sum NaN
+            const uint32_t t = to_e4m3x2(lo, hi);
+            const float2 v = from_e4m3x2(t);
+            const float l2 = fabsf(lo) < -kNegInf ? lo - v.x : __uint_as_float(0x7fffffffu);
+            const float h2 = fabsf(hi) < -kNegInf ? hi - v.y : __uint_as_float(0x7fffffffu);
+            a[i >> 1] |= t << (16 * (i & 1));
+            b[i >> 1] |= to_e4m3x2(l2, h2) << (16 * (i & 1));
+        }
+        uint8_t *dst = p.q8 + r * D + u * 8;
+        *reinterpret_cast<uint2 *>(dst) = make_uint2(a[0], a[1]);
+        *reinterpret_cast<uint2 *>(dst + rows * D) = make_uint2(b[0], b[1]);
+        if (u == 0)
+            p.q_scale[r] = __uint_as_float(s);
+    }
+    ptx::fence_proxy_async_all(); // TMA reads it
 }
 
 } // namespace

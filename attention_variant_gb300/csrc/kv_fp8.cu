@@ -16,9 +16,9 @@
 // second time out of L2.  Bound by HBM; for single tokens by the launch and one chain of
 // loads.
 #include <cuda_bf16.h>
-#include <cuda_fp16.h>
 #include <cstdint>
 
+#include "e4m3.cuh"
 #include "rope.cuh"
 
 namespace fl {
@@ -27,30 +27,6 @@ namespace {
 constexpr int kRowsKept = 4;      // (token, head) rows a thread keeps
 constexpr int kRunAngles = 4096;  // tokens of a chunk times pairs
 constexpr int kRunHeads = 16;     // heads of a group, at most
-constexpr uint32_t kLeastScale = (127u - 100u) << 23;
-
-// The scale that a block with the largest size a needs, as bits of a float.
-__device__ __forceinline__ uint32_t scale_bits(uint32_t a)
-{
-    const uint32_t e = (a + 0x1fffffu) >> 23; // 448 = 1.75 * 2^8
-    return e > (kLeastScale >> 23) + 8u ? (e - 8u) << 23 : kLeastScale;
-}
-
-// Two values to codes, the first in the low byte.
-__device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi)
-{
-    uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
-// Two codes (the low bytes of c) to values.
-__device__ __forceinline__ float2 from_e4m3x2(uint32_t c)
-{
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(c)));
-    return __half22float2(*reinterpret_cast<const __half2 *>(&h));
-}
 
 struct RunShared {
     float2 cs[kRunAngles];

@@ -379,6 +379,10 @@ struct ChunkParams {
     int64_t ks_p, ks_b, vs_p, vs_b;
     int scale_shift;           // log2 of the keys per block
     int n_pages;
+    const __nv_bfloat16 *q;    // element strides (token, head)
+    int64_t q_st, q_sh;
+    uint8_t *q8;               // the workspace: [2][T][Hq][D], q's e4m3 terms
+    float *q_scale;            // [T][Hq], their scales
 };
 
 #ifndef __CUDACC_RTC__

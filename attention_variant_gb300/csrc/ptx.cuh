@@ -63,6 +63,9 @@ __device__ __forceinline__ void fence_proxy_async_smem()
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+// The same for every state space.
+__device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
+
 __device__ __forceinline__ void mbar_arrive(uint32_t bar)
 {
     asm volatile(
@@ -183,6 +186,17 @@ __device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_
         "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate));
+}
+
+// The same, kind::f8f6f4 (e4m3 in, fp32 accumulate): 32 bytes of K.
+__device__ __forceinline__ void mma_ss_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                          uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate));
 }
 
@@ -414,6 +428,13 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
+__device__ __forceinline__ float lg2(float x)
+{
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 __device__ __forceinline__ float rcp_approx(float x)
 {
     float y;
@@ -481,7 +502,7 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
 // leading-dimension byte offset >> 4 in bits 16-29, stride-dimension byte
 // offset >> 4 in bits 32-45, the fixed version value 1 in bits 46-47, base
 // offset 0 (every tile is 1024-byte aligned), swizzle mode in bits 61-63
-// (2 = 128-byte, 4 = 64-byte).
+// (2 = 128-byte, 4 = 64-byte, 6 = 32-byte).
 //
 // K-major operands (Q and K: one row per M/N index, the head dimension
 // contiguous): 8-row core groups are `sbo` bytes apart; the leading offset is
@@ -512,6 +533,7 @@ __host__ __device__ constexpr uint64_t umma_desc_hi(uint32_t lbo, uint32_t sbo, 
 
 constexpr uint32_t kSwizzle128B = 2;
 constexpr uint32_t kSwizzle64B = 4;
+constexpr uint32_t kSwizzle32B = 6;
 
 // Instruction descriptor, kind::f16: fp32 accumulator (bits 4-5 = 1), A and B
 // bf16 (bits 7-9 = 1, bits 10-12 = 1), A K-major (bit 15 = 0), B K-major or
@@ -520,6 +542,12 @@ __host__ __device__ constexpr uint32_t umma_idesc_bf16(uint32_t M, uint32_t N, b
 {
     return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn_major ? 1u : 0u) << 16) |
            ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+
+// The same for kind::f8f6f4, both operands e4m3 (0), K-major (bits 15, 16: MN-major).
+__host__ __device__ constexpr uint32_t umma_idesc_e4m3(uint32_t M, uint32_t N)
+{
+    return (1u << 4) | ((N >> 3) << 17) | ((M >> 4) << 24);
 }
 
 } // namespace fl
