@@ -54,6 +54,7 @@
 #include <cuda_bf16.h>
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include "chunk_few.cuh"
 #include "chunk_plan.cuh"
@@ -72,9 +73,8 @@ struct ChunkCfg {
     static_assert(D == 64 || D == 128, "head dimension");
     static constexpr int kBN = chunk_key_tile(D);
     static constexpr int kStages = D == 128 ? 3 : 4; // of K and V as they are loaded
-    static constexpr int kVStages = F8 ? (D == 128 ? 2 : 3) : kStages; // of V in bf16
-    static constexpr int kThreads = chunk_threads(F8);
-    static constexpr bool kOnes = D <= 64; // sum of the rounded P from a ones column block
+    static constexpr int kVStages = F8 ? (D == 128 ? 2 : 3) : kStages; // of V in 16 bits
+    static constexpr bool kOnes = D <= 64 && !F8; // sum of the rounded P from a ones column block
     static constexpr int kHalves = D / 64;
     static constexpr uint32_t kRowBytes = 128;
     static constexpr uint32_t kGroupBytes = 8 * kRowBytes;
@@ -105,7 +105,7 @@ struct Item {
     int step;
     int t0[2], rows[2], pos0[2]; // slot's first token row, rows, first position
     int L, key_lo;               // cached keys; lowest key that any row of the item sees
-    int kvh, b;
+    int kvh;
     int n_parts;                 // CTAs that share the item
     int cta;                     // this part among those of both paths
     int mine;                    // its buffer: 1 if the item begins here
@@ -130,6 +130,8 @@ struct __align__(1024) ChunkSmem {
     uint32_t abort_flag;
     // a cache in 8 bits: V as it is loaded, and the stages of what it is converted to
     uint64_t v_full[F8 ? C::kVStages : 1], v_empty[F8 ? C::kVStages : 1];
+    std::conditional_t<F8, ScaleRing, char> scales;
+    std::conditional_t<F8, TileFactors, char> factors[2][4]; // [slot][its tiles in turn]
     alignas(F8 ? 128 : 4) uint8_t raw_v[F8 ? C::kStages : 1][F8 ? C::kLoadBytes : 4];
 };
 
@@ -189,7 +191,6 @@ __device__ void producer_role(const KernelCtx<D, F8> &cx, const ChunkParams &p, 
         if (!it.stop) {
             it.cta = me.cta;
             it.kvh = h;
-            it.b = en.b;
             it.L = en.L;
             it.key_lo = en.key_lo;
             it.pair = en.n_tok > p.TQ;
@@ -268,6 +269,8 @@ __device__ void producer_role(const KernelCtx<D, F8> &cx, const ChunkParams &p, 
             ok = warp_wait(bar(sm.kv_empty[s]), ((kv_count / kStages) & 1) ^ 1, cx.wc, W_KV_EMPTY);
             if (!ok)
                 break;
+            if constexpr (F8)
+                copy_scales<kBoxes>(p, sm.scales, kv_count, bar(sm.kv_full[s]), page, 4, j * kBN, it.key_lo, it.L, it.kvh);
             const int left = it.L - j * kBN;
             const int boxes = left <= 0 ? 0 : min(kBoxes, (left + kBox - 1) / kBox);
             const uint32_t b_full = bar(sm.kv_full[s]);
@@ -311,53 +314,6 @@ __device__ void producer_role(const KernelCtx<D, F8> &cx, const ChunkParams &p, 
     }
 }
 
-// ------------------------------------------------------------------ conversion
-
-// Converts the tiles of V of a cache in 8 bits, keys that no row sees to zeros.  Four
-// warps.
-template <int D>
-__device__ void convert_role(const KernelCtx<D, true> &cx, const ChunkParams &p)
-{
-    using C = ChunkCfg<D, true>;
-    constexpr int kBN = C::kBN, kStages = C::kStages, kVStages = C::kVStages;
-    ChunkSmem<D, true> &sm = *cx.sm;
-    uint32_t idx = 0;
-    for (uint32_t n = 0;; ++n) {
-        const uint32_t slot = n % kInfo;
-        if (!warp_wait(bar(sm.info_full[slot]), (n / kInfo) & 1, cx.wc, W_INFO_FULL))
-            return;
-        const Item &inf = sm.info[slot];
-        const int stop = inf.stop, u_lo = inf.u_lo, u_hi = inf.u_hi, L = inf.L, key_lo = inf.key_lo, kvh = inf.kvh,
-                  b = inf.b;
-        __syncwarp();
-        if (ptx::lane_id() == 0)
-            ptx::mbar_arrive(bar(sm.info_empty[slot]));
-        if (stop)
-            return;
-        auto scales_of = [&](int j) {
-            return tile_scales(p, p.v_scale, p.vs_p, p.vs_b, b, j * kBN, key_lo, L, kvh);
-        };
-        float next = scales_of(u_lo);
-        for (int j = u_lo; j < u_hi; ++j, ++idx) {
-            const float scales = next;
-            if (j + 1 < u_hi)
-                next = scales_of(j + 1);
-            const uint32_t from = idx % kStages, to = idx % kVStages;
-            const int j0 = j * kBN, dead_lo = min(kBN, max(0, key_lo - j0)), dead_hi = min(kBN, max(0, L - j0));
-            if (!warp_wait(bar(sm.kv_full[from]), (idx / kStages) & 1, cx.wc, W_KV_FULL) ||
-                !warp_wait(bar(sm.v_empty[to]), ((idx / kVStages) & 1) ^ 1, cx.wc, W_KV_EMPTY))
-                return;
-            convert_tile<D, kBN>(sm.raw_v[from], sm.v[to], scales, dead_lo, dead_hi);
-            ptx::fence_proxy_async_smem();
-            __syncwarp();
-            if (ptx::lane_id() == 0) {
-                ptx::mbar_arrive(bar(sm.v_full[to]));
-                ptx::mbar_arrive(bar(sm.kv_empty[from]));
-            }
-        }
-    }
-}
-
 // ------------------------------------------------------------------ MMA issuers
 
 // The slot's tile among [u_lo, u_hi)?
@@ -398,11 +354,17 @@ __device__ void s_role(const KernelCtx<D, F8> &cx)
         ok = warp_wait(bar(sm.q_full[ring]), (n >> 1) & 1, cx.wc, W_Q_FULL);
         if (!ok)
             break;
+        float top[2] = {kLeastLog, kLeastLog}; // 8 bits: the largest scale of V in each slot's tiles so far
         for (int j = u_lo; j < u_hi; ++j, ++idx) {
             const uint32_t stage = idx % kStages;
             ok = warp_wait(bar(sm.kv_full[stage]), (idx / kStages) & 1, cx.wc, W_KV_FULL);
             if (!ok)
                 break;
+            float scale_k = 0.f, scale_v = 0.f;
+            if constexpr (F8) {
+                scale_k = *const_cast<const volatile float *>(&sm.scales.k[idx % kScaleRing][lane & 7]);
+                scale_v = *const_cast<const volatile float *>(&sm.scales.v[idx % kScaleRing][lane & 7]);
+            }
             // rows of V that no query row sees: zero (their P is 0, but the bytes
             // may be anything); with softcap those of K, too (softcap_scores).  Some slot
             // uses every tile, and its P V, which releases the stage, waits for this
@@ -431,6 +393,9 @@ __device__ void s_role(const KernelCtx<D, F8> &cx)
             for (int t = 0; t < 2; ++t) {
                 if (!uses(j, t ? first1 : first0, t ? hi1 : hi0, step))
                     continue;
+                // four places: with the last tile's S the softmax was done with the one before that
+                if constexpr (F8)
+                    tile_factors(sm.factors[t][issued[t] & 3], scale_k, scale_v, top[t]);
                 if (issued[t] > 0) {
                     // the softmax has copied the slot's previous S out of TMEM
                     ok = warp_wait(bar(sm.s_free[t]), (issued[t] - 1) & 1, cx.wc, W_S_FULL);
@@ -438,6 +403,11 @@ __device__ void s_role(const KernelCtx<D, F8> &cx)
                         break;
                 }
                 ++issued[t];
+                if (F8) {
+                    __syncwarp();
+                    if (lane == 0)
+                        ptx::mbar_arrive(bar(sm.s_full[t])); // release: the factors first
+                }
                 ptx::tc_fence_after();
                 if (lane == 0) {
                     const uint32_t qlo = q_lo0 + (2 * ring + (pair ? t : 0)) * kTileLo;
@@ -488,7 +458,7 @@ __device__ void pv_role(const KernelCtx<D, F8> &cx, int t)
     ChunkSmem<D, F8> &sm = *cx.sm;
     const uint32_t lane = ptx::lane_id();
     uint64_t *const full = F8 ? sm.v_full : sm.kv_full, *const empty = F8 ? sm.v_empty : sm.kv_empty;
-    constexpr uint32_t idesc_pv = umma_idesc_bf16(BM, C::kDvExt, true);
+    constexpr uint32_t idesc_pv = F8 ? umma_idesc_f16(BM, C::kDvExt, true) : umma_idesc_bf16(BM, C::kDvExt, true);
     constexpr uint32_t kKVLo = C::kKVBytes >> 4;
     const uint32_t v_lo0 = ptx::smem_u32(sm.v[0]) >> 4;
     const uint32_t ones_lo = ptx::smem_u32(sm.ones) >> 4;
@@ -503,14 +473,43 @@ __device__ void pv_role(const KernelCtx<D, F8> &cx, int t)
             break;
         const Item &inf = sm.info[slot];
         const int stop = inf.stop, u_lo = inf.u_lo, u_hi = inf.u_hi, step = inf.step;
-        const int first = inf.first[t], hi = inf.hi[t];
+        const int first = inf.first[t], hi = inf.hi[t], L = inf.L, key_lo = inf.key_lo;
         __syncwarp();
         if (lane == 0)
             ptx::mbar_arrive(bar(sm.info_empty[slot]));
         if (stop)
             break;
+        // 8 bits: this warp's half of V's tile j, the CTA's number i
+        auto convert = [&](int j, uint32_t i) {
+            if constexpr (F8) {
+                const uint32_t from = i % C::kStages, to = i % kStages;
+                if (!warp_wait(bar(sm.kv_full[from]), (i / C::kStages) & 1, cx.wc, W_KV_FULL) ||
+                    !warp_wait(bar(empty[to]), ((i / kStages) & 1) ^ 1, cx.wc, W_KV_EMPTY))
+                    return false;
+                const int j0 = j * kBN;
+                convert_half<D, kBN>(sm.raw_v[from], sm.v[to], t, min(kBN, max(0, key_lo - j0)),
+                                     min(kBN, max(0, L - j0)));
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    ptx::mbar_arrive(bar(full[to]));
+                    ptx::mbar_arrive(bar(sm.kv_empty[from]));
+                }
+            }
+            return true;
+        };
+        if (F8 && u_lo < u_hi) {
+            ok = convert(u_lo, idx);
+            if (!ok)
+                break;
+        }
         for (int j = u_lo; j < u_hi; ++j, ++idx) {
             const uint32_t stage = idx % kStages;
+            if (F8 && j + 1 < u_hi) { // a tile ahead, while the softmax works on this one
+                ok = convert(j + 1, idx + 1);
+                if (!ok)
+                    break;
+            }
             if (!uses(j, first, hi, step)) {
                 // tile not used by this slot: release it once it has landed
                 ok = warp_wait(bar(full[stage]), (idx / kStages) & 1, cx.wc, W_KV_FULL);
@@ -589,13 +588,13 @@ __device__ __forceinline__ RowOut<D> row_out(const ChunkParams &p, const Item &i
 }
 
 // Epilogue of a pair: the slot's own rows, every column.  An active warp.
-template <int D>
+template <int D, bool F8>
 __device__ __forceinline__ void write_slot(const ChunkParams &p, const Item &inf, int t, int r, uint32_t tO,
-                                           const RowState &st, bool any)
+                                           const RowState &st, bool any, float unit)
 {
     const bool live = r < inf.rows[t], whole = inf.n_parts == 1;
     const RowOut<D> w = row_out<D>(p, inf, t, r);
-    const float inv = row_inv_norm(st);
+    const float inv = F8 ? row_inv_norm(st) * unit : row_inv_norm(st);
     // an accumulator without a tile, or a row without a key, is not read
     const bool keys = any && st.m_ref != kNegInf;
 #pragma unroll 1
@@ -620,7 +619,7 @@ __device__ __forceinline__ void write_slot(const ChunkParams &p, const Item &inf
         } else if (keys) {
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-                w.mine[(c + i) * 128] = __uint_as_float(raw[i]);
+                w.mine[(c + i) * 128] = F8 ? __uint_as_float(raw[i]) * unit : __uint_as_float(raw[i]);
         }
     }
     if (whole) {
@@ -637,9 +636,9 @@ __device__ __forceinline__ void write_slot(const ChunkParams &p, const Item &inf
 
 // Epilogue of one row block, after both slots are done: this warpgroup's half
 // of the columns from both accumulators.  An active warp.
-template <int D>
+template <int D, bool F8>
 __device__ __forceinline__ void write_joined(const ChunkParams &p, const Item &inf, int t, int r, uint32_t tO,
-                                             uint32_t tO_other, uint32_t tX_other, const RowState &st)
+                                             uint32_t tO_other, uint32_t tX_other, const RowState &st, float unit)
 {
     constexpr int H = D / 2;
     const bool live = r < inf.rows[t], whole = inf.n_parts == 1;
@@ -649,10 +648,14 @@ __device__ __forceinline__ void write_joined(const ChunkParams &p, const Item &i
     ptx::tmem_wait_ld();
     ptx::reg_fence<4>(other);
     const float m1 = __uint_as_float(other[0]), m = fmaxf(st.m_ref, m1);
-    const float w0 = st.m_ref == kNegInf ? 0.f : ptx::ex2(st.m_ref - m);
-    const float w1 = m1 == kNegInf ? 0.f : ptx::ex2(m1 - m);
+    float w0 = st.m_ref == kNegInf ? 0.f : ptx::ex2(st.m_ref - m);
+    float w1 = m1 == kNegInf ? 0.f : ptx::ex2(m1 - m);
     const float l = w0 * st.l + w1 * __uint_as_float(other[1]);
     const float lr = w0 * st.l_round + w1 * __uint_as_float(other[2]);
+    if constexpr (F8) { // the accumulators' units
+        w0 *= unit;
+        w1 *= __uint_as_float(other[3]);
+    }
     const float inv = lr > 0.f ? ptx::rcp_approx(lr) : 0.f;
 #pragma unroll 1
     for (int c = 0; c < H; c += 16) {
@@ -754,6 +757,7 @@ __device__ void softmax_role(const KernelCtx<D, F8> &cx, const ChunkParams &p, i
         // rows past the item's (other requests', or whatever Q's buffer held) start with a
         // reference that nothing exceeds: they have no say in when the warp rescales
         RowState st{r < inf.rows[t] ? kNegInf : -kNegInf, 0.f, 0.f};
+        float unit = 0.f; // 8 bits: log2 of the unit that O is counted in
         if (take_turns) // turns of tiles before this slot's
             for (int j = n_mine ? first - inf.u_lo : inf.u_hi - inf.u_lo; j > 0; --j, ++turns) {
                 if (!turn_wait())
@@ -762,17 +766,11 @@ __device__ void softmax_role(const KernelCtx<D, F8> &cx, const ChunkParams &p, i
             }
         if (active) {
             const int pos0 = inf.pos0[t], L = inf.L;
-            // 8 bits: the scale of this row's Q; those of a tile's keys, 16 to a lane, a tile ahead
-            float q_scale = 1.f, next = 0.f;
-            auto scales_of = [&](int j) {
-                return tile_scales(p, p.k_scale, p.ks_p, p.ks_b, inf.b, j * kBN, inf.key_lo, L, inf.kvh);
-            };
+            float q_scale = 1.f; // 8 bits: of this row's Q
             if constexpr (F8) {
                 const int r_tok = fast_div(r, p.div_g);
                 if (r < inf.rows[t])
                     q_scale = __ldcg(p.q_scale + static_cast<int64_t>(inf.t0[t] + r_tok) * p.Hq + inf.kvh * p.G + r - r_tok * p.G);
-                if (n_mine)
-                    next = scales_of(first);
             }
             const float qk = p.qk_log2 * q_scale, cap_in = p.softcap_in * q_scale;
             int row_lo, row_hi, full_lo, full_hi, unused;
@@ -783,9 +781,6 @@ __device__ void softmax_role(const KernelCtx<D, F8> &cx, const ChunkParams &p, i
                 key_range(p, L, pos0, pos0, unused, full_hi);
             }
             for (int kk = 0; kk < n_mine; ++kk) {
-                const float scales = next;
-                if (F8 && kk + 1 < n_mine)
-                    next = scales_of(first + (kk + 1) * step);
                 if (!warp_wait(bar(sm.s_full[t]), scount & 1, cx.wc, W_S_FULL))
                     return;
                 ++scount;
@@ -794,29 +789,43 @@ __device__ void softmax_role(const KernelCtx<D, F8> &cx, const ChunkParams &p, i
                 load_scores<kBN>(tS, x);
                 ptx::tc_fence_before();
                 ptx::mbar_arrive(bar(sm.s_free[t])); // S[t] may be overwritten
-                if constexpr (F8) {
-#pragma unroll
-                    for (int g = 0; g < kBN / 16; ++g) {
-                        const float k = __shfl_sync(0xffffffffu, scales, g);
-#pragma unroll
-                        for (int e = 16 * g; e < 16 * g + 16; e += 2)
-                            ptx::fma2(x[e], x[e + 1], x[e], x[e + 1], k, k, 0.f, 0.f);
-                    }
-                }
                 if (take_turns && !turn_wait())
                     return;
                 const int j0 = (first + kk * step) * kBN;
-                if constexpr (MOD == MOD_SOFTCAP)
-                    softcap_scores<kBN>(x, F8 ? cap_in : p.softcap_in, p.softcap_out);
+                float c[F8 ? kBN / 16 : 1]; // 8 bits: what each 16 scores are multiplied by
+                if constexpr (F8) {
+                    const volatile float *k = sm.factors[t][(scount - 1) & 3].k;
+#pragma unroll
+                    for (int g = 0; g < kBN / 16; ++g)
+                        c[g] = k[g] * (MOD == MOD_SOFTCAP ? cap_in : qk);
+                    if constexpr (MOD == MOD_SOFTCAP) {
+#pragma unroll
+                        for (int g = 0; g < kBN / 16; ++g) {
+                            softcap_scores<16>(*reinterpret_cast<float (*)[16]>(x + 16 * g), c[g], p.softcap_out);
+                            c[g] = 1.f;
+                        }
+                    }
+                } else if constexpr (MOD == MOD_SOFTCAP) {
+                    softcap_scores<kBN>(x, p.softcap_in, p.softcap_out);
+                }
                 if (!(j0 >= full_lo && j0 + kBN <= full_hi))
                     apply_row_mask<kBN>(x, j0, row_lo, row_hi);
                 uint32_t pk[kBN / 2];
                 bool rescale;
-                const float alpha =
-                    C::kOnes ? softmax_compute_p_exact_sum<kBN>(x, MOD == MOD_NONE ? (F8 ? qk : p.qk_log2) : 1.f, st, false,
-                                                                pk, rescale)
-                             : softmax_compute_p<kBN>(x, MOD == MOD_NONE ? (F8 ? qk : p.qk_log2) : 1.f, st, false, pk,
-                                                      rescale);
+                float alpha;
+                if constexpr (F8) {
+                    const TileFactors &fac = sm.factors[t][(scount - 1) & 3];
+                    alpha = softmax_compute_p_scaled<kBN>(x, c, fac, st, pk, rescale);
+                    const float a = *const_cast<const volatile float *>(&fac.alpha);
+                    unit = *const_cast<const volatile float *>(&fac.unit);
+                    alpha *= a;
+                    rescale |= a != 1.f;
+                } else {
+                    alpha = C::kOnes ? softmax_compute_p_exact_sum<kBN>(x, MOD == MOD_NONE ? p.qk_log2 : 1.f, st, false,
+                                                                        pk, rescale)
+                                     : softmax_compute_p<kBN>(x, MOD == MOD_NONE ? p.qk_log2 : 1.f, st, false, pk,
+                                                              rescale);
+                }
                 if (take_turns) {
                     ptx::mbar_arrive(b_turn_other); // hand the turn over
                     ++turns;
@@ -876,14 +885,17 @@ __device__ void softmax_role(const KernelCtx<D, F8> &cx, const ChunkParams &p, i
                 st.l_round = __uint_as_float(sum[0]);
             }
         }
+        if constexpr (F8)
+            st.l_round = st.l; // P in f16 is within 2^-12 of it
+        const float o_unit = F8 ? ptx::ex2(unit) : 1.f;
         if (inf.pair) {
             if (active)
-                write_slot<D>(p, inf, t, r, tO, st, n_mine > 0);
+                write_slot<D, F8>(p, inf, t, r, tO, st, n_mine > 0, o_unit);
         } else {
             const uint32_t tX = cx.tmem + lanes + C::kColX;
             if (active) {
                 const uint32_t ml[8] = {__float_as_uint(st.m_ref), __float_as_uint(st.l),
-                                        __float_as_uint(st.l_round), 0, 0, 0, 0, 0};
+                                        __float_as_uint(st.l_round), __float_as_uint(o_unit), 0, 0, 0, 0};
                 ptx::tmem_st8(tX + C::kStrideX * t, ml);
                 ptx::tmem_wait_st();
             }
@@ -893,8 +905,8 @@ __device__ void softmax_role(const KernelCtx<D, F8> &cx, const ChunkParams &p, i
                 return;
             ptx::tc_fence_after();
             if (active)
-                write_joined<D>(p, inf, t, r, tO, cx.tmem + lanes + C::kColO + C::kStrideO * (t ^ 1),
-                                tX + C::kStrideX * (t ^ 1), st);
+                write_joined<D, F8>(p, inf, t, r, tO, cx.tmem + lanes + C::kColO + C::kStrideO * (t ^ 1),
+                                    tX + C::kStrideX * (t ^ 1), st, o_unit);
             ptx::tc_fence_before();
             ptx::mbar_arrive(bar(sm.x_free[t ^ 1])); // the other slot's O and sums have been read
             // the other warpgroup has read this slot's O before the next item's P V
@@ -913,11 +925,11 @@ __device__ void softmax_role(const KernelCtx<D, F8> &cx, const ChunkParams &p, i
 
 // The kernel of the row blocks.
 template <int MOD, int D, bool F8>
-__global__ void __launch_bounds__(chunk_threads(F8), 1)
+__global__ void __launch_bounds__(kThreads, 1)
     chunk_kernel(const __grid_constant__ ChunkMaps maps, const __grid_constant__ ChunkParams p)
 {
     using C = ChunkCfg<D, F8>;
-    constexpr int kStages = C::kStages, kThreads = C::kThreads;
+    constexpr int kStages = C::kStages;
     extern __shared__ uint8_t smem_raw[];
     ChunkSmem<D, F8> *sm =
         reinterpret_cast<ChunkSmem<D, F8> *>(smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u));
@@ -940,18 +952,18 @@ __global__ void __launch_bounds__(chunk_threads(F8), 1)
         }
         for (int b = 0; b < kInfo; ++b) {
             ptx::mbar_init(bar(sm->info_full[b]), 1);
-            ptx::mbar_init(bar(sm->info_empty[b]), F8 ? 15 : 11); // S, two P V, eight softmax and four converting warps
+            ptx::mbar_init(bar(sm->info_empty[b]), 11); // S, two P V and eight softmax warps
         }
         for (int s = 0; s < kStages; ++s) {
-            ptx::mbar_init(bar(sm->kv_full[s]), 1);
-            ptx::mbar_init(bar(sm->kv_empty[s]), F8 ? 5 : 2); // one arrival per P V warp; or S's and each converting warp's
+            ptx::mbar_init(bar(sm->kv_full[s]), F8 ? 1 + kScaleArrivals : 1);
+            ptx::mbar_init(bar(sm->kv_empty[s]), F8 ? 3 : 2); // one arrival per P V warp, in 8 bits S's, too
         }
         for (int s = 0; s < (F8 ? C::kVStages : 0); ++s) {
-            ptx::mbar_init(bar(sm->v_full[s]), 4);
+            ptx::mbar_init(bar(sm->v_full[s]), 2); // one arrival per P V warp, here and below
             ptx::mbar_init(bar(sm->v_empty[s]), 2);
         }
         for (int t = 0; t < 2; ++t) {
-            ptx::mbar_init(bar(sm->s_full[t]), 1);
+            ptx::mbar_init(bar(sm->s_full[t]), F8 ? 2 : 1); // the product, and its factors
             ptx::mbar_init(bar(sm->p_full[t]), 128);
             ptx::mbar_init(bar(sm->s_free[t]), 128);
             ptx::mbar_init(bar(sm->pv_done[t]), 1);
@@ -979,19 +991,14 @@ __global__ void __launch_bounds__(chunk_threads(F8), 1)
 
     // each branch ends with its own copy of the teardown barrier, so no code
     // runs under both register limits
-    if (F8 && warp >= 12) {
-        ptx::setmaxnreg_dec<chunk_regs_other(F8)>();
-        if constexpr (F8)
-            convert_role<D>(cx, p);
-        ptx::named_barrier_sync(1, kThreads);
-    } else if (warp >= 4) {
+    if (warp >= 4) {
         ptx::setmaxnreg_inc<kRegsSoftmax>();
         tell_second(p, cx.part);
         softmax_role<MOD, D, F8>(cx, p, (warp >> 2) - 1);
         ptx::tc_fence_before();
         ptx::named_barrier_sync(1, kThreads);
     } else {
-        ptx::setmaxnreg_dec<chunk_regs_other(F8)>();
+        ptx::setmaxnreg_dec<kRegsOther>();
         if (warp == 0)
             producer_role(cx, p, &maps.q, &maps.k, &maps.v);
         else if (warp == 1)
@@ -1045,8 +1052,8 @@ cudaError_t configure(int device)
     cudaError_t e = cudaFuncGetAttributes(&attr, chunk_kernel<MOD, D, F8>);
     if (e != cudaSuccess)
         return e;
-    // the setmaxnreg split assumes exactly this many registers at launch
-    if (attr.numRegs != static_cast<int>(chunk_regs_launch(F8)))
+    // the setmaxnreg split assumes exactly kRegsLaunch registers at launch
+    if (attr.numRegs != static_cast<int>(kRegsLaunch))
         return cudaErrorInvalidConfiguration;
     e = cudaFuncSetAttribute(chunk_kernel<MOD, D, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(smem_bytes<ChunkSmem<D, F8>>()));
@@ -1086,7 +1093,7 @@ cudaError_t launch_mod(const ChunkMaps &maps, ChunkParams &p, cudaStream_t strea
     auto launch = [&](bool few_kernel) {
         const cudaError_t err = few_kernel
             ? launch_after(chunk_few_kernel<MOD, D, F8>, dim3(p.n_cta), kThreads, smem_bytes<FewSmem<D, F8>>(), stream, maps, p)
-            : launch_after(chunk_kernel<MOD, D, F8>, dim3(p.n_cta), chunk_threads(F8), smem_bytes<ChunkSmem<D, F8>>(), stream, maps, p);
+            : launch_after(chunk_kernel<MOD, D, F8>, dim3(p.n_cta), kThreads, smem_bytes<ChunkSmem<D, F8>>(), stream, maps, p);
         p.second = 1;
         p.warm = 0;
         return err;

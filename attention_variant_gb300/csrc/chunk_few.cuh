@@ -127,6 +127,7 @@ struct __align__(1024) FewSmem {
     float red[2][4][kFewRows];       // maxima or sums of each softmax warp
     uint32_t rows[2][2][4];          // by tile parity, of each softmax warp: see few_softmax
     uint32_t large[2][2][4];         // the same of rows whose P asks for a reference (8 bits)
+    std::conditional_t<F8, ScaleRing, char> scales;
     uint32_t tmem_base;
     uint32_t abort_flag;
 };
@@ -151,13 +152,19 @@ struct FewRing {
     uint32_t count;
 
     // Tile v of an item into the next stage: lane g loads the g-th box, of its page.
-    __device__ __forceinline__ bool load(const FewCtx<D, F8> &cx, const ChunkParams &p, const FewItem &it, int v, int page)
+    __device__ __forceinline__ bool load(const FewCtx<D, F8> &cx, const ChunkParams &p, const FewItem &it, int v, int page,
+                                         bool with_scales)
     {
         const int lane = static_cast<int>(ptx::lane_id());
         const int box = 1 << p.few_shift, key0 = (v >> it.shift) * C::kBN, left = it.L - key0;
         const uint32_t s = count % C::kStages;
         if (!warp_wait(bar(empty[s]), ((count / C::kStages) & 1) ^ 1, cx.wc, W_KV_EMPTY))
             return false;
+        if constexpr (F8) {
+            if (with_scales)
+                copy_scales<C::kBN / 16>(p, cx.sm->scales, count, bar(full[s]), page, p.few_shift, key0, it.key_lo,
+                                         it.L, it.kvh + (it.shift ? v & 1 : 0));
+        }
         const int boxes = left <= 0 ? 0 : min(C::kBN >> p.few_shift, (left + box - 1) >> p.few_shift);
         if (lane == 0)
             ptx::mbar_arrive_expect_tx(bar(full[s]), static_cast<uint32_t>(C::kHalves * boxes * box) * C::kRowBytes);
@@ -323,9 +330,9 @@ __device__ void few_producer(const FewCtx<D, F8> &cx, const ChunkParams &p, cons
             if (v + 1 < it.u_hi)
                 page_next = few_page<D>(p, it, (v + 1) >> it.shift);
             if (v < it.u_hi)
-                ok = keys.load(cx, p, it, v, page[0]);
+                ok = keys.load(cx, p, it, v, page[0], true);
             if (ok && !split && v - C::kLag >= it.u_lo)
-                ok = values.load(cx, p, it, v - C::kLag, page[C::kLag]);
+                ok = values.load(cx, p, it, v - C::kLag, page[C::kLag], false);
         }
         if (!ok)
             break;
@@ -374,7 +381,7 @@ __device__ void few_v_producer(const FewCtx<D, F8> &cx, const ChunkParams &p, co
             const int page = page_next;
             if (v + 1 < it.u_hi)
                 page_next = few_page<D>(p, it, (v + 1) >> it.shift);
-            ok = values.load(cx, p, it, v, page);
+            ok = values.load(cx, p, it, v, page, false);
         }
     }
     values.drain(cx);
@@ -604,6 +611,7 @@ constexpr float kFewPUnset = -1e30f;
 // What a softmax thread carries from item to item.
 struct FewState {
     uint32_t s, pv, group, tiles; // phases of s_full, pv_done, group; tiles so far
+    uint32_t loaded;              // tiles of the CTA before this item
 };
 
 // One item of at most R rows.  False when a wait ran out.
@@ -651,14 +659,8 @@ __device__ __forceinline__ bool few_item(const FewCtx<D, F8> &cx, const ChunkPar
     }
     uint32_t set = 0;  // rows that have a reference
     bool moved = false; // some reference is not 0
-    // 8 bits: the factor of a row's scores, the reference of its P; this thread's key's scales
+    // 8 bits: the factor of a row's scores, the reference of its P
     float q_factor[F8 ? R : 1], mp[F8 ? R : 1];
-    float next_k = 0.f, next_v = 0.f;
-    auto scales_of = [&](int v) {
-        const int key = (v >> inf.shift) * kBN + r;
-        next_k = box_scale(p, p.k_scale, p.ks_p, p.ks_b, inf.b, key, inf.key_lo, inf.L, inf.kvh + t);
-        next_v = box_scale(p, p.v_scale, p.vs_p, p.vs_b, inf.b, key, inf.key_lo, inf.L, inf.kvh + t);
-    };
     if constexpr (F8) {
 #pragma unroll
         for (int n = 0; n < R; ++n) {
@@ -669,18 +671,19 @@ __device__ __forceinline__ bool few_item(const FewCtx<D, F8> &cx, const ChunkPar
                                     (MOD == MOD_NONE ? p.qk_log2 : 1.f)
                               : 0.f;
         }
-        if (n_mine)
-            scales_of(f.first);
     }
     for (int kk = 0; kk < n_mine; ++kk) {
-        const float key_k = next_k, key_v = next_v;
-        if (F8 && kk + 1 < n_mine)
-            scales_of(f.first + (kk + 1) * f.step);
         if (!warp_wait(bar(sm.s_full[t]), ct.s & 1, cx.wc, W_S_FULL))
             return false;
         ++ct.s;
         ++ct.tiles;
         ptx::tc_fence_after();
+        float key_k = 1.f, key_v = 1.f; // 8 bits: the key's scales
+        if constexpr (F8) {
+            const uint32_t i = (ct.loaded + static_cast<uint32_t>(f.first + kk * f.step - inf.u_lo)) % kScaleRing;
+            key_k = *const_cast<const volatile float *>(&sm.scales.k[i][r >> 4]);
+            key_v = *const_cast<const volatile float *>(&sm.scales.v[i][r >> 4]);
+        }
         float x[R];
         {
             uint32_t raw[R];
@@ -993,7 +996,7 @@ template <int MOD, int D, bool F8>
 __device__ void few_softmax(const FewCtx<D, F8> &cx, const ChunkParams &p, int t)
 {
     FewSmem<D, F8> &sm = *cx.sm;
-    FewState ct{0u, 0u, 0u, 0u};
+    FewState ct{0u, 0u, 0u, 0u, 0u};
     for (uint32_t item = 0;; ++item) {
         if (!warp_wait(bar(sm.info_full[item % kInfo]), (item / kInfo) & 1, cx.wc, W_INFO_FULL))
             return;
@@ -1004,6 +1007,7 @@ __device__ void few_softmax(const FewCtx<D, F8> &cx, const ChunkParams &p, int t
         if (t < inf.heads && !(inf.rows <= 8 ? few_item<MOD, D, F8, 8>(cx, p, inf, t, ct)
                                              : few_item<MOD, D, F8, 16>(cx, p, inf, t, ct)))
             return;
+        ct.loaded += inf.u_hi - inf.u_lo;
         __syncwarp();
         if (ptx::lane_id() == 0)
             ptx::mbar_arrive(bar(sm.info_empty[item % kInfo]));
@@ -1037,7 +1041,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::mbar_init(bar(sm->info_empty[b]), 11); // all but the producer
         }
         for (int s = 0; s < C::kStages; ++s) {
-            ptx::mbar_init(bar(sm->k_full[s]), 1);
+            ptx::mbar_init(bar(sm->k_full[s]), F8 ? 1 + kScaleArrivals : 1);
             ptx::mbar_init(bar(sm->k_empty[s]), 1);
             ptx::mbar_init(bar(sm->v_full[s]), 1);
             ptx::mbar_init(bar(sm->v_empty[s]), few_split_loads(p) ? 1 : 2); // the warps that issue O^T

@@ -18,15 +18,11 @@ namespace fl {
 namespace {
 
 constexpr int kThreads = 384;
-// Row blocks of a cache in 8 bits (F8) take four warps more, which convert V.
-__host__ __device__ constexpr int chunk_threads(bool f8) { return f8 ? 512 : 384; }
-__host__ __device__ constexpr uint32_t chunk_regs_launch(bool f8) { return f8 ? 128 : 168; }
-__host__ __device__ constexpr uint32_t chunk_regs_other(bool f8) { return f8 ? 56 : 104; }
+constexpr uint32_t kRegsLaunch = 168;
 constexpr uint32_t kRegsSoftmax = 200;
-static_assert(2 * 128 * kRegsSoftmax + 128 * chunk_regs_other(false) == chunk_threads(false) * chunk_regs_launch(false) &&
-                  2 * 128 * kRegsSoftmax + 256 * chunk_regs_other(true) == chunk_threads(true) * chunk_regs_launch(true),
+constexpr uint32_t kRegsOther = 104;
+static_assert(2 * 128 * kRegsSoftmax + 128 * kRegsOther == kThreads * kRegsLaunch,
               "register split must equal the launch allocation");
-constexpr int kLastSoftmax = 383; // the last softmax thread
 constexpr int kInfo = 4; // items published ahead of the slowest role
 
 __device__ uint32_t g_lib_error_word;
@@ -143,7 +139,7 @@ __device__ __forceinline__ bool idle_second(const ChunkParams &p, int kind, int 
 // The word of the first kernel for the second.  The softmax warps.
 __device__ __forceinline__ void tell_second(const ChunkParams &p, int part)
 {
-    if (!p.second && p.seen_mark && part == 0 && threadIdx.x == kLastSoftmax) {
+    if (!p.second && p.seen_mark && part == 0 && threadIdx.x == kThreads - 1) {
         ptx::wait_dependency();
         ptx::store_release(p.seen, p.seen_mark);
     }

@@ -25,11 +25,16 @@ __device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi)
     return r;
 }
 
-// Two codes (the low bytes of c) to values.
-__device__ __forceinline__ float2 from_e4m3x2(uint32_t c)
+// Two codes (the low bytes of c) to values, exactly.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t c)
 {
     uint32_t h;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(c)));
+    return h;
+}
+__device__ __forceinline__ float2 from_e4m3x2(uint32_t c)
+{
+    const uint32_t h = e4m3x2_to_f16x2(c);
     return __half22float2(*reinterpret_cast<const __half2 *>(&h));
 }
 

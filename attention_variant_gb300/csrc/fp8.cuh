@@ -1,126 +1,166 @@
 // fp8.cuh -- e4m3 on the way through the kernels of the 8-bit KV cache.
 //
-// A key's D codes stand for code * scale, scale by block of keys and KV head
-// (fl_attn.h).  e4m3 has 4 significant bits, bf16 has 8: where the scale is a power of
-// two, code * scale is a bf16 number, and the conversion is exact.
-//
-// A byte s eeee mmm shifted to where bf16 has its sign, the low bits of its exponent
-// and the high ones of its mantissa stands for 2^-120 times its value, subnormals
-// too, so one packed multiplication by 2^120 scale finishes two of them.  (The
-// NaN codes come out as +-480.)
+// A key's D codes stand for code * scale, scale by block of keys and KV head (fl_attn.h).
 #pragma once
 
 #include "chunk_plan.cuh"
 #include "e4m3.cuh"
+#include "softmax_tile.cuh"
 
 namespace fl {
 namespace {
 
-constexpr int kConvertThreads = 128; // four warps
-
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b)
-{
-    uint32_t d;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-    return d;
-}
-
-// The multipliers of a block of codes: value = bits * first * second.  Their product,
-// 2^120 scale, may exceed bf16's range; scales up to 2^7 need the first alone.
-struct Fp8Scale {
-    uint32_t first, second;
-    bool one;
+// The scales of the last tiles, of K's and V's boxes of 16 keys.  The warp that loads
+// K copies them along, and the barrier of the K tile covers them.  Who reads them has done so
+// before the tile of 32 places on is loaded: loads are at most the rings and a few items
+// ahead of the softmax (S of a tile waits for what its slot's last one was read for).
+constexpr int kScaleRing = 32;
+struct ScaleRing {
+    float k[kScaleRing][8], v[kScaleRing][8];
 };
-__device__ __forceinline__ Fp8Scale fp8_scale(float scale)
+constexpr int kScaleArrivals = 16; // on the tile's barrier: one per lane that copies
+
+// Copies the scales of the BOXES boxes from key0 on of request b; `page` is that of this
+// lane's box of 2^page_box keys.  Boxes that no row sees and pages outside the cache get
+// zeros.  A warp.
+template <int BOXES>
+__device__ __forceinline__ void copy_scales(const ChunkParams &p, ScaleRing &ring, uint32_t idx, uint32_t bar, int page,
+                                            int page_box, int key0, int key_lo, int L, int kvh)
 {
-    Fp8Scale f;
-    f.one = !(scale > 64.f);
-    const float a = f.one ? scale * 0x1p120f : 0x1p126f, b = f.one ? 1.f : scale * 0x1p-6f;
-    f.first = ptx::pack_bf16(a, a);
-    f.second = ptx::pack_bf16(b, b);
-    return f;
+    const int lane = static_cast<int>(ptx::lane_id()), g = lane & 7, key = key0 + g * 16;
+    const int pg = __shfl_sync(0xffffffffu, page, g * 16 >> page_box);
+    if (lane >= kScaleArrivals)
+        return;
+    const bool v = lane >= 8;
+    const int at = p.page_shift < 0 ? key : key & ((1 << p.page_shift) - 1);
+    const bool read = g < BOXES && key < L && key >= (key_lo & ~15) &&
+                      static_cast<uint32_t>(pg) < static_cast<uint32_t>(p.n_pages);
+    const float *from = v ? p.v_scale : p.k_scale;
+    if (read)
+        from += pg * (v ? p.vs_p : p.ks_p) + static_cast<int64_t>(at >> p.scale_shift) * (v ? p.vs_b : p.ks_b) + kvh;
+    const uint32_t i = idx % kScaleRing;
+    ptx::copy_word(ptx::smem_u32(v ? &ring.v[i][g] : &ring.k[i][g]), from, read);
+    ptx::copies_arrive(bar);
 }
 
-// Four codes -> two words of two bf16.
-__device__ __forceinline__ uint2 fp8_to_bf16(uint32_t w, const Fp8Scale &f)
-{
-    uint32_t out[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const uint32_t t = __byte_perm(w, 0, i ? 0x3424 : 0x1404); // each code in the high byte of its half
-        const uint32_t bits = ((t & 0x7f007f00u) >> 4) | (t & 0x80008000u);
-        out[i] = mul_bf16x2(bits, f.first);
-    }
-    if (!f.one) {
-        out[0] = mul_bf16x2(out[0], f.second);
-        out[1] = mul_bf16x2(out[1], f.second);
-    }
-    return make_uint2(out[0], out[1]);
-}
-
-// The scale of a key of request b.  Keys that no row sees and pages outside the
-// cache have none.
-__device__ __forceinline__ float box_scale(const ChunkParams &p, const float *scale, int64_t s_page, int64_t s_block,
-                                           int b, int key, int key_lo, int L, int kvh)
-{
-    if (key >= L || key < key_lo)
-        return 0.f;
-    int page = b, at = key;
-    if (p.page_shift >= 0) {
-        page = __ldg(p.block_table + static_cast<int64_t>(b) * p.bt_stride + (key >> p.page_shift));
-        at = key & ((1 << p.page_shift) - 1);
-    }
-    if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(p.n_pages))
-        return 0.f;
-    return __ldg(scale + page * s_page + static_cast<int64_t>(at >> p.scale_shift) * s_block + kvh);
-}
-
-// The scales of a tile's boxes of 16 keys in the lanes of a warp.  (A box that holds
-// some key that a row sees has that key's.)
-__device__ __forceinline__ float tile_scales(const ChunkParams &p, const float *scale, int64_t s_page, int64_t s_block,
-                                             int b, int key0, int key_lo, int L, int kvh)
-{
-    const int lane = static_cast<int>(ptx::lane_id());
-    return lane < 8 ? box_scale(p, scale, s_page, s_block, b, key0 + lane * 16, key_lo & ~15, L, kvh) : 0.f;
-}
-
-// A tile of KEYS keys from codes (a key's D bytes after another's) to bf16 in the layout
-// of the 128-byte swizzle, halves of 64 dimensions, by four warps.  Keys outside
-// [dead_lo, dead_hi) become zero.  16 codes a thread and step: a 16-byte load (all of
-// them first) and two 16-byte stores, 8 threads of which meet in no bank.
+// Half `part` of the KEYS keys of a tile from codes (a key's D bytes after another's) to
+// f16, which holds them exactly, in the layout of the 128-byte swizzle, halves of 64
+// dimensions, by a warp.  Keys outside [dead_lo, dead_hi) become zero.  16 codes a lane and
+// step: a 16-byte load (all of them first) and two 16-byte stores, 8 lanes of which
+// meet in no bank.
 template <int D, int KEYS>
-__device__ __forceinline__ void convert_tile(const uint8_t *raw, uint8_t *dst, float scales, int dead_lo, int dead_hi)
+__device__ __forceinline__ void convert_half(const uint8_t *raw, uint8_t *dst, int part, int dead_lo, int dead_hi)
 {
-    constexpr int kUnits = D / 16, kSteps = (KEYS * kUnits + kConvertThreads - 1) / kConvertThreads;
-    constexpr bool kRagged = KEYS * kUnits % kConvertThreads != 0; // the last step is some warps' alone
-    const int tid = threadIdx.x & (kConvertThreads - 1), u = tid % kUnits;
+    constexpr int kUnits = D / 16, kStepKeys = 32 / kUnits, kSteps = KEYS / 2 / kStepKeys;
+    static_assert(kSteps * kStepKeys * 2 == KEYS, "whole steps");
+    const int lane = static_cast<int>(ptx::lane_id()), u = lane % kUnits, key0 = part * (KEYS / 2) + lane / kUnits;
     uint4 w[kSteps];
 #pragma unroll
     for (int i = 0; i < kSteps; ++i)
-        if (!kRagged || i + 1 < kSteps || tid + i * kConvertThreads < KEYS * kUnits)
-            w[i] = *reinterpret_cast<const uint4 *>(raw + (tid + i * kConvertThreads) * 16);
+        w[i] = *reinterpret_cast<const uint4 *>(raw + (key0 + i * kStepKeys) * D + u * 16);
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
-        const int key = tid / kUnits + i * (kConvertThreads / kUnits);
-        const Fp8Scale f = fp8_scale(__shfl_sync(0xffffffffu, scales, (key >> 4) & 7));
-        if (kRagged && i + 1 == kSteps && tid + i * kConvertThreads >= KEYS * kUnits)
-            break;
+        const int key = key0 + i * kStepKeys;
+        if (key < dead_lo || key >= dead_hi)
+            w[i] = make_uint4(0, 0, 0, 0);
         uint4 out[2];
         const uint32_t in[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
         uint32_t *o = reinterpret_cast<uint32_t *>(out);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-            const uint2 y = fp8_to_bf16(in[c], f);
-            o[2 * c] = y.x;
-            o[2 * c + 1] = y.y;
+            o[2 * c] = e4m3x2_to_f16x2(in[c] & 0xffffu);
+            o[2 * c + 1] = e4m3x2_to_f16x2(in[c] >> 16);
         }
-        if (key < dead_lo || key >= dead_hi)
-            out[0] = out[1] = make_uint4(0, 0, 0, 0);
         uint4 *row = reinterpret_cast<uint4 *>(dst + (u >> 2) * (KEYS * 128) + key * 128);
         const int at = (u & 3) * 2;
         row[at ^ (key & 7)] = out[0];
         row[(at + 1) ^ (key & 7)] = out[1];
     }
+}
+
+// What the scales of a tile do to a slot of row blocks.  V's codes are multiplied as they
+// are; the scale of a key goes into its weight, as a power of two relative to the
+// largest scale of the item so far: P = 2^(z - m + log_v), and the accumulator counts
+// in units of 2^unit (the sums divide what goes into them by 2^log_v again).  So P stays
+// below 2^(8 + kPBias) in f16 whatever the scales are, and holds 11 bits of a product of weight
+// and scale down to 2^(-14 - kPBias) of the largest.
+constexpr float kPBias = 6.f, kLeastLogV = -60.f, kLeastLog = -110.f;
+struct alignas(16) TileFactors {
+    float k[8];         // K's scales, of 16 keys each
+    float log_v[8];
+    float inv_v[8];     // 2^-log_v
+    float alpha, unit;  // what the accumulator is multiplied by first; its unit's logarithm
+    float pad[2];
+};
+
+// The factors of a tile for a slot whose largest scale so far is 2^top, by a warp; lane
+// g < 8 has the scales k and v of box g (0 or NaN: a box that no row sees).
+__device__ __forceinline__ void tile_factors(TileFactors &f, float k, float v, float &top)
+{
+    const int lane = static_cast<int>(ptx::lane_id());
+    const float log_v = fmaxf(ptx::lg2(v), kLeastLog);
+    float most = log_v;
+#pragma unroll
+    for (int d = 1; d < 8; d *= 2)
+        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
+    most = fmaxf(top, most);
+    const float lf = fmaxf(log_v - most, kLeastLogV) + kPBias;
+    if (lane < 8) {
+        f.k[lane] = k > 0.f ? k : 1.f;
+        f.log_v[lane] = lf;
+        f.inv_v[lane] = ptx::ex2(-lf);
+        if (lane == 0) {
+            f.alpha = ptx::ex2(top - most);
+            f.unit = most - kPBias;
+        }
+    }
+    top = most;
+}
+
+// softmax_compute_p_exact_sum under these factors: P in f16.
+template <int N>
+__device__ __forceinline__ float softmax_compute_p_scaled(float (&x)[N], const float (&c)[N / 16], const TileFactors &f,
+                                                          RowState &st, uint32_t (&pk)[N / 2], bool &rescale)
+{
+    float mx = kNegInf;
+#pragma unroll
+    for (int g = 0; g < N / 16; ++g) {
+        const float *v = x + 16 * g;
+        float a = fmaxf(v[0], v[1]), b = fmaxf(v[2], v[3]);
+#pragma unroll
+        for (int e = 4; e < 16; e += 4) {
+            a = ptx::max3(a, v[e], v[e + 1]);
+            b = ptx::max3(b, v[e + 2], v[e + 3]);
+        }
+        mx = fmaxf(mx, fmaxf(a, b) * c[g]); // c > 0
+    }
+    float alpha = 1.f;
+    rescale = false;
+    const bool need = mx > st.m_ref + kRescaleThreshold;
+    if (__any_sync(0xffffffffu, need)) {
+        const float m_new = fmaxf(st.m_ref, mx);
+        alpha = (m_new == kNegInf) ? 1.f : ptx::ex2(st.m_ref - m_new);
+        st.l *= alpha;
+        st.m_ref = m_new;
+        rescale = true;
+    }
+    const float nmu = (st.m_ref == kNegInf) ? 0.f : -st.m_ref;
+#pragma unroll
+    for (int g = 0; g < N / 16; ++g) {
+        const float nm = nmu + *const_cast<const volatile float *>(&f.log_v[g]);
+        float le[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            float a0, a1;
+            ptx::fma2(a0, a1, x[16 * g + 2 * e], x[16 * g + 2 * e + 1], c[g], c[g], nm, nm);
+            const float p0 = ptx::ex2(a0), p1 = ptx::ex2(a1);
+            pk[8 * g + e] = ptx::pack_f16(p0, p1);
+            const int i = 2 * (e & 1);
+            ptx::add2(le[i], le[i + 1], p0, p1);
+        }
+        st.l = fmaf((le[0] + le[1]) + (le[2] + le[3]), *const_cast<const volatile float *>(&f.inv_v[g]), st.l);
+    }
+    return alpha;
 }
 
 // Q as two e4m3 terms a row, relative to the row's scale: q = s (q1 + q2).  e4m3 has 4

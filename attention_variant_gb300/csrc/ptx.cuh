@@ -142,6 +142,17 @@ __device__ __forceinline__ void tma_load_5d(uint32_t dst, const void *tmap, uint
         : "memory");
 }
 
+// A 32-bit word into shared memory, or a zero where `from` is not read, and an arrival on
+// `bar` (counted among those it expects) when the thread's copies so far are there.
+__device__ __forceinline__ void copy_word(uint32_t dst, const void *from, bool read)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(from), "r"(read ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_arrive(uint32_t bar)
+{
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
 // ---------------------------------------------------------------- tcgen05
 
 // Allocate `ncols` TMEM columns (power of two >= 32); the base address is
@@ -494,6 +505,14 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
     return r;
 }
 
+// The same to f16x2.
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
 } // namespace ptx
 
 // ------------------------------------------------------------------ UMMA descriptors
@@ -544,7 +563,13 @@ __host__ __device__ constexpr uint32_t umma_idesc_bf16(uint32_t M, uint32_t N, b
            ((N >> 3) << 17) | ((M >> 4) << 24);
 }
 
-// The same for kind::f8f6f4, both operands e4m3 (0), K-major (bits 15, 16: MN-major).
+// The same with both operands f16 (0).
+__host__ __device__ constexpr uint32_t umma_idesc_f16(uint32_t M, uint32_t N, bool b_mn_major)
+{
+    return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+
+// For kind::f8f6f4, both operands e4m3 (0), K-major (bits 15, 16: MN-major).
 __host__ __device__ constexpr uint32_t umma_idesc_e4m3(uint32_t M, uint32_t N)
 {
     return (1u << 4) | ((N >> 3) << 17) | ((M >> 4) << 24);
