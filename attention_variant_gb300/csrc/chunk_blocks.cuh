@@ -730,7 +730,7 @@ __device__ void softmax_role(const KernelCtx<D, F8> &cx, const ChunkParams &p, i
     // the warpgroups of a pair take turns on the exponentials; with softcap at D =
     // 64 they run freely, as in the standard kernel (321 us with turns, 236
     // without; at D = 128 157 and 160)
-    constexpr bool kTurns = MOD != MOD_SOFTCAP || D == 128;
+    constexpr bool kTurns = !F8 && (MOD != MOD_SOFTCAP || D == 128);
     ChunkSmem<D, F8> &sm = *cx.sm;
     const int r = threadIdx.x & 127;            // row of the block = TMEM lane
     const int wq = (threadIdx.x >> 5) & 3;      // warp's quarter of the lanes
@@ -789,21 +789,32 @@ __device__ void softmax_role(const KernelCtx<D, F8> &cx, const ChunkParams &p, i
                 load_scores<kBN>(tS, x);
                 ptx::tc_fence_before();
                 ptx::mbar_arrive(bar(sm.s_free[t])); // S[t] may be overwritten
-                if (take_turns && !turn_wait())
-                    return;
-                const int j0 = (first + kk * step) * kBN;
-                float c[F8 ? kBN / 16 : 1]; // 8 bits: what each 16 scores are multiplied by
+                // 8 bits: the factors of each 16 scores, of their weights and of O
+                float c[F8 ? kBN / 16 : 1], log_v[8], inv_v[8], tile_alpha = 1.f;
                 if constexpr (F8) {
-                    const volatile float *k = sm.factors[t][(scount - 1) & 3].k;
+                    const uint32_t at = ptx::smem_u32(&sm.factors[t][(scount - 1) & 3]);
+                    float k[8], rest[4];
+#pragma unroll
+                    for (int i = 0; i < 8; i += 4) {
+                        ptx::load_shared_v4(at + 4 * i, k + i);
+                        ptx::load_shared_v4(at + 32 + 4 * i, log_v + i);
+                        ptx::load_shared_v4(at + 64 + 4 * i, inv_v + i);
+                    }
+                    ptx::load_shared_v4(at + 96, rest);
+                    tile_alpha = rest[0];
+                    unit = rest[1];
 #pragma unroll
                     for (int g = 0; g < kBN / 16; ++g)
                         c[g] = k[g] * (MOD == MOD_SOFTCAP ? cap_in : qk);
-                    if constexpr (MOD == MOD_SOFTCAP) {
+                }
+                if (take_turns && !turn_wait())
+                    return;
+                const int j0 = (first + kk * step) * kBN;
+                if constexpr (MOD == MOD_SOFTCAP && F8) {
 #pragma unroll
-                        for (int g = 0; g < kBN / 16; ++g) {
-                            softcap_scores<16>(*reinterpret_cast<float (*)[16]>(x + 16 * g), c[g], p.softcap_out);
-                            c[g] = 1.f;
-                        }
+                    for (int g = 0; g < kBN / 16; ++g) {
+                        softcap_scores<16>(*reinterpret_cast<float (*)[16]>(x + 16 * g), c[g], p.softcap_out);
+                        c[g] = 1.f;
                     }
                 } else if constexpr (MOD == MOD_SOFTCAP) {
                     softcap_scores<kBN>(x, p.softcap_in, p.softcap_out);
@@ -814,12 +825,8 @@ __device__ void softmax_role(const KernelCtx<D, F8> &cx, const ChunkParams &p, i
                 bool rescale;
                 float alpha;
                 if constexpr (F8) {
-                    const TileFactors &fac = sm.factors[t][(scount - 1) & 3];
-                    alpha = softmax_compute_p_scaled<kBN>(x, c, fac, st, pk, rescale);
-                    const float a = *const_cast<const volatile float *>(&fac.alpha);
-                    unit = *const_cast<const volatile float *>(&fac.unit);
-                    alpha *= a;
-                    rescale |= a != 1.f;
+                    alpha = softmax_compute_p_scaled<kBN>(x, c, log_v, inv_v, st, pk, rescale) * tile_alpha;
+                    rescale |= tile_alpha != 1.f;
                 } else {
                     alpha = C::kOnes ? softmax_compute_p_exact_sum<kBN>(x, MOD == MOD_NONE ? p.qk_log2 : 1.f, st, false,
                                                                         pk, rescale)

@@ -80,35 +80,34 @@ __device__ __forceinline__ void convert_half(const uint8_t *raw, uint8_t *dst, i
 
 // What the scales of a tile do to a slot of row blocks.  V's codes are multiplied as they
 // are; the scale of a key goes into its weight, as a power of two relative to the
-// largest scale of the item so far: P = 2^(z - m + log_v), and the accumulator counts
-// in units of 2^unit (the sums divide what goes into them by 2^log_v again).  So P stays
-// below 2^(8 + kPBias) in f16 whatever the scales are, and holds 11 bits of a product of weight
-// and scale down to 2^(-14 - kPBias) of the largest.
-constexpr float kPBias = 6.f, kLeastLogV = -60.f, kLeastLog = -110.f;
+// largest scale of the item so far, v = scale 2^-unit (at least 2^-60), and the accumulator
+// counts in units of 2^unit: a weight goes into P times v and into its row's sum as it is.
+// So P stays below 2^(8 + kPBias) in f16 whatever the scales are, and holds 11 bits of a
+// product of weight and scale down to 2^(-14 - kPBias) of the largest.
+constexpr float kPBias = 6.f, kLeastLog = -110.f, kLeastV = -60.f;
 struct alignas(16) TileFactors {
-    float k[8];         // K's scales, of 16 keys each
-    float log_v[8];
-    float inv_v[8];     // 2^-log_v
-    float alpha, unit;  // what the accumulator is multiplied by first; its unit's logarithm
+    float k[8];                 // of 16 keys each
+    float log_v[8], inv_v[8];   // log2 of v, 1 / v
+    float alpha, unit;          // what the accumulator is multiplied by first; its unit's logarithm
     float pad[2];
 };
 
 // The factors of a tile for a slot whose largest scale so far is 2^top, by a warp; lane
-// g < 8 has the scales k and v of box g (0 or NaN: a box that no row sees).
-__device__ __forceinline__ void tile_factors(TileFactors &f, float k, float v, float &top)
+// g < 8 has the scales of box g (0 or NaN: a box that no row sees).
+__device__ __forceinline__ void tile_factors(TileFactors &f, float k, float scale_v, float &top)
 {
     const int lane = static_cast<int>(ptx::lane_id());
-    const float log_v = fmaxf(ptx::lg2(v), kLeastLog);
+    const float log_v = fmaxf(ptx::lg2(scale_v), kLeastLog);
     float most = log_v;
 #pragma unroll
     for (int d = 1; d < 8; d *= 2)
         most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
     most = fmaxf(top, most);
-    const float lf = fmaxf(log_v - most, kLeastLogV) + kPBias;
     if (lane < 8) {
         f.k[lane] = k > 0.f ? k : 1.f;
-        f.log_v[lane] = lf;
-        f.inv_v[lane] = ptx::ex2(-lf);
+        const float v = fmaxf(log_v - most, kLeastV) + kPBias;
+        f.log_v[lane] = v;
+        f.inv_v[lane] = ptx::ex2(-v);
         if (lane == 0) {
             f.alpha = ptx::ex2(top - most);
             f.unit = most - kPBias;
@@ -117,20 +116,22 @@ __device__ __forceinline__ void tile_factors(TileFactors &f, float k, float v, f
     top = most;
 }
 
-// softmax_compute_p_exact_sum under these factors: P in f16.
+// softmax_compute_p_exact_sum under these factors: c, of 16 scores each, in place of
+// one, log2 of v in the exponent and 1 / v on the sums of 16 weights.  P in f16.
 template <int N>
-__device__ __forceinline__ float softmax_compute_p_scaled(float (&x)[N], const float (&c)[N / 16], const TileFactors &f,
+__device__ __forceinline__ float softmax_compute_p_scaled(float (&x)[N], const float (&c)[N / 16],
+                                                          const float (&log_v)[8], const float (&inv_v)[8],
                                                           RowState &st, uint32_t (&pk)[N / 2], bool &rescale)
 {
     float mx = kNegInf;
 #pragma unroll
     for (int g = 0; g < N / 16; ++g) {
-        const float *v = x + 16 * g;
-        float a = fmaxf(v[0], v[1]), b = fmaxf(v[2], v[3]);
+        const float *s = x + 16 * g;
+        float a = fmaxf(s[0], s[1]), b = fmaxf(s[2], s[3]);
 #pragma unroll
         for (int e = 4; e < 16; e += 4) {
-            a = ptx::max3(a, v[e], v[e + 1]);
-            b = ptx::max3(b, v[e + 2], v[e + 3]);
+            a = ptx::max3(a, s[e], s[e + 1]);
+            b = ptx::max3(b, s[e + 2], s[e + 3]);
         }
         mx = fmaxf(mx, fmaxf(a, b) * c[g]); // c > 0
     }
@@ -145,9 +146,10 @@ __device__ __forceinline__ float softmax_compute_p_scaled(float (&x)[N], const f
         rescale = true;
     }
     const float nmu = (st.m_ref == kNegInf) ? 0.f : -st.m_ref;
+    float l0 = 0.f, l1 = 0.f;
 #pragma unroll
     for (int g = 0; g < N / 16; ++g) {
-        const float nm = nmu + *const_cast<const volatile float *>(&f.log_v[g]);
+        const float nm = nmu + log_v[g];
         float le[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -156,10 +158,17 @@ __device__ __forceinline__ float softmax_compute_p_scaled(float (&x)[N], const f
             const float p0 = ptx::ex2(a0), p1 = ptx::ex2(a1);
             pk[8 * g + e] = ptx::pack_f16(p0, p1);
             const int i = 2 * (e & 1);
-            ptx::add2(le[i], le[i + 1], p0, p1);
+            if (e < 2) {
+                le[i] = p0;
+                le[i + 1] = p1;
+            } else {
+                ptx::add2(le[i], le[i + 1], p0, p1);
+            }
         }
-        st.l = fmaf((le[0] + le[1]) + (le[2] + le[3]), *const_cast<const volatile float *>(&f.inv_v[g]), st.l);
+        ptx::add2(le[0], le[1], le[2], le[3]);
+        ptx::fma2(l0, l1, le[0], le[1], inv_v[g], inv_v[g], l0, l1);
     }
+    st.l += l0 + l1;
     return alpha;
 }
 
