@@ -1316,7 +1316,7 @@ fl_status chunk_run(const fl_tensor *q, const fl_tensor *k_cache, const fl_tenso
         return fail(FL_ERR_UNSUPPORTED, "%d SMs: chunks need 4", info.sm_count);
     const int64_t G = pl.Hq / pl.Hk;
     const int few_tq = G <= fl::kFewRows ? int(fl::kFewRows / G) : 1;
-    const int few_box = desc->block_table && pl.page < fl::kFewTile ? int(pl.page) : fl::kFewTile;
+    const int few_box = std::min(desc->block_table ? int(pl.page) : 256, fl::few_tile(int(pl.D), fp8));
     const CUtensorMapDataType type = fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     const CUtensorMapSwizzle rows_swizzle = fp8 && pl.D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
     fl::ChunkMaps maps;
@@ -1426,7 +1426,7 @@ fl_status chunk_run(const fl_tensor *q, const fl_tensor *k_cache, const fl_tenso
         p.q_sh = pl.Q.stride[1];
         p.q8 = ws + pl.q8;
         p.q_scale = reinterpret_cast<float *>(ws + pl.q_scale);
-        p.cost_few = (p.cost_few + 1) / 2; // half the bytes
+        p.cost_few = (p.cost_few * fl::few_tile(int(pl.D), true) / 128 + 1) / 2; // half the bytes
     }
     const cudaError_t e = (fp8 ? fl::launch_chunk_fp8 : fl::launch_chunk)(maps, p, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess)

@@ -361,7 +361,7 @@ __device__ void s_role(const KernelCtx<D, F8> &cx)
             if (!ok)
                 break;
             float scale_k = 0.f, scale_v = 0.f;
-            if constexpr (F8) {
+            if constexpr (F8) if ((lane & 7) < kBN / 16) {
                 scale_k = *const_cast<const volatile float *>(&sm.scales.k[idx % kScaleRing][lane & 7]);
                 scale_v = *const_cast<const volatile float *>(&sm.scales.v[idx % kScaleRing][lane & 7]);
             }

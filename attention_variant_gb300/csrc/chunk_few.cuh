@@ -33,13 +33,11 @@
 // shorter ones pay more is the plan (6 us until it is seen), the first loads
 // (5 us), the uneven end (5 us) and the joins (5 us).
 //
-// A cache in 8 bits (F8) goes through the same rings and products as it is, half the bytes a
-// tile: tcgen05's kind::f8f6f4 multiplies its e4m3 codes.  Q comes as two e4m3 terms, which
+// A cache in 8 bits (F8) goes through the same products as it is, half the bytes a
+// key: tcgen05's kind::f8f6f4 multiplies its e4m3 codes.  Q comes as two e4m3 terms, which
 // hold a bf16 number exactly (split_q), and a key's scale, one number per TMEM lane, goes
-// into its scores.  V's scale goes into P, as two e4m3 terms against a reference of
-// their own (kFewPTop): off by 2^-9 of a weight down to 2^-12 of the row's largest
-// product of weight and scale, and by 2^-22 of that one below.  The sums of the weights are
-// taken from the fp32 ones.
+// into its scores; P goes as two e4m3 terms with V's scale in it (few_item_fp8), off by
+// 2^-9 of a weight, and where that is more by 2^-16 of the row's largest.
 //
 //   warp  0     walks the CTA's items, publishes them, loads Q, K and V by TMA
 //   warp  1     issues S^T of both slots
@@ -61,10 +59,10 @@ constexpr float kFewRange = 60.f; // log2 units
 
 template <int D, bool F8 = false>
 struct FewCfg {
-    static constexpr int kBN = kFewTile;
+    static constexpr int kBN = few_tile(D, F8), kSub = kBN / 128; // keys of a tile, of 128 each
     static constexpr int kHalves = F8 ? 1 : D / 64;
-    static constexpr int kStages = F8 ? (D == 128 ? 5 : 10) : D == 128 ? 3 : 6; // of K, and of V
-    static constexpr int kLag = F8 ? (D == 128 ? 2 : 3) : D == 128 ? 1 : 2; // tiles that V is loaded behind K
+    static constexpr int kStages = F8 ? 5 : D == 128 ? 3 : 6; // of K, and of V
+    static constexpr int kLag = F8 ? 0 : D == 128 ? 1 : 2;  // tiles that V is loaded behind K
     static_assert(kLag < kStages, "K of the lag's tiles is loaded before V frees anything");
     static constexpr uint32_t kRowBytes = F8 ? D : 128;     // a row, or 64 columns of it
     static constexpr uint32_t kRowSwizzle = kRowBytes == 64 ? kSwizzle64B : kSwizzle128B;
@@ -74,8 +72,11 @@ struct FewCfg {
     static constexpr uint32_t kQBytes = kQParts * kQPart;
     static constexpr uint32_t kHalf = kBN * kRowBytes;      // half a K or V tile, or all of it
     static constexpr uint32_t kTileBytes = kHalves * kHalf;
-    static constexpr uint32_t kPRow = F8 ? 32 : 64;         // bytes of a key's row of P: two terms of 8 or 16 rows
+    static constexpr uint32_t kPRow = F8 ? 32 : 64;         // bytes of a key's row of P: two terms of up to 16 rows
+    // Buffers of a slot's P: the next tile's may be written while this one's product runs
+    static constexpr int kPBufs = F8 ? 2 : 1;
     static constexpr uint32_t kColS = 0, kColO = 64, kStride = 32; // TMEM columns of slot t: + 32 t
+    static constexpr uint32_t kSubS = 16;                   // and of S of the tile's second 128 keys
 };
 
 // A CTA's part of an item.  Tiles are numbered as they pass through the
@@ -115,18 +116,18 @@ struct __align__(1024) FewSmem {
     uint8_t k[C::kStages][C::kTileBytes];
     uint8_t v[C::kStages][C::kTileBytes];
     uint8_t q[2][2][C::kQBytes];     // [Q buffer][slot]
-    uint8_t p[2][C::kBN * C::kPRow]; // [slot]
+    uint8_t p[2][C::kPBufs][C::kBN * C::kPRow]; // [slot]
     uint64_t q_full[2], q_empty[2];
     uint64_t k_full[C::kStages], k_empty[C::kStages];
     uint64_t v_full[C::kStages], v_empty[C::kStages];
-    uint64_t s_full[2], s_free[2], p_full[2], pv_done[2];
+    uint64_t s_full[2], s_free[2], p_full[2][C::kPBufs], pv_done[2][C::kPBufs];
     uint64_t group[2];               // the slot's softmax warps among themselves
     uint64_t final_bar[3];
     uint64_t info_full[kInfo], info_empty[kInfo];
     FewItem info[kInfo];
     float red[2][4][kFewRows];       // maxima or sums of each softmax warp
     uint32_t rows[2][2][4];          // by tile parity, of each softmax warp: see few_softmax
-    uint32_t large[2][2][4];         // the same of rows whose P asks for a reference (8 bits)
+    uint32_t large[2][4];            // 8 bits: of tiles in turn, rows that ask for a reference
     std::conditional_t<F8, ScaleRing, char> scales;
     uint32_t tmem_base;
     uint32_t abort_flag;
@@ -143,28 +144,22 @@ struct FewCtx {
 // ------------------------------------------------------------------ producers
 
 // A ring of K or V tiles and the one warp that fills it.
-template <int D, bool F8>
+template <int D>
 struct FewRing {
-    using C = FewCfg<D, F8>;
+    using C = FewCfg<D, false>;
     const CUtensorMap *map;
     uint8_t (*tile)[C::kTileBytes];
     uint64_t *full, *empty;
     uint32_t count;
 
     // Tile v of an item into the next stage: lane g loads the g-th box, of its page.
-    __device__ __forceinline__ bool load(const FewCtx<D, F8> &cx, const ChunkParams &p, const FewItem &it, int v, int page,
-                                         bool with_scales)
+    __device__ __forceinline__ bool load(const FewCtx<D, false> &cx, const ChunkParams &p, const FewItem &it, int v, int page)
     {
         const int lane = static_cast<int>(ptx::lane_id());
         const int box = 1 << p.few_shift, key0 = (v >> it.shift) * C::kBN, left = it.L - key0;
         const uint32_t s = count % C::kStages;
         if (!warp_wait(bar(empty[s]), ((count / C::kStages) & 1) ^ 1, cx.wc, W_KV_EMPTY))
             return false;
-        if constexpr (F8) {
-            if (with_scales)
-                copy_scales<C::kBN / 16>(p, cx.sm->scales, count, bar(full[s]), page, p.few_shift, key0, it.key_lo,
-                                         it.L, it.kvh + (it.shift ? v & 1 : 0));
-        }
         const int boxes = left <= 0 ? 0 : min(C::kBN >> p.few_shift, (left + box - 1) >> p.few_shift);
         if (lane == 0)
             ptx::mbar_arrive_expect_tx(bar(full[s]), static_cast<uint32_t>(C::kHalves * boxes * box) * C::kRowBytes);
@@ -183,19 +178,48 @@ struct FewRing {
     }
 
     // Waits (bounded, ignoring the abort) for the warp's loads in flight.
-    __device__ __forceinline__ void drain(const FewCtx<D, F8> &cx) const
+    __device__ __forceinline__ void drain(const FewCtx<D, false> &cx) const
     {
         for (uint32_t idx = count > C::kStages ? count - C::kStages : 0; idx < count; ++idx)
             mbar_wait_drain(bar(full[idx % C::kStages]), (idx / C::kStages) & 1, cx.wc, W_DRAIN);
     }
 };
 
-// The page of this lane's box of key tile j.
+// Tile v of an item of a cache in 8 bits, the CTA's number `count`: K and V together, with
+// their scales.  Lane g loads the g-th box of K, lane 16 + g that of V.
 template <int D>
+__device__ __forceinline__ bool few_load_fp8(const FewCtx<D, true> &cx, const ChunkParams &p, const CUtensorMap *tm_k,
+                                             const CUtensorMap *tm_v, const FewItem &it, int v, uint32_t count, int page)
+{
+    using C = FewCfg<D, true>;
+    FewSmem<D, true> &sm = *cx.sm;
+    const int lane = static_cast<int>(ptx::lane_id()), g = lane & 15;
+    const int box = 1 << p.few_shift, key0 = (v >> it.shift) * C::kBN, left = it.L - key0;
+    const int kvh = it.kvh + (it.shift ? v & 1 : 0);
+    const uint32_t s = count % C::kStages, full = bar(sm.k_full[s]);
+    if (!warp_wait(bar(sm.k_empty[s]), ((count / C::kStages) & 1) ^ 1, cx.wc, W_KV_EMPTY))
+        return false;
+    copy_scales<C::kBN / 16>(p, sm.scales, count, full, page, p.few_shift, key0, it.key_lo, it.L, kvh);
+    const int boxes = left <= 0 ? 0 : min(C::kBN >> p.few_shift, (left + box - 1) >> p.few_shift);
+    if (lane == 0)
+        ptx::mbar_arrive_expect_tx(full, static_cast<uint32_t>(2 * boxes * box) * C::kRowBytes);
+    __syncwarp();
+    if (g < boxes) {
+        const int key = key0 + g * box;
+        const int at = p.page_shift < 0 ? key : key & ((1 << p.page_shift) - 1);
+        ptx::tma_load_4d(ptx::smem_u32(lane < 16 ? sm.k[s] : sm.v[s]) + g * box * C::kRowBytes, lane < 16 ? tm_k : tm_v,
+                         full, 0, at, kvh, page);
+    }
+    __syncwarp();
+    return true;
+}
+
+// The page of this lane's box of key tile j.
+template <int D, bool F8>
 __device__ __forceinline__ int few_page(const ChunkParams &p, const FewItem &it, int j)
 {
-    const int lane = static_cast<int>(ptx::lane_id()), key = j * FewCfg<D>::kBN + (lane << p.few_shift);
-    if (lane >= FewCfg<D>::kBN >> p.few_shift || key >= it.L)
+    const int lane = static_cast<int>(ptx::lane_id()) & (F8 ? 15 : 31), key = j * FewCfg<D, F8>::kBN + (lane << p.few_shift);
+    if (lane >= FewCfg<D, F8>::kBN >> p.few_shift || key >= it.L)
         return 0; // never loaded
     return p.page_shift < 0 ? it.b : __ldg(p.block_table + static_cast<int64_t>(it.b) * p.bt_stride + (key >> p.page_shift));
 }
@@ -205,7 +229,9 @@ __device__ __forceinline__ int few_page(const ChunkParams &p, const FewItem &it,
 // against 178 us for 64 requests of 8192 keys, 128 against 107 of 512 to 8192),
 // and V gets the warp that otherwise issues O^T of slot 1, which costs 2 to 7%
 // with larger pages (of 32 keys: 108 against 104 us of 512 to 8192).
-__device__ __forceinline__ bool few_split_loads(const ChunkParams &p) { return p.few_shift < 5; }
+// (In 8 bits a lane loads a box of each, at once.)
+template <bool F8>
+__device__ __forceinline__ bool few_split_loads(const ChunkParams &p) { return !F8 && p.few_shift < 5; }
 
 // Walks the CTA's items, publishes them, loads Q, K and, mostly, V.
 template <int D, bool F8>
@@ -216,8 +242,13 @@ __device__ void few_producer(const FewCtx<D, F8> &cx, const ChunkParams &p, cons
     constexpr int kBN = C::kBN;
     FewSmem<D, F8> &sm = *cx.sm;
     const uint32_t lane = ptx::lane_id();
-    FewRing<D, F8> keys{tm_k, sm.k, sm.k_full, sm.k_empty, 0u}, values{tm_v, sm.v, sm.v_full, sm.v_empty, 0u};
-    const bool split = few_split_loads(p);
+    std::conditional_t<F8, char, FewRing<D>> keys, values;
+    uint32_t kv_count = 0;
+    if constexpr (!F8) {
+        keys = {tm_k, sm.k, sm.k_full, sm.k_empty, 0u};
+        values = {tm_v, sm.v, sm.v_full, sm.v_empty, 0u};
+    }
+    const bool split = few_split_loads<F8>(p);
     uint32_t item_count = 0;
     bool ok = true;
     ChunkPart me{};
@@ -320,19 +351,30 @@ __device__ void few_producer(const FewCtx<D, F8> &cx, const ChunkParams &p, cons
         // not wait in shared memory for its weights (not past the item: the next
         // item's buffers may wait for the V of its last tile).  Pages are fetched
         // a tile ahead.
-        int page_next = few_page<D>(p, it, it.u_lo >> it.shift);
-        int page[C::kLag + 1]; // of the last kLag + 1 tiles, the latest first
-        for (int v = it.u_lo; v < it.u_hi + (split ? 0 : C::kLag) && ok; ++v) {
+        int page_next = few_page<D, F8>(p, it, it.u_lo >> it.shift);
+        if constexpr (F8) {
+            for (int v = it.u_lo; v < it.u_hi && ok; ++v, ++kv_count) {
+                const int page = page_next;
+                if (v + 1 < it.u_hi)
+                    page_next = few_page<D, F8>(p, it, (v + 1) >> it.shift);
+                ok = few_load_fp8(cx, p, tm_k, tm_v, it, v, kv_count, page);
+                if (!ok)
+                    break;
+            }
+        } else {
+            int page[C::kLag + 1]; // of the last kLag + 1 tiles, the latest first
+            for (int v = it.u_lo; v < it.u_hi + (split ? 0 : C::kLag) && ok; ++v) {
 #pragma unroll
-            for (int i = C::kLag; i > 0; --i)
-                page[i] = page[i - 1];
-            page[0] = page_next;
-            if (v + 1 < it.u_hi)
-                page_next = few_page<D>(p, it, (v + 1) >> it.shift);
-            if (v < it.u_hi)
-                ok = keys.load(cx, p, it, v, page[0], true);
-            if (ok && !split && v - C::kLag >= it.u_lo)
-                ok = values.load(cx, p, it, v - C::kLag, page[C::kLag], false);
+                for (int i = C::kLag; i > 0; --i)
+                    page[i] = page[i - 1];
+                page[0] = page_next;
+                if (v + 1 < it.u_hi)
+                    page_next = few_page<D, F8>(p, it, (v + 1) >> it.shift);
+                if (v < it.u_hi)
+                    ok = keys.load(cx, p, it, v, page[0]);
+                if (ok && !split && v - C::kLag >= it.u_lo)
+                    ok = values.load(cx, p, it, v - C::kLag, page[C::kLag]);
+            }
         }
         if (!ok)
             break;
@@ -351,19 +393,25 @@ __device__ void few_producer(const FewCtx<D, F8> &cx, const ChunkParams &p, cons
         }
     }
     if (!ok) {
-        keys.drain(cx);
-        values.drain(cx);
+        if constexpr (F8) {
+            for (uint32_t idx = kv_count > C::kStages ? kv_count - C::kStages : 0; idx < kv_count; ++idx)
+                mbar_wait_drain(bar(sm.k_full[idx % C::kStages]), (idx / C::kStages) & 1, cx.wc, W_DRAIN);
+        } else {
+            keys.drain(cx);
+            values.drain(cx);
+        }
         for (uint32_t n = item_count > 2 ? item_count - 2 : 0; n < item_count; ++n)
             mbar_wait_drain(bar(sm.q_full[n & 1]), (n >> 1) & 1, cx.wc, W_DRAIN);
     }
 }
 
 // Loads V alone (few_split_loads).
-template <int D, bool F8>
-__device__ void few_v_producer(const FewCtx<D, F8> &cx, const ChunkParams &p, const CUtensorMap *tm_v)
+template <int D>
+__device__ void few_v_producer(const FewCtx<D, false> &cx, const ChunkParams &p, const CUtensorMap *tm_v)
 {
+    constexpr bool F8 = false;
     FewSmem<D, F8> &sm = *cx.sm;
-    FewRing<D, F8> values{tm_v, sm.v, sm.v_full, sm.v_empty, 0u};
+    FewRing<D> values{tm_v, sm.v, sm.v_full, sm.v_empty, 0u};
     bool ok = true;
     for (uint32_t n = 0; ok; ++n) {
         const uint32_t slot = n % kInfo;
@@ -376,12 +424,12 @@ __device__ void few_v_producer(const FewCtx<D, F8> &cx, const ChunkParams &p, co
             ptx::mbar_arrive(bar(sm.info_empty[slot]));
         if (it.stop)
             return;
-        int page_next = few_page<D>(p, it, it.u_lo >> it.shift);
+        int page_next = few_page<D, F8>(p, it, it.u_lo >> it.shift);
         for (int v = it.u_lo; v < it.u_hi && ok; ++v) {
             const int page = page_next;
             if (v + 1 < it.u_hi)
-                page_next = few_page<D>(p, it, (v + 1) >> it.shift);
-            ok = values.load(cx, p, it, v, page, false);
+                page_next = few_page<D, F8>(p, it, (v + 1) >> it.shift);
+            ok = values.load(cx, p, it, v, page);
         }
     }
     values.drain(cx);
@@ -396,7 +444,7 @@ __device__ void few_s_role(const FewCtx<D, F8> &cx)
     constexpr int kBN = C::kBN, kStages = C::kStages;
     FewSmem<D, F8> &sm = *cx.sm;
     const uint32_t lane = ptx::lane_id();
-    constexpr uint32_t idesc = F8 ? umma_idesc_e4m3(kBN, kFewRows) : umma_idesc_bf16(kBN, kFewRows, false);
+    constexpr uint32_t idesc = F8 ? umma_idesc_e4m3(128, kFewRows) : umma_idesc_bf16(kBN, kFewRows, false);
     constexpr uint64_t kHi = umma_desc_hi(16, C::kGroupBytes, C::kRowSwizzle); // Q, K: K-major
     const uint32_t q_lo0 = ptx::smem_u32(sm.q[0][0]) >> 4, k_lo0 = ptx::smem_u32(sm.k[0]) >> 4;
     uint32_t idx = 0, issued[2] = {0u, 0u};
@@ -443,10 +491,13 @@ __device__ void few_s_role(const FewCtx<D, F8> &cx)
                 const uint32_t tS = cx.tmem + C::kColS + C::kStride * t;
                 if constexpr (F8) { // both terms of Q with the same K
 #pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk)
-                        ptx::mma_ss_f8(tS, kHi | (klo + 2 * (kk % (D / 32))),
-                                       kHi | (qlo + kk / (D / 32) * (C::kQPart >> 4) + 2 * (kk % (D / 32))), idesc,
-                                       kk > 0 ? 1u : 0u);
+                    for (int sub = 0; sub < C::kSub; ++sub)
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk)
+                            ptx::mma_ss_f8(tS + sub * C::kSubS,
+                                           kHi | (klo + sub * (128 * C::kRowBytes >> 4) + 2 * (kk % (D / 32))),
+                                           kHi | (qlo + kk / (D / 32) * (C::kQPart >> 4) + 2 * (kk % (D / 32))), idesc,
+                                           kk > 0 ? 1u : 0u);
                 } else {
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk)
@@ -482,6 +533,7 @@ __device__ void few_pv_role(const FewCtx<D, F8> &cx, int slot_lo, int slot_hi)
     constexpr int kBN = C::kBN, kStages = C::kStages;
     FewSmem<D, F8> &sm = *cx.sm;
     const uint32_t lane = ptx::lane_id();
+    uint64_t *const full = F8 ? sm.k_full : sm.v_full, *const empty = F8 ? sm.k_empty : sm.v_empty;
     // O^T = V^T P^T: both operands with their long index contiguous.  V^T has
     // 128 rows: at D = 64 the second 64 repeat the first (block stride 0).  P
     // has 64-byte rows of a key, 64-byte swizzle.
@@ -492,7 +544,7 @@ __device__ void few_pv_role(const FewCtx<D, F8> &cx, int slot_lo, int slot_hi)
     constexpr uint64_t kHiV = umma_desc_hi(D == 128 ? C::kHalf : 0, C::kGroupBytes, C::kRowSwizzle);
     constexpr uint64_t kHiP = umma_desc_hi(16, 8 * C::kPRow, F8 ? kSwizzle32B : kSwizzle64B);
     constexpr int kKeys = F8 ? 32 : 16; // of an MMA
-    const uint32_t v_lo0 = ptx::smem_u32(sm.v[0]) >> 4, p_lo0 = ptx::smem_u32(sm.p[0]) >> 4;
+    const uint32_t v_lo0 = ptx::smem_u32(sm.v[0]) >> 4, p_lo0 = ptx::smem_u32(sm.p[0][0]) >> 4;
     uint32_t idx = 0, pcount[2] = {0u, 0u};
     bool ok = true;
     for (uint32_t n = 0; ok; ++n) {
@@ -513,13 +565,13 @@ __device__ void few_pv_role(const FewCtx<D, F8> &cx, int slot_lo, int slot_hi)
         for (int v = u_lo; v < u_hi; ++v, ++idx) {
             const uint32_t stage = idx % kStages;
             const int t = shift ? v & 1 : 0, j0 = (v >> shift) * kBN;
-            ok = warp_wait(bar(sm.v_full[stage]), (idx / kStages) & 1, cx.wc, W_KV_FULL);
+            ok = warp_wait(bar(full[stage]), (idx / kStages) & 1, cx.wc, W_KV_FULL);
             if (!ok)
                 break;
             if (v < lo || v >= hi || t < slot_lo || t > slot_hi) {
                 // no row sees it, or another warp's
                 if (lane == 0)
-                    ptx::mbar_arrive(bar(sm.v_empty[stage]));
+                    ptx::mbar_arrive(bar(empty[stage]));
                 __syncwarp();
                 continue;
             }
@@ -539,21 +591,22 @@ __device__ void few_pv_role(const FewCtx<D, F8> &cx, int slot_lo, int slot_hi)
                 ptx::fence_proxy_async_smem();
                 __syncwarp();
             }
-            ok = warp_wait(bar(sm.p_full[t]), pcount[t] & 1, cx.wc, W_P_FULL);
+            const uint32_t buf = pcount[t] % C::kPBufs; // of P
+            ok = warp_wait(bar(sm.p_full[t][buf]), (pcount[t] / C::kPBufs) & 1, cx.wc, W_P_FULL);
             if (!ok)
                 break;
             ++pcount[t];
             ptx::tc_fence_after();
             if (lane == 0) {
-                const uint32_t vlo = v_lo0 + stage * (C::kTileBytes >> 4), plo = p_lo0 + t * (kBN * C::kPRow >> 4);
+                const uint32_t vlo = v_lo0 + stage * (C::kTileBytes >> 4), plo = p_lo0 + (t * C::kPBufs + buf) * (kBN * C::kPRow >> 4);
                 const bool begun = v - first >= 1 << shift; // not the slot's first tile
 #pragma unroll
                 for (int kk = 0; kk < kBN / kKeys; ++kk)
                     (F8 ? ptx::mma_ss_f8 : ptx::mma_ss)(
                         cx.tmem + C::kColO + C::kStride * t, kHiV | (vlo + kk * (kKeys * C::kRowBytes >> 4)),
                         kHiP | (plo + kk * (kKeys * C::kPRow >> 4)), idesc, (begun || kk > 0) ? 1u : 0u);
-                ptx::mma_commit(bar(sm.pv_done[t]));
-                ptx::mma_commit(bar(sm.v_empty[stage]));
+                ptx::mma_commit(bar(sm.pv_done[t][buf]));
+                ptx::mma_commit(bar(empty[stage]));
             }
             __syncwarp();
         }
@@ -602,41 +655,34 @@ __device__ __forceinline__ void few_load_o(uint32_t tO, uint32_t (&o)[2 * R])
     ptx::reg_fence<2 * R>(o);
 }
 
-// P in 8 bits: weights times V's scale, 2^(z + log2 s - ref), as two e4m3 terms, the second 16
-// times what the first left out.  A row's reference is set to make the largest of a
-// tile 2^5, and again where one would pass e4m3's 448.
-constexpr float kFewPTop = 5.f, kFewPMost = 8.8f, kFewPRest = 16.f;
-constexpr float kFewPUnset = -1e30f;
-
 // What a softmax thread carries from item to item.
 struct FewState {
     uint32_t s, pv, group, tiles; // phases of s_full, pv_done, group; tiles so far
-    uint32_t loaded;              // tiles of the CTA before this item
 };
 
 // One item of at most R rows.  False when a wait ran out.
-template <int MOD, int D, bool F8, int R>
-__device__ __forceinline__ bool few_item(const FewCtx<D, F8> &cx, const ChunkParams &p, const FewItem &inf, int t,
+template <int MOD, int D, int R>
+__device__ __forceinline__ bool few_item(const FewCtx<D, false> &cx, const ChunkParams &p, const FewItem &inf, int t,
                                          FewState &ct)
 {
-    using C = FewCfg<D, F8>;
+    using C = FewCfg<D, false>;
     constexpr int kBN = C::kBN;
-    FewSmem<D, F8> &sm = *cx.sm;
+    FewSmem<D, false> &sm = *cx.sm;
     const int r = threadIdx.x & 127; // key of the tile = TMEM lane of S^T; of O^T: dimension
     const int wq = (threadIdx.x >> 5) & 3, lane = static_cast<int>(ptx::lane_id());
     const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
     const uint32_t tS = cx.tmem + lanes + C::kColS + C::kStride * t;
     const uint32_t tO = cx.tmem + lanes + C::kColO + C::kStride * t;
     const uint32_t b_group = bar(sm.group[t]);
-    const float c = MOD == MOD_NONE && !F8 ? p.qk_log2 : 1.f; // in 8 bits it is in q_factor
+    const float c = MOD == MOD_NONE ? p.qk_log2 : 1.f;
     ScoreMod smod;
     smod.qk_log2 = p.qk_log2;
     smod.softcap_in = p.softcap_in;
     smod.softcap_out = p.softcap_out;
     smod.alibi_c = smod.scale = smod.b = smod.h = 0.f;
-    // 64-byte swizzle: 16-byte unit u of key r at u ^ (r / 2 mod 4); 32-byte: at u ^ (r / 4 mod 2)
-    uint4 *const pdst = reinterpret_cast<uint4 *>(sm.p[t] + r * C::kPRow);
-    const int sw = F8 ? (r >> 2) & 1 : (r >> 1) & 3;
+    // 64-byte swizzle: 16-byte unit u of key r at u ^ (r / 2 mod 4)
+    uint4 *const pdst = reinterpret_cast<uint4 *>(sm.p[t][0] + r * C::kPRow);
+    const int sw = (r >> 1) & 3;
     auto group_sync = [&]() {
         ptx::mbar_arrive(b_group);
         return warp_wait(b_group, ct.group++ & 1, cx.wc, W_JOIN);
@@ -659,31 +705,12 @@ __device__ __forceinline__ bool few_item(const FewCtx<D, F8> &cx, const ChunkPar
     }
     uint32_t set = 0;  // rows that have a reference
     bool moved = false; // some reference is not 0
-    // 8 bits: the factor of a row's scores, the reference of its P
-    float q_factor[F8 ? R : 1], mp[F8 ? R : 1];
-    if constexpr (F8) {
-#pragma unroll
-        for (int n = 0; n < R; ++n) {
-            const int s = fast_div(n, p.div_g);
-            mp[n] = n < rows ? kFewPUnset : -kFewPUnset; // columns past the rows ask for nothing
-            q_factor[n] = n < rows && inf.n_parts
-                              ? __ldcg(p.q_scale + static_cast<int64_t>(inf.t0 + s) * p.Hq + (inf.kvh + t) * p.G + n - s * p.G) *
-                                    (MOD == MOD_NONE ? p.qk_log2 : 1.f)
-                              : 0.f;
-        }
-    }
     for (int kk = 0; kk < n_mine; ++kk) {
         if (!warp_wait(bar(sm.s_full[t]), ct.s & 1, cx.wc, W_S_FULL))
             return false;
         ++ct.s;
         ++ct.tiles;
         ptx::tc_fence_after();
-        float key_k = 1.f, key_v = 1.f; // 8 bits: the key's scales
-        if constexpr (F8) {
-            const uint32_t i = (ct.loaded + static_cast<uint32_t>(f.first + kk * f.step - inf.u_lo)) % kScaleRing;
-            key_k = *const_cast<const volatile float *>(&sm.scales.k[i][r >> 4]);
-            key_v = *const_cast<const volatile float *>(&sm.scales.v[i][r >> 4]);
-        }
         float x[R];
         {
             uint32_t raw[R];
@@ -700,13 +727,6 @@ __device__ __forceinline__ bool few_item(const FewCtx<D, F8> &cx, const ChunkPar
         ptx::tc_fence_before();
         ptx::mbar_arrive(bar(sm.s_free[t]));
         const int j0 = ((f.first + kk * f.step) >> inf.shift) * kBN;
-        if constexpr (F8) {
-#pragma unroll
-            for (int n = 0; n < R; n += 2) {
-                ptx::fma2(x[n], x[n + 1], x[n], x[n + 1], key_k, key_k, 0.f, 0.f);
-                ptx::fma2(x[n], x[n + 1], x[n], x[n + 1], q_factor[n], q_factor[n + 1], 0.f, 0.f);
-            }
-        }
         apply_score_mod<MOD, R>(x, smod, 0, j0);
         if (!(j0 >= full_lo && j0 + kBN <= full_hi)) {
 #pragma unroll
@@ -741,22 +761,6 @@ __device__ __forceinline__ bool few_item(const FewCtx<D, F8> &cx, const ChunkPar
         bits = __reduce_or_sync(0xffffffffu, bits);
         if (lane == 0)
             sm.rows[t][ct.tiles & 1][wq] = bits;
-        uint32_t large = 0; // 8 bits: rows whose P wants another reference
-        const float log_v = F8 ? ptx::lg2(key_v) : 0.f;
-        if constexpr (F8) {
-            float most = x[0] - mp[0];
-#pragma unroll
-            for (int n = 1; n < R; ++n)
-                most = fmaxf(most, x[n] - mp[n]);
-            if (most + log_v > kFewPMost) {
-#pragma unroll
-                for (int n = 0; n < R; ++n)
-                    large |= x[n] - mp[n] + log_v > kFewPMost ? 1u << n : 0u;
-            }
-            large = __reduce_or_sync(0xffffffffu, large);
-            if (lane == 0)
-                sm.large[t][ct.tiles & 1][wq] = large;
-        }
         float w[R];
         few_exp(x, c, m, !moved, w);
         if (!group_sync())
@@ -765,13 +769,9 @@ __device__ __forceinline__ bool few_item(const FewCtx<D, F8> &cx, const ChunkPar
             const volatile uint32_t *all = sm.rows[t][ct.tiles & 1];
             bits = all[0] | all[1] | all[2] | all[3];
         }
-        if constexpr (F8) {
-            const volatile uint32_t *all = sm.large[t][ct.tiles & 1];
-            large = (all[0] | all[1] | all[2] | all[3]) & row_bits;
-        }
         if (kk > 0) {
             // the previous tile's product has read P and landed in O^T
-            if (!warp_wait(bar(sm.pv_done[t]), ct.pv & 1, cx.wc, W_O_FULL))
+            if (!warp_wait(bar(sm.pv_done[t][0]), ct.pv & 1, cx.wc, W_O_FULL))
                 return false;
             ++ct.pv;
             ptx::tc_fence_after();
@@ -803,12 +803,7 @@ __device__ __forceinline__ bool few_item(const FewCtx<D, F8> &cx, const ChunkPar
                 m[n] = m_new;
             }
             set |= (bits | bits >> 16) & row_bits;
-            if (ask && F8) {
-#pragma unroll
-                for (int n = 0; n < R; ++n)
-                    l[n] *= alpha[n];
-                few_exp(x, c, m, false, w);
-            } else if (ask) {
+            if (ask) {
                 if (kk > 0) {
                     uint32_t o[2 * R];
                     few_load_o<R>(tO, o);
@@ -827,65 +822,6 @@ __device__ __forceinline__ bool few_item(const FewCtx<D, F8> &cx, const ChunkPar
                 few_exp(x, c, m, false, w);
             }
         }
-        if constexpr (F8) {
-            if (large || inf.n_parts == 0) {
-                // the largest of each row, and O^T to its new reference
-                if (!group_sync()) // the maxima above have been read
-                    return false;
-#pragma unroll
-                for (int n = 0; n < R; ++n) {
-                    const int mx = __reduce_max_sync(0xffffffffu, ordered(x[n] + log_v));
-                    if (lane == n)
-                        sm.red[t][wq][n] = unordered(mx);
-                }
-                if (!group_sync())
-                    return false;
-                float beta[R];
-#pragma unroll
-                for (int n = 0; n < R; ++n) {
-                    beta[n] = 1.f;
-                    if (large >> n & 1u) {
-                        const volatile float *red = &sm.red[t][0][n];
-                        const float top = fmaxf(fmaxf(red[0], red[kFewRows]), fmaxf(red[2 * kFewRows], red[3 * kFewRows])) - kFewPTop;
-                        beta[n] = mp[n] == kFewPUnset ? 0.f : ptx::ex2(mp[n] - top);
-                        mp[n] = top;
-                    }
-                }
-                if (kk > 0) {
-                    uint32_t o[2 * R];
-                    few_load_o<R>(tO, o);
-#pragma unroll
-                    for (int n = 0; n < R; ++n) { // a row without a key so far holds zeros
-                        o[n] = __float_as_uint(__uint_as_float(o[n]) * beta[n]);
-                        o[R + n] = __float_as_uint(__uint_as_float(o[R + n]) * beta[n]);
-                    }
-                    if constexpr (R == 8)
-                        ptx::tmem_st16(tO, o);
-                    else
-                        ptx::tmem_st32(tO, o);
-                    ptx::tmem_wait_st();
-                }
-            }
-            uint32_t hi[R / 4], lo[R / 4];
-#pragma unroll
-            for (int n = 0; n < R; n += 4) {
-                float e[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    e[i] = ptx::ex2(x[n + i] - mp[n + i] + log_v);
-                const uint32_t h0 = to_e4m3x2(e[0], e[1]), h1 = to_e4m3x2(e[2], e[3]);
-                const float2 a = from_e4m3x2(h0), b = from_e4m3x2(h1);
-                hi[n / 4] = h0 | h1 << 16;
-                lo[n / 4] = to_e4m3x2((e[0] - a.x) * kFewPRest, (e[1] - a.y) * kFewPRest) |
-                            to_e4m3x2((e[2] - b.x) * kFewPRest, (e[3] - b.y) * kFewPRest) << 16;
-            }
-            if constexpr (R == 8) {
-                pdst[sw] = make_uint4(hi[0], hi[1], lo[0], lo[1]);
-            } else {
-                pdst[sw] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                pdst[1 ^ sw] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-            }
-        } else {
         // the key's row of P: R rounded weights, then R rests
         uint32_t hi[R / 2], lo[R / 2];
 #pragma unroll
@@ -899,16 +835,15 @@ __device__ __forceinline__ bool few_item(const FewCtx<D, F8> &cx, const ChunkPar
             pdst[u ^ sw] = make_uint4(hi[4 * u], hi[4 * u + 1], hi[4 * u + 2], hi[4 * u + 3]);
             pdst[(R / 8 + u) ^ sw] = make_uint4(lo[4 * u], lo[4 * u + 1], lo[4 * u + 2], lo[4 * u + 3]);
         }
-        }
         ptx::fence_proxy_async_smem();
         ptx::tc_fence_before();
-        ptx::mbar_arrive(bar(sm.p_full[t]));
+        ptx::mbar_arrive(bar(sm.p_full[t][0]));
 #pragma unroll
         for (int n = 0; n < R; n += 2)
             ptx::add2(l[n], l[n + 1], w[n], w[n + 1]);
     }
     if (n_mine) {
-        if (!warp_wait(bar(sm.pv_done[t]), ct.pv & 1, cx.wc, W_O_FULL))
+        if (!warp_wait(bar(sm.pv_done[t][0]), ct.pv & 1, cx.wc, W_O_FULL))
             return false;
         ++ct.pv;
         ptx::tc_fence_after();
@@ -933,7 +868,7 @@ __device__ __forceinline__ bool few_item(const FewCtx<D, F8> &cx, const ChunkPar
         few_load_o<R>(tO, raw);
 #pragma unroll
         for (int n = 0; n < R; ++n)
-            o[n] = __uint_as_float(raw[n]) + __uint_as_float(raw[R + n]) * (F8 ? 1.f / kFewPRest : 1.f);
+            o[n] = __uint_as_float(raw[n]) + __uint_as_float(raw[R + n]);
     } else {
 #pragma unroll
         for (int n = 0; n < R; ++n)
@@ -946,11 +881,8 @@ __device__ __forceinline__ bool few_item(const FewCtx<D, F8> &cx, const ChunkPar
         float *mine = partial<D>(p, inf.cta, inf.mine, t), *sums = mine + kFewRows * 128;
 #pragma unroll
         for (int n = 0; n < R; ++n) {
-            if (n < rows && (D == 128 || (n & 1) == r >> 6)) {
-                if constexpr (F8) // from P's reference to the weights'
-                    o[n] = mp[n] == kFewPUnset ? 0.f : o[n] * ptx::ex2(mp[n] - m[n]);
+            if (n < rows && (D == 128 || (n & 1) == r >> 6))
                 mine[n * 128 + dim] = o[n];
-            }
             if (r == n)
                 sums[n] = m[n];
         }
@@ -967,14 +899,10 @@ __device__ __forceinline__ bool few_item(const FewCtx<D, F8> &cx, const ChunkPar
     // a row's sum per lane, so that the reciprocals and logarithms are taken at once
     const volatile float *red = sm.red[t][0] + (lane & (R - 1));
     const float sum = red[0] + red[kFewRows] + red[2 * kFewRows] + red[3 * kFewRows];
-    const float inv = sum == 0.f ? 0.f : ptx::rcp_approx(sum), log_l = F8 ? ptx::lg2(sum) : 0.f;
+    const float inv = sum == 0.f ? 0.f : ptx::rcp_approx(sum);
 #pragma unroll
     for (int n = 0; n < R; ++n) {
-        float norm;
-        if constexpr (F8) // from P's reference to the weights' and over their sum, in one exponent
-            norm = mp[n] == kFewPUnset ? 0.f : ptx::ex2(mp[n] - m[n] - __shfl_sync(0xffffffffu, log_l, n));
-        else
-            norm = __shfl_sync(0xffffffffu, inv, n);
+        const float norm = __shfl_sync(0xffffffffu, inv, n);
         if (n >= rows || (D == 64 && (n & 1) != r >> 6))
             continue;
         const int s = fast_div(n, p.div_g);
@@ -992,11 +920,11 @@ __device__ __forceinline__ bool few_item(const FewCtx<D, F8> &cx, const ChunkPar
     return true;
 }
 
-template <int MOD, int D, bool F8>
-__device__ void few_softmax(const FewCtx<D, F8> &cx, const ChunkParams &p, int t)
+template <int MOD, int D>
+__device__ void few_softmax(const FewCtx<D, false> &cx, const ChunkParams &p, int t)
 {
-    FewSmem<D, F8> &sm = *cx.sm;
-    FewState ct{0u, 0u, 0u, 0u, 0u};
+    FewSmem<D, false> &sm = *cx.sm;
+    FewState ct{0u, 0u, 0u, 0u};
     for (uint32_t item = 0;; ++item) {
         if (!warp_wait(bar(sm.info_full[item % kInfo]), (item / kInfo) & 1, cx.wc, W_INFO_FULL))
             return;
@@ -1004,8 +932,385 @@ __device__ void few_softmax(const FewCtx<D, F8> &cx, const ChunkParams &p, int t
         if (inf.stop)
             return;
         // an odd head's item has no second slot; half the rows, half the work
-        if (t < inf.heads && !(inf.rows <= 8 ? few_item<MOD, D, F8, 8>(cx, p, inf, t, ct)
-                                             : few_item<MOD, D, F8, 16>(cx, p, inf, t, ct)))
+        if (t < inf.heads && !(inf.rows <= 8 ? few_item<MOD, D, 8>(cx, p, inf, t, ct)
+                                             : few_item<MOD, D, 16>(cx, p, inf, t, ct)))
+            return;
+        __syncwarp();
+        if (ptx::lane_id() == 0)
+            ptx::mbar_arrive(bar(sm.info_empty[item % kInfo]));
+    }
+}
+
+// ------------------------------------------------------------------ softmax, 8 bits
+//
+// A thread has keys r (and, of a tile of 256, 128 + r).  One reference a row, ref, for the
+// weights times V's scale: P = 2^(z + log2 s - ref), as two e4m3 terms, the second 16
+// times what the first left out; the row's sum takes P / s.  The reference makes the
+// largest of a tile 2^kFewTop when it is set, and is set again where one would pass
+// e4m3's 448: until then the slot's warps only agree, once a tile, that none does.
+
+constexpr float kFewTop = 2.f, kFewMost = 8.8f, kFewRest = 16.f;
+
+struct FewState8 {
+    uint32_t s, group, tiles; // phases of s_full, group; tiles so far
+    uint32_t loaded;          // tiles of the CTA before this item
+};
+
+template <int R>
+__device__ __forceinline__ void few_load_o8(uint32_t tO, uint32_t (&o)[2 * R])
+{
+    if constexpr (R == 4)
+        ptx::tmem_ld8(tO, o);
+    else if constexpr (R == 8)
+        ptx::tmem_ld16(tO, o);
+    else
+        ptx::tmem_ld32(tO, o);
+    ptx::tmem_wait_ld();
+    ptx::reg_fence<2 * R>(o);
+}
+
+// A key's row of P and its part of the sums: d = log2 of P.
+template <int R>
+__device__ __forceinline__ void few_p8(const float (&d)[R], float inv_v, float (&sum)[R], uint32_t (&hi)[R / 4],
+                                       uint32_t (&lo)[R / 4])
+{
+#pragma unroll
+    for (int n = 0; n < R; n += 4) {
+        float e[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            e[i] = ptx::ex2(d[n + i]);
+        ptx::fma2(sum[n], sum[n + 1], e[0], e[1], inv_v, inv_v, sum[n], sum[n + 1]);
+        ptx::fma2(sum[n + 2], sum[n + 3], e[2], e[3], inv_v, inv_v, sum[n + 2], sum[n + 3]);
+        const uint32_t h0 = to_e4m3x2(e[0], e[1]), h1 = to_e4m3x2(e[2], e[3]);
+        const float2 a = from_e4m3x2(h0), b = from_e4m3x2(h1);
+        hi[n / 4] = h0 | h1 << 16;
+        lo[n / 4] = to_e4m3x2((e[0] - a.x) * kFewRest, (e[1] - a.y) * kFewRest) |
+                    to_e4m3x2((e[2] - b.x) * kFewRest, (e[3] - b.y) * kFewRest) << 16;
+    }
+}
+
+// One item of at most R rows.  False when a wait ran out.
+template <int MOD, int D, int R>
+__device__ __forceinline__ bool few_item_fp8(const FewCtx<D, true> &cx, const ChunkParams &p, const FewItem &inf, int t,
+                                             FewState8 &ct)
+{
+    using C = FewCfg<D, true>;
+    constexpr int kBN = C::kBN, kSub = C::kSub;
+    FewSmem<D, true> &sm = *cx.sm;
+    const int r = threadIdx.x & 127;
+    const int wq = (threadIdx.x >> 5) & 3, lane = static_cast<int>(ptx::lane_id());
+    const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
+    const uint32_t tS = cx.tmem + lanes + C::kColS + C::kStride * t;
+    const uint32_t tO = cx.tmem + lanes + C::kColO + C::kStride * t;
+    const uint32_t b_group = bar(sm.group[t]);
+    ScoreMod smod;
+    smod.qk_log2 = p.qk_log2;
+    smod.softcap_in = p.softcap_in;
+    smod.softcap_out = p.softcap_out;
+    smod.alibi_c = smod.scale = smod.b = smod.h = 0.f;
+    const int sw = (r >> 2) & 1; // 32-byte swizzle: 16-byte unit u of key r at u ^ (r / 4 mod 2)
+    auto group_wait = [&]() { return warp_wait(b_group, ct.group++ & 1, cx.wc, W_JOIN); };
+    const FewTiles f = few_tiles(inf, t);
+    const int n_mine = f.hi > f.first ? (f.hi - f.first + f.step - 1) / f.step : 0;
+    const int rows = inf.rows, pos0 = inf.pos0;
+    int full_lo, full_hi, unused;
+    {
+        const int last = pos0 + fast_div(rows - 1, p.div_g);
+        key_range(p, inf.L, last, last, full_lo, unused);
+        key_range(p, inf.L, pos0, pos0, unused, full_hi);
+    }
+    float ref[R], l[R], q_factor[R];
+#pragma unroll
+    for (int n = 0; n < R; ++n) {
+        const int s = fast_div(n, p.div_g);
+        l[n] = 0.f;
+        ref[n] = n < rows ? 0.f : 1e30f; // columns past the rows ask for nothing
+        q_factor[n] = n < rows && inf.n_parts
+                          ? __ldcg(p.q_scale + static_cast<int64_t>(inf.t0 + s) * p.Hq + (inf.kvh + t) * p.G + n - s * p.G) *
+                                (MOD == MOD_NONE ? p.qk_log2 : 1.f)
+                          : 0.f;
+    }
+    const uint32_t row_bits = (1u << rows) - 1;
+    uint32_t unset = row_bits; // rows without a reference, which counts as 0
+    for (int kk = 0; kk < n_mine; ++kk) {
+        if (!warp_wait(bar(sm.s_full[t]), ct.s & 1, cx.wc, W_S_FULL))
+            return false;
+        ++ct.s;
+        const uint32_t buf = ct.tiles % C::kPBufs, buf_phase = (ct.tiles / C::kPBufs) & 1; // of P
+        const uint32_t ring = (ct.loaded + static_cast<uint32_t>(f.first + kk * f.step - inf.u_lo)) % kScaleRing;
+        volatile uint32_t *const flags = &sm.large[t][ct.tiles & 3];
+        const int j0 = ((f.first + kk * f.step) >> inf.shift) * kBN;
+        ++ct.tiles;
+        ptx::tc_fence_after();
+        uint32_t raw[kSub][R];
+        float key_k[kSub], log_v[kSub], inv_v[kSub];
+#pragma unroll
+        for (int sub = 0; sub < kSub; ++sub) {
+            if constexpr (R == 4)
+                ptx::tmem_ld4(tS + sub * C::kSubS, raw[sub]);
+            else if constexpr (R == 8)
+                ptx::tmem_ld8(tS + sub * C::kSubS, raw[sub]);
+            else
+                ptx::tmem_ld16(tS + sub * C::kSubS, raw[sub]);
+            key_k[sub] = *const_cast<const volatile float *>(&sm.scales.k[ring][sub * 8 + (r >> 4)]);
+            log_v[sub] = *const_cast<const volatile float *>(&sm.scales.v[ring][sub * 8 + (r >> 4)]);
+        }
+        ptx::tmem_wait_ld();
+#pragma unroll
+        for (int sub = 0; sub < kSub; ++sub)
+            ptx::reg_fence<R>(raw[sub]);
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(bar(sm.s_free[t]));
+        // ---- log2 of P, relative to the references as they are
+        float d[kSub][R];
+        bool more = false;
+#pragma unroll
+        for (int sub = 0; sub < kSub; ++sub) {
+            log_v[sub] = fmaxf(ptx::lg2(log_v[sub]), kLeastLog);
+            inv_v[sub] = ptx::ex2(-log_v[sub]);
+            float (&x)[R] = d[sub];
+            if constexpr (MOD == MOD_NONE) {
+#pragma unroll
+                for (int n = 0; n < R; n += 2) {
+                    float a0, a1;
+                    ptx::fma2(a0, a1, q_factor[n], q_factor[n + 1], key_k[sub], key_k[sub], 0.f, 0.f);
+                    ptx::fma2(x[n], x[n + 1], __uint_as_float(raw[sub][n]), __uint_as_float(raw[sub][n + 1]), a0, a1,
+                              log_v[sub] - ref[n], log_v[sub] - ref[n + 1]);
+                }
+            } else {
+#pragma unroll
+                for (int n = 0; n < R; ++n)
+                    x[n] = __uint_as_float(raw[sub][n]) * (q_factor[n] * key_k[sub]);
+                apply_score_mod<MOD, R>(x, smod, 0, j0);
+#pragma unroll
+                for (int n = 0; n < R; ++n)
+                    x[n] += log_v[sub] - ref[n];
+            }
+            if (!(j0 >= full_lo && j0 + kBN <= full_hi)) {
+                const int key = j0 + sub * 128 + r;
+#pragma unroll
+                for (int n = 0; n < R; ++n) {
+                    int lo, hi;
+                    const int pos = pos0 + fast_div(n, p.div_g);
+                    key_range(p, inf.L, pos, pos, lo, hi);
+                    if (key < lo || key >= hi)
+                        x[n] = kNegInf;
+                }
+            }
+            float most = x[0];
+#pragma unroll
+            for (int n = 1; n < R; ++n)
+                most = fmaxf(most, x[n]);
+            more |= most > (unset ? kNegInf : kFewMost);
+        }
+        if (__any_sync(0xffffffffu, more)) { // bit n: a key of row n asks for a new reference
+            uint32_t bits = 0;
+#pragma unroll
+            for (int sub = 0; sub < kSub; ++sub)
+#pragma unroll
+                for (int n = 0; n < R; ++n)
+                    bits |= d[sub][n] > (unset >> n & 1u ? kNegInf : kFewMost) ? 1u << n : 0u;
+            bits = __reduce_or_sync(0xffffffffu, bits);
+            if (lane == 0)
+                atomicOr(&sm.large[t][(ct.tiles - 1) & 3], bits);
+            __syncwarp();
+        }
+        ptx::mbar_arrive(b_group);
+        // ---- P, as if no row did
+        float sum[R];
+        uint32_t hi[kSub][R / 4], lo[kSub][R / 4];
+#pragma unroll
+        for (int n = 0; n < R; ++n)
+            sum[n] = l[n];
+#pragma unroll
+        for (int sub = 0; sub < kSub; ++sub)
+            few_p8<R>(d[sub], inv_v[sub], sum, hi[sub], lo[sub]);
+        if (!group_wait())
+            return false;
+        const uint32_t large = *flags & row_bits;
+        // the word of the next tile but one: every warp has read what it held
+        if (r == 0)
+            sm.large[t][(ct.tiles + 1) & 3] = 0;
+        if (large || inf.n_parts == 0) {
+            // the largest of each row that asked, over the slot's warps
+#pragma unroll
+            for (int n = 0; n < R; ++n) {
+                float top = d[0][n];
+                if constexpr (kSub == 2)
+                    top = fmaxf(top, d[1][n]);
+                const int mx = __reduce_max_sync(0xffffffffu, ordered(top));
+                if (lane == n)
+                    sm.red[t][wq][n] = unordered(mx);
+            }
+            ptx::mbar_arrive(b_group);
+            if (!group_wait())
+                return false;
+            float beta[R];
+#pragma unroll
+            for (int n = 0; n < R; ++n) {
+                beta[n] = 1.f;
+                if (large >> n & 1u) {
+                    const volatile float *red = &sm.red[t][0][n];
+                    const float up = fmaxf(fmaxf(red[0], red[kFewRows]), fmaxf(red[2 * kFewRows], red[3 * kFewRows])) - kFewTop;
+                    beta[n] = unset >> n & 1u ? 0.f : ptx::ex2(-up);
+                    ref[n] += up;
+#pragma unroll
+                    for (int sub = 0; sub < kSub; ++sub)
+                        d[sub][n] -= up;
+                }
+                sum[n] = l[n] * beta[n];
+            }
+            unset &= ~large;
+            if (kk > 0) {
+                const uint32_t last = ct.tiles - 2; // the tile before, its product done
+                if (!warp_wait(bar(sm.pv_done[t][last % C::kPBufs]), (last / C::kPBufs) & 1, cx.wc, W_O_FULL))
+                    return false;
+                ptx::tc_fence_after();
+                uint32_t o[2 * R];
+                few_load_o8<R>(tO, o);
+#pragma unroll
+                for (int n = 0; n < R; ++n) { // a row without a key so far holds zeros
+                    o[n] = __float_as_uint(__uint_as_float(o[n]) * beta[n]);
+                    o[R + n] = __float_as_uint(__uint_as_float(o[R + n]) * beta[n]);
+                }
+                if constexpr (R == 4)
+                    ptx::tmem_st8(tO, o);
+                else if constexpr (R == 8)
+                    ptx::tmem_st16(tO, o);
+                else
+                    ptx::tmem_st32(tO, o);
+                ptx::tmem_wait_st();
+            }
+#pragma unroll
+            for (int sub = 0; sub < kSub; ++sub)
+                few_p8<R>(d[sub], inv_v[sub], sum, hi[sub], lo[sub]);
+        }
+#pragma unroll
+        for (int n = 0; n < R; ++n)
+            l[n] = sum[n];
+        if (kk >= C::kPBufs) {
+            // the product of the buffer's last tile has read it
+            if (!warp_wait(bar(sm.pv_done[t][buf]), buf_phase ^ 1, cx.wc, W_O_FULL))
+                return false;
+        }
+#pragma unroll
+        for (int sub = 0; sub < kSub; ++sub) {
+            uint4 *const pdst = reinterpret_cast<uint4 *>(sm.p[t][buf] + (sub * 128 + r) * C::kPRow);
+            if constexpr (R == 4) {
+                pdst[sw] = make_uint4(hi[sub][0], lo[sub][0], 0, 0);
+            } else if constexpr (R == 8) {
+                pdst[sw] = make_uint4(hi[sub][0], hi[sub][1], lo[sub][0], lo[sub][1]);
+            } else {
+                pdst[sw] = make_uint4(hi[sub][0], hi[sub][1], hi[sub][2], hi[sub][3]);
+                pdst[1 ^ sw] = make_uint4(lo[sub][0], lo[sub][1], lo[sub][2], lo[sub][3]);
+            }
+        }
+        ptx::fence_proxy_async_smem();
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(bar(sm.p_full[t][buf]));
+    }
+    if (n_mine) {
+        const uint32_t last = ct.tiles - 1;
+        if (!warp_wait(bar(sm.pv_done[t][last % C::kPBufs]), (last / C::kPBufs) & 1, cx.wc, W_O_FULL))
+            return false;
+        ptx::tc_fence_after();
+    }
+    if (inf.n_parts == 0) // the warm-up
+        return true;
+    // ---- the slot's sums over the warp, halved at each exchange until lane i
+    // holds row i mod R
+#pragma unroll
+    for (int h = R / 2; h; h >>= 1) {
+        const bool up = lane & h;
+#pragma unroll
+        for (int i = 0; i < h; ++i)
+            l[i] = (up ? l[i + h] : l[i]) + __shfl_xor_sync(0xffffffffu, up ? l[i] : l[i + h], h);
+    }
+#pragma unroll
+    for (int d = R; d < 32; d *= 2)
+        l[0] += __shfl_xor_sync(0xffffffffu, l[0], d);
+    float o[R];
+    if (n_mine) {
+        uint32_t raw[2 * R];
+        few_load_o8<R>(tO, raw);
+#pragma unroll
+        for (int n = 0; n < R; ++n)
+            o[n] = __uint_as_float(raw[n]) + __uint_as_float(raw[R + n]) * (1.f / kFewRest);
+    } else {
+#pragma unroll
+        for (int n = 0; n < R; ++n)
+            o[n] = 0.f;
+    }
+#pragma unroll
+    for (int n = 0; n < R; ++n)
+        if (unset >> n & 1u)
+            ref[n] = kNegInf; // no key
+    // lane = dimension; at D = 64 the upper 64 lanes repeat the lower ones and
+    // take the odd rows
+    const int dim = D == 128 ? r : r & 63;
+    if (inf.n_parts > 1) {
+        float *mine = partial<D>(p, inf.cta, inf.mine, t), *sums = mine + kFewRows * 128;
+#pragma unroll
+        for (int n = 0; n < R; ++n) {
+            if (n < rows && (D == 128 || (n & 1) == r >> 6))
+                mine[n * 128 + dim] = o[n];
+            if (r == n)
+                sums[n] = ref[n];
+        }
+        if (lane < R)
+            sums[kFewRows + wq * kFewRows + lane] = l[0];
+        return true;
+    }
+    auto group_sync = [&]() {
+        ptx::mbar_arrive(b_group);
+        return group_wait();
+    };
+    if (!n_mine && !group_sync()) // the last item's sums have been read
+        return false;
+    if (lane < R)
+        sm.red[t][wq][lane] = l[0];
+    if (!group_sync())
+        return false;
+    // a row's sum per lane, so that the reciprocals and logarithms are taken at once
+    const volatile float *red = sm.red[t][0] + (lane & (R - 1));
+    const float sum = red[0] + red[kFewRows] + red[2 * kFewRows] + red[3 * kFewRows];
+    const float inv = sum == 0.f ? 0.f : ptx::rcp_approx(sum);
+#pragma unroll
+    for (int n = 0; n < R; ++n) {
+        const float norm = __shfl_sync(0xffffffffu, inv, n);
+        if (n >= rows || (D == 64 && (n & 1) != r >> 6))
+            continue;
+        const int s = fast_div(n, p.div_g);
+        const int64_t tok = inf.t0 + s, head = (inf.kvh + t) * p.G + n - s * p.G;
+        p.out[tok * p.o_st + head * p.o_sh + dim] = __float2bfloat16(o[n] * norm);
+    }
+    if (r < rows) {
+        float top = ref[0];
+#pragma unroll
+        for (int n = 1; n < R; ++n)
+            top = r == n ? ref[n] : top;
+        const int s = fast_div(r, p.div_g);
+        join_lse(p, inf.t0 + s, (inf.kvh + t) * p.G + r - s * p.G, top, sum);
+    }
+    return true;
+}
+
+template <int MOD, int D>
+__device__ void few_softmax_fp8(const FewCtx<D, true> &cx, const ChunkParams &p, int t)
+{
+    FewSmem<D, true> &sm = *cx.sm;
+    FewState8 ct{0u, 0u, 0u, 0u};
+    for (uint32_t item = 0;; ++item) {
+        if (!warp_wait(bar(sm.info_full[item % kInfo]), (item / kInfo) & 1, cx.wc, W_INFO_FULL))
+            return;
+        const FewItem &inf = sm.info[item % kInfo];
+        if (inf.stop)
+            return;
+        // an odd head's item has no second slot; half the rows, half the work
+        if (t < inf.heads && !(inf.rows <= 4   ? few_item_fp8<MOD, D, 4>(cx, p, inf, t, ct)
+                               : inf.rows <= 8 ? few_item_fp8<MOD, D, 8>(cx, p, inf, t, ct)
+                                               : few_item_fp8<MOD, D, 16>(cx, p, inf, t, ct)))
             return;
         ct.loaded += inf.u_hi - inf.u_lo;
         __syncwarp();
@@ -1042,19 +1347,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int s = 0; s < C::kStages; ++s) {
             ptx::mbar_init(bar(sm->k_full[s]), F8 ? 1 + kScaleArrivals : 1);
-            ptx::mbar_init(bar(sm->k_empty[s]), 1);
+            ptx::mbar_init(bar(sm->k_empty[s]), F8 ? 3 : 1); // S's; in 8 bits those of the warps that issue O^T, too
             ptx::mbar_init(bar(sm->v_full[s]), 1);
-            ptx::mbar_init(bar(sm->v_empty[s]), few_split_loads(p) ? 1 : 2); // the warps that issue O^T
+            ptx::mbar_init(bar(sm->v_empty[s]), few_split_loads<F8>(p) ? 1 : 2); // the warps that issue O^T
         }
         for (int t = 0; t < 2; ++t) {
             ptx::mbar_init(bar(sm->s_full[t]), 1);
             ptx::mbar_init(bar(sm->s_free[t]), 128);
-            ptx::mbar_init(bar(sm->p_full[t]), 128);
-            ptx::mbar_init(bar(sm->pv_done[t]), 1);
+            for (int b = 0; b < C::kPBufs; ++b) {
+                ptx::mbar_init(bar(sm->p_full[t][b]), 128);
+                ptx::mbar_init(bar(sm->pv_done[t][b]), 1);
+            }
             ptx::mbar_init(bar(sm->group[t]), 128);
         }
         for (int b = 0; b < 3; ++b)
             ptx::mbar_init(bar(sm->final_bar[b]), 1);
+        for (int b = 0; b < 8; ++b)
+            sm->large[b >> 2][b & 3] = 0;
         sm->abort_flag = 0;
         ptx::fence_mbarrier_init();
         ptx::fence_proxy_async_smem();
@@ -1072,7 +1381,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     cx.wc = wait_ctl(p, &sm->abort_flag);
     if (warp >= 4) {
         tell_second(p, cx.part);
-        few_softmax<MOD, D, F8>(cx, p, (warp >> 2) - 1);
+        if constexpr (F8)
+            few_softmax_fp8<MOD, D>(cx, p, (warp >> 2) - 1);
+        else
+            few_softmax<MOD, D>(cx, p, (warp >> 2) - 1);
         ptx::tc_fence_before();
         ptx::named_barrier_sync(1, kThreads);
     } else {
@@ -1080,11 +1392,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             few_producer(cx, p, &maps.few_q, &maps.few_k, &maps.few_v);
         else if (warp == 1)
             few_s_role(cx);
-        else if (!few_split_loads(p))
+        else if (!few_split_loads<F8>(p))
             few_pv_role(cx, warp - 2, warp - 2);
         else if (warp == 2)
             few_pv_role(cx, 0, 1);
-        else
+        else if constexpr (!F8)
             few_v_producer(cx, p, &maps.few_v);
         ptx::tc_fence_before();
         ptx::named_barrier_sync(1, kThreads);

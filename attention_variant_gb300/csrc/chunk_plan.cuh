@@ -280,7 +280,7 @@ struct PlanShared {
 };
 
 // The lists of entries, by `threads` threads.
-template <int D>
+template <int D, bool F8>
 __device__ __forceinline__ void plan_entries(const ChunkParams &p, PlanShared &sm, int threads)
 {
     const int tid = threadIdx.x;
@@ -338,7 +338,7 @@ __device__ __forceinline__ void plan_entries(const ChunkParams &p, PlanShared &s
                 key_range(p, en.L, en.pos0, en.pos0 + en.n_tok - 1, k0, k1);
                 en.key_lo = k0;
                 kind = is_few(p, en.n_tok) ? 1 : 0;
-                const int tile = kind ? kFewTile : chunk_key_tile(D);
+                const int tile = kind ? few_tile(D, F8) : chunk_key_tile(D);
                 en.lo = k0 / tile;
                 en.n_tiles = max(1, (max(k1, 0) + tile - 1) / tile - en.lo);
                 en.tile_cost = kind ? p.cost_few : en.n_tok > p.TQ ? p.cost_pair : p.cost_single;
@@ -400,7 +400,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
         }
     }
     if (static_cast<int>(threadIdx.x) < threads)
-        plan_entries<D>(p, sm, threads);
+        plan_entries<D, F8>(p, sm, threads);
     __syncthreads();
     // parts of each list by its share of the cost, in pairs (see part_of); a part is
     // at least one tile long, so that every part between the first and the last

@@ -16,9 +16,9 @@ namespace {
 // ahead of the softmax (S of a tile waits for what its slot's last one was read for).
 constexpr int kScaleRing = 32;
 struct ScaleRing {
-    float k[kScaleRing][8], v[kScaleRing][8];
+    float k[kScaleRing][16], v[kScaleRing][16];
 };
-constexpr int kScaleArrivals = 16; // on the tile's barrier: one per lane that copies
+constexpr int kScaleArrivals = 32; // on the tile's barrier: one per lane
 
 // Copies the scales of the BOXES boxes from key0 on of request b; `page` is that of this
 // lane's box of 2^page_box keys.  Boxes that no row sees and pages outside the cache get
@@ -27,11 +27,9 @@ template <int BOXES>
 __device__ __forceinline__ void copy_scales(const ChunkParams &p, ScaleRing &ring, uint32_t idx, uint32_t bar, int page,
                                             int page_box, int key0, int key_lo, int L, int kvh)
 {
-    const int lane = static_cast<int>(ptx::lane_id()), g = lane & 7, key = key0 + g * 16;
+    const int lane = static_cast<int>(ptx::lane_id()), g = lane & 15, key = key0 + g * 16;
     const int pg = __shfl_sync(0xffffffffu, page, g * 16 >> page_box);
-    if (lane >= kScaleArrivals)
-        return;
-    const bool v = lane >= 8;
+    const bool v = lane >= 16;
     const int at = p.page_shift < 0 ? key : key & ((1 << p.page_shift) - 1);
     const bool read = g < BOXES && key < L && key >= (key_lo & ~15) &&
                       static_cast<uint32_t>(pg) < static_cast<uint32_t>(p.n_pages);
@@ -39,7 +37,8 @@ __device__ __forceinline__ void copy_scales(const ChunkParams &p, ScaleRing &rin
     if (read)
         from += pg * (v ? p.vs_p : p.ks_p) + static_cast<int64_t>(at >> p.scale_shift) * (v ? p.vs_b : p.ks_b) + kvh;
     const uint32_t i = idx % kScaleRing;
-    ptx::copy_word(ptx::smem_u32(v ? &ring.v[i][g] : &ring.k[i][g]), from, read);
+    if (g < BOXES)
+        ptx::copy_word(ptx::smem_u32(v ? &ring.v[i][g] : &ring.k[i][g]), from, read);
     ptx::copies_arrive(bar);
 }
 

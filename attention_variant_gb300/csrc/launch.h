@@ -313,7 +313,7 @@ constexpr int kChunkMaxCtas = 160; // persistent CTAs the workspace has room for
 // Keys per K/V tile (the standard kernel's, for the same TMEM budget), and of
 // the few-row path.
 __host__ __device__ constexpr int chunk_key_tile(int D) { return D == 128 ? 64 : 112; }
-constexpr int kFewTile = 128;
+__host__ __device__ constexpr int few_tile(int D, bool f8) { return f8 && D == 64 ? 256 : 128; }
 constexpr int kFewRows = 16; // query rows of a request and KV head, at most
 
 // One or two row blocks of a request, as the planning kernel lists them.
