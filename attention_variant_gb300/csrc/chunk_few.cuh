@@ -42,7 +42,8 @@
 //   warp  0     walks the CTA's items, publishes them, loads Q, K and V by TMA
 //   warp  1     issues S^T of both slots
 //   warps 2, 3  issue O^T of slot 0, slot 1, after zeroing V rows that no row sees
-//               (or warp 2 both, and warp 3 loads V: few_split_loads)
+//               (or warp 2 both, and warp 3 loads V: few_split_loads; in 8 bits
+//               warp 3 walks the items)
 //   warps 4-11  the slots' softmax warpgroups
 #pragma once
 
@@ -233,39 +234,79 @@ __device__ __forceinline__ int few_page(const ChunkParams &p, const FewItem &it,
 template <bool F8>
 __device__ __forceinline__ bool few_split_loads(const ChunkParams &p) { return !F8 && p.few_shift < 5; }
 
-// Walks the CTA's items, publishes them, loads Q, K and, mostly, V.
+// The next item of the CTA's part from tile k of item h of entry e on (it.stop: none); en, its entry.
 template <int D, bool F8>
-__device__ void few_producer(const FewCtx<D, F8> &cx, const ChunkParams &p, const CUtensorMap *tm_q,
+__device__ __forceinline__ void few_next(const ChunkParams &p, const ChunkPart &me, int cta, int &e, int &h, int &k,
+                                         FewItem &it, ChunkEntry &en)
+{
+    constexpr int kBN = FewCfg<D, F8>::kBN;
+    const ChunkEntry *entries = p.entries + p.max_entries;
+    int k_end = 0;
+    while (e < me.n_entries) {
+        en = e == me.entry ? me.at : load_plan(entries + e);
+        const int full = item_heads(p, en), heads = min(full, p.Hk - h * full), n_tiles = en.n_tiles * heads;
+        const int64_t x0 = en.cum + h * item_cost(p, en);
+        if (x0 + static_cast<int64_t>(k) * en.tile_cost >= me.end) {
+            e = me.n_entries; // the cut falls before this tile
+            break;
+        }
+        if (k < n_tiles) {
+            const PartRange r = part_range(x0, n_tiles, en.tile_cost, k, me.end, me.total, cta, me.parts);
+            k_end = r.k_end;
+            it.n_parts = r.n_parts;
+            it.mine = r.first == cta ? 1 : 0;
+            it.heads = heads;
+            it.kvh = h * full;
+            it.stop = 0;
+            break;
+        }
+        k = 0; // the cut fell into the item's closing cost
+        if (++h * full >= p.Hk) {
+            h = 0;
+            ++e;
+        }
+    }
+    if (!it.stop) {
+        it.shift = it.heads - 1;
+        it.cta = me.cta;
+        it.u_lo = (en.lo << it.shift) + k;
+        it.u_hi = (en.lo << it.shift) + k_end;
+        it.b = en.b;
+        it.t0 = en.t0;
+        it.rows = en.n_tok * p.G;
+        it.pos0 = en.pos0;
+        it.L = en.L;
+        it.key_lo = en.key_lo;
+        int k0, k1;
+        key_range(p, en.L, en.pos0, en.pos0 + en.n_tok - 1, k0, k1);
+        it.lo = k0 / kBN;
+        it.hi = (max(k1, 0) + kBN - 1) / kBN;
+    }
+}
+
+// Walks the CTA's items, publishes them, loads Q, K and, mostly, V.
+template <int D>
+__device__ void few_producer(const FewCtx<D, false> &cx, const ChunkParams &p, const CUtensorMap *tm_q,
                              const CUtensorMap *tm_k, const CUtensorMap *tm_v)
 {
-    using C = FewCfg<D, F8>;
-    constexpr int kBN = C::kBN;
-    FewSmem<D, F8> &sm = *cx.sm;
+    using C = FewCfg<D, false>;
+    FewSmem<D, false> &sm = *cx.sm;
     const uint32_t lane = ptx::lane_id();
-    std::conditional_t<F8, char, FewRing<D>> keys, values;
-    uint32_t kv_count = 0;
-    if constexpr (!F8) {
-        keys = {tm_k, sm.k, sm.k_full, sm.k_empty, 0u};
-        values = {tm_v, sm.v, sm.v_full, sm.v_empty, 0u};
-    }
-    const bool split = few_split_loads<F8>(p);
+    FewRing<D> keys{tm_k, sm.k, sm.k_full, sm.k_empty, 0u}, values{tm_v, sm.v, sm.v_full, sm.v_empty, 0u};
+    const bool split = few_split_loads<false>(p);
     uint32_t item_count = 0;
     bool ok = true;
     ChunkPart me{};
-    const ChunkEntry *entries = p.entries + p.max_entries;
     const int cta = cx.part;
     int e = 0, h = 0, k = 0; // entry, item of it, tile of that
     bool warm = p.warm;
     if (!warm)
         read_part(p, 1, cta, me, e, h, k);
-    if (F8)
-        ptx::fence_proxy_async_all(); // Q's terms, which the planning kernel has written
     for (;;) {
         // ---- the next part
         FewItem it{};
         it.stop = 1;
         ChunkEntry en{};
-        int k_end = 0;
         // the warm-up, beside the planning kernel: a tile of no keys for each slot, of
         // which nothing is written, so that the roles' instructions are there before
         // the loads begin (behind those of a full GPU they took 12 us)
@@ -277,46 +318,8 @@ __device__ void few_producer(const FewCtx<D, F8> &cx, const ChunkParams &p, cons
             it.u_hi = it.heads;
             it.rows = min(p.G, kFewRows);
         }
-        while (e < me.n_entries) {
-            en = e == me.entry ? me.at : load_plan(entries + e);
-            const int full = item_heads(p, en), heads = min(full, p.Hk - h * full), n_tiles = en.n_tiles * heads;
-            const int64_t x0 = en.cum + h * item_cost(p, en);
-            if (x0 + static_cast<int64_t>(k) * en.tile_cost >= me.end) {
-                e = me.n_entries; // the cut falls before this tile
-                break;
-            }
-            if (k < n_tiles) {
-                const PartRange r = part_range(x0, n_tiles, en.tile_cost, k, me.end, me.total, cta, me.parts);
-                k_end = r.k_end;
-                it.n_parts = r.n_parts;
-                it.mine = r.first == cta ? 1 : 0;
-                it.heads = heads;
-                it.kvh = h * full;
-                it.stop = 0;
-                break;
-            }
-            k = 0; // the cut fell into the item's closing cost
-            if (++h * full >= p.Hk) {
-                h = 0;
-                ++e;
-            }
-        }
-        if (!it.stop && !warm) {
-            it.shift = it.heads - 1;
-            it.cta = me.cta;
-            it.u_lo = (en.lo << it.shift) + k;
-            it.u_hi = (en.lo << it.shift) + k_end;
-            it.b = en.b;
-            it.t0 = en.t0;
-            it.rows = en.n_tok * p.G;
-            it.pos0 = en.pos0;
-            it.L = en.L;
-            it.key_lo = en.key_lo;
-            int k0, k1;
-            key_range(p, en.L, en.pos0, en.pos0 + en.n_tok - 1, k0, k1);
-            it.lo = k0 / kBN;
-            it.hi = (max(k1, 0) + kBN - 1) / kBN;
-        }
+        if (!warm)
+            few_next<D, false>(p, me, cta, e, h, k, it, en);
         const uint32_t ring = item_count & 1, slot = item_count % kInfo;
         ok = warp_wait(bar(sm.info_empty[slot]), ((item_count / kInfo) & 1) ^ 1, cx.wc, W_INFO_EMPTY);
         if (!ok)
@@ -338,12 +341,12 @@ __device__ void few_producer(const FewCtx<D, F8> &cx, const ChunkParams &p, cons
         if (lane == 0) {
             const int slots = warm ? 0 : it.heads;
             ptx::mbar_arrive_expect_tx(bar(sm.q_full[ring]),
-                                       static_cast<uint32_t>(slots * C::kQParts * p.few_tq * p.G) * C::kRowBytes);
+                                       static_cast<uint32_t>(slots * C::kHalves * p.few_tq * p.G) * C::kRowBytes);
             for (int t = 0; t < slots; ++t)
 #pragma unroll
-                for (int i = 0; i < C::kQParts; ++i)
-                    ptx::tma_load_4d(ptx::smem_u32(sm.q[ring][t]) + i * C::kQPart, tm_q, bar(sm.q_full[ring]),
-                                     F8 ? 0 : i * 64, 0, it.kvh + t, it.t0 + (F8 ? i * p.T : 0));
+                for (int hf = 0; hf < C::kHalves; ++hf)
+                    ptx::tma_load_4d(ptx::smem_u32(sm.q[ring][t]) + hf * C::kQPart, tm_q, bar(sm.q_full[ring]),
+                                     hf * 64, 0, it.kvh + t, it.t0);
         }
         __syncwarp();
         ++item_count;
@@ -351,38 +354,25 @@ __device__ void few_producer(const FewCtx<D, F8> &cx, const ChunkParams &p, cons
         // not wait in shared memory for its weights (not past the item: the next
         // item's buffers may wait for the V of its last tile).  Pages are fetched
         // a tile ahead.
-        int page_next = few_page<D, F8>(p, it, it.u_lo >> it.shift);
-        if constexpr (F8) {
-            for (int v = it.u_lo; v < it.u_hi && ok; ++v, ++kv_count) {
-                const int page = page_next;
-                if (v + 1 < it.u_hi)
-                    page_next = few_page<D, F8>(p, it, (v + 1) >> it.shift);
-                ok = few_load_fp8(cx, p, tm_k, tm_v, it, v, kv_count, page);
-                if (!ok)
-                    break;
-            }
-        } else {
-            int page[C::kLag + 1]; // of the last kLag + 1 tiles, the latest first
-            for (int v = it.u_lo; v < it.u_hi + (split ? 0 : C::kLag) && ok; ++v) {
+        int page_next = few_page<D, false>(p, it, it.u_lo >> it.shift);
+        int page[C::kLag + 1]; // of the last kLag + 1 tiles, the latest first
+        for (int v = it.u_lo; v < it.u_hi + (split ? 0 : C::kLag) && ok; ++v) {
 #pragma unroll
-                for (int i = C::kLag; i > 0; --i)
-                    page[i] = page[i - 1];
-                page[0] = page_next;
-                if (v + 1 < it.u_hi)
-                    page_next = few_page<D, F8>(p, it, (v + 1) >> it.shift);
-                if (v < it.u_hi)
-                    ok = keys.load(cx, p, it, v, page[0]);
-                if (ok && !split && v - C::kLag >= it.u_lo)
-                    ok = values.load(cx, p, it, v - C::kLag, page[C::kLag]);
-            }
+            for (int i = C::kLag; i > 0; --i)
+                page[i] = page[i - 1];
+            page[0] = page_next;
+            if (v + 1 < it.u_hi)
+                page_next = few_page<D, false>(p, it, (v + 1) >> it.shift);
+            if (v < it.u_hi)
+                ok = keys.load(cx, p, it, v, page[0]);
+            if (ok && !split && v - C::kLag >= it.u_lo)
+                ok = values.load(cx, p, it, v - C::kLag, page[C::kLag]);
         }
         if (!ok)
             break;
         if (warm) {
             warm = false;
             read_part(p, 1, cta, me, e, h, k);
-            if (F8)
-                ptx::fence_proxy_async_all();
             continue;
         }
         // ---- on to the next item
@@ -393,15 +383,118 @@ __device__ void few_producer(const FewCtx<D, F8> &cx, const ChunkParams &p, cons
         }
     }
     if (!ok) {
-        if constexpr (F8) {
-            for (uint32_t idx = kv_count > C::kStages ? kv_count - C::kStages : 0; idx < kv_count; ++idx)
-                mbar_wait_drain(bar(sm.k_full[idx % C::kStages]), (idx / C::kStages) & 1, cx.wc, W_DRAIN);
-        } else {
-            keys.drain(cx);
-            values.drain(cx);
-        }
+        keys.drain(cx);
+        values.drain(cx);
         for (uint32_t n = item_count > 2 ? item_count - 2 : 0; n < item_count; ++n)
             mbar_wait_drain(bar(sm.q_full[n & 1]), (n >> 1) & 1, cx.wc, W_DRAIN);
+    }
+}
+
+// A cache in 8 bits: warp 3 walks the items and publishes them, as far ahead as there is
+// room (an item takes it a few microseconds of divisions and loads, which short items'
+// loads do not hide), and warp 0 loads them.
+template <int D>
+__device__ void few_walker_fp8(const FewCtx<D, true> &cx, const ChunkParams &p)
+{
+    FewSmem<D, true> &sm = *cx.sm;
+    ChunkPart me{};
+    int e = 0, h = 0, k = 0; // entry, item of it, tile of that
+    bool warm = p.warm; // see few_producer
+    if (!warm)
+        read_part(p, 1, cx.part, me, e, h, k);
+    for (uint32_t n = 0;; ++n) {
+        FewItem it{};
+        ChunkEntry en{};
+        if (warm) {
+            it.heads = min(p.Hk, 2);
+            it.shift = it.heads - 1;
+            it.hi = 1;
+            it.u_hi = it.heads;
+            it.rows = min(p.G, kFewRows);
+        } else {
+            it.stop = 1;
+            few_next<D, true>(p, me, cx.part, e, h, k, it, en);
+        }
+        const uint32_t slot = n % kInfo;
+        if (!warp_wait(bar(sm.info_empty[slot]), ((n / kInfo) & 1) ^ 1, cx.wc, W_INFO_EMPTY))
+            return;
+        if (ptx::lane_id() == 0) {
+            sm.info[slot] = it;
+            ptx::mbar_arrive(bar(sm.info_full[slot])); // release: the fields above first
+            if (!it.stop && it.mine && it.n_parts > 1)
+                p.joins[me.cta] = ChunkJoin{it.n_parts, JOIN_FEW, it.kvh, {it.t0, it.t0},
+                                                {it.rows, it.heads == 2 ? it.rows : 0}, 0};
+        }
+        __syncwarp();
+        if (it.stop)
+            return;
+        if (warm) {
+            warm = false;
+            read_part(p, 1, cx.part, me, e, h, k);
+            continue;
+        }
+        k = 0;
+        if (++h * item_heads(p, en) >= p.Hk) {
+            h = 0;
+            ++e;
+        }
+    }
+}
+
+template <int D>
+__device__ void few_loader_fp8(const FewCtx<D, true> &cx, const ChunkParams &p, const CUtensorMap *tm_q,
+                               const CUtensorMap *tm_k, const CUtensorMap *tm_v)
+{
+    using C = FewCfg<D, true>;
+    FewSmem<D, true> &sm = *cx.sm;
+    const uint32_t lane = ptx::lane_id();
+    uint32_t kv_count = 0, n = 0;
+    bool ok = true;
+    for (;; ++n) {
+        const uint32_t slot = n % kInfo, ring = n & 1;
+        ok = warp_wait(bar(sm.info_full[slot]), (n / kInfo) & 1, cx.wc, W_INFO_FULL);
+        if (!ok)
+            break;
+        const FewItem it = sm.info[slot];
+        __syncwarp();
+        if (lane == 0)
+            ptx::mbar_arrive(bar(sm.info_empty[slot]));
+        if (it.stop)
+            break;
+        int page_next = few_page<D, true>(p, it, it.u_lo >> it.shift);
+        ok = warp_wait(bar(sm.q_empty[ring]), ((n >> 1) & 1) ^ 1, cx.wc, W_Q_EMPTY);
+        if (!ok)
+            break;
+        if (lane == 0) {
+            const int slots = it.n_parts ? it.heads : 0; // none for the warm-up
+            ptx::fence_proxy_async_all(); // Q's terms, which the planning kernel has written
+            ptx::mbar_arrive_expect_tx(bar(sm.q_full[ring]),
+                                       static_cast<uint32_t>(slots * C::kQParts * p.few_tq * p.G) * C::kRowBytes);
+            for (int t = 0; t < slots; ++t)
+#pragma unroll
+                for (int i = 0; i < C::kQParts; ++i)
+                    ptx::tma_load_4d(ptx::smem_u32(sm.q[ring][t]) + i * C::kQPart, tm_q, bar(sm.q_full[ring]), 0, 0,
+                                     it.kvh + t, it.t0 + i * p.T);
+        }
+        __syncwarp();
+        for (int v = it.u_lo; v < it.u_hi; ++v, ++kv_count) {
+            const int page = page_next;
+            if (v + 1 < it.u_hi)
+                page_next = few_page<D, true>(p, it, (v + 1) >> it.shift);
+            ok = few_load_fp8(cx, p, tm_k, tm_v, it, v, kv_count, page);
+            if (!ok)
+                break;
+        }
+        if (!ok) {
+            ++n;
+            break;
+        }
+    }
+    if (!ok) { // wait (bounded, ignoring the abort) for the loads in flight
+        for (uint32_t idx = kv_count > C::kStages ? kv_count - C::kStages : 0; idx < kv_count; ++idx)
+            mbar_wait_drain(bar(sm.k_full[idx % C::kStages]), (idx / C::kStages) & 1, cx.wc, W_DRAIN);
+        for (uint32_t i = n > 2 ? n - 2 : 0; i < n; ++i)
+            mbar_wait_drain(bar(sm.q_full[i & 1]), (i >> 1) & 1, cx.wc, W_DRAIN);
     }
 }
 
@@ -1347,7 +1440,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int s = 0; s < C::kStages; ++s) {
             ptx::mbar_init(bar(sm->k_full[s]), F8 ? 1 + kScaleArrivals : 1);
-            ptx::mbar_init(bar(sm->k_empty[s]), F8 ? 3 : 1); // S's; in 8 bits those of the warps that issue O^T, too
+            ptx::mbar_init(bar(sm->k_empty[s]), F8 ? 2 : 1); // S's; in 8 bits O^T's, too
             ptx::mbar_init(bar(sm->v_full[s]), 1);
             ptx::mbar_init(bar(sm->v_empty[s]), few_split_loads<F8>(p) ? 1 : 2); // the warps that issue O^T
         }
@@ -1388,15 +1481,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::tc_fence_before();
         ptx::named_barrier_sync(1, kThreads);
     } else {
-        if (warp == 0)
-            few_producer(cx, p, &maps.few_q, &maps.few_k, &maps.few_v);
-        else if (warp == 1)
+        if (warp == 0) {
+            if constexpr (F8)
+                few_loader_fp8(cx, p, &maps.few_q, &maps.few_k, &maps.few_v);
+            else
+                few_producer(cx, p, &maps.few_q, &maps.few_k, &maps.few_v);
+        } else if (warp == 1)
             few_s_role(cx);
-        else if (!few_split_loads<F8>(p))
+        else if (!F8 && !few_split_loads<F8>(p))
             few_pv_role(cx, warp - 2, warp - 2);
         else if (warp == 2)
             few_pv_role(cx, 0, 1);
-        else if constexpr (!F8)
+        else if constexpr (F8)
+            few_walker_fp8(cx, p);
+        else
             few_v_producer(cx, p, &maps.few_v);
         ptx::tc_fence_before();
         ptx::named_barrier_sync(1, kThreads);
