@@ -505,11 +505,6 @@ __device__ void pv_role(const KernelCtx<D, F8> &cx, int t)
         }
         for (int j = u_lo; j < u_hi; ++j, ++idx) {
             const uint32_t stage = idx % kStages;
-            if (F8 && j + 1 < u_hi) { // a tile ahead, while the softmax works on this one
-                ok = convert(j + 1, idx + 1);
-                if (!ok)
-                    break;
-            }
             if (!uses(j, first, hi, step)) {
                 // tile not used by this slot: release it once it has landed
                 ok = warp_wait(bar(full[stage]), (idx / kStages) & 1, cx.wc, W_KV_FULL);
@@ -518,6 +513,11 @@ __device__ void pv_role(const KernelCtx<D, F8> &cx, int t)
                 if (lane == 0)
                     ptx::mbar_arrive(bar(empty[stage]));
                 __syncwarp();
+                if (F8 && j + 1 < u_hi) {
+                    ok = convert(j + 1, idx + 1);
+                    if (!ok)
+                        break;
+                }
                 continue;
             }
             ok = warp_wait(bar(sm.p_full[t]), pcount & 1, cx.wc, W_P_FULL);
@@ -544,6 +544,11 @@ __device__ void pv_role(const KernelCtx<D, F8> &cx, int t)
                 ptx::mma_commit(bar(empty[stage]));
             }
             __syncwarp();
+            if (F8 && j + 1 < u_hi) {
+                ok = convert(j + 1, idx + 1);
+                if (!ok)
+                    break;
+            }
         }
     }
     const uint32_t b_final = bar(sm.final_bar[1 + t]);
@@ -1083,9 +1088,10 @@ cudaError_t launch_mod(const ChunkMaps &maps, ChunkParams &p, cudaStream_t strea
     while (threads < kPlanThreads && (threads < p.batch || threads < p.max_entries))
         threads *= 2;
     const int block = std::min(std::max(threads, (2 * p.n_cta + 31) & ~31), kPlanThreads);
-    // in 8 bits q is split beside it, a few rows to a thread where there are many
-    const int64_t split = F8 ? (static_cast<int64_t>(p.T) * p.Hq * (D / 8) + block - 1) / block : 0;
-    chunk_plan_kernel<D, F8><<<1 + static_cast<int>(std::min<int64_t>(split, p.n_cta - 1)), block, 0, stream>>>(p, threads);
+    // in 8 bits q is split beside it
+    const int64_t rows = static_cast<int64_t>(p.T) * p.Hq, per_block = block / (D / 8) * kSplitRows;
+    const int split = F8 ? static_cast<int>(std::min<int64_t>((rows + per_block - 1) / per_block, 4 * p.n_cta)) : 0;
+    chunk_plan_kernel<D, F8><<<1 + split, block, 0, stream>>>(p, threads);
     e = cudaGetLastError();
     // groups of more than kFewRows heads have row blocks alone, and no more
     // tokens than few rows hold make no row block.  Where both may have work the

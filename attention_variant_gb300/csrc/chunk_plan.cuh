@@ -198,6 +198,7 @@ __device__ __forceinline__ float *partial(const ChunkParams &p, int cta, int buf
 
 // ------------------------------------------------------------------ planning
 
+constexpr int kSplitRows = 4;
 template <int D>
 __device__ __forceinline__ void split_q(const ChunkParams &p); // fp8.cuh
 

@@ -32,6 +32,13 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t c)
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(c)));
     return h;
 }
+__device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t c, uint32_t &lo, uint32_t &hi)
+{
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(c));
+}
 __device__ __forceinline__ float2 from_e4m3x2(uint32_t c)
 {
     const uint32_t h = e4m3x2_to_f16x2(c);

@@ -57,19 +57,21 @@ __device__ __forceinline__ void convert_half(const uint8_t *raw, uint8_t *dst, i
 #pragma unroll
     for (int i = 0; i < kSteps; ++i)
         w[i] = *reinterpret_cast<const uint4 *>(raw + (key0 + i * kStepKeys) * D + u * 16);
+    if (dead_lo > 0 || dead_hi < KEYS) {
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i)
+            if (key0 + i * kStepKeys < dead_lo || key0 + i * kStepKeys >= dead_hi)
+                w[i] = make_uint4(0, 0, 0, 0);
+    }
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
         const int key = key0 + i * kStepKeys;
-        if (key < dead_lo || key >= dead_hi)
-            w[i] = make_uint4(0, 0, 0, 0);
         uint4 out[2];
         const uint32_t in[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
         uint32_t *o = reinterpret_cast<uint32_t *>(out);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            o[2 * c] = e4m3x2_to_f16x2(in[c] & 0xffffu);
-            o[2 * c + 1] = e4m3x2_to_f16x2(in[c] >> 16);
-        }
+        for (int c = 0; c < 4; ++c)
+            e4m3x4_to_f16x4(in[c], o[2 * c], o[2 * c + 1]);
         uint4 *row = reinterpret_cast<uint4 *>(dst + (u >> 2) * (KEYS * 128) + key * 128);
         const int at = (u & 3) * 2;
         row[at ^ (key & 7)] = out[0];
@@ -179,53 +181,57 @@ __device__ __forceinline__ float softmax_compute_p_scaled(float (&x)[N], const f
 template <int D>
 __device__ __forceinline__ void split_q(const ChunkParams &p)
 {
-    constexpr int kLanes = D / 8; // of a row, 8 elements each
+    constexpr int kLanes = D / 8, kRows = kSplitRows; // lanes of a row, 8 elements each; rows a thread has in flight
     const int per = blockDim.x / kLanes, y = threadIdx.x / kLanes, u = threadIdx.x % kLanes;
     const int64_t rows = static_cast<int64_t>(p.T) * p.Hq;
-    for (int64_t r0 = static_cast<int64_t>(blockIdx.x - 1) * per; r0 < rows; r0 += static_cast<int64_t>(gridDim.x - 1) * per) {
-        const int64_t r = r0 + y, tok = r / p.Hq;
-        float x[8];
-        if (r < rows) {
-            const uint4 w = __ldg(reinterpret_cast<const uint4 *>(p.q + tok * p.q_st + (r - tok * p.Hq) * p.q_sh + u * 8));
-            const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+    for (int64_t r0 = static_cast<int64_t>(blockIdx.x - 1) * per * kRows; r0 < rows;
+         r0 += static_cast<int64_t>(gridDim.x - 1) * per * kRows) {
+        uint4 in[kRows];
+#pragma unroll
+        for (int k = 0; k < kRows; ++k) {
+            const int64_t r = r0 + k * per + y;
+            in[k] = make_uint4(0, 0, 0, 0);
+            if (r < rows) {
+                const int64_t tok = rows >> 32 ? r / p.Hq : static_cast<uint32_t>(r) / static_cast<uint32_t>(p.Hq);
+                in[k] = __ldg(reinterpret_cast<const uint4 *>(p.q + tok * p.q_st + (r - tok * p.Hq) * p.q_sh + u * 8));
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kRows; ++k) {
+            const int64_t r = r0 + k * per + y;
+            const uint32_t w[4] = {in[k].x, in[k].y, in[k].z, in[k].w};
+            float x[8], m = 0.f;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                x[2 * i] = __uint_as_float(in[i] << 16);
-                x[2 * i + 1] = __uint_as_float(in[i] & 0xffff0000u);
+                x[2 * i] = __uint_as_float(w[i] << 16);
+                x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+                m = fmaxf(m, fmaxf(fabsf(x[2 * i]), fabsf(x[2 * i + 1])));
             }
-        } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                x[i] = 0.f;
+            for (int d = kLanes / 2; d; d >>= 1)
+                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+            if (r >= rows)
+                continue;
+            const uint32_t s = m < -kNegInf ? scale_bits(__float_as_uint(m)) : 0x3f800000u;
+            const float inv = __uint_as_float((254u << 23) - s); // 1 / s, s a power of two
+            uint32_t a[2] = {0, 0}, b[2] = {0, 0};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float lo = x[2 * i] * inv, hi = x[2 * i + 1] * inv;
+                const uint32_t t = to_e4m3x2(lo, hi);
+                const float2 v = from_e4m3x2(t);
+                // an infinity saturates: its second term makes the sum NaN
+                const float l2 = fabsf(lo) < -kNegInf ? lo - v.x : __uint_as_float(0x7fffffffu);
+                const float h2 = fabsf(hi) < -kNegInf ? hi - v.y : __uint_as_float(0x7fffffffu);
+                a[i >> 1] |= t << (16 * (i & 1));
+                b[i >> 1] |= to_e4m3x2(l2, h2) << (16 * (i & 1));
+            }
+            uint8_t *dst = p.q8 + r * D + u * 8;
+            *reinterpret_cast<uint2 *>(dst) = make_uint2(a[0], a[1]);
+            *reinterpret_cast<uint2 *>(dst + rows * D) = make_uint2(b[0], b[1]);
+            if (u == 0)
+                p.q_scale[r] = __uint_as_float(s);
         }
-        float m = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            m = fmaxf(m, fabsf(x[i]));
-#pragma unroll
-        for (int d = kLanes / 2; d; d >>= 1)
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-        if (r >= rows)
-            continue;
-        const uint32_t s = m < -kNegInf ? scale_bits(__float_as_uint(m)) : 0x3f800000u;
-        const float inv = __uint_as_float((254u << 23) - s); // 1 / s, s a power of two
-        uint32_t a[2] = {0, 0}, b[2] = {0, 0};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float lo = x[2 * i] * inv, hi = x[2 * i + 1] * inv;
-            // an infinity saturates; its difference from that makes the second term's sum NaN
-            const uint32_t t = to_e4m3x2(lo, hi);
-            const float2 v = from_e4m3x2(t);
-            const float l2 = fabsf(lo) < -kNegInf ? lo - v.x : __uint_as_float(0x7fffffffu);
-            const float h2 = fabsf(hi) < -kNegInf ? hi - v.y : __uint_as_float(0x7fffffffu);
-            a[i >> 1] |= t << (16 * (i & 1));
-            b[i >> 1] |= to_e4m3x2(l2, h2) << (16 * (i & 1));
-        }
-        uint8_t *dst = p.q8 + r * D + u * 8;
-        *reinterpret_cast<uint2 *>(dst) = make_uint2(a[0], a[1]);
-        *reinterpret_cast<uint2 *>(dst + rows * D) = make_uint2(b[0], b[1]);
-        if (u == 0)
-            p.q_scale[r] = __uint_as_float(s);
     }
     ptx::fence_proxy_async_all(); // TMA reads it
 }
