@@ -2370,7 +2370,7 @@ fl_status fl_kv_read_fp8(const fl_tensor *k_cache, const fl_tensor *v_cache, con
     f.page_rows = c.K.size[1];
     f.block_shift = c.block_shift;
     const int per = dtype == FL_F32 ? 4 : 8; // elements of 16 bytes
-    f.div_units = fl::make_fastdiv(int32_t(Hk * D / per));
+    f.units = int(Hk * D / per);
     while ((int64_t(per) << f.head_shift) < D)
         ++f.head_shift;
     const cudaError_t e = fl::launch_read_fp8(f, dtype == FL_F32, info.sm_count, reinterpret_cast<cudaStream_t>(stream));

@@ -276,8 +276,9 @@ struct Fp8AppendParams {
     Fp8Stream k, v;
     int heads, lane_shift;     // KV heads; log2 of a row's 16-element pieces
     int block_shift;           // log2 of the keys per scale
-    FastDiv div_group;         // heads of a group, groups, tokens per chunk of a
-    int groups, chunk, tile;   // run and per thread block (set by launch_append_fp8)
+    FastDiv div_group;         // heads of a group; groups, tokens per chunk of a
+    int groups, chunk, tile;   // run and window, rows of the grid for q (set by
+    int q_rows;                // launch_append_fp8)
 };
 struct Fp8ReadStream {
     const uint8_t *cache;
@@ -293,9 +294,9 @@ struct Fp8ReadParams {
     const int64_t *slots;
     int64_t n_slots, page_rows;
     int block_shift;
-    FastDiv div_units;         // 16-byte units of a token's output
-    int head_shift;            // log2 of those of a head
-    int tile;                  // tokens per thread block (set by launch_read_fp8)
+    int units, head_shift;     // 16-byte units of a token's output, log2 of those of a head
+    FastDiv div_units;         // units and tokens that a block walks at a time, its tokens
+    int uy, tile;              // (set by launch_read_fp8)
 };
 
 // ---- the book-keeping of a serving step (kv_plan.cu)
