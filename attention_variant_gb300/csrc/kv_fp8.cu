@@ -11,8 +11,9 @@
 // The tokens of a block that a call brings are neighbours (fl_kv_plan lists them
 // so): a run.  A thread block takes the runs that begin in its window of tokens, as many at a
 // time as fit, for a group of heads: each thread keeps its 16 elements of up to four
-// (token, head) rows in registers, rotated, from the maximum (over the lanes of a row, then in
-// shared memory) to the codes.  A run too long for that is read and rotated twice, the
+// (token, head) rows in registers from the maximum (over the lanes of a row, then in
+// shared memory) to the codes (as bf16, and rotates them twice: kept rotated, in fp32, they left two
+// blocks to a SM).  A run too long for that is read and rotated twice, the
 // second time out of L2.  Bound by HBM; for single tokens by the launch and one chain of
 // loads.
 #include <cuda_bf16.h>
@@ -34,6 +35,7 @@ struct RunShared {
     int64_t place[kRunRows];      // of each token of the chunk: its row in the cache, or -1
     int64_t block[kRunRows];      // of each run: its first row in the cache
     int64_t scale[kRunRows];      // and its scales
+    int32_t pos[kRunRows];        // position of each token
     uint32_t size[kRunRows];      // of each run and head: the largest |x|, as bits
     uint32_t old[kRunRows];       // and the scale before
     uint8_t run[kRunRows], fresh[kRunRows]; // run of each token; the run has its block's first row
@@ -81,97 +83,122 @@ __device__ __forceinline__ void append_runs(const Fp8AppendParams &f, const Fp8S
         scale = page * st.s_p + (in >> f.block_shift) * st.s_b + h0;
     };
     // a token of the chunk
-    auto place_token = [&](int i, int t, int run, int64_t row) {
+    auto place_token = [&](int i, int t, int run, int64_t row, bool position) {
         const int in = static_cast<int>(__ldg(p.slots + t) & (sb - 1));
         sm.place[i] = row + in * st.d_r;
+        if (ROT && position)
+            sm.pos[i] = __ldg(p.positions + t);
         sm.run[i] = static_cast<uint8_t>(run);
         if (in == 0)
             sm.fresh[run] = 1;
     };
-    auto angles = [&](int c0, int n) {
+    // a thread meets one frequency where the pairs divide the threads; frequencies are
+    // constants, which the lanes of a warp fetch one after another
+    int turn_i = 0;
+    uint64_t turn = 0;
+    if constexpr (ROT) {
+        turn_i = tid - fast_div(tid, p.div_pairs) * pairs;
+        turn = p.turns[turn_i];
+    }
+    auto angles = [&](int n) {
         if constexpr (ROT) {
             for (int e = tid; e < n * pairs; e += kRopeThreads) {
                 const int tl = fast_div(e, p.div_pairs), i = e - tl * pairs;
-                float2 cs = turn_cos_sin(static_cast<uint64_t>(p.offset + __ldg(p.positions + c0 + tl)) * p.turns[i]);
+                if (i != turn_i) {
+                    turn_i = i;
+                    turn = p.turns[i];
+                }
+                float2 cs = turn_cos_sin(static_cast<uint64_t>(p.offset + sm.pos[tl]) * turn);
                 cs.x *= p.magnitude;
                 cs.y *= p.magnitude;
                 sm.cs[tl * pairs + angle_at<V>(i, rot_units)] = cs;
             }
         }
     };
-    float x[kRowsKept][16];
-    // this thread's elements of its rows, rotated; what is infinite is not a number
-    auto load = [&](int c0, int n, bool measure) {
+    uint32_t raw[kRowsKept][8]; // this thread's elements of its rows: per unit V of a, V of b
+    auto load = [&](int c0, int n) {
 #pragma unroll
         for (int i = 0; i < kRowsKept; ++i) {
             const int r = y + i * rp, tok = fast_div(r, f.div_group), h = r - tok * group;
-            const bool live = tok < n && sm.place[tok < n ? tok : 0] >= 0;
-            if (live) {
-                const __nv_bfloat16 *src = st.src + static_cast<int64_t>(c0 + tok) * st.s_s + (h0 + h) * st.s_h;
 #pragma unroll
-                for (int k = 0; k < kUnits; ++k) {
-                    int b_at;
-                    const int at = unit_at<V, INTER, ROT>(piece * kUnits + k, rot_units, rot, pairs, b_at);
-                    const auto a = *reinterpret_cast<const Vec<__nv_bfloat16, V> *>(src + at);
-                    const auto b = *reinterpret_cast<const Vec<__nv_bfloat16, V> *>(src + at + b_at);
-                    float *w = x[i] + k * 2 * V; // V elements of a, V of b
+            for (int e = 0; e < 8; ++e)
+                raw[i][e] = 0u;
+            if (tok >= n || sm.place[tok] < 0)
+                continue;
+            const __nv_bfloat16 *src = st.src + static_cast<int64_t>(c0 + tok) * st.s_s + (h0 + h) * st.s_h;
 #pragma unroll
-                    for (int e = 0; e < V; ++e) {
-                        w[e] = __bfloat162float(a.e[e]);
-                        w[V + e] = __bfloat162float(b.e[e]);
+            for (int k = 0; k < kUnits; ++k) {
+                int b_at;
+                const int at = unit_at<V, INTER, ROT>(piece * kUnits + k, rot_units, rot, pairs, b_at);
+                if constexpr (V == 1) {
+                    const uint16_t *w = reinterpret_cast<const uint16_t *>(src);
+                    raw[i][k] = w[at] | static_cast<uint32_t>(w[at + b_at]) << 16;
+                } else {
+                    using W = Vec<uint32_t, V / 2 == 0 ? 1 : V / 2>;
+                    const W a = *reinterpret_cast<const W *>(src + at), b = *reinterpret_cast<const W *>(src + at + b_at);
+#pragma unroll
+                    for (int e = 0; e < V / 2; ++e) {
+                        raw[i][k * V + e] = a.e[e];
+                        raw[i][k * V + V / 2 + e] = b.e[e];
                     }
                 }
-            } else {
-#pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    x[i][e] = 0.f;
             }
         }
+    };
+    // Row i's elements in fp32, rotated, and the largest size among them; what is
+    // infinite is not a number.
+    auto expand = [&](int i, int tok, float (&x)[16]) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            x[2 * e] = __uint_as_float(raw[i][e] << 16);
+            x[2 * e + 1] = __uint_as_float(raw[i][e] & 0xffff0000u);
+        }
+        if constexpr (ROT) {
+#pragma unroll
+            for (int k = 0; k < kUnits; ++k) {
+                const int u = piece * kUnits + k;
+                float *w = x + k * 2 * V;
+                if (u < rot_units) {
+                    const float2 *cs = sm.cs + tok * pairs + u * (V == 1 ? 1 : 2);
+#pragma unroll
+                    for (int e = 0; e < V; ++e) {
+                        const float2 c = V <= 2 ? cs[e] : cs[(e / 2) * rot_units * 2 + e % 2];
+                        float &ra = INTER ? w[2 * e] : w[e], &rb = INTER ? w[2 * e + 1] : w[V + e];
+                        const float xa = ra, xb = rb;
+                        ra = xa * c.x - xb * c.y;
+                        rb = xa * c.y + xb * c.x;
+                    }
+                }
+            }
+        }
+        float m = 0.f;
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+            m = fmaxf(m, fabsf(x[e]));
+        if (m == -kNegInf) {
+            m = 0.f;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                if (fabsf(x[e]) == -kNegInf)
+                    x[e] = __uint_as_float(0x7fffffffu);
+                else
+                    m = fmaxf(m, fabsf(x[e]));
+            }
+        }
+        return m;
+    };
+    auto measure = [&](int n) {
 #pragma unroll
         for (int i = 0; i < kRowsKept; ++i) {
             const int r = y + i * rp, tok = fast_div(r, f.div_group), h = r - tok * group;
             if (y - lane / lpr + i * rp >= n * group)
                 break; // no row of the warp's is in the chunk
-            const int t = tok < n ? tok : 0;
-            if constexpr (ROT) {
-#pragma unroll
-                for (int k = 0; k < kUnits; ++k) {
-                    const int u = piece * kUnits + k;
-                    float *w = x[i] + k * 2 * V;
-                    if (u < rot_units) {
-                        const float2 *cs = sm.cs + t * pairs + u * (V == 1 ? 1 : 2);
-#pragma unroll
-                        for (int e = 0; e < V; ++e) {
-                            const float2 c = V <= 2 ? cs[e] : cs[(e / 2) * rot_units * 2 + e % 2];
-                            float &ra = INTER ? w[2 * e] : w[e], &rb = INTER ? w[2 * e + 1] : w[V + e];
-                            const float xa = ra, xb = rb;
-                            ra = xa * c.x - xb * c.y;
-                            rb = xa * c.y + xb * c.x;
-                        }
-                    }
-                }
-            }
-            float m = 0.f;
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-                m = fmaxf(m, fabsf(x[i][e]));
-            if (m == -kNegInf) {
-                m = 0.f;
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    if (fabsf(x[i][e]) == -kNegInf)
-                        x[i][e] = __uint_as_float(0x7fffffffu);
-                    else
-                        m = fmaxf(m, fabsf(x[i][e]));
-                }
-            }
-            if (!measure)
-                continue;
-            uint32_t top = __float_as_uint(m);
+            float x[16];
+            uint32_t top = __float_as_uint(expand(i, tok < n ? tok : 0, x));
             for (int d = lpr / 2; d; d >>= 1)
                 top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
             if (tok < n && piece == 0 && top)
-                atomicMax(&sm.size[sm.run[t] * group + h], top);
+                atomicMax(&sm.size[sm.run[tok] * group + h], top);
         }
     };
     auto store = [&](int n) {
@@ -180,6 +207,8 @@ __device__ __forceinline__ void append_runs(const Fp8AppendParams &f, const Fp8S
             const int r = y + i * rp, tok = fast_div(r, f.div_group), h = r - tok * group;
             if (tok >= n || sm.place[tok] < 0)
                 continue;
+            float x[16];
+            expand(i, tok, x);
             const int at_run = sm.run[tok] * group + h;
             const float s = __uint_as_float(max(scale_bits(sm.size[at_run]), sm.old[at_run]));
             const float inv = 1.f / s;
@@ -188,7 +217,7 @@ __device__ __forceinline__ void append_runs(const Fp8AppendParams &f, const Fp8S
             for (int k = 0; k < kUnits; ++k) {
                 int b_at;
                 const int at = unit_at<V, INTER, ROT>(piece * kUnits + k, rot_units, rot, pairs, b_at);
-                const float *w = x[i] + k * 2 * V;
+                const float *w = x + k * 2 * V;
                 uint32_t c[V]; // two codes each
 #pragma unroll
                 for (int e = 0; e < V; ++e)
@@ -220,6 +249,8 @@ __device__ __forceinline__ void append_runs(const Fp8AppendParams &f, const Fp8S
         }
         const int t = s + tid;
         const int64_t mine = tid < f.chunk ? block_of(t) : -1;
+        if (ROT && tid < f.chunk)
+            sm.pos[tid] = t < p.tokens ? __ldg(p.positions + t) : 0;
         const bool leader = mine >= 0 && mine != block_of(t - 1);
         const uint32_t ballot = __ballot_sync(0xffffffffu, leader);
         if (lane == 0)
@@ -254,10 +285,11 @@ __device__ __forceinline__ void append_runs(const Fp8AppendParams &f, const Fp8S
         if (tid < n && mine >= 0 && run >= 0) {
             locate(mine, row, scale);
             if (leader) {
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(st.scale + scale));
                 sm.block[run] = row;
                 sm.scale[run] = scale;
             }
-            place_token(tid, t, run, row);
+            place_token(tid, t, run, row, false);
         }
         int runs = 0;
         {
@@ -265,7 +297,8 @@ __device__ __forceinline__ void append_runs(const Fp8AppendParams &f, const Fp8S
             __syncthreads();
             if (lane == 0)
                 sm.leaders[warp] = __popc(in);
-            angles(s, n);
+            load(s, n);
+            angles(n);
             __syncthreads();
 #pragma unroll
             for (int w = 0; w < kRopeThreads / 32; ++w)
@@ -279,7 +312,7 @@ __device__ __forceinline__ void append_runs(const Fp8AppendParams &f, const Fp8S
         }
         __syncthreads();
         // ---- the largest sizes of each run
-        load(s, n, true);
+        measure(n);
         int total = n;
         if (go_long) {
             const int64_t blk = block_of(s);
@@ -293,13 +326,14 @@ __device__ __forceinline__ void append_runs(const Fp8AppendParams &f, const Fp8S
                     if (block_of(s + total + tid) != blk)
                         atomicMin(&sm.end, tid);
                     else
-                        place_token(tid, s + total + tid, 0, block_row);
+                        place_token(tid, s + total + tid, 0, block_row, true);
                 }
                 __syncthreads();
                 more = sm.end;
-                angles(s + total, more);
+                load(s + total, more);
+                angles(more);
                 __syncthreads();
-                load(s + total, more, true);
+                measure(more);
             }
         }
         __syncthreads();
@@ -348,10 +382,11 @@ __device__ __forceinline__ void append_runs(const Fp8AppendParams &f, const Fp8S
                 __syncthreads();
                 more = min(f.chunk, total - done);
                 if (tid < more && block_of(s + done + tid) == blk)
-                    place_token(tid, s + done + tid, 0, block_row);
-                angles(s + done, more);
+                    place_token(tid, s + done + tid, 0, block_row, true);
                 __syncthreads();
-                load(s + done, more, false);
+                load(s + done, more);
+                angles(more);
+                __syncthreads();
                 store(more);
             }
         }
@@ -361,7 +396,7 @@ __device__ __forceinline__ void append_runs(const Fp8AppendParams &f, const Fp8S
 
 // Blocks of the first row rotate q, where it comes along; then K's groups of heads, then V's.
 template <int V, bool INTER, bool ROT>
-__global__ void __launch_bounds__(kRopeThreads, 2) append_fp8_kernel(const __grid_constant__ Fp8AppendParams f)
+__global__ void __launch_bounds__(kRopeThreads, 3) append_fp8_kernel(const __grid_constant__ Fp8AppendParams f)
 {
     __shared__ __align__(16) union {
         RunShared run;

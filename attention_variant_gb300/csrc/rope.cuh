@@ -125,16 +125,26 @@ __device__ __forceinline__ void rope_tile(const RopeParams &p, const RopeStream 
         s_src[tid] = b * st.s_b + s * st.s_s;
         s_dst[tid] = dst;
     }
-    if (st.rotate)
+    if (st.rotate) {
+        // frequencies are constants, which the lanes of a warp fetch one after another: a
+        // thread keeps its own, the same one throughout where the pairs divide the threads
+        // (append of 11,810 tokens of 16 + 2 + 2 heads of 128: 28.0 -> 24.5 us)
+        int turn_i = -1;
+        uint64_t turn = 0;
         for (int e = tid; e < n_tok * p.pairs; e += kRopeThreads) {
             const int tl = fast_div(e, p.div_pairs), i = e - tl * p.pairs;
             const int t = t0 + tl, b = fast_div(t, p.div_seq), s = t - b * p.div_seq.d;
             const int64_t pos = p.offset + (p.positions ? __ldg(p.positions + b * p.positions_stride + s) : s);
-            float2 cs = turn_cos_sin(static_cast<uint64_t>(pos) * p.turns[i]);
+            if (i != turn_i) {
+                turn_i = i;
+                turn = p.turns[i];
+            }
+            float2 cs = turn_cos_sin(static_cast<uint64_t>(pos) * turn);
             cs.x *= p.magnitude;
             cs.y *= p.backward ? -p.magnitude : p.magnitude;
             s_cs[tl * p.pairs + angle_at<V>(i, rot_units)] = cs;
         }
+    }
     __syncthreads();
 
     // unit ux of a head: the vectors a (at element `at`) and b (b_at further) of
