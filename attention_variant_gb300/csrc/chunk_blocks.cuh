@@ -498,54 +498,48 @@ __device__ void pv_role(const KernelCtx<D, F8> &cx, int t)
             }
             return true;
         };
-        if (F8 && u_lo < u_hi) {
-            ok = convert(u_lo, idx);
-            if (!ok)
-                break;
-        }
-        for (int j = u_lo; j < u_hi; ++j, ++idx) {
-            const uint32_t stage = idx % kStages;
-            if (!uses(j, first, hi, step)) {
-                // tile not used by this slot: release it once it has landed
-                ok = warp_wait(bar(full[stage]), (idx / kStages) & 1, cx.wc, W_KV_FULL);
-                if (!ok)
-                    break;
-                if (lane == 0)
-                    ptx::mbar_arrive(bar(empty[stage]));
-                __syncwarp();
-                if (F8 && j + 1 < u_hi) {
-                    ok = convert(j + 1, idx + 1);
+        // in 8 bits a tile's V is converted when the P V before has been issued
+        for (int j = F8 ? u_lo - 1 : u_lo; j < u_hi; ++j) {
+            if (j >= u_lo) {
+                const uint32_t stage = idx % kStages;
+                if (!uses(j, first, hi, step)) {
+                    // tile not used by this slot: release it once it has landed
+                    ok = warp_wait(bar(full[stage]), (idx / kStages) & 1, cx.wc, W_KV_FULL);
                     if (!ok)
                         break;
-                }
-                continue;
-            }
-            ok = warp_wait(bar(sm.p_full[t]), pcount & 1, cx.wc, W_P_FULL);
-            if (!ok)
-                break;
-            ++pcount;
-            if (F8) { // S has waited for K alone
-                ok = warp_wait(bar(full[stage]), (idx / kStages) & 1, cx.wc, W_KV_FULL);
-                if (!ok)
-                    break;
-            }
-            ptx::tc_fence_after();
-            if (lane == 0) {
-                // D = 64: O += P [V_j | 1] (V's second column block is the ones
-                // tile, LBO bytes away); D = 128: V's two 64-column halves
-                const uint32_t vlo = v_lo0 + stage * kKVLo;
-                const uint32_t lbo = C::kOnes ? (ones_lo - vlo) << 4 : C::kKVHalf;
-                const uint64_t hi_v = umma_desc_hi(lbo, C::kGroupBytes, kSwizzle128B);
+                    if (lane == 0)
+                        ptx::mbar_arrive(bar(empty[stage]));
+                    __syncwarp();
+                } else {
+                    ok = warp_wait(bar(sm.p_full[t]), pcount & 1, cx.wc, W_P_FULL);
+                    if (!ok)
+                        break;
+                    ++pcount;
+                    if (F8) { // S has waited for K alone
+                        ok = warp_wait(bar(full[stage]), (idx / kStages) & 1, cx.wc, W_KV_FULL);
+                        if (!ok)
+                            break;
+                    }
+                    ptx::tc_fence_after();
+                    if (lane == 0) {
+                        // D = 64: O += P [V_j | 1] (V's second column block is the ones
+                        // tile, LBO bytes away); D = 128: V's two 64-column halves
+                        const uint32_t vlo = v_lo0 + stage * kKVLo;
+                        const uint32_t lbo = C::kOnes ? (ones_lo - vlo) << 4 : C::kKVHalf;
+                        const uint64_t hi_v = umma_desc_hi(lbo, C::kGroupBytes, kSwizzle128B);
 #pragma unroll
-                for (int kk = 0; kk < kBN / 16; ++kk)
-                    ptx::mma_ts(tO, tP + 8 * kk, hi_v | (vlo + kk * (16 * C::kRowBytes >> 4)), idesc_pv,
-                                (j > first || kk > 0) ? 1u : 0u);
-                ptx::mma_commit(bar(sm.pv_done[t]));
-                ptx::mma_commit(bar(empty[stage]));
+                        for (int kk = 0; kk < kBN / 16; ++kk)
+                            ptx::mma_ts(tO, tP + 8 * kk, hi_v | (vlo + kk * (16 * C::kRowBytes >> 4)), idesc_pv,
+                                        (j > first || kk > 0) ? 1u : 0u);
+                        ptx::mma_commit(bar(sm.pv_done[t]));
+                        ptx::mma_commit(bar(empty[stage]));
+                    }
+                    __syncwarp();
+                }
+                ++idx;
             }
-            __syncwarp();
             if (F8 && j + 1 < u_hi) {
-                ok = convert(j + 1, idx + 1);
+                ok = convert(j + 1, idx);
                 if (!ok)
                     break;
             }
@@ -798,16 +792,10 @@ __device__ void softmax_role(const KernelCtx<D, F8> &cx, const ChunkParams &p, i
                 float c[F8 ? kBN / 16 : 1], log_v[8], inv_v[8], tile_alpha = 1.f;
                 if constexpr (F8) {
                     const uint32_t at = ptx::smem_u32(&sm.factors[t][(scount - 1) & 3]);
-                    float k[8], rest[4];
+                    float k[8];
 #pragma unroll
-                    for (int i = 0; i < 8; i += 4) {
+                    for (int i = 0; i < 8; i += 4)
                         ptx::load_shared_v4(at + 4 * i, k + i);
-                        ptx::load_shared_v4(at + 32 + 4 * i, log_v + i);
-                        ptx::load_shared_v4(at + 64 + 4 * i, inv_v + i);
-                    }
-                    ptx::load_shared_v4(at + 96, rest);
-                    tile_alpha = rest[0];
-                    unit = rest[1];
 #pragma unroll
                     for (int g = 0; g < kBN / 16; ++g)
                         c[g] = k[g] * (MOD == MOD_SOFTCAP ? cap_in : qk);
@@ -830,6 +818,16 @@ __device__ void softmax_role(const KernelCtx<D, F8> &cx, const ChunkParams &p, i
                 bool rescale;
                 float alpha;
                 if constexpr (F8) {
+                    const uint32_t at = ptx::smem_u32(&sm.factors[t][(scount - 1) & 3]);
+                    float rest[4];
+#pragma unroll
+                    for (int i = 0; i < 8; i += 4) {
+                        ptx::load_shared_v4(at + 32 + 4 * i, log_v + i);
+                        ptx::load_shared_v4(at + 64 + 4 * i, inv_v + i);
+                    }
+                    ptx::load_shared_v4(at + 96, rest);
+                    tile_alpha = rest[0];
+                    unit = rest[1];
                     alpha = softmax_compute_p_scaled<kBN>(x, c, log_v, inv_v, st, pk, rescale) * tile_alpha;
                     rescale |= tile_alpha != 1.f;
                 } else {

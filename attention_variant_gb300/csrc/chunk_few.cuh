@@ -251,7 +251,7 @@ __device__ __forceinline__ void few_next(const ChunkParams &p, const ChunkPart &
             break;
         }
         if (k < n_tiles) {
-            const PartRange r = part_range(x0, n_tiles, en.tile_cost, k, me.end, me.total, cta, me.parts);
+            const PartRange r = part_range<F8>(x0, n_tiles, en.tile_cost, k, me.end, me.total, cta, me.parts);
             k_end = r.k_end;
             it.n_parts = r.n_parts;
             it.mine = r.first == cta ? 1 : 0;
@@ -416,6 +416,11 @@ __device__ void few_walker_fp8(const FewCtx<D, true> &cx, const ChunkParams &p)
             few_next<D, true>(p, me, cx.part, e, h, k, it, en);
         }
         const uint32_t slot = n % kInfo;
+        if (p.page_shift >= 0 && !it.stop) { // the loader's first look at the block table
+            const int key = ((it.u_lo >> it.shift) * FewCfg<D, true>::kBN >> p.page_shift) + static_cast<int>(ptx::lane_id());
+            if (key < p.bt_stride)
+                asm volatile("prefetch.global.L1 [%0];" ::"l"(p.block_table + static_cast<int64_t>(it.b) * p.bt_stride + key));
+        }
         if (!warp_wait(bar(sm.info_empty[slot]), ((n / kInfo) & 1) ^ 1, cx.wc, W_INFO_EMPTY))
             return;
         if (ptx::lane_id() == 0) {
@@ -449,7 +454,7 @@ __device__ void few_loader_fp8(const FewCtx<D, true> &cx, const ChunkParams &p, 
     FewSmem<D, true> &sm = *cx.sm;
     const uint32_t lane = ptx::lane_id();
     uint32_t kv_count = 0, n = 0;
-    bool ok = true;
+    bool ok = true, fenced = false;
     for (;; ++n) {
         const uint32_t slot = n % kInfo, ring = n & 1;
         ok = warp_wait(bar(sm.info_full[slot]), (n / kInfo) & 1, cx.wc, W_INFO_FULL);
@@ -467,7 +472,9 @@ __device__ void few_loader_fp8(const FewCtx<D, true> &cx, const ChunkParams &p, 
             break;
         if (lane == 0) {
             const int slots = it.n_parts ? it.heads : 0; // none for the warm-up
-            ptx::fence_proxy_async_all(); // Q's terms, which the planning kernel has written
+            if (slots && !fenced)
+                ptx::fence_proxy_async_all(); // Q's terms, which the planning kernel has written
+            fenced = slots;
             ptx::mbar_arrive_expect_tx(bar(sm.q_full[ring]),
                                        static_cast<uint32_t>(slots * C::kQParts * p.few_tq * p.G) * C::kRowBytes);
             for (int t = 0; t < slots; ++t)

@@ -102,7 +102,8 @@ __device__ __forceinline__ T load_plan(const T *src)
 // should it not come soon, they wait for the first kernel's end.  (The release is
 // a softmax thread's, which has nothing to do yet: from the producer it cost 1 us.)
 // Its CTAs take the SMs as those without work leave them.  Both end with a
-// wait for the one before: the second stands for the first to what follows, and
+// wait for the one before: the second stands for the first to what follows (one of its CTAs is
+// enough), and
 // a CTA of the first that gave up early is not gone before the plan is there.
 // (One kernel for both: the path laid out second started 6 to 9 us late, its
 // instructions fetched from memory.)
@@ -119,7 +120,7 @@ __device__ __forceinline__ int part_of(const ChunkParams &p)
 }
 
 // At the start: a CTA of the second kernel without work (kind 0: row blocks, 1:
-// few rows) has only to wait for the first.
+// few rows) has at most to wait for the first.
 __device__ __forceinline__ bool idle_second(const ChunkParams &p, int kind, int part)
 {
     if (!p.second)
@@ -132,7 +133,9 @@ __device__ __forceinline__ bool idle_second(const ChunkParams &p, int kind, int 
         ptx::wait_dependency();
     if (__ldcg(&p.parts[kind * p.n_cta + part].parts))
         return false;
-    ptx::wait_dependency();
+    // one CTA stands for all: the others leave their SMs to the joins (1 us)
+    if (part == 0)
+        ptx::wait_dependency();
     return true;
 }
 
@@ -167,15 +170,23 @@ struct PartRange {
     int first, n_parts; // the item's first part and number of parts
 };
 
+// a / b for a >= 0, b > 0, by the short division where that does.
+__device__ __forceinline__ int64_t div_short(int64_t a, int64_t b)
+{
+    return ((a | b) >> 32) == 0 ? static_cast<uint32_t>(a) / static_cast<uint32_t>(b) : a / b;
+}
+
+template <bool SHORT = false>
 __device__ __forceinline__ PartRange part_range(int64_t x0, int n_tiles, int tile_cost, int k, int64_t x_end,
                                                 int64_t total, int part, int parts)
 {
     PartRange r;
-    r.k_end = static_cast<int>(min(static_cast<int64_t>(n_tiles), (x_end - x0 + tile_cost - 1) / tile_cost));
-    r.first = k == 0 ? part : static_cast<int>(x0 * parts / total);
+    auto div = [](int64_t a, int64_t b) { return SHORT ? div_short(a, b) : a / b; };
+    r.k_end = static_cast<int>(min(static_cast<int64_t>(n_tiles), div(x_end - x0 + tile_cost - 1, tile_cost)));
+    r.first = k == 0 ? part : static_cast<int>(div(x0 * parts, total));
     const int last = r.k_end == n_tiles
                          ? part
-                         : static_cast<int>((x0 + static_cast<int64_t>(n_tiles - 1) * tile_cost) * parts / total);
+                         : static_cast<int>(div((x0 + static_cast<int64_t>(n_tiles - 1) * tile_cost) * parts, total));
     r.n_parts = last - r.first + 1;
     return r;
 }
@@ -544,15 +555,41 @@ __device__ __forceinline__ void join_few(const ChunkParams &p, const ChunkJoin &
     const int lane = threadIdx.x & 31, dim = threadIdx.x & (D - 1), n_parts = jn.n_parts;
     auto part = [&](int q) { return partial<D>(p, cta + q, q == 0 ? 1 : 0, slot); };
     for (int n = z * kPerBlock + static_cast<int>(threadIdx.x) / D; n < jn.rows[slot]; n += kJoinSplit * kPerBlock) {
-        float M = kNegInf;
-        for (int q = lane; q < n_parts; q += 32)
-            M = fmaxf(M, part(q)[R * 128 + n]);
+        const int few = n_parts <= kDepth; // everything is loaded at once
+        float M = kNegInf, sums[4] = {0.f, 0.f, 0.f, 0.f}, l = 0.f, o = 0.f;
+        if (few) {
+            float v[kDepth];
+            if (lane < n_parts) {
+                const float *s = part(lane) + R * 128 + n;
+                M = s[0];
 #pragma unroll
-        for (int d = 16; d; d >>= 1)
-            M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+                for (int k = 0; k < 4; ++k)
+                    sums[k] = s[R * (k + 1)];
+            }
+            const float mine = M;
+#pragma unroll
+            for (int i = 0; i < kDepth; ++i)
+                v[i] = i < n_parts ? part(i)[n * 128 + dim] : 0.f;
+#pragma unroll
+            for (int d = 16; d; d >>= 1)
+                M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+            const float w = lane < n_parts ? ptx::ex2(mine - (M == kNegInf ? 0.f : M)) : 0.f;
+            l = (((0.f + sums[0]) + sums[1]) + sums[2] + sums[3]) * w;
+#pragma unroll
+            for (int d = 16; d; d >>= 1)
+                l += __shfl_xor_sync(0xffffffffu, l, d);
+#pragma unroll
+            for (int i = 0; i < kDepth; ++i)
+                o = fmaf(__shfl_sync(0xffffffffu, w, i), v[i], o);
+        } else {
+            for (int q = lane; q < n_parts; q += 32)
+                M = fmaxf(M, part(q)[R * 128 + n]);
+#pragma unroll
+            for (int d = 16; d; d >>= 1)
+                M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+        }
         const float M0 = M == kNegInf ? 0.f : M;
-        float l = 0.f, o = 0.f;
-        for (int q0 = 0; q0 < n_parts; q0 += 32) {
+        for (int q0 = 0; q0 < (few ? 0 : n_parts); q0 += 32) {
             float w = 0.f, a = 0.f;
             if (q0 + lane < n_parts) {
                 const float *s = part(q0 + lane) + R * 128 + n;
