@@ -593,9 +593,10 @@ __device__ __forceinline__ void write_slot(const ChunkParams &p, const Item &inf
 {
     const bool live = r < inf.rows[t], whole = inf.n_parts == 1;
     const RowOut<D> w = row_out<D>(p, inf, t, r);
-    const float inv = F8 ? row_inv_norm(st) * unit : row_inv_norm(st);
+    // (in 8 bits a row of q that is not finite, whose sum is NaN, comes out as NaN)
+    const float inv = F8 ? (st.l_round == 0.f ? 0.f : ptx::rcp_approx(st.l_round) * unit) : row_inv_norm(st);
     // an accumulator without a tile, or a row without a key, is not read
-    const bool keys = any && st.m_ref != kNegInf;
+    const bool keys = any && (F8 ? !(st.l_round == 0.f) : st.m_ref != kNegInf);
 #pragma unroll 1
     for (int c = 0; c < D; c += 32) {
         uint32_t raw[32];
@@ -623,7 +624,7 @@ __device__ __forceinline__ void write_slot(const ChunkParams &p, const Item &inf
     }
     if (whole) {
         if (live && w.lse)
-            *w.lse = row_lse(st);
+            *w.lse = F8 && st.l != st.l ? st.l : row_lse(st);
         return;
     }
     if (live) {
@@ -655,7 +656,7 @@ __device__ __forceinline__ void write_joined(const ChunkParams &p, const Item &i
         w0 *= unit;
         w1 *= __uint_as_float(other[3]);
     }
-    const float inv = lr > 0.f ? ptx::rcp_approx(lr) : 0.f;
+    const float inv = (F8 ? lr == 0.f : !(lr > 0.f)) ? 0.f : ptx::rcp_approx(lr);
 #pragma unroll 1
     for (int c = 0; c < H; c += 16) {
         uint32_t a[16], b[16];
@@ -682,7 +683,7 @@ __device__ __forceinline__ void write_joined(const ChunkParams &p, const Item &i
         return;
     if (whole) {
         if (t == 0 && w.lse)
-            *w.lse = l > 0.f ? (m + log2f(l)) * kLn2 : kNegInf;
+            *w.lse = (F8 ? l == 0.f : !(l > 0.f)) ? kNegInf : (m + log2f(l)) * kLn2;
     } else {
         w.mine[H * 128] = m;
         w.mine[(H + 1) * 128] = l;
@@ -798,7 +799,8 @@ __device__ void softmax_role(const KernelCtx<D, F8> &cx, const ChunkParams &p, i
                         ptx::load_shared_v4(at + 4 * i, k + i);
 #pragma unroll
                     for (int g = 0; g < kBN / 16; ++g)
-                        c[g] = k[g] * (MOD == MOD_SOFTCAP ? cap_in : qk);
+                        // not 0: hidden scores stay -inf
+                        c[g] = MOD == MOD_SOFTCAP ? k[g] * cap_in : fmaxf(k[g] * qk, 1e-37f);
                 }
                 if (take_turns && !turn_wait())
                     return;

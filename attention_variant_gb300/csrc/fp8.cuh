@@ -103,7 +103,7 @@ __device__ __forceinline__ void tile_factors(TileFactors &f, float k, float scal
         most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
     most = fmaxf(top, most);
     if (lane < 8) {
-        f.k[lane] = k > 0.f ? k : 1.f;
+        f.k[lane] = k > 0.f ? k : 0.f;
         const float v = fmaxf(log_v - most, kLeastV) + kPBias;
         f.log_v[lane] = v;
         f.inv_v[lane] = ptx::ex2(-v);

@@ -592,9 +592,8 @@ fl_status fl_attn_chunk(const fl_tensor *q, const fl_tensor *k_cache, const fl_t
  *                     (both tensors the same; it follows from the shapes)
  * Element d of key row r of page p and head h stands for
  *     cache[p][r][h][d] * scale[p][r / block][h].
- * Scales are positive powers of two, between 2^-100 and 2^100: code times scale is then
- * exact in bf16.  Others are allowed where a cache comes from elsewhere and cost a rounding
- * of the scale and of each value to bf16.
+ * Scales are positive, between 2^-100 and 2^100.  The append makes powers of two; caches
+ * from elsewhere may have others.
  *
  * fl_kv_append_fp8 -- fl_kv_append into such a cache.
  * Arguments as there, but page_size a multiple of block.  Per KV head, k (rotated in
@@ -631,9 +630,13 @@ fl_status fl_kv_read_fp8(const fl_tensor *k_cache, const fl_tensor *v_cache, con
 /*
  * fl_attn_chunk_fp8 -- fl_attn_chunk over such a cache (contiguous ones are
  * [B, S_max, Hk, D] with scales [B, S_max / block, Hk]).  Everything said there holds, with
- * the values of the cache in place of its elements.  Codes and scales of keys that no row of
- * their request sees may be anything; those of the others must not be NaN.  The
- * workspace is larger: ask fl_attn_chunk_fp8_workspace_size.
+ * the values of the cache in place of its elements, and fewer than 2^30 tokens.  Codes and scales
+ * of keys that no row of their request sees may be anything; those of the others must not
+ * be NaN.  Weights times scales of V are held relative to the largest of their row (few rows) or
+ * of their item (row blocks): what lies 2^-20 below counts with fewer bits, and scales of V that
+ * are 2^-60 of another's in the request count as that.  The workspace is larger (q in two e4m3
+ * terms, which hold bf16 exactly down to 2^-10 of a row's largest element and to 2^-18 of it
+ * below): ask fl_attn_chunk_fp8_workspace_size.
  */
 fl_status fl_attn_chunk_fp8_workspace_size(const fl_tensor *q, const fl_tensor *k_cache,
                                            const fl_chunk_desc *desc, size_t *bytes);

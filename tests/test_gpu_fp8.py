@@ -430,18 +430,84 @@ def test_chunk_scales_far_apart(D, lo, hi):
 
 
 def test_chunk_scales_that_are_no_powers_of_two():
-    # allowed: the scale of V and each of its values rounded to bf16 (2^-8 each), those of K
-    # the same, which moves scores by up to 2^-7 |z|
-    p = _problem([1, 70], [200, 150], 4, 2, 64, 32, 16)
+    p = _problem([1, 70, 4], [200, 150, 300], 4, 2, 64, 32, 16)
     for n in "kv":
         p[n + "s"] *= 1.3
         p[n] = [x * float(torch.tensor(1.3)) for x in p[n]]
-    out, lse, tol = _expected(p)
-    got, = _launch(p)
-    z = 2.0 ** -7 * 8 * 1.3 ** 2  # |z| of these inputs is below 8
-    spread = max(float(x.abs().max()) for x in p["v"])
-    assert ((got[0].double().cpu() - out).abs() <= tol + 2.0 ** -7 * out.abs() + 2 * z * spread).all()
-    assert (got[1].double().cpu() - lse).abs().max() <= z + 2e-4
+    _compare(_launch(p)[0], _expected(p), "scales times 1.3")
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_chunk_rows_that_are_not_finite(D):
+    # a row of q with an infinity or NaN is NaN, the others are as they were; rows of tiny and
+    # of huge elements keep their precision
+    p = _problem([1, 2, 50], [300, 40, 90], 8, 2, D, 32, 16, seed=3)
+    q = p["q"]
+    q[1, 3, 5], q[2, 0, 0], q[10, 7, 9], q[30, 2, 1] = math.inf, NAN, -math.inf, NAN
+    bad = [(1, 3), (2, 0), (10, 7), (30, 2)]
+    q[0, 1] *= 2.0 ** -90
+    q[20, 6] *= 2.0 ** -70
+    q[21, 5] = (q[21, 5].float() * torch.exp2(-torch.arange(D) / 4.0)).to(torch.bfloat16)
+    clean = dict(p, q=q.clone())
+    for t, h in bad:
+        clean["q"][t, h] = 0
+    want = _expected(clean)
+    out, lse = _launch(p)[0]
+    for t, h in bad:
+        assert bool(torch.isnan(out[t, h]).all())
+        out[t, h], lse[h, t] = want[0][t, h].to(out), want[1][h, t].to(lse)
+    _compare((out, lse), want, "rows that are not finite")
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("window", [0, 3, 130, 256, 300])
+def test_chunk_few_rows_at_the_tiles_borders(D, window):
+    lens = [255, 256, 257, 511, 512, 513, 16, 17, 271, 273]
+    _case([1] * 9 + [3], lens, Hq=5, Hk=5, D=D, page=16, window=window, calls=2)
+    _case([2] * 10, lens, Hq=16, Hk=2, D=D, page=0, block=32, window=window)
+
+
+def test_chunk_lengths_past_their_bound():
+    p = _problem([4], [100], 8, 2, 64, 16, 16)
+    for strict, want in ((False, 0), (True, fa.FL_DEVERR_LENGTHS)):
+        err = _ints([0])
+        d = _desc(p, 60, err, strict_lengths=strict)
+        q, kc, vc, ks, vs = (p[n].cuda() for n in ("q", "kc", "vc", "ks", "vs"))
+        ws = torch.empty(fa.fl_attn_chunk_fp8_workspace_size(q, kc, d), dtype=torch.uint8, device="cuda")
+        out, lse = torch.zeros_like(q), torch.zeros((8, 4), device="cuda")
+        fa.fl_attn_chunk_fp8(q, kc, vc, ks, vs, out, lse, d, ws)
+        torch.cuda.synchronize()
+        assert int(err.item()) == want
+        cut = dict(p, kv_lens=[60])
+        _compare((out, lse), _expected(cut), "cut to 60 keys")
+
+
+def test_caches_of_more_than_4_gigabytes():
+    # codes 2^32 and more into the caches, scales far into theirs
+    P, page, block, Hk, D, T = 70000, 256, 16, 4, 64, 40
+    dev = "cuda"
+    codes = [torch.zeros((P, page, Hk, D), dtype=torch.uint8, device=dev).view(FP8) for _ in "kv"]
+    scales = [torch.full((P, page // block, Hk), 2.0 ** -5, device=dev) for _ in "kv"]
+    k, v, q = (_rand((T, h, D), i) for i, h in enumerate((Hk, Hk, 8)))
+    slots = torch.cat((torch.arange(30) + (P - 1) * page + 100, torch.arange(10) + (P - 3) * page))
+    fa.fl_kv_append_fp8(None, k.to(dev), v.to(dev), None, *codes, *scales, slots.to(dev))
+    back = [torch.zeros((T, Hk, D), device=dev) for _ in "kv"]
+    fa.fl_kv_read_fp8(*codes, *scales, slots.to(dev), *back)
+    for x, b, c, s in zip((k, v), back, codes, scales):
+        held_c, held_s = ref8.append(c[P - 3:].cpu(), torch.full((3, page // block, Hk), 2.0 ** -5), x, slots - (P - 3) * page)
+        assert torch.equal(s[P - 3:].cpu(), held_s)
+        assert torch.equal(_bits(c[P - 3:]), _bits(held_c))
+        assert torch.equal(b.cpu().double(), ref8.values(held_c, held_s).view(-1, Hk, D)[slots - (P - 3) * page])
+    # both kinds of rows over the last page, and over the one before the last but one
+    d = fa.make_chunk_desc(_ints([0, 1, 31]), _ints([10, 256]), _ints([[P - 3], [P - 1]]), 256)
+    q = q[:31].to(dev)
+    out, lse = torch.zeros_like(q), torch.zeros((8, 31), device=dev)
+    ws = torch.empty(fa.fl_attn_chunk_fp8_workspace_size(q, codes[0], d), dtype=torch.uint8, device=dev)
+    fa.fl_attn_chunk_fp8(q, *codes, *scales, out, lse, d, ws)
+    for a, z, page_at, L in ((0, 1, P - 3, 10), (1, 31, P - 1, 256)):
+        kk, vv = (ref8.values(c[page_at:page_at + 1].cpu(), s[page_at:page_at + 1].cpu())[0, :L] for c, s in zip(codes, scales))
+        want, wl, tol = ref.chunk_rows(q[a:z].cpu(), kk, vv, None)
+        _compare((out[a:z], lse[:, a:z]), (want, wl, tol), "far into the cache")
 
 
 def test_chunk_rows_without_keys():
