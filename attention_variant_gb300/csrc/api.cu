@@ -1427,6 +1427,7 @@ fl_status chunk_run(const fl_tensor *q, const fl_tensor *k_cache, const fl_tenso
         p.q8 = ws + pl.q8;
         p.q_scale = reinterpret_cast<float *>(ws + pl.q_scale);
         p.cost_few = (p.cost_few * fl::few_tile(int(pl.D), true) / 128 + 1) / 2; // half the bytes
+        p.cost_more = p.cost_few + (p.cost_few + 2) / 3; // 16 rows a KV head
         p.cost_item = p.cost_few_item = 50; // as measured, over batches of both kinds
     }
     const cudaError_t e = (fp8 ? fl::launch_chunk_fp8 : fl::launch_chunk)(maps, p, reinterpret_cast<cudaStream_t>(stream));

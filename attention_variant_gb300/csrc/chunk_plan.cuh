@@ -353,7 +353,7 @@ __device__ __forceinline__ void plan_entries(const ChunkParams &p, PlanShared &s
                 const int tile = kind ? few_tile(D, F8) : chunk_key_tile(D);
                 en.lo = k0 / tile;
                 en.n_tiles = max(1, (max(k1, 0) + tile - 1) / tile - en.lo);
-                en.tile_cost = kind ? p.cost_few : en.n_tok > p.TQ ? p.cost_pair : p.cost_single;
+                en.tile_cost = kind ? (F8 && en.n_tok * p.G > 8 ? p.cost_more : p.cost_few) : en.n_tok > p.TQ ? p.cost_pair : p.cost_single;
                 add.places = kind ? 1 << 16 : 1;
                 const int64_t cost = entry_cost(p, en);
                 add.cost[0] = kind ? 0 : cost;
@@ -426,7 +426,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
             share = min(max(static_cast<int>(div64(cum[0] * p.n_cta + both, 2 * both)) * 2, 2), p.n_cta - 2);
 #pragma unroll
         for (int kind = 0; kind < 2; ++kind) {
-            const int64_t tile = kind ? p.cost_few : sm.most, least = max(tile, static_cast<int64_t>(p.cost_least));
+            const int64_t tile = kind ? (F8 ? p.cost_more : p.cost_few) : sm.most, least = max(tile, static_cast<int64_t>(p.cost_least));
             int g = kind ? p.n_cta - share : share;
             if (cum[kind] < least * g)
                 g = static_cast<int>(div64(cum[kind] + least - 1, least));

@@ -380,6 +380,7 @@ struct ChunkParams {
     int64_t ks_p, ks_b, vs_p, vs_b;
     int scale_shift;           // log2 of the keys per block
     int n_pages;
+    int cost_more;             // of a tile of few rows that are more than 8, at least cost_few
     const __nv_bfloat16 *q;    // element strides (token, head)
     int64_t q_st, q_sh;
     uint8_t *q8;               // the workspace: [2][T][Hq][D], q's e4m3 terms
