@@ -37,7 +37,12 @@
 // key: tcgen05's kind::f8f6f4 multiplies its e4m3 codes.  Q comes as two e4m3 terms, which
 // hold a bf16 number exactly (split_q), and a key's scale, one number per TMEM lane, goes
 // into its scores; P goes as two e4m3 terms with V's scale in it (few_item_fp8), off by
-// 2^-9 of a weight, and where that is more by 2^-16 of the row's largest.
+// 2^-9 of a weight, and where that is more by 2^-16 of the row's largest.  K and V come
+// together, in tiles of 16 KB and one ring: at half the bytes a key it is the chain of a tile (S, its
+// softmax, P, the product) that limits, so tiles have 256 keys at D = 64 (128: 112 us on
+// the 64 requests above) and a row one reference for all its keys, which moves rarely.
+// 64 requests of 512 to 8192 keys take 68 us, of 8192 keys 107 (0.74 of the copy's
+// rate); the start (14 us until the first S) and the end (8 us) weigh twice as much here.
 //
 //   warp  0     walks the CTA's items, publishes them, loads Q, K and V by TMA
 //   warp  1     issues S^T of both slots

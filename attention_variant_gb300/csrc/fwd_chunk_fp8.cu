@@ -1,5 +1,6 @@
 // fwd_chunk_fp8.cu -- attention of ragged chunks of new tokens over a cache in
-// 8 bits: the kernels of chunk_blocks.cuh and chunk_few.cuh.
+// 8 bits: the kernels of chunk_blocks.cuh and chunk_few.cuh (mathematics, bounds and
+// figures there).  A unit of its own, compiled beside fwd_chunk.cu.
 #include "chunk_blocks.cuh"
 
 namespace fl {
