@@ -16,7 +16,7 @@
 // pairs -- and walks the (token, head) rows with it, so that a unit costs an
 // address, two loads, the rotation and two stores (about 90 instructions for
 // 8 bf16 pairs; with the place and the tensor worked out for every unit it
-// was 290, in 116 registers, and 45 us where this takes 25 for q and k of 8 x
+// was 290, in 116 registers, and 45 us where this takes 24 for q and k of 8 x
 // 2048 tokens of 16 heads of 64).
 #include "rope.cuh"
 
