@@ -36,8 +36,8 @@
 // A cache in 8 bits (F8) goes through the same products as it is, half the bytes a
 // key: tcgen05's kind::f8f6f4 multiplies its e4m3 codes.  Q comes as two e4m3 terms, which
 // hold a bf16 number exactly (split_q), and a key's scale, one number per TMEM lane, goes
-// into its scores; P goes as two e4m3 terms with V's scale in it (few_item_fp8), off by
-// 2^-9 of a weight, and where that is more by 2^-16 of the row's largest.  K and V come
+// into its scores; P goes in f16's precision, as three e5m2 terms with V's scale in it
+// (few_item_fp8).  K and V come
 // together, in tiles of 16 KB and one ring: at half the bytes a key it is the chain of a tile (S, its
 // softmax, P, the product) that limits, so tiles have 256 keys at D = 64 (128: 112 us on
 // the 64 requests above) and a row one reference for all its keys, which moves rarely.
@@ -78,10 +78,12 @@ struct FewCfg {
     static constexpr uint32_t kQBytes = kQParts * kQPart;
     static constexpr uint32_t kHalf = kBN * kRowBytes;      // half a K or V tile, or all of it
     static constexpr uint32_t kTileBytes = kHalves * kHalf;
-    static constexpr uint32_t kPRow = F8 ? 32 : 64;         // bytes of a key's row of P: two terms of up to 16 rows
+    static constexpr uint32_t kPRow = F8 ? 48 : 64;         // bytes of a key's row of P: two terms (8 bits: three) of up to 16 rows
     // Buffers of a slot's P: the next tile's may be written while this one's product runs
     static constexpr int kPBufs = F8 ? 2 : 1;
     static constexpr uint32_t kColS = 0, kColO = 64, kStride = 32; // TMEM columns of slot t: + 32 t
+    static constexpr uint32_t kStrideO = F8 ? 64 : 32;      // (of O)
+    static constexpr uint32_t kColumns = F8 ? 256 : 128;
     static constexpr uint32_t kSubS = 16;                   // and of S of the tile's second 128 keys
 };
 
@@ -642,13 +644,16 @@ __device__ void few_pv_role(const FewCtx<D, F8> &cx, int slot_lo, int slot_hi)
     // O^T = V^T P^T: both operands with their long index contiguous.  V^T has
     // 128 rows: at D = 64 the second 64 repeat the first (block stride 0).  P
     // has 64-byte rows of a key, 64-byte swizzle.
-    // In 8 bits V^T's rows are 64 or 128 bytes, P's 32, each swizzled over its length.
+    // In 8 bits V^T's rows are 64 or 128 bytes, swizzled over their length, and P (e5m2) is
+    // not: units of 16 bytes, those of a key kBN * 16 bytes apart.
     constexpr uint32_t kMajor = 1u << 15 | 1u << 16;
-    constexpr uint32_t idesc8 = (F8 ? umma_idesc_e4m3(128, 16) : umma_idesc_bf16(128, 16, true)) | kMajor;
-    constexpr uint32_t idesc16 = (F8 ? umma_idesc_e4m3(128, 32) : umma_idesc_bf16(128, 32, true)) | kMajor;
+    constexpr uint32_t idesc4 = umma_idesc_e4m3_e5m2(128, 16) | kMajor; // F8 alone
+    constexpr uint32_t idesc8 = (F8 ? umma_idesc_e4m3_e5m2(128, 32) : umma_idesc_bf16(128, 16, true)) | kMajor;
+    constexpr uint32_t idesc16 = (F8 ? umma_idesc_e4m3_e5m2(128, 48) : umma_idesc_bf16(128, 32, true)) | kMajor;
     constexpr uint64_t kHiV = umma_desc_hi(D == 128 ? C::kHalf : 0, C::kGroupBytes, C::kRowSwizzle);
-    constexpr uint64_t kHiP = umma_desc_hi(16, 8 * C::kPRow, F8 ? kSwizzle32B : kSwizzle64B);
+    constexpr uint64_t kHiP = F8 ? umma_desc_hi(8 * 16, kBN * 16, kSwizzleNone) : umma_desc_hi(16, 8 * C::kPRow, kSwizzle64B);
     constexpr int kKeys = F8 ? 32 : 16; // of an MMA
+    constexpr uint32_t kPKey = F8 ? 16 : C::kPRow; // bytes from one key to the next
     const uint32_t v_lo0 = ptx::smem_u32(sm.v[0]) >> 4, p_lo0 = ptx::smem_u32(sm.p[0][0]) >> 4;
     uint32_t idx = 0, pcount[2] = {0u, 0u};
     bool ok = true;
@@ -661,7 +666,7 @@ __device__ void few_pv_role(const FewCtx<D, F8> &cx, int slot_lo, int slot_hi)
         const int stop = inf.stop, shift = inf.shift, u_lo = inf.u_lo, u_hi = inf.u_hi;
         const int lo = inf.lo << shift, hi = inf.hi << shift, L = inf.L, key_lo = inf.key_lo;
         const int first = max(u_lo, lo);
-        const uint32_t idesc = inf.rows <= 8 ? idesc8 : idesc16; // two terms a row
+        const uint32_t idesc = F8 && inf.rows <= 4 ? idesc4 : inf.rows <= 8 ? idesc8 : idesc16; // two or three terms a row
         __syncwarp();
         if (lane == 0)
             ptx::mbar_arrive(bar(sm.info_empty[slot]));
@@ -708,8 +713,8 @@ __device__ void few_pv_role(const FewCtx<D, F8> &cx, int slot_lo, int slot_hi)
 #pragma unroll
                 for (int kk = 0; kk < kBN / kKeys; ++kk)
                     (F8 ? ptx::mma_ss_f8 : ptx::mma_ss)(
-                        cx.tmem + C::kColO + C::kStride * t, kHiV | (vlo + kk * (kKeys * C::kRowBytes >> 4)),
-                        kHiP | (plo + kk * (kKeys * C::kPRow >> 4)), idesc, (begun || kk > 0) ? 1u : 0u);
+                        cx.tmem + C::kColO + C::kStrideO * t, kHiV | (vlo + kk * (kKeys * C::kRowBytes >> 4)),
+                        kHiP | (plo + kk * (kKeys * kPKey >> 4)), idesc, (begun || kk > 0) ? 1u : 0u);
                 ptx::mma_commit(bar(sm.pv_done[t][buf]));
                 ptx::mma_commit(bar(empty[stage]));
             }
@@ -777,7 +782,7 @@ __device__ __forceinline__ bool few_item(const FewCtx<D, false> &cx, const Chunk
     const int wq = (threadIdx.x >> 5) & 3, lane = static_cast<int>(ptx::lane_id());
     const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
     const uint32_t tS = cx.tmem + lanes + C::kColS + C::kStride * t;
-    const uint32_t tO = cx.tmem + lanes + C::kColO + C::kStride * t;
+    const uint32_t tO = cx.tmem + lanes + C::kColO + C::kStrideO * t;
     const uint32_t b_group = bar(sm.group[t]);
     const float c = MOD == MOD_NONE ? p.qk_log2 : 1.f;
     ScoreMod smod;
@@ -1049,35 +1054,46 @@ __device__ void few_softmax(const FewCtx<D, false> &cx, const ChunkParams &p, in
 // ------------------------------------------------------------------ softmax, 8 bits
 //
 // A thread has keys r (and, of a tile of 256, 128 + r).  One reference a row, ref, for the
-// weights times V's scale: P = 2^(z + log2 s - ref), as two e4m3 terms, the second 16
-// times what the first left out; the row's sum takes P / s.  The reference makes the
-// largest of a tile 2^kFewTop when it is set, and is set again where one would pass
-// e4m3's 448: until then the slot's warps only agree, once a tile, that none does.
+// weights times V's scale: P = 2^(kFewTop + z + log2 s - ref); the row's sum takes P / (s 2^kFewTop).
+// The reference makes the largest P of a tile 2^kFewTop when it is set, and is set again where
+// one would pass 2^kFewMost: until then the slot's warps only agree, once a tile, that
+// none does.
+//
+// P is rounded to f16, 11 bits down to 2^-26 of the row's largest and steps of 2^-36 of it
+// below, and goes as three e5m2 terms of 3 bits and a sign each, 16 times apart, which hold
+// f16 exactly.  (In two e4m3 terms, 9 bits from 2^2 on and steps of 2^-13, a row that has most of its
+// weight on one key lost the others': relative errors of 0.1 to 0.5 at 8192 to 32768 keys.)
 
-constexpr float kFewTop = 2.f, kFewMost = 8.8f, kFewRest = 16.f;
+constexpr float kFewTop = 12.f, kFewMost = 14.8f; // rounded to e5m2, 2^14.8 times 2^-3 times 16 stays in range
+constexpr int kFewTerms = 3;
 
 struct FewState8 {
     uint32_t s, group, tiles; // phases of s_full, group; tiles so far
     uint32_t loaded;          // tiles of the CTA before this item
 };
 
-template <int R>
-__device__ __forceinline__ void few_load_o8(uint32_t tO, uint32_t (&o)[2 * R])
+// Four numbers to f16, and those to three e5m2 terms (the upper bytes of f16 numbers): a term
+// is what is left, rounded; what that leaves is exact, and is multiplied by 16.
+__device__ __forceinline__ void split_p(const float (&e)[4], uint32_t &t0, uint32_t &t1, uint32_t &t2)
 {
-    if constexpr (R == 4)
-        ptx::tmem_ld8(tO, o);
-    else if constexpr (R == 8)
-        ptx::tmem_ld16(tO, o);
-    else
-        ptx::tmem_ld32(tO, o);
-    ptx::tmem_wait_ld();
-    ptx::reg_fence<2 * R>(o);
+    uint32_t a = ptx::pack_f16(e[0], e[1]), b = ptx::pack_f16(e[2], e[3]);
+    auto rounded = [](uint32_t x) { return (x + 0x00800080u) & 0xff00ff00u; };
+    auto rest = [](uint32_t x, uint32_t t) {
+        const __half2 r = __hmul2(__hsub2(*reinterpret_cast<const __half2 *>(&x), *reinterpret_cast<const __half2 *>(&t)),
+                                  __half2half2(__ushort_as_half(0x4c00))); // 16
+        return *reinterpret_cast<const uint32_t *>(&r);
+    };
+    uint32_t ra = rounded(a), rb = rounded(b);
+    t0 = __byte_perm(ra, rb, 0x7531);
+    a = rest(a, ra), b = rest(b, rb);
+    ra = rounded(a), rb = rounded(b);
+    t1 = __byte_perm(ra, rb, 0x7531);
+    t2 = __byte_perm(rounded(rest(a, ra)), rounded(rest(b, rb)), 0x7531);
 }
 
 // A key's row of P and its part of the sums: d = log2 of P.
 template <int R>
-__device__ __forceinline__ void few_p8(const float (&d)[R], float inv_v, float (&sum)[R], uint32_t (&hi)[R / 4],
-                                       uint32_t (&lo)[R / 4])
+__device__ __forceinline__ void few_p8(const float (&d)[R], float inv_v, float (&sum)[R], uint32_t (&p)[kFewTerms][R / 4])
 {
 #pragma unroll
     for (int n = 0; n < R; n += 4) {
@@ -1087,13 +1103,13 @@ __device__ __forceinline__ void few_p8(const float (&d)[R], float inv_v, float (
             e[i] = ptx::ex2(d[n + i]);
         ptx::fma2(sum[n], sum[n + 1], e[0], e[1], inv_v, inv_v, sum[n], sum[n + 1]);
         ptx::fma2(sum[n + 2], sum[n + 3], e[2], e[3], inv_v, inv_v, sum[n + 2], sum[n + 3]);
-        const uint32_t h0 = to_e4m3x2(e[0], e[1]), h1 = to_e4m3x2(e[2], e[3]);
-        const float2 a = from_e4m3x2(h0), b = from_e4m3x2(h1);
-        hi[n / 4] = h0 | h1 << 16;
-        lo[n / 4] = to_e4m3x2((e[0] - a.x) * kFewRest, (e[1] - a.y) * kFewRest) |
-                    to_e4m3x2((e[2] - b.x) * kFewRest, (e[3] - b.y) * kFewRest) << 16;
+        split_p(e, p[0][n / 4], p[1][n / 4], p[2][n / 4]);
     }
 }
+
+// 16 columns of O^T at a time, where column c is term c / R of row c % R.
+template <int R>
+constexpr int kFewColumns = (kFewTerms * R + 15) / 16;
 
 // One item of at most R rows.  False when a wait ran out.
 template <int MOD, int D, int R>
@@ -1107,14 +1123,13 @@ __device__ __forceinline__ bool few_item_fp8(const FewCtx<D, true> &cx, const Ch
     const int wq = (threadIdx.x >> 5) & 3, lane = static_cast<int>(ptx::lane_id());
     const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
     const uint32_t tS = cx.tmem + lanes + C::kColS + C::kStride * t;
-    const uint32_t tO = cx.tmem + lanes + C::kColO + C::kStride * t;
+    const uint32_t tO = cx.tmem + lanes + C::kColO + C::kStrideO * t;
     const uint32_t b_group = bar(sm.group[t]);
     ScoreMod smod;
     smod.qk_log2 = p.qk_log2;
     smod.softcap_in = p.softcap_in;
     smod.softcap_out = p.softcap_out;
     smod.alibi_c = smod.scale = smod.b = smod.h = 0.f;
-    const int sw = (r >> 2) & 1; // 32-byte swizzle: 16-byte unit u of key r at u ^ (r / 4 mod 2)
     auto group_wait = [&]() { return warp_wait(b_group, ct.group++ & 1, cx.wc, W_JOIN); };
     const FewTiles f = few_tiles(inf, t);
     const int n_mine = f.hi > f.first ? (f.hi - f.first + f.step - 1) / f.step : 0;
@@ -1172,7 +1187,7 @@ __device__ __forceinline__ bool few_item_fp8(const FewCtx<D, true> &cx, const Ch
         bool more = false;
 #pragma unroll
         for (int sub = 0; sub < kSub; ++sub) {
-            log_v[sub] = fmaxf(ptx::lg2(log_v[sub]), kLeastLog);
+            log_v[sub] = fmaxf(ptx::lg2(log_v[sub]), kLeastLog) + kFewTop;
             inv_v[sub] = ptx::ex2(-log_v[sub]);
             float (&x)[R] = d[sub];
             if constexpr (MOD == MOD_NONE) {
@@ -1224,13 +1239,13 @@ __device__ __forceinline__ bool few_item_fp8(const FewCtx<D, true> &cx, const Ch
         ptx::mbar_arrive(b_group);
         // ---- P, as if no row did
         float sum[R];
-        uint32_t hi[kSub][R / 4], lo[kSub][R / 4];
+        uint32_t pt[kSub][kFewTerms][R / 4];
 #pragma unroll
         for (int n = 0; n < R; ++n)
             sum[n] = l[n];
 #pragma unroll
         for (int sub = 0; sub < kSub; ++sub)
-            few_p8<R>(d[sub], inv_v[sub], sum, hi[sub], lo[sub]);
+            few_p8<R>(d[sub], inv_v[sub], sum, pt[sub]);
         if (!group_wait())
             return false;
         const uint32_t large = *flags & row_bits;
@@ -1272,24 +1287,22 @@ __device__ __forceinline__ bool few_item_fp8(const FewCtx<D, true> &cx, const Ch
                 if (!warp_wait(bar(sm.pv_done[t][last % C::kPBufs]), (last / C::kPBufs) & 1, cx.wc, W_O_FULL))
                     return false;
                 ptx::tc_fence_after();
-                uint32_t o[2 * R];
-                few_load_o8<R>(tO, o);
 #pragma unroll
-                for (int n = 0; n < R; ++n) { // a row without a key so far holds zeros
-                    o[n] = __float_as_uint(__uint_as_float(o[n]) * beta[n]);
-                    o[R + n] = __float_as_uint(__uint_as_float(o[R + n]) * beta[n]);
+                for (int i = 0; i < kFewColumns<R>; ++i) {
+                    uint32_t o[16];
+                    ptx::tmem_ld16(tO + 16 * i, o);
+                    ptx::tmem_wait_ld();
+                    ptx::reg_fence<16>(o);
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) // a row without a key so far holds zeros
+                        o[c] = __float_as_uint(__uint_as_float(o[c]) * beta[(16 * i + c) % R]);
+                    ptx::tmem_st16(tO + 16 * i, o);
                 }
-                if constexpr (R == 4)
-                    ptx::tmem_st8(tO, o);
-                else if constexpr (R == 8)
-                    ptx::tmem_st16(tO, o);
-                else
-                    ptx::tmem_st32(tO, o);
                 ptx::tmem_wait_st();
             }
 #pragma unroll
             for (int sub = 0; sub < kSub; ++sub)
-                few_p8<R>(d[sub], inv_v[sub], sum, hi[sub], lo[sub]);
+                few_p8<R>(d[sub], inv_v[sub], sum, pt[sub]);
         }
 #pragma unroll
         for (int n = 0; n < R; ++n)
@@ -1301,14 +1314,18 @@ __device__ __forceinline__ bool few_item_fp8(const FewCtx<D, true> &cx, const Ch
         }
 #pragma unroll
         for (int sub = 0; sub < kSub; ++sub) {
-            uint4 *const pdst = reinterpret_cast<uint4 *>(sm.p[t][buf] + (sub * 128 + r) * C::kPRow);
+            // 16 bytes of a key beside those of the next, the key's others kBN * 16 further
+            uint4 *const pdst = reinterpret_cast<uint4 *>(sm.p[t][buf]) + sub * 128 + r;
+            const uint32_t(&w)[kFewTerms][R / 4] = pt[sub];
             if constexpr (R == 4) {
-                pdst[sw] = make_uint4(hi[sub][0], lo[sub][0], 0, 0);
+                pdst[0] = make_uint4(w[0][0], w[1][0], w[2][0], 0);
             } else if constexpr (R == 8) {
-                pdst[sw] = make_uint4(hi[sub][0], hi[sub][1], lo[sub][0], lo[sub][1]);
+                pdst[0] = make_uint4(w[0][0], w[0][1], w[1][0], w[1][1]);
+                pdst[kBN] = make_uint4(w[2][0], w[2][1], 0, 0);
             } else {
-                pdst[sw] = make_uint4(hi[sub][0], hi[sub][1], hi[sub][2], hi[sub][3]);
-                pdst[1 ^ sw] = make_uint4(lo[sub][0], lo[sub][1], lo[sub][2], lo[sub][3]);
+#pragma unroll
+                for (int i = 0; i < kFewTerms; ++i)
+                    pdst[i * kBN] = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
             }
         }
         ptx::fence_proxy_async_smem();
@@ -1336,16 +1353,21 @@ __device__ __forceinline__ bool few_item_fp8(const FewCtx<D, true> &cx, const Ch
     for (int d = R; d < 32; d *= 2)
         l[0] += __shfl_xor_sync(0xffffffffu, l[0], d);
     float o[R];
+#pragma unroll
+    for (int n = 0; n < R; ++n)
+        o[n] = 0.f;
     if (n_mine) {
-        uint32_t raw[2 * R];
-        few_load_o8<R>(tO, raw);
+        constexpr float kTerm[] = {0x1p-12f, 0x1p-16f, 0x1p-20f}; // of 2^kFewTop, 16 apart
 #pragma unroll
-        for (int n = 0; n < R; ++n)
-            o[n] = __uint_as_float(raw[n]) + __uint_as_float(raw[R + n]) * (1.f / kFewRest);
-    } else {
+        for (int i = 0; i < kFewColumns<R>; ++i) {
+            uint32_t raw[16];
+            ptx::tmem_ld16(tO + 16 * i, raw);
+            ptx::tmem_wait_ld();
+            ptx::reg_fence<16>(raw);
 #pragma unroll
-        for (int n = 0; n < R; ++n)
-            o[n] = 0.f;
+            for (int c = 16 * i; c < min(16 * i + 16, kFewTerms * R); ++c)
+                o[c % R] = fmaf(__uint_as_float(raw[c % 16]), kTerm[c / R], o[c % R]);
+        }
     }
 #pragma unroll
     for (int n = 0; n < R; ++n)
@@ -1474,7 +1496,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::fence_proxy_async_smem();
     }
     if (warp == 1) {
-        ptx::tmem_alloc(ptx::smem_u32(&sm->tmem_base), 128);
+        ptx::tmem_alloc(ptx::smem_u32(&sm->tmem_base), C::kColumns);
         ptx::tmem_relinquish();
     }
     ptx::tc_fence_before();
@@ -1512,7 +1534,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::named_barrier_sync(1, kThreads);
         if (warp == 1) {
             ptx::tc_fence_after();
-            ptx::tmem_dealloc(cx.tmem, 128);
+            ptx::tmem_dealloc(cx.tmem, C::kColumns);
         }
         ptx::wait_dependency(); // see chunk_plan.cuh
     }

@@ -530,14 +530,15 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
 // leading-dimension byte offset >> 4 in bits 16-29, stride-dimension byte
 // offset >> 4 in bits 32-45, the fixed version value 1 in bits 46-47, base
 // offset 0 (every tile is 1024-byte aligned), swizzle mode in bits 61-63
-// (2 = 128-byte, 4 = 64-byte, 6 = 32-byte).
+// (2 = 128-byte, 4 = 64-byte, 0 = none).
 //
 // K-major operands (Q and K: one row per M/N index, the head dimension
 // contiguous): 8-row core groups are `sbo` bytes apart; the leading offset is
 // unused because one MMA's K extent (16 bf16 = 32 bytes) never leaves a
 // swizzle row.  MN-major operand (V: keys are K, the head dimension N is
 // contiguous): `sbo` is the distance between groups of 8 keys and `lbo` the
-// distance between swizzle-width column blocks of N.
+// distance between swizzle-width column blocks of N.  MN-major without a swizzle: rows of 16
+// bytes, groups of 8 keys `lbo` apart and 16-byte column blocks of N `sbo`.
 __device__ __forceinline__ uint64_t umma_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo,
                                               uint32_t swizzle_code)
 {
@@ -561,7 +562,7 @@ __host__ __device__ constexpr uint64_t umma_desc_hi(uint32_t lbo, uint32_t sbo, 
 
 constexpr uint32_t kSwizzle128B = 2;
 constexpr uint32_t kSwizzle64B = 4;
-constexpr uint32_t kSwizzle32B = 6;
+constexpr uint32_t kSwizzleNone = 0;
 
 // Instruction descriptor, kind::f16: fp32 accumulator (bits 4-5 = 1), A and B
 // bf16 (bits 7-9 = 1, bits 10-12 = 1), A K-major (bit 15 = 0), B K-major or
@@ -582,6 +583,12 @@ __host__ __device__ constexpr uint32_t umma_idesc_f16(uint32_t M, uint32_t N, bo
 __host__ __device__ constexpr uint32_t umma_idesc_e4m3(uint32_t M, uint32_t N)
 {
     return (1u << 4) | ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+
+// The same with B in e5m2 (1).
+__host__ __device__ constexpr uint32_t umma_idesc_e4m3_e5m2(uint32_t M, uint32_t N)
+{
+    return umma_idesc_e4m3(M, N) | (1u << 10);
 }
 
 } // namespace fl

@@ -1,0 +1,167 @@
+"""Weights of very different sizes in attention over the 8-bit KV cache: one key that holds
+most of a row's weight.
+
+A result is bounded relative to what its own row sees, sum_j w_j |v_j|: see _expected."""
+from __future__ import annotations
+
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+from tests import fp8_ref as ref8  # noqa: E402
+from tests import serving_ref as ref  # noqa: E402
+from tests import test_gpu_fp8 as base  # noqa: E402
+from tests.fp8_ref import FP8  # noqa: E402
+
+# what an f16 weight loses below its smallest step, relative to the largest weight times scale of
+# its row: half of 2^-24 where that one is 2^12 (few rows) or 2^6 (row blocks)
+FEW, BLOCKS = 2.0 ** -37, 2.0 ** -31
+
+
+def _scales(x, block):
+    """The append's scales of x [L, Hk, D], L a multiple of block: [L / block, Hk]."""
+    size = x.abs().view(-1, block, *x.shape[1:]).amax((1, 3))
+    return torch.tensor([[ref8.need(float(a)) for a in row] for row in size], dtype=torch.float64)
+
+
+def _held(q, keys, vals, q_lens, page=64, block=16, seed=0):
+    """A problem of requests whose keys and values are given (float64 [L, Hk, D] each), coded as the
+    append does, in a pool of pages in any order."""
+    kv_lens = [k.shape[0] for k in keys]
+    Hk, D = keys[0].shape[1:]
+    per = [-(-L // page) for L in kv_lens]
+    ids = torch.randperm(sum(per), generator=torch.Generator().manual_seed(seed))
+    p = dict(q=q, T=q.shape[0], q_lens=q_lens, kv_lens=kv_lens, cu=[0])
+    for n in q_lens:
+        p["cu"].append(p["cu"][-1] + n)
+    p["table"] = torch.full((len(keys), max(per)), -1, dtype=torch.int32)
+    for n, all_x in (("k", keys), ("v", vals)):
+        codes = torch.zeros((sum(per), page, Hk, D), dtype=torch.uint8).view(FP8)
+        scales = torch.full((sum(per), page // block, Hk), 2.0 ** -100)
+        p[n], p[n + "_scale"], at = [], [], 0
+        for b, x in enumerate(all_x):
+            L = x.shape[0]
+            mine = ids[at: at + per[b]]
+            at += per[b]
+            p["table"][b, : per[b]] = mine.to(torch.int32)
+            full = torch.zeros((per[b] * page, Hk, D), dtype=torch.float64)
+            full[:L] = x
+            s = _scales(full, block)
+            by_key = s.repeat_interleave(block, 0)
+            c = (full / by_key[..., None]).float().to(FP8)
+            codes.view(torch.uint8)[mine] = c.view(torch.uint8).view(per[b], page, Hk, D)
+            scales[mine] = s.float().view(per[b], page // block, Hk)
+            p[n].append((c.double() * by_key[..., None])[:L])
+            p[n + "_scale"].append(by_key[:L])
+        p[n + "c"], p[n + "s"] = codes, scales
+    return p
+
+
+def _expected(p, floor, *, causal=True, window=0):
+    """float64 O [T, Hq, D], LSE [Hq, T] and bounds on the errors of both.
+
+    A score is off by dz at the most: its fp32 sum (2^-21 of the sum of the products' sizes), q's second
+    term (2^-18 of the row's largest element, times the key's), and 2^-16 for the exponent's
+    sums, whose terms are below 2^8.  A weight is off by 2^-11 of itself in f16, by dz through its score
+    and by as much through the sum of all, or by `floor` of the row's largest weight times scale,
+    in which it counts a code; the output's rounding adds 2^-8 of O."""
+    T, Hq, D = p["q"].shape
+    Hk = p["k"][0].shape[1]
+    G = Hq // Hk
+    out, lse = torch.zeros(T, Hq, D, dtype=torch.float64), torch.full((Hq, T), -math.inf, dtype=torch.float64)
+    tol, lse_tol = torch.zeros_like(out), torch.zeros_like(lse)
+    for b, n in enumerate(p["q_lens"]):
+        L, a = p["kv_lens"][b], p["cu"][b]
+        pos, j = L - n + torch.arange(n), torch.arange(L)
+        seen = torch.ones((n, L), dtype=torch.bool)
+        if causal:
+            seen &= j <= pos[:, None]
+        if window:
+            seen &= j > pos[:, None] - window
+        for h in range(Hq):
+            q, k, v = p["q"][a: a + n, h].double(), p["k"][b][:, h // G], p["v"][b][:, h // G]
+            s = p["v_scale"][b][:, h // G]
+            z = (q @ k.T * D ** -0.5).masked_fill(~seen, -math.inf)
+            dz = D ** -0.5 * (2.0 ** -21 * (q.abs() @ k.abs().T) + 2.0 ** -18 * q.abs().amax(-1)[:, None] * k.abs().sum(-1))
+            dz = 2.0 ** -16 + dz.masked_fill(~seen, 0).amax(-1)
+            w = torch.softmax(z, -1)
+            o = w @ v
+            out[a: a + n, h], lse[h, a: a + n] = o, torch.logsumexp(z, -1)
+            codes = seen.double() @ (v.abs() / s[:, None])
+            tol[a: a + n, h] = (2.0 ** -8 * o.abs() + (2.0 ** -11 + 2 * dz)[:, None] * (w @ v.abs())
+                                + floor * (w * s).amax(-1)[:, None] * codes)
+            lse_tol[h, a: a + n] = dz + 2.0 ** -21 * lse[h, a: a + n].abs() + 2.0 ** -18
+    return out, lse, tol, lse_tol
+
+
+def _check(p, floor, what, calls=1, **mask):
+    out, lse, tol, lse_tol = _expected(p, floor, **mask)
+    for o, l in base._launch(p, calls=calls, **mask):
+        o, l = o.cpu().double(), l.cpu().double()
+        assert bool(torch.isfinite(o).all()) and bool(torch.isfinite(l).all()), f"{what}: not finite"
+        worst = ((l - lse).abs() / lse_tol).max().item()
+        assert worst <= 1, f"{what}: LSE {worst:.3g} times its bound"
+        # (1e-300: rows whose values are all zero)
+        worst = ((o - out).abs() / (tol + 1e-300)).max().item()
+        assert worst <= 1, f"{what}: O {worst:.3g} times its bound"
+    return out, lse
+
+
+def _normal(shape, seed):
+    return torch.randn(shape, generator=torch.Generator().manual_seed(seed), dtype=torch.float64)
+
+
+def _sink_problem(D, n, L, share, Hq=8, Hk=2, seed=1):
+    """Requests of n new tokens on L keys, one of which has about `share` of every row's weight: the first
+    key, one in the middle, the first of the last tile.  Its V is a twentieth of the others', which have a mean."""
+    at = [0, L // 2 + 5, (L - n) // 256 * 256 - 256]
+    # scores of the others are N(0, 1): their exponentials sum up to L e^(1/2)
+    z = math.log(share / (1 - share) * L) + 0.5
+    q = _normal((3 * n, Hq, D), seed)
+    q[..., 0] = z * D ** 0.5 / 16
+    keys, vals = [], []
+    for b, i in enumerate(at):
+        k, v = _normal((L, Hk, D), seed + 2 * b + 1), 0.5 + 0.25 * _normal((L, Hk, D), seed + 2 * b + 2)
+        k[..., 0] = 0
+        k[i] = 0
+        k[i, :, 0] = 16
+        v[i] /= 20
+        keys.append(k)
+        vals.append(v)
+    return _held(q.to(torch.bfloat16), keys, vals, [n] * 3, page=256)
+
+
+@pytest.mark.parametrize("share", [0.5, 0.9, 0.99])
+@pytest.mark.parametrize("L", [8192, 32768])
+@pytest.mark.parametrize("n", [1, 2, 3])
+@pytest.mark.parametrize("D", [64, 128])
+def test_small_weights_beside_a_large_one(D, n, L, share):
+    # tokens of 4, 8 and 12 rows a KV head
+    p = _sink_problem(D, n, L, share)
+    out, lse = _check(p, FEW, f"{share} on one of {L} keys")
+    for b in range(3):  # and inside the bound that weights in bf16 have
+        a, z = b * n, (b + 1) * n
+        want, _, tol = ref.chunk_rows(p["q"][a:z], p["k"][b], p["v"][b], None)
+        assert torch.allclose(want, out[a:z], rtol=1e-12, atol=1e-12)
+        got = base._launch(p)[0][0][a:z].cpu().double()
+        assert bool(((got - want).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_small_weights_beside_one_that_is_nearly_all(D):
+    # the others together have 2^-14 of the weight, each 2^-27, and the large one's V is 0
+    p = _sink_problem(D, 1, 8192, 1 - 2.0 ** -14)
+    for b, i in enumerate([0, 8192 // 2 + 5, 8191 // 256 * 256 - 256]):
+        page, row = int(p["table"][b, i // 256]), i % 256
+        p["vc"].view(torch.uint8)[page, row] = 0
+        p["v"][b][i] = 0
+    _check(p, FEW, "nearly all")
+
+
+@pytest.mark.parametrize("share", [0.5, 0.99])
+@pytest.mark.parametrize("D", [64, 128])
+def test_small_weights_beside_a_large_one_in_row_blocks(D, share):
+    _check(_sink_problem(D, 40, 8192, share), BLOCKS, f"{share} in row blocks")
