@@ -1129,7 +1129,7 @@ cudaError_t launch_mod(const ChunkMaps &maps, ChunkParams &p, cudaStream_t strea
         e = launch(!few_first);
     if (e != cudaSuccess)
         return e;
-    return launch_after(chunk_join_kernel<D>, dim3(p.n_cta, 2, kJoinSplit), kJoinThreads, 0, stream, p);
+    return launch_after(chunk_join_kernel<D, F8>, dim3(p.n_cta, 2, kJoinSplit), kJoinThreads, 0, stream, p);
 }
 
 } // namespace

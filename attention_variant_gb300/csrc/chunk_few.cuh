@@ -118,6 +118,12 @@ __device__ __forceinline__ FewTiles few_tiles(const FewItem &it, int t)
     return f;
 }
 
+// A cache in 8 bits: maxima of z - m of each softmax warp, and ref - m, each warp's own.
+struct FewSums {
+    float most[2][4][kFewRows];
+    alignas(16) float gap[2][4][kFewRows];
+};
+
 template <int D, bool F8>
 struct __align__(1024) FewSmem {
     using C = FewCfg<D, F8>;
@@ -135,8 +141,9 @@ struct __align__(1024) FewSmem {
     FewItem info[kInfo];
     float red[2][4][kFewRows];       // maxima or sums of each softmax warp
     uint32_t rows[2][2][4];          // by tile parity, of each softmax warp: see few_softmax
-    uint32_t large[2][4];            // 8 bits: of tiles in turn, rows that ask for a reference
+    uint32_t large[2][4];            // 8 bits: of tiles in turn, whether a row may ask for a reference
     std::conditional_t<F8, ScaleRing, char> scales;
+    std::conditional_t<F8, FewSums, char> sums;
     uint32_t tmem_base;
     uint32_t abort_flag;
 };
@@ -1054,10 +1061,14 @@ __device__ void few_softmax(const FewCtx<D, false> &cx, const ChunkParams &p, in
 // ------------------------------------------------------------------ softmax, 8 bits
 //
 // A thread has keys r (and, of a tile of 256, 128 + r).  One reference a row, ref, for the
-// weights times V's scale: P = 2^(kFewTop + z + log2 s - ref); the row's sum takes P / (s 2^kFewTop).
-// The reference makes the largest P of a tile 2^kFewTop when it is set, and is set again where
-// one would pass 2^kFewMost: until then the slot's warps only agree, once a tile, that
-// none does.
+// weights times V's scale, P = 2^(z + lv - ref) with lv = kFewTop + log2 s, and one for the row's
+// sum, of 2^(z - m) with m = ref - gap: scales may be 2^200 apart (a block of zeros has 2^-100), so
+// neither exponential can be had from the other.  The references make the largest P of a tile
+// 2^kFewTop and the largest weight 1 when they are set, and are set again where one would pass
+// 2^kFewMost or 2^kFewSumMost: until then the slot's warps only agree, once a tile, that none does.
+// (The second exponentials take 64 tokens on 512 to 8192 keys from 68 to 70 us.  A path of its own for
+// scales far apart took 73, two copies of the code for P 79: what this loop costs is its instructions'
+// fetch.)
 //
 // P is rounded to f16, 11 bits down to 2^-26 of the row's largest and steps of 2^-36 of it
 // below, and goes as three e5m2 terms of 3 bits and a sign each, 16 times apart, which hold
@@ -1065,6 +1076,7 @@ __device__ void few_softmax(const FewCtx<D, false> &cx, const ChunkParams &p, in
 // weight on one key lost the others': relative errors of 0.1 to 0.5 at 8192 to 32768 keys.)
 
 constexpr float kFewTop = 12.f, kFewMost = 14.8f; // rounded to e5m2, 2^14.8 times 2^-3 times 16 stays in range
+constexpr float kFewSumMost = 60.f;
 constexpr int kFewTerms = 3;
 
 struct FewState8 {
@@ -1091,18 +1103,23 @@ __device__ __forceinline__ void split_p(const float (&e)[4], uint32_t &t0, uint3
     t2 = __byte_perm(rounded(rest(a, ra)), rounded(rest(b, rb)), 0x7531);
 }
 
-// A key's row of P and its part of the sums: d = log2 of P.
+// A key's row of P and its part of the sums: d = log2 of P; d - lv + gap that of the weight.
 template <int R>
-__device__ __forceinline__ void few_p8(const float (&d)[R], float inv_v, float (&sum)[R], uint32_t (&p)[kFewTerms][R / 4])
+__device__ __forceinline__ void few_p8(const float (&d)[R], float lv, uint32_t gap, float (&sum)[R],
+                                       uint32_t (&p)[kFewTerms][R / 4])
 {
 #pragma unroll
     for (int n = 0; n < R; n += 4) {
-        float e[4];
+        float e[4], z[4];
+        ptx::load_shared_v4(gap + 4 * n, z);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 4; i += 2) {
+            ptx::add2(z[i], z[i + 1], -lv, -lv);
+            ptx::add2(z[i], z[i + 1], d[n + i], d[n + i + 1]);
             e[i] = ptx::ex2(d[n + i]);
-        ptx::fma2(sum[n], sum[n + 1], e[0], e[1], inv_v, inv_v, sum[n], sum[n + 1]);
-        ptx::fma2(sum[n + 2], sum[n + 3], e[2], e[3], inv_v, inv_v, sum[n + 2], sum[n + 3]);
+            e[i + 1] = ptx::ex2(d[n + i + 1]);
+            ptx::add2(sum[n + i], sum[n + i + 1], ptx::ex2(z[i]), ptx::ex2(z[i + 1]));
+        }
         split_p(e, p[0][n / 4], p[1][n / 4], p[2][n / 4]);
     }
 }
@@ -1151,8 +1168,14 @@ __device__ __forceinline__ bool few_item_fp8(const FewCtx<D, true> &cx, const Ch
                                 (MOD == MOD_NONE ? p.qk_log2 : 1.f)
                           : 0.f;
     }
-    const uint32_t row_bits = (1u << rows) - 1;
-    uint32_t unset = row_bits; // rows without a reference, which counts as 0
+    uint32_t unset = (1u << rows) - 1; // rows without references, which count as 0
+    float gap_most = 0.f;      // the largest gap
+    volatile float *const gap = sm.sums.gap[t][wq];
+    const uint32_t gap_at = ptx::smem_u32(sm.sums.gap[t][wq]);
+    __syncwarp();
+    if (lane < R)
+        gap[lane] = 0.f;
+    __syncwarp();
     for (int kk = 0; kk < n_mine; ++kk) {
         if (!warp_wait(bar(sm.s_full[t]), ct.s & 1, cx.wc, W_S_FULL))
             return false;
@@ -1164,7 +1187,7 @@ __device__ __forceinline__ bool few_item_fp8(const FewCtx<D, true> &cx, const Ch
         ++ct.tiles;
         ptx::tc_fence_after();
         uint32_t raw[kSub][R];
-        float key_k[kSub], log_v[kSub], inv_v[kSub];
+        float key_k[kSub], log_v[kSub];
 #pragma unroll
         for (int sub = 0; sub < kSub; ++sub) {
             if constexpr (R == 4)
@@ -1184,11 +1207,9 @@ __device__ __forceinline__ bool few_item_fp8(const FewCtx<D, true> &cx, const Ch
         ptx::mbar_arrive(bar(sm.s_free[t]));
         // ---- log2 of P, relative to the references as they are
         float d[kSub][R];
-        bool more = false;
 #pragma unroll
         for (int sub = 0; sub < kSub; ++sub) {
             log_v[sub] = fmaxf(ptx::lg2(log_v[sub]), kLeastLog) + kFewTop;
-            inv_v[sub] = ptx::ex2(-log_v[sub]);
             float (&x)[R] = d[sub];
             if constexpr (MOD == MOD_NONE) {
 #pragma unroll
@@ -1207,81 +1228,105 @@ __device__ __forceinline__ bool few_item_fp8(const FewCtx<D, true> &cx, const Ch
                 for (int n = 0; n < R; ++n)
                     x[n] += log_v[sub] - ref[n];
             }
-            if (!(j0 >= full_lo && j0 + kBN <= full_hi)) {
-                const int key = j0 + sub * 128 + r;
+        }
+        if (!(j0 >= full_lo && j0 + kBN <= full_hi)) {
 #pragma unroll
-                for (int n = 0; n < R; ++n) {
-                    int lo, hi;
-                    const int pos = pos0 + fast_div(n, p.div_g);
-                    key_range(p, inf.L, pos, pos, lo, hi);
+            for (int n = 0; n < R; ++n) {
+                int lo, hi;
+                const int pos = pos0 + fast_div(n, p.div_g);
+                key_range(p, inf.L, pos, pos, lo, hi);
+#pragma unroll
+                for (int sub = 0; sub < kSub; ++sub) {
+                    const int key = j0 + sub * 128 + r;
                     if (key < lo || key >= hi)
-                        x[n] = kNegInf;
+                        d[sub][n] = kNegInf;
                 }
             }
-            float most = x[0];
+        }
+        // does a key ask for a new reference? (at the most)
+        bool more = false;
+#pragma unroll
+        for (int sub = 0; sub < kSub; ++sub) {
+            float most = d[sub][0];
 #pragma unroll
             for (int n = 1; n < R; ++n)
-                most = fmaxf(most, x[n]);
-            more |= most > (unset ? kNegInf : kFewMost);
+                most = fmaxf(most, d[sub][n]);
+            more |= most > (unset ? kNegInf : kFewMost) || most - log_v[sub] + gap_most > kFewSumMost;
         }
-        if (__any_sync(0xffffffffu, more)) { // bit n: a key of row n asks for a new reference
-            uint32_t bits = 0;
-#pragma unroll
-            for (int sub = 0; sub < kSub; ++sub)
-#pragma unroll
-                for (int n = 0; n < R; ++n)
-                    bits |= d[sub][n] > (unset >> n & 1u ? kNegInf : kFewMost) ? 1u << n : 0u;
-            bits = __reduce_or_sync(0xffffffffu, bits);
-            if (lane == 0)
-                atomicOr(&sm.large[t][(ct.tiles - 1) & 3], bits);
-            __syncwarp();
-        }
+        if (__any_sync(0xffffffffu, more) && lane == 0)
+            *flags = 1;
         ptx::mbar_arrive(b_group);
-        // ---- P, as if no row did
+        // ---- P, as if no row did, and again if one does
         float sum[R];
         uint32_t pt[kSub][kFewTerms][R / 4];
+#pragma unroll 1
+        for (int pass = 0;; ++pass) {
 #pragma unroll
-        for (int n = 0; n < R; ++n)
-            sum[n] = l[n];
+            for (int n = 0; n < R; ++n)
+                sum[n] = l[n];
 #pragma unroll
-        for (int sub = 0; sub < kSub; ++sub)
-            few_p8<R>(d[sub], inv_v[sub], sum, pt[sub]);
-        if (!group_wait())
-            return false;
-        const uint32_t large = *flags & row_bits;
-        // the word of the next tile but one: every warp has read what it held
-        if (r == 0)
-            sm.large[t][(ct.tiles + 1) & 3] = 0;
-        if (large || inf.n_parts == 0) {
-            // the largest of each row that asked, over the slot's warps
+            for (int sub = 0; sub < kSub; ++sub)
+                few_p8<R>(d[sub], log_v[sub], gap_at, sum, pt[sub]);
+            if (pass)
+                break;
+            if (!group_wait())
+                return false;
+            const bool large = *flags;
+            // the word of the next tile but one: every warp has read what it held
+            if (r == 0)
+                sm.large[t][(ct.tiles + 1) & 3] = 0;
+            if (!(large || inf.n_parts == 0))
+                break;
+            // the largest of each row, over the slot's warps
 #pragma unroll
             for (int n = 0; n < R; ++n) {
                 float top = d[0][n];
                 if constexpr (kSub == 2)
                     top = fmaxf(top, d[1][n]);
                 const int mx = __reduce_max_sync(0xffffffffu, ordered(top));
-                if (lane == n)
+                top = d[0][n] - log_v[0];
+                if constexpr (kSub == 2)
+                    top = fmaxf(top, d[1][n] - log_v[1]);
+                const int mz = __reduce_max_sync(0xffffffffu, ordered(top));
+                if (lane == n) {
                     sm.red[t][wq][n] = unordered(mx);
+                    sm.sums.most[t][wq][n] = unordered(mz);
+                }
             }
             ptx::mbar_arrive(b_group);
             if (!group_wait())
                 return false;
+            // a row per lane: how far its references move
+            auto over_warps = [&](const volatile float *m) {
+                return fmaxf(fmaxf(m[0], m[kFewRows]), fmaxf(m[2 * kFewRows], m[3 * kFewRows]));
+            };
+            const int row = lane & (R - 1);
+            const float own_gap = gap[row];
+            float row_up = over_warps(&sm.red[t][0][row]) - kFewTop, row_up_m = over_warps(&sm.sums.most[t][0][row]) + own_gap;
+            const bool first = unset >> row & 1u;
+            const bool moves = row < rows && (first ? row_up > kNegInf : row_up > kFewMost - kFewTop || row_up_m > kFewSumMost);
+            // (one that is set may move for the other's sake)
+            row_up = !moves ? 0.f : first ? row_up : fmaxf(row_up, 0.f);
+            row_up_m = !moves ? 0.f : first ? row_up_m : fmaxf(row_up_m, 0.f);
+            const float row_beta = moves && first ? 0.f : ptx::ex2(-row_up), row_beta_l = moves && first ? 0.f : ptx::ex2(-row_up_m);
+            const float row_gap = own_gap + row_up - row_up_m;
+            __syncwarp();
+            if (lane < R)
+                gap[lane] = row_gap;
+            unset &= ~__ballot_sync(0xffffffffu, moves);
+            gap_most = unordered(__reduce_max_sync(0xffffffffu, ordered(row < rows && !(unset >> row & 1u) ? row_gap : 0.f)));
+            __syncwarp();
             float beta[R];
 #pragma unroll
             for (int n = 0; n < R; ++n) {
-                beta[n] = 1.f;
-                if (large >> n & 1u) {
-                    const volatile float *red = &sm.red[t][0][n];
-                    const float up = fmaxf(fmaxf(red[0], red[kFewRows]), fmaxf(red[2 * kFewRows], red[3 * kFewRows])) - kFewTop;
-                    beta[n] = unset >> n & 1u ? 0.f : ptx::ex2(-up);
-                    ref[n] += up;
+                const float up = __shfl_sync(0xffffffffu, row_up, n);
+                beta[n] = __shfl_sync(0xffffffffu, row_beta, n);
+                ref[n] += up;
 #pragma unroll
-                    for (int sub = 0; sub < kSub; ++sub)
-                        d[sub][n] -= up;
-                }
-                sum[n] = l[n] * beta[n];
+                for (int sub = 0; sub < kSub; ++sub)
+                    d[sub][n] -= up;
+                l[n] *= __shfl_sync(0xffffffffu, row_beta_l, n);
             }
-            unset &= ~large;
             if (kk > 0) {
                 const uint32_t last = ct.tiles - 2; // the tile before, its product done
                 if (!warp_wait(bar(sm.pv_done[t][last % C::kPBufs]), (last / C::kPBufs) & 1, cx.wc, W_O_FULL))
@@ -1300,9 +1345,6 @@ __device__ __forceinline__ bool few_item_fp8(const FewCtx<D, true> &cx, const Ch
                 }
                 ptx::tmem_wait_st();
             }
-#pragma unroll
-            for (int sub = 0; sub < kSub; ++sub)
-                few_p8<R>(d[sub], inv_v[sub], sum, pt[sub]);
         }
 #pragma unroll
         for (int n = 0; n < R; ++n)
@@ -1369,24 +1411,30 @@ __device__ __forceinline__ bool few_item_fp8(const FewCtx<D, true> &cx, const Ch
                 o[c % R] = fmaf(__uint_as_float(raw[c % 16]), kTerm[c / R], o[c % R]);
         }
     }
+    // lane i's row, i mod R: m, and log2 of O's unit relative to 2^m
+    const int row = lane & (R - 1);
+    const float unit = gap[row];
+    float m = ref[0];
 #pragma unroll
-    for (int n = 0; n < R; ++n)
-        if (unset >> n & 1u)
-            ref[n] = kNegInf; // no key
+    for (int n = 1; n < R; ++n)
+        m = row == n ? ref[n] : m;
+    m = unset >> row & 1u ? kNegInf : m - unit; // or no key
     // lane = dimension; at D = 64 the upper 64 lanes repeat the lower ones and
     // take the odd rows
     const int dim = D == 128 ? r : r & 63;
     if (inf.n_parts > 1) {
         float *mine = partial<D>(p, inf.cta, inf.mine, t), *sums = mine + kFewRows * 128;
 #pragma unroll
-        for (int n = 0; n < R; ++n) {
+        for (int n = 0; n < R; ++n)
             if (n < rows && (D == 128 || (n & 1) == r >> 6))
                 mine[n * 128 + dim] = o[n];
-            if (r == n)
-                sums[n] = ref[n];
-        }
-        if (lane < R)
+        if (lane < R) {
             sums[kFewRows + wq * kFewRows + lane] = l[0];
+            if (wq == 0) {
+                sums[lane] = m;
+                sums[5 * kFewRows + lane] = unit;
+            }
+        }
         return true;
     }
     auto group_sync = [&]() {
@@ -1400,9 +1448,9 @@ __device__ __forceinline__ bool few_item_fp8(const FewCtx<D, true> &cx, const Ch
     if (!group_sync())
         return false;
     // a row's sum per lane, so that the reciprocals and logarithms are taken at once
-    const volatile float *red = sm.red[t][0] + (lane & (R - 1));
+    const volatile float *red = sm.red[t][0] + row;
     const float sum = red[0] + red[kFewRows] + red[2 * kFewRows] + red[3 * kFewRows];
-    const float inv = sum == 0.f ? 0.f : ptx::rcp_approx(sum);
+    const float inv = few_norm(sum, unit);
 #pragma unroll
     for (int n = 0; n < R; ++n) {
         const float norm = __shfl_sync(0xffffffffu, inv, n);
@@ -1413,12 +1461,8 @@ __device__ __forceinline__ bool few_item_fp8(const FewCtx<D, true> &cx, const Ch
         p.out[tok * p.o_st + head * p.o_sh + dim] = __float2bfloat16(o[n] * norm);
     }
     if (r < rows) {
-        float top = ref[0];
-#pragma unroll
-        for (int n = 1; n < R; ++n)
-            top = r == n ? ref[n] : top;
         const int s = fast_div(r, p.div_g);
-        join_lse(p, inf.t0 + s, (inf.kvh + t) * p.G + r - s * p.G, top, sum);
+        join_lse(p, inf.t0 + s, (inf.kvh + t) * p.G + r - s * p.G, m, sum);
     }
     return true;
 }

@@ -195,8 +195,8 @@ __device__ __forceinline__ PartRange part_range(int64_t x0, int n_tiles, int til
 //   JOIN_PAIR   the slot's own rows: [D columns][128 rows]
 //   JOIN_HALF   one row block, the slot's half of the columns: [D / 2][128]
 //               then, for both, m, l and the sum of the rounded P: [3][128]
-//   JOIN_FEW    [16 rows][128 dimensions], m [16], then each warp's sums of l:
-//               [4 warps][16]
+//   JOIN_FEW    [16 rows][128 dimensions], m [16], each warp's sums of l: [4 warps][16],
+//               in 8 bits the logarithm of O's unit relative to 2^m [16]
 enum : int { JOIN_PAIR = 0, JOIN_HALF = 1, JOIN_FEW = 2 };
 
 // Floats of one slot's buffer, and the place of a slot's buffer of a CTA
@@ -502,6 +502,15 @@ __device__ __forceinline__ void join_lse(const ChunkParams &p, int64_t tok, int6
         p.lse[head * p.l_sh + tok] = l == 0.f ? kNegInf : (m + log2f(l)) * kLn2;
 }
 
+// 2^unit / sum, in range wherever that is (0 for a sum of nothing).
+__device__ __forceinline__ float few_norm(float sum, float unit)
+{
+    const uint32_t bits = __float_as_uint(sum);
+    const float k = static_cast<float>(static_cast<int>(bits >> 23) - 127); // sum = 2^k times one in [1, 2)
+    const float inv = ptx::ex2(unit - k) * ptx::rcp_approx(__uint_as_float((bits & 0x7fffffu) | 0x3f800000u));
+    return sum == 0.f ? 0.f : sum < -kNegInf ? inv : __uint_as_float(0x7fffffffu);
+}
+
 // Row-block layouts: a row per thread, N / kJoinSplit columns.
 template <int N, int D>
 __device__ __forceinline__ void join_block(const ChunkParams &p, const ChunkJoin &jn, int cta, int slot, int z)
@@ -547,8 +556,9 @@ __device__ __forceinline__ void join_block(const ChunkParams &p, const ChunkJoin
 }
 
 // Few rows: a dimension per thread (at D = 64 half the threads a row), a part
-// per lane while the weights are made.
-template <int D>
+// per lane while the weights are made.  In 8 bits O has weights of its own: those of l
+// and of O may be 2^200 apart.
+template <int D, bool F8>
 __device__ __forceinline__ void join_few(const ChunkParams &p, const ChunkJoin &jn, int cta, int slot, int z)
 {
     constexpr int R = kFewRows, kDepth = 16, kPerBlock = 128 / D;
@@ -556,7 +566,7 @@ __device__ __forceinline__ void join_few(const ChunkParams &p, const ChunkJoin &
     auto part = [&](int q) { return partial<D>(p, cta + q, q == 0 ? 1 : 0, slot); };
     for (int n = z * kPerBlock + static_cast<int>(threadIdx.x) / D; n < jn.rows[slot]; n += kJoinSplit * kPerBlock) {
         const int few = n_parts <= kDepth; // everything is loaded at once
-        float M = kNegInf, sums[4] = {0.f, 0.f, 0.f, 0.f}, l = 0.f, o = 0.f;
+        float M = kNegInf, U = kNegInf, sums[4] = {0.f, 0.f, 0.f, 0.f}, l = 0.f, o = 0.f;
         if (few) {
             float v[kDepth];
             if (lane < n_parts) {
@@ -565,30 +575,44 @@ __device__ __forceinline__ void join_few(const ChunkParams &p, const ChunkJoin &
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     sums[k] = s[R * (k + 1)];
+                if constexpr (F8)
+                    U = M + s[R * 5];
             }
-            const float mine = M;
+            const float mine = M, mine_o = U;
 #pragma unroll
             for (int i = 0; i < kDepth; ++i)
                 v[i] = i < n_parts ? part(i)[n * 128 + dim] : 0.f;
 #pragma unroll
-            for (int d = 16; d; d >>= 1)
+            for (int d = 16; d; d >>= 1) {
                 M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-            const float w = lane < n_parts ? ptx::ex2(mine - (M == kNegInf ? 0.f : M)) : 0.f;
+                if constexpr (F8)
+                    U = fmaxf(U, __shfl_xor_sync(0xffffffffu, U, d));
+            }
+            float w = lane < n_parts ? ptx::ex2(mine - (M == kNegInf ? 0.f : M)) : 0.f;
             l = (((0.f + sums[0]) + sums[1]) + sums[2] + sums[3]) * w;
 #pragma unroll
             for (int d = 16; d; d >>= 1)
                 l += __shfl_xor_sync(0xffffffffu, l, d);
+            if constexpr (F8)
+                w = lane < n_parts ? ptx::ex2(mine_o - (U == kNegInf ? 0.f : U)) : 0.f;
 #pragma unroll
             for (int i = 0; i < kDepth; ++i)
                 o = fmaf(__shfl_sync(0xffffffffu, w, i), v[i], o);
         } else {
-            for (int q = lane; q < n_parts; q += 32)
-                M = fmaxf(M, part(q)[R * 128 + n]);
+            for (int q = lane; q < n_parts; q += 32) {
+                const float *s = part(q) + R * 128 + n;
+                M = fmaxf(M, s[0]);
+                if constexpr (F8)
+                    U = fmaxf(U, s[0] + s[R * 5]);
+            }
 #pragma unroll
-            for (int d = 16; d; d >>= 1)
+            for (int d = 16; d; d >>= 1) {
                 M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+                if constexpr (F8)
+                    U = fmaxf(U, __shfl_xor_sync(0xffffffffu, U, d));
+            }
         }
-        const float M0 = M == kNegInf ? 0.f : M;
+        const float M0 = M == kNegInf ? 0.f : M, U0 = U == kNegInf ? 0.f : U;
         for (int q0 = 0; q0 < (few ? 0 : n_parts); q0 += 32) {
             float w = 0.f, a = 0.f;
             if (q0 + lane < n_parts) {
@@ -598,6 +622,8 @@ __device__ __forceinline__ void join_few(const ChunkParams &p, const ChunkJoin &
                 for (int k = 1; k <= 4; ++k)
                     a += s[R * k];
                 a *= w;
+                if constexpr (F8)
+                    w = ptx::ex2(s[0] + s[R * 5] - U0);
             }
 #pragma unroll
             for (int d = 16; d; d >>= 1)
@@ -615,13 +641,16 @@ __device__ __forceinline__ void join_few(const ChunkParams &p, const ChunkJoin &
         }
         const int s = fast_div(n, p.div_g);
         const int64_t tok = jn.t0[slot] + s, head = (jn.kvh + slot) * p.G + n - s * p.G;
-        join_write(p, tok, head, dim, o, l);
+        if constexpr (F8)
+            p.out[tok * p.o_st + head * p.o_sh + dim] = __float2bfloat16(o * few_norm(l, U0 - M0));
+        else
+            join_write(p, tok, head, dim, o, l);
         if (dim == 0)
             join_lse(p, tok, head, M, l);
     }
 }
 
-template <int D>
+template <int D, bool F8>
 __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const __grid_constant__ ChunkParams p)
 {
     ptx::wait_dependency();
@@ -632,7 +661,7 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const __grid_c
     if (jn.n_parts < 2)
         return;
     if (jn.mode == JOIN_FEW)
-        join_few<D>(p, jn, cta, slot, z);
+        join_few<D, F8>(p, jn, cta, slot, z);
     else if (jn.mode == JOIN_PAIR)
         join_block<D, D>(p, jn, cta, slot, z);
     else

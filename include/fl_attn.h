@@ -634,8 +634,8 @@ fl_status fl_kv_read_fp8(const fl_tensor *k_cache, const fl_tensor *v_cache, con
  * of keys that no row of their request sees may be anything; those of the others must not
  * be NaN.  Weights times scales of V are held in f16 relative to the largest of their row (up to 16
  * rows of a request and KV head: 11 bits down to 2^-26 of it, steps of 2^-36 of it below) or of their
- * item (more rows: 11 bits down to 2^-20), and scales of V that are 2^-60 of another's in the
- * request count as that.  The workspace is larger (q in two e4m3
+ * item (more rows: 11 bits down to 2^-20, and scales of V that are 2^-60 of another's count as that).
+ * The workspace is larger (q in two e4m3
  * terms, which hold bf16 exactly down to 2^-10 of a row's largest element and to 2^-18 of it
  * below): ask fl_attn_chunk_fp8_workspace_size.
  */

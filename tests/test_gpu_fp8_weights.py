@@ -1,5 +1,5 @@
-"""Weights of very different sizes in attention over the 8-bit KV cache: one key that holds
-most of a row's weight.
+"""Weights of very different sizes in attention over the 8-bit KV cache: one key that holds most of a
+row's weight, blocks of V whose scales are far apart, loud keys that a row does not see.
 
 A result is bounded relative to what its own row sees, sum_j w_j |v_j|: see _expected."""
 from __future__ import annotations
@@ -165,3 +165,91 @@ def test_small_weights_beside_one_that_is_nearly_all(D):
 @pytest.mark.parametrize("D", [64, 128])
 def test_small_weights_beside_a_large_one_in_row_blocks(D, share):
     _check(_sink_problem(D, 40, 8192, share), BLOCKS, f"{share} in row blocks")
+
+
+# ------------------------------------------------------------------ scales of V far apart
+
+
+def _zero_blocks(D, n, L, log_s, Hq=8, Hk=2):
+    """Requests whose V is zero in every other 48 keys (scale 2^-100) and has scales near 2^log_s between;
+    the last request begins with zeros, the others do not."""
+    q = _normal((3 * n, Hq, D), 3).to(torch.bfloat16)
+    keys = [_normal((x, Hk, D), 4 + b) for b, x in enumerate((L, L + 33, n + 7))]
+    vals = []
+    for b, k in enumerate(keys):
+        v = _normal(k.shape, 8 + b) * 2.0 ** (log_s + 7)
+        j = torch.arange(k.shape[0]) // 48
+        v[(j % 2 == (1 if b < 2 else 0)) & (torch.arange(k.shape[0]) < k.shape[0] - 1)] = 0
+        vals.append(v)
+    return _held(q, keys, vals, [n] * 3, page=16)
+
+
+@pytest.mark.parametrize("log_s", [-8, 20, 30, 60, 99])
+@pytest.mark.parametrize("n,L", [(1, 200), (1, 9000), (2, 3000), (4, 700), (40, 400), (70, 1500)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_blocks_of_zeros_beside_loud_ones(D, n, L, log_s):
+    _check(_zero_blocks(D, n, L, log_s), FEW if 4 * n <= 16 else BLOCKS, f"zeros beside 2^{log_s}", calls=2)
+
+
+def _loud(D, n, L, at, gain, z=None, Hq=8, Hk=2):
+    """Two requests of n new tokens on L keys, the V of keys `at` 2^gain times the others'; with z, those keys' scores are z."""
+    q = _normal((2 * n, Hq, D), 5)
+    keys, vals = [_normal((L, Hk, D), 6 + b) for b in (0, 1)], [_normal((L, Hk, D), 9 + b) for b in (0, 1)]
+    if z is not None:
+        q[..., 0] = 4
+    for k, v in zip(keys, vals):
+        v[at] *= 2.0 ** gain
+        if z is not None:
+            k[..., 0] = 0
+            k[at] = 0
+            k[at, :, 0] = z * D ** 0.5 / 4
+    return _held(q.to(torch.bfloat16), keys, vals, [n] * 2, page=32)
+
+
+@pytest.mark.parametrize("gain", [20, 35, 60, 100])
+@pytest.mark.parametrize("n,L", [(3, 290), (4, 4994)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_loud_values_that_come_later(D, n, L, gain):
+    # the last 2 tokens' V, a block of its own, is 2^gain louder, which the rows before do not see
+    _check(_loud(D, n, L, slice(L - 2, L), gain), FEW if 4 * n <= 16 else BLOCKS, f"2^{gain} later", calls=2)
+
+
+@pytest.mark.parametrize("gain,z", [(40, -60.0), (60, -60.0), (90, -90.0), (-90, 60.0), (60, -20.0), (-60, 20.0)])
+@pytest.mark.parametrize("n,L", [(1, 300), (1, 6000), (4, 2000)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_loud_values_of_little_weight(D, n, L, gain, z):
+    # a block whose scale and weights differ by 2^90 and more from the others', in either order
+    p = _loud(D, n, L, slice(32, 48), gain, z)
+    _check(p, FEW if 4 * n <= 16 else BLOCKS, f"2^{gain} at {z}", calls=2)
+
+
+@pytest.mark.parametrize("log_s", [-100, 100])
+@pytest.mark.parametrize("n,L", [(1, 20000), (4, 9000), (40, 16000), (100, 9000)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_scales_at_the_ends_of_their_range(D, n, L, log_s):
+    # many keys of the largest or smallest scale; scores rise by 5 after the first tiles, less than
+    # what moves a reference, so that sums of weights reach 2^20
+    q, k = _normal((n, 8, D), 1), _normal((L, 2, D), 2) / 8
+    q[..., 0], k[..., 0] = 4, 0
+    k[:300, :, 0] = -5 * D ** 0.5 / 4
+    v = _normal((L, 2, D), 3).sign() * 400 * 2.0 ** log_s
+    v[..., : D // 2] = 448 * 2.0 ** log_s
+    _check(_held(q.to(torch.bfloat16), [k], [v], [n], page=256), FEW if 4 * n <= 16 else BLOCKS, f"scales of 2^{log_s}")
+
+
+# ------------------------------------------------------------------ rows that are not numbers
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_rows_that_are_not_finite_have_no_lse(D):
+    # an LSE of NaN for a row of q that holds an infinity or a NaN, in both kinds of rows,
+    # of one part and of several
+    p = base._problem([1, 2, 50, 1], [300, 40, 90, 9000], 8, 2, D, 32, 16, seed=3)
+    q = p["q"]
+    q[1, 3, 5], q[2, 0, 0], q[10, 7, 9], q[30, 2, 1], q[53, 4, 0] = math.inf, math.nan, -math.inf, math.nan, math.inf
+    bad = torch.zeros((8, p["T"]), dtype=torch.bool)
+    for t, h in ((1, 3), (2, 0), (10, 7), (30, 2), (53, 4)):
+        bad[h, t] = True
+    out, lse = base._launch(p)[0]
+    assert torch.equal(torch.isnan(lse.cpu()), bad)
+    assert torch.equal(torch.isnan(out.cpu()).any(-1), bad.T) and torch.equal(torch.isnan(out.cpu()).all(-1), bad.T)
