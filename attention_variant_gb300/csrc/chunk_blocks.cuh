@@ -54,7 +54,7 @@
 // A cache in 8 bits: S as in chunk_few.cuh, K's codes against Q's two terms.  For
 // O, warps 2 and 3 turn V's codes into f16 (exact) in shared memory while the
 // softmax of the next tile runs, and P is f16 with V's scale in its exponent, one for 16
-// keys, relative to the largest of the item (softmax_compute_p_scaled).  V's codes straight into
+// keys, relative to the largest product of weight and scale of the row (softmax_compute_p_scaled).  V's codes straight into
 // the product want P in e4m3, in two terms for bf16's accuracy: twice the rows of the 128 an MMA
 // has.  Converted by the softmax's own warps the long prompt above took 1.6 times as long.
 // It takes 584 us, 824 TFLOP/s: the conversion and the factors are 15% more instructions, and
@@ -366,7 +366,6 @@ __device__ void s_role(const KernelCtx<D, F8> &cx)
         ok = warp_wait(bar(sm.q_full[ring]), (n >> 1) & 1, cx.wc, W_Q_FULL);
         if (!ok)
             break;
-        float top[2] = {kLeastLog, kLeastLog}; // 8 bits: the largest scale of V in each slot's tiles so far
         for (int j = u_lo; j < u_hi; ++j, ++idx) {
             const uint32_t stage = idx % kStages;
             ok = warp_wait(bar(sm.kv_full[stage]), (idx / kStages) & 1, cx.wc, W_KV_FULL);
@@ -407,7 +406,7 @@ __device__ void s_role(const KernelCtx<D, F8> &cx)
                     continue;
                 // four places: with the last tile's S the softmax was done with the one before that
                 if constexpr (F8)
-                    tile_factors(sm.factors[t][issued[t] & 3], scale_k, scale_v, top[t]);
+                    tile_factors(sm.factors[t][issued[t] & 3], scale_k, scale_v);
                 if (issued[t] > 0) {
                     // the softmax has copied the slot's previous S out of TMEM
                     ok = warp_wait(bar(sm.s_free[t]), (issued[t] - 1) & 1, cx.wc, W_S_FULL);
@@ -598,14 +597,14 @@ __device__ __forceinline__ RowOut<D> row_out(const ChunkParams &p, const Item &i
     return w;
 }
 
-// Epilogue of a pair: the slot's own rows, every column.  An active warp.
+// Epilogue of a pair: the slot's own rows, every column.  An active warp.  (In 8 bits `unit` is O's
+// relative to 2^m_ref, and a row of q that is not finite, whose sum is NaN, comes out as NaN.)
 template <int D, bool F8>
 __device__ __forceinline__ void write_slot(const ChunkParams &p, const Item &inf, int t, int r, uint32_t tO,
                                            const RowState &st, bool any, float unit)
 {
     const bool live = r < inf.rows[t], whole = inf.n_parts == 1;
     const RowOut<D> w = row_out<D>(p, inf, t, r);
-    // (in 8 bits a row of q that is not finite, whose sum is NaN, comes out as NaN)
     const float inv = F8 ? (st.l_round == 0.f ? 0.f : ptx::rcp_approx(st.l_round) * unit) : row_inv_norm(st);
     // an accumulator without a tile, or a row without a key, is not read
     const bool keys = any && (F8 ? !(st.l_round == 0.f) : st.m_ref != kNegInf);
@@ -769,7 +768,7 @@ __device__ void softmax_role(const KernelCtx<D, F8> &cx, const ChunkParams &p, i
         // rows past the item's (other requests', or whatever Q's buffer held) start with a
         // reference that nothing exceeds: they have no say in when the warp rescales
         RowState st{r < inf.rows[t] ? kNegInf : -kNegInf, 0.f, 0.f};
-        float unit = 0.f; // 8 bits: log2 of the unit that O is counted in
+        float gap = 0.f; // 8 bits: how far the sum's reference is below m_ref
         if (take_turns) // turns of tiles before this slot's
             for (int j = n_mine ? first - inf.u_lo : inf.u_hi - inf.u_lo; j > 0; --j, ++turns) {
                 if (!turn_wait())
@@ -801,8 +800,8 @@ __device__ void softmax_role(const KernelCtx<D, F8> &cx, const ChunkParams &p, i
                 load_scores<kBN>(tS, x);
                 ptx::tc_fence_before();
                 ptx::mbar_arrive(bar(sm.s_free[t])); // S[t] may be overwritten
-                // 8 bits: the factors of each 16 scores, of their weights and of O
-                float c[F8 ? kBN / 16 : 1], log_v[8], inv_v[8], tile_alpha = 1.f;
+                // 8 bits: the factors of each 16 scores, and of their weights
+                float c[F8 ? kBN / 16 : 1], log_v[8];
                 if constexpr (F8) {
                     const uint32_t at = ptx::smem_u32(&sm.factors[t][(scount - 1) & 3]);
                     float k[8];
@@ -833,17 +832,10 @@ __device__ void softmax_role(const KernelCtx<D, F8> &cx, const ChunkParams &p, i
                 float alpha;
                 if constexpr (F8) {
                     const uint32_t at = ptx::smem_u32(&sm.factors[t][(scount - 1) & 3]);
-                    float rest[4];
 #pragma unroll
-                    for (int i = 0; i < 8; i += 4) {
+                    for (int i = 0; i < 8; i += 4)
                         ptx::load_shared_v4(at + 32 + 4 * i, log_v + i);
-                        ptx::load_shared_v4(at + 64 + 4 * i, inv_v + i);
-                    }
-                    ptx::load_shared_v4(at + 96, rest);
-                    tile_alpha = rest[0];
-                    unit = rest[1];
-                    alpha = softmax_compute_p_scaled<kBN>(x, c, log_v, inv_v, st, pk, rescale) * tile_alpha;
-                    rescale |= tile_alpha != 1.f;
+                    alpha = softmax_compute_p_scaled<kBN>(x, c, log_v, st, gap, pk, rescale);
                 } else {
                     alpha = C::kOnes ? softmax_compute_p_exact_sum<kBN>(x, MOD == MOD_NONE ? p.qk_log2 : 1.f, st, false,
                                                                         pk, rescale)
@@ -909,9 +901,16 @@ __device__ void softmax_role(const KernelCtx<D, F8> &cx, const ChunkParams &p, i
                 st.l_round = __uint_as_float(sum[0]);
             }
         }
-        if constexpr (F8)
+        float o_unit = 1.f;
+        if constexpr (F8) {
+            // the sum as one in [1, 2), m and O's unit to go with it: then O is no larger than
+            // twice a value of V, whatever the scales are
+            const float k = st.l == 0.f ? 0.f : static_cast<float>(static_cast<int>(__float_as_uint(st.l) >> 23) - 127);
+            st.m_ref = (st.m_ref == kNegInf ? kNegInf : st.m_ref - gap + k);
+            st.l *= ptx::ex2(-k);
             st.l_round = st.l; // P in f16 is within 2^-12 of it
-        const float o_unit = F8 ? ptx::ex2(unit) : 1.f;
+            o_unit = ptx::ex2(gap - k) * ptx::ex2(-kPBias);
+        }
         if (inf.pair) {
             if (active)
                 write_slot<D, F8>(p, inf, t, r, tO, st, n_mine > 0, o_unit);

@@ -77,52 +77,40 @@ __device__ __forceinline__ void convert_half(const uint8_t *raw, uint8_t *dst, i
     }
 }
 
-// What the scales of a tile do to a slot of row blocks.  V's codes are multiplied as they
-// are; the scale of a key goes into its weight, as a power of two relative to the
-// largest scale of the item so far, v = scale 2^-unit (at least 2^-60), and the accumulator
-// counts in units of 2^unit: a weight goes into P times v and into its row's sum as it is.
-// So P stays below 2^(8 + kPBias) in f16 whatever the scales are, and holds 11 bits of a
-// product of weight and scale down to 2^(-14 - kPBias) of the largest.
-constexpr float kPBias = 6.f, kLeastLog = -110.f, kLeastV = -60.f;
+// The scales of a tile, as the softmax of row blocks takes them: of 16 keys each, K's and the logarithm
+// of V's.  0 or NaN: a box that no row sees.
+constexpr float kLeastLog = -110.f;
 struct alignas(16) TileFactors {
-    float k[8];                 // of 16 keys each
-    float log_v[8], inv_v[8];   // log2 of v, 1 / v
-    float alpha, unit;          // what the accumulator is multiplied by first; its unit's logarithm
-    float pad[2];
+    float k[8], log_v[8];
 };
 
-// The factors of a tile for a slot whose largest scale so far is 2^top, by a warp; lane
-// g < 8 has the scales of box g (0 or NaN: a box that no row sees).
-__device__ __forceinline__ void tile_factors(TileFactors &f, float k, float scale_v, float &top)
+// By a warp; lane g < 8 has the scales of box g.
+__device__ __forceinline__ void tile_factors(TileFactors &f, float k, float scale_v)
 {
     const int lane = static_cast<int>(ptx::lane_id());
-    const float log_v = fmaxf(ptx::lg2(scale_v), kLeastLog);
-    float most = log_v;
-#pragma unroll
-    for (int d = 1; d < 8; d *= 2)
-        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
-    most = fmaxf(top, most);
     if (lane < 8) {
         f.k[lane] = k > 0.f ? k : 0.f;
-        const float v = fmaxf(log_v - most, kLeastV) + kPBias;
-        f.log_v[lane] = v;
-        f.inv_v[lane] = ptx::ex2(-v);
-        if (lane == 0) {
-            f.alpha = ptx::ex2(top - most);
-            f.unit = most - kPBias;
-        }
+        f.log_v[lane] = fmaxf(ptx::lg2(scale_v), kLeastLog);
     }
-    top = most;
 }
 
-// softmax_compute_p_exact_sum under these factors: c, of 16 scores each, in place of
-// one, log2 of v in the exponent and 1 / v on the sums of 16 weights.  P in f16.
+// softmax_compute_p_exact_sum with a factor c of 16 scores each in place of one, and with V's
+// scale in P, which multiplies V's codes: P = 2^(kPBias + z + log_v - m_ref) in f16, and the sum is
+// relative to m = m_ref - gap, a reference of the scores alone.  Both references are the row's own:
+// keys that it does not see have no say, however loud they are.  P stays below 2^(8 + kPBias), and
+// holds 11 bits of a product of weight and scale down to 2^(-14 - kPBias) of the row's largest.
+//
+// The sum takes the same exponentials, times 2^(gap - kPBias - log_v) for 16 keys at a time.  Where
+// log_v is 2^-kPSpread and more below the gap, P is below 2^(8 + kPBias - kPSpread) and 0 in f16; in its place
+// stands that, and the sum's factor is as if log_v were that: so that neither goes out of
+// range, whatever the scales are.
+constexpr float kPBias = 6.f, kPSpread = 40.f;
 template <int N>
 __device__ __forceinline__ float softmax_compute_p_scaled(float (&x)[N], const float (&c)[N / 16],
-                                                          const float (&log_v)[8], const float (&inv_v)[8],
-                                                          RowState &st, uint32_t (&pk)[N / 2], bool &rescale)
+                                                          const float (&log_v)[8], RowState &st, float &gap,
+                                                          uint32_t (&pk)[N / 2], bool &rescale)
 {
-    float mx = kNegInf;
+    float mp = kNegInf, mz = kNegInf;
 #pragma unroll
     for (int g = 0; g < N / 16; ++g) {
         const float *s = x + 16 * g;
@@ -132,23 +120,29 @@ __device__ __forceinline__ float softmax_compute_p_scaled(float (&x)[N], const f
             a = ptx::max3(a, s[e], s[e + 1]);
             b = ptx::max3(b, s[e + 2], s[e + 3]);
         }
-        mx = fmaxf(mx, fmaxf(a, b) * c[g]); // c > 0
+        const float z = fmaxf(a, b) * c[g]; // c > 0
+        mz = fmaxf(mz, z);
+        mp = fmaxf(mp, z + log_v[g]);
     }
     float alpha = 1.f;
     rescale = false;
-    const bool need = mx > st.m_ref + kRescaleThreshold;
+    const float m = st.m_ref - gap;
+    const bool need = mp > st.m_ref + kRescaleThreshold || mz > m + kRescaleThreshold;
     if (__any_sync(0xffffffffu, need)) {
-        const float m_new = fmaxf(st.m_ref, mx);
-        alpha = (m_new == kNegInf) ? 1.f : ptx::ex2(st.m_ref - m_new);
-        st.l *= alpha;
-        st.m_ref = m_new;
+        const float ref_new = fmaxf(st.m_ref, mp), m_new = fmaxf(m, mz);
+        const bool none = ref_new == kNegInf;
+        alpha = none ? 1.f : ptx::ex2(st.m_ref - ref_new);
+        st.l *= none ? 1.f : ptx::ex2(m - m_new);
+        st.m_ref = ref_new;
+        gap = none ? 0.f : ref_new - m_new;
         rescale = true;
     }
-    const float nmu = (st.m_ref == kNegInf) ? 0.f : -st.m_ref;
+    const float nmu = (st.m_ref == kNegInf) ? kPBias : kPBias - st.m_ref;
+    const float least = gap - kPSpread, unit = gap - kPBias;
     float l0 = 0.f, l1 = 0.f;
 #pragma unroll
     for (int g = 0; g < N / 16; ++g) {
-        const float nm = nmu + log_v[g];
+        const float v = fmaxf(log_v[g], least), nm = nmu + v, f = ptx::ex2(unit - v);
         float le[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -165,7 +159,7 @@ __device__ __forceinline__ float softmax_compute_p_scaled(float (&x)[N], const f
             }
         }
         ptx::add2(le[0], le[1], le[2], le[3]);
-        ptx::fma2(l0, l1, le[0], le[1], inv_v[g], inv_v[g], l0, l1);
+        ptx::fma2(l0, l1, le[0], le[1], f, f, l0, l1);
     }
     st.l += l0 + l1;
     return alpha;

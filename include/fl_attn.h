@@ -632,12 +632,11 @@ fl_status fl_kv_read_fp8(const fl_tensor *k_cache, const fl_tensor *v_cache, con
  * [B, S_max, Hk, D] with scales [B, S_max / block, Hk]).  Everything said there holds, with
  * the values of the cache in place of its elements, and fewer than 2^30 tokens.  Codes and scales
  * of keys that no row of their request sees may be anything; those of the others must not
- * be NaN.  Weights times scales of V are held in f16 relative to the largest of their row (up to 16
- * rows of a request and KV head: 11 bits down to 2^-26 of it, steps of 2^-36 of it below) or of their
- * item (more rows: 11 bits down to 2^-20, and scales of V that are 2^-60 of another's count as that).
- * The workspace is larger (q in two e4m3
- * terms, which hold bf16 exactly down to 2^-10 of a row's largest element and to 2^-18 of it
- * below): ask fl_attn_chunk_fp8_workspace_size.
+ * be NaN.  Weights times scales of V are held in f16, relative to the largest of their row among the
+ * keys that it sees: with 11 bits down to 2^-26 of it, in steps of 2^-36 of it below (requests with
+ * more than 16 rows a KV head: 2^-20 and 2^-30).  The sums that divide them take every weight in fp32,
+ * whatever its scale.  The workspace is larger (q in two e4m3 terms, which hold bf16 exactly down to
+ * 2^-10 of a row's largest element and to 2^-18 of it below): ask fl_attn_chunk_fp8_workspace_size.
  */
 fl_status fl_attn_chunk_fp8_workspace_size(const fl_tensor *q, const fl_tensor *k_cache,
                                            const fl_chunk_desc *desc, size_t *bytes);

@@ -207,15 +207,22 @@ def _loud(D, n, L, at, gain, z=None, Hq=8, Hk=2):
 
 
 @pytest.mark.parametrize("gain", [20, 35, 60, 100])
-@pytest.mark.parametrize("n,L", [(3, 290), (4, 4994)])
+@pytest.mark.parametrize("n,L", [(3, 290), (4, 4994), (60, 306), (100, 2002), (300, 706)])
 @pytest.mark.parametrize("D", [64, 128])
 def test_loud_values_that_come_later(D, n, L, gain):
     # the last 2 tokens' V, a block of its own, is 2^gain louder, which the rows before do not see
     _check(_loud(D, n, L, slice(L - 2, L), gain), FEW if 4 * n <= 16 else BLOCKS, f"2^{gain} later", calls=2)
 
 
+@pytest.mark.parametrize("gain", [35, 60, 100])
+@pytest.mark.parametrize("n,window", [(60, 20), (200, 90), (130, 300)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_loud_values_that_a_window_has_left(D, n, window, gain):
+    _check(_loud(D, n, 600, slice(600 - n - 10, 600 - n - 6), gain), BLOCKS, f"2^{gain} left", window=window)
+
+
 @pytest.mark.parametrize("gain,z", [(40, -60.0), (60, -60.0), (90, -90.0), (-90, 60.0), (60, -20.0), (-60, 20.0)])
-@pytest.mark.parametrize("n,L", [(1, 300), (1, 6000), (4, 2000)])
+@pytest.mark.parametrize("n,L", [(1, 300), (1, 6000), (4, 2000), (60, 300), (150, 1200)])
 @pytest.mark.parametrize("D", [64, 128])
 def test_loud_values_of_little_weight(D, n, L, gain, z):
     # a block whose scale and weights differ by 2^90 and more from the others', in either order
