@@ -8,8 +8,8 @@
 // s_old / s), which rounds subnormals alone.  So the codes of a block hardly depend on how
 // its tokens were split over calls, and its scale not at all.
 //
-// The tokens of a block that a call brings are neighbours (fl_kv_plan lists them
-// so): a run.  A thread block takes the runs that begin in its window of tokens, as many at a
+// The tokens of a block that a call brings are neighbours but for skipped ones (fl_kv_plan lists
+// them so): a run, with the skipped ones inside and behind it.  A thread block takes the runs that begin in its window of tokens, as many at a
 // time as fit, for a group of heads: each thread keeps its 16 elements of up to four
 // (token, head) rows in registers from the maximum (over the lanes of a row, then in
 // shared memory) to the codes (as bf16, and rotates them twice: kept rotated, in fp32, they left two
@@ -44,7 +44,8 @@ struct RunShared {
     uint32_t old[kRunRows];       // and the scale before
     uint8_t run[kRunRows], fresh[kRunRows]; // run of each token; the run has its block's first row
     int leaders[kRopeThreads / 32];
-    int end, last, cut;
+    int end, last;
+    int64_t last_block;
 };
 
 // Where a thread's unit k of 2 V elements lies: vector a at the first place, b
@@ -243,19 +244,60 @@ __device__ __forceinline__ void append_runs(const Fp8AppendParams &f, const Fp8S
         }
     };
 
+    // Is the first token from u on that is not skipped one of block blk?  All threads.
+    auto goes_on = [&](int u, int64_t blk) {
+        constexpr int kAhead = 16;
+        for (; u < p.tokens; u += kAhead * kRopeThreads) {
+            const int64_t here = block_of(u);
+            if (here >= 0)
+                return here == blk;
+            int at = INT32_MAX;
+#pragma unroll
+            for (int i = kAhead - 1; i >= 0; --i)
+                at = block_of(u + i * kRopeThreads + tid) >= 0 ? u + i * kRopeThreads + tid : at;
+            __syncthreads();
+            if (tid == 0)
+                sm.end = INT32_MAX;
+            __syncthreads();
+            if (at < INT32_MAX)
+                atomicMin(&sm.end, at);
+            __syncthreads();
+            at = sm.end;
+            if (at < INT32_MAX)
+                return block_of(at) == blk;
+        }
+        return false;
+    };
+
     for (int s = t0; s < t1;) {
         // ---- the chunk: tokens s .. s + n - 1, whole runs but the one that began before the
         // window, or (longer) the beginning of a run that does not fit
         __syncthreads(); // the last chunk's have been read
         if (tid == 0) {
             sm.end = f.chunk;
-            sm.last = sm.cut = 0;
+            sm.last = -1;
         }
         const int t = s + tid;
         const int64_t mine = tid < f.chunk ? block_of(t) : -1;
         if (ROT && tid < f.chunk)
             sm.pos[tid] = t < p.tokens ? __ldg(p.positions + t) : 0;
-        const bool leader = mine >= 0 && mine != block_of(t - 1);
+        // the block of the last token before that is not skipped
+        int64_t before = block_of(t - 1);
+        for (uint32_t todo = __ballot_sync(0xffffffffu, mine >= 0 && before < 0); todo; todo &= todo - 1) {
+            const int of = __ffs(todo) - 1;
+            int64_t found = -1;
+            for (int u = s + warp * 32 + of - 2 - lane;; u -= 32) { // 32 tokens at a time
+                const int64_t b = block_of(u);
+                const uint32_t hit = __ballot_sync(0xffffffffu, b >= 0 || u < 0);
+                if (hit) {
+                    found = __shfl_sync(0xffffffffu, b, __ffs(hit) - 1);
+                    break;
+                }
+            }
+            if (lane == of)
+                before = found;
+        }
+        const bool leader = mine >= 0 && mine != before;
         const uint32_t ballot = __ballot_sync(0xffffffffu, leader);
         if (lane == 0)
             sm.leaders[warp] = __popc(ballot);
@@ -269,16 +311,21 @@ __device__ __forceinline__ void append_runs(const Fp8AppendParams &f, const Fp8S
             atomicMin(&sm.end, tid); // the next window's, or past the last
         __syncthreads();
         int n = sm.end;
-        if (n == f.chunk && tid == f.chunk - 1 && mine >= 0 && block_of(t + 1) == mine)
-            sm.cut = 1; // the last run goes on
         if (leader && tid < n)
             atomicMax(&sm.last, tid);
         __syncthreads();
-        const bool cut = sm.cut, longer = cut && sm.last == 0 && run >= 0;
-        // (the run in question is the one at the chunk's beginning)
-        const bool go_long = __syncthreads_or(tid == 0 && longer);
-        if (cut && !go_long && sm.last > 0)
-            n = sm.last;
+        const int last = sm.last;
+        bool go_long = false;
+        if (n == f.chunk && last >= 0) { // the last run may go on past the chunk
+            if (tid == last)
+                sm.last_block = mine;
+            __syncthreads();
+            const int64_t open = sm.last_block, next = block_of(s + n);
+            if (last == 0)
+                go_long = goes_on(s + n, open);
+            else if (next == open || (next < 0 && s + n < p.tokens))
+                n = last;
+        }
         if (n == 0)
             break;
         if (tid < n) {
@@ -321,16 +368,19 @@ __device__ __forceinline__ void append_runs(const Fp8AppendParams &f, const Fp8S
         if (go_long) {
             const int64_t blk = block_of(s);
             const int64_t block_row = sm.block[0];
-            for (int more = n; more == f.chunk; total += more) {
+            for (int more = n; more == f.chunk && goes_on(s + total, blk); total += more) {
                 __syncthreads();
                 if (tid == 0)
                     sm.end = f.chunk;
                 __syncthreads();
                 if (tid < f.chunk) {
-                    if (block_of(s + total + tid) != blk)
+                    const int x = s + total + tid;
+                    const int64_t b = block_of(x);
+                    if (x >= p.tokens || (b >= 0 && b != blk))
                         atomicMin(&sm.end, tid);
-                    else
-                        place_token(tid, s + total + tid, 0, block_row, true);
+                    sm.place[tid] = -1;
+                    if (b == blk)
+                        place_token(tid, x, 0, block_row, true);
                 }
                 __syncthreads();
                 more = sm.end;
@@ -385,8 +435,11 @@ __device__ __forceinline__ void append_runs(const Fp8AppendParams &f, const Fp8S
             for (int done = 0, more; done < total; done += more) {
                 __syncthreads();
                 more = min(f.chunk, total - done);
-                if (tid < more && block_of(s + done + tid) == blk)
-                    place_token(tid, s + done + tid, 0, block_row, true);
+                if (tid < more) {
+                    sm.place[tid] = -1;
+                    if (block_of(s + done + tid) == blk)
+                        place_token(tid, s + done + tid, 0, block_row, true);
+                }
                 __syncthreads();
                 load(s + done, more);
                 angles(more);

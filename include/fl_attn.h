@@ -607,8 +607,8 @@ fl_status fl_attn_chunk(const fl_tensor *q, const fl_tensor *k_cache, const fl_t
  * does not depend on how its tokens were split over calls.  A scale found that is not
  * positive and finite counts as none.  Values that are not finite are stored as NaN.
  * The tokens of a call that share a block must follow one another in k, v and
- * slots (in any order), as fl_kv_plan lists them; blocks that tokens apart from one another
- * share hold any of their scales and codes afterwards.  Slots must differ from one
+ * slots (in any order, with skipped ones between them or not), as fl_kv_plan lists them; a block whose
+ * tokens have another block's between them holds any of their scales and codes afterwards.  Slots must differ from one
  * another.  q_out may be q.
  */
 fl_status fl_kv_append_fp8(const fl_tensor *q, const fl_tensor *k, const fl_tensor *v, const fl_tensor *q_out,
