@@ -45,5 +45,13 @@ __device__ __forceinline__ float2 from_e4m3x2(uint32_t c)
     return __half22float2(*reinterpret_cast<const __half2 *>(&h));
 }
 
+// A code's value times a scale (up to 28 bits) in 24, rounded to odd: rounded again to
+// fewer, it comes out as if rounded once.
+__device__ __forceinline__ float times_to_odd(float c, float s)
+{
+    const float p = __fmul_rz(c, s);
+    return fmaf(c, s, -p) == 0.f ? p : __uint_as_float(__float_as_uint(p) | 1u);
+}
+
 } // namespace
 } // namespace fl

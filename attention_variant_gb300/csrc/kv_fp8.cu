@@ -6,7 +6,8 @@
 // s is the smallest power of two that 448 s holds every finite |x| of the block,
 // at least 2^-100: then x / s is exact, and a scale that grows leaves codes c -> rn(c
 // s_old / s), which rounds subnormals alone.  So the codes of a block hardly depend on how
-// its tokens were split over calls, and its scale not at all.
+// its tokens were split over calls, and its scale not at all.  (A scale found may be no power
+// of two: quotients and products are rounded once then, too, by the exact sign of what is left.)
 //
 // The tokens of a block that a call brings are neighbours but for skipped ones (fl_kv_plan lists
 // them so): a run, with the skipped ones inside and behind it.  A thread block takes the runs that begin in its window of tokens, as many at a
@@ -47,6 +48,25 @@ struct RunShared {
     int end, last;
     int64_t last_block;
 };
+
+// Two quotients x / m to codes, for 1 <= m < 2, rounded once: where x times 1 / m, off by less than
+// 4 of its last places, is that near a number of 8 bits -- the borders between codes are
+// some of these --, the sign of x - g m, exact, says on which side x / m lies.
+__device__ __noinline__ uint32_t quotients_to_e4m3x2(float x0, float x1, float m)
+{
+    const float inv = 1.f / m, x[2] = {x0, x1};
+    float y[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        y[i] = x[i] * inv;
+        const uint32_t b = __float_as_uint(y[i]), g = (b + 0x8000u) & 0xffff0000u;
+        if (fabsf(y[i]) < 1024.f && b - g + 4u <= 8u) { // (past 448 anything is 448; NaN stays NaN)
+            const float r = fmaf(-__uint_as_float(g), m, x[i]);
+            y[i] = __uint_as_float(r == 0.f ? g : (r > 0.f) == (x[i] > 0.f) ? g + 1u : g - 1u);
+        }
+    }
+    return to_e4m3x2(y[0], y[1]);
+}
 
 // Where a thread's unit k of 2 V elements lies: vector a at the first place, b
 // `b_at` further (V elements each).
@@ -216,17 +236,25 @@ __device__ __forceinline__ void append_runs(const Fp8AppendParams &f, const Fp8S
             expand(i, tok, x);
             const int at_run = sm.run[tok] * group + h;
             const float s = __uint_as_float(max(scale_bits(sm.size[at_run]), sm.old[at_run]));
-            const float inv = 1.f / s;
+            // s = m times a power of two; m is 1 but for scales from elsewhere
+            const float m = __uint_as_float((__float_as_uint(s) & 0x7fffffu) | 0x3f800000u);
+            const float inv = 1.f / __uint_as_float(__float_as_uint(s) & 0x7f800000u);
             uint8_t *dst = st.cache + sm.place[tok] + h * st.d_h;
+            uint32_t codes[8]; // two each
+            if (m == 1.f) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    codes[e] = to_e4m3x2(x[2 * e] * inv, x[2 * e + 1] * inv);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    codes[e] = quotients_to_e4m3x2(x[2 * e] * inv, x[2 * e + 1] * inv, m);
+            }
 #pragma unroll
             for (int k = 0; k < kUnits; ++k) {
                 int b_at;
                 const int at = unit_at<V, INTER, ROT>(piece * kUnits + k, rot_units, rot, pairs, b_at);
-                const float *w = x + k * 2 * V;
-                uint32_t c[V]; // two codes each
-#pragma unroll
-                for (int e = 0; e < V; ++e)
-                    c[e] = to_e4m3x2(w[2 * e] * inv, w[2 * e + 1] * inv);
+                const uint32_t *c = codes + k * V;
                 if constexpr (V == 8) {
                     *reinterpret_cast<uint2 *>(dst + at) = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
                     *reinterpret_cast<uint2 *>(dst + at + b_at) = make_uint2(c[4] | c[5] << 16, c[6] | c[7] << 16);
@@ -420,7 +448,8 @@ __device__ __forceinline__ void append_runs(const Fp8AppendParams &f, const Fp8S
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         const float2 lo = from_e4m3x2(w[k] & 0xffffu), hi = from_e4m3x2(w[k] >> 16);
-                        w[k] = to_e4m3x2(lo.x * ratio, lo.y * ratio) | to_e4m3x2(hi.x * ratio, hi.y * ratio) << 16;
+                        w[k] = to_e4m3x2(times_to_odd(lo.x, ratio), times_to_odd(lo.y, ratio)) |
+                               to_e4m3x2(times_to_odd(hi.x, ratio), times_to_odd(hi.y, ratio)) << 16;
                     }
                     *at = make_uint2(w[0], w[1]);
                 }

@@ -603,13 +603,14 @@ fl_status fl_attn_chunk(const fl_tensor *q, const fl_tensor *k_cache, const fl_t
  * 2^-100.  If the block's first row is among them the block starts anew, with s = need;
  * other rows keep codes that mean nothing until they are written.  Otherwise s = max(the
  * scale found, need), and where that grows, codes c of the block's other rows become
- * c s_old / s, rounded (exact but for codes that leave e4m3's normal range).  So a block's scale
- * does not depend on how its tokens were split over calls.  A scale found that is not
- * positive and finite counts as none.  Values that are not finite are stored as NaN.
- * The tokens of a call that share a block must follow one another in k, v and
- * slots (in any order, with skipped ones between them or not), as fl_kv_plan lists them; a block whose
- * tokens have another block's between them holds any of their scales and codes afterwards.  Slots must differ from one
- * another.  q_out may be q.
+ * c s_old / s, rounded (exact where s_old is a power of two, but for codes that leave e4m3's
+ * normal range).  So the scale of a block that the append has filled does not depend on how its
+ * tokens were split over calls.  A scale found that is not positive and finite counts as none.
+ * Values that are not finite are stored as NaN.
+ * The tokens of a call that share a block must follow one another in k, v and slots (in any
+ * order, with skipped ones between them or not), as fl_kv_plan lists them; a block whose tokens
+ * have another block's between them holds any of their scales and codes afterwards.  Slots must
+ * differ from one another.  q_out may be q.
  */
 fl_status fl_kv_append_fp8(const fl_tensor *q, const fl_tensor *k, const fl_tensor *v, const fl_tensor *q_out,
                            const fl_tensor *k_cache, const fl_tensor *v_cache, const fl_tensor *k_scale,

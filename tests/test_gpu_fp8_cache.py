@@ -1,4 +1,4 @@
-"""Writing the 8-bit KV cache where slots are skipped."""
+"""Writing the 8-bit KV cache where scales are no powers of two or slots are skipped."""
 from __future__ import annotations
 
 import random
@@ -8,7 +8,57 @@ import pytest
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
+from tests import fp8_ref as ref8  # noqa: E402
 from tests import test_gpu_fp8 as base  # noqa: E402
+from tests.fp8_ref import FP8  # noqa: E402
+
+
+def _rounded(y, bits, least):
+    """float64 y rounded once, to `bits` significant bits or the step of 2^least, to nearest even."""
+    e = torch.clamp(torch.frexp(y)[1].double() - 1, min=least)
+    step = torch.exp2(e - (bits - 1))
+    return torch.round(y / step) * step
+
+
+def _e4m3(y):
+    return _rounded(y, 4, -6).clamp(-448, 448).float().to(FP8)
+
+
+def _odd_scales(shape, seed):
+    """Scales that are no powers of two."""
+    g = torch.Generator().manual_seed(seed)
+    return torch.exp2(16 * torch.rand(shape, generator=g) - 12).float()
+
+
+# ------------------------------------------------------------------ scales that are no powers of two
+
+
+@pytest.mark.parametrize("block", [16, 64])
+@pytest.mark.parametrize("Hk,D", [(3, 64), (8, 128)])
+def test_append_into_blocks_of_such_scales(Hk, D, block):
+    # rows after a block's first: a scale that stays, or grows to a power of two
+    P, page = 400, 64
+    rng = random.Random(Hk)
+    slots = torch.tensor([b * block + r for b in range(P * page // block) for r in sorted(rng.sample(range(1, block), 3))])
+    T = slots.numel()
+    loud = torch.exp2(torch.randint(-6, 7, (T, Hk, 1), generator=torch.Generator().manual_seed(1)).float())
+    x = [(base._rand((T, Hk, D), s, torch.float32) * loud).to(torch.bfloat16) for s in (1, 2)]
+    codes = [base._pool(P, page, block, Hk, D, s)[0] for s in (3, 4)]
+    scale = [_odd_scales((P, page // block, Hk), s) for s in (5, 6)]
+    got = base._append(*x, slots, *codes, *scale)
+    stays = 0
+    for i in (0, 1):
+        old = scale[i].double().view(-1, Hk)
+        size = x[i].double().abs().amax(-1).view(-1, 3, Hk).amax(1)
+        need = torch.tensor([[ref8.need(float(a)) for a in row] for row in size], dtype=torch.float64)
+        new = torch.maximum(old, need)
+        stays += int((new == old).sum())
+        assert torch.equal(got[2 + i].double().view(-1, Hk), new)
+        c = codes[i].double().view(-1, block, Hk, D)
+        want = torch.where((need > old)[:, None, :, None], _e4m3(c * (old / new)[:, None, :, None]).double(), c)
+        want.view(-1, Hk, D)[slots] = _e4m3(x[i].double() / new[slots // block][..., None]).double()
+        assert torch.equal(got[i].double().view(want.shape), want)
+    assert T // 6 < stays < T // 3 * 2 * Hk
 
 
 # ------------------------------------------------------------------ skipped slots
