@@ -23,6 +23,7 @@
 // into bf16 37.7 us, 5750 GB/s.
 #include <cuda_bf16.h>
 #include <cstdint>
+#include <type_traits>
 
 #include "e4m3.cuh"
 #include "rope.cuh"
@@ -600,6 +601,8 @@ __global__ void __launch_bounds__(kReadThreads) read_fp8_kernel(const __grid_con
             for (int k = 0; k < kReadUnits; ++k) {
                 const int tok = t + k * f.uy;
                 const int64_t row = tok < n_tok ? s_row[tok] : -1;
+                if constexpr (sizeof(T) == 2)
+                    s[k] = 0.f;
                 if (row < 0)
                     continue;
                 if constexpr (E == 8) {
@@ -611,25 +614,37 @@ __global__ void __launch_bounds__(kReadThreads) read_fp8_kernel(const __grid_con
                 }
                 s[k] = __ldg(scale + s_scale[tok]);
             }
+            // a product of up to 28 bits; into bf16 only exact ones may go by way of fp32
+            uint32_t rest = 0;
 #pragma unroll
-            for (int k = 0; k < kReadUnits; ++k) {
-                const int tok = t + k * f.uy;
-                if (tok >= n_tok || s_row[tok] < 0)
-                    continue;
-                float v[E];
+            for (int k = 0; k < (sizeof(T) == 2 ? kReadUnits : 0); ++k)
+                rest |= __float_as_uint(s[k]) & 0x7fffffu;
+            auto write = [&](auto once) {
+                constexpr bool ONCE = decltype(once)::value;
 #pragma unroll
-                for (int q = 0; q < E / 2; ++q) {
-                    const float2 c = from_e4m3x2((q & 1 ? w[k][q / 2] >> 16 : w[k][q / 2]) & 0xffffu);
-                    v[2 * q] = c.x * s[k];
-                    v[2 * q + 1] = c.y * s[k];
+                for (int k = 0; k < kReadUnits; ++k) {
+                    const int tok = t + k * f.uy;
+                    if (tok >= n_tok || s_row[tok] < 0)
+                        continue;
+                    float v[E];
+#pragma unroll
+                    for (int q = 0; q < E / 2; ++q) {
+                        const float2 c = from_e4m3x2((q & 1 ? w[k][q / 2] >> 16 : w[k][q / 2]) & 0xffffu);
+                        v[2 * q] = ONCE ? times_to_odd(c.x, s[k]) : c.x * s[k];
+                        v[2 * q + 1] = ONCE ? times_to_odd(c.y, s[k]) : c.y * s[k];
+                    }
+                    T *dst = out + tok * st.o_t;
+                    if constexpr (sizeof(T) == 2)
+                        *reinterpret_cast<uint4 *>(dst) = make_uint4(ptx::pack_bf16(v[0], v[1]), ptx::pack_bf16(v[2], v[3]),
+                                                                     ptx::pack_bf16(v[4], v[5]), ptx::pack_bf16(v[6], v[7]));
+                    else
+                        *reinterpret_cast<float4 *>(dst) = make_float4(v[0], v[1], v[2], v[3]);
                 }
-                T *dst = out + tok * st.o_t;
-                if constexpr (sizeof(T) == 2)
-                    *reinterpret_cast<uint4 *>(dst) = make_uint4(ptx::pack_bf16(v[0], v[1]), ptx::pack_bf16(v[2], v[3]),
-                                                                 ptx::pack_bf16(v[4], v[5]), ptx::pack_bf16(v[6], v[7]));
-                else
-                    *reinterpret_cast<float4 *>(dst) = make_float4(v[0], v[1], v[2], v[3]);
-            }
+            };
+            if (rest == 0)
+                write(std::false_type{});
+            else
+                write(std::true_type{});
         }
     }
 }

@@ -1,4 +1,4 @@
-"""Writing the 8-bit KV cache where scales are no powers of two or slots are skipped."""
+"""Writing and reading the 8-bit KV cache where scales are no powers of two or slots are skipped."""
 from __future__ import annotations
 
 import random
@@ -8,6 +8,7 @@ import pytest
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
+import attention_variant_gb300 as fa  # noqa: E402
 from tests import fp8_ref as ref8  # noqa: E402
 from tests import test_gpu_fp8 as base  # noqa: E402
 from tests.fp8_ref import FP8  # noqa: E402
@@ -31,6 +32,23 @@ def _odd_scales(shape, seed):
 
 
 # ------------------------------------------------------------------ scales that are no powers of two
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_read_rounds_once(D):
+    # every code times 4 x 20,000 scales: the product has up to 28 bits, and is rounded to bf16 once
+    P, page, Hk = 2500, 32, 4
+    codes = (torch.arange(P * page * Hk * D) % 254).to(torch.uint8)
+    codes[codes >= 127] += 1  # no NaN
+    codes = codes.view(P, page, Hk, D).view(FP8)
+    scale = [_odd_scales((P, 2, Hk), i) for i in (1, 2)]
+    slots = torch.arange(P * page)
+    for dtype, bits in ((torch.bfloat16, 8), (torch.float32, 24)):
+        out = [torch.zeros((P * page, Hk, D), dtype=dtype, device="cuda") for _ in "kv"]
+        fa.fl_kv_read_fp8(codes.cuda(), codes.cuda(), *(s.cuda() for s in scale), slots.cuda(), *out)
+        for got, s in zip(out, scale):
+            want = _rounded(ref8.values(codes, s), bits, -126).view(-1, Hk, D)
+            assert torch.equal(got.cpu().double(), want)
 
 
 @pytest.mark.parametrize("block", [16, 64])
