@@ -1,6 +1,7 @@
-"""Writing and reading the 8-bit KV cache where scales are no powers of two or slots are skipped."""
+"""Writing and reading the 8-bit KV cache where scales are no powers of two, slots are skipped, or q is long."""
 from __future__ import annotations
 
+import math
 import random
 
 import pytest
@@ -10,6 +11,7 @@ pytestmark = pytest.mark.gpu
 
 import attention_variant_gb300 as fa  # noqa: E402
 from tests import fp8_ref as ref8  # noqa: E402
+from tests import serving_ref as ref  # noqa: E402
 from tests import test_gpu_fp8 as base  # noqa: E402
 from tests.fp8_ref import FP8  # noqa: E402
 
@@ -116,3 +118,62 @@ def test_append_of_one_block_with_every_other_slot_skipped():
     base._check_append(*x, slots, P, page, block)
     base._check_append(x[0].repeat(20, 1, 1), x[1].repeat(20, 1, 1),
                        torch.cat((slots[:300], torch.full((20 * 512 - 512,), -1), slots[300:])), P, page, block)
+
+
+# ------------------------------------------------------------------ many tokens of q
+
+
+@pytest.mark.parametrize("layout,D,rot", [("half", 128, 128), ("interleaved", 64, 64), ("half", 64, 0), ("half", 64, 20)])
+def test_append_with_more_of_q_than_the_gpu_holds(layout, D, rot):
+    # q in a kernel of its own beside K's and V's, also in place and in a captured graph
+    Hq, Hk, page, block, T = 16, 2, 64, 64, 11000
+    P = T // page + 1
+    at = torch.randperm(P * page // block, generator=torch.Generator().manual_seed(1))
+    slots = (at[:, None] * block + torch.arange(block)).flatten()[:T]
+    slots[4992:5056] = -1  # a whole block
+    live = slots >= 0
+    pos = torch.randint(0, 100000, (T,), generator=torch.Generator().manual_seed(2))
+    q, k, v = base._rand((T, Hq, D), 1), base._rand((T, Hk, D), 2), base._rand((T, Hk, D), 3)
+    pools = [base._pool(P, page, block, Hk, D, s) for s in (1, 2)]
+    kw = dict(rope=fa.make_rope_table(rot, layout=layout), positions=pos.to(torch.int32).cuda()) if rot else {}
+    dev = [x.cuda() for x in (q, k, v, slots)]
+    want = [q[live].double(), k[live].double()]
+    bound = [torch.zeros_like(x) for x in want]
+    if rot:
+        want, bound = zip(*(ref.rope(x[live], pos[live], rot, layout) for x in (q, k)))
+    results = []
+    for graph in (False, True):
+        caches = [x.cuda() for x in (pools[0][0], pools[1][0], pools[0][1], pools[1][1])]
+        for in_place in (False, True):
+            t = [c.clone() for c in caches]
+            qi = dev[0].clone()
+            qo = qi if in_place else torch.full_like(qi, 7.0)
+
+            def call():
+                fa.fl_kv_append_fp8(qi, dev[1], dev[2], qo, *t, dev[3], **kw)
+
+            if graph:
+                torch.cuda.synchronize()
+                g = torch.cuda.CUDAGraph()
+                with torch.cuda.graph(g):
+                    call()
+                g.replay()
+            else:
+                call()
+            # what follows in the stream sees both kernels' work
+            results.append([x.cpu() for x in (qo.clone(), *(c.clone() for c in t))])
+            if not in_place:
+                assert bool((results[-1][0][~live] == 7).all())
+    for r in results:
+        assert bool(((r[0][live].double() - want[0]).abs() <= bound[0] * 1.01 + 2.0 ** -8 * want[0].abs()).all())
+        for i in range(5):
+            a, b = (x if i else x[live] for x in (r[i], results[0][i]))
+            assert torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8))
+    _, kc, vc, ks, vs = results[0]
+    want_c, want_s = ref8.append(*pools[1], v, slots)
+    assert torch.equal(vs, want_s) and torch.equal(vc.view(torch.uint8), want_c.view(torch.uint8))
+    at = slots[live]
+    s = ks.double()[at // page, at % page // block][..., None]
+    got = kc.double().view(-1, Hk, D)[at] * s
+    err = bound[1] * 1.01
+    assert bool(((got - want[1]).abs() <= err + torch.maximum(2.0 ** -4 * (want[1].abs() + err), s * 2.0 ** -10)).all())
