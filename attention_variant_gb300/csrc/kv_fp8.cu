@@ -10,17 +10,17 @@
 // of two: quotients and products are rounded once then, too, by the exact sign of what is left.)
 //
 // The tokens of a block that a call brings are neighbours but for skipped ones (fl_kv_plan lists
-// them so): a run, with the skipped ones inside and behind it.  A thread block takes the runs that begin in its window of tokens, as many at a
-// time as fit, for a group of heads: each thread keeps its 16 elements of up to four
-// (token, head) rows in registers from the maximum (over the lanes of a row, then in
-// shared memory) to the codes (as bf16, and rotates them twice: kept rotated, in fp32, they left two
-// blocks to a SM).  A run too long for that is read and rotated twice, the
+// them so): a run, with the skipped ones inside and behind it.  A thread block takes the runs that
+// begin in its window of tokens, as many at a time as fit, for a group of heads: each thread keeps
+// its 16 elements of up to four (token, head) rows in registers from the maximum (over the lanes of
+// a row, then in shared memory) to the codes (as bf16, and rotates them twice: kept rotated, in
+// fp32, they left two blocks to a SM).  A run too long for that is read and rotated twice, the
 // second time out of L2.
 //
-// Bound by HBM in part, and by the rotation: 11,810 tokens of 16 + 2 + 2 heads of 128 take 35.8 us
-// (3200 GB/s of 6794; q's rotation, a kernel of its own beside, is 80% of the bytes);
-// 64 single tokens 5.2 us, the launch and one chain of loads.  Reading 79,000 tokens back
-// into bf16 37.7 us, 5750 GB/s.
+// Bound by HBM in part, and by the rotation: 11,810 tokens of 16 + 2 + 2 heads of 128 take 35.7 us
+// (3220 GB/s of 6794; q's rotation, a kernel of its own beside, is 80% of the bytes);
+// 64 single tokens 4.7 us, the launch and one chain of loads.  Reading 79,000 tokens back
+// into bf16 35.4 us, 6130 GB/s.
 #include <cuda_bf16.h>
 #include <cstdint>
 #include <type_traits>
@@ -273,7 +273,8 @@ __device__ __forceinline__ void append_runs(const Fp8AppendParams &f, const Fp8S
         }
     };
 
-    // Is the first token from u on that is not skipped one of block blk?  All threads.
+    // Is the first token from u on that is not skipped one of block blk?  All threads, 16 tokens
+    // each at a time.  (64 tokens and 960 of padding take 9.0 us; 8.5 where a run ended at a skipped slot.)
     auto goes_on = [&](int u, int64_t blk) {
         constexpr int kAhead = 16;
         for (; u < p.tokens; u += kAhead * kRopeThreads) {
@@ -284,7 +285,8 @@ __device__ __forceinline__ void append_runs(const Fp8AppendParams &f, const Fp8S
 #pragma unroll
             for (int i = kAhead - 1; i >= 0; --i)
                 at = block_of(u + i * kRopeThreads + tid) >= 0 ? u + i * kRopeThreads + tid : at;
-            __syncthreads();
+            if (!__syncthreads_or(at < INT32_MAX))
+                continue;
             if (tid == 0)
                 sm.end = INT32_MAX;
             __syncthreads();
@@ -292,8 +294,7 @@ __device__ __forceinline__ void append_runs(const Fp8AppendParams &f, const Fp8S
                 atomicMin(&sm.end, at);
             __syncthreads();
             at = sm.end;
-            if (at < INT32_MAX)
-                return block_of(at) == blk;
+            return block_of(at) == blk;
         }
         return false;
     };
@@ -349,11 +350,10 @@ __device__ __forceinline__ void append_runs(const Fp8AppendParams &f, const Fp8S
             if (tid == last)
                 sm.last_block = mine;
             __syncthreads();
-            const int64_t open = sm.last_block, next = block_of(s + n);
-            if (last == 0)
-                go_long = goes_on(s + n, open);
-            else if (next == open || (next < 0 && s + n < p.tokens))
-                n = last;
+            if (goes_on(s + n, sm.last_block)) {
+                go_long = last == 0;
+                n = go_long ? n : last;
+            }
         }
         if (n == 0)
             break;
@@ -525,7 +525,7 @@ cudaError_t launch_append(Fp8AppendParams &f, int sm_count, cudaStream_t stream)
     if (f.rope.n_streams) {
         // where q has more blocks than the two of this kernel that a SM holds carry, they get a
         // kernel of their own (11,810 tokens of 16 heads of 128: 50 -> 36 us), else a
-        // launch is saved (64 tokens: 4.3 us)
+        // launch is saved
         const int q_blocks = rope_shape(f.rope, V, sm_count);
         if (q_blocks > 4 * sm_count) {
             append_q_kernel<V, INTER><<<q_blocks, kRopeThreads, 0, stream>>>(f);
@@ -662,7 +662,7 @@ cudaError_t launch_append_fp8(const Fp8AppendParams &params, bool interleaved, i
         V /= 2;
     // heads of a group: a divisor of their number, few enough that a whole block of
     // keys stays in registers (of few tokens, which are hardly all of one block, 32 keys:
-    // 64 single tokens of 8 heads, scales by 256 keys: 12.6 us with a head to a group, 4.6
+    // 64 single tokens of 8 heads, scales by 256 keys: 12.6 us with a head to a group, 4.9
     // with all)
     const int rows = kRowsKept * (kRopeThreads >> f.lane_shift), sb = 1 << f.block_shift;
     const int keys = p.tokens <= 2 * sm_count && sb > 32 ? 32 : sb;
