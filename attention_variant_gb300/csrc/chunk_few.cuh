@@ -37,11 +37,10 @@
 // key: tcgen05's kind::f8f6f4 multiplies its e4m3 codes.  Q comes as two e4m3 terms, which
 // hold a bf16 number exactly (split_q), and a key's scale, one number per TMEM lane, goes
 // into its scores; P goes in f16's precision, as three e5m2 terms with V's scale in it
-// (few_item_fp8).  K and V come
-// together, in tiles of 16 KB and one ring: at half the bytes a key it is the chain of a tile (S, its
-// softmax, P, the product) that limits, so tiles have 256 keys at D = 64 (128: 112 us on
-// the 64 requests above) and a row one reference for all its keys, which moves rarely.
-// 64 requests of 512 to 8192 keys take 68 us, of 8192 keys 107 (0.74 of the copy's
+// (few_item_fp8).  K and V come together, in tiles of 16 KB and one ring: at half the bytes a
+// key it is the chain of a tile (S, its softmax, P, the product) that limits, so tiles have 256 keys
+// at D = 64 (128: 112 us on the 64 requests above) and a row references for all its keys, which
+// move rarely.  64 requests of 512 to 8192 keys take 70 us, of 8192 keys 107 (0.74 of the copy's
 // rate); the start (14 us until the first S) and the end (8 us) weigh twice as much here.
 //
 //   warp  0     walks the CTA's items, publishes them, loads Q, K and V by TMA
@@ -133,7 +132,7 @@ struct __align__(1024) FewSmem {
     uint8_t p[2][C::kPBufs][C::kBN * C::kPRow]; // [slot]
     uint64_t q_full[2], q_empty[2];
     uint64_t k_full[C::kStages], k_empty[C::kStages];
-    uint64_t v_full[C::kStages], v_empty[C::kStages];
+    uint64_t v_full[F8 ? 1 : C::kStages], v_empty[F8 ? 1 : C::kStages]; // (in 8 bits V comes with K)
     uint64_t s_full[2], s_free[2], p_full[2][C::kPBufs], pv_done[2][C::kPBufs];
     uint64_t group[2];               // the slot's softmax warps among themselves
     uint64_t final_bar[3];
@@ -523,8 +522,7 @@ __device__ void few_loader_fp8(const FewCtx<D, true> &cx, const ChunkParams &p, 
 template <int D>
 __device__ void few_v_producer(const FewCtx<D, false> &cx, const ChunkParams &p, const CUtensorMap *tm_v)
 {
-    constexpr bool F8 = false;
-    FewSmem<D, F8> &sm = *cx.sm;
+    FewSmem<D, false> &sm = *cx.sm;
     FewRing<D> values{tm_v, sm.v, sm.v_full, sm.v_empty, 0u};
     bool ok = true;
     for (uint32_t n = 0; ok; ++n) {
@@ -538,11 +536,11 @@ __device__ void few_v_producer(const FewCtx<D, false> &cx, const ChunkParams &p,
             ptx::mbar_arrive(bar(sm.info_empty[slot]));
         if (it.stop)
             return;
-        int page_next = few_page<D, F8>(p, it, it.u_lo >> it.shift);
+        int page_next = few_page<D, false>(p, it, it.u_lo >> it.shift);
         for (int v = it.u_lo; v < it.u_hi && ok; ++v) {
             const int page = page_next;
             if (v + 1 < it.u_hi)
-                page_next = few_page<D, F8>(p, it, (v + 1) >> it.shift);
+                page_next = few_page<D, false>(p, it, (v + 1) >> it.shift);
             ok = values.load(cx, p, it, v, page);
         }
     }
@@ -1519,8 +1517,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int s = 0; s < C::kStages; ++s) {
             ptx::mbar_init(bar(sm->k_full[s]), F8 ? 1 + kScaleArrivals : 1);
             ptx::mbar_init(bar(sm->k_empty[s]), F8 ? 2 : 1); // S's; in 8 bits O^T's, too
-            ptx::mbar_init(bar(sm->v_full[s]), 1);
-            ptx::mbar_init(bar(sm->v_empty[s]), few_split_loads<F8>(p) ? 1 : 2); // the warps that issue O^T
+            if constexpr (!F8) {
+                ptx::mbar_init(bar(sm->v_full[s]), 1);
+                ptx::mbar_init(bar(sm->v_empty[s]), few_split_loads<F8>(p) ? 1 : 2); // the warps that issue O^T
+            }
         }
         for (int t = 0; t < 2; ++t) {
             ptx::mbar_init(bar(sm->s_full[t]), 1);
