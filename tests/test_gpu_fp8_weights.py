@@ -29,11 +29,13 @@ def _scales(x, block):
 
 def _held(q, keys, vals, q_lens, page=64, block=16, seed=0):
     """A problem of requests whose keys and values are given (float64 [L, Hk, D] each), coded as the
-    append does, in a pool of pages in any order."""
+    append does, in a pool of pages in any order (page 0: a contiguous cache)."""
+    contiguous = not page
+    page = page or -(-max(k.shape[0] for k in keys) // block) * block
     kv_lens = [k.shape[0] for k in keys]
     Hk, D = keys[0].shape[1:]
     per = [-(-L // page) for L in kv_lens]
-    ids = torch.randperm(sum(per), generator=torch.Generator().manual_seed(seed))
+    ids = torch.arange(sum(per)) if contiguous else torch.randperm(sum(per), generator=torch.Generator().manual_seed(seed))
     p = dict(q=q, T=q.shape[0], q_lens=q_lens, kv_lens=kv_lens, cu=[0])
     for n in q_lens:
         p["cu"].append(p["cu"][-1] + n)
@@ -57,15 +59,17 @@ def _held(q, keys, vals, q_lens, page=64, block=16, seed=0):
             p[n].append((c.double() * by_key[..., None])[:L])
             p[n + "_scale"].append(by_key[:L])
         p[n + "c"], p[n + "s"] = codes, scales
+    if contiguous:
+        p["table"] = None
     return p
 
 
-def _expected(p, floor, *, causal=True, window=0):
+def _expected(p, floor, *, causal=True, window=0, softcap=0.0):
     """float64 O [T, Hq, D], LSE [Hq, T] and bounds on the errors of both.
 
     A score is off by dz at the most: its fp32 sum (2^-21 of the sum of the products' sizes), q's second
-    term (2^-18 of the row's largest element, times the key's), and 2^-16 for the exponent's
-    sums, whose terms are below 2^8.  A weight is off by 2^-11 of itself in f16, by dz through its score
+    term (2^-18 of the row's largest element, times the key's), 2^-16 for the exponent's sums, whose
+    terms are below 2^8, and 2^-21 of a softcap, which makes none of the others larger.  A weight is off by 2^-11 of itself in f16, by dz through its score
     and by as much through the sum of all, or by `floor` of the row's largest weight times scale,
     in which it counts a code; the output's rounding adds 2^-8 of O."""
     T, Hq, D = p["q"].shape
@@ -84,9 +88,12 @@ def _expected(p, floor, *, causal=True, window=0):
         for h in range(Hq):
             q, k, v = p["q"][a: a + n, h].double(), p["k"][b][:, h // G], p["v"][b][:, h // G]
             s = p["v_scale"][b][:, h // G]
-            z = (q @ k.T * D ** -0.5).masked_fill(~seen, -math.inf)
+            z = q @ k.T * D ** -0.5
+            if softcap:
+                z = softcap * torch.tanh(z / softcap)
+            z = z.masked_fill(~seen, -math.inf)
             dz = D ** -0.5 * (2.0 ** -21 * (q.abs() @ k.abs().T) + 2.0 ** -18 * q.abs().amax(-1)[:, None] * k.abs().sum(-1))
-            dz = 2.0 ** -16 + dz.masked_fill(~seen, 0).amax(-1)
+            dz = 2.0 ** -16 + 2.0 ** -21 * softcap + dz.masked_fill(~seen, 0).amax(-1)
             w = torch.softmax(z, -1)
             o = w @ v
             out[a: a + n, h], lse[h, a: a + n] = o, torch.logsumexp(z, -1)
@@ -191,7 +198,7 @@ def test_blocks_of_zeros_beside_loud_ones(D, n, L, log_s):
     _check(_zero_blocks(D, n, L, log_s), FEW if 4 * n <= 16 else BLOCKS, f"zeros beside 2^{log_s}", calls=2)
 
 
-def _loud(D, n, L, at, gain, z=None, Hq=8, Hk=2):
+def _loud(D, n, L, at, gain, z=None, Hq=8, Hk=2, page=32):
     """Two requests of n new tokens on L keys, the V of keys `at` 2^gain times the others'; with z, those keys' scores are z."""
     q = _normal((2 * n, Hq, D), 5)
     keys, vals = [_normal((L, Hk, D), 6 + b) for b in (0, 1)], [_normal((L, Hk, D), 9 + b) for b in (0, 1)]
@@ -203,7 +210,7 @@ def _loud(D, n, L, at, gain, z=None, Hq=8, Hk=2):
             k[..., 0] = 0
             k[at] = 0
             k[at, :, 0] = z * D ** 0.5 / 4
-    return _held(q.to(torch.bfloat16), keys, vals, [n] * 2, page=32)
+    return _held(q.to(torch.bfloat16), keys, vals, [n] * 2, page=page)
 
 
 @pytest.mark.parametrize("gain", [20, 35, 60, 100])
@@ -215,10 +222,11 @@ def test_loud_values_that_come_later(D, n, L, gain):
 
 
 @pytest.mark.parametrize("gain", [35, 60, 100])
-@pytest.mark.parametrize("n,window", [(60, 20), (200, 90), (130, 300)])
+@pytest.mark.parametrize("n,window", [(3, 5), (60, 20), (200, 90), (130, 300)])
 @pytest.mark.parametrize("D", [64, 128])
 def test_loud_values_that_a_window_has_left(D, n, window, gain):
-    _check(_loud(D, n, 600, slice(600 - n - 10, 600 - n - 6), gain), BLOCKS, f"2^{gain} left", window=window)
+    p = _loud(D, n, 600, slice(600 - n - 10, 600 - n - 6), gain)
+    _check(p, FEW if 4 * n <= 16 else BLOCKS, f"2^{gain} left", window=window)
 
 
 @pytest.mark.parametrize("gain,z", [(40, -60.0), (60, -60.0), (90, -90.0), (-90, 60.0), (60, -20.0), (-60, 20.0)])
@@ -228,6 +236,31 @@ def test_loud_values_of_little_weight(D, n, L, gain, z):
     # a block whose scale and weights differ by 2^90 and more from the others', in either order
     p = _loud(D, n, L, slice(32, 48), gain, z)
     _check(p, FEW if 4 * n <= 16 else BLOCKS, f"2^{gain} at {z}", calls=2)
+
+
+@pytest.mark.parametrize("n,L", [(1, 9000), (2, 300), (4, 700), (40, 400), (300, 700)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_scales_far_apart_under_a_softcap(D, n, L):
+    floor = FEW if 4 * n <= 16 else BLOCKS
+    for log_s in (-8, 60):
+        _check(_zero_blocks(D, n, L, log_s), floor, f"zeros beside 2^{log_s}", softcap=20.0)
+    _check(_loud(D, n, L, slice(L // 16 * 16, L), 60), floor, "later", softcap=5.0)
+    _check(_loud(D, n, L, slice(32, 48), 60, -30.0), floor, "of little weight", softcap=40.0)
+    _check(_loud(D, n, L, slice(32, 48), -60, 30.0), floor, "of great weight", softcap=40.0)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Hq,Hk,page", [(5, 5, 16), (16, 1, 256), (6, 2, 0), (32, 8, 64)])
+def test_scales_far_apart_by_head_groups(Hq, Hk, page, D):
+    # one slot, sixteen rows of a token, odd groups, a contiguous cache; rows before the sequence
+    for n, L in ((1, 1000), (2, 129), (20, 700), (9, 4)):
+        p = _loud(D, n, L, slice(L // 32 * 16, L // 32 * 16 + 16), 70, Hq=Hq, Hk=Hk, page=page)
+        floor = FEW if n * Hq // Hk <= 16 else BLOCKS
+        if L < n:
+            out, lse = base._launch(p)[0]
+            assert not bool(out.view(2, n, Hq, D)[:, : n - L].any()) and bool((lse.view(Hq, 2, n)[..., : n - L] == -math.inf).all())
+        else:
+            _check(p, floor, f"{n} on {L}")
 
 
 @pytest.mark.parametrize("log_s", [-100, 100])
