@@ -54,13 +54,13 @@
 // A cache in 8 bits: S as in chunk_few.cuh, K's codes against Q's two terms.  For
 // O, warps 2 and 3 turn V's codes into f16 (exact) in shared memory while the
 // softmax of the next tile runs, and P is f16 with V's scale in its exponent, one for 16
-// keys, relative to the largest product of weight and scale of the row (softmax_compute_p_scaled).  V's codes straight into
-// the product want P in e4m3, in two terms for bf16's accuracy: twice the rows of the 128 an MMA
-// has.  Converted by the softmax's own warps the long prompt above took 1.6 times as long.
-// It takes 584 us, 824 TFLOP/s: the conversion and the factors are 15% more instructions, and
-// the larger code misses the instruction caches (issue 49%, tensor 31%, special functions 34%);
-// at D = 128 471 us, 1020 TFLOP/s.  Windows of 1024 keys, 4023 tokens, 16 heads over 2
-// of 128: 71 us, 64 in bf16.
+// keys, relative to the largest product of weight and scale of the row (softmax_compute_p_scaled).
+// V's codes straight into the product want P in 8 bits, in three terms for as much: three times the
+// rows of the 128 an MMA has.  Converted by the softmax's own warps the long prompt above took 1.6
+// times as long.
+// It takes 583 us, 825 TFLOP/s: the conversion and the factors are 15% more instructions (issue
+// 50%, tensor 32%, special functions 34%); at D = 128 433 us, 1110 TFLOP/s.  Windows of 1024 keys,
+// 4023 tokens, 16 heads over 2 of 128: 69 us, 64 in bf16.
 #pragma once
 
 #include <cuda_bf16.h>

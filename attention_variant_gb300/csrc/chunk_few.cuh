@@ -40,7 +40,7 @@
 // (few_item_fp8).  K and V come together, in tiles of 16 KB and one ring: at half the bytes a
 // key it is the chain of a tile (S, its softmax, P, the product) that limits, so tiles have 256 keys
 // at D = 64 (128: 112 us on the 64 requests above) and a row references for all its keys, which
-// move rarely.  64 requests of 512 to 8192 keys take 70 us, of 8192 keys 107 (0.74 of the copy's
+// move rarely.  64 requests of 512 to 8192 keys take 69 us, of 8192 keys 107 (0.74 of the copy's
 // rate); the start (14 us until the first S) and the end (8 us) weigh twice as much here.
 //
 //   warp  0     walks the CTA's items, publishes them, loads Q, K and V by TMA
@@ -1064,8 +1064,8 @@ __device__ void few_softmax(const FewCtx<D, false> &cx, const ChunkParams &p, in
 // neither exponential can be had from the other.  The references make the largest P of a tile
 // 2^kFewTop and the largest weight 1 when they are set, and are set again where one would pass
 // 2^kFewMost or 2^kFewSumMost: until then the slot's warps only agree, once a tile, that none does.
-// (The second exponentials take 64 tokens on 512 to 8192 keys from 68 to 70 us.  A path of its own for
-// scales far apart took 73, two copies of the code for P 79: what this loop costs is its instructions'
+// (The second exponentials take 64 tokens on 512 to 8192 keys from 68 to 69 us.  A function of its own for
+// scales far apart took 75, two copies of the code for P 79: what this loop costs is its instructions'
 // fetch.)
 //
 // P is rounded to f16, 11 bits down to 2^-26 of the row's largest and steps of 2^-36 of it

@@ -17,10 +17,10 @@
 // fp32, they left two blocks to a SM).  A run too long for that is read and rotated twice, the
 // second time out of L2.
 //
-// Bound by HBM in part, and by the rotation: 11,810 tokens of 16 + 2 + 2 heads of 128 take 35.7 us
-// (3220 GB/s of 6794; q's rotation, a kernel of its own beside, is 80% of the bytes);
-// 64 single tokens 4.7 us, the launch and one chain of loads.  Reading 79,000 tokens back
-// into bf16 35.4 us, 6130 GB/s.
+// Bound by HBM in part, and by the rotation: 11,810 tokens of 16 + 2 + 2 heads of 128 take 35.8 us
+// (3210 GB/s of 6794; q's rotation, a kernel of its own beside, is 80% of the bytes);
+// 64 single tokens 5.1 us, the launch and one chain of loads.  Reading 79,000 tokens back
+// into bf16 35.8 us, 6070 GB/s.
 #include <cuda_bf16.h>
 #include <cstdint>
 #include <type_traits>
@@ -662,7 +662,7 @@ cudaError_t launch_append_fp8(const Fp8AppendParams &params, bool interleaved, i
         V /= 2;
     // heads of a group: a divisor of their number, few enough that a whole block of
     // keys stays in registers (of few tokens, which are hardly all of one block, 32 keys:
-    // 64 single tokens of 8 heads, scales by 256 keys: 12.6 us with a head to a group, 4.9
+    // 64 single tokens of 8 heads, scales by 256 keys: 12.8 us with a head to a group, 4.9
     // with all)
     const int rows = kRowsKept * (kRopeThreads >> f.lane_shift), sb = 1 << f.block_shift;
     const int keys = p.tokens <= 2 * sm_count && sb > 32 ? 32 : sb;
